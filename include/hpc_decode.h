@@ -510,6 +510,200 @@ hpc_status hpc_decode_noalloc(const void* q, const void* k_cache, const void* v_
                               int num_kv_heads, int head_dim, int page_size, int num_ctas,
                               int min_chunks_per_cta, void* out, float* out_lse, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Prompt attention and shared-prefix attention, over the same paged caches.
+ *
+ * Both work on a tile map: the query tokens of each sequence in tiles of 32
+ * tokens x the 8 query heads of a KV head, each tile over the 128-token KV
+ * blocks that it sees, all tiles walked head by head, sequence by sequence and
+ * cut into equal runs, one per CTA ([SGL] "Scheduling around live KV work",
+ * the same balance for prompts). Tiles that fall to one CTA are written to the
+ * output by the attention call; cut ones leave partial rows for the combine.
+ */
+#define HPC_MAX_TILE_CTAS 4096
+
+/*
+ * Tile map. The caller fills `buf` (device memory of at least
+ * hpc_tile_plan_bytes, 16-byte aligned) and `bytes`; hpc_prefill_plan or
+ * hpc_prefix_plan fills the rest. It holds a copy of the lengths it was made
+ * from, so the attention calls need no lengths, and one map serves every layer.
+ * Byte layout of buf (int32):
+ *   [0, 16)   header {units_per_head (int64), bucket (int64), used_ctas,
+ *             num_seqs, num_kv_heads, num_ctas, num_tokens, mode,
+ *             tiles_per_head, q_len, error word, 0, 0, 0}
+ *   starts    [num_ctas + 1][8] {kv head, sequence, tile, block, tile number, 0, 0, 0}:
+ *             where each CTA's run begins
+ *   seqs      [num_seqs][4] {first query token, query tokens, keys, tiles before}
+ *   units     int64 [num_seqs + 1]: units of the sequences before (a block is one
+ *             unit; a tile of a prompt costs one more)
+ * The buffer is deterministic: the same lengths give the same bytes.
+ */
+typedef struct hpc_tile_plan {
+    int32_t* buf;      /* device, caller-owned */
+    size_t bytes;      /* size of buf in bytes */
+    int num_seqs;      /* filled by the planner from here on */
+    int num_tokens;
+    int num_kv_heads;
+    int num_ctas;      /* grid size of the attention call */
+    int mode;          /* 0 prompts, 1 prefixes */
+    int q_len;
+    int table_stride;
+} hpc_tile_plan;
+
+/* Bytes of a tile map; independent of the lengths. 0 on invalid sizes
+ * (1 <= num_seqs <= HPC_MAX_BATCH, 1 <= num_ctas <= HPC_MAX_TILE_CTAS). */
+size_t hpc_tile_plan_bytes(int num_seqs, int num_ctas);
+
+/* CTA count to plan for on the current device: one per SM. 0 if the device
+ * cannot be queried. */
+int hpc_tile_default_num_ctas(void);
+
+/* Rows of 128 floats in split_o (and floats in split_lse) of hpc_prefill_attn
+ * and of hpc_prefix_attn. 0 on invalid sizes. */
+size_t hpc_prefill_split_rows(int num_ctas);
+size_t hpc_prefix_split_rows(int num_groups, int batch, int q_len, int num_kv_heads, int num_ctas);
+
+/*
+ * Tile map of a batch of prompts, or pieces of prompts, packed one after the
+ * other: sequence b has the query tokens [q_starts[b], q_starts[b + 1]) and
+ * seq_lens[b] keys in the cache, its query tokens being the last of them (they
+ * are already written). Query token i of n sees keys [0, seq_lens[b] - n + i]
+ * (causal); where n > seq_lens[b] the first ones see nothing. A sequence of one
+ * query token is a decode step; one without any is passed over.
+ *   d_q_starts    device int32 [batch + 1], not decreasing, inside [0, num_tokens]
+ *   d_seq_lens    device int32 [batch]
+ *   num_tokens    rows of q and out; rows of no sequence are left as they are
+ *   page_table_stride  of the table that the attention call gets
+ *   min_blocks_per_cta  least 128-token blocks of a CTA's run (fewer CTAs get
+ *                 work in small batches); 0 or 1: no floor
+ * One block, integer only, reads the lengths on the device. A sequence whose
+ * starts decrease or leave [0, num_tokens] is passed over
+ * (HPC_DEVERR_BAD_DESCRIPTOR); keys beyond the page table's row are not seen
+ * (HPC_DEVERR_PAGE_OUT_OF_RANGE); a negative length counts as 0
+ * (HPC_DEVERR_NEGATIVE_LENGTH).
+ * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_WORKSPACE_TOO_SMALL, HPC_ERR_CUDA.
+ */
+hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens, int batch, int num_tokens,
+                            int num_kv_heads, int page_table_stride, int num_ctas, int min_blocks_per_cta,
+                            hpc_tile_plan* plan, void* stream);
+
+/*
+ * Attention of the mapped prompts, on tcgen05 tensor cores. Whole tiles go to
+ * out and out_lse; pieces of cut tiles to split_o and split_lse, for
+ * hpc_prefill_combine (call it even if nothing is cut: it then does nothing).
+ *   q          device bf16 [num_tokens][num_q_heads][128], 16-byte aligned
+ *   split_o    device float32 [hpc_prefill_split_rows][128], 16-byte aligned
+ *   split_lse  device float32 [hpc_prefill_split_rows]
+ *   out        device bf16 [num_tokens][num_q_heads][128], 16-byte aligned
+ *   out_lse    device float32 [num_tokens][num_q_heads] or NULL
+ * A row that sees no key gets out = 0 and out_lse = -inf. Scores and sums are
+ * float32; probabilities enter the second product as bf16 (f16 with an e4m3
+ * cache, where V enters as code x scale rounded to f16: |v| <= 65504, and values
+ * under 2^-14 keep multiples of 2^-24). Keys and values of tokens that a row does
+ * not see never reach it through its maximum and sum; a value of V that is not
+ * finite reaches every row of the 128-token blocks that hold its token.
+ * A page id outside [0, num_pages) hides its 64 tokens
+ * (HPC_DEVERR_PAGE_OUT_OF_RANGE).
+ * Errors: HPC_ERR_INVALID_ARG (also a plan made for other sizes or by
+ * hpc_prefix_plan), HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA.
+ */
+hpc_status hpc_prefill_attn(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, int kv_dtype, int num_pages, const int32_t* page_table,
+                            int page_table_stride, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                            const hpc_tile_plan* plan, float* split_o, float* split_lse, void* out, float* out_lse,
+                            void* stream);
+
+/* Merges the pieces of cut tiles into out and out_lse, as hpc_decode_combine
+ * merges splits; rows of whole tiles are not touched. Errors: as above. */
+hpc_status hpc_prefill_combine(const hpc_tile_plan* plan, const float* split_o, const float* split_lse, void* out,
+                               float* out_lse, int num_q_heads, int num_kv_heads, int head_dim, void* stream);
+
+/*
+ * Tile map of the prefixes that groups of a decode batch share: group g is the
+ * requests [group_starts[g], group_starts[g + 1]), all of which see the whole
+ * prefix of prefix_lens[g] tokens, whose pages prefix_table's row g names. A
+ * request of no group, or of a group whose prefix is empty, has only its own
+ * tokens. Every request has q_len query tokens.
+ *   d_group_starts  device int32 [num_groups + 1], not decreasing, inside [0, batch]
+ *   d_prefix_lens   device int32 [num_groups]
+ * Checks and errors as hpc_prefill_plan.
+ */
+hpc_status hpc_prefix_plan(const int32_t* d_group_starts, const int32_t* d_prefix_lens, int num_groups, int batch,
+                           int q_len, int num_kv_heads, int prefix_table_stride, int num_ctas, int min_blocks_per_cta,
+                           hpc_tile_plan* plan, void* stream);
+
+/*
+ * Attention of every query row over its group's prefix, each prefix read once
+ * per 32 query tokens of the group instead of once per request: partial rows and LSEs for
+ * hpc_prefix_combine.
+ *   q             device bf16 [batch][q_len][num_q_heads][128], 16-byte aligned
+ *   prefix_table  device int32 [num_groups][prefix_table_stride]
+ *   split_o       device float32 [hpc_prefix_split_rows][128], 16-byte aligned
+ *   split_lse     device float32 [hpc_prefix_split_rows]
+ * Numerics, bad pages and errors as hpc_prefill_attn.
+ */
+hpc_status hpc_prefix_attn(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, int kv_dtype, int num_pages, const int32_t* prefix_table,
+                           int prefix_table_stride, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                           const hpc_tile_plan* plan, float* split_o, float* split_lse, void* stream);
+
+/*
+ * Merges every row's prefix pieces and the splits of its own tokens: plan,
+ * split_o and split_lse are those of hpc_decode_plan and hpc_decode_attn (q_len
+ * 1) or hpc_decode_attn_multi over the tokens behind the prefix (seq_lens and
+ * page_table hold those alone; 0 tokens are allowed).
+ *   out       device bf16 [batch][q_len][num_q_heads][128], 8-byte aligned
+ *   out_lse   device float32 [batch][q_len][num_q_heads] or NULL
+ * Errors: HPC_ERR_INVALID_ARG (also plans of other sizes), HPC_ERR_UNSUPPORTED,
+ * HPC_ERR_CUDA.
+ */
+hpc_status hpc_prefix_combine(const hpc_tile_plan* prefix_plan, const float* prefix_o, const float* prefix_lse,
+                              const hpc_plan* plan, const float* split_o, const float* split_lse, void* out,
+                              float* out_lse, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                              void* stream);
+
+/* Synchronises the device, then reads the tile map's error word, as
+ * hpc_decode_read_error does a task map's. */
+hpc_status hpc_tile_read_error(const hpc_tile_plan* plan, int* device_error_word);
+
+/*
+ * K and V rows into the cache as they are (what hpc_rope_norm does after its
+ * norm and rotation): token t's heads go to slot_mapping[t] = page * 64 + offset
+ * (negative: not written) as bf16, or as e4m3 codes with a scale per (token, KV
+ * head): scale = amax / 448 (1 if all 128 are 0), code = x / scale rounded to
+ * nearest even. Two tokens must not name one slot (what it then holds is not
+ * determined).
+ *   k, v    device bf16, 16-byte aligned; token t's [num_kv_heads][128] elements
+ *           begin at t * k_token_stride / t * v_token_stride elements (multiples
+ *           of 8, at least num_kv_heads * 128): parts of a fused projection's
+ *           output need no copy
+ *   d_error_word  device int32 or NULL: HPC_DEVERR_PAGE_OUT_OF_RANGE (slot skipped)
+ * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA. num_tokens == 0
+ * enqueues nothing.
+ */
+hpc_status hpc_kv_write(const void* k, const void* v, long long k_token_stride, long long v_token_stride,
+                        const int32_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim, int page_size,
+                        void* k_cache, void* v_cache, float* k_scale, float* v_scale, int kv_dtype, int num_pages,
+                        int* d_error_word, void* stream);
+
+/*
+ * K and V of a batch read back from the cache, packed: rows
+ * [out_starts[b], out_starts[b + 1]) of k_out and v_out get tokens first[b],
+ * first[b] + 1, ... of request b. e4m3 values are code * scale in float32,
+ * rounded to bf16 once.
+ *   first       device int32 [batch] or NULL (0)
+ *   out_starts  device int32 [batch + 1], not decreasing
+ *   num_rows    rows of k_out and v_out; rows of no request are left as they are
+ *   k_out, v_out  device bf16 [num_rows][num_kv_heads][128], 16-byte aligned
+ *   d_error_word  device int32 or NULL: HPC_DEVERR_PAGE_OUT_OF_RANGE (a token
+ *               beyond the table's row or with a page id out of range reads as 0)
+ * Errors: as hpc_kv_write. num_rows == 0 enqueues nothing.
+ */
+hpc_status hpc_kv_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int kv_dtype,
+                       int num_pages, const int32_t* page_table, int page_table_stride, const int32_t* first,
+                       const int32_t* out_starts, int batch, int num_rows, int num_kv_heads, int head_dim, int page_size,
+                       void* k_out, void* v_out, int* d_error_word, void* stream);
+
 /* Synchronises the device, then reads the task map's error word into
  * *device_error_word. Returns HPC_ERR_DEVICE_CHECK when it is non-zero.
  * For tests and diagnostics, not for the hot loop. */

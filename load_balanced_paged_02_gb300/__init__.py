@@ -14,7 +14,10 @@ _BINDING_NAMES = {
     "KV_BF16", "KV_FP8_E4M3", "HpcError", "Plan", "build", "default_num_ctas",
     "hpc_decode_attn", "hpc_decode_combine", "hpc_decode_plan", "hpc_decode_plan_static",
     "hpc_decode_read_error", "hpc_decode_step_host", "lib", "split_buffers", "decode",
-    "sm_count", "hpc_rope_norm",
+    "sm_count", "hpc_rope_norm", "TilePlan", "hpc_prefill_plan", "hpc_prefill_attn", "hpc_prefill_combine",
+    "prefill_split_buffers", "prefill", "hpc_prefix_plan", "hpc_prefix_attn", "hpc_prefix_combine",
+    "prefix_split_buffers", "decode_shared_prefix", "hpc_tile_read_error", "tile_num_ctas", "hpc_kv_write",
+    "hpc_kv_read",
 }
 
 

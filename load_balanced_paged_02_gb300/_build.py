@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(ROOT, "_build", "hpcdecode")
 LIB_PATH = os.path.join(HERE, "libhpcdecode.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["plan.cu", "attn.cu", "attn_mt.cu", "attn_tc.cu", "combine.cu", "prologue.cu", "api.cu", "noalloc.cu",
-           "stage.cu"]
+           "stage.cu", "tile_plan.cu", "tile_attn.cu", "tile_combine.cu", "kv.cu", "api_tile.cu"]
 
 
 def nvcc() -> str:

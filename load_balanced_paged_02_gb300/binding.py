@@ -45,7 +45,14 @@ class PlanStruct(ctypes.Structure):
                 ("num_ctas", _i), ("min_chunks", _i), ("mode", _i), ("max_tasks", _i)]
 
 
+class TilePlanStruct(ctypes.Structure):
+    _fields_ = [("buf", _vp), ("bytes", _sz), ("num_seqs", _i), ("num_tokens", _i), ("num_kv_heads", _i),
+                ("num_ctas", _i), ("mode", _i), ("q_len", _i), ("table_stride", _i)]
+
+
 _P = ctypes.POINTER(PlanStruct)
+_TP = ctypes.POINTER(TilePlanStruct)
+_ll = ctypes.c_longlong
 SIGNATURES = {
     "hpc_decode_plan_bytes": (_sz, [_i, _i, _i]),
     "hpc_decode_split_capacity": (_sz, [_i, _i, _i]),
@@ -79,6 +86,20 @@ SIGNATURES = {
                                 _i, _vp, _vp, _vp]),
     "hpc_decode_read_error": (_i, [_P, ctypes.POINTER(_i)]),
     "hpc_status_string": (ctypes.c_char_p, [_i]),
+    "hpc_tile_plan_bytes": (_sz, [_i, _i]),
+    "hpc_tile_default_num_ctas": (_i, []),
+    "hpc_prefill_split_rows": (_sz, [_i]),
+    "hpc_prefix_split_rows": (_sz, [_i, _i, _i, _i, _i]),
+    "hpc_prefill_plan": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _TP, _vp]),
+    "hpc_prefill_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _i, _i, _i, _i, _TP, _vp, _vp, _vp, _vp,
+                              _vp]),
+    "hpc_prefill_combine": (_i, [_TP, _vp, _vp, _vp, _vp, _i, _i, _i, _vp]),
+    "hpc_prefix_plan": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _TP, _vp]),
+    "hpc_prefix_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _i, _i, _i, _i, _TP, _vp, _vp, _vp]),
+    "hpc_prefix_combine": (_i, [_TP, _vp, _vp, _P, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "hpc_tile_read_error": (_i, [_TP, ctypes.POINTER(_i)]),
+    "hpc_kv_write": (_i, [_vp, _vp, _ll, _ll, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp]),
+    "hpc_kv_read": (_i, [_vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
 }
 
 _lock = threading.Lock()
@@ -425,3 +446,305 @@ def hpc_rope_norm(qkv, positions, cos_sin, q_weight, k_weight, slot_mapping, q_o
         _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kv_dtype_of(k_cache),
         int(num_pages if num_pages is not None else k_cache.shape[0]), _ptr(error_word), _stream(stream))
     _check("hpc_rope_norm", rc)
+
+
+# ---------------------------------------------------------------- prompts, shared prefixes, cache write / read
+
+class TilePlan:
+    """A tile map in device memory (``buf``) plus its host header."""
+
+    def __init__(self, num_seqs: int, num_ctas: int, device):
+        nbytes = lib().hpc_tile_plan_bytes(num_seqs, num_ctas)
+        if nbytes == 0:
+            raise HpcError("hpc_tile_plan_bytes", detail="sizes outside the supported limits")
+        self.buf = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
+        self.struct = TilePlanStruct(self.buf.data_ptr(), nbytes, 0, 0, 0, 0, 0, 0, 0)
+
+    @property
+    def num_ctas(self):
+        return self.struct.num_ctas
+
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+
+def tile_num_ctas() -> int:
+    """hpc_tile_default_num_ctas: one CTA per SM."""
+    n = lib().hpc_tile_default_num_ctas()
+    if n <= 0:
+        raise HpcError("hpc_tile_default_num_ctas", detail="device query failed")
+    return n
+
+
+def _same_device(what, *tensors):
+    """Every tensor (None passed over) on the first one's device, which is the current one."""
+    dev = tensors[0].device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise HpcError(what, detail=f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise HpcError(what, detail=f"tensors on {dev} and {t.device}")
+
+
+def _check_caches(what, k_cache, v_cache, k_scale, v_scale):
+    """Shapes and types of a paged cache; returns its hpc_kv_dtype."""
+    kvd = kv_dtype_of(k_cache)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise HpcError(what, detail="k_cache and v_cache must be [pages, 64, heads, 128] of one type")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise HpcError(what, detail="k_cache and v_cache must be contiguous")
+    if kvd == KV_FP8_E4M3:
+        shape = (k_cache.shape[0], k_cache.shape[2], k_cache.shape[1])
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None or tuple(t.shape) != shape or t.dtype != torch.float32 or not t.is_contiguous():
+                raise HpcError(n, detail=f"an e4m3 cache needs contiguous float32 scales of shape {shape}")
+    return kvd
+
+
+def _check_out(what, t, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise HpcError(what, detail=f"must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def hpc_prefill_plan(q_starts, seq_lens, num_tokens: int, num_kv_heads: int, page_table_stride: int,
+                     num_ctas: int | None = None, min_blocks_per_cta: int = 1, plan: TilePlan | None = None,
+                     stream=None) -> TilePlan:
+    """Tile map of packed prompts from device-side starts and lengths (one launch, no host sync)."""
+    _cuda_i32(q_starts, "q_starts")
+    _cuda_i32(seq_lens, "seq_lens")
+    B = seq_lens.numel()
+    if q_starts.numel() != B + 1:
+        raise HpcError("q_starts", detail=f"must hold {B + 1} starts")
+    _same_device("hpc_prefill_plan", seq_lens, q_starts)
+    num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
+    plan = TilePlan(B, num_ctas, seq_lens.device) if plan is None else plan
+    rc = lib().hpc_prefill_plan(_ptr(q_starts), _ptr(seq_lens), B, num_tokens, num_kv_heads, page_table_stride, num_ctas,
+                                min_blocks_per_cta, plan.ref(), _stream(stream))
+    _check("hpc_prefill_plan", rc)
+    return plan
+
+
+def _split_rows(rows, device):
+    return (torch.empty((rows, HEAD_DIM), dtype=torch.float32, device=device),
+            torch.empty(rows, dtype=torch.float32, device=device))
+
+
+def prefill_split_buffers(plan: TilePlan):
+    """split_o and split_lse of hpc_prefill_attn for this map."""
+    return _split_rows(int(lib().hpc_prefill_split_rows(plan.struct.num_ctas)), plan.buf.device)
+
+
+def _check_q_table(what, q, table, seqs):
+    if q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise HpcError(what, detail="q must be a contiguous bfloat16 tensor")
+    _cuda_i32(table, "page table")
+    if table.dim() != 2 or table.shape[0] != seqs:
+        raise HpcError(what, detail=f"the page table must have {seqs} rows")
+
+
+def _check_splits(what, rows, split_o, split_lse):
+    for t, n in ((split_o, rows * HEAD_DIM), (split_lse, rows)):
+        if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() < n:
+            raise HpcError(what, detail=f"split buffers need {rows} rows of contiguous float32")
+
+
+def hpc_prefill_attn(q, k_cache, v_cache, page_table, plan: TilePlan, split_o, split_lse, out, out_lse=None, k_scale=None,
+                     v_scale=None, num_pages: int | None = None, stream=None):
+    """Causal attention of packed prompts over the paged cache; whole tiles go to
+    out [T, Hq, 128] (and out_lse [T, Hq]), pieces of cut ones to the split buffers."""
+    kvd = _check_caches("hpc_prefill_attn", k_cache, v_cache, k_scale, v_scale)
+    T, Hq, D = q.shape
+    _check_q_table("hpc_prefill_attn", q, page_table, plan.struct.num_seqs)
+    _same_device("hpc_prefill_attn", q, k_cache, v_cache, k_scale, v_scale, page_table, split_o, split_lse, out, out_lse)
+    if T != plan.struct.num_tokens:
+        raise HpcError("hpc_prefill_attn", detail=f"q has {T} tokens, the plan {plan.struct.num_tokens}")
+    _check_out("out", out, q.shape, torch.bfloat16)
+    if out_lse is not None:
+        _check_out("out_lse", out_lse, (T, Hq), torch.float32)
+    _check_splits("hpc_prefill_attn", int(lib().hpc_prefill_split_rows(plan.struct.num_ctas)), split_o, split_lse)
+    rc = lib().hpc_prefill_attn(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kvd, _pages(k_cache, num_pages),
+        _ptr(page_table), int(page_table.shape[1]), Hq, int(k_cache.shape[2]), D, int(k_cache.shape[1]), plan.ref(),
+        _ptr(split_o), _ptr(split_lse), _ptr(out), _ptr(out_lse), _stream(stream))
+    _check("hpc_prefill_attn", rc)
+
+
+def _pages(k_cache, num_pages):
+    """The pages in use; never more than the cache has."""
+    if num_pages is None:
+        return int(k_cache.shape[0])
+    if num_pages > k_cache.shape[0]:
+        raise HpcError("num_pages", detail=f"{num_pages}, but the cache has {k_cache.shape[0]}")
+    return int(num_pages)
+
+
+def hpc_prefill_combine(plan: TilePlan, split_o, split_lse, out, out_lse=None, stream=None):
+    """Merges the pieces of cut tiles into out and out_lse."""
+    Hq, D = out.shape[-2:]
+    rc = lib().hpc_prefill_combine(plan.ref(), _ptr(split_o), _ptr(split_lse), _ptr(out), _ptr(out_lse), Hq,
+                                   plan.struct.num_kv_heads, D, _stream(stream))
+    _check("hpc_prefill_combine", rc)
+
+
+def _on(stream):
+    """Allocations for work on ``stream`` belong to it."""
+    import contextlib
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
+
+
+def prefill(q, k_cache, v_cache, page_table, q_starts, seq_lens, k_scale=None, v_scale=None, num_ctas: int | None = None,
+            min_blocks_per_cta: int = 1, num_pages: int | None = None, out=None, out_lse=None, stream=None):
+    """plan -> attention -> combine of packed prompts, q bf16 [T, Hq, 128], with buffers
+    allocated here (and out, out_lse where they are not given). Returns (out, lse, plan)."""
+    with _on(stream):
+        plan = hpc_prefill_plan(q_starts, seq_lens, q.shape[0], k_cache.shape[2], page_table.shape[1], num_ctas,
+                                min_blocks_per_cta, stream=stream)
+        so, sl = prefill_split_buffers(plan)
+        if out is None:
+            out = torch.empty_like(q)
+        if out_lse is None:
+            out_lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        hpc_prefill_attn(q, k_cache, v_cache, page_table, plan, so, sl, out, out_lse, k_scale, v_scale, num_pages,
+                         stream=stream)
+        hpc_prefill_combine(plan, so, sl, out, out_lse, stream=stream)
+    return out, out_lse, plan
+
+
+def hpc_prefix_plan(group_starts, prefix_lens, batch: int, num_kv_heads: int, prefix_table_stride: int, q_len: int = 1,
+                    num_ctas: int | None = None, min_blocks_per_cta: int = 1, plan: TilePlan | None = None,
+                    stream=None) -> TilePlan:
+    """Tile map of the prefixes that groups of a decode batch share."""
+    _cuda_i32(group_starts, "group_starts")
+    _cuda_i32(prefix_lens, "prefix_lens")
+    G = prefix_lens.numel()
+    if group_starts.numel() != G + 1:
+        raise HpcError("group_starts", detail=f"must hold {G + 1} starts")
+    _same_device("hpc_prefix_plan", prefix_lens, group_starts)
+    num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
+    plan = TilePlan(G, num_ctas, prefix_lens.device) if plan is None else plan
+    rc = lib().hpc_prefix_plan(_ptr(group_starts), _ptr(prefix_lens), G, batch, q_len, num_kv_heads, prefix_table_stride,
+                               num_ctas, min_blocks_per_cta, plan.ref(), _stream(stream))
+    _check("hpc_prefix_plan", rc)
+    return plan
+
+
+def _prefix_rows(plan: TilePlan):
+    p = plan.struct
+    return int(lib().hpc_prefix_split_rows(p.num_seqs, p.num_tokens // p.q_len, p.q_len, p.num_kv_heads, p.num_ctas))
+
+
+def prefix_split_buffers(plan: TilePlan):
+    """split_o and split_lse of hpc_prefix_attn for this map."""
+    return _split_rows(_prefix_rows(plan), plan.buf.device)
+
+
+def hpc_prefix_attn(q, k_cache, v_cache, prefix_table, plan: TilePlan, split_o, split_lse, k_scale=None, v_scale=None,
+                    num_pages: int | None = None, stream=None):
+    """Attention of every query row of a decode batch (q bf16 [B, Hq, 128] or
+    [B, q_len, Hq, 128]) over its group's prefix; partial rows for hpc_prefix_combine."""
+    kvd = _check_caches("hpc_prefix_attn", k_cache, v_cache, k_scale, v_scale)
+    Hq, D = q.shape[-2:]
+    _check_q_table("hpc_prefix_attn", q, prefix_table, plan.struct.num_seqs)
+    _same_device("hpc_prefix_attn", q, k_cache, v_cache, k_scale, v_scale, prefix_table, split_o, split_lse)
+    if q.numel() != plan.struct.num_tokens * Hq * D or (q.shape[1] if q.dim() == 4 else 1) != plan.struct.q_len:
+        raise HpcError("hpc_prefix_attn", detail="q and the plan differ in requests or new tokens")
+    _check_splits("hpc_prefix_attn", _prefix_rows(plan), split_o, split_lse)
+    rc = lib().hpc_prefix_attn(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kvd, _pages(k_cache, num_pages),
+        _ptr(prefix_table), int(prefix_table.shape[1]), Hq, int(k_cache.shape[2]), D, int(k_cache.shape[1]), plan.ref(),
+        _ptr(split_o), _ptr(split_lse), _stream(stream))
+    _check("hpc_prefix_attn", rc)
+
+
+def hpc_prefix_combine(prefix_plan: TilePlan, prefix_o, prefix_lse, plan: Plan, split_o, split_lse, out, out_lse=None,
+                       stream=None):
+    """Merges the prefix pieces and the splits of the requests' own tokens into out
+    ([B, Hq, 128] or [B, q_len, Hq, 128] bf16) and out_lse."""
+    B, Hq, D = out.shape[0], out.shape[-2], out.shape[-1]
+    q_len = out.shape[1] if out.dim() == 4 else 1
+    rc = lib().hpc_prefix_combine(prefix_plan.ref(), _ptr(prefix_o), _ptr(prefix_lse), plan.ref(), _ptr(split_o),
+                                  _ptr(split_lse), _ptr(out), _ptr(out_lse), B, q_len, Hq, Hq // GROUP, D, _stream(stream))
+    _check("hpc_prefix_combine", rc)
+
+
+def decode_shared_prefix(q, k_cache, v_cache, page_table, seq_lens, prefix_table, prefix_lens, group_starts, k_scale=None,
+                         v_scale=None, num_ctas: int | None = None, min_chunks_per_cta: int = 2,
+                         prefix_num_ctas: int | None = None, min_blocks_per_cta: int = 1, num_pages: int | None = None,
+                         stream=None):
+    """One decode step of a batch whose groups share prefixes: requests
+    [group_starts[g], group_starts[g + 1]) see the prefix_lens[g] tokens that
+    prefix_table[g] names, then their own seq_lens[b] tokens (page_table). Each
+    prefix is computed once for its group. Returns (out, lse, prefix_plan, plan)."""
+    q_len = q.shape[1] if q.dim() == 4 else 1
+    B, Hkv = q.shape[0], k_cache.shape[2]
+    with _on(stream):
+        pplan = hpc_prefix_plan(group_starts, prefix_lens, B, Hkv, prefix_table.shape[1], q_len, prefix_num_ctas,
+                                min_blocks_per_cta, stream=stream)
+        po, pl = prefix_split_buffers(pplan)
+        plan = hpc_decode_plan(seq_lens, Hkv, num_ctas or default_num_ctas(kv_dtype_of(k_cache)), min_chunks_per_cta,
+                               stream=stream)
+        so, sl = split_buffers(plan, q_len=q_len)
+        hpc_prefix_attn(q, k_cache, v_cache, prefix_table, pplan, po, pl, k_scale, v_scale, num_pages, stream=stream)
+        hpc_decode_attn(q, k_cache, v_cache, page_table, seq_lens, plan, so, sl, k_scale, v_scale,
+                        _pages(k_cache, num_pages), stream=stream)
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        hpc_prefix_combine(pplan, po, pl, plan, so, sl, out, lse, stream=stream)
+    return out, lse, pplan, plan
+
+
+def hpc_tile_read_error(plan: TilePlan) -> int:
+    """Synchronise and read the tile map's device error word (HPC_DEVERR_* bits)."""
+    w = ctypes.c_int(0)
+    rc = lib().hpc_tile_read_error(plan.ref(), ctypes.byref(w))
+    if rc not in (0, 5):
+        _check("hpc_tile_read_error", rc)
+    return int(w.value)
+
+
+def hpc_kv_write(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None, num_pages: int | None = None,
+                 error_word=None, stream=None):
+    """K and V (bf16 [T, Hkv, 128]; any token stride, such as slices of a fused
+    projection's output) into the cache slots, bf16 or quantised to e4m3."""
+    kvd = _check_caches("hpc_kv_write", k_cache, v_cache, k_scale, v_scale)
+    T, Hkv, D = k.shape
+    _cuda_i32(slot_mapping, "slot_mapping")
+    _same_device("hpc_kv_write", k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, error_word)
+    if v.shape != k.shape or slot_mapping.numel() != T or Hkv != k_cache.shape[2]:
+        raise HpcError("hpc_kv_write", detail="k, v, slot_mapping and the cache differ in tokens or heads")
+    for t, n in ((k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16 or (T > 0 and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D))):
+            raise HpcError(n, detail="must be bfloat16 with each token's heads contiguous")
+    row = Hkv * D
+    ks, vs = (t.stride(0) if T > 1 else row for t in (k, v))
+    rc = lib().hpc_kv_write(_ptr(k), _ptr(v), ks, vs, _ptr(slot_mapping), T, Hkv, D, int(k_cache.shape[1]), _ptr(k_cache),
+                            _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kvd, _pages(k_cache, num_pages), _ptr(error_word),
+                            _stream(stream))
+    _check("hpc_kv_write", rc)
+
+
+def hpc_kv_read(k_cache, v_cache, page_table, out_starts, k_out, v_out, k_scale=None, v_scale=None, first=None,
+                num_pages: int | None = None, error_word=None, stream=None):
+    """Tokens first[b], first[b] + 1, ... of each request into rows
+    [out_starts[b], out_starts[b + 1]) of k_out and v_out (bf16 [rows, Hkv, 128])."""
+    kvd = _check_caches("hpc_kv_read", k_cache, v_cache, k_scale, v_scale)
+    _cuda_i32(page_table, "page_table")
+    _cuda_i32(out_starts, "out_starts")
+    B = page_table.shape[0]
+    if page_table.dim() != 2 or out_starts.numel() != B + 1:
+        raise HpcError("hpc_kv_read", detail="page_table must be [batch, pages] and out_starts hold batch + 1 rows")
+    if first is not None and _cuda_i32(first, "first").numel() != B:
+        raise HpcError("first", detail=f"must hold {B} positions")
+    _same_device("hpc_kv_read", k_cache, v_cache, k_scale, v_scale, page_table, out_starts, first, k_out, v_out, error_word)
+    rows = k_out.shape[0]
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        _check_out(n, t, (rows, k_cache.shape[2], HEAD_DIM), torch.bfloat16)
+    rc = lib().hpc_kv_read(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kvd, _pages(k_cache, num_pages),
+                           _ptr(page_table), int(page_table.shape[1]), _ptr(first), _ptr(out_starts), B, rows,
+                           int(k_cache.shape[2]), HEAD_DIM, int(k_cache.shape[1]), _ptr(k_out), _ptr(v_out),
+                           _ptr(error_word), _stream(stream))
+    _check("hpc_kv_read", rc)

@@ -1,0 +1,276 @@
+// extern "C" entry points of prompt attention, shared-prefix attention and the
+// cache write / read calls (declared in include/hpc_decode.h): host-side argument
+// checks, then the launches in tile_plan.cu, tile_attn.cu, tile_combine.cu and
+// kv.cu. Nothing here allocates or synchronises, except hpc_tile_read_error.
+#include "kv.cuh"
+#include "tile.cuh"
+
+using namespace hpc;
+
+namespace {
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+inline hpc_status launched(cudaError_t e) {
+    if (e == cudaErrorInvalidValue) return HPC_ERR_INVALID_ARG;
+    return e == cudaSuccess ? HPC_OK : HPC_ERR_CUDA;
+}
+
+bool seqs_ok(int num_seqs, int num_ctas) {
+    return num_seqs >= 1 && num_seqs <= HPC_MAX_BATCH && num_ctas >= 1 && num_ctas <= HPC_MAX_TILE_CTAS;
+}
+
+bool heads_ok(int num_kv_heads) { return num_kv_heads >= 1 && num_kv_heads <= HPC_MAX_KV_HEADS; }
+
+// Tile numbers over all heads stay in int32.
+bool tokens_ok(int num_tokens, int num_seqs, int num_kv_heads) {
+    return num_tokens >= 0 && ((long long)num_tokens / kTileTokens + num_seqs) * num_kv_heads < 2147483647LL;
+}
+
+hpc_status plan_common(const int32_t* d_starts, const int32_t* d_lens, int num_seqs, int num_tokens, int num_kv_heads,
+                       int table_stride, int num_ctas, int min_blocks, int mode, int q_len, hpc_tile_plan* plan,
+                       void* stream) {
+    if (!d_starts || !d_lens || !plan || !plan->buf || !aligned(plan->buf, 16) || min_blocks < 0 || table_stride < 1)
+        return HPC_ERR_INVALID_ARG;
+    if (!seqs_ok(num_seqs, num_ctas) || !heads_ok(num_kv_heads) || !tokens_ok(num_tokens, num_seqs, num_kv_heads))
+        return HPC_ERR_INVALID_ARG;
+    if (plan->bytes < hpc_tile_plan_bytes(num_seqs, num_ctas)) return HPC_ERR_WORKSPACE_TOO_SMALL;
+    plan->num_seqs = num_seqs;
+    plan->num_tokens = num_tokens;
+    plan->num_kv_heads = num_kv_heads;
+    plan->num_ctas = num_ctas;
+    plan->mode = mode;
+    plan->q_len = q_len;
+    plan->table_stride = table_stride;
+    const long long max_len = (long long)table_stride * kChunk;
+    return launched(launch_tile_plan(d_starts, d_lens, num_seqs, num_tokens, num_kv_heads, num_ctas, min_blocks,
+                                     max_len > 2147483647LL ? 2147483647 : (int)max_len, mode, q_len, plan->buf,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+hpc_status plan_check(const hpc_tile_plan* plan, int mode, int num_kv_heads) {
+    if (!plan || !plan->buf || plan->mode != mode || plan->num_kv_heads != num_kv_heads) return HPC_ERR_INVALID_ARG;
+    if (!seqs_ok(plan->num_seqs, plan->num_ctas) || plan->bytes < hpc_tile_plan_bytes(plan->num_seqs, plan->num_ctas))
+        return HPC_ERR_INVALID_ARG;
+    return HPC_OK;
+}
+
+hpc_status shape_check(int num_q_heads, int num_kv_heads, int head_dim, int page_size) {
+    if (num_q_heads < 1 || !heads_ok(num_kv_heads)) return HPC_ERR_INVALID_ARG;
+    if (head_dim != kHeadDim || page_size != kChunk || num_q_heads != kGroup * num_kv_heads) return HPC_ERR_UNSUPPORTED;
+    return HPC_OK;
+}
+
+hpc_status cache_check(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int kv_dtype,
+                       int num_pages, int num_kv_heads) {
+    if (kv_dtype != HPC_KV_BF16 && kv_dtype != HPC_KV_FP8_E4M3) return HPC_ERR_UNSUPPORTED;
+    const bool fp8 = kv_dtype == HPC_KV_FP8_E4M3;
+    if (!k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16)) return HPC_ERR_INVALID_ARG;
+    if (fp8 && (!k_scale || !v_scale || !aligned(k_scale, 16) || !aligned(v_scale, 16))) return HPC_ERR_INVALID_ARG;
+    // token and scale-row coordinates, one page past the pool included
+    if (num_pages < 1 || ((long long)num_pages + 1) * kChunk > 2147483647LL ||
+        ((long long)num_pages + 1) * num_kv_heads > 2147483647LL)
+        return HPC_ERR_INVALID_ARG;
+    return HPC_OK;
+}
+
+hpc_status attn_common(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                       const float* v_scale, int kv_dtype, int num_pages, const int32_t* table, int table_stride,
+                       int num_q_heads, int num_kv_heads, int head_dim, int page_size, const hpc_tile_plan* plan, int mode,
+                       float* split_o, float* split_lse, void* out, float* out_lse, void* stream) {
+    hpc_status st = shape_check(num_q_heads, num_kv_heads, head_dim, page_size);
+    if (st != HPC_OK) return st;
+    if ((st = cache_check(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, num_kv_heads)) != HPC_OK) return st;
+    if ((st = plan_check(plan, mode, num_kv_heads)) != HPC_OK) return st;
+    if (!q || !aligned(q, 16) || !table || table_stride != plan->table_stride) return HPC_ERR_INVALID_ARG;
+    if (!split_o || !split_lse || !aligned(split_o, 16)) return HPC_ERR_INVALID_ARG;
+    if (mode == kModePrefill && (!out || !aligned(out, 16))) return HPC_ERR_INVALID_ARG;
+    if (plan->num_tokens == 0) return HPC_OK;
+    const bool fp8 = kv_dtype == HPC_KV_FP8_E4M3;
+    TileAttnArgs a;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = fp8 ? k_scale : nullptr;
+    a.v_scale = fp8 ? v_scale : nullptr;
+    a.fp8 = fp8;
+    a.num_pages = num_pages;
+    a.page_table = table;
+    a.pt_stride = table_stride;
+    a.S = plan->num_seqs;
+    a.num_tokens = plan->num_tokens;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.plan = plan->buf;
+    a.num_ctas = plan->num_ctas;
+    a.mode = mode;
+    a.split_o = split_o;
+    a.split_lse = split_lse;
+    a.out = out;
+    a.out_lse = out_lse;
+    return launched(launch_tile_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t hpc_tile_plan_bytes(int num_seqs, int num_ctas) {
+    if (!seqs_ok(num_seqs, num_ctas)) return 0;
+    return (size_t)tile_layout(num_seqs, num_ctas).total_ints * sizeof(int32_t);
+}
+
+int hpc_tile_default_num_ctas(void) { return tile_default_ctas(); }
+
+size_t hpc_prefill_split_rows(int num_ctas) {
+    if (!seqs_ok(1, num_ctas)) return 0;
+    return (size_t)2 * num_ctas * kTileRows;
+}
+
+size_t hpc_prefix_split_rows(int num_groups, int batch, int q_len, int num_kv_heads, int num_ctas) {
+    if (!seqs_ok(num_groups, num_ctas) || batch < 1 || batch > HPC_MAX_BATCH || q_len < 1 || q_len > HPC_MAX_Q_LEN ||
+        !heads_ok(num_kv_heads))
+        return 0;
+    // every group has at most one tile that is not full
+    const long long tiles = ((long long)batch * q_len / kTileTokens + num_groups) * num_kv_heads;
+    return (size_t)(tiles + num_ctas) * kTileRows;
+}
+
+hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens, int batch, int num_tokens,
+                            int num_kv_heads, int page_table_stride, int num_ctas, int min_blocks_per_cta,
+                            hpc_tile_plan* plan, void* stream) {
+    return plan_common(d_q_starts, d_seq_lens, batch, num_tokens, num_kv_heads, page_table_stride, num_ctas,
+                       min_blocks_per_cta, kModePrefill, 1, plan, stream);
+}
+
+hpc_status hpc_prefix_plan(const int32_t* d_group_starts, const int32_t* d_prefix_lens, int num_groups, int batch,
+                           int q_len, int num_kv_heads, int prefix_table_stride, int num_ctas, int min_blocks_per_cta,
+                           hpc_tile_plan* plan, void* stream) {
+    if (batch < 1 || batch > HPC_MAX_BATCH || q_len < 1 || q_len > HPC_MAX_Q_LEN) return HPC_ERR_INVALID_ARG;
+    return plan_common(d_group_starts, d_prefix_lens, num_groups, batch * q_len, num_kv_heads, prefix_table_stride,
+                       num_ctas, min_blocks_per_cta, kModePrefix, q_len, plan, stream);
+}
+
+hpc_status hpc_prefill_attn(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, int kv_dtype, int num_pages, const int32_t* page_table,
+                            int page_table_stride, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                            const hpc_tile_plan* plan, float* split_o, float* split_lse, void* out, float* out_lse,
+                            void* stream) {
+    return attn_common(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, page_table, page_table_stride,
+                       num_q_heads, num_kv_heads, head_dim, page_size, plan, kModePrefill, split_o, split_lse, out,
+                       out_lse, stream);
+}
+
+hpc_status hpc_prefill_combine(const hpc_tile_plan* plan, const float* split_o, const float* split_lse, void* out,
+                               float* out_lse, int num_q_heads, int num_kv_heads, int head_dim, void* stream) {
+    hpc_status st = shape_check(num_q_heads, num_kv_heads, head_dim, kChunk);
+    if (st != HPC_OK) return st;
+    if ((st = plan_check(plan, kModePrefill, num_kv_heads)) != HPC_OK) return st;
+    if (!split_o || !split_lse || !out || !aligned(split_o, 16) || !aligned(out, 16)) return HPC_ERR_INVALID_ARG;
+    if (plan->num_tokens == 0) return HPC_OK;
+    return launched(launch_prefill_combine(plan->buf, plan->num_seqs, num_q_heads, plan->num_ctas, split_o, split_lse,
+                                           out, out_lse, static_cast<cudaStream_t>(stream)));
+}
+
+hpc_status hpc_prefix_attn(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, int kv_dtype, int num_pages, const int32_t* prefix_table,
+                           int prefix_table_stride, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                           const hpc_tile_plan* plan, float* split_o, float* split_lse, void* stream) {
+    return attn_common(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, prefix_table, prefix_table_stride,
+                       num_q_heads, num_kv_heads, head_dim, page_size, plan, kModePrefix, split_o, split_lse, nullptr,
+                       nullptr, stream);
+}
+
+hpc_status hpc_prefix_combine(const hpc_tile_plan* prefix_plan, const float* prefix_o, const float* prefix_lse,
+                              const hpc_plan* plan, const float* split_o, const float* split_lse, void* out,
+                              float* out_lse, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                              void* stream) {
+    hpc_status st = shape_check(num_q_heads, num_kv_heads, head_dim, kChunk);
+    if (st != HPC_OK) return st;
+    if ((st = plan_check(prefix_plan, kModePrefix, num_kv_heads)) != HPC_OK) return st;
+    if (q_len < 1 || q_len > HPC_MAX_Q_LEN || q_len != prefix_plan->q_len) return HPC_ERR_INVALID_ARG;
+    if (batch < 1 || (long long)batch * q_len != prefix_plan->num_tokens) return HPC_ERR_INVALID_ARG;
+    if (!plan || !plan->buf || plan->batch != batch || plan->num_kv_heads != num_kv_heads || plan->num_ctas < 1 ||
+        plan->bytes < hpc_decode_plan_bytes(batch, num_kv_heads, plan->num_ctas))
+        return HPC_ERR_INVALID_ARG;
+    if (!prefix_o || !prefix_lse || !split_o || !split_lse || !out || !aligned(prefix_o, 16) || !aligned(split_o, 16) ||
+        !aligned(out, 8))
+        return HPC_ERR_INVALID_ARG;
+    return launched(launch_prefix_combine(prefix_plan->buf, prefix_plan->num_seqs, prefix_plan->num_ctas, prefix_o,
+                                          prefix_lse, plan->buf, plan->num_ctas, split_o, split_lse,
+                                          static_cast<__nv_bfloat16*>(out), out_lse, batch, num_q_heads, num_kv_heads,
+                                          q_len, static_cast<cudaStream_t>(stream)));
+}
+
+hpc_status hpc_kv_write(const void* k, const void* v, long long k_token_stride, long long v_token_stride,
+                        const int32_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim, int page_size,
+                        void* k_cache, void* v_cache, float* k_scale, float* v_scale, int kv_dtype, int num_pages,
+                        int* d_error_word, void* stream) {
+    if (head_dim != kHeadDim || page_size != kChunk) return HPC_ERR_UNSUPPORTED;
+    if (num_tokens < 0 || !heads_ok(num_kv_heads)) return HPC_ERR_INVALID_ARG;
+    hpc_status st = cache_check(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, num_kv_heads);
+    if (st != HPC_OK) return st;
+    if (!k || !v || !slot_mapping || !aligned(k, 16) || !aligned(v, 16)) return HPC_ERR_INVALID_ARG;
+    // rows of 16-byte pieces; a stride shorter than a token's heads would be a mistake
+    const long long row = (long long)num_kv_heads * kHeadDim;
+    if (k_token_stride < row || v_token_stride < row || k_token_stride % 8 != 0 || v_token_stride % 8 != 0)
+        return HPC_ERR_INVALID_ARG;
+    if (num_tokens == 0) return HPC_OK;
+    KvWriteArgs a;
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.k_stride = k_token_stride;
+    a.v_stride = v_token_stride;
+    a.slots = slot_mapping;
+    a.num_tokens = num_tokens;
+    a.num_kv_heads = num_kv_heads;
+    a.num_pages = num_pages;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.err = d_error_word;
+    return launched(launch_kv_write(a, kv_dtype == HPC_KV_FP8_E4M3, static_cast<cudaStream_t>(stream)));
+}
+
+hpc_status hpc_kv_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int kv_dtype,
+                       int num_pages, const int32_t* page_table, int page_table_stride, const int32_t* first,
+                       const int32_t* out_starts, int batch, int num_rows, int num_kv_heads, int head_dim, int page_size,
+                       void* k_out, void* v_out, int* d_error_word, void* stream) {
+    if (head_dim != kHeadDim || page_size != kChunk) return HPC_ERR_UNSUPPORTED;
+    if (batch < 1 || batch > HPC_MAX_BATCH || num_rows < 0 || !heads_ok(num_kv_heads) || page_table_stride < 1)
+        return HPC_ERR_INVALID_ARG;
+    hpc_status st = cache_check(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, num_kv_heads);
+    if (st != HPC_OK) return st;
+    if (!page_table || !out_starts || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16))
+        return HPC_ERR_INVALID_ARG;
+    if (num_rows == 0) return HPC_OK;
+    KvReadArgs a;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.page_table = page_table;
+    a.pt_stride = page_table_stride;
+    a.first = first;
+    a.out_starts = out_starts;
+    a.batch = batch;
+    a.num_rows = num_rows;
+    a.num_kv_heads = num_kv_heads;
+    a.num_pages = num_pages;
+    a.k_out = static_cast<__nv_bfloat16*>(k_out);
+    a.v_out = static_cast<__nv_bfloat16*>(v_out);
+    a.err = d_error_word;
+    return launched(launch_kv_read(a, kv_dtype == HPC_KV_FP8_E4M3, static_cast<cudaStream_t>(stream)));
+}
+
+hpc_status hpc_tile_read_error(const hpc_tile_plan* plan, int* device_error_word) {
+    if (!plan || !plan->buf || !device_error_word) return HPC_ERR_INVALID_ARG;
+    if (cudaDeviceSynchronize() != cudaSuccess) return HPC_ERR_CUDA;
+    int w = 0;
+    if (cudaMemcpy(&w, plan->buf + kTError, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return HPC_ERR_CUDA;
+    *device_error_word = w;
+    return w ? HPC_ERR_DEVICE_CHECK : HPC_OK;
+}
+
+}  // extern "C"

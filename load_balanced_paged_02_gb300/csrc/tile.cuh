@@ -1,0 +1,211 @@
+// Tile maps: the work of prompt attention (hpc_prefill_*) and of shared-prefix
+// attention (hpc_prefix_*) as tiles of 32 query tokens x the 8 query heads of
+// one KV head, each over a run of 128-token KV blocks. Layout of the map and
+// the walk over it, shared by the planner, the attention kernel and the
+// kernels that merge split tiles.
+//
+// Sequence s (a prompt, or a group of requests behind one prefix) has n query
+// tokens and L keys. Tile i holds query tokens [32 i, min(n, 32 i + 32)) and
+//   prompts:  the keys before L - n + min(n, 32 i + 32) (causal: query token t
+//             sits at position L - n + t), at least one block, so that rows
+//             without a visible key are written too;
+//   prefixes: all L keys (no tile where L is 0).
+// The walk is KV head by KV head, sequence by sequence, tile by tile, block by
+// block; CTA j gets units [j * bucket, (j + 1) * bucket) of it, where a tile is
+// kTileCost[mode] units of fixed cost followed by one unit per block. A
+// boundary inside the fixed cost is a boundary before block 0.
+#pragma once
+
+#include "hpc_internal.cuh"
+
+namespace hpc {
+
+constexpr int kTileTokens = 32;                   // query tokens of a tile
+constexpr int kTileRows = kTileTokens * kGroup;   // 256 query rows
+constexpr int kBlock = 128;                       // keys of a block: two pages
+constexpr int kModePrefill = 0, kModePrefix = 1;
+
+enum TileHdrSlot {
+    kTUnitsPerHead = 0,   // int64
+    kTBucket = 2,         // int64
+    kTUsedCtas = 4,
+    kTBatch = 5,
+    kTNumKvHeads = 6,
+    kTNumCtas = 7,
+    kTNumTokens = 8,
+    kTMode = 9,
+    kTTilesPerHead = 10,
+    kTQLen = 11,
+    kTError = 12,
+};
+
+// Offsets (int32 units) of the sections of a tile map.
+struct TileLayout {
+    long long starts, seqs, units, total_ints;
+};
+
+__host__ __device__ inline TileLayout tile_layout(long long S, long long C) {
+    TileLayout L;
+    L.starts = kHdrInts;                      // [C + 1] rows of 8: {kv head, sequence, tile, block, tile number, 0, 0, 0}
+    L.seqs = L.starts + (C + 1) * 8;          // [S] rows of 4: {first query token, n, L, tiles of the sequences before}
+    L.units = L.seqs + S * 4;                 // int64 [S + 1]: units of the sequences before
+    L.total_ints = L.units + (S + 1) * 2;
+    return L;
+}
+
+__host__ __device__ inline int tile_cost(int mode) { return mode == kModePrefill ? 1 : 0; }
+
+__host__ __device__ inline int tile_count(int n) { return (n + kTileTokens - 1) / kTileTokens; }
+
+// Blocks of tile i.
+__host__ __device__ inline int tile_blocks(int mode, int n, int L, int i) {
+    if (mode == kModePrefix) return (int)(((long long)L + kBlock - 1) / kBlock);
+    const long long t1 = (long long)kTileTokens * (i + 1) < n ? (long long)kTileTokens * (i + 1) : n;
+    const long long e = (long long)L - n + t1;  // keys the tile's last query token sees
+    return e <= kBlock ? 1 : (int)((e + kBlock - 1) / kBlock);
+}
+
+// sum of max(1, floor(m / 4)) over m < x, up to a constant
+__host__ __device__ inline long long quarter_sum(long long x) {
+    if (x <= 8) return x;
+    const long long q = x >> 2, s = x & 3;
+    return 8 + (2 * q * (q - 1) + s * q) - 4;  // sum of floor(m / 4) over 8 <= m < x, plus 8
+}
+
+// Units of tiles [0, i) of a sequence, i <= tile_count(n). Every tile but the
+// last has 32 query tokens, so tile j's last key is at L - n + 32 (j + 1) and it
+// has max(1, floor((a + j) / 4)) blocks with a = floor((L - n + 159) / 32).
+__host__ __device__ inline long long tile_units(int mode, int n, int L, int i) {
+    if (i <= 0) return 0;
+    if (mode == kModePrefix) return (long long)i * tile_blocks(mode, n, L, 0);
+    const int nt = tile_count(n);
+    const int full = i < nt ? i : nt - 1;
+    const long long x = (long long)L - n + 159;
+    const long long a = x >= 0 ? x / kTileTokens : -((-x + kTileTokens - 1) / kTileTokens);
+    long long u = quarter_sum(a + full) - quarter_sum(a) + (long long)i * tile_cost(mode);
+    if (i == nt) u += tile_blocks(mode, n, L, nt - 1);
+    return u;
+}
+
+// ----------------------------------------------------------------- launchers
+
+cudaError_t launch_tile_plan(const int32_t* q_starts, const int32_t* lens, int S, int num_tokens, int Hkv, int C,
+                             int min_blocks, int max_len, int mode, int q_len, int32_t* buf, cudaStream_t s);
+
+struct TileAttnArgs {
+    const void* q;  // bf16 [num_tokens][Hq][128]
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    int fp8;
+    int num_pages;
+    const int32_t* page_table;
+    int pt_stride;
+    int S, num_tokens, num_q_heads, num_kv_heads;
+    int32_t* plan;
+    int num_ctas, mode;
+    float* split_o;
+    float* split_lse;
+    void* out;       // prompts only
+    float* out_lse;  // prompts only, nullable
+};
+cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s);
+int tile_default_ctas();
+
+cudaError_t launch_prefill_combine(const int32_t* plan, int S, int Hq, int C, const float* split_o, const float* split_lse,
+                                   void* out, float* out_lse, cudaStream_t s);
+
+cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_ctas, const float* prefix_o,
+                                  const float* prefix_lse, const int32_t* plan, int ctas, const float* split_o,
+                                  const float* split_lse, __nv_bfloat16* out, float* out_lse, int B, int Hq, int Hkv,
+                                  int q_len, cudaStream_t s);
+
+#if defined(__CUDACC__)
+
+struct TilePos {
+    int h, s, i, blk;
+};
+
+// One piece of work: blocks [b0, b1) of tile i of sequence s for KV head h.
+struct TileItem {
+    int h, i, s;
+    int q0, n, L;    // the sequence's first query token, its query tokens and keys
+    int b0, b1;
+    int whole;       // all of the tile's blocks
+    int tile;        // number of the tile in the walk
+};
+
+// Walks the items of one CTA's part of the map.
+struct TileWalk {
+    const int4* seqs;
+    int S, mode, tiles_per_head;
+    TilePos at, end;
+
+    __device__ __forceinline__ void start(const int32_t* plan, int S_, int mode_, int cta, long long seqs_off) {
+        const int4* st = reinterpret_cast<const int4*>(plan + kHdrInts + (long long)cta * 8);
+        const int4 a = st[0], e = st[2];
+        at = TilePos{a.x, a.y, a.z, a.w};
+        end = TilePos{e.x, e.y, e.z, e.w};
+        seqs = reinterpret_cast<const int4*>(plan + seqs_off);
+        S = S_;
+        mode = mode_;
+        tiles_per_head = plan[kTTilesPerHead];
+    }
+
+    // The next item; false at the end of the CTA's part.
+    __device__ __forceinline__ bool next(TileItem& it) {
+        for (;;) {
+            const bool last = at.h == end.h && at.s == end.s && at.i == end.i;
+            if (last && at.blk >= end.blk) return false;
+            const int4 q = seqs[at.s];
+            const int blocks = tile_blocks(mode, q.y, q.z, at.i);
+            it.h = at.h;
+            it.s = at.s;
+            it.i = at.i;
+            it.q0 = q.x;
+            it.n = q.y;
+            it.L = q.z;
+            it.b0 = at.blk;
+            it.b1 = last ? end.blk : blocks;
+            it.whole = it.b0 == 0 && it.b1 == blocks;
+            it.tile = at.h * tiles_per_head + q.w + at.i;
+            if (last) {
+                at.blk = end.blk;
+            } else {
+                at.blk = 0;
+                if (++at.i >= tile_count(q.y)) {
+                    at.i = 0;
+                    // the next sequence that has tiles (the walk ends at `end`, which
+                    // has, or at the head after the last)
+                    do {
+                        if (++at.s >= S) {
+                            at.s = 0;
+                            ++at.h;
+                        }
+                        if (at.h > end.h || (at.h == end.h && at.s > end.s)) {
+                            at = end;
+                            break;
+                        }
+                        if (at.h == end.h && at.s == end.s) break;
+                        const int4 x = seqs[at.s];
+                        if (x.y > 0 && (mode == kModePrefill || x.z > 0)) break;
+                    } while (true);
+                }
+            }
+            if (it.b1 > it.b0) return true;
+        }
+    }
+};
+
+// Row of the split buffers where a piece of a tile goes, in units of kTileRows
+// rows. Prompts: only cut tiles have pieces; a CTA has at most one that goes on
+// from the CTA before and one that starts there. Prefixes: every piece; from one
+// piece to the next the tile number, the CTA number or both grow.
+__device__ __forceinline__ long long tile_slot(int mode, int cta, const TileItem& it) {
+    return mode == kModePrefill ? 2LL * cta + (it.b0 == 0 ? 1 : 0) : (long long)it.tile + cta;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace hpc

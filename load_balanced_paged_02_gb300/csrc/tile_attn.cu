@@ -1,0 +1,861 @@
+// Prompt attention and shared-prefix attention on the fifth-generation tensor
+// cores, over the paged cache. Both are the same product: a tile of 32 query
+// tokens x 8 query heads (256 rows, two halves of 128) against a run of
+// 128-token KV blocks, with the running maximum and sum of a softmax:
+//   S_j = Q K_j^T,  m = max(m, rowmax S_j),  P_j = exp(S_j - m),
+//   l += rowsum P_j,  O += P_j V_j   (O and l scaled when m moves),
+// then O / l and m + ln l. Prompts add the causal limit (query token t of a
+// sequence of n tokens and L keys sees keys [0, L - n + t]); a prefix is seen
+// whole by every row of its group. A tile map (tile.cuh) gives every CTA an
+// equal run of blocks; a tile that falls to one CTA is written to the output,
+// a cut one (and every prefix piece) as normalised float32 rows with their LSE,
+// which the kernels in tile_combine.cu merge.
+//
+// One CTA per SM, 12 warps (e4m3: 16):
+//  * warps 0-3 and 4-7, the softmax warpgroups of the two halves: one thread
+//    per query row. Scores come from TMEM, P goes back over them as 16-bit
+//    pairs (the A operand of the second product), O is scaled in TMEM only when
+//    a row's maximum has grown by more than 2^8 since its reference was taken.
+//  * warp 8, producer: one thread issues TMA copies of the tile's query rows
+//    and of K_0 V_0 K_1 V_1 ... into a ring of stages, pages through the table.
+//  * warp 9, issuer: one thread issues the MMAs in the order
+//      S0(0) S1(0) | PV0(0) S0(1) PV1(0) S1(1) | PV0(1) ...
+//    so that one half's products run while the other half's softmax does. MMAs
+//    of one thread run in order, so S(j+1) may overwrite P(j) once PV(j) has
+//    been issued.
+//  * e4m3, warps 12-15: the query rows split into two e4m3 tiles of codes
+//    (Q = (Q_hi + Q_lo) 2^e, as in attn_tc.cu), so that Q K^T runs on the K
+//    codes as they are; V widened to f16 (code x scale) into a ring of its own.
+// Every wait is bounded; on expiry the CTA records HPC_DEVERR_WAIT_TIMEOUT.
+#include <atomic>
+#include <cstring>
+
+#include "attn_common.cuh"
+#include "tcgen05.cuh"
+#include "tile.cuh"
+
+namespace hpc {
+namespace {
+
+using attn::kDrainLimitNs;
+using attn::kLn2;
+using attn::kNegInf;
+using attn::kWaitLimitNs;
+using attn::wait_bounded;
+
+constexpr int kHalfRows = 128;
+constexpr int kHalfTokens = kTileTokens / 2;
+constexpr int kQBytes = 32768;           // a half's query rows: [2 dim halves][128 rows][128 B]
+constexpr float kRescaleLog2 = 8.0f;     // lazy rescale threshold: P <= 2^8
+constexpr int kMetaRing = 8;             // blocks whose page checks (and, e4m3, K scales) are kept
+constexpr uint32_t kTmemCols = 512;      // S of half t at column 128 t (P over its first 64), O at 256 + 128 t
+
+template <bool FP8>
+struct Cfg {
+    static constexpr int kStages = 5;
+    static constexpr int kStageBytes = FP8 ? 16384 : 32768;  // 128 tokens of K or of V
+    static constexpr int kWide = FP8 ? 2 : 0;                // f16 V tiles of 32 KB
+    static constexpr int kWarps = FP8 ? 16 : 12;
+    static constexpr int kThreads = kWarps * 32;
+    // registers per thread after the split (setmaxnreg): the launch's total, 384 x
+    // 168 or 512 x 128, is what the two softmax warpgroups and the others share
+    static constexpr int kRegsSoftmax = FP8 ? 184 : 208;
+    static constexpr int kRegsOther = FP8 ? 72 : 88;
+    static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * (FP8 ? 128 : 168), "register split");
+};
+
+template <bool FP8>
+struct Smem {
+    using C = Cfg<FP8>;
+    static constexpr size_t kQ = 0;
+    static constexpr size_t kRing = kQ + 2 * kQBytes;
+    static constexpr size_t kWide = kRing + (size_t)C::kStages * C::kStageBytes;
+    static constexpr size_t kKs = kWide + (size_t)C::kWide * 32768;            // float [ring][128] K scales
+    static constexpr size_t kVs = kKs + (FP8 ? kMetaRing * 512 : 0);           // float [ring][128] V scales
+    static constexpr size_t kQs = kVs + (FP8 ? kMetaRing * 512 : 0);           // float [2 parities][2 halves][128]
+    static constexpr size_t kMeta = kQs + (FP8 ? 2048 : 0);
+    static constexpr size_t kBars = kMeta + kMetaRing * 4;
+    // full, empty (stages); qfull, qempty, sfull, pfull, ofull, ofree (halves); e4m3: q8full (halves), wfull, wempty
+    static constexpr int kNumBars = 2 * C::kStages + 12 + (FP8 ? 6 : 0);
+    static constexpr size_t kTmemSlot = kBars + kNumBars * 8;
+    static constexpr size_t kFlag = kTmemSlot + 8;
+    static constexpr size_t kAlloc = kFlag + 8 + 1024;
+    static_assert(kAlloc <= 232448, "over the 227 KB shared-memory limit of a CTA");
+};
+
+// A whole warp waits; one answer for all its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, kWaitLimitNs));
+}
+
+struct TileParams {
+    const int32_t* plan;
+    long long seqs_off;
+    const int32_t* page_table;
+    long long pt_stride;
+    int* err;
+    int S, mode, num_q_heads, num_pages, num_kv_heads;
+    float* split_o;
+    float* split_lse;
+    __nv_bfloat16* out;
+    float* out_lse;
+    float scale_log2;
+};
+
+__device__ __forceinline__ void tma_load_3d_plain(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                                  int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_plain(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// D (TMEM) (+)= A . B^T with A (16-bit, K-major) in TMEM: lane = row, two
+// elements of K per column.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// 32 columns of this thread's lane (32x32b shape: thread t of a warp holds lane t
+// of the warp's quarter).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+          "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+          "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]),
+        "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]),
+        "f"(r[18]), "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]),
+        "f"(r[27]), "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// (a.x b.x + c.x, a.y b.y + c.y) and (a.x + b.x, a.y + b.y) in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Barrier 1 over the 128 threads of warps 12-15.
+__device__ __forceinline__ void named_sync_128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool named_any_128(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.red.or.pred.aligned q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+// One half's bf16 query rows -> e4m3 hi / lo tiles in place ([128 rows][128 B]
+// each) and their power-of-two row scales. Lane pair (2 j, 2 j + 1) of warp wq
+// takes row 32 wq + j + 16 u, u < 2; half hh = lane & 1 reads bf16 dims
+// [64 hh, 64 hh + 64), which sit where row r of the hi tile (hh = 0) or of the lo
+// tile (hh = 1) goes, and writes the hi and lo codes of its dims once both have
+// read.
+__device__ __forceinline__ void split_query_rows(uint8_t* qt, float* qs, int wq, int lane) {
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+        const int r = 32 * wq + 16 * u + (lane >> 1), hh = lane & 1;
+        uint4 raw[8];
+        float amax = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            raw[c] = *reinterpret_cast<const uint4*>(qt + hh * 16384 + r * 128 + ((c ^ (r & 7)) << 4));
+            const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        __syncwarp();  // the partner lane has read its half row
+        // the smallest power of two 2^ex with amax / 2^ex <= 448: q / 2^ex is exact
+        // (rows under 2^-90 keep fewer bits: their scores are 0 to float32 anyway; an
+        // infinite element makes the row's scores infinite or NaN)
+        float qscale = 1.f, qinv = 1.f;
+        if (amax > 3.4e38f) {
+            qscale = amax;
+        } else if (amax > 0.f) {
+            int e;
+            const float m = frexpf(amax * (1.f / 448.f), &e);
+            const int ex = max(m == 0.5f ? e - 1 : e, -100);
+            qscale = ldexpf(1.f, ex);
+            qinv = ldexpf(1.f, -ex);
+        }
+        if (hh == 0) qs[r] = qscale;
+#pragma unroll
+        for (int c2 = 0; c2 < 4; ++c2) {
+            uint2 hp[2], lp[2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const uint4 x4 = raw[2 * c2 + v];
+                const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[2 * j] = __uint_as_float(w[j] << 16) * qinv;
+                    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * qinv;
+                }
+                split_e4m3x8(x, hp[v], lp[v]);
+            }
+            const int off = r * 128 + (((4 * hh + c2) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(qt + off) = make_uint4(hp[0].x, hp[0].y, hp[1].x, hp[1].y);
+            *reinterpret_cast<uint4*>(qt + 16384 + off) = make_uint4(lp[0].x, lp[0].y, lp[1].x, lp[1].y);
+        }
+        __syncwarp();
+    }
+}
+
+// 128 tokens of V codes -> an f16 tile (code x scale, rounded to f16; rows from
+// nv on zero), [2 dim halves][128 rows][128 B] swizzled. The scale is taken as
+// (f 2^a) (2^b) with 1 <= |f| < 2, so that a scale far below f16's smallest normal
+// number keeps its bits until the last product. Thread tg takes the 16-code
+// pieces (tg & 3) + 4 hf of rows 32 rr + tg / 4: loads and stores of a warp spread
+// over all banks.
+__device__ __forceinline__ void widen_v(const uint8_t* codes, const float* vs, uint8_t* wide, int nv, int tg) {
+#pragma unroll 2
+    for (int rr = 0; rr < 4; ++rr) {
+        const int row = 32 * rr + (tg >> 2);
+        const bool in = row < nv;
+        const uint32_t sb = in ? __float_as_uint(vs[row]) : 0u;
+        const int e = (int)((sb >> 23) & 255u) - 127, a = e < -14 ? -10 : 0;
+        // f 2^a (NaN or infinity stay what they are) and 2^b, b = e - a (0 where it underflows)
+        const float fa = e == 128 ? __uint_as_float(sb)
+                                  : __uint_as_float((sb & 0x807fffffu) | (uint32_t)(127 + a) << 23);
+        const float fb = e == 128 ? 1.f : __uint_as_float((uint32_t)max(e - a + 127, 0) << 23);
+        const uint32_t s2 = pack_f16x2(fa, fa), p2 = pack_f16x2(fb, fb);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int c16 = (tg & 3) + 4 * hf;
+            uint4 vl = make_uint4(0, 0, 0, 0), vh = vl;
+            if (in) {
+                const uint4 w = *reinterpret_cast<const uint4*>(codes + row * 128 + ((c16 ^ (row & 7)) << 4));
+                e4m3x4_to_f16x2x2(w.x, vl.x, vl.y);
+                e4m3x4_to_f16x2x2(w.y, vl.z, vl.w);
+                e4m3x4_to_f16x2x2(w.z, vh.x, vh.y);
+                e4m3x4_to_f16x2x2(w.w, vh.z, vh.w);
+                vl.x = hmul2_u32(hmul2_u32(vl.x, s2), p2), vl.y = hmul2_u32(hmul2_u32(vl.y, s2), p2);
+                vl.z = hmul2_u32(hmul2_u32(vl.z, s2), p2), vl.w = hmul2_u32(hmul2_u32(vl.w, s2), p2);
+                vh.x = hmul2_u32(hmul2_u32(vh.x, s2), p2), vh.y = hmul2_u32(hmul2_u32(vh.y, s2), p2);
+                vh.z = hmul2_u32(hmul2_u32(vh.z, s2), p2), vh.w = hmul2_u32(hmul2_u32(vh.w, s2), p2);
+            }
+            const int f0 = 2 * (tg & 3);
+            *reinterpret_cast<uint4*>(wide + hf * 16384 + row * 128 + ((f0 ^ (row & 7)) << 4)) = vl;
+            *reinterpret_cast<uint4*>(wide + hf * 16384 + row * 128 + (((f0 + 1) ^ (row & 7)) << 4)) = vh;
+        }
+    }
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
+    tile_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
+                     const __grid_constant__ CUtensorMap tm_vs, const TileParams p) {
+    using C = Cfg<FP8>;
+    using LY = Smem<FP8>;
+    constexpr int NS = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem =
+        reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + LY::kBars);
+    uint64_t* empty = full + NS;
+    uint64_t* qfull = empty + NS;
+    uint64_t* qempty = qfull + 2;
+    uint64_t* sfull = qempty + 2;
+    uint64_t* pfull = sfull + 2;
+    uint64_t* ofull = pfull + 2;
+    uint64_t* ofree = ofull + 2;
+    uint64_t* q8full = ofree + 2;  // e4m3 from here on
+    uint64_t* wfull = q8full + 2;
+    uint64_t* wempty = wfull + 2;
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + LY::kTmemSlot);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kFlag);
+    volatile int* meta = reinterpret_cast<volatile int*>(smem + LY::kMeta);
+    uint8_t* qbuf = smem + LY::kQ;
+    uint8_t* ring = smem + LY::kRing;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&qfull[t], 1);
+            mbar_init(&qempty[t], 1);
+            mbar_init(&sfull[t], 1);
+            mbar_init(&pfull[t], 4);  // one arrival per softmax warp
+            mbar_init(&ofull[t], 1);
+            mbar_init(&ofree[t], 4);
+            if constexpr (FP8) {
+                mbar_init(&q8full[t], 4);
+                mbar_init(&wfull[t], 1);
+                mbar_init(&wempty[t], 1);
+            }
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(const_cast<uint32_t*>(tmem_slot))),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency_wait();  // the map, the query and the new tokens' keys come from the kernels before
+    grid_launch_dependents();
+
+    TileWalk walk;
+    walk.start(p.plan, p.S, p.mode, blockIdx.x, p.seqs_off);
+    TileItem it;
+    bool ok = true;
+
+    if (warp >= 8 && warp < 12) {
+        reg_dec<C::kRegsOther>();
+        if (warp == 8) {
+            // ============================ producer
+            uint32_t kv = 0;    // stages filled
+            uint32_t blks = 0;  // blocks
+            int nd[2] = {0, 0};
+            while (ok && walk.next(it)) {
+                if (lane == 0) {
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        const int tok = it.i * kTileTokens + t * kHalfTokens;
+                        if (tok >= it.n) break;
+                        ok = wait_bounded(&qempty[t], (nd[t] & 1) ^ 1, abort_flag, kWaitLimitNs);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&qfull[t], kQBytes);
+                        tma_load_3d_plain(qbuf + t * kQBytes, &tm_q, &qfull[t], 0, it.h * kGroup, it.q0 + tok);
+                        tma_load_3d_plain(qbuf + t * kQBytes + kQBytes / 2, &tm_q, &qfull[t], 64, it.h * kGroup, it.q0 + tok);
+                        ++nd[t];
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                const int32_t* prow = p.page_table + (long long)it.s * p.pt_stride;
+                const int pages = (int)(((long long)it.L + kChunk - 1) / kChunk);
+                for (int c0 = 2 * it.b0; c0 < 2 * it.b1 && ok; c0 += 32) {
+                    const int c = c0 + lane;
+                    // a page past the last or with an id out of range becomes the page after
+                    // the pool's last one: the copy fills its rows with zeros
+                    int page = p.num_pages;
+                    if (c < 2 * it.b1 && c < pages) {
+                        page = prow[c];
+                        if ((unsigned)page >= (unsigned)p.num_pages) {
+                            atomicOr(p.err, (int)HPC_DEVERR_PAGE_OUT_OF_RANGE);
+                            page = p.num_pages;
+                        }
+                    }
+                    const int nb = min(16, it.b1 - (c0 >> 1));
+                    for (int b = 0; b < nb && ok; ++b, ++blks) {
+                        const int pg0 = __shfl_sync(0xffffffffu, page, 2 * b);
+                        const int pg1 = __shfl_sync(0xffffffffu, page, 2 * b + 1);
+                        if (lane == 0) {
+                            for (int kvi = 0; kvi < 2 && ok; ++kvi, ++kv) {
+                                const uint32_t st = kv % NS;
+                                ok = wait_bounded(&empty[st], ((kv / NS) & 1) ^ 1, abort_flag, kWaitLimitNs);
+                                if (!ok) break;
+                                if (kvi == 0) meta[blks % kMetaRing] = (pg0 < p.num_pages ? 1 : 0) | (pg1 < p.num_pages ? 2 : 0);
+                                const CUtensorMap* tm = kvi == 0 ? &tm_k : &tm_v;
+                                uint8_t* dst = ring + (size_t)st * C::kStageBytes;
+                                if constexpr (FP8) {
+                                    float* sc = reinterpret_cast<float*>(smem + (kvi == 0 ? LY::kKs : LY::kVs)) +
+                                                (blks % kMetaRing) * kBlock;
+                                    const CUtensorMap* ts = kvi == 0 ? &tm_ks : &tm_vs;
+                                    mbar_arrive_expect_tx(&full[st], C::kStageBytes + kBlock * 4);
+                                    tma_load_2d_plain(sc, ts, &full[st], 0, pg0 * p.num_kv_heads + it.h);
+                                    tma_load_2d_plain(sc + kChunk, ts, &full[st], 0, pg1 * p.num_kv_heads + it.h);
+                                    tma_load_3d_plain(dst, tm, &full[st], 0, it.h, pg0 * kChunk);
+                                    tma_load_3d_plain(dst + 8192, tm, &full[st], 0, it.h, pg1 * kChunk);
+                                } else {
+                                    mbar_arrive_expect_tx(&full[st], C::kStageBytes);
+                                    tma_load_3d_plain(dst, tm, &full[st], 0, it.h, pg0 * kChunk);
+                                    tma_load_3d_plain(dst + 16384, tm, &full[st], 64, it.h, pg0 * kChunk);
+                                    tma_load_3d_plain(dst + 8192, tm, &full[st], 0, it.h, pg1 * kChunk);
+                                    tma_load_3d_plain(dst + 24576, tm, &full[st], 64, it.h, pg1 * kChunk);
+                                }
+                            }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        kv = __shfl_sync(0xffffffffu, kv, 0);
+                    }
+                }
+            }
+            // no copy is in flight when the CTA ends, whichever way the walk ended
+            if (lane == 0) {
+                for (uint32_t k = kv > (uint32_t)NS ? kv - NS : 0u; k < kv; ++k)
+                    wait_bounded(&full[k % NS], (k / NS) & 1, nullptr, kDrainLimitNs);
+                for (int t = 0; t < 2; ++t)
+                    if (nd[t] > 0) wait_bounded(&qfull[t], (nd[t] - 1) & 1, nullptr, kDrainLimitNs);
+            }
+        } else if (warp == 9) {
+            // ============================ issuer
+            constexpr uint32_t kIdS = FP8 ? idesc_e4m3(kHalfRows, kBlock) : idesc_16bit(false, kHalfRows, kBlock, 0);
+            constexpr uint32_t kIdO = idesc_16bit(FP8, kHalfRows, kHeadDim, 1);
+            uint64_t* const qready = FP8 ? q8full : qfull;
+            uint32_t kv = 0;            // stages taken
+            uint32_t blks = 0;          // V blocks taken
+            uint32_t np[2] = {0, 0};    // P tiles taken
+            int nd[2] = {0, 0};         // items
+            while (ok && walk.next(it)) {
+                const int halves = it.n - it.i * kTileTokens > kHalfTokens ? 2 : 1;
+                // S of half t from the K tile in stage st
+                auto issue_s = [&](int t, uint32_t st) {
+                    const uint32_t qa = smem_u32(qbuf + t * kQBytes), ka = smem_u32(ring + (size_t)st * C::kStageBytes);
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            umma_e4m3(tmem + 128 * t, sdesc_sw128(qa + kk * 32, 16, 1024), sdesc_sw128(ka + kk * 32, 16, 1024),
+                                      kIdS, kk > 0);
+                            umma_e4m3(tmem + 128 * t, sdesc_sw128(qa + 16384 + kk * 32, 16, 1024),
+                                      sdesc_sw128(ka + kk * 32, 16, 1024), kIdS, 1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
+                            umma_f16(tmem + 128 * t, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), kIdS,
+                                     kk > 0);
+                        }
+                    }
+                    umma_commit(&sfull[t]);
+                };
+                // first S of both halves
+                ok = wait_warp(&full[kv % NS], (kv / NS) & 1, abort_flag);
+                for (int t = 0; t < halves && ok; ++t) {
+                    ok = wait_warp(&qready[t], nd[t] & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        issue_s(t, kv % NS);
+                        if (it.b1 - it.b0 == 1) umma_commit(&qempty[t]);
+                        if (t == halves - 1) umma_commit(&empty[kv % NS]);
+                    }
+                    __syncwarp();
+                }
+                ++kv;
+                for (int b = it.b0; b < it.b1 && ok; ++b, ++blks) {
+                    const uint32_t vst = kv % NS;
+                    const bool more = b + 1 < it.b1;
+                    uint32_t va;
+                    if constexpr (FP8) {
+                        va = smem_u32(smem + LY::kWide + (blks & 1) * 32768);
+                        ok = wait_warp(&wfull[blks & 1], (blks >> 1) & 1, abort_flag);
+                    } else {
+                        uint8_t* vt = ring + (size_t)vst * C::kStageBytes;
+                        va = smem_u32(vt);
+                        ok = wait_warp(&full[vst], (kv / NS) & 1, abort_flag);
+                        // rows of the last page past the sequence's end may hold any bits, and
+                        // 0 x NaN would reach the sums: zero them (whole missing pages came as zeros)
+                        const int nv = it.L - b * kBlock;
+                        if (nv < kBlock && (nv & (kChunk - 1)) != 0) {
+                            const int hi = (max(nv, 0) + kChunk - 1) / kChunk * kChunk;
+                            for (int i = lane; i < (hi - max(nv, 0)) * 16; i += 32) {
+                                const int row = max(nv, 0) + i / 16, part = i % 16;
+                                *reinterpret_cast<uint4*>(vt + (part >> 3) * 16384 + row * 128 + (part & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                    }
+                    if (!ok) break;
+                    ++kv;
+                    for (int t = 0; t < halves && ok; ++t) {
+                        // the first product of an item overwrites O: the item before must have left it
+                        if (b == it.b0 && nd[t] > 0) ok = wait_warp(&ofree[t], (nd[t] - 1) & 1, abort_flag);
+                        ok = ok && wait_warp(&pfull[t], np[t] & 1, abort_flag);
+                        if (ok && more && t == 0) ok = wait_warp(&full[kv % NS], (kv / NS) & 1, abort_flag);
+                        if (!ok) break;
+                        ++np[t];
+                        tc_fence_after();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                umma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + kk * 8, sdesc_sw128(va + kk * 2048, 16384, 1024),
+                                            kIdO, b > it.b0 || kk > 0);
+                            if (t == halves - 1) umma_commit(FP8 ? &wempty[blks & 1] : &empty[vst]);
+                            if (more) {
+                                issue_s(t, kv % NS);
+                                if (b + 2 == it.b1) umma_commit(&qempty[t]);
+                                if (t == halves - 1) umma_commit(&empty[kv % NS]);
+                            } else {
+                                umma_commit(&ofull[t]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (more) ++kv;
+                }
+                for (int t = 0; t < halves; ++t) ++nd[t];
+            }
+        }
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            atomicOr(p.err, (int)HPC_DEVERR_WAIT_TIMEOUT);
+        }
+    } else if (warp >= 12) {
+        // ============================ e4m3: query rows split, V widened
+        if constexpr (FP8) {
+            reg_dec<C::kRegsOther>();
+            const int tg = threadIdx.x & 127, wq = warp & 3;
+            uint32_t blks = 0;
+            int nd[2] = {0, 0};
+            while (ok && walk.next(it)) {
+                const int halves = it.n - it.i * kTileTokens > kHalfTokens ? 2 : 1;
+                for (int t = 0; t < halves && ok; ++t) {
+                    ok = wait_warp(&qfull[t], nd[t] & 1, abort_flag);
+                    if (!ok) break;
+                    split_query_rows(qbuf + t * kQBytes, reinterpret_cast<float*>(smem + LY::kQs) + (nd[t] & 1) * 256 + t * 128,
+                                     wq, lane);
+                    ++nd[t];
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&q8full[t]);
+                }
+                // (a warp that gave up must not leave the others at a barrier)
+                ok = !named_any_128(!ok);
+                for (int b = it.b0; b < it.b1 && ok; ++b, ++blks) {
+                    const uint32_t kv = 2 * blks + 1, st = kv % NS;  // V of the CTA's block number blks
+                    // (in this order: the P . V of block blks - 2 shows that the stage's use
+                    // before this one, as K of that block, is over, so the parity of its
+                    // barrier is not mistaken)
+                    ok = wait_warp(&wempty[blks & 1], ((blks >> 1) & 1) ^ 1, abort_flag) &&
+                         wait_warp(&full[st], (kv / NS) & 1, abort_flag);
+                    ok = !named_any_128(!ok);
+                    if (!ok) break;
+                    widen_v(ring + (size_t)st * C::kStageBytes,
+                            reinterpret_cast<const float*>(smem + LY::kVs) + (blks % kMetaRing) * kBlock,
+                            smem + LY::kWide + (blks & 1) * 32768, it.L - b * kBlock, tg);
+                    fence_proxy_async_smem();
+                    named_sync_128();
+                    if (tg == 0) {
+                        mbar_arrive(&wfull[blks & 1]);
+                        mbar_arrive(&empty[st]);
+                    }
+                }
+            }
+            if (!ok && lane == 0) {
+                *abort_flag = 1;
+                atomicOr(p.err, (int)HPC_DEVERR_WAIT_TIMEOUT);
+            }
+        }
+    } else {
+        reg_inc<C::kRegsSoftmax>();
+        // ============================ softmax warpgroup of half t, one thread per row
+        const int t = warp >> 2;
+        const int row = threadIdx.x & 127;
+        const uint32_t lane_addr = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t scol = tmem + lane_addr + 128 * t, ocol = tmem + lane_addr + 256 + 128 * t;
+        const int tok_in = t * kHalfTokens + row / kGroup, head = row % kGroup;
+        uint32_t blks = 0;  // blocks of this CTA
+        uint32_t ns = 0;    // score tiles of this half
+        int nd = 0;
+        while (ok && walk.next(it)) {
+            const int tok = it.i * kTileTokens + tok_in;
+            if (it.n - it.i * kTileTokens <= t * kHalfTokens) {  // an empty half
+                blks += it.b1 - it.b0;
+                continue;
+            }
+            // keys this row sees; rows past the sequence's last token (computed, not
+            // written) see no more than the sequence has
+            const int lim = p.mode == kModePrefix ? it.L : min(it.L, it.L - it.n + tok + 1);
+            float m = kNegInf, l = 0.f;  // reference maximum (log2 domain) and sum
+            float sc = p.scale_log2;
+            for (int b = it.b0; b < it.b1; ++b, ++blks, ++ns) {
+                if (!wait_warp(&sfull[t], ns & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float s[128];
+                tmem_ld32(scol, s);
+                tmem_ld32(scol + 32, s + 32);
+                tmem_ld32(scol + 64, s + 64);
+                tmem_ld32(scol + 96, s + 96);
+                tmem_ld_wait();
+                if constexpr (FP8) {
+                    // (the scores exist, so the splitter's row scales do too)
+                    if (b == it.b0) sc = p.scale_log2 * reinterpret_cast<const float*>(smem + LY::kQs)[(nd & 1) * 256 + t * 128 + row];
+                    const float4* ks = reinterpret_cast<const float4*>(smem + LY::kKs + (blks % kMetaRing) * 512);
+#pragma unroll
+                    for (int c = 0; c < 128; c += 4) {
+                        const float4 f = ks[c / 4];
+                        const float2 x = mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
+                        const float2 y = mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
+                        s[c] = x.x, s[c + 1] = x.y, s[c + 2] = y.x, s[c + 3] = y.y;
+                    }
+                }
+                const int nv = lim - b * kBlock, pages_ok = meta[blks % kMetaRing];
+                if (!__all_sync(0xffffffffu, nv >= kBlock && pages_ok == 3)) {
+                    const int n0 = (pages_ok & 1) ? min(nv, kChunk) : 0, n1 = (pages_ok & 2) ? nv - kChunk : 0;
+#pragma unroll
+                    for (int c = 0; c < kChunk; ++c) {
+                        if (c >= n0) s[c] = kNegInf;
+                        if (c >= n1) s[c + kChunk] = kNegInf;
+                    }
+                }
+                float mx[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) mx[u] = s[u];
+#pragma unroll
+                for (int c = 4; c + 4 < 128; c += 8)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[c + u], s[c + 4 + u]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], s[124 + u]);
+                const float mraw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                // the reference moves only when the block's maximum is far above it
+                const bool move = mraw > m + kRescaleLog2 || (m == kNegInf && mraw != kNegInf);
+                const bool resc = move && m != kNegInf;
+                if (__any_sync(0xffffffffu, resc)) {
+                    // (the product of the block before is done: it was issued before this
+                    // block's scores)
+                    const float al = resc ? fast_exp2(m - mraw) : 1.f;
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 32) {
+                        float o[32];
+                        tmem_ld32(ocol + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int u = 0; u < 32; ++u) o[u] *= al;
+                        tmem_st32(ocol + c, o);
+                    }
+                    l *= al;
+                }
+                if (move) m = mraw;
+                const float neg = m == kNegInf ? 0.f : -m;
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) {
+                        float2 x = fma2(make_float2(s[c + 2 * u], s[c + 2 * u + 1]), make_float2(sc, sc), make_float2(neg, neg));
+                        x.x = fast_exp2(x.x);
+                        x.y = fast_exp2(x.y);
+                        sum[u & 1] = add2(sum[u & 1], x);
+                        pk[u] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
+                    }
+                    tmem_st16(scol + c / 2, pk);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfull[t]);
+            }
+            if (!ok) break;
+            // ---- the tile's rows
+            if (!wait_warp(&ofull[t], nd & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const bool live = tok < it.n;
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            const float lse = l > 0.f || l != l ? (m == kNegInf ? 0.f : m) * kLn2 + logf(l) : kNegInf;
+            const bool direct = p.mode == kModePrefill && it.whole;
+            const long long orow = (long long)(it.q0 + tok) * p.num_q_heads + it.h * kGroup + head;
+            const long long prow = tile_slot(p.mode, blockIdx.x, it) * kTileRows + tok_in * kGroup + head;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                float o[32];
+                tmem_ld32(ocol + c, o);
+                tmem_ld_wait();
+                // rows that saw nothing are zero, whatever O holds
+#pragma unroll
+                for (int u = 0; u < 32; ++u) o[u] = inv == 0.f ? 0.f : o[u] * inv;
+                if (live && direct) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kHeadDim + c);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        dst[u] = make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
+                                            pack_bf16x2(o[8 * u + 4], o[8 * u + 5]), pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
+                } else if (live) {
+                    float4* dst = reinterpret_cast<float4*>(p.split_o + prow * kHeadDim + c);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                }
+            }
+            if (live && direct) {
+                if (p.out_lse) p.out_lse[orow] = lse;
+            } else if (live) {
+                p.split_lse[prow] = lse;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ofree[t]);
+            ++nd;
+        }
+        if (!ok && lane == 0) {
+            *abort_flag = 1;
+            atomicOr(p.err, (int)HPC_DEVERR_WAIT_TIMEOUT);
+        }
+    }
+    // normal end: every MMA was waited for by an epilogue; after a timeout give
+    // what is in flight a bounded time
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        if (*abort_flag) {
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < kDrainLimitNs) {
+            }
+        }
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// 3-D map over the query [tokens][Hq][128] bf16: box = 64 dims x 8 heads x 16
+// tokens, 128-byte swizzle (half of an MMA operand tile).
+bool make_tile_q_map(CUtensorMap* map, const void* q, int tokens, int Hq) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)Hq, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)Hq * kHeadDim * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)kGroup, (cuuint32_t)kHalfTokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8>
+cudaError_t launch(const CUtensorMap (&maps)[5], const TileParams& p, int num_ctas, cudaStream_t s) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&tile_attn_kernel<FP8>),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<FP8>::kAlloc);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return launch_pdl(tile_attn_kernel<FP8>, dim3(num_ctas), dim3(Cfg<FP8>::kThreads), Smem<FP8>::kAlloc, s, maps[0],
+                      maps[1], maps[2], maps[3], maps[4], p);
+}
+
+}  // namespace
+
+int tile_default_ctas() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    return sms;
+}
+
+cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s) {
+    CUtensorMap maps[5];  // K, V, Q, K scales, V scales (the last two e4m3 only)
+    memset(maps, 0, sizeof maps);
+    if (!make_kv_map(&maps[0], a.k_cache, a.fp8, a.num_pages, a.num_kv_heads) ||
+        !make_kv_map(&maps[1], a.v_cache, a.fp8, a.num_pages, a.num_kv_heads) ||
+        !make_tile_q_map(&maps[2], a.q, a.num_tokens, a.num_q_heads))
+        return cudaErrorInvalidValue;
+    if (a.fp8 && (!make_scale_map(&maps[3], a.k_scale, a.num_pages, a.num_kv_heads) ||
+                  !make_scale_map(&maps[4], a.v_scale, a.num_pages, a.num_kv_heads)))
+        return cudaErrorInvalidValue;
+    TileParams p;
+    memset(&p, 0, sizeof p);
+    p.plan = a.plan;
+    p.seqs_off = tile_layout(a.S, a.num_ctas).seqs;
+    p.page_table = a.page_table;
+    p.pt_stride = a.pt_stride;
+    p.err = a.plan + kTError;
+    p.S = a.S;
+    p.mode = a.mode;
+    p.num_q_heads = a.num_q_heads;
+    p.num_kv_heads = a.num_kv_heads;
+    p.num_pages = a.num_pages;
+    p.split_o = a.split_o;
+    p.split_lse = a.split_lse;
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    p.out_lse = a.out_lse;
+    p.scale_log2 = 1.4426950408889634f / sqrtf((float)kHeadDim);
+    return a.fp8 ? launch<true>(maps, p, a.num_ctas, s) : launch<false>(maps, p, a.num_ctas, s);
+}
+
+}  // namespace hpc
