@@ -513,12 +513,12 @@ hpc_status hpc_decode_noalloc(const void* q, const void* k_cache, const void* v_
 /* ------------------------------------------------------------------------
  * Prompt attention and shared-prefix attention, over the same paged caches.
  *
- * Both work on a tile map: the query tokens of each sequence in tiles of 32
- * tokens x the 8 query heads of a KV head, each tile over the 128-token KV
+ * Both work on a tile map: the query tokens of each sequence in tiles of 32 or
+ * 64 tokens x the 8 query heads of a KV head, each tile over the 128-token KV
  * blocks that it sees, all tiles walked head by head, sequence by sequence and
- * cut into equal runs, one per CTA ([SGL] "Scheduling around live KV work",
- * the same balance for prompts). Tiles that fall to one CTA are written to the
- * output by the attention call; cut ones leave partial rows for the combine.
+ * cut into equal runs, one per worker (a CTA, or a pair of CTAs for 64 tokens) ([SGL] "Scheduling around live KV work",
+ * the same balance for prompts). Tiles that fall to one worker are written to
+ * the output by the attention call; cut ones leave partial rows for the combine.
  */
 #define HPC_MAX_TILE_CTAS 4096
 
@@ -528,11 +528,11 @@ hpc_status hpc_decode_noalloc(const void* q, const void* k_cache, const void* v_
  * hpc_prefix_plan fills the rest. It holds a copy of the lengths it was made
  * from, so the attention calls need no lengths, and one map serves every layer.
  * Byte layout of buf (int32):
- *   [0, 16)   header {units_per_head (int64), bucket (int64), used_ctas,
- *             num_seqs, num_kv_heads, num_ctas, num_tokens, mode,
- *             tiles_per_head, q_len, error word, 0, 0, 0}
- *   starts    [num_ctas + 1][8] {kv head, sequence, tile, block, tile number, 0, 0, 0}:
- *             where each CTA's run begins
+ *   [0, 16)   header {units_per_head (int64), bucket (int64), used workers,
+ *             num_seqs, num_kv_heads, num_workers, num_tokens, mode,
+ *             tiles_per_head, q_len, error word, tile_tokens, 0, 0}
+ *   starts    [num_workers + 1][8] {kv head, sequence, tile, block, tile number, 0, 0, 0}:
+ *             where each worker's run begins
  *   seqs      [num_seqs][4] {first query token, query tokens, keys, tiles before}
  *   units     int64 [num_seqs + 1]: units of the sequences before (a block is one
  *             unit; a tile of a prompt costs one more)
@@ -544,8 +544,9 @@ typedef struct hpc_tile_plan {
     int num_seqs;      /* filled by the planner from here on */
     int num_tokens;
     int num_kv_heads;
-    int num_ctas;      /* grid size of the attention call */
+    int num_workers;   /* CTAs, or pairs of CTAs, that share the walk */
     int mode;          /* 0 prompts, 1 prefixes */
+    int tile_tokens;   /* 32 (one CTA per tile) or 64 (a pair) */
     int q_len;
     int table_stride;
 } hpc_tile_plan;
@@ -574,8 +575,10 @@ size_t hpc_prefix_split_rows(int num_groups, int batch, int q_len, int num_kv_he
  *   d_seq_lens    device int32 [batch]
  *   num_tokens    rows of q and out; rows of no sequence are left as they are
  *   page_table_stride  of the table that the attention call gets
- *   min_blocks_per_cta  least 128-token blocks of a CTA's run (fewer CTAs get
- *                 work in small batches); 0 or 1: no floor
+ *   min_blocks_per_cta  least units of a worker's run (fewer workers get work in
+ *                 small batches); 0 or 1: no floor
+ *   tile_tokens   32, 64, or 0: the one that is faster for the average sequence
+ *                 (num_ctas 1 takes 32)
  * One block, integer only, reads the lengths on the device. A sequence whose
  * starts decrease or leave [0, num_tokens] is passed over
  * (HPC_DEVERR_BAD_DESCRIPTOR); keys beyond the page table's row are not seen
@@ -585,7 +588,7 @@ size_t hpc_prefix_split_rows(int num_groups, int batch, int q_len, int num_kv_he
  */
 hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens, int batch, int num_tokens,
                             int num_kv_heads, int page_table_stride, int num_ctas, int min_blocks_per_cta,
-                            hpc_tile_plan* plan, void* stream);
+                            int tile_tokens, hpc_tile_plan* plan, void* stream);
 
 /*
  * Attention of the mapped prompts, on tcgen05 tensor cores. Whole tiles go to
@@ -630,7 +633,7 @@ hpc_status hpc_prefill_combine(const hpc_tile_plan* plan, const float* split_o, 
  */
 hpc_status hpc_prefix_plan(const int32_t* d_group_starts, const int32_t* d_prefix_lens, int num_groups, int batch,
                            int q_len, int num_kv_heads, int prefix_table_stride, int num_ctas, int min_blocks_per_cta,
-                           hpc_tile_plan* plan, void* stream);
+                           int tile_tokens, hpc_tile_plan* plan, void* stream);
 
 /*
  * Attention of every query row over its group's prefix, each prefix read once

@@ -23,6 +23,7 @@ ATTN_TEST_WAIT_EXPIRY = 2
 HEAD_DIM = 128
 PAGE = 64
 GROUP = 8
+TILE_CTA, TILE_PAIR = 32, 64  # query tokens of a tile: one CTA's, or a pair's
 
 _STATUS = {0: "HPC_OK", 1: "HPC_ERR_INVALID_ARG", 2: "HPC_ERR_UNSUPPORTED",
            3: "HPC_ERR_WORKSPACE_TOO_SMALL", 4: "HPC_ERR_CUDA", 5: "HPC_ERR_DEVICE_CHECK"}
@@ -47,7 +48,7 @@ class PlanStruct(ctypes.Structure):
 
 class TilePlanStruct(ctypes.Structure):
     _fields_ = [("buf", _vp), ("bytes", _sz), ("num_seqs", _i), ("num_tokens", _i), ("num_kv_heads", _i),
-                ("num_ctas", _i), ("mode", _i), ("q_len", _i), ("table_stride", _i)]
+                ("num_workers", _i), ("mode", _i), ("tile_tokens", _i), ("q_len", _i), ("table_stride", _i)]
 
 
 _P = ctypes.POINTER(PlanStruct)
@@ -90,11 +91,11 @@ SIGNATURES = {
     "hpc_tile_default_num_ctas": (_i, []),
     "hpc_prefill_split_rows": (_sz, [_i]),
     "hpc_prefix_split_rows": (_sz, [_i, _i, _i, _i, _i]),
-    "hpc_prefill_plan": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _TP, _vp]),
+    "hpc_prefill_plan": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _TP, _vp]),
     "hpc_prefill_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _i, _i, _i, _i, _TP, _vp, _vp, _vp, _vp,
                               _vp]),
     "hpc_prefill_combine": (_i, [_TP, _vp, _vp, _vp, _vp, _i, _i, _i, _vp]),
-    "hpc_prefix_plan": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _TP, _vp]),
+    "hpc_prefix_plan": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _TP, _vp]),
     "hpc_prefix_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _i, _i, _i, _i, _TP, _vp, _vp, _vp]),
     "hpc_prefix_combine": (_i, [_TP, _vp, _vp, _P, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
     "hpc_tile_read_error": (_i, [_TP, ctypes.POINTER(_i)]),
@@ -462,7 +463,12 @@ class TilePlan:
 
     @property
     def num_ctas(self):
-        return self.struct.num_ctas
+        """CTAs of the attention call."""
+        return self.struct.num_workers * (self.struct.tile_tokens // TILE_CTA)
+
+    @property
+    def tile_tokens(self):
+        return self.struct.tile_tokens
 
     def ref(self):
         return ctypes.byref(self.struct)
@@ -507,8 +513,8 @@ def _check_out(what, t, shape, dtype):
 
 
 def hpc_prefill_plan(q_starts, seq_lens, num_tokens: int, num_kv_heads: int, page_table_stride: int,
-                     num_ctas: int | None = None, min_blocks_per_cta: int = 1, plan: TilePlan | None = None,
-                     stream=None) -> TilePlan:
+                     num_ctas: int | None = None, min_blocks_per_cta: int = 1, tile_tokens: int = 0,
+                     plan: TilePlan | None = None, stream=None) -> TilePlan:
     """Tile map of packed prompts from device-side starts and lengths (one launch, no host sync)."""
     _cuda_i32(q_starts, "q_starts")
     _cuda_i32(seq_lens, "seq_lens")
@@ -519,7 +525,7 @@ def hpc_prefill_plan(q_starts, seq_lens, num_tokens: int, num_kv_heads: int, pag
     num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
     plan = TilePlan(B, num_ctas, seq_lens.device) if plan is None else plan
     rc = lib().hpc_prefill_plan(_ptr(q_starts), _ptr(seq_lens), B, num_tokens, num_kv_heads, page_table_stride, num_ctas,
-                                min_blocks_per_cta, plan.ref(), _stream(stream))
+                                min_blocks_per_cta, tile_tokens, plan.ref(), _stream(stream))
     _check("hpc_prefill_plan", rc)
     return plan
 
@@ -531,7 +537,7 @@ def _split_rows(rows, device):
 
 def prefill_split_buffers(plan: TilePlan):
     """split_o and split_lse of hpc_prefill_attn for this map."""
-    return _split_rows(int(lib().hpc_prefill_split_rows(plan.struct.num_ctas)), plan.buf.device)
+    return _split_rows(int(lib().hpc_prefill_split_rows(plan.num_ctas)), plan.buf.device)
 
 
 def _check_q_table(what, q, table, seqs):
@@ -561,7 +567,7 @@ def hpc_prefill_attn(q, k_cache, v_cache, page_table, plan: TilePlan, split_o, s
     _check_out("out", out, q.shape, torch.bfloat16)
     if out_lse is not None:
         _check_out("out_lse", out_lse, (T, Hq), torch.float32)
-    _check_splits("hpc_prefill_attn", int(lib().hpc_prefill_split_rows(plan.struct.num_ctas)), split_o, split_lse)
+    _check_splits("hpc_prefill_attn", int(lib().hpc_prefill_split_rows(plan.num_ctas)), split_o, split_lse)
     rc = lib().hpc_prefill_attn(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kvd, _pages(k_cache, num_pages),
         _ptr(page_table), int(page_table.shape[1]), Hq, int(k_cache.shape[2]), D, int(k_cache.shape[1]), plan.ref(),
@@ -597,12 +603,13 @@ def _on(stream):
 
 
 def prefill(q, k_cache, v_cache, page_table, q_starts, seq_lens, k_scale=None, v_scale=None, num_ctas: int | None = None,
-            min_blocks_per_cta: int = 1, num_pages: int | None = None, out=None, out_lse=None, stream=None):
+            min_blocks_per_cta: int = 1, tile_tokens: int = 0, num_pages: int | None = None, out=None, out_lse=None,
+            stream=None):
     """plan -> attention -> combine of packed prompts, q bf16 [T, Hq, 128], with buffers
     allocated here (and out, out_lse where they are not given). Returns (out, lse, plan)."""
     with _on(stream):
         plan = hpc_prefill_plan(q_starts, seq_lens, q.shape[0], k_cache.shape[2], page_table.shape[1], num_ctas,
-                                min_blocks_per_cta, stream=stream)
+                                min_blocks_per_cta, tile_tokens, stream=stream)
         so, sl = prefill_split_buffers(plan)
         if out is None:
             out = torch.empty_like(q)
@@ -615,8 +622,8 @@ def prefill(q, k_cache, v_cache, page_table, q_starts, seq_lens, k_scale=None, v
 
 
 def hpc_prefix_plan(group_starts, prefix_lens, batch: int, num_kv_heads: int, prefix_table_stride: int, q_len: int = 1,
-                    num_ctas: int | None = None, min_blocks_per_cta: int = 1, plan: TilePlan | None = None,
-                    stream=None) -> TilePlan:
+                    num_ctas: int | None = None, min_blocks_per_cta: int = 1, tile_tokens: int = 0,
+                    plan: TilePlan | None = None, stream=None) -> TilePlan:
     """Tile map of the prefixes that groups of a decode batch share."""
     _cuda_i32(group_starts, "group_starts")
     _cuda_i32(prefix_lens, "prefix_lens")
@@ -627,14 +634,14 @@ def hpc_prefix_plan(group_starts, prefix_lens, batch: int, num_kv_heads: int, pr
     num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
     plan = TilePlan(G, num_ctas, prefix_lens.device) if plan is None else plan
     rc = lib().hpc_prefix_plan(_ptr(group_starts), _ptr(prefix_lens), G, batch, q_len, num_kv_heads, prefix_table_stride,
-                               num_ctas, min_blocks_per_cta, plan.ref(), _stream(stream))
+                               num_ctas, min_blocks_per_cta, tile_tokens, plan.ref(), _stream(stream))
     _check("hpc_prefix_plan", rc)
     return plan
 
 
 def _prefix_rows(plan: TilePlan):
     p = plan.struct
-    return int(lib().hpc_prefix_split_rows(p.num_seqs, p.num_tokens // p.q_len, p.q_len, p.num_kv_heads, p.num_ctas))
+    return int(lib().hpc_prefix_split_rows(p.num_seqs, p.num_tokens // p.q_len, p.q_len, p.num_kv_heads, plan.num_ctas))
 
 
 def prefix_split_buffers(plan: TilePlan):
@@ -673,8 +680,8 @@ def hpc_prefix_combine(prefix_plan: TilePlan, prefix_o, prefix_lse, plan: Plan, 
 
 def decode_shared_prefix(q, k_cache, v_cache, page_table, seq_lens, prefix_table, prefix_lens, group_starts, k_scale=None,
                          v_scale=None, num_ctas: int | None = None, min_chunks_per_cta: int = 2,
-                         prefix_num_ctas: int | None = None, min_blocks_per_cta: int = 1, num_pages: int | None = None,
-                         stream=None):
+                         prefix_num_ctas: int | None = None, min_blocks_per_cta: int = 1, tile_tokens: int = 0,
+                         num_pages: int | None = None, stream=None):
     """One decode step of a batch whose groups share prefixes: requests
     [group_starts[g], group_starts[g + 1]) see the prefix_lens[g] tokens that
     prefix_table[g] names, then their own seq_lens[b] tokens (page_table). Each
@@ -683,7 +690,7 @@ def decode_shared_prefix(q, k_cache, v_cache, page_table, seq_lens, prefix_table
     B, Hkv = q.shape[0], k_cache.shape[2]
     with _on(stream):
         pplan = hpc_prefix_plan(group_starts, prefix_lens, B, Hkv, prefix_table.shape[1], q_len, prefix_num_ctas,
-                                min_blocks_per_cta, stream=stream)
+                                min_blocks_per_cta, tile_tokens, stream=stream)
         po, pl = prefix_split_buffers(pplan)
         plan = hpc_decode_plan(seq_lens, Hkv, num_ctas or default_num_ctas(kv_dtype_of(k_cache)), min_chunks_per_cta,
                                stream=stream)

@@ -24,33 +24,44 @@ bool heads_ok(int num_kv_heads) { return num_kv_heads >= 1 && num_kv_heads <= HP
 
 // Tile numbers over all heads stay in int32.
 bool tokens_ok(int num_tokens, int num_seqs, int num_kv_heads) {
-    return num_tokens >= 0 && ((long long)num_tokens / kTileTokens + num_seqs) * num_kv_heads < 2147483647LL;
+    return num_tokens >= 0 && ((long long)num_tokens / kTileCta + num_seqs) * num_kv_heads < 2147483647LL;
+}
+
+// Tiles of 64 tokens on pairs of CTAs where the sequences fill them, of 32 on
+// single CTAs otherwise.
+int auto_tile(int num_tokens, int num_seqs) {
+    return (long long)num_tokens >= 2LL * kTilePair * num_seqs ? kTilePair : kTileCta;
 }
 
 hpc_status plan_common(const int32_t* d_starts, const int32_t* d_lens, int num_seqs, int num_tokens, int num_kv_heads,
-                       int table_stride, int num_ctas, int min_blocks, int mode, int q_len, hpc_tile_plan* plan,
-                       void* stream) {
+                       int table_stride, int num_ctas, int min_blocks, int tile_tokens, int mode, int q_len,
+                       hpc_tile_plan* plan, void* stream) {
     if (!d_starts || !d_lens || !plan || !plan->buf || !aligned(plan->buf, 16) || min_blocks < 0 || table_stride < 1)
         return HPC_ERR_INVALID_ARG;
     if (!seqs_ok(num_seqs, num_ctas) || !heads_ok(num_kv_heads) || !tokens_ok(num_tokens, num_seqs, num_kv_heads))
         return HPC_ERR_INVALID_ARG;
+    if (tile_tokens != 0 && tile_tokens != kTileCta && tile_tokens != kTilePair) return HPC_ERR_INVALID_ARG;
     if (plan->bytes < hpc_tile_plan_bytes(num_seqs, num_ctas)) return HPC_ERR_WORKSPACE_TOO_SMALL;
+    if (tile_tokens == 0) tile_tokens = auto_tile(num_tokens, num_seqs);
+    if (num_ctas == 1) tile_tokens = kTileCta;
     plan->num_seqs = num_seqs;
     plan->num_tokens = num_tokens;
     plan->num_kv_heads = num_kv_heads;
-    plan->num_ctas = num_ctas;
+    plan->num_workers = tile_tokens == kTilePair ? num_ctas / 2 : num_ctas;
+    plan->tile_tokens = tile_tokens;
     plan->mode = mode;
     plan->q_len = q_len;
     plan->table_stride = table_stride;
     const long long max_len = (long long)table_stride * kChunk;
-    return launched(launch_tile_plan(d_starts, d_lens, num_seqs, num_tokens, num_kv_heads, num_ctas, min_blocks,
-                                     max_len > 2147483647LL ? 2147483647 : (int)max_len, mode, q_len, plan->buf,
+    return launched(launch_tile_plan(d_starts, d_lens, num_seqs, num_tokens, num_kv_heads, plan->num_workers,
+                                     min_blocks, max_len > 2147483647LL ? 2147483647 : (int)max_len, mode, q_len, tile_tokens, plan->buf,
                                      static_cast<cudaStream_t>(stream)));
 }
 
 hpc_status plan_check(const hpc_tile_plan* plan, int mode, int num_kv_heads) {
     if (!plan || !plan->buf || plan->mode != mode || plan->num_kv_heads != num_kv_heads) return HPC_ERR_INVALID_ARG;
-    if (!seqs_ok(plan->num_seqs, plan->num_ctas) || plan->bytes < hpc_tile_plan_bytes(plan->num_seqs, plan->num_ctas))
+    if (plan->tile_tokens != kTileCta && plan->tile_tokens != kTilePair) return HPC_ERR_INVALID_ARG;
+    if (!seqs_ok(plan->num_seqs, plan->num_workers) || plan->bytes < hpc_tile_plan_bytes(plan->num_seqs, plan->num_workers))
         return HPC_ERR_INVALID_ARG;
     return HPC_OK;
 }
@@ -102,7 +113,8 @@ hpc_status attn_common(const void* q, const void* k_cache, const void* v_cache, 
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = num_kv_heads;
     a.plan = plan->buf;
-    a.num_ctas = plan->num_ctas;
+    a.num_workers = plan->num_workers;
+    a.tile_tokens = plan->tile_tokens;
     a.mode = mode;
     a.split_o = split_o;
     a.split_lse = split_lse;
@@ -124,31 +136,31 @@ int hpc_tile_default_num_ctas(void) { return tile_default_ctas(); }
 
 size_t hpc_prefill_split_rows(int num_ctas) {
     if (!seqs_ok(1, num_ctas)) return 0;
-    return (size_t)2 * num_ctas * kTileRows;
+    return (size_t)2 * num_ctas * kTileCta * kGroup;  // the same for half as many pairs
 }
 
 size_t hpc_prefix_split_rows(int num_groups, int batch, int q_len, int num_kv_heads, int num_ctas) {
     if (!seqs_ok(num_groups, num_ctas) || batch < 1 || batch > HPC_MAX_BATCH || q_len < 1 || q_len > HPC_MAX_Q_LEN ||
         !heads_ok(num_kv_heads))
         return 0;
-    // every group has at most one tile that is not full
-    const long long tiles = ((long long)batch * q_len / kTileTokens + num_groups) * num_kv_heads;
-    return (size_t)(tiles + num_ctas) * kTileRows;
+    // every group has at most one tile that is not full, of 64 tokens at most
+    const long long tiles = ((long long)batch * q_len / kTileCta + 2LL * num_groups) * num_kv_heads;
+    return (size_t)(tiles + num_ctas) * kTileCta * kGroup;
 }
 
 hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens, int batch, int num_tokens,
                             int num_kv_heads, int page_table_stride, int num_ctas, int min_blocks_per_cta,
-                            hpc_tile_plan* plan, void* stream) {
+                            int tile_tokens, hpc_tile_plan* plan, void* stream) {
     return plan_common(d_q_starts, d_seq_lens, batch, num_tokens, num_kv_heads, page_table_stride, num_ctas,
-                       min_blocks_per_cta, kModePrefill, 1, plan, stream);
+                       min_blocks_per_cta, tile_tokens, kModePrefill, 1, plan, stream);
 }
 
 hpc_status hpc_prefix_plan(const int32_t* d_group_starts, const int32_t* d_prefix_lens, int num_groups, int batch,
                            int q_len, int num_kv_heads, int prefix_table_stride, int num_ctas, int min_blocks_per_cta,
-                           hpc_tile_plan* plan, void* stream) {
+                           int tile_tokens, hpc_tile_plan* plan, void* stream) {
     if (batch < 1 || batch > HPC_MAX_BATCH || q_len < 1 || q_len > HPC_MAX_Q_LEN) return HPC_ERR_INVALID_ARG;
     return plan_common(d_group_starts, d_prefix_lens, num_groups, batch * q_len, num_kv_heads, prefix_table_stride,
-                       num_ctas, min_blocks_per_cta, kModePrefix, q_len, plan, stream);
+                       num_ctas, min_blocks_per_cta, tile_tokens, kModePrefix, q_len, plan, stream);
 }
 
 hpc_status hpc_prefill_attn(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -168,7 +180,7 @@ hpc_status hpc_prefill_combine(const hpc_tile_plan* plan, const float* split_o, 
     if ((st = plan_check(plan, kModePrefill, num_kv_heads)) != HPC_OK) return st;
     if (!split_o || !split_lse || !out || !aligned(split_o, 16) || !aligned(out, 16)) return HPC_ERR_INVALID_ARG;
     if (plan->num_tokens == 0) return HPC_OK;
-    return launched(launch_prefill_combine(plan->buf, plan->num_seqs, num_q_heads, plan->num_ctas, split_o, split_lse,
+    return launched(launch_prefill_combine(plan->buf, plan->num_seqs, num_q_heads, plan->num_workers, plan->tile_tokens, split_o, split_lse,
                                            out, out_lse, static_cast<cudaStream_t>(stream)));
 }
 
@@ -196,7 +208,7 @@ hpc_status hpc_prefix_combine(const hpc_tile_plan* prefix_plan, const float* pre
     if (!prefix_o || !prefix_lse || !split_o || !split_lse || !out || !aligned(prefix_o, 16) || !aligned(split_o, 16) ||
         !aligned(out, 8))
         return HPC_ERR_INVALID_ARG;
-    return launched(launch_prefix_combine(prefix_plan->buf, prefix_plan->num_seqs, prefix_plan->num_ctas, prefix_o,
+    return launched(launch_prefix_combine(prefix_plan->buf, prefix_plan->num_seqs, prefix_plan->num_workers, prefix_plan->tile_tokens, prefix_o,
                                           prefix_lse, plan->buf, plan->num_ctas, split_o, split_lse,
                                           static_cast<__nv_bfloat16*>(out), out_lse, batch, num_q_heads, num_kv_heads,
                                           q_len, static_cast<cudaStream_t>(stream)));

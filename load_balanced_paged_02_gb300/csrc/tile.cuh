@@ -1,17 +1,19 @@
 // Tile maps: the work of prompt attention (hpc_prefill_*) and of shared-prefix
-// attention (hpc_prefix_*) as tiles of 32 query tokens x the 8 query heads of
-// one KV head, each over a run of 128-token KV blocks. Layout of the map and
+// attention (hpc_prefix_*) as tiles of 32 or 64 query tokens x the 8 query heads
+// of one KV head, each over a run of 128-token KV blocks. Layout of the map and
 // the walk over it, shared by the planner, the attention kernel and the
 // kernels that merge split tiles.
 //
 // Sequence s (a prompt, or a group of requests behind one prefix) has n query
-// tokens and L keys. Tile i holds query tokens [32 i, min(n, 32 i + 32)) and
-//   prompts:  the keys before L - n + min(n, 32 i + 32) (causal: query token t
+// tokens and L keys. With T tokens per tile (32: a CTA takes a tile; 64: a pair of
+// CTAs does), tile i holds query tokens [T i, min(n, T i + T)) and
+//   prompts:  the keys before L - n + min(n, T i + T) (causal: query token t
 //             sits at position L - n + t), at least one block, so that rows
 //             without a visible key are written too;
 //   prefixes: all L keys (no tile where L is 0).
 // The walk is KV head by KV head, sequence by sequence, tile by tile, block by
-// block; CTA j gets units [j * bucket, (j + 1) * bucket) of it, where a tile is
+// block; worker j (a CTA or a pair) gets units [j * bucket, (j + 1) * bucket) of
+// it, where a tile is
 // kTileCost[mode] units of fixed cost followed by one unit per block. A
 // boundary inside the fixed cost is a boundary before block 0.
 #pragma once
@@ -20,23 +22,24 @@
 
 namespace hpc {
 
-constexpr int kTileTokens = 32;                   // query tokens of a tile
-constexpr int kTileRows = kTileTokens * kGroup;   // 256 query rows
+constexpr int kHalfTokens = 16;                   // query tokens of an MMA's 128 rows
+constexpr int kTileCta = 2 * kHalfTokens, kTilePair = 4 * kHalfTokens;
 constexpr int kBlock = 128;                       // keys of a block: two pages
 constexpr int kModePrefill = 0, kModePrefix = 1;
 
 enum TileHdrSlot {
     kTUnitsPerHead = 0,   // int64
     kTBucket = 2,         // int64
-    kTUsedCtas = 4,
+    kTUsedWorkers = 4,
     kTBatch = 5,
     kTNumKvHeads = 6,
-    kTNumCtas = 7,
+    kTNumWorkers = 7,
     kTNumTokens = 8,
     kTMode = 9,
     kTTilesPerHead = 10,
     kTQLen = 11,
     kTError = 12,
+    kTTileTokens = 13,
 };
 
 // Offsets (int32 units) of the sections of a tile map.
@@ -55,42 +58,42 @@ __host__ __device__ inline TileLayout tile_layout(long long S, long long C) {
 
 __host__ __device__ inline int tile_cost(int mode) { return mode == kModePrefill ? 1 : 0; }
 
-__host__ __device__ inline int tile_count(int n) { return (n + kTileTokens - 1) / kTileTokens; }
+__host__ __device__ inline int tile_count(int n, int T) { return (n + T - 1) / T; }
 
 // Blocks of tile i.
-__host__ __device__ inline int tile_blocks(int mode, int n, int L, int i) {
+__host__ __device__ inline int tile_blocks(int mode, int n, int L, int i, int T) {
     if (mode == kModePrefix) return (int)(((long long)L + kBlock - 1) / kBlock);
-    const long long t1 = (long long)kTileTokens * (i + 1) < n ? (long long)kTileTokens * (i + 1) : n;
+    const long long t1 = (long long)T * (i + 1) < n ? (long long)T * (i + 1) : n;
     const long long e = (long long)L - n + t1;  // keys the tile's last query token sees
     return e <= kBlock ? 1 : (int)((e + kBlock - 1) / kBlock);
 }
 
-// sum of max(1, floor(m / 4)) over m < x, up to a constant
-__host__ __device__ inline long long quarter_sum(long long x) {
-    if (x <= 8) return x;
-    const long long q = x >> 2, s = x & 3;
-    return 8 + (2 * q * (q - 1) + s * q) - 4;  // sum of floor(m / 4) over 8 <= m < x, plus 8
+// sum of max(1, floor(m / R)) over m < x, up to a constant
+__host__ __device__ inline long long step_sum(long long x, int R) {
+    if (x <= 2 * R) return x;
+    const long long q = x / R, s = x % R;
+    return 2 * R + (R * (q * (q - 1) / 2) + s * q) - R;  // sum of floor(m / R) over 2 R <= m < x, plus 2 R
 }
 
-// Units of tiles [0, i) of a sequence, i <= tile_count(n). Every tile but the
-// last has 32 query tokens, so tile j's last key is at L - n + 32 (j + 1) and it
-// has max(1, floor((a + j) / 4)) blocks with a = floor((L - n + 159) / 32).
-__host__ __device__ inline long long tile_units(int mode, int n, int L, int i) {
+// Units of tiles [0, i) of a sequence, i <= tile_count. Every tile but the last
+// has T query tokens, so tile j's last key is at L - n + T (j + 1) and, with R = 128
+// / T, it has max(1, floor((a + j) / R)) blocks, a = floor((L - n + T + 127) / T).
+__host__ __device__ inline long long tile_units(int mode, int n, int L, int i, int T) {
     if (i <= 0) return 0;
-    if (mode == kModePrefix) return (long long)i * tile_blocks(mode, n, L, 0);
-    const int nt = tile_count(n);
+    if (mode == kModePrefix) return (long long)i * tile_blocks(mode, n, L, 0, T);
+    const int nt = tile_count(n, T);
     const int full = i < nt ? i : nt - 1;
-    const long long x = (long long)L - n + 159;
-    const long long a = x >= 0 ? x / kTileTokens : -((-x + kTileTokens - 1) / kTileTokens);
-    long long u = quarter_sum(a + full) - quarter_sum(a) + (long long)i * tile_cost(mode);
-    if (i == nt) u += tile_blocks(mode, n, L, nt - 1);
+    const long long x = (long long)L - n + T + kBlock - 1;
+    const long long a = x >= 0 ? x / T : -((-x + T - 1) / T);
+    long long u = step_sum(a + full, kBlock / T) - step_sum(a, kBlock / T) + (long long)i * tile_cost(mode);
+    if (i == nt) u += tile_blocks(mode, n, L, nt - 1, T);
     return u;
 }
 
 // ----------------------------------------------------------------- launchers
 
 cudaError_t launch_tile_plan(const int32_t* q_starts, const int32_t* lens, int S, int num_tokens, int Hkv, int C,
-                             int min_blocks, int max_len, int mode, int q_len, int32_t* buf, cudaStream_t s);
+                             int min_blocks, int max_len, int mode, int q_len, int T, int32_t* buf, cudaStream_t s);
 
 struct TileAttnArgs {
     const void* q;  // bf16 [num_tokens][Hq][128]
@@ -104,7 +107,7 @@ struct TileAttnArgs {
     int pt_stride;
     int S, num_tokens, num_q_heads, num_kv_heads;
     int32_t* plan;
-    int num_ctas, mode;
+    int num_workers, mode, tile_tokens;
     float* split_o;
     float* split_lse;
     void* out;       // prompts only
@@ -113,10 +116,10 @@ struct TileAttnArgs {
 cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s);
 int tile_default_ctas();
 
-cudaError_t launch_prefill_combine(const int32_t* plan, int S, int Hq, int C, const float* split_o, const float* split_lse,
-                                   void* out, float* out_lse, cudaStream_t s);
+cudaError_t launch_prefill_combine(const int32_t* plan, int S, int Hq, int C, int T, const float* split_o,
+                                   const float* split_lse, void* out, float* out_lse, cudaStream_t s);
 
-cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_ctas, const float* prefix_o,
+cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_workers, int T, const float* prefix_o,
                                   const float* prefix_lse, const int32_t* plan, int ctas, const float* split_o,
                                   const float* split_lse, __nv_bfloat16* out, float* out_lse, int B, int Hq, int Hkv,
                                   int q_len, cudaStream_t s);
@@ -136,14 +139,15 @@ struct TileItem {
     int tile;        // number of the tile in the walk
 };
 
-// Walks the items of one CTA's part of the map.
+// Walks the items of one worker's part of the map.
+template <int T>
 struct TileWalk {
     const int4* seqs;
     int S, mode, tiles_per_head;
     TilePos at, end;
 
-    __device__ __forceinline__ void start(const int32_t* plan, int S_, int mode_, int cta, long long seqs_off) {
-        const int4* st = reinterpret_cast<const int4*>(plan + kHdrInts + (long long)cta * 8);
+    __device__ __forceinline__ void start(const int32_t* plan, int S_, int mode_, int worker, long long seqs_off) {
+        const int4* st = reinterpret_cast<const int4*>(plan + kHdrInts + (long long)worker * 8);
         const int4 a = st[0], e = st[2];
         at = TilePos{a.x, a.y, a.z, a.w};
         end = TilePos{e.x, e.y, e.z, e.w};
@@ -153,13 +157,13 @@ struct TileWalk {
         tiles_per_head = plan[kTTilesPerHead];
     }
 
-    // The next item; false at the end of the CTA's part.
+    // The next item; false at the end of the worker's part.
     __device__ __forceinline__ bool next(TileItem& it) {
         for (;;) {
             const bool last = at.h == end.h && at.s == end.s && at.i == end.i;
             if (last && at.blk >= end.blk) return false;
             const int4 q = seqs[at.s];
-            const int blocks = tile_blocks(mode, q.y, q.z, at.i);
+            const int blocks = tile_blocks(mode, q.y, q.z, at.i, T);
             it.h = at.h;
             it.s = at.s;
             it.i = at.i;
@@ -174,7 +178,7 @@ struct TileWalk {
                 at.blk = end.blk;
             } else {
                 at.blk = 0;
-                if (++at.i >= tile_count(q.y)) {
+                if (++at.i >= tile_count(q.y, T)) {
                     at.i = 0;
                     // the next sequence that has tiles (the walk ends at `end`, which
                     // has, or at the head after the last)
@@ -198,12 +202,12 @@ struct TileWalk {
     }
 };
 
-// Row of the split buffers where a piece of a tile goes, in units of kTileRows
-// rows. Prompts: only cut tiles have pieces; a CTA has at most one that goes on
-// from the CTA before and one that starts there. Prefixes: every piece; from one
-// piece to the next the tile number, the CTA number or both grow.
-__device__ __forceinline__ long long tile_slot(int mode, int cta, const TileItem& it) {
-    return mode == kModePrefill ? 2LL * cta + (it.b0 == 0 ? 1 : 0) : (long long)it.tile + cta;
+// Row of the split buffers where a piece of a tile goes, in units of a tile's
+// rows. Prompts: only cut tiles have pieces; a worker has at most one that goes on
+// from the worker before and one that starts there. Prefixes: every piece; from one
+// piece to the next the tile number, the worker number or both grow.
+__device__ __forceinline__ long long tile_slot(int mode, int worker, const TileItem& it) {
+    return mode == kModePrefill ? 2LL * worker + (it.b0 == 0 ? 1 : 0) : (long long)it.tile + worker;
 }
 
 #endif  // __CUDACC__

@@ -11,7 +11,12 @@
 // a cut one (and every prefix piece) as normalised float32 rows with their LSE,
 // which the kernels in tile_combine.cu merge.
 //
-// One CTA per SM, 12 warps (e4m3: 16):
+// One CTA per SM, 12 warps (e4m3: 16). A tile of 32 query tokens belongs to one
+// CTA (CG = 1), one of 64 to a pair of CTAs (CG = 2) whose products run on both
+// SMs' tensor cores at once (cta_group::2, M = 256): each CTA keeps its own query
+// rows, scores and sums, and loads only half of every K and V block (one page of
+// K, one dim half of V), which halves the copies and the shared memory that the
+// products read. The leader (rank 0) issues for both.
 //  * warps 0-3 and 4-7, the softmax warpgroups of the two halves: one thread
 //    per query row. Scores come from TMEM, P goes back over them as 16-bit
 //    pairs (the A operand of the second product), O is scaled in TMEM only when
@@ -22,13 +27,15 @@
 //      S0(0) S1(0) | PV0(0) S0(1) PV1(0) S1(1) | PV0(1) ...
 //    so that one half's products run while the other half's softmax does. MMAs
 //    of one thread run in order, so S(j+1) may overwrite P(j) once PV(j) has
-//    been issued.
+//    been issued. In the other CTA of a pair this warp tells the leader which of
+//    its stages are filled.
 //  * e4m3, warps 12-15: the query rows split into two e4m3 tiles of codes
 //    (Q = (Q_hi + Q_lo) 2^e, as in attn_tc.cu), so that Q K^T runs on the K
 //    codes as they are; V widened to f16 (code x scale) into a ring of its own.
 // Every wait is bounded; on expiry the CTA records HPC_DEVERR_WAIT_TIMEOUT.
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "tcgen05.cuh"
@@ -44,48 +51,79 @@ using attn::kWaitLimitNs;
 using attn::wait_bounded;
 
 constexpr int kHalfRows = 128;
-constexpr int kHalfTokens = kTileTokens / 2;
 constexpr int kQBytes = 32768;           // a half's query rows: [2 dim halves][128 rows][128 B]
 constexpr float kRescaleLog2 = 8.0f;     // lazy rescale threshold: P <= 2^8
-constexpr int kMetaRing = 8;             // blocks whose page checks (and, e4m3, K scales) are kept
+constexpr int kMetaRing = 8;             // blocks whose page checks (and, e4m3, scales) are kept
+constexpr int kWide = 2;                 // e4m3: f16 V tiles
+constexpr int kOutBytes = 2048;          // a softmax warp's staging of 32 output rows x 64 B
 constexpr uint32_t kTmemCols = 512;      // S of half t at column 128 t (P over its first 64), O at 256 + 128 t
 
-template <bool FP8>
+template <bool FP8, int CG>
 struct Cfg {
-    static constexpr int kStages = 5;
-    static constexpr int kStageBytes = FP8 ? 16384 : 32768;  // 128 tokens of K or of V
-    static constexpr int kWide = FP8 ? 2 : 0;                // f16 V tiles of 32 KB
+    static constexpr int kStageBytes = (FP8 ? 16384 : 32768) / CG;  // 128 tokens of K or of V, or this CTA's half
+    static constexpr int kWideBytes = 32768 / CG;
+    // an even number: a stage serves K always, or V always
+    static constexpr int kStages = 4 * CG;
+    static_assert(kStages % 2 == 0 && kStages <= kMetaRing, "stages");
     static constexpr int kWarps = FP8 ? 16 : 12;
     static constexpr int kThreads = kWarps * 32;
     // registers per thread after the split (setmaxnreg): the launch's total, 384 x
     // 168 or 512 x 128, is what the two softmax warpgroups and the others share
-    static constexpr int kRegsSoftmax = FP8 ? 184 : 208;
-    static constexpr int kRegsOther = FP8 ? 72 : 88;
+    static constexpr int kRegsSoftmax = FP8 ? 192 : 208;
+    static constexpr int kRegsOther = FP8 ? 64 : 88;
     static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * (FP8 ? 128 : 168), "register split");
 };
 
-template <bool FP8>
+template <bool FP8, int CG>
 struct Smem {
-    using C = Cfg<FP8>;
+    using C = Cfg<FP8, CG>;
     static constexpr size_t kQ = 0;
     static constexpr size_t kRing = kQ + 2 * kQBytes;
-    static constexpr size_t kWide = kRing + (size_t)C::kStages * C::kStageBytes;
-    static constexpr size_t kKs = kWide + (size_t)C::kWide * 32768;            // float [ring][128] K scales
+    static constexpr size_t kWideV = kRing + (size_t)C::kStages * C::kStageBytes;
+    static constexpr size_t kOut = kWideV + (FP8 ? (size_t)kWide * C::kWideBytes : 0);
+    static constexpr size_t kKs = kOut + 8 * kOutBytes;                        // float [ring][128] K scales
     static constexpr size_t kVs = kKs + (FP8 ? kMetaRing * 512 : 0);           // float [ring][128] V scales
     static constexpr size_t kQs = kVs + (FP8 ? kMetaRing * 512 : 0);           // float [2 parities][2 halves][128]
     static constexpr size_t kMeta = kQs + (FP8 ? 2048 : 0);
     static constexpr size_t kBars = kMeta + kMetaRing * 4;
-    // full, empty (stages); qfull, qempty, sfull, pfull, ofull, ofree (halves); e4m3: q8full (halves), wfull, wempty
-    static constexpr int kNumBars = 2 * C::kStages + 12 + (FP8 ? 6 : 0);
+    // full, empty, rfull (stages); qfull, rqfull, qempty, sfull, pfull (2), ofull,
+    // ofree (halves); e4m3: q8full (halves), wfull, wempty (wide tiles)
+    static constexpr int kNumBars = 3 * C::kStages + 16 + (FP8 ? 2 + 2 * kWide : 0);
     static constexpr size_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr size_t kFlag = kTmemSlot + 8;
     static constexpr size_t kAlloc = kFlag + 8 + 1024;
     static_assert(kAlloc <= 232448, "over the 227 KB shared-memory limit of a CTA");
+    static_assert(kWideV % 1024 == 0 && kOut % 1024 == 0, "swizzled tiles need 1 KB alignment");
 };
+
+// ------------------------------------------------------------------ waits and arrivals
 
 // A whole warp waits; one answer for all its lanes.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, kWaitLimitNs));
+}
+
+// Arrives on the leader's barrier at this address (this CTA's own for CG 1).
+template <int CG>
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    if constexpr (CG == 1) {
+        mbar_arrive(bar);
+    } else {
+        asm volatile(
+            "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+            "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+            : "memory");
+    }
+}
+
+template <int CG>
+__device__ __forceinline__ void cluster_sync_all() {
+    if constexpr (CG == 2) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
 }
 
 struct TileParams {
@@ -119,14 +157,84 @@ __device__ __forceinline__ void tma_load_2d_plain(void* dst, const CUtensorMap* 
         : "memory");
 }
 
-// D (TMEM) (+)= A . B^T with A (16-bit, K-major) in TMEM: lane = row, two
-// elements of K per column.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+// D (TMEM) (+)= A . B^T for one CTA, or for a pair at once (each CTA's rows of A
+// and D, half of B from each). ss: A and B in shared memory; ts: A (16-bit,
+// K-major) in TMEM, lane = row, two elements of K per column.
+// The whole warp runs these with the same operands and only its elected lane (el)
+// issues: the operands then stay in uniform registers. Inside an `if (lane == 0)`
+// they were moved there for every instruction, and with two busy softmax warps on
+// the same scheduler the issue, not the tensor core, set the pace (a product pair
+// of 16 MMAs took 1670 clocks in place of 1024).
+template <int CG>
+__device__ __forceinline__ void mma_ss_16(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma_ts_16(uint32_t el, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(el)
+            : "memory");
+}
+
+// Arrives on bar (in both CTAs of a pair) once the MMAs issued before are done.
+template <int CG>
+__device__ __forceinline__ void mma_commit(uint32_t el, uint64_t* bar) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+            "r"(el)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3), "r"(el)
+            : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e;
 }
 
 // 32 columns of this thread's lane (32x32b shape: thread t of a warp holds lane t
@@ -139,6 +247,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
           "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
           "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
           "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
         : "r"(taddr)
         : "memory");
 }
@@ -197,6 +314,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// The same, kept in program order by the compiler.
+__device__ __forceinline__ float max3_in_order(float a, float b, float c) {
+    float d;
+    asm volatile("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float exp2_in_order(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 template <int N>
 __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -220,27 +349,27 @@ __device__ __forceinline__ bool named_any_128(bool x) {
 }
 
 // One half's bf16 query rows -> e4m3 hi / lo tiles in place ([128 rows][128 B]
-// each) and their power-of-two row scales. Lane pair (2 j, 2 j + 1) of warp wq
-// takes row 32 wq + j + 16 u, u < 2; half hh = lane & 1 reads bf16 dims
-// [64 hh, 64 hh + 64), which sit where row r of the hi tile (hh = 0) or of the lo
-// tile (hh = 1) goes, and writes the hi and lo codes of its dims once both have
-// read.
+// each) and their power-of-two row scales. Lanes 4 j .. 4 j + 3 of warp wq take row
+// 32 wq + j + 8 u, u < 4; lane quarter qq reads bf16 dims [32 qq, 32 qq + 32), which
+// sit where row r of the hi tile (qq < 2) or of the lo tile goes, and writes the hi
+// and lo codes of its dims once all four have read.
 __device__ __forceinline__ void split_query_rows(uint8_t* qt, float* qs, int wq, int lane) {
 #pragma unroll 1
-    for (int u = 0; u < 2; ++u) {
-        const int r = 32 * wq + 16 * u + (lane >> 1), hh = lane & 1;
-        uint4 raw[8];
+    for (int u = 0; u < 4; ++u) {
+        const int r = 32 * wq + 8 * u + (lane >> 2), qq = lane & 3;
+        uint4 raw[4];
         float amax = 0.f;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            raw[c] = *reinterpret_cast<const uint4*>(qt + hh * 16384 + r * 128 + ((c ^ (r & 7)) << 4));
+        for (int c = 0; c < 4; ++c) {
+            raw[c] = *reinterpret_cast<const uint4*>(qt + (qq >> 1) * 16384 + r * 128 + (((4 * (qq & 1) + c) ^ (r & 7)) << 4));
             const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
         }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        __syncwarp();  // the partner lane has read its half row
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        __syncwarp();  // the row's other lanes have read it
         // the smallest power of two 2^ex with amax / 2^ex <= 448: q / 2^ex is exact
         // (rows under 2^-90 keep fewer bits: their scores are 0 to float32 anyway; an
         // infinite element makes the row's scores infinite or NaN)
@@ -254,9 +383,9 @@ __device__ __forceinline__ void split_query_rows(uint8_t* qt, float* qs, int wq,
             qscale = ldexpf(1.f, ex);
             qinv = ldexpf(1.f, -ex);
         }
-        if (hh == 0) qs[r] = qscale;
+        if (qq == 0) qs[r] = qscale;
 #pragma unroll
-        for (int c2 = 0; c2 < 4; ++c2) {
+        for (int c2 = 0; c2 < 2; ++c2) {
             uint2 hp[2], lp[2];
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
@@ -270,7 +399,7 @@ __device__ __forceinline__ void split_query_rows(uint8_t* qt, float* qs, int wq,
                 }
                 split_e4m3x8(x, hp[v], lp[v]);
             }
-            const int off = r * 128 + (((4 * hh + c2) ^ (r & 7)) << 4);
+            const int off = r * 128 + (((2 * qq + c2) ^ (r & 7)) << 4);
             *reinterpret_cast<uint4*>(qt + off) = make_uint4(hp[0].x, hp[0].y, hp[1].x, hp[1].y);
             *reinterpret_cast<uint4*>(qt + 16384 + off) = make_uint4(lp[0].x, lp[0].y, lp[1].x, lp[1].y);
         }
@@ -279,11 +408,13 @@ __device__ __forceinline__ void split_query_rows(uint8_t* qt, float* qs, int wq,
 }
 
 // 128 tokens of V codes -> an f16 tile (code x scale, rounded to f16; rows from
-// nv on zero), [2 dim halves][128 rows][128 B] swizzled. The scale is taken as
-// (f 2^a) (2^b) with 1 <= |f| < 2, so that a scale far below f16's smallest normal
-// number keeps its bits until the last product. Thread tg takes the 16-code
-// pieces (tg & 3) + 4 hf of rows 32 rr + tg / 4: loads and stores of a warp spread
-// over all banks.
+// nv on zero), [dim halves][128 rows][128 B] swizzled: both dim halves from rows of
+// 128 swizzled bytes (CG 1), or this CTA's half from plain rows of 64 bytes (CG 2).
+// The scale is taken as (f 2^a) (2^b) with 1 <= |f| < 2, so that a scale far below
+// f16's smallest normal number keeps its bits until the last product. Thread tg
+// takes the 16-code pieces (tg & 3) + 4 hf of rows 32 rr + tg / 4: loads and stores
+// of a warp spread over all banks.
+template <int CG>
 __device__ __forceinline__ void widen_v(const uint8_t* codes, const float* vs, uint8_t* wide, int nv, int tg) {
 #pragma unroll 2
     for (int rr = 0; rr < 4; ++rr) {
@@ -297,11 +428,12 @@ __device__ __forceinline__ void widen_v(const uint8_t* codes, const float* vs, u
         const float fb = e == 128 ? 1.f : __uint_as_float((uint32_t)max(e - a + 127, 0) << 23);
         const uint32_t s2 = pack_f16x2(fa, fa), p2 = pack_f16x2(fb, fb);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+        for (int hf = 0; hf < 2 / CG; ++hf) {
             const int c16 = (tg & 3) + 4 * hf;
             uint4 vl = make_uint4(0, 0, 0, 0), vh = vl;
             if (in) {
-                const uint4 w = *reinterpret_cast<const uint4*>(codes + row * 128 + ((c16 ^ (row & 7)) << 4));
+                const uint4 w = *reinterpret_cast<const uint4*>(
+                    CG == 1 ? codes + row * 128 + ((c16 ^ (row & 7)) << 4) : codes + row * 64 + c16 * 16);
                 e4m3x4_to_f16x2x2(w.x, vl.x, vl.y);
                 e4m3x4_to_f16x2x2(w.y, vl.z, vl.w);
                 e4m3x4_to_f16x2x2(w.z, vh.x, vh.y);
@@ -318,28 +450,46 @@ __device__ __forceinline__ void widen_v(const uint8_t* codes, const float* vs, u
     }
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
+// Rows [nv, end of their page) of a bf16 V tile to zero: slots behind the
+// sequence's last token may hold any bits, and 0 x NaN would reach the sums. Done by
+// one warp. (Rows of pages that were not loaded came as zeros.)
+template <int CG>
+__device__ __forceinline__ void zero_tail(uint8_t* vt, int nv, int lane) {
+    const int lo = max(nv, 0), hi = (lo + kChunk - 1) / kChunk * kChunk;
+    constexpr int kPieces = 16 / CG;  // 16-byte pieces of a row
+    for (int i = lane; i < (hi - lo) * kPieces; i += 32) {
+        const int row = lo + i / kPieces, part = i % kPieces;
+        *reinterpret_cast<uint4*>(vt + (part >> 3) * 16384 + row * 128 + (part & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+template <bool FP8, int CG>
+__global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
     tile_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
                      const __grid_constant__ CUtensorMap tm_vs, const TileParams p) {
-    using C = Cfg<FP8>;
-    using LY = Smem<FP8>;
+    using C = Cfg<FP8, CG>;
+    using LY = Smem<FP8, CG>;
     constexpr int NS = C::kStages;
+    constexpr int T = kTileCta * CG;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + LY::kBars);
     uint64_t* empty = full + NS;
-    uint64_t* qfull = empty + NS;
-    uint64_t* qempty = qfull + 2;
+    uint64_t* rfull = empty + NS;  // leader of a pair: the other CTA's stage is filled
+    uint64_t* qfull = rfull + NS;
+    uint64_t* rqfull = qfull + 2;  // leader of a pair: the other CTA's query rows
+    uint64_t* qempty = rqfull + 2;
     uint64_t* sfull = qempty + 2;
     uint64_t* pfull = sfull + 2;
-    uint64_t* ofull = pfull + 2;
+    uint64_t* ofull = pfull + 4;  // (two P barriers per half: its first 64 tokens, its last)
     uint64_t* ofree = ofull + 2;
     uint64_t* q8full = ofree + 2;  // e4m3 from here on
     uint64_t* wfull = q8full + 2;
-    uint64_t* wempty = wfull + 2;
+    uint64_t* wempty = wfull + kWide;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + LY::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kFlag);
     volatile int* meta = reinterpret_cast<volatile int*>(smem + LY::kMeta);
@@ -347,43 +497,58 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
     uint8_t* ring = smem + LY::kRing;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0, worker = (int)blockIdx.x / CG;
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
+            mbar_init(&rfull[i], 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&qfull[t], 1);
+            mbar_init(&rqfull[t], 1);
             mbar_init(&qempty[t], 1);
             mbar_init(&sfull[t], 1);
-            mbar_init(&pfull[t], 4);  // one arrival per softmax warp
+            mbar_init(&pfull[2 * t], 4 * CG);  // one arrival per softmax warp
+            mbar_init(&pfull[2 * t + 1], 4 * CG);
             mbar_init(&ofull[t], 1);
-            mbar_init(&ofree[t], 4);
-            if constexpr (FP8) {
-                mbar_init(&q8full[t], 4);
-                mbar_init(&wfull[t], 1);
-                mbar_init(&wempty[t], 1);
+            mbar_init(&ofree[t], 4 * CG);
+        }
+        if constexpr (FP8) {
+            for (int t = 0; t < 2; ++t) mbar_init(&q8full[t], 4 * CG);
+            for (int i = 0; i < kWide; ++i) {
+                mbar_init(&wfull[i], CG);
+                mbar_init(&wempty[i], 1);
             }
         }
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(const_cast<uint32_t*>(tmem_slot))),
-                     "r"(kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (CG == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(const_cast<uint32_t*>(tmem_slot))),
+                         "r"(kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(const_cast<uint32_t*>(tmem_slot))),
+                         "r"(kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all<CG>();  // the other CTA's barriers are set up too
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();  // the map, the query and the new tokens' keys come from the kernels before
     grid_launch_dependents();
 
-    TileWalk walk;
-    walk.start(p.plan, p.S, p.mode, blockIdx.x, p.seqs_off);
+    TileWalk<T> walk;
+    walk.start(p.plan, p.S, p.mode, worker, p.seqs_off);
     TileItem it;
     bool ok = true;
 
@@ -397,13 +562,15 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             while (ok && walk.next(it)) {
                 if (lane == 0) {
                     for (int t = 0; t < 2 && ok; ++t) {
-                        const int tok = it.i * kTileTokens + t * kHalfTokens;
-                        if (tok >= it.n) break;
+                        if (it.i * T + t * kHalfTokens * CG >= it.n) break;
+                        // rows past the sequence's last token load whatever follows (zeros
+                        // past the last query row); they are computed and not written
+                        const int tok = it.q0 + it.i * T + (t * CG + rank) * kHalfTokens;
                         ok = wait_bounded(&qempty[t], (nd[t] & 1) ^ 1, abort_flag, kWaitLimitNs);
                         if (!ok) break;
                         mbar_arrive_expect_tx(&qfull[t], kQBytes);
-                        tma_load_3d_plain(qbuf + t * kQBytes, &tm_q, &qfull[t], 0, it.h * kGroup, it.q0 + tok);
-                        tma_load_3d_plain(qbuf + t * kQBytes + kQBytes / 2, &tm_q, &qfull[t], 64, it.h * kGroup, it.q0 + tok);
+                        tma_load_3d_plain(qbuf + t * kQBytes, &tm_q, &qfull[t], 0, it.h * kGroup, tok);
+                        tma_load_3d_plain(qbuf + t * kQBytes + kQBytes / 2, &tm_q, &qfull[t], 64, it.h * kGroup, tok);
                         ++nd[t];
                     }
                 }
@@ -434,21 +601,31 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                                 if (kvi == 0) meta[blks % kMetaRing] = (pg0 < p.num_pages ? 1 : 0) | (pg1 < p.num_pages ? 2 : 0);
                                 const CUtensorMap* tm = kvi == 0 ? &tm_k : &tm_v;
                                 uint8_t* dst = ring + (size_t)st * C::kStageBytes;
+                                mbar_arrive_expect_tx(&full[st], C::kStageBytes + (FP8 ? kBlock * 4 : 0));
                                 if constexpr (FP8) {
                                     float* sc = reinterpret_cast<float*>(smem + (kvi == 0 ? LY::kKs : LY::kVs)) +
                                                 (blks % kMetaRing) * kBlock;
                                     const CUtensorMap* ts = kvi == 0 ? &tm_ks : &tm_vs;
-                                    mbar_arrive_expect_tx(&full[st], C::kStageBytes + kBlock * 4);
                                     tma_load_2d_plain(sc, ts, &full[st], 0, pg0 * p.num_kv_heads + it.h);
                                     tma_load_2d_plain(sc + kChunk, ts, &full[st], 0, pg1 * p.num_kv_heads + it.h);
-                                    tma_load_3d_plain(dst, tm, &full[st], 0, it.h, pg0 * kChunk);
-                                    tma_load_3d_plain(dst + 8192, tm, &full[st], 0, it.h, pg1 * kChunk);
+                                }
+                                if constexpr (CG == 2) {
+                                    // K: this CTA's page, both dim halves; V: both pages, this CTA's dim half
+                                    if (kvi == 0) {
+                                        const int tok = (rank ? pg1 : pg0) * kChunk;
+                                        tma_load_3d_plain(dst, tm, &full[st], 0, it.h, tok);
+                                        if constexpr (!FP8) tma_load_3d_plain(dst + 8192, tm, &full[st], 64, it.h, tok);
+                                    } else {
+                                        tma_load_3d_plain(dst, tm, &full[st], 64 * rank, it.h, pg0 * kChunk);
+                                        tma_load_3d_plain(dst + (FP8 ? 4096 : 8192), tm, &full[st], 64 * rank, it.h, pg1 * kChunk);
+                                    }
                                 } else {
-                                    mbar_arrive_expect_tx(&full[st], C::kStageBytes);
                                     tma_load_3d_plain(dst, tm, &full[st], 0, it.h, pg0 * kChunk);
-                                    tma_load_3d_plain(dst + 16384, tm, &full[st], 64, it.h, pg0 * kChunk);
                                     tma_load_3d_plain(dst + 8192, tm, &full[st], 0, it.h, pg1 * kChunk);
-                                    tma_load_3d_plain(dst + 24576, tm, &full[st], 64, it.h, pg1 * kChunk);
+                                    if constexpr (!FP8) {
+                                        tma_load_3d_plain(dst + 16384, tm, &full[st], 64, it.h, pg0 * kChunk);
+                                        tma_load_3d_plain(dst + 24576, tm, &full[st], 64, it.h, pg1 * kChunk);
+                                    }
                                 }
                             }
                         }
@@ -464,106 +641,131 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 for (int t = 0; t < 2; ++t)
                     if (nd[t] > 0) wait_bounded(&qfull[t], (nd[t] - 1) & 1, nullptr, kDrainLimitNs);
             }
-        } else if (warp == 9) {
+        } else if (warp == 9 && rank == 0) {
             // ============================ issuer
-            constexpr uint32_t kIdS = FP8 ? idesc_e4m3(kHalfRows, kBlock) : idesc_16bit(false, kHalfRows, kBlock, 0);
-            constexpr uint32_t kIdO = idesc_16bit(FP8, kHalfRows, kHeadDim, 1);
-            uint64_t* const qready = FP8 ? q8full : qfull;
+            constexpr uint32_t kIdS = FP8 ? idesc_e4m3(CG * kHalfRows, kBlock) : idesc_16bit(false, CG * kHalfRows, kBlock, 0);
+            constexpr uint32_t kIdO = idesc_16bit(FP8, CG * kHalfRows, kHeadDim, 1);
+            constexpr uint32_t kKHalf = 16384 / CG;  // bytes of a K tile's dim half
             uint32_t kv = 0;            // stages taken
             uint32_t blks = 0;          // V blocks taken
             uint32_t np[2] = {0, 0};    // P tiles taken
             int nd[2] = {0, 0};         // items
-            while (ok && walk.next(it)) {
-                const int halves = it.n - it.i * kTileTokens > kHalfTokens ? 2 : 1;
-                // S of half t from the K tile in stage st
-                auto issue_s = [&](int t, uint32_t st) {
-                    const uint32_t qa = smem_u32(qbuf + t * kQBytes), ka = smem_u32(ring + (size_t)st * C::kStageBytes);
-                    if constexpr (FP8) {
+            // stage number kv filled (in both CTAs)
+            auto wait_stage = [&](uint32_t k) {
+                return wait_warp(&full[k % NS], (k / NS) & 1, abort_flag) &&
+                       (CG == 1 || wait_warp(&rfull[k % NS], (k / NS) & 1, abort_flag));
+            };
+            const uint32_t el = elect_one();
+            // descriptors of the first query tile, stage and V tile; the others lie at
+            // fixed distances (in 16-byte units, the low bits of a descriptor)
+            const uint64_t dq = sdesc_sw128(smem_u32(qbuf), 16, 1024), dk = sdesc_sw128(smem_u32(ring), 16, 1024);
+            const uint64_t dv = sdesc_sw128(smem_u32(FP8 ? smem + LY::kWideV : ring), 16384, 1024);
+            // S of half t from the K tile in stage st
+            auto issue_s = [&](int t, uint32_t st) {
+                const uint64_t q = dq + (uint32_t)t * (kQBytes >> 4), k = dk + st * (C::kStageBytes >> 4);
+                if constexpr (FP8) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            umma_e4m3(tmem + 128 * t, sdesc_sw128(qa + kk * 32, 16, 1024), sdesc_sw128(ka + kk * 32, 16, 1024),
-                                      kIdS, kk > 0);
-                            umma_e4m3(tmem + 128 * t, sdesc_sw128(qa + 16384 + kk * 32, 16, 1024),
-                                      sdesc_sw128(ka + kk * 32, 16, 1024), kIdS, 1);
-                        }
-                    } else {
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
-                            umma_f16(tmem + 128 * t, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), kIdS,
-                                     kk > 0);
-                        }
+                    for (int kk = 0; kk < 4; ++kk) {
+                        mma_ss_e4m3<CG>(el, tmem + 128 * t, q + kk * 2, k + kk * 2, kIdS, kk > 0);
+                        mma_ss_e4m3<CG>(el, tmem + 128 * t, q + 1024 + kk * 2, k + kk * 2, kIdS, 1);
                     }
-                    umma_commit(&sfull[t]);
-                };
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ss_16<CG>(el, tmem + 128 * t, q + (kk >> 2) * 1024 + (kk & 3) * 2,
+                                      k + (kk >> 2) * (kKHalf >> 4) + (kk & 3) * 2, kIdS, kk > 0);
+                }
+                mma_commit<CG>(el, &sfull[t]);
+            };
+            while (ok && walk.next(it)) {
+                const int halves = it.n - it.i * T > kHalfTokens * CG ? 2 : 1;
                 // first S of both halves
-                ok = wait_warp(&full[kv % NS], (kv / NS) & 1, abort_flag);
+                ok = wait_stage(kv);
                 for (int t = 0; t < halves && ok; ++t) {
-                    ok = wait_warp(&qready[t], nd[t] & 1, abort_flag);
+                    ok = wait_warp(FP8 ? &q8full[t] : &qfull[t], nd[t] & 1, abort_flag) &&
+                         (FP8 || CG == 1 || wait_warp(&rqfull[t], nd[t] & 1, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) {
-                        issue_s(t, kv % NS);
-                        if (it.b1 - it.b0 == 1) umma_commit(&qempty[t]);
-                        if (t == halves - 1) umma_commit(&empty[kv % NS]);
-                    }
-                    __syncwarp();
+                    issue_s(t, kv % NS);
+                    if (it.b1 - it.b0 == 1) mma_commit<CG>(el, &qempty[t]);
+                    if (t == halves - 1) mma_commit<CG>(el, &empty[kv % NS]);
                 }
                 ++kv;
                 for (int b = it.b0; b < it.b1 && ok; ++b, ++blks) {
                     const uint32_t vst = kv % NS;
                     const bool more = b + 1 < it.b1;
-                    uint32_t va;
+                    uint8_t* vt = FP8 ? smem + LY::kWideV + (blks % kWide) * C::kWideBytes : ring + (size_t)vst * C::kStageBytes;
+                    const uint64_t v = dv + (FP8 ? (blks % kWide) * (C::kWideBytes >> 4) : vst * (C::kStageBytes >> 4));
                     if constexpr (FP8) {
-                        va = smem_u32(smem + LY::kWide + (blks & 1) * 32768);
-                        ok = wait_warp(&wfull[blks & 1], (blks >> 1) & 1, abort_flag);
+                        ok = wait_warp(&wfull[blks % kWide], (blks / kWide) & 1, abort_flag);
                     } else {
-                        uint8_t* vt = ring + (size_t)vst * C::kStageBytes;
-                        va = smem_u32(vt);
-                        ok = wait_warp(&full[vst], (kv / NS) & 1, abort_flag);
-                        // rows of the last page past the sequence's end may hold any bits, and
-                        // 0 x NaN would reach the sums: zero them (whole missing pages came as zeros)
+                        ok = wait_stage(kv);
                         const int nv = it.L - b * kBlock;
-                        if (nv < kBlock && (nv & (kChunk - 1)) != 0) {
-                            const int hi = (max(nv, 0) + kChunk - 1) / kChunk * kChunk;
-                            for (int i = lane; i < (hi - max(nv, 0)) * 16; i += 32) {
-                                const int row = max(nv, 0) + i / 16, part = i % 16;
-                                *reinterpret_cast<uint4*>(vt + (part >> 3) * 16384 + row * 128 + (part & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
+                        if (ok && nv < kBlock && (nv & (kChunk - 1)) != 0) zero_tail<CG>(vt, nv, lane);
                     }
                     if (!ok) break;
                     ++kv;
                     for (int t = 0; t < halves && ok; ++t) {
                         // the first product of an item overwrites O: the item before must have left it
                         if (b == it.b0 && nd[t] > 0) ok = wait_warp(&ofree[t], (nd[t] - 1) & 1, abort_flag);
-                        ok = ok && wait_warp(&pfull[t], np[t] & 1, abort_flag);
-                        if (ok && more && t == 0) ok = wait_warp(&full[kv % NS], (kv / NS) & 1, abort_flag);
+                        // P comes in two parts, so that its first product runs while the softmax
+                        // still works on the second
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            ok = ok && wait_warp(&pfull[2 * t + u], np[t] & 1, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 4 * u; kk < 4 * u + 4; ++kk)
+                                mma_ts_16<CG>(el, tmem + 256 + 128 * t, tmem + 128 * t + kk * 8, v + kk * 128, kIdO,
+                                              b > it.b0 || kk > 0);
+                        }
                         if (!ok) break;
                         ++np[t];
-                        tc_fence_after();
-                        if (lane == 0) {
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                umma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + kk * 8, sdesc_sw128(va + kk * 2048, 16384, 1024),
-                                            kIdO, b > it.b0 || kk > 0);
-                            if (t == halves - 1) umma_commit(FP8 ? &wempty[blks & 1] : &empty[vst]);
-                            if (more) {
-                                issue_s(t, kv % NS);
-                                if (b + 2 == it.b1) umma_commit(&qempty[t]);
-                                if (t == halves - 1) umma_commit(&empty[kv % NS]);
-                            } else {
-                                umma_commit(&ofull[t]);
+                        if (t == halves - 1) mma_commit<CG>(el, FP8 ? &wempty[blks % kWide] : &empty[vst]);
+                        if (more) {
+                            if (t == 0) {
+                                ok = wait_stage(kv);
+                                if (!ok) break;
+                                tc_fence_after();
                             }
+                            issue_s(t, kv % NS);
+                            if (b + 2 == it.b1) mma_commit<CG>(el, &qempty[t]);
+                            if (t == halves - 1) mma_commit<CG>(el, &empty[kv % NS]);
+                        } else {
+                            mma_commit<CG>(el, &ofull[t]);
                         }
-                        __syncwarp();
                     }
                     if (more) ++kv;
                 }
                 for (int t = 0; t < halves; ++t) ++nd[t];
+            }
+        } else if (warp == 9) {
+            // ============================ the other CTA of a pair: its filled query rows and
+            // stages, told to the leader in order
+            uint32_t kv = 0;
+            int nd[2] = {0, 0};
+            auto relay = [&](uint64_t* bar, uint32_t parity, uint64_t* to) {
+                ok = ok && wait_warp(bar, parity, abort_flag);
+                if (ok && lane == 0) arrive_leader<CG>(to);
+            };
+            while (ok && walk.next(it)) {
+                const int halves = it.n - it.i * T > kHalfTokens * CG ? 2 : 1;
+                if constexpr (!FP8)
+                    for (int t = 0; t < halves; ++t, ++nd[t - 1]) relay(&qfull[t], nd[t] & 1, &rqfull[t]);
+                for (int b = it.b0; b < it.b1 && ok; ++b) {
+                    relay(&full[kv % NS], (kv / NS) & 1, &rfull[kv % NS]);
+                    ++kv;
+                    if constexpr (!FP8) {
+                        const int nv = it.L - b * kBlock;
+                        if (nv < kBlock && (nv & (kChunk - 1)) != 0) {
+                            ok = ok && wait_warp(&full[kv % NS], (kv / NS) & 1, abort_flag);
+                            if (ok) zero_tail<CG>(ring + (size_t)(kv % NS) * C::kStageBytes, nv, lane);
+                        }
+                        relay(&full[kv % NS], (kv / NS) & 1, &rfull[kv % NS]);
+                    }
+                    ++kv;
+                }
             }
         }
         if (!ok && lane == 0) {
@@ -578,7 +780,7 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
             uint32_t blks = 0;
             int nd[2] = {0, 0};
             while (ok && walk.next(it)) {
-                const int halves = it.n - it.i * kTileTokens > kHalfTokens ? 2 : 1;
+                const int halves = it.n - it.i * T > kHalfTokens * CG ? 2 : 1;
                 for (int t = 0; t < halves && ok; ++t) {
                     ok = wait_warp(&qfull[t], nd[t] & 1, abort_flag);
                     if (!ok) break;
@@ -587,26 +789,23 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                     ++nd[t];
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&q8full[t]);
+                    if (lane == 0) arrive_leader<CG>(&q8full[t]);
                 }
                 // (a warp that gave up must not leave the others at a barrier)
                 ok = !named_any_128(!ok);
                 for (int b = it.b0; b < it.b1 && ok; ++b, ++blks) {
                     const uint32_t kv = 2 * blks + 1, st = kv % NS;  // V of the CTA's block number blks
-                    // (in this order: the P . V of block blks - 2 shows that the stage's use
-                    // before this one, as K of that block, is over, so the parity of its
-                    // barrier is not mistaken)
-                    ok = wait_warp(&wempty[blks & 1], ((blks >> 1) & 1) ^ 1, abort_flag) &&
+                    ok = wait_warp(&wempty[blks % kWide], ((blks / kWide) & 1) ^ 1, abort_flag) &&
                          wait_warp(&full[st], (kv / NS) & 1, abort_flag);
                     ok = !named_any_128(!ok);
                     if (!ok) break;
-                    widen_v(ring + (size_t)st * C::kStageBytes,
-                            reinterpret_cast<const float*>(smem + LY::kVs) + (blks % kMetaRing) * kBlock,
-                            smem + LY::kWide + (blks & 1) * 32768, it.L - b * kBlock, tg);
+                    widen_v<CG>(ring + (size_t)st * C::kStageBytes,
+                                reinterpret_cast<const float*>(smem + LY::kVs) + (blks % kMetaRing) * kBlock,
+                                smem + LY::kWideV + (blks % kWide) * C::kWideBytes, it.L - b * kBlock, tg);
                     fence_proxy_async_smem();
                     named_sync_128();
                     if (tg == 0) {
-                        mbar_arrive(&wfull[blks & 1]);
+                        arrive_leader<CG>(&wfull[blks % kWide]);
                         mbar_arrive(&empty[st]);
                     }
                 }
@@ -623,19 +822,21 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
         const int row = threadIdx.x & 127;
         const uint32_t lane_addr = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t scol = tmem + lane_addr + 128 * t, ocol = tmem + lane_addr + 256 + 128 * t;
-        const int tok_in = t * kHalfTokens + row / kGroup, head = row % kGroup;
+        const int half_tok = (t * CG + rank) * kHalfTokens;  // the half's first token in the tile
+        uint8_t* stage = smem + LY::kOut + warp * kOutBytes;
         uint32_t blks = 0;  // blocks of this CTA
         uint32_t ns = 0;    // score tiles of this half
         int nd = 0;
         while (ok && walk.next(it)) {
-            const int tok = it.i * kTileTokens + tok_in;
-            if (it.n - it.i * kTileTokens <= t * kHalfTokens) {  // an empty half
+            if (it.n - it.i * T <= t * kHalfTokens * CG) {  // an empty half
                 blks += it.b1 - it.b0;
                 continue;
             }
             // keys this row sees; rows past the sequence's last token (computed, not
             // written) see no more than the sequence has
-            const int lim = p.mode == kModePrefix ? it.L : min(it.L, it.L - it.n + tok + 1);
+            const int lim = p.mode == kModePrefix
+                                ? it.L
+                                : min(it.L, it.L - it.n + it.i * T + half_tok + row / kGroup + 1);
             float m = kNegInf, l = 0.f;  // reference maximum (log2 domain) and sum
             float sc = p.scale_log2;
             for (int b = it.b0; b < it.b1; ++b, ++blks, ++ns) {
@@ -671,55 +872,73 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                         if (c >= n1) s[c + kChunk] = kNegInf;
                     }
                 }
-                float mx[4];
+                // P = exp2(s sc - m) of 64 columns, to TMEM as 16-bit pairs; returns their sum
+                // and, with MAX, takes the maximum of all 128 scores along the way: four per
+                // pair of exponentials, whose unit has a quarter of the others' rate, so that
+                // the two run side by side
+                float mx[8];
+                auto exps = [&](int c0, float neg, auto max_too) {
+                    constexpr bool kMax = decltype(max_too)::value;
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int u = 0; u < 4; ++u) mx[u] = s[u];
+                    for (int c = c0; c < c0 + 64; c += 32) {
+                        uint32_t pk[16];
 #pragma unroll
-                for (int c = 4; c + 4 < 128; c += 8)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[c + u], s[c + 4 + u]);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], s[124 + u]);
-                const float mraw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                // the reference moves only when the block's maximum is far above it
+                        for (int u = 0; u < 16; ++u) {
+                            float2 x = fma2(make_float2(s[c + 2 * u], s[c + 2 * u + 1]), make_float2(sc, sc), make_float2(neg, neg));
+                            x.x = exp2_in_order(x.x);
+                            if constexpr (kMax) {
+                                const int i = 2 * (c + 2 * u);
+                                mx[(i / 2) & 7] = i < 16 ? fmaxf(s[i], s[i + 1]) : max3_in_order(mx[(i / 2) & 7], s[i], s[i + 1]);
+                            }
+                            x.y = exp2_in_order(x.y);
+                            if constexpr (kMax) {
+                                const int i = 2 * (c + 2 * u) + 2;
+                                mx[(i / 2) & 7] = i < 16 ? fmaxf(s[i], s[i + 1]) : max3_in_order(mx[(i / 2) & 7], s[i], s[i + 1]);
+                            }
+                            sum[u & 1] = add2(sum[u & 1], x);
+                            pk[u] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
+                        }
+                        tmem_st16(scol + c / 2, pk);
+                    }
+                    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                };
+                // The first 64 columns against the reference as it stands, while the block's
+                // maximum is found: the reference moves only when that is far above it, which
+                // after a tile's first blocks is rare, and they are then done again.
+                float sum0 = exps(0, m == kNegInf ? 0.f : -m, std::true_type{});
+                const float mraw = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
                 const bool move = mraw > m + kRescaleLog2 || (m == kNegInf && mraw != kNegInf);
-                const bool resc = move && m != kNegInf;
-                if (__any_sync(0xffffffffu, resc)) {
-                    // (the product of the block before is done: it was issued before this
-                    // block's scores)
-                    const float al = resc ? fast_exp2(m - mraw) : 1.f;
+                if (__any_sync(0xffffffffu, move)) {
+                    const bool resc = move && m != kNegInf;
+                    if (__any_sync(0xffffffffu, resc)) {
+                        // (the product of the block before is done: it was issued before this
+                        // block's scores)
+                        const float al = resc ? fast_exp2(m - mraw) : 1.f;
 #pragma unroll 1
-                    for (int c = 0; c < 128; c += 32) {
-                        float o[32];
-                        tmem_ld32(ocol + c, o);
-                        tmem_ld_wait();
+                        for (int c = 0; c < 128; c += 32) {
+                            float o[32];
+                            tmem_ld32(ocol + c, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int u = 0; u < 32; ++u) o[u] *= al;
-                        tmem_st32(ocol + c, o);
+                            for (int u = 0; u < 32; ++u) o[u] *= al;
+                            tmem_st32(ocol + c, o);
+                        }
+                        l *= al;
                     }
-                    l *= al;
+                    if (move) m = mraw;
+                    sum0 = exps(0, m == kNegInf ? 0.f : -m, std::false_type{});
                 }
-                if (move) m = mraw;
-                const float neg = m == kNegInf ? 0.f : -m;
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int u = 0; u < 16; ++u) {
-                        float2 x = fma2(make_float2(s[c + 2 * u], s[c + 2 * u + 1]), make_float2(sc, sc), make_float2(neg, neg));
-                        x.x = fast_exp2(x.x);
-                        x.y = fast_exp2(x.y);
-                        sum[u & 1] = add2(sum[u & 1], x);
-                        pk[u] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
-                    }
-                    tmem_st16(scol + c / 2, pk);
-                }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&pfull[t]);
+                if (lane == 0) arrive_leader<CG>(&pfull[2 * t]);
+                const float sum1 = exps(64, m == kNegInf ? 0.f : -m, std::false_type{});
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader<CG>(&pfull[2 * t + 1]);
+                l += sum0 + sum1;
             }
             if (!ok) break;
             // ---- the tile's rows
@@ -728,40 +947,68 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
                 break;
             }
             tc_fence_after();
-            const bool live = tok < it.n;
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             const float lse = l > 0.f || l != l ? (m == kNegInf ? 0.f : m) * kLn2 + logf(l) : kNegInf;
             const bool direct = p.mode == kModePrefill && it.whole;
-            const long long orow = (long long)(it.q0 + tok) * p.num_q_heads + it.h * kGroup + head;
-            const long long prow = tile_slot(p.mode, blockIdx.x, it) * kTileRows + tok_in * kGroup + head;
+            const int tok0 = it.i * T + half_tok;              // the half's first token in the sequence
+            const int live = min(it.n - tok0, kHalfTokens) * kGroup;  // the half's rows that exist
+            const long long orow0 = (long long)(it.q0 + tok0) * p.num_q_heads + it.h * kGroup;
+            const long long prow0 = tile_slot(p.mode, worker, it) * (T * kGroup) + half_tok * kGroup;
+            // 64 bytes of every row at a time, through shared memory: a warp then writes
+            // eight rows' 64 bytes at once (row r = token r / 8, query head r % 8)
+            const int wr = 32 * (warp & 3) + lane / 4;  // + 8 i
+            if (direct) {
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                float o[32];
-                tmem_ld32(ocol + c, o);
-                tmem_ld_wait();
-                // rows that saw nothing are zero, whatever O holds
+                for (int c = 0; c < 128; c += 32) {
+                    float o[32];
+                    tmem_ld32(ocol + c, o);
+                    tmem_ld_wait();
+                    // rows that saw nothing are zero, whatever O holds
 #pragma unroll
-                for (int u = 0; u < 32; ++u) o[u] = inv == 0.f ? 0.f : o[u] * inv;
-                if (live && direct) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kHeadDim + c);
+                    for (int u = 0; u < 32; ++u) o[u] = inv == 0.f ? 0.f : o[u] * inv;
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        dst[u] = make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
-                                            pack_bf16x2(o[8 * u + 4], o[8 * u + 5]), pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
-                } else if (live) {
-                    float4* dst = reinterpret_cast<float4*>(p.split_o + prow * kHeadDim + c);
+                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ (lane >> 1 & 3)) << 4)) =
+                            make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
+                                       pack_bf16x2(o[8 * u + 4], o[8 * u + 5]), pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
+                    __syncwarp();
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const int lr = lane / 4 + 8 * i, r = wr + 8 * i;
+                        const uint4 v = *reinterpret_cast<const uint4*>(stage + lr * 64 + (((lane & 3) ^ (lr >> 1 & 3)) << 4));
+                        if (r < live)
+                            *reinterpret_cast<uint4*>(p.out + (orow0 + (long long)(r / kGroup) * p.num_q_heads + r % kGroup) * kHeadDim + c +
+                                                      8 * (lane & 3)) = v;
+                    }
+                    __syncwarp();
                 }
-            }
-            if (live && direct) {
-                if (p.out_lse) p.out_lse[orow] = lse;
-            } else if (live) {
-                p.split_lse[prow] = lse;
+                if (row < live && p.out_lse) p.out_lse[orow0 + (long long)(row / kGroup) * p.num_q_heads + row % kGroup] = lse;
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 16) {
+                    float o[16];
+                    tmem_ld16(ocol + c, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) o[u] = inv == 0.f ? 0.f : o[u] * inv;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        *reinterpret_cast<float4*>(stage + lane * 64 + ((u ^ (lane >> 1 & 3)) << 4)) =
+                            make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int lr = lane / 4 + 8 * i, r = wr + 8 * i;
+                        const float4 v = *reinterpret_cast<const float4*>(stage + lr * 64 + (((lane & 3) ^ (lr >> 1 & 3)) << 4));
+                        if (r < live) *reinterpret_cast<float4*>(p.split_o + (prow0 + r) * kHeadDim + c + 4 * (lane & 3)) = v;
+                    }
+                    __syncwarp();
+                }
+                if (row < live) p.split_lse[prow0 + row] = lse;
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ofree[t]);
+            if (lane == 0) arrive_leader<CG>(&ofree[t]);
             ++nd;
         }
         if (!ok && lane == 0) {
@@ -772,16 +1019,20 @@ __global__ void __launch_bounds__(Cfg<FP8>::kThreads, 1)
     // normal end: every MMA was waited for by an epilogue; after a timeout give
     // what is in flight a bounded time
     __syncwarp();
+    if (*abort_flag && warp == 0) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < kDrainLimitNs) {
+        }
+    }
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all<CG>();  // no CTA of a pair ends while the other still works with it
     tc_fence_after();
     if (warp == 0) {
-        if (*abort_flag) {
-            const uint64_t t0 = global_timer_ns();
-            while (global_timer_ns() - t0 < kDrainLimitNs) {
-            }
-        }
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        if constexpr (CG == 1)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
 }
 
@@ -799,21 +1050,51 @@ bool make_tile_q_map(CUtensorMap* map, const void* q, int tokens, int Hq) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8>
-cudaError_t launch(const CUtensorMap (&maps)[5], const TileParams& p, int num_ctas, cudaStream_t s) {
+// 3-D map over an e4m3 cache's V codes with boxes of 64 dims x 64 tokens, rows
+// as they are: one CTA's half of a page.
+bool make_v_half_map(CUtensorMap* map, const void* base, int num_pages, int Hkv) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)Hkv, (cuuint64_t)num_pages * kChunk};
+    cuuint64_t strides[2] = {kHeadDim, (cuuint64_t)Hkv * kHeadDim};
+    cuuint32_t box[3] = {64u, 1u, (cuuint32_t)kChunk};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8, int CG>
+cudaError_t launch(const CUtensorMap (&maps)[5], const TileParams& p, int workers, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&tile_attn_kernel<FP8>),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<FP8>::kAlloc);
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&tile_attn_kernel<FP8, CG>),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<FP8, CG>::kAlloc);
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_acq_rel);
     }
-    return launch_pdl(tile_attn_kernel<FP8>, dim3(num_ctas), dim3(Cfg<FP8>::kThreads), Smem<FP8>::kAlloc, s, maps[0],
-                      maps[1], maps[2], maps[3], maps[4], p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(workers * CG);
+    cfg.blockDim = dim3(Cfg<FP8, CG>::kThreads);
+    cfg.dynamicSmemBytes = Smem<FP8, CG>::kAlloc;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, tile_attn_kernel<FP8, CG>, maps[0], maps[1], maps[2], maps[3], maps[4], p);
+    // a refused launch is reported through the return value, not left pending
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
 }
 
 }  // namespace
@@ -831,8 +1112,10 @@ int tile_default_ctas() {
 cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s) {
     CUtensorMap maps[5];  // K, V, Q, K scales, V scales (the last two e4m3 only)
     memset(maps, 0, sizeof maps);
+    const bool pair = a.tile_tokens == kTilePair;
     if (!make_kv_map(&maps[0], a.k_cache, a.fp8, a.num_pages, a.num_kv_heads) ||
-        !make_kv_map(&maps[1], a.v_cache, a.fp8, a.num_pages, a.num_kv_heads) ||
+        !(a.fp8 && pair ? make_v_half_map(&maps[1], a.v_cache, a.num_pages, a.num_kv_heads)
+                        : make_kv_map(&maps[1], a.v_cache, a.fp8, a.num_pages, a.num_kv_heads)) ||
         !make_tile_q_map(&maps[2], a.q, a.num_tokens, a.num_q_heads))
         return cudaErrorInvalidValue;
     if (a.fp8 && (!make_scale_map(&maps[3], a.k_scale, a.num_pages, a.num_kv_heads) ||
@@ -841,7 +1124,7 @@ cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s) {
     TileParams p;
     memset(&p, 0, sizeof p);
     p.plan = a.plan;
-    p.seqs_off = tile_layout(a.S, a.num_ctas).seqs;
+    p.seqs_off = tile_layout(a.S, a.num_workers).seqs;
     p.page_table = a.page_table;
     p.pt_stride = a.pt_stride;
     p.err = a.plan + kTError;
@@ -855,7 +1138,9 @@ cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s) {
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.out_lse = a.out_lse;
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)kHeadDim);
-    return a.fp8 ? launch<true>(maps, p, a.num_ctas, s) : launch<false>(maps, p, a.num_ctas, s);
+    if (pair)
+        return a.fp8 ? launch<true, 2>(maps, p, a.num_workers, s) : launch<false, 2>(maps, p, a.num_workers, s);
+    return a.fp8 ? launch<true, 1>(maps, p, a.num_workers, s) : launch<false, 1>(maps, p, a.num_workers, s);
 }
 
 }  // namespace hpc

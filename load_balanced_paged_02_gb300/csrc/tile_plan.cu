@@ -1,5 +1,5 @@
 // Planner of tile maps (integer only, one block): sequence table and unit
-// prefix sums by block scans, then every CTA's start by a binary search over
+// prefix sums by block scans, then every worker's start by a binary search over
 // the sequences and one over the tiles of the sequence found, whose unit sums
 // have a closed form (tile_units). The same load balancing as the decode
 // planner's (equal runs of one walk over all KV heads), with tiles of a prompt
@@ -41,7 +41,7 @@ __device__ long long scan_exclusive(long long v, long long* total, long long* wa
 
 __global__ void __launch_bounds__(kThreads)
     tile_plan_kernel(const int32_t* q_starts, const int32_t* lens, int S, int num_tokens,
-                     int Hkv, int C, int min_blocks, int max_len, int mode, int q_len, int32_t* buf) {
+                     int Hkv, int C, int min_blocks, int max_len, int mode, int q_len, int T, int32_t* buf) {
     __shared__ long long sums[kWarps];
     __shared__ int err_sh;
     grid_dependency_wait();  // the lengths may come from the kernel before
@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
         const bool any = n > 0 && (mode == kModePrefill || L > 0);
-        const int tiles = any ? tile_count(n) : 0;
-        const long long u = any ? tile_units(mode, n, L, tiles) : 0;
+        const int tiles = any ? tile_count(n, T) : 0;
+        const long long u = any ? tile_units(mode, n, L, tiles, T) : 0;
         long long u_total, t_total;
         const long long ub = unit_base + scan_exclusive(u, &u_total, sums);
         const long long tb = tile_base + scan_exclusive(tiles, &t_total, sums);
@@ -102,15 +102,16 @@ __global__ void __launch_bounds__(kThreads)
             case kTUnitsPerHead + 1: v = (int)(per_head >> 32); break;
             case kTBucket: v = (int)(bucket & 0xffffffffLL); break;
             case kTBucket + 1: v = (int)(bucket >> 32); break;
-            case kTUsedCtas: v = used; break;
+            case kTUsedWorkers: v = used; break;
             case kTBatch: v = S; break;
             case kTNumKvHeads: v = Hkv; break;
-            case kTNumCtas: v = C; break;
+            case kTNumWorkers: v = C; break;
             case kTNumTokens: v = num_tokens; break;
             case kTMode: v = mode; break;
             case kTTilesPerHead: v = (int)tile_base; break;
             case kTQLen: v = q_len; break;
             case kTError: v = err_sh; break;
+            case kTTileTokens: v = T; break;
         }
         buf[threadIdx.x] = v;
     }
@@ -130,15 +131,15 @@ __global__ void __launch_bounds__(kThreads)
             }
             const int4 q = seqs[lo];
             const long long u = r - units[lo];
-            int i0 = 0, i1 = tile_count(q.y);  // the last tile with tile_units <= u
+            int i0 = 0, i1 = tile_count(q.y, T);  // the last tile with tile_units <= u
             while (i1 - i0 > 1) {
                 const int mid = (i0 + i1) >> 1;
-                if (tile_units(mode, q.y, q.z, mid) <= u)
+                if (tile_units(mode, q.y, q.z, mid, T) <= u)
                     i0 = mid;
                 else
                     i1 = mid;
             }
-            const long long blk = u - tile_units(mode, q.y, q.z, i0) - tile_cost(mode);
+            const long long blk = u - tile_units(mode, q.y, q.z, i0, T) - tile_cost(mode);
             a = make_int4(h, lo, i0, blk > 0 ? (int)blk : 0);
             b.x = h * (int)tile_base + q.w + i0;
         }
@@ -151,9 +152,9 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 cudaError_t launch_tile_plan(const int32_t* q_starts, const int32_t* lens, int S, int num_tokens, int Hkv, int C,
-                             int min_blocks, int max_len, int mode, int q_len, int32_t* buf, cudaStream_t s) {
+                             int min_blocks, int max_len, int mode, int q_len, int T, int32_t* buf, cudaStream_t s) {
     return launch_pdl(tile_plan_kernel, dim3(1), dim3(kThreads), 0, s, q_starts, lens, S, num_tokens, Hkv, C, min_blocks,
-                      max_len, mode, q_len, buf);
+                      max_len, mode, q_len, T, buf);
 }
 
 }  // namespace hpc
