@@ -665,6 +665,40 @@ hpc_status hpc_prefix_combine(const hpc_tile_plan* prefix_plan, const float* pre
                               float* out_lse, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
                               void* stream);
 
+/*
+ * Plan, attention and combine of packed prompts in one call, with the map and the
+ * split rows in a workspace (device, 256-byte aligned; calls that overlap on the
+ * GPU need one each). `plan` gets the map's header (its buf points into the
+ * workspace), for hpc_tile_read_error. Every check is made before the first
+ * launch. Errors: as the three calls, plus HPC_ERR_WORKSPACE_TOO_SMALL.
+ */
+size_t hpc_prefill_workspace_bytes(int batch, int num_ctas);
+hpc_status hpc_prefill(const void* q, const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                       int kv_dtype, int num_pages, const int32_t* page_table, int page_table_stride,
+                       const int32_t* q_starts, const int32_t* seq_lens, int batch, int num_tokens, int num_q_heads,
+                       int num_kv_heads, int head_dim, int page_size, int num_ctas, int min_blocks_per_cta,
+                       int tile_tokens, void* workspace, size_t workspace_bytes, hpc_tile_plan* plan, void* out,
+                       float* out_lse, void* stream);
+
+/*
+ * One decode step of a batch whose groups share prefixes, in one call: both
+ * plans, the prefixes' attention, the requests' own (hpc_decode_attn_multi) and
+ * the combine, with maps and split rows in a workspace (device, 256-byte aligned;
+ * calls that overlap on the GPU need one each). seq_lens and page_table hold the
+ * tokens behind the prefix alone; prefix_plan and plan get the maps' headers, for
+ * hpc_tile_read_error and hpc_decode_read_error. Errors: as the chained calls.
+ */
+size_t hpc_decode_shared_prefix_workspace_bytes(int num_groups, int batch, int q_len, int num_kv_heads,
+                                                int prefix_num_ctas, int num_ctas);
+hpc_status hpc_decode_shared_prefix(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                    const float* v_scale, int kv_dtype, int num_pages, const int32_t* page_table,
+                                    int page_table_stride, const int32_t* seq_lens, const int32_t* prefix_table,
+                                    int prefix_table_stride, const int32_t* prefix_lens, const int32_t* group_starts,
+                                    int num_groups, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int page_size, int num_ctas, int min_chunks_per_cta, int prefix_num_ctas,
+                                    int min_blocks_per_cta, int tile_tokens, void* workspace, size_t workspace_bytes,
+                                    hpc_tile_plan* prefix_plan, hpc_plan* plan, void* out, float* out_lse, void* stream);
+
 /* Synchronises the device, then reads the tile map's error word, as
  * hpc_decode_read_error does a task map's. */
 hpc_status hpc_tile_read_error(const hpc_tile_plan* plan, int* device_error_word);

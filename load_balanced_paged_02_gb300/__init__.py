@@ -17,7 +17,7 @@ _BINDING_NAMES = {
     "sm_count", "hpc_rope_norm", "TilePlan", "hpc_prefill_plan", "hpc_prefill_attn", "hpc_prefill_combine",
     "prefill_split_buffers", "prefill", "hpc_prefix_plan", "hpc_prefix_attn", "hpc_prefix_combine",
     "prefix_split_buffers", "decode_shared_prefix", "hpc_tile_read_error", "tile_num_ctas", "hpc_kv_write",
-    "hpc_kv_read",
+    "hpc_kv_read", "prefill_workspace_bytes", "decode_shared_prefix_workspace_bytes",
 }
 
 

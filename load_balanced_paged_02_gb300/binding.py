@@ -7,6 +7,7 @@ when the library is missing or returns a non-OK status.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -98,6 +99,12 @@ SIGNATURES = {
     "hpc_prefix_plan": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _TP, _vp]),
     "hpc_prefix_attn": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _i, _i, _i, _i, _TP, _vp, _vp, _vp]),
     "hpc_prefix_combine": (_i, [_TP, _vp, _vp, _P, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "hpc_prefill_workspace_bytes": (_sz, [_i, _i]),
+    "hpc_prefill": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _sz,
+                         _TP, _vp, _vp, _vp]),
+    "hpc_decode_shared_prefix_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "hpc_decode_shared_prefix": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
+                                      _i, _i, _i, _i, _i, _i, _i, _vp, _sz, _TP, _P, _vp, _vp, _vp]),
     "hpc_tile_read_error": (_i, [_TP, ctypes.POINTER(_i)]),
     "hpc_kv_write": (_i, [_vp, _vp, _ll, _ll, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp]),
     "hpc_kv_read": (_i, [_vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
@@ -115,6 +122,8 @@ def build(force: bool = False) -> str:
 def lib():
     """The loaded library; raises HpcError if it has not been built."""
     global _LIB
+    if _LIB is not None:
+        return _LIB
     with _lock:
         if _LIB is None:
             if not os.path.exists(_build.LIB_PATH):
@@ -450,16 +459,95 @@ def hpc_rope_norm(qkv, positions, cos_sin, q_weight, k_weight, slot_mapping, q_o
 
 
 # ---------------------------------------------------------------- prompts, shared prefixes, cache write / read
+#
+# A decode step's calls take microseconds on the device, so these bindings keep
+# their own cost down: integers for pointers, one pass of checks, and the
+# one-call forms with a workspace.
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device_index):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _on_device(what, *tensors):
+    """The device index that all tensors (None passed over) share, which must be the current one."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise HpcError(what, detail=f"tensors on {tensors[0].device} and {t.device}")
+    if index < 0:
+        raise HpcError(what, detail="tensors must be on a CUDA device")
+    if index != torch.cuda.current_device():
+        raise HpcError(what, detail=f"tensors on cuda:{index}, but the current device is cuda:{torch.cuda.current_device()}")
+    return index
+
+
+def _i32(what, t, numel=None):
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise HpcError(what, detail="must be a contiguous int32 tensor")
+    if numel is not None and t.numel() != numel:
+        raise HpcError(what, detail=f"must hold {numel} values")
+
+
+def _table(what, t, rows):
+    _i32(what, t)
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise HpcError(what, detail=f"must have {rows} rows")
+
+
+def _tensor(what, t, shape, dtype):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise HpcError(what, detail=f"must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _query(what, q):
+    if q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise HpcError(what, detail="q must be a contiguous bfloat16 tensor")
+
+
+def _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages):
+    """Checks of a paged cache; returns its hpc_kv_dtype, pages in use, page size and KV heads."""
+    kvd = kv_dtype_of(k_cache)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
+        raise HpcError(what, detail="k_cache and v_cache must be [pages, 64, heads, 128] of one type")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise HpcError(what, detail="k_cache and v_cache must be contiguous")
+    pages, page, heads, _ = shape
+    if kvd == KV_FP8_E4M3:
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None:
+                raise HpcError(n, detail="an e4m3 cache needs scales")
+            _tensor(n, t, (pages, heads, page), torch.float32)
+    if num_pages is not None:
+        if num_pages > pages:
+            raise HpcError("num_pages", detail=f"{num_pages}, but the cache has {pages}")
+        pages = num_pages
+    return kvd, pages, page, heads
+
 
 class TilePlan:
-    """A tile map in device memory (``buf``) plus its host header."""
+    """A tile map in device memory (``buf``, int32) plus its host header."""
 
     def __init__(self, num_seqs: int, num_ctas: int, device):
         nbytes = lib().hpc_tile_plan_bytes(num_seqs, num_ctas)
         if nbytes == 0:
             raise HpcError("hpc_tile_plan_bytes", detail="sizes outside the supported limits")
         self.buf = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
-        self.struct = TilePlanStruct(self.buf.data_ptr(), nbytes, 0, 0, 0, 0, 0, 0, 0)
+        self.struct = TilePlanStruct(self.buf.data_ptr(), nbytes, 0, 0, 0, 0, 0, 0, 0, 0)
+
+    @classmethod
+    def of_workspace(cls, struct, workspace):
+        """The map that a one-call form left at the start of its workspace."""
+        plan = cls.__new__(cls)
+        plan.buf = workspace
+        plan.struct = struct
+        return plan
 
     @property
     def num_ctas(self):
@@ -470,82 +558,46 @@ class TilePlan:
     def tile_tokens(self):
         return self.struct.tile_tokens
 
+    def words(self):
+        """The map as an int32 tensor."""
+        return self.buf.view(torch.int32)[:self.struct.bytes // 4]
+
     def ref(self):
         return ctypes.byref(self.struct)
 
 
+_CTAS = {}
+
+
 def tile_num_ctas() -> int:
-    """hpc_tile_default_num_ctas: one CTA per SM."""
-    n = lib().hpc_tile_default_num_ctas()
+    """hpc_tile_default_num_ctas: one CTA per SM of the current device."""
+    dev = torch.cuda.current_device()
+    n = _CTAS.get(("tile", dev), 0)
     if n <= 0:
-        raise HpcError("hpc_tile_default_num_ctas", detail="device query failed")
+        n = _CTAS[("tile", dev)] = lib().hpc_tile_default_num_ctas()
+        if n <= 0:
+            raise HpcError("hpc_tile_default_num_ctas", detail="device query failed")
     return n
 
 
-def _same_device(what, *tensors):
-    """Every tensor (None passed over) on the first one's device, which is the current one."""
-    dev = tensors[0].device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise HpcError(what, detail=f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise HpcError(what, detail=f"tensors on {dev} and {t.device}")
+def _decode_num_ctas(kvd):
+    dev = torch.cuda.current_device()
+    n = _CTAS.get((kvd, dev), 0)
+    if n <= 0:
+        n = _CTAS[(kvd, dev)] = default_num_ctas(kvd)
+    return n
 
 
-def _check_caches(what, k_cache, v_cache, k_scale, v_scale):
-    """Shapes and types of a paged cache; returns its hpc_kv_dtype."""
-    kvd = kv_dtype_of(k_cache)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise HpcError(what, detail="k_cache and v_cache must be [pages, 64, heads, 128] of one type")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        raise HpcError(what, detail="k_cache and v_cache must be contiguous")
-    if kvd == KV_FP8_E4M3:
-        shape = (k_cache.shape[0], k_cache.shape[2], k_cache.shape[1])
-        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t is None or tuple(t.shape) != shape or t.dtype != torch.float32 or not t.is_contiguous():
-                raise HpcError(n, detail=f"an e4m3 cache needs contiguous float32 scales of shape {shape}")
-    return kvd
-
-
-def _check_out(what, t, shape, dtype):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise HpcError(what, detail=f"must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-
-
-def hpc_prefill_plan(q_starts, seq_lens, num_tokens: int, num_kv_heads: int, page_table_stride: int,
-                     num_ctas: int | None = None, min_blocks_per_cta: int = 1, tile_tokens: int = 0,
-                     plan: TilePlan | None = None, stream=None) -> TilePlan:
-    """Tile map of packed prompts from device-side starts and lengths (one launch, no host sync)."""
-    _cuda_i32(q_starts, "q_starts")
-    _cuda_i32(seq_lens, "seq_lens")
-    B = seq_lens.numel()
-    if q_starts.numel() != B + 1:
-        raise HpcError("q_starts", detail=f"must hold {B + 1} starts")
-    _same_device("hpc_prefill_plan", seq_lens, q_starts)
-    num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
-    plan = TilePlan(B, num_ctas, seq_lens.device) if plan is None else plan
-    rc = lib().hpc_prefill_plan(_ptr(q_starts), _ptr(seq_lens), B, num_tokens, num_kv_heads, page_table_stride, num_ctas,
-                                min_blocks_per_cta, tile_tokens, plan.ref(), _stream(stream))
-    _check("hpc_prefill_plan", rc)
-    return plan
+def _on(stream):
+    """Allocations for work on ``stream`` belong to it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
 
 
 def _split_rows(rows, device):
     return (torch.empty((rows, HEAD_DIM), dtype=torch.float32, device=device),
             torch.empty(rows, dtype=torch.float32, device=device))
-
-
-def prefill_split_buffers(plan: TilePlan):
-    """split_o and split_lse of hpc_prefill_attn for this map."""
-    return _split_rows(int(lib().hpc_prefill_split_rows(plan.num_ctas)), plan.buf.device)
-
-
-def _check_q_table(what, q, table, seqs):
-    if q.dtype != torch.bfloat16 or not q.is_contiguous():
-        raise HpcError(what, detail="q must be a contiguous bfloat16 tensor")
-    _cuda_i32(table, "page table")
-    if table.dim() != 2 or table.shape[0] != seqs:
-        raise HpcError(what, detail=f"the page table must have {seqs} rows")
 
 
 def _check_splits(what, rows, split_o, split_lse):
@@ -554,87 +606,126 @@ def _check_splits(what, rows, split_o, split_lse):
             raise HpcError(what, detail=f"split buffers need {rows} rows of contiguous float32")
 
 
+def hpc_prefill_plan(q_starts, seq_lens, num_tokens: int, num_kv_heads: int, page_table_stride: int,
+                     num_ctas: int | None = None, min_blocks_per_cta: int = 1, tile_tokens: int = 0,
+                     plan: TilePlan | None = None, stream=None) -> TilePlan:
+    """Tile map of packed prompts from device-side starts and lengths (one launch, no host sync)."""
+    _i32("seq_lens", seq_lens)
+    B = seq_lens.numel()
+    _i32("q_starts", q_starts, B + 1)
+    dev = _on_device("hpc_prefill_plan", seq_lens, q_starts)
+    num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
+    if plan is None:
+        with _on(stream):
+            plan = TilePlan(B, num_ctas, seq_lens.device)
+    rc = lib().hpc_prefill_plan(q_starts.data_ptr(), seq_lens.data_ptr(), B, num_tokens, num_kv_heads, page_table_stride,
+                                num_ctas, min_blocks_per_cta, tile_tokens, plan.ref(), _raw_stream(stream, dev))
+    _check("hpc_prefill_plan", rc)
+    return plan
+
+
+def prefill_split_buffers(plan: TilePlan):
+    """split_o and split_lse of hpc_prefill_attn for this map."""
+    return _split_rows(int(lib().hpc_prefill_split_rows(plan.num_ctas)), plan.buf.device)
+
+
 def hpc_prefill_attn(q, k_cache, v_cache, page_table, plan: TilePlan, split_o, split_lse, out, out_lse=None, k_scale=None,
                      v_scale=None, num_pages: int | None = None, stream=None):
     """Causal attention of packed prompts over the paged cache; whole tiles go to
     out [T, Hq, 128] (and out_lse [T, Hq]), pieces of cut ones to the split buffers."""
-    kvd = _check_caches("hpc_prefill_attn", k_cache, v_cache, k_scale, v_scale)
+    what = "hpc_prefill_attn"
+    kvd, pages, page, Hkv = _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages)
+    _query(what, q)
     T, Hq, D = q.shape
-    _check_q_table("hpc_prefill_attn", q, page_table, plan.struct.num_seqs)
-    _same_device("hpc_prefill_attn", q, k_cache, v_cache, k_scale, v_scale, page_table, split_o, split_lse, out, out_lse)
+    _table("page_table", page_table, plan.struct.num_seqs)
+    dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, split_o, split_lse, out, out_lse)
     if T != plan.struct.num_tokens:
-        raise HpcError("hpc_prefill_attn", detail=f"q has {T} tokens, the plan {plan.struct.num_tokens}")
-    _check_out("out", out, q.shape, torch.bfloat16)
+        raise HpcError(what, detail=f"q has {T} tokens, the plan {plan.struct.num_tokens}")
+    _tensor("out", out, (T, Hq, D), torch.bfloat16)
     if out_lse is not None:
-        _check_out("out_lse", out_lse, (T, Hq), torch.float32)
-    _check_splits("hpc_prefill_attn", int(lib().hpc_prefill_split_rows(plan.num_ctas)), split_o, split_lse)
+        _tensor("out_lse", out_lse, (T, Hq), torch.float32)
+    _check_splits(what, int(lib().hpc_prefill_split_rows(plan.num_ctas)), split_o, split_lse)
     rc = lib().hpc_prefill_attn(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kvd, _pages(k_cache, num_pages),
-        _ptr(page_table), int(page_table.shape[1]), Hq, int(k_cache.shape[2]), D, int(k_cache.shape[1]), plan.ref(),
-        _ptr(split_o), _ptr(split_lse), _ptr(out), _ptr(out_lse), _stream(stream))
-    _check("hpc_prefill_attn", rc)
-
-
-def _pages(k_cache, num_pages):
-    """The pages in use; never more than the cache has."""
-    if num_pages is None:
-        return int(k_cache.shape[0])
-    if num_pages > k_cache.shape[0]:
-        raise HpcError("num_pages", detail=f"{num_pages}, but the cache has {k_cache.shape[0]}")
-    return int(num_pages)
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), kvd, pages,
+        page_table.data_ptr(), page_table.shape[1], Hq, Hkv, D, page, plan.ref(), split_o.data_ptr(), split_lse.data_ptr(),
+        out.data_ptr(), _addr(out_lse), _raw_stream(stream, dev))
+    _check(what, rc)
 
 
 def hpc_prefill_combine(plan: TilePlan, split_o, split_lse, out, out_lse=None, stream=None):
     """Merges the pieces of cut tiles into out and out_lse."""
-    Hq, D = out.shape[-2:]
-    rc = lib().hpc_prefill_combine(plan.ref(), _ptr(split_o), _ptr(split_lse), _ptr(out), _ptr(out_lse), Hq,
-                                   plan.struct.num_kv_heads, D, _stream(stream))
-    _check("hpc_prefill_combine", rc)
-
-
-def _on(stream):
-    """Allocations for work on ``stream`` belong to it."""
-    import contextlib
-    if stream is None:
-        return contextlib.nullcontext()
-    if isinstance(stream, torch.cuda.Stream):
-        return torch.cuda.stream(stream)
-    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
+    what = "hpc_prefill_combine"
+    T, Hq, D = out.shape
+    dev = _on_device(what, out, split_o, split_lse, out_lse, plan.buf)
+    _tensor("out", out, (plan.struct.num_tokens, Hq, D), torch.bfloat16)
+    if out_lse is not None:
+        _tensor("out_lse", out_lse, (T, Hq), torch.float32)
+    _check_splits(what, int(lib().hpc_prefill_split_rows(plan.num_ctas)), split_o, split_lse)
+    rc = lib().hpc_prefill_combine(plan.ref(), split_o.data_ptr(), split_lse.data_ptr(), out.data_ptr(), _addr(out_lse), Hq,
+                                   plan.struct.num_kv_heads, D, _raw_stream(stream, dev))
+    _check(what, rc)
 
 
 def prefill(q, k_cache, v_cache, page_table, q_starts, seq_lens, k_scale=None, v_scale=None, num_ctas: int | None = None,
             min_blocks_per_cta: int = 1, tile_tokens: int = 0, num_pages: int | None = None, out=None, out_lse=None,
-            stream=None):
-    """plan -> attention -> combine of packed prompts, q bf16 [T, Hq, 128], with buffers
-    allocated here (and out, out_lse where they are not given). Returns (out, lse, plan)."""
+            workspace=None, stream=None):
+    """Causal attention of packed prompts, q bf16 [T, Hq, 128], over the paged cache: plan,
+    attention and combine in one call (hpc_prefill). Buffers that are not given are allocated
+    here; a given ``workspace`` is a uint8 tensor of prefill_workspace_bytes. Returns (out,
+    lse, plan)."""
+    what = "hpc_prefill"
+    kvd, pages, page, Hkv = _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages)
+    _query(what, q)
+    T, Hq, D = q.shape
+    _i32("seq_lens", seq_lens)
+    B = seq_lens.numel()
+    _i32("q_starts", q_starts, B + 1)
+    _table("page_table", page_table, B)
+    dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, q_starts, seq_lens, out, out_lse, workspace)
+    num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
+    L = lib()
+    need = L.hpc_prefill_workspace_bytes(B, num_ctas)
     with _on(stream):
-        plan = hpc_prefill_plan(q_starts, seq_lens, q.shape[0], k_cache.shape[2], page_table.shape[1], num_ctas,
-                                min_blocks_per_cta, tile_tokens, stream=stream)
-        so, sl = prefill_split_buffers(plan)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         if out is None:
             out = torch.empty_like(q)
+        else:
+            _tensor("out", out, q.shape, torch.bfloat16)
         if out_lse is None:
-            out_lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        hpc_prefill_attn(q, k_cache, v_cache, page_table, plan, so, sl, out, out_lse, k_scale, v_scale, num_pages,
-                         stream=stream)
-        hpc_prefill_combine(plan, so, sl, out, out_lse, stream=stream)
+            out_lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        else:
+            _tensor("out_lse", out_lse, (T, Hq), torch.float32)
+    plan = TilePlan.of_workspace(TilePlanStruct(), workspace)
+    rc = L.hpc_prefill(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), kvd, pages,
+        page_table.data_ptr(), page_table.shape[1], q_starts.data_ptr(), seq_lens.data_ptr(), B, T, Hq, Hkv, D, page,
+        num_ctas, min_blocks_per_cta, tile_tokens, workspace.data_ptr(), workspace.nbytes, plan.ref(), out.data_ptr(),
+        out_lse.data_ptr(), _raw_stream(stream, dev))
+    _check(what, rc)
     return out, out_lse, plan
+
+
+def prefill_workspace_bytes(batch: int, num_ctas: int | None = None) -> int:
+    """Bytes of the workspace that prefill takes for this many sequences."""
+    return int(lib().hpc_prefill_workspace_bytes(batch, tile_num_ctas() if num_ctas is None else num_ctas))
 
 
 def hpc_prefix_plan(group_starts, prefix_lens, batch: int, num_kv_heads: int, prefix_table_stride: int, q_len: int = 1,
                     num_ctas: int | None = None, min_blocks_per_cta: int = 1, tile_tokens: int = 0,
                     plan: TilePlan | None = None, stream=None) -> TilePlan:
     """Tile map of the prefixes that groups of a decode batch share."""
-    _cuda_i32(group_starts, "group_starts")
-    _cuda_i32(prefix_lens, "prefix_lens")
+    _i32("prefix_lens", prefix_lens)
     G = prefix_lens.numel()
-    if group_starts.numel() != G + 1:
-        raise HpcError("group_starts", detail=f"must hold {G + 1} starts")
-    _same_device("hpc_prefix_plan", prefix_lens, group_starts)
+    _i32("group_starts", group_starts, G + 1)
+    dev = _on_device("hpc_prefix_plan", prefix_lens, group_starts)
     num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
-    plan = TilePlan(G, num_ctas, prefix_lens.device) if plan is None else plan
-    rc = lib().hpc_prefix_plan(_ptr(group_starts), _ptr(prefix_lens), G, batch, q_len, num_kv_heads, prefix_table_stride,
-                               num_ctas, min_blocks_per_cta, tile_tokens, plan.ref(), _stream(stream))
+    if plan is None:
+        with _on(stream):
+            plan = TilePlan(G, num_ctas, prefix_lens.device)
+    rc = lib().hpc_prefix_plan(group_starts.data_ptr(), prefix_lens.data_ptr(), G, batch, q_len, num_kv_heads,
+                               prefix_table_stride, num_ctas, min_blocks_per_cta, tile_tokens, plan.ref(),
+                               _raw_stream(stream, dev))
     _check("hpc_prefix_plan", rc)
     return plan
 
@@ -653,55 +744,102 @@ def hpc_prefix_attn(q, k_cache, v_cache, prefix_table, plan: TilePlan, split_o, 
                     num_pages: int | None = None, stream=None):
     """Attention of every query row of a decode batch (q bf16 [B, Hq, 128] or
     [B, q_len, Hq, 128]) over its group's prefix; partial rows for hpc_prefix_combine."""
-    kvd = _check_caches("hpc_prefix_attn", k_cache, v_cache, k_scale, v_scale)
+    what = "hpc_prefix_attn"
+    kvd, pages, page, Hkv = _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages)
+    _query(what, q)
     Hq, D = q.shape[-2:]
-    _check_q_table("hpc_prefix_attn", q, prefix_table, plan.struct.num_seqs)
-    _same_device("hpc_prefix_attn", q, k_cache, v_cache, k_scale, v_scale, prefix_table, split_o, split_lse)
+    _table("prefix_table", prefix_table, plan.struct.num_seqs)
+    dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, prefix_table, split_o, split_lse)
     if q.numel() != plan.struct.num_tokens * Hq * D or (q.shape[1] if q.dim() == 4 else 1) != plan.struct.q_len:
-        raise HpcError("hpc_prefix_attn", detail="q and the plan differ in requests or new tokens")
-    _check_splits("hpc_prefix_attn", _prefix_rows(plan), split_o, split_lse)
+        raise HpcError(what, detail="q and the plan differ in requests or new tokens")
+    _check_splits(what, _prefix_rows(plan), split_o, split_lse)
     rc = lib().hpc_prefix_attn(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kvd, _pages(k_cache, num_pages),
-        _ptr(prefix_table), int(prefix_table.shape[1]), Hq, int(k_cache.shape[2]), D, int(k_cache.shape[1]), plan.ref(),
-        _ptr(split_o), _ptr(split_lse), _stream(stream))
-    _check("hpc_prefix_attn", rc)
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), kvd, pages,
+        prefix_table.data_ptr(), prefix_table.shape[1], Hq, Hkv, D, page, plan.ref(), split_o.data_ptr(),
+        split_lse.data_ptr(), _raw_stream(stream, dev))
+    _check(what, rc)
 
 
 def hpc_prefix_combine(prefix_plan: TilePlan, prefix_o, prefix_lse, plan: Plan, split_o, split_lse, out, out_lse=None,
                        stream=None):
     """Merges the prefix pieces and the splits of the requests' own tokens into out
     ([B, Hq, 128] or [B, q_len, Hq, 128] bf16) and out_lse."""
+    what = "hpc_prefix_combine"
     B, Hq, D = out.shape[0], out.shape[-2], out.shape[-1]
     q_len = out.shape[1] if out.dim() == 4 else 1
-    rc = lib().hpc_prefix_combine(prefix_plan.ref(), _ptr(prefix_o), _ptr(prefix_lse), plan.ref(), _ptr(split_o),
-                                  _ptr(split_lse), _ptr(out), _ptr(out_lse), B, q_len, Hq, Hq // GROUP, D, _stream(stream))
-    _check("hpc_prefix_combine", rc)
+    dev = _on_device(what, out, prefix_o, prefix_lse, split_o, split_lse, out_lse)
+    _tensor("out", out, out.shape, torch.bfloat16)
+    if out_lse is not None:
+        _tensor("out_lse", out_lse, out.shape[:-1], torch.float32)
+    _check_splits(what, _prefix_rows(prefix_plan), prefix_o, prefix_lse)
+    _check_splits(what, plan.split_capacity * q_len * GROUP, split_o, split_lse)
+    rc = lib().hpc_prefix_combine(prefix_plan.ref(), prefix_o.data_ptr(), prefix_lse.data_ptr(), plan.ref(),
+                                  split_o.data_ptr(), split_lse.data_ptr(), out.data_ptr(), _addr(out_lse), B, q_len, Hq,
+                                  Hq // GROUP, D, _raw_stream(stream, dev))
+    _check(what, rc)
+
+
+class _WorkspacePlan:
+    """The task map that decode_shared_prefix left in its workspace: what hpc_decode_read_error takes."""
+
+    def __init__(self, struct, workspace):
+        self.struct = struct
+        self.workspace = workspace
+
+    def ref(self):
+        return ctypes.byref(self.struct)
 
 
 def decode_shared_prefix(q, k_cache, v_cache, page_table, seq_lens, prefix_table, prefix_lens, group_starts, k_scale=None,
                          v_scale=None, num_ctas: int | None = None, min_chunks_per_cta: int = 2,
                          prefix_num_ctas: int | None = None, min_blocks_per_cta: int = 1, tile_tokens: int = 0,
-                         num_pages: int | None = None, stream=None):
+                         num_pages: int | None = None, workspace=None, stream=None):
     """One decode step of a batch whose groups share prefixes: requests
     [group_starts[g], group_starts[g + 1]) see the prefix_lens[g] tokens that
     prefix_table[g] names, then their own seq_lens[b] tokens (page_table). Each
-    prefix is computed once for its group. Returns (out, lse, prefix_plan, plan)."""
+    prefix is computed once for its group. q bf16 [B, Hq, 128] or [B, q_len, Hq, 128]; a
+    given ``workspace`` is a uint8 tensor of decode_shared_prefix_workspace_bytes. Returns
+    (out, lse, prefix_plan, plan)."""
+    what = "hpc_decode_shared_prefix"
+    kvd, pages, page, Hkv = _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages)
+    _query(what, q)
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
     q_len = q.shape[1] if q.dim() == 4 else 1
-    B, Hkv = q.shape[0], k_cache.shape[2]
+    _i32("seq_lens", seq_lens, B)
+    _table("page_table", page_table, B)
+    _i32("prefix_lens", prefix_lens)
+    G = prefix_lens.numel()
+    _i32("group_starts", group_starts, G + 1)
+    _table("prefix_table", prefix_table, G)
+    dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, prefix_table, prefix_lens,
+                     group_starts, workspace)
+    num_ctas = _decode_num_ctas(kvd) if num_ctas is None else num_ctas
+    prefix_num_ctas = tile_num_ctas() if prefix_num_ctas is None else prefix_num_ctas
+    L = lib()
     with _on(stream):
-        pplan = hpc_prefix_plan(group_starts, prefix_lens, B, Hkv, prefix_table.shape[1], q_len, prefix_num_ctas,
-                                min_blocks_per_cta, tile_tokens, stream=stream)
-        po, pl = prefix_split_buffers(pplan)
-        plan = hpc_decode_plan(seq_lens, Hkv, num_ctas or default_num_ctas(kv_dtype_of(k_cache)), min_chunks_per_cta,
-                               stream=stream)
-        so, sl = split_buffers(plan, q_len=q_len)
-        hpc_prefix_attn(q, k_cache, v_cache, prefix_table, pplan, po, pl, k_scale, v_scale, num_pages, stream=stream)
-        hpc_decode_attn(q, k_cache, v_cache, page_table, seq_lens, plan, so, sl, k_scale, v_scale,
-                        _pages(k_cache, num_pages), stream=stream)
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if workspace is None:
+            need = L.hpc_decode_shared_prefix_workspace_bytes(G, B, q_len, Hkv, prefix_num_ctas, num_ctas)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        out = torch.empty_like(q)
         lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-        hpc_prefix_combine(pplan, po, pl, plan, so, sl, out, lse, stream=stream)
+    pplan, plan = TilePlan.of_workspace(TilePlanStruct(), workspace), _WorkspacePlan(PlanStruct(), workspace)
+    rc = L.hpc_decode_shared_prefix(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), kvd, pages,
+        page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), prefix_table.data_ptr(), prefix_table.shape[1],
+        prefix_lens.data_ptr(), group_starts.data_ptr(), G, B, q_len, Hq, Hkv, D, page, num_ctas, min_chunks_per_cta,
+        prefix_num_ctas, min_blocks_per_cta, tile_tokens, workspace.data_ptr(), workspace.nbytes, pplan.ref(), plan.ref(),
+        out.data_ptr(), lse.data_ptr(), _raw_stream(stream, dev))
+    _check(what, rc)
     return out, lse, pplan, plan
+
+
+def decode_shared_prefix_workspace_bytes(num_groups: int, batch: int, num_kv_heads: int, q_len: int = 1,
+                                         kv_dtype: int = KV_BF16, prefix_num_ctas: int | None = None,
+                                         num_ctas: int | None = None) -> int:
+    """Bytes of the workspace that decode_shared_prefix takes."""
+    return int(lib().hpc_decode_shared_prefix_workspace_bytes(
+        num_groups, batch, q_len, num_kv_heads, tile_num_ctas() if prefix_num_ctas is None else prefix_num_ctas,
+        _decode_num_ctas(kv_dtype) if num_ctas is None else num_ctas))
 
 
 def hpc_tile_read_error(plan: TilePlan) -> int:
@@ -717,41 +855,48 @@ def hpc_kv_write(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=Non
                  error_word=None, stream=None):
     """K and V (bf16 [T, Hkv, 128]; any token stride, such as slices of a fused
     projection's output) into the cache slots, bf16 or quantised to e4m3."""
-    kvd = _check_caches("hpc_kv_write", k_cache, v_cache, k_scale, v_scale)
-    T, Hkv, D = k.shape
-    _cuda_i32(slot_mapping, "slot_mapping")
-    _same_device("hpc_kv_write", k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, error_word)
-    if v.shape != k.shape or slot_mapping.numel() != T or Hkv != k_cache.shape[2]:
-        raise HpcError("hpc_kv_write", detail="k, v, slot_mapping and the cache differ in tokens or heads")
+    what = "hpc_kv_write"
+    kvd, pages, page, Hkv = _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages)
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or shape[1] != Hkv or shape[2] != HEAD_DIM:
+        raise HpcError(what, detail=f"k and v must be [tokens, {Hkv}, {HEAD_DIM}]")
+    T = shape[0]
+    _i32("slot_mapping", slot_mapping, T)
+    dev = _on_device(what, k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, error_word)
+    strides = []
     for t, n in ((k, "k"), (v, "v")):
-        if t.dtype != torch.bfloat16 or (T > 0 and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D))):
+        st = t.stride()
+        if t.dtype != torch.bfloat16 or (T > 0 and (st[2] != 1 or (Hkv > 1 and st[1] != HEAD_DIM))):
             raise HpcError(n, detail="must be bfloat16 with each token's heads contiguous")
-    row = Hkv * D
-    ks, vs = (t.stride(0) if T > 1 else row for t in (k, v))
-    rc = lib().hpc_kv_write(_ptr(k), _ptr(v), ks, vs, _ptr(slot_mapping), T, Hkv, D, int(k_cache.shape[1]), _ptr(k_cache),
-                            _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kvd, _pages(k_cache, num_pages), _ptr(error_word),
-                            _stream(stream))
-    _check("hpc_kv_write", rc)
+        strides.append(st[0] if T > 1 else Hkv * HEAD_DIM)
+    if error_word is not None:
+        _i32("error_word", error_word)
+    rc = lib().hpc_kv_write(k.data_ptr(), v.data_ptr(), strides[0], strides[1], slot_mapping.data_ptr(), T, Hkv, HEAD_DIM,
+                            page, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), kvd, pages,
+                            _addr(error_word), _raw_stream(stream, dev))
+    _check(what, rc)
 
 
 def hpc_kv_read(k_cache, v_cache, page_table, out_starts, k_out, v_out, k_scale=None, v_scale=None, first=None,
                 num_pages: int | None = None, error_word=None, stream=None):
     """Tokens first[b], first[b] + 1, ... of each request into rows
     [out_starts[b], out_starts[b + 1]) of k_out and v_out (bf16 [rows, Hkv, 128])."""
-    kvd = _check_caches("hpc_kv_read", k_cache, v_cache, k_scale, v_scale)
-    _cuda_i32(page_table, "page_table")
-    _cuda_i32(out_starts, "out_starts")
-    B = page_table.shape[0]
-    if page_table.dim() != 2 or out_starts.numel() != B + 1:
-        raise HpcError("hpc_kv_read", detail="page_table must be [batch, pages] and out_starts hold batch + 1 rows")
-    if first is not None and _cuda_i32(first, "first").numel() != B:
-        raise HpcError("first", detail=f"must hold {B} positions")
-    _same_device("hpc_kv_read", k_cache, v_cache, k_scale, v_scale, page_table, out_starts, first, k_out, v_out, error_word)
+    what = "hpc_kv_read"
+    kvd, pages, page, Hkv = _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages)
+    _i32("page_table", page_table)
+    if page_table.dim() != 2:
+        raise HpcError("page_table", detail="must be [batch, pages]")
+    B, width = page_table.shape
+    _i32("out_starts", out_starts, B + 1)
+    if first is not None:
+        _i32("first", first, B)
     rows = k_out.shape[0]
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        _check_out(n, t, (rows, k_cache.shape[2], HEAD_DIM), torch.bfloat16)
-    rc = lib().hpc_kv_read(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kvd, _pages(k_cache, num_pages),
-                           _ptr(page_table), int(page_table.shape[1]), _ptr(first), _ptr(out_starts), B, rows,
-                           int(k_cache.shape[2]), HEAD_DIM, int(k_cache.shape[1]), _ptr(k_out), _ptr(v_out),
-                           _ptr(error_word), _stream(stream))
-    _check("hpc_kv_read", rc)
+    _tensor("k_out", k_out, (rows, Hkv, HEAD_DIM), torch.bfloat16)
+    _tensor("v_out", v_out, (rows, Hkv, HEAD_DIM), torch.bfloat16)
+    if error_word is not None:
+        _i32("error_word", error_word)
+    dev = _on_device(what, k_cache, v_cache, k_scale, v_scale, page_table, out_starts, first, k_out, v_out, error_word)
+    rc = lib().hpc_kv_read(k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), kvd, pages,
+                           page_table.data_ptr(), width, _addr(first), out_starts.data_ptr(), B, rows, Hkv, HEAD_DIM, page,
+                           k_out.data_ptr(), v_out.data_ptr(), _addr(error_word), _raw_stream(stream, dev))
+    _check(what, rc)

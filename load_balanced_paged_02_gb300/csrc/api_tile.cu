@@ -123,6 +123,35 @@ hpc_status attn_common(const void* q, const void* k_cache, const void* v_cache, 
     return launched(launch_tile_attn(a, static_cast<cudaStream_t>(stream)));
 }
 
+inline size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspaces of the one-call forms: the maps first, then the split rows.
+struct PrefillSpace {
+    size_t plan, split_o, split_lse, total;
+    PrefillSpace(int batch, int num_ctas) {
+        const size_t rows = hpc_prefill_split_rows(num_ctas);
+        plan = 0;
+        split_o = align_up(hpc_tile_plan_bytes(batch, num_ctas));
+        split_lse = split_o + align_up(rows * kHeadDim * sizeof(float));
+        total = split_lse + align_up(rows * sizeof(float));
+    }
+};
+
+struct PrefixSpace {
+    size_t prefix_plan, plan, prefix_o, prefix_lse, split_o, split_lse, total;
+    PrefixSpace(int groups, int batch, int q_len, int num_kv_heads, int prefix_ctas, int ctas) {
+        const size_t pr = hpc_prefix_split_rows(groups, batch, q_len, num_kv_heads, prefix_ctas);
+        const size_t sr = hpc_decode_split_capacity(batch, num_kv_heads, ctas) * q_len * kGroup;
+        prefix_plan = 0;
+        plan = align_up(hpc_tile_plan_bytes(groups, prefix_ctas));
+        prefix_o = plan + align_up(hpc_decode_plan_bytes(batch, num_kv_heads, ctas));
+        prefix_lse = prefix_o + align_up(pr * kHeadDim * sizeof(float));
+        split_o = prefix_lse + align_up(pr * sizeof(float));
+        split_lse = split_o + align_up(sr * kHeadDim * sizeof(float));
+        total = split_lse + align_up(sr * sizeof(float));
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -212,6 +241,92 @@ hpc_status hpc_prefix_combine(const hpc_tile_plan* prefix_plan, const float* pre
                                           prefix_lse, plan->buf, plan->num_ctas, split_o, split_lse,
                                           static_cast<__nv_bfloat16*>(out), out_lse, batch, num_q_heads, num_kv_heads,
                                           q_len, static_cast<cudaStream_t>(stream)));
+}
+
+size_t hpc_prefill_workspace_bytes(int batch, int num_ctas) {
+    if (!seqs_ok(batch, num_ctas)) return 0;
+    return PrefillSpace(batch, num_ctas).total;
+}
+
+hpc_status hpc_prefill(const void* q, const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                       int kv_dtype, int num_pages, const int32_t* page_table, int page_table_stride,
+                       const int32_t* q_starts, const int32_t* seq_lens, int batch, int num_tokens, int num_q_heads,
+                       int num_kv_heads, int head_dim, int page_size, int num_ctas, int min_blocks_per_cta,
+                       int tile_tokens, void* workspace, size_t workspace_bytes, hpc_tile_plan* plan, void* out,
+                       float* out_lse, void* stream) {
+    if (!plan || !workspace || !aligned(workspace, 256) || !seqs_ok(batch, num_ctas)) return HPC_ERR_INVALID_ARG;
+    const PrefillSpace w(batch, num_ctas);
+    if (workspace_bytes < w.total) return HPC_ERR_WORKSPACE_TOO_SMALL;
+    // every check of the attention call comes before the first launch
+    hpc_status st = shape_check(num_q_heads, num_kv_heads, head_dim, page_size);
+    if (st != HPC_OK) return st;
+    if ((st = cache_check(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, num_kv_heads)) != HPC_OK) return st;
+    if (!q || !aligned(q, 16) || !page_table || !out || !aligned(out, 16)) return HPC_ERR_INVALID_ARG;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    plan->buf = reinterpret_cast<int32_t*>(ws + w.plan);
+    plan->bytes = hpc_tile_plan_bytes(batch, num_ctas);
+    if ((st = hpc_prefill_plan(q_starts, seq_lens, batch, num_tokens, num_kv_heads, page_table_stride, num_ctas,
+                               min_blocks_per_cta, tile_tokens, plan, stream)) != HPC_OK)
+        return st;
+    float* so = reinterpret_cast<float*>(ws + w.split_o);
+    float* sl = reinterpret_cast<float*>(ws + w.split_lse);
+    if ((st = hpc_prefill_attn(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, page_table, page_table_stride,
+                               num_q_heads, num_kv_heads, head_dim, page_size, plan, so, sl, out, out_lse, stream)) != HPC_OK)
+        return st;
+    return hpc_prefill_combine(plan, so, sl, out, out_lse, num_q_heads, num_kv_heads, head_dim, stream);
+}
+
+size_t hpc_decode_shared_prefix_workspace_bytes(int num_groups, int batch, int q_len, int num_kv_heads,
+                                                int prefix_num_ctas, int num_ctas) {
+    if (!seqs_ok(num_groups, prefix_num_ctas) || !heads_ok(num_kv_heads) || batch < 1 || batch > HPC_MAX_BATCH ||
+        q_len < 1 || q_len > HPC_MAX_Q_LEN || num_ctas < 1 || num_ctas > HPC_MAX_CTAS)
+        return 0;
+    return PrefixSpace(num_groups, batch, q_len, num_kv_heads, prefix_num_ctas, num_ctas).total;
+}
+
+hpc_status hpc_decode_shared_prefix(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                    const float* v_scale, int kv_dtype, int num_pages, const int32_t* page_table,
+                                    int page_table_stride, const int32_t* seq_lens, const int32_t* prefix_table,
+                                    int prefix_table_stride, const int32_t* prefix_lens, const int32_t* group_starts,
+                                    int num_groups, int batch, int q_len, int num_q_heads, int num_kv_heads, int head_dim,
+                                    int page_size, int num_ctas, int min_chunks_per_cta, int prefix_num_ctas,
+                                    int min_blocks_per_cta, int tile_tokens, void* workspace, size_t workspace_bytes,
+                                    hpc_tile_plan* prefix_plan, hpc_plan* plan, void* out, float* out_lse, void* stream) {
+    if (!prefix_plan || !plan || !workspace || !aligned(workspace, 256)) return HPC_ERR_INVALID_ARG;
+    const size_t need = hpc_decode_shared_prefix_workspace_bytes(num_groups, batch, q_len, num_kv_heads, prefix_num_ctas, num_ctas);
+    if (need == 0) return HPC_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return HPC_ERR_WORKSPACE_TOO_SMALL;
+    // every check of the chained calls comes before the first launch
+    hpc_status st = cache_check(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, num_kv_heads);
+    if (st != HPC_OK) return st;
+    if ((st = step_args_check(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, page_table, page_table_stride,
+                              seq_lens, batch, num_q_heads, num_kv_heads, head_dim, page_size, num_ctas, min_chunks_per_cta,
+                              out)) != HPC_OK)
+        return st;
+    if (!prefix_table) return HPC_ERR_INVALID_ARG;
+    const PrefixSpace w(num_groups, batch, q_len, num_kv_heads, prefix_num_ctas, num_ctas);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    prefix_plan->buf = reinterpret_cast<int32_t*>(ws + w.prefix_plan);
+    prefix_plan->bytes = hpc_tile_plan_bytes(num_groups, prefix_num_ctas);
+    plan->buf = reinterpret_cast<int32_t*>(ws + w.plan);
+    plan->bytes = hpc_decode_plan_bytes(batch, num_kv_heads, num_ctas);
+    float* po = reinterpret_cast<float*>(ws + w.prefix_o);
+    float* pl = reinterpret_cast<float*>(ws + w.prefix_lse);
+    float* so = reinterpret_cast<float*>(ws + w.split_o);
+    float* sl = reinterpret_cast<float*>(ws + w.split_lse);
+    if ((st = hpc_prefix_plan(group_starts, prefix_lens, num_groups, batch, q_len, num_kv_heads, prefix_table_stride,
+                              prefix_num_ctas, min_blocks_per_cta, tile_tokens, prefix_plan, stream)) != HPC_OK)
+        return st;
+    if ((st = hpc_decode_plan(seq_lens, batch, num_kv_heads, num_ctas, min_chunks_per_cta, plan, stream)) != HPC_OK) return st;
+    if ((st = hpc_prefix_attn(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, prefix_table, prefix_table_stride,
+                              num_q_heads, num_kv_heads, head_dim, page_size, prefix_plan, po, pl, stream)) != HPC_OK)
+        return st;
+    if ((st = hpc_decode_attn_multi(q, q_len, k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, page_table,
+                                    page_table_stride, seq_lens, batch, num_q_heads, num_kv_heads, head_dim, page_size, plan,
+                                    so, sl, stream)) != HPC_OK)
+        return st;
+    return hpc_prefix_combine(prefix_plan, po, pl, plan, so, sl, out, out_lse, batch, q_len, num_q_heads, num_kv_heads,
+                              head_dim, stream);
 }
 
 hpc_status hpc_kv_write(const void* k, const void* v, long long k_token_stride, long long v_token_stride,

@@ -314,18 +314,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// The same, kept in program order by the compiler.
-__device__ __forceinline__ float max3_in_order(float a, float b, float c) {
-    float d;
-    asm volatile("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ float exp2_in_order(float x) {
-    float y;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 template <int N>
 __device__ __forceinline__ void reg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -886,15 +874,15 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
 #pragma unroll
                         for (int u = 0; u < 16; ++u) {
                             float2 x = fma2(make_float2(s[c + 2 * u], s[c + 2 * u + 1]), make_float2(sc, sc), make_float2(neg, neg));
-                            x.x = exp2_in_order(x.x);
+                            x.x = fast_exp2(x.x);
                             if constexpr (kMax) {
                                 const int i = 2 * (c + 2 * u);
-                                mx[(i / 2) & 7] = i < 16 ? fmaxf(s[i], s[i + 1]) : max3_in_order(mx[(i / 2) & 7], s[i], s[i + 1]);
+                                mx[(i / 2) & 7] = i < 16 ? fmaxf(s[i], s[i + 1]) : max3(mx[(i / 2) & 7], s[i], s[i + 1]);
                             }
-                            x.y = exp2_in_order(x.y);
+                            x.y = fast_exp2(x.y);
                             if constexpr (kMax) {
                                 const int i = 2 * (c + 2 * u) + 2;
-                                mx[(i / 2) & 7] = i < 16 ? fmaxf(s[i], s[i + 1]) : max3_in_order(mx[(i / 2) & 7], s[i], s[i + 1]);
+                                mx[(i / 2) & 7] = i < 16 ? fmaxf(s[i], s[i + 1]) : max3(mx[(i / 2) & 7], s[i], s[i + 1]);
                             }
                             sum[u & 1] = add2(sum[u & 1], x);
                             pk[u] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
