@@ -6,17 +6,20 @@
 // prologue. hpc_kv_read: tokens of each request, packed, as bf16; e4m3 values
 // are code x scale in float32, rounded once.
 //
-// Both are streams: a half-warp per (token, head) row, K or V, 16 bytes of bf16
-// per lane (a 256-byte row in one access of the half-warp), kRows rows per
-// half-warp loaded before any is used. Bound by HBM for long calls, by launch
-// latency for a decode step's.
+// Both are streams, bound by HBM for long calls and by launch latency for a decode
+// step's. A block takes a run of tokens (64 at most, fewer while that leaves SMs
+// without blocks) with all their heads of K and V; groups of lanes take one row of
+// 128 elements each, 16 bytes per lane and load, and kUnroll rows are loaded before
+// the first is used.
 #include "kv.cuh"
 
 namespace hpc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHalfWarps = kThreads / 16;
+constexpr int kUnroll = 4;
+constexpr int kMaxTokens = 64;     // tokens of a block at most
+constexpr int kSmemStarts = 1025;  // out_starts kept in shared memory up to this many
 constexpr float kE4m3Max = 448.f;
 
 __device__ __forceinline__ void unpack8(const uint4& r, float (&y)[8]) {
@@ -36,182 +39,198 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float (&y)[8]) {
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// Row index -> (token, K or V, head): heads fastest, so that a token's slot is
-// read by neighbouring half-warps and its K rows are contiguous.
-template <bool FP8, int ROWS>
-__global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteArgs a) {
+// A half-warp per row (lane k: elements [8 k, 8 k + 8)); row r of the block is token
+// r / (2 Hkv), K heads before V heads.
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteArgs a, int tokens_per_block) {
     grid_dependency_wait();  // the projection may still be finishing
     grid_launch_dependents();
     const int hl = threadIdx.x & 15;
     const unsigned mask = (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
-    const long long rows = (long long)a.num_tokens * 2 * a.num_kv_heads;
-    const long long first = ((long long)blockIdx.x * kHalfWarps + (threadIdx.x >> 4)) * ROWS;
-    uint4 raw[ROWS];
-    int slot[ROWS], kvh[ROWS];
+    const int t0 = blockIdx.x * tokens_per_block, nt = min(tokens_per_block, a.num_tokens - t0);
+    const unsigned per_token = 2u * (unsigned)a.num_kv_heads, rows = (unsigned)nt * per_token;
+    for (unsigned r0 = threadIdx.x >> 4; r0 < rows; r0 += kThreads / 16 * kUnroll) {
+        uint4 raw[kUnroll];
+        int slot[kUnroll], kvh[kUnroll];
 #pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-        const long long r = first + u;
-        slot[u] = -1;
-        kvh[u] = 0;
-        raw[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-            const int t = (int)(r / (2 * a.num_kv_heads));
-            kvh[u] = (int)(r % (2 * a.num_kv_heads));
-            slot[u] = a.slots[t];
+        for (int u = 0; u < kUnroll; ++u) {
+            const unsigned r = r0 + u * (kThreads / 16);
+            slot[u] = -1;
+            kvh[u] = 0;
+            raw[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows) {
+                const unsigned tl = r / per_token;
+                const int t = t0 + (int)tl;
+                kvh[u] = (int)(r - tl * per_token);
+                slot[u] = a.slots[t];
+                const bool is_v = kvh[u] >= a.num_kv_heads;
+                const __nv_bfloat16* src = is_v ? a.v + t * a.v_stride + (kvh[u] - a.num_kv_heads) * kHeadDim
+                                                : a.k + t * a.k_stride + kvh[u] * kHeadDim;
+                raw[u] = reinterpret_cast<const uint4*>(src)[hl];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (slot[u] < 0) continue;  // padding (or no row): uniform over the half-warp
+            const int page = slot[u] / kChunk, off = slot[u] % kChunk;
+            if (page >= a.num_pages) {
+                if (hl == 0 && a.err) atomicOr(a.err, (int)HPC_DEVERR_PAGE_OUT_OF_RANGE);
+                continue;
+            }
             const bool is_v = kvh[u] >= a.num_kv_heads;
-            const __nv_bfloat16* src = is_v ? a.v + (long long)t * a.v_stride + (long long)(kvh[u] - a.num_kv_heads) * kHeadDim
-                                            : a.k + (long long)t * a.k_stride + (long long)kvh[u] * kHeadDim;
-            raw[u] = reinterpret_cast<const uint4*>(src)[hl];
-        }
-    }
+            const int h = is_v ? kvh[u] - a.num_kv_heads : kvh[u];
+            void* cache = is_v ? a.v_cache : a.k_cache;
+            const long long dst = ((long long)slot[u] * a.num_kv_heads + h) * kHeadDim + 8 * hl;
+            if constexpr (!FP8) {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + dst) = raw[u];
+            } else {
+                float y[8];
+                unpack8(raw[u], y);
+                float am = 0.f;
 #pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-        if (slot[u] < 0) continue;  // padding (or no row): uniform over the half-warp
-        if (slot[u] / kChunk >= a.num_pages) {
-            if (hl == 0 && a.err) atomicOr(a.err, (int)HPC_DEVERR_PAGE_OUT_OF_RANGE);
-            continue;
-        }
-        const bool is_v = kvh[u] >= a.num_kv_heads;
-        const int h = is_v ? kvh[u] - a.num_kv_heads : kvh[u];
-        void* cache = is_v ? a.v_cache : a.k_cache;
-        const long long dst = ((long long)slot[u] * a.num_kv_heads + h) * kHeadDim + 8 * hl;
-        if constexpr (!FP8) {
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + dst) = raw[u];
-        } else {
-            float y[8];
-            unpack8(raw[u], y);
-            float am = 0.f;
+                for (int k = 0; k < 8; ++k) am = fmaxf(am, fabsf(y[k]));
 #pragma unroll
-            for (int k = 0; k < 8; ++k) am = fmaxf(am, fabsf(y[k]));
+                for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(mask, am, o));
+                float scale = __fdiv_rn(am, kE4m3Max);
+                if (!(scale > 0.f)) scale = 1.f;
+                // x / scale: a product with the reciprocal and one correction step (the
+                // quotient rounded, but for results near float32's ends, where the codes
+                // do not see the difference)
+                const float inv = __frcp_rn(scale);
+                const bool plain = inv <= 3.0e38f && scale >= 1.2e-38f;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(mask, am, o));
-            float scale = __fdiv_rn(am, kE4m3Max);
-            if (!(scale > 0.f)) scale = 1.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = __fdiv_rn(y[k], scale);
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + dst) = pack_e4m3x8(y);
-            if (hl == 0)
-                (is_v ? a.v_scale : a.k_scale)[((long long)(slot[u] / kChunk) * a.num_kv_heads + h) * kChunk + slot[u] % kChunk] =
-                    scale;
+                for (int k = 0; k < 8; ++k) {
+                    const float q = y[k] * inv;
+                    const float c = fmaf(fmaf(-q, scale, y[k]), inv, q);
+                    y[k] = plain && fabsf(q) <= 3.0e38f ? c : __fdiv_rn(y[k], scale);
+                }
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + dst) = pack_e4m3x8(y);
+                if (hl == 0)
+                    (is_v ? a.v_scale : a.k_scale)[((long long)page * a.num_kv_heads + h) * kChunk + off] = scale;
+            }
         }
     }
 }
 
-// One block per (64-row piece of a request's output, ...): see launch_kv_read.
-template <bool FP8, int ROWS>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a) {
-    grid_dependency_wait();  // the cache may still be being written
+// First the block's tokens, one per thread: the request by a search in out_starts,
+// then the page. Then 16 lanes (bf16) or 8 (e4m3, 16 codes each) per row.
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a, int tokens_per_block) {
+    __shared__ int starts[kSmemStarts];
+    __shared__ int src_sh[kMaxTokens];  // page * 64 + slot; -1: no valid page (zeros); -2: no request's row
+    grid_dependency_wait();             // the cache may still be being written
     grid_launch_dependents();
-    const int hl = threadIdx.x & 15;
-    const long long rows = (long long)a.num_rows * 2 * a.num_kv_heads;
-    const long long first = ((long long)blockIdx.x * kHalfWarps + (threadIdx.x >> 4)) * ROWS;
-    if (first >= rows) return;
-    // request of the first row's token: the last one that starts at or before it
-    int tok = (int)(first / (2 * a.num_kv_heads)), b = 0;
-    {
-        int lo = 0, hi = a.batch;
+    const bool in_smem = a.batch + 1 <= kSmemStarts;
+    if (in_smem) {
+        for (int i = threadIdx.x; i <= a.batch; i += kThreads) starts[i] = a.out_starts[i];
+        __syncthreads();
+    }
+    const int* st = in_smem ? starts : a.out_starts;
+    const int t0 = blockIdx.x * tokens_per_block, nt = min(tokens_per_block, a.num_rows - t0);
+    if ((int)threadIdx.x < nt) {
+        const int tok = t0 + threadIdx.x;
+        int lo = 0, hi = a.batch;  // the last request that starts at or before the row
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (a.out_starts[mid] <= tok)
+            if (st[mid] <= tok)
                 lo = mid;
             else
                 hi = mid;
         }
-        b = lo;
-    }
-    int bs = a.out_starts[b], be = a.out_starts[b + 1];
-    long long src[ROWS];
-    int kvh[ROWS], trow[ROWS];
-#pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-        const long long r = first + u;
-        trow[u] = -1;
-        src[u] = -1;
-        kvh[u] = 0;
-        if (r >= rows) continue;
-        tok = (int)(r / (2 * a.num_kv_heads));
-        kvh[u] = (int)(r % (2 * a.num_kv_heads));
-        while (tok >= be && b + 1 < a.batch) {
-            ++b;
-            bs = be;
-            be = a.out_starts[b + 1];
+        int src = -2;
+        if (tok >= st[lo] && tok < st[lo + 1]) {
+            src = -1;
+            const long long pos = (long long)tok - st[lo] + (a.first ? a.first[lo] : 0);
+            int page = -1;
+            if (pos >= 0 && pos / kChunk < a.pt_stride) page = a.page_table[(long long)lo * a.pt_stride + pos / kChunk];
+            if ((unsigned)page < (unsigned)a.num_pages)
+                src = page * kChunk + (int)(pos % kChunk);
+            else if (a.err)
+                atomicOr(a.err, (int)HPC_DEVERR_PAGE_OUT_OF_RANGE);
         }
-        if (tok < bs || tok >= be) continue;  // a row of no request: left as it is
-        trow[u] = tok;
-        const long long pos = (long long)tok - bs + (a.first ? a.first[b] : 0);
-        int page = -1;
-        if (pos >= 0 && pos / kChunk < a.pt_stride) page = a.page_table[(long long)b * a.pt_stride + pos / kChunk];
-        if ((unsigned)page < (unsigned)a.num_pages)
-            src[u] = (long long)page * kChunk + pos % kChunk;
-        else if (hl == 0 && a.err)
-            atomicOr(a.err, (int)HPC_DEVERR_PAGE_OUT_OF_RANGE);
+        src_sh[threadIdx.x] = src;
     }
-    uint4 raw[ROWS];
-    float scale[ROWS];
+    __syncthreads();
+    constexpr int kLanes = FP8 ? 8 : 16;
+    const int hl = threadIdx.x % kLanes;
+    const unsigned per_token = 2u * (unsigned)a.num_kv_heads, rows = (unsigned)nt * per_token;
+    for (unsigned r0 = threadIdx.x / kLanes; r0 < rows; r0 += kThreads / kLanes * kUnroll) {
+        uint4 raw[kUnroll];
+        float scale[kUnroll];
+        long long dst[kUnroll];  // element of k_out or v_out; -1: nothing to write
+        bool is_v[kUnroll];
 #pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-        raw[u] = make_uint4(0u, 0u, 0u, 0u);  // tokens without a valid page read as zeros
-        scale[u] = 0.f;
-        if (src[u] < 0) continue;
-        const bool is_v = kvh[u] >= a.num_kv_heads;
-        const int h = is_v ? kvh[u] - a.num_kv_heads : kvh[u];
-        const long long at = (src[u] * a.num_kv_heads + h) * kHeadDim + 8 * hl;
-        if constexpr (FP8) {
-            const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v_cache : a.k_cache) + at);
-            raw[u].x = c.x;
-            raw[u].y = c.y;
-            scale[u] = (is_v ? a.v_scale : a.k_scale)[(src[u] / kChunk * a.num_kv_heads + h) * kChunk + src[u] % kChunk];
-        } else {
-            raw[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(is_v ? a.v_cache : a.k_cache) + at);
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-        if (trow[u] < 0) continue;
-        const bool is_v = kvh[u] >= a.num_kv_heads;
-        const int h = is_v ? kvh[u] - a.num_kv_heads : kvh[u];
-        uint4 o = raw[u];
-        if constexpr (FP8) {
-            uint32_t f[4];
-            e4m3x4_to_f16x2x2(raw[u].x, f[0], f[1]);
-            e4m3x4_to_f16x2x2(raw[u].y, f[2], f[3]);
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f[k]));
-                w[k] = pack_bf16x2(x.x * scale[u], x.y * scale[u]);
+        for (int u = 0; u < kUnroll; ++u) {
+            const unsigned r = r0 + u * (kThreads / kLanes);
+            raw[u] = make_uint4(0u, 0u, 0u, 0u);
+            scale[u] = 0.f;
+            dst[u] = -1;
+            is_v[u] = false;
+            if (r >= rows) continue;
+            const unsigned tl = r / per_token;
+            const int kvh = (int)(r - tl * per_token);
+            const int src = src_sh[tl];
+            is_v[u] = kvh >= a.num_kv_heads;
+            const int h = is_v[u] ? kvh - a.num_kv_heads : kvh;
+            if (src == -2) continue;
+            dst[u] = ((long long)(t0 + (int)tl) * a.num_kv_heads + h) * kHeadDim + hl * (kHeadDim / kLanes);
+            if (src < 0) continue;
+            const long long at = ((long long)src * a.num_kv_heads + h) * kHeadDim + hl * (kHeadDim / kLanes);
+            const void* cache = is_v[u] ? a.v_cache : a.k_cache;
+            if constexpr (FP8) {
+                raw[u] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) + at);
+                scale[u] = (is_v[u] ? a.v_scale : a.k_scale)[((long long)(src / kChunk) * a.num_kv_heads + h) * kChunk + src % kChunk];
+            } else {
+                raw[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(cache) + at);
             }
-            o = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        __nv_bfloat16* dst = (is_v ? a.v_out : a.k_out) + ((long long)trow[u] * a.num_kv_heads + h) * kHeadDim + 8 * hl;
-        *reinterpret_cast<uint4*>(dst) = o;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (dst[u] < 0) continue;
+            uint4* out = reinterpret_cast<uint4*>((is_v[u] ? a.v_out : a.k_out) + dst[u]);
+            if constexpr (FP8) {
+                const uint32_t c[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t f[2];
+                    e4m3x4_to_f16x2x2(c[k], f[0], f[1]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f[j]));
+                        w[2 * k + j] = pack_bf16x2(x.x * scale[u], x.y * scale[u]);
+                    }
+                }
+                out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+                out[0] = raw[u];
+            }
+        }
     }
 }
 
-constexpr int kRowsMany = 4;
-
-template <typename K1, typename K4, typename A>
-cudaError_t launch_rows(K1 one, K4 many, long long rows, const A& a, cudaStream_t s) {
-    // a row per half-warp while that leaves the GPU's blocks unfilled, else several
-    const bool few = rows <= 152LL * 8 * kHalfWarps;
-    const int per = few ? 1 : kRowsMany;
-    const long long blocks = (rows + (long long)kHalfWarps * per - 1) / ((long long)kHalfWarps * per);
-    return few ? launch_pdl(one, dim3((unsigned)blocks), dim3(kThreads), 0, s, a)
-               : launch_pdl(many, dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
+// Tokens of a block: as many as leave four blocks per SM, at most 64.
+int tokens_per_block(int tokens) {
+    int n = kMaxTokens;
+    while (n > 1 && (tokens + n - 1) / n < 152 * 4) n >>= 1;
+    return n;
 }
 
 }  // namespace
 
 cudaError_t launch_kv_write(const KvWriteArgs& a, bool fp8, cudaStream_t s) {
-    const long long rows = (long long)a.num_tokens * 2 * a.num_kv_heads;
-    return fp8 ? launch_rows(kv_write_kernel<true, 1>, kv_write_kernel<true, kRowsMany>, rows, a, s)
-               : launch_rows(kv_write_kernel<false, 1>, kv_write_kernel<false, kRowsMany>, rows, a, s);
+    const int n = tokens_per_block(a.num_tokens);
+    const dim3 grid((a.num_tokens + n - 1) / n);
+    return fp8 ? launch_pdl(kv_write_kernel<true>, grid, dim3(kThreads), 0, s, a, n)
+               : launch_pdl(kv_write_kernel<false>, grid, dim3(kThreads), 0, s, a, n);
 }
 
 cudaError_t launch_kv_read(const KvReadArgs& a, bool fp8, cudaStream_t s) {
-    const long long rows = (long long)a.num_rows * 2 * a.num_kv_heads;
-    return fp8 ? launch_rows(kv_read_kernel<true, 1>, kv_read_kernel<true, kRowsMany>, rows, a, s)
-               : launch_rows(kv_read_kernel<false, 1>, kv_read_kernel<false, kRowsMany>, rows, a, s);
+    const int n = tokens_per_block(a.num_rows);
+    const dim3 grid((a.num_rows + n - 1) / n);
+    return fp8 ? launch_pdl(kv_read_kernel<true>, grid, dim3(kThreads), 0, s, a, n)
+               : launch_pdl(kv_read_kernel<false>, grid, dim3(kThreads), 0, s, a, n);
 }
 
 }  // namespace hpc

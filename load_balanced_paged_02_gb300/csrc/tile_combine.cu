@@ -7,8 +7,8 @@
 // worker) into the output rows; whole tiles were written by the attention kernel.
 // prefix_combine_kernel: for every (request, new token, query head) the pieces
 // of its group's prefix tile and the splits of its own suffix.
-// Both: a warp per row, lane k owning dims [4 k, 4 k + 4). Bound by the reads of
-// the partial rows, mostly from L2, and by launch latency for small batches.
+// Both: a warp per four rows, lane k owning dims [4 k, 4 k + 4). Bound by the reads
+// of the partial rows, mostly from L2, and by launch latency for small batches.
 #include "tile.cuh"
 
 namespace hpc {
@@ -26,33 +26,102 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* out, long long row, int
     *reinterpret_cast<uint2*>(out + row * kHeadDim + 4 * lane) = w;
 }
 
-// Running merge of partial rows.
-struct Merge {
-    float m = -INFINITY, w = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-
-    __device__ __forceinline__ void add(float lse, const float4& o) {
-        if (lse == -INFINITY) return;  // a piece without a visible key
-        const float M = fmaxf(m, lse);
-        const float a = m == -INFINITY ? 0.f : exp2f((m - M) * kLog2e), b = exp2f((lse - M) * kLog2e);
-        m = M;
-        w = w * a + b;
-        acc.x = acc.x * a + o.x * b;
-        acc.y = acc.y * a + o.y * b;
-        acc.z = acc.z * a + o.z * b;
-        acc.w = acc.w * a + o.w * b;
-    }
-    __device__ __forceinline__ float lse() const { return w == 0.f ? -INFINITY : m + logf(w); }
-    __device__ __forceinline__ float4 row() const {
-        const float inv = w == 0.f ? 0.f : 1.f / w;
-        return make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    }
+// Partial rows at equal distances: run.n of them, the first at row run.row of (o,
+// lse), run.step rows apart.
+struct Run {
+    const float* o;
+    const float* lse;
+    long long row, step;
+    int n;
 };
 
+constexpr int kRows = 4;   // neighbouring rows (query heads of one token) that a warp merges at once
+constexpr int kBatch = 8;  // pieces whose LSEs the warp holds at once: lane 8 r + i has piece i of row r
+
+// A warp merges two runs into kRows neighbouring rows: v[r] gets dims [4 k, 4 k + 4)
+// of row r (k the lane), lse the LSE of row lane / kBatch. A piece without a visible
+// key (LSE -inf) has weight 0 and is not added.
+__device__ __forceinline__ void merge_runs(const Run& a, const Run& b, int lane, float4 (&v)[kRows], float& lse) {
+    const int n = a.n + b.n, lr = lane / kBatch, li = lane % kBatch;
+    float m = -INFINITY, sum = 0.f;  // of row lr
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) v[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+        const int i = i0 + li;
+        float l = -INFINITY;
+        if (i < a.n)
+            l = a.lse[a.row + i * a.step + lr];
+        else if (i < n)
+            l = b.lse[b.row + (i - a.n) * b.step + lr];
+        // the first pieces' rows are on their way while the weights are made
+        const int cnt = min(kBatch, n - i0);
+        float4 x[2][kRows];
+        auto load = [&](int k, float4 (&y)[kRows]) {
+            const int j = i0 + k;
+            const float* src = j < a.n ? a.o + (a.row + j * a.step) * kHeadDim : b.o + (b.row + (j - a.n) * b.step) * kHeadDim;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) y[r] = *reinterpret_cast<const float4*>(src + r * kHeadDim + 4 * lane);
+        };
+        load(0, x[0]);
+        if (cnt > 1) load(1, x[1]);
+        // (fmaxf passes a NaN over; its weight stays NaN)
+        float M = l;
+#pragma unroll
+        for (int o = kBatch / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        M = fmaxf(M, m);
+        const float old = m == -INFINITY ? 0.f : exp2f((m - M) * kLog2e);  // what the sums so far still weigh
+        m = M;
+        const float w = l == -INFINITY ? 0.f : exp2f((l - (M == -INFINITY ? 0.f : M)) * kLog2e);
+        float ws = w;
+#pragma unroll
+        for (int o = kBatch / 2; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+        sum = sum * old + ws;
+        if (i0 > 0) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float f = __shfl_sync(0xffffffffu, old, r * kBatch);
+                v[r].x *= f, v[r].y *= f, v[r].z *= f, v[r].w *= f;
+            }
+        }
+        for (int k = 0; k < cnt; k += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (k + u >= cnt) break;
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const float f = __shfl_sync(0xffffffffu, w, r * kBatch + k + u);
+                    if (f != 0.f) {
+                        v[r].x += f * x[u][r].x;
+                        v[r].y += f * x[u][r].y;
+                        v[r].z += f * x[u][r].z;
+                        v[r].w += f * x[u][r].w;
+                    }
+                }
+                if (k + u + 2 < cnt) load(k + u + 2, x[u]);
+            }
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    lse = sum == 0.f ? -INFINITY : m + logf(sum);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        const float f = __shfl_sync(0xffffffffu, inv, r * kBatch);
+        v[r] = make_float4(v[r].x * f, v[r].y * f, v[r].z * f, v[r].w * f);
+    }
+}
+
+// Writes merged rows to output rows orow, orow + 1, ...
+__device__ __forceinline__ void store_rows(__nv_bfloat16* out, float* out_lse, long long orow, int lane,
+                                           const float4 (&v)[kRows], float lse) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) store_row(out, orow + r, lane, v[r]);
+    if (out_lse && lane % kBatch == 0) out_lse[orow + lane / kBatch] = lse;
+}
+static_assert(kRows * kBatch == 32 && kGroup % kRows == 0, "a warp's lanes; rows of one token");
+
 __global__ void __launch_bounds__(kWarps * 32)
-    prefill_combine_kernel(const int32_t* plan, long long seqs_off, int Hq, int C, int T,
-                           const float* split_o, const float* split_lse,
-                           __nv_bfloat16* out, float* out_lse) {
+    prefill_combine_kernel(const int32_t* plan, long long seqs_off, long long units_off, int Hq, int T,
+                           const float* split_o, const float* split_lse, __nv_bfloat16* out, float* out_lse) {
     grid_dependency_wait();  // the pieces come from the attention kernel
     grid_launch_dependents();
     const int4* starts = reinterpret_cast<const int4*>(plan + kHdrInts);
@@ -62,42 +131,42 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (e.w == 0) return;
     const bool same = a.x == e.x && a.y == e.y && a.z == e.z;
     if (same && a.w > 0) return;
-    int pieces = 2;  // worker j's and the next ones', until one reaches the tile's end
-    for (int k = j + 1; k < C; ++k) {
-        const int4 f = starts[2 * (k + 1)];
-        if (!(f.x == e.x && f.y == e.y && f.z == e.z && f.w > 0)) break;
-        ++pieces;
-    }
     const int4 q = reinterpret_cast<const int4*>(plan + seqs_off)[e.y];
+    const long long per_head = *reinterpret_cast<const long long*>(plan + kTUnitsPerHead);
+    const long long bucket = *reinterpret_cast<const long long*>(plan + kTBucket);
+    const long long end = e.x * per_head + reinterpret_cast<const long long*>(plan + units_off)[e.y] +
+                          tile_units(kModePrefill, q.y, q.z, e.z + 1, T);
+    const int last = (int)((end - 1) / bucket);  // the worker with the tile's last block
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int r = blockIdx.y * kWarps + warp; r < T * kGroup; r += kParts * kWarps) {
+    for (int r = (blockIdx.y * kWarps + warp) * kRows; r < T * kGroup; r += kParts * kWarps * kRows) {
         const int tok = e.z * T + r / kGroup;
         if (tok >= q.y) break;
-        Merge mg;
-        for (int u = 0; u < pieces; ++u) {
-            const long long row = (u == 0 ? 2LL * j + 1 : 2LL * (j + u)) * (T * kGroup) + r;
-            mg.add(split_lse[row], *reinterpret_cast<const float4*>(split_o + row * kHeadDim + 4 * lane));
-        }
-        const long long orow = (long long)(q.x + tok) * Hq + e.x * kGroup + r % kGroup;
-        store_row(out, orow, lane, mg.row());
-        if (out_lse && lane == 0) out_lse[orow] = mg.lse();
+        // worker j's piece, and one of every worker after it up to the last
+        const Run head{split_o, split_lse, (2LL * j + 1) * (T * kGroup) + r, 0, 1};
+        const Run rest{split_o, split_lse, (2LL * j + 2) * (T * kGroup) + r, 2LL * T * kGroup, last - j};
+        float4 v[kRows];
+        float lse;
+        merge_runs(head, rest, lane, v, lse);
+        store_rows(out, out_lse, (long long)(q.x + tok) * Hq + e.x * kGroup + r % kGroup, lane, v, lse);
     }
 }
 
 __global__ void __launch_bounds__(kWarps * 32)
     prefix_combine_kernel(const int32_t* prefix_plan, long long seqs_off, long long units_off, int S, int T,
-                          const float* prefix_o, const float* prefix_lse,
-                          const int32_t* pair_nsplit, const int32_t* pair_split0,
-                          const float* split_o, const float* split_lse,
-                          __nv_bfloat16* out, float* out_lse, int B, int Hq, int Q) {
+                          const float* prefix_o, const float* prefix_lse, const int32_t* pair_nsplit,
+                          const int32_t* pair_split0, const float* split_o, const float* split_lse, __nv_bfloat16* out,
+                          float* out_lse, int B, int Hq, int Q) {
     grid_dependency_wait();  // the pieces come from the attention kernels
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long orow = (long long)blockIdx.x * kWarps + warp;  // (request, new token, query head)
+    const long long orow = ((long long)blockIdx.x * kWarps + warp) * kRows;  // (request, new token, query head)
     if (orow >= (long long)B * Q * Hq) return;
     const int tok = (int)(orow / Hq), qh = (int)(orow % Hq);
     const int h = qh / kGroup, j = qh % kGroup, b = tok / Q, qi = tok % Q;
-    Merge mg;
+    const long long pair = (long long)h * B + b;
+    const long long rs = (long long)Q * kGroup;
+    const Run own{split_o, split_lse, pair_split0[pair] * rs + qi * kGroup + j, rs, pair_nsplit[pair]};
+    Run prefix{prefix_o, prefix_lse, 0, (long long)T * kGroup, 0};
     // the group whose query tokens hold this one: the last that starts at or before it
     const int4* seqs = reinterpret_cast<const int4*>(prefix_plan + seqs_off);
     int lo = 0, hi = S;
@@ -110,35 +179,28 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     const int4 q = seqs[lo];
     if (tok >= q.x && tok < q.x + q.y && q.z > 0) {
-        const long long* units = reinterpret_cast<const long long*>(prefix_plan + units_off);
         const long long per_head = *reinterpret_cast<const long long*>(prefix_plan + kTUnitsPerHead);
         const long long bucket = *reinterpret_cast<const long long*>(prefix_plan + kTBucket);
         const int i = (tok - q.x) / T, r = (tok - q.x) % T * kGroup + j;
         const int blocks = tile_blocks(kModePrefix, q.y, q.z, i, T);
-        const long long g0 = h * per_head + units[lo] + (long long)i * blocks;
+        const long long g0 = h * per_head + reinterpret_cast<const long long*>(prefix_plan + units_off)[lo] + (long long)i * blocks;
         const long long tile = (long long)h * prefix_plan[kTTilesPerHead] + q.w + i;
-        for (long long c = g0 / bucket; c <= (g0 + blocks - 1) / bucket; ++c) {
-            const long long row = (tile + c) * (T * kGroup) + r;
-            mg.add(prefix_lse[row], *reinterpret_cast<const float4*>(prefix_o + row * kHeadDim + 4 * lane));
-        }
+        const long long c0 = g0 / bucket;  // one piece per worker that the tile's blocks touch
+        prefix.row = (tile + c0) * (T * kGroup) + r;
+        prefix.n = (int)((g0 + blocks - 1) / bucket - c0) + 1;
     }
-    const long long pair = (long long)h * B + b;
-    const int n = pair_nsplit[pair];
-    const long long s0 = pair_split0[pair];
-    for (int u = 0; u < n; ++u) {
-        const long long row = ((s0 + u) * Q + qi) * kGroup + j;
-        mg.add(split_lse[row], *reinterpret_cast<const float4*>(split_o + row * kHeadDim + 4 * lane));
-    }
-    store_row(out, orow, lane, mg.row());
-    if (out_lse && lane == 0) out_lse[orow] = mg.lse();
+    float4 v[kRows];
+    float lse;
+    merge_runs(prefix, own, lane, v, lse);
+    store_rows(out, out_lse, orow, lane, v, lse);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill_combine(const int32_t* plan, int S, int Hq, int C, int T, const float* split_o,
                                    const float* split_lse, void* out, float* out_lse, cudaStream_t s) {
-    return launch_pdl(prefill_combine_kernel, dim3(C, kParts), dim3(kWarps * 32), 0, s, plan, tile_layout(S, C).seqs, Hq, C, T,
-                      split_o, split_lse, static_cast<__nv_bfloat16*>(out), out_lse);
+    return launch_pdl(prefill_combine_kernel, dim3(C, kParts), dim3(kWarps * 32), 0, s, plan, tile_layout(S, C).seqs,
+                      tile_layout(S, C).units, Hq, T, split_o, split_lse, static_cast<__nv_bfloat16*>(out), out_lse);
 }
 
 cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_workers, int T, const float* prefix_o,
@@ -147,7 +209,7 @@ cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_
                                   int q_len, cudaStream_t s) {
     const TileLayout t = tile_layout(S, prefix_workers);
     const PlanLayout L = plan_layout(B, Hkv, ctas);
-    const long long blocks = ((long long)B * q_len * Hq + kWarps - 1) / kWarps;
+    const long long blocks = ((long long)B * q_len * Hq / kRows + kWarps - 1) / kWarps;
     return launch_pdl(prefix_combine_kernel, dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, prefix_plan, t.seqs, t.units,
                       S, T, prefix_o, prefix_lse, plan + L.pair_nsplit, plan + L.pair_split0, split_o, split_lse, out, out_lse,
                       B, Hq, q_len);
