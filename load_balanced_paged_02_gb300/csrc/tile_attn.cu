@@ -404,17 +404,23 @@ __device__ __forceinline__ void split_query_rows(uint8_t* qt, float* qs, int wq,
 // of a warp spread over all banks.
 template <int CG>
 __device__ __forceinline__ void widen_v(const uint8_t* codes, const float* vs, uint8_t* wide, int nv, int tg) {
-#pragma unroll 2
+#pragma unroll 1
     for (int rr = 0; rr < 4; ++rr) {
         const int row = 32 * rr + (tg >> 2);
         const bool in = row < nv;
-        const uint32_t sb = in ? __float_as_uint(vs[row]) : 0u;
-        const int e = (int)((sb >> 23) & 255u) - 127, a = e < -14 ? -10 : 0;
-        // f 2^a (NaN or infinity stay what they are) and 2^b, b = e - a (0 where it underflows)
-        const float fa = e == 128 ? __uint_as_float(sb)
-                                  : __uint_as_float((sb & 0x807fffffu) | (uint32_t)(127 + a) << 23);
-        const float fb = e == 128 ? 1.f : __uint_as_float((uint32_t)max(e - a + 127, 0) << 23);
-        const uint32_t s2 = pack_f16x2(fa, fa), p2 = pack_f16x2(fb, fb);
+        const float sv = in ? vs[row] : 0.f;
+        const uint32_t sb = __float_as_uint(sv);
+        const int e = (int)((sb >> 23) & 255u) - 127;
+        // one product where the scale is a normal f16 number (or zero) in all the warp's rows
+        const bool small = __any_sync(0xffffffffu, sv != 0.f && e < -14);
+        uint32_t s2 = pack_f16x2(sv, sv), p2 = 0;
+        if (small) {
+            // f 2^a (NaN or infinity stay what they are) and 2^b, b = e - a (0 where it underflows)
+            const int a = e < -14 ? -10 : 0;
+            const float fa = e == 128 ? sv : __uint_as_float((sb & 0x807fffffu) | (uint32_t)(127 + a) << 23);
+            const float fb = e == 128 ? 1.f : __uint_as_float((uint32_t)max(e - a + 127, 0) << 23);
+            s2 = pack_f16x2(fa, fa), p2 = pack_f16x2(fb, fb);
+        }
 #pragma unroll
         for (int hf = 0; hf < 2 / CG; ++hf) {
             const int c16 = (tg & 3) + 4 * hf;
@@ -426,10 +432,12 @@ __device__ __forceinline__ void widen_v(const uint8_t* codes, const float* vs, u
                 e4m3x4_to_f16x2x2(w.y, vl.z, vl.w);
                 e4m3x4_to_f16x2x2(w.z, vh.x, vh.y);
                 e4m3x4_to_f16x2x2(w.w, vh.z, vh.w);
-                vl.x = hmul2_u32(hmul2_u32(vl.x, s2), p2), vl.y = hmul2_u32(hmul2_u32(vl.y, s2), p2);
-                vl.z = hmul2_u32(hmul2_u32(vl.z, s2), p2), vl.w = hmul2_u32(hmul2_u32(vl.w, s2), p2);
-                vh.x = hmul2_u32(hmul2_u32(vh.x, s2), p2), vh.y = hmul2_u32(hmul2_u32(vh.y, s2), p2);
-                vh.z = hmul2_u32(hmul2_u32(vh.z, s2), p2), vh.w = hmul2_u32(hmul2_u32(vh.w, s2), p2);
+                vl.x = hmul2_u32(vl.x, s2), vl.y = hmul2_u32(vl.y, s2), vl.z = hmul2_u32(vl.z, s2), vl.w = hmul2_u32(vl.w, s2);
+                vh.x = hmul2_u32(vh.x, s2), vh.y = hmul2_u32(vh.y, s2), vh.z = hmul2_u32(vh.z, s2), vh.w = hmul2_u32(vh.w, s2);
+                if (small) {
+                    vl.x = hmul2_u32(vl.x, p2), vl.y = hmul2_u32(vl.y, p2), vl.z = hmul2_u32(vl.z, p2), vl.w = hmul2_u32(vl.w, p2);
+                    vh.x = hmul2_u32(vh.x, p2), vh.y = hmul2_u32(vh.y, p2), vh.z = hmul2_u32(vh.z, p2), vh.w = hmul2_u32(vh.w, p2);
+                }
             }
             const int f0 = 2 * (tg & 3);
             *reinterpret_cast<uint4*>(wide + hf * 16384 + row * 128 + ((f0 ^ (row & 7)) << 4)) = vl;
