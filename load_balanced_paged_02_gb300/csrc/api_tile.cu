@@ -93,10 +93,11 @@ hpc_status attn_common(const void* q, const void* k_cache, const void* v_cache, 
     if (st != HPC_OK) return st;
     if ((st = cache_check(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, num_kv_heads)) != HPC_OK) return st;
     if ((st = plan_check(plan, mode, num_kv_heads)) != HPC_OK) return st;
-    if (!q || !aligned(q, 16) || !table || table_stride != plan->table_stride) return HPC_ERR_INVALID_ARG;
+    if (!table || table_stride != plan->table_stride) return HPC_ERR_INVALID_ARG;
     if (!split_o || !split_lse || !aligned(split_o, 16)) return HPC_ERR_INVALID_ARG;
+    if (plan->num_tokens == 0) return HPC_OK;  // q and out have no rows, and may be null
+    if (!q || !aligned(q, 16)) return HPC_ERR_INVALID_ARG;
     if (mode == kModePrefill && (!out || !aligned(out, 16))) return HPC_ERR_INVALID_ARG;
-    if (plan->num_tokens == 0) return HPC_OK;
     const bool fp8 = kv_dtype == HPC_KV_FP8_E4M3;
     TileAttnArgs a;
     a.q = q;
@@ -207,8 +208,9 @@ hpc_status hpc_prefill_combine(const hpc_tile_plan* plan, const float* split_o, 
     hpc_status st = shape_check(num_q_heads, num_kv_heads, head_dim, kChunk);
     if (st != HPC_OK) return st;
     if ((st = plan_check(plan, kModePrefill, num_kv_heads)) != HPC_OK) return st;
-    if (!split_o || !split_lse || !out || !aligned(split_o, 16) || !aligned(out, 16)) return HPC_ERR_INVALID_ARG;
+    if (!split_o || !split_lse || !aligned(split_o, 16)) return HPC_ERR_INVALID_ARG;
     if (plan->num_tokens == 0) return HPC_OK;
+    if (!out || !aligned(out, 16)) return HPC_ERR_INVALID_ARG;
     return launched(launch_prefill_combine(plan->buf, plan->num_seqs, num_q_heads, plan->num_workers, plan->tile_tokens, split_o, split_lse,
                                            out, out_lse, static_cast<cudaStream_t>(stream)));
 }
@@ -261,7 +263,8 @@ hpc_status hpc_prefill(const void* q, const void* k_cache, const void* v_cache, 
     hpc_status st = shape_check(num_q_heads, num_kv_heads, head_dim, page_size);
     if (st != HPC_OK) return st;
     if ((st = cache_check(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, num_kv_heads)) != HPC_OK) return st;
-    if (!q || !aligned(q, 16) || !page_table || !out || !aligned(out, 16)) return HPC_ERR_INVALID_ARG;
+    if (!page_table) return HPC_ERR_INVALID_ARG;
+    if (num_tokens != 0 && (!q || !aligned(q, 16) || !out || !aligned(out, 16))) return HPC_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     plan->buf = reinterpret_cast<int32_t*>(ws + w.plan);
     plan->bytes = hpc_tile_plan_bytes(batch, num_ctas);
@@ -337,12 +340,12 @@ hpc_status hpc_kv_write(const void* k, const void* v, long long k_token_stride, 
     if (num_tokens < 0 || !heads_ok(num_kv_heads)) return HPC_ERR_INVALID_ARG;
     hpc_status st = cache_check(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, num_kv_heads);
     if (st != HPC_OK) return st;
-    if (!k || !v || !slot_mapping || !aligned(k, 16) || !aligned(v, 16)) return HPC_ERR_INVALID_ARG;
     // rows of 16-byte pieces; a stride shorter than a token's heads would be a mistake
     const long long row = (long long)num_kv_heads * kHeadDim;
     if (k_token_stride < row || v_token_stride < row || k_token_stride % 8 != 0 || v_token_stride % 8 != 0)
         return HPC_ERR_INVALID_ARG;
-    if (num_tokens == 0) return HPC_OK;
+    if (num_tokens == 0) return HPC_OK;  // the rows' pointers may be null then
+    if (!k || !v || !slot_mapping || !aligned(k, 16) || !aligned(v, 16)) return HPC_ERR_INVALID_ARG;
     KvWriteArgs a;
     a.k = static_cast<const __nv_bfloat16*>(k);
     a.v = static_cast<const __nv_bfloat16*>(v);
@@ -369,9 +372,9 @@ hpc_status hpc_kv_read(const void* k_cache, const void* v_cache, const float* k_
         return HPC_ERR_INVALID_ARG;
     hpc_status st = cache_check(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, num_kv_heads);
     if (st != HPC_OK) return st;
-    if (!page_table || !out_starts || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16))
-        return HPC_ERR_INVALID_ARG;
+    if (!page_table || !out_starts) return HPC_ERR_INVALID_ARG;
     if (num_rows == 0) return HPC_OK;
+    if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)) return HPC_ERR_INVALID_ARG;
     KvReadArgs a;
     a.k_cache = k_cache;
     a.v_cache = v_cache;
