@@ -531,8 +531,8 @@ hpc_status hpc_decode_noalloc(const void* q, const void* k_cache, const void* v_
  *   [0, 16)   header {units_per_head (int64), bucket (int64), used workers,
  *             num_seqs, num_kv_heads, num_workers, num_tokens, mode,
  *             tiles_per_head, q_len, error word, tile_tokens, 0, 0}
- *   starts    [num_workers + 1][8] {kv head, sequence, tile, block, tile number, 0, 0, 0}:
- *             where each worker's run begins
+ *   starts    [num_workers + 1][8] {kv head, sequence, tile, block} and that
+ *             sequence's row of seqs: where each worker's run begins
  *   seqs      [num_seqs][4] {first query token, query tokens, keys, tiles before}
  *   units     int64 [num_seqs + 1]: units of the sequences before (a block is one
  *             unit; a tile of a prompt costs one more)

@@ -49,7 +49,7 @@ struct TileLayout {
 
 __host__ __device__ inline TileLayout tile_layout(long long S, long long C) {
     TileLayout L;
-    L.starts = kHdrInts;                      // [C + 1] rows of 8: {kv head, sequence, tile, block, tile number, 0, 0, 0}
+    L.starts = kHdrInts;                      // [C + 1] rows of 8: {kv head, sequence, tile, block} and the sequence's row of seqs
     L.seqs = L.starts + (C + 1) * 8;          // [S] rows of 4: {first query token, n, L, tiles of the sequences before}
     L.units = L.seqs + S * 4;                 // int64 [S + 1]: units of the sequences before
     L.total_ints = L.units + (S + 1) * 2;
@@ -145,10 +145,12 @@ struct TileWalk {
     const int4* seqs;
     int S, mode, tiles_per_head;
     TilePos at, end;
+    int4 q;  // at.s's row of seqs
 
     __device__ __forceinline__ void start(const int32_t* plan, int S_, int mode_, int worker, long long seqs_off) {
         const int4* st = reinterpret_cast<const int4*>(plan + kHdrInts + (long long)worker * 8);
         const int4 a = st[0], e = st[2];
+        q = st[1];
         at = TilePos{a.x, a.y, a.z, a.w};
         end = TilePos{e.x, e.y, e.z, e.w};
         seqs = reinterpret_cast<const int4*>(plan + seqs_off);
@@ -162,7 +164,6 @@ struct TileWalk {
         for (;;) {
             const bool last = at.h == end.h && at.s == end.s && at.i == end.i;
             if (last && at.blk >= end.blk) return false;
-            const int4 q = seqs[at.s];
             const int blocks = tile_blocks(mode, q.y, q.z, at.i, T);
             it.h = at.h;
             it.s = at.s;
@@ -191,9 +192,9 @@ struct TileWalk {
                             at = end;
                             break;
                         }
+                        q = seqs[at.s];
                         if (at.h == end.h && at.s == end.s) break;
-                        const int4 x = seqs[at.s];
-                        if (x.y > 0 && (mode == kModePrefill || x.z > 0)) break;
+                        if (q.y > 0 && (mode == kModePrefill || q.z > 0)) break;
                     } while (true);
                 }
             }

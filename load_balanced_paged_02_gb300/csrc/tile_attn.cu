@@ -946,61 +946,72 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             const float lse = l > 0.f || l != l ? (m == kNegInf ? 0.f : m) * kLn2 + logf(l) : kNegInf;
             const bool direct = p.mode == kModePrefill && it.whole;
-            const int tok0 = it.i * T + half_tok;              // the half's first token in the sequence
-            const int live = min(it.n - tok0, kHalfTokens) * kGroup;  // the half's rows that exist
-            const long long orow0 = (long long)(it.q0 + tok0) * p.num_q_heads + it.h * kGroup;
-            const long long prow0 = tile_slot(p.mode, worker, it) * (T * kGroup) + half_tok * kGroup;
-            // 64 bytes of every row at a time, through shared memory: a warp then writes
-            // eight rows' 64 bytes at once (row r = token r / 8, query head r % 8)
-            const int wr = 32 * (warp & 3) + lane / 4;  // + 8 i
+            const int tok0 = it.i * T + half_tok;        // the half's first token in the sequence
+            const int wtok = 4 * (warp & 3);             // the warp's first token in the half
+            const int live = it.n - tok0 - wtok;         // the warp's tokens that exist
+            // Rows go out 64 bytes at a time, through shared memory: the warp then writes 64
+            // bytes of one token's eight rows at once (lane / 4: query head, lane % 4: 16-byte
+            // piece), its four tokens one after the other.
+            const int sw = (lane >> 1) & 3, hd = lane >> 2;
+            uint4* const put = reinterpret_cast<uint4*>(stage + lane * 64);
+            const uint8_t* const get = stage + hd * 64 + (((lane & 3) ^ ((hd >> 1) & 3)) << 4);
             if (direct) {
+                const long long row0 = (long long)(it.q0 + tok0 + wtok) * p.num_q_heads + it.h * kGroup;
+                const long long step = (long long)p.num_q_heads * kHeadDim;
+                __nv_bfloat16* dst = p.out + (row0 + hd) * kHeadDim + 8 * (lane & 3);
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < 128; c += 32, dst += 32) {
                     float o[32];
                     tmem_ld32(ocol + c, o);
                     tmem_ld_wait();
                     // rows that saw nothing are zero, whatever O holds
+                    if (inv == 0.f) {
 #pragma unroll
-                    for (int u = 0; u < 32; ++u) o[u] = inv == 0.f ? 0.f : o[u] * inv;
+                        for (int u = 0; u < 32; ++u) o[u] = 0.f;
+                    }
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((u ^ (lane >> 1 & 3)) << 4)) =
-                            make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]), pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
-                                       pack_bf16x2(o[8 * u + 4], o[8 * u + 5]), pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
+                        put[u ^ sw] = make_uint4(pack_bf16x2(o[8 * u] * inv, o[8 * u + 1] * inv),
+                                                 pack_bf16x2(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
+                                                 pack_bf16x2(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
+                                                 pack_bf16x2(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
                     __syncwarp();
+                    uint4 v[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int lr = lane / 4 + 8 * i, r = wr + 8 * i;
-                        const uint4 v = *reinterpret_cast<const uint4*>(stage + lr * 64 + (((lane & 3) ^ (lr >> 1 & 3)) << 4));
-                        if (r < live)
-                            *reinterpret_cast<uint4*>(p.out + (orow0 + (long long)(r / kGroup) * p.num_q_heads + r % kGroup) * kHeadDim + c +
-                                                      8 * (lane & 3)) = v;
-                    }
+                    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(get + 512 * i);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < live) *reinterpret_cast<uint4*>(dst + i * step) = v[i];
                     __syncwarp();
                 }
-                if (row < live && p.out_lse) p.out_lse[orow0 + (long long)(row / kGroup) * p.num_q_heads + row % kGroup] = lse;
+                // this thread's own row: token lane / 8 of the warp, query head lane % 8
+                if (p.out_lse && (lane >> 3) < live) p.out_lse[row0 + (long long)(lane >> 3) * p.num_q_heads + (lane & 7)] = lse;
             } else {
+                const long long row0 = tile_slot(p.mode, worker, it) * (T * kGroup) + (half_tok + wtok) * kGroup;
+                float* dst = p.split_o + (row0 + hd) * kHeadDim + 4 * (lane & 3);
 #pragma unroll 1
-                for (int c = 0; c < 128; c += 16) {
+                for (int c = 0; c < 128; c += 16, dst += 16) {
                     float o[16];
                     tmem_ld16(ocol + c, o);
                     tmem_ld_wait();
+                    if (inv == 0.f) {
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) o[u] = inv == 0.f ? 0.f : o[u] * inv;
+                        for (int u = 0; u < 16; ++u) o[u] = 0.f;
+                    }
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        *reinterpret_cast<float4*>(stage + lane * 64 + ((u ^ (lane >> 1 & 3)) << 4)) =
-                            make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                        reinterpret_cast<float4*>(put)[u ^ sw] =
+                            make_float4(o[4 * u] * inv, o[4 * u + 1] * inv, o[4 * u + 2] * inv, o[4 * u + 3] * inv);
                     __syncwarp();
+                    float4 v[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int lr = lane / 4 + 8 * i, r = wr + 8 * i;
-                        const float4 v = *reinterpret_cast<const float4*>(stage + lr * 64 + (((lane & 3) ^ (lr >> 1 & 3)) << 4));
-                        if (r < live) *reinterpret_cast<float4*>(p.split_o + (prow0 + r) * kHeadDim + c + 4 * (lane & 3)) = v;
-                    }
+                    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float4*>(get + 512 * i);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < live) *reinterpret_cast<float4*>(dst + i * kGroup * kHeadDim) = v[i];
                     __syncwarp();
                 }
-                if (row < live) p.split_lse[prow0 + row] = lse;
+                if ((lane >> 3) < live) p.split_lse[row0 + lane] = lse;
             }
             tc_fence_before();
             __syncwarp();

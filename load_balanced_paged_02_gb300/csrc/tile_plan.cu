@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     for (int j = threadIdx.x; j <= C; j += kThreads) {
         const long long g = (long long)j * bucket;
-        int4 a = make_int4(Hkv, 0, 0, 0), b = make_int4(Hkv * (int)tile_base, 0, 0, 0);
+        int4 a = make_int4(Hkv, 0, 0, 0), b = make_int4(0, 0, 0, 0);
         if (g < total) {
             const int h = (int)(g / per_head);
             const long long r = g % per_head;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads)
             }
             const long long blk = u - tile_units(mode, q.y, q.z, i0, T) - tile_cost(mode);
             a = make_int4(h, lo, i0, blk > 0 ? (int)blk : 0);
-            b.x = h * (int)tile_base + q.w + i0;
+            b = q;
         }
         int4* st = reinterpret_cast<int4*>(buf + lay.starts) + 2 * j;
         st[0] = a;

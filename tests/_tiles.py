@@ -164,11 +164,11 @@ def tile_map(mode, q_starts, lens, num_tokens, hkv, workers, min_blocks, T, q_le
     for j in range(workers + 1):
         g = j * bucket
         if g >= total:
-            words += [hkv, 0, 0, 0, hkv * tiles_before, 0, 0, 0]
+            words += [hkv, 0, 0, 0, 0, 0, 0, 0]
         else:
             s, i, blk = walk[g % per_head]
             h = g // per_head
-            words += [h, s, i, max(blk, 0), h * tiles_before + seqs[s][3] + i, 0, 0, 0]
+            words += [h, s, i, max(blk, 0)] + seqs[s]
     for x in seqs:
         words += x
     for u in units_before:
