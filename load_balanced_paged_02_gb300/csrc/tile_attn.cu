@@ -828,11 +828,11 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                 blks += it.b1 - it.b0;
                 continue;
             }
-            // keys this row sees; rows past the sequence's last token (computed, not
-            // written) see no more than the sequence has
-            const int lim = p.mode == kModePrefix
-                                ? it.L
-                                : min(it.L, it.L - it.n + it.i * T + half_tok + row / kGroup + 1);
+            // keys that this row sees, and those that the warp's first row does; rows past the
+            // sequence's last token (computed, not written) see no more than the sequence has
+            const int lim0 = it.L - it.n + it.i * T + half_tok + 4 * (warp & 3) + 1;
+            const int lim_w = p.mode == kModePrefix ? it.L : min(it.L, lim0);
+            const int lim = p.mode == kModePrefix ? it.L : min(it.L, lim0 + lane / kGroup);
             float m = kNegInf, l = 0.f;  // reference maximum (log2 domain) and sum
             float sc = p.scale_log2;
             for (int b = it.b0; b < it.b1; ++b, ++blks, ++ns) {
@@ -846,6 +846,9 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                 tmem_ld32(scol + 32, s + 32);
                 tmem_ld32(scol + 64, s + 64);
                 tmem_ld32(scol + 96, s + 96);
+                // which of the block's keys this row sees, found while the scores arrive
+                const int nv = lim - b * kBlock, pages_ok = meta[blks % kMetaRing];
+                const bool all_seen = lim_w - b * kBlock >= kBlock && pages_ok == 3;
                 tmem_ld_wait();
                 if constexpr (FP8) {
                     // (the scores exist, so the splitter's row scales do too)
@@ -859,8 +862,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                         s[c] = x.x, s[c + 1] = x.y, s[c + 2] = y.x, s[c + 3] = y.y;
                     }
                 }
-                const int nv = lim - b * kBlock, pages_ok = meta[blks % kMetaRing];
-                if (!__all_sync(0xffffffffu, nv >= kBlock && pages_ok == 3)) {
+                if (!all_seen) {
                     const int n0 = (pages_ok & 1) ? min(nv, kChunk) : 0, n1 = (pages_ok & 2) ? nv - kChunk : 0;
 #pragma unroll
                     for (int c = 0; c < kChunk; ++c) {
