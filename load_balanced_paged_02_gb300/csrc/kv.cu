@@ -7,18 +7,20 @@
 // are code x scale in float32, rounded once.
 //
 // Both are streams, bound by HBM for long calls and by launch latency for a decode
-// step's. A block takes a run of tokens (64 at most, fewer while that leaves SMs
+// step's. A block takes a run of tokens (16 at most, fewer while that leaves SMs
 // without blocks) with all their heads of K and V; groups of lanes take one row of
 // 128 elements each, 16 bytes per lane and load, and kUnroll rows are loaded before
-// the first is used.
+// the first is used. Blocks of 16 tokens measured best (96k tokens at 8 heads, e4m3
+// read: 64 tokens 170 us, 32 161 us, 16 156 us).
 #include "kv.cuh"
 
 namespace hpc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
-constexpr int kMaxTokens = 64;     // tokens of a block at most
+constexpr int kUnroll = 4;         // rows that a reading group of lanes loads at once
+constexpr int kWriteRows = 2;      // and a writing one
+constexpr int kMaxTokens = 16;     // tokens of a block at most
 constexpr int kSmemStarts = 1025;  // out_starts kept in shared memory up to this many
 constexpr float kE4m3Max = 448.f;
 
@@ -31,6 +33,12 @@ __device__ __forceinline__ void unpack8(const uint4& r, float (&y)[8]) {
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint2 pack_e4m3x8(const float (&y)[8]) {
     uint32_t c[4];
 #pragma unroll
@@ -39,25 +47,26 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float (&y)[8]) {
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// A half-warp per row (lane k: elements [8 k, 8 k + 8)); row r of the block is token
-// r / (2 Hkv), K heads before V heads.
+// Eight lanes per row (lane k: elements [16 k, 16 k + 16)); row r of the block is
+// token r / (2 Hkv), K heads before V heads. Fewer lanes per row share its index
+// arithmetic, scale and maximum: sixteen took 15.9 us for 8192 tokens at 8 heads.
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteArgs a, int tokens_per_block) {
+    constexpr int kLanes = 8, kGroups = kThreads / kLanes;
     grid_dependency_wait();  // the projection may still be finishing
     grid_launch_dependents();
-    const int hl = threadIdx.x & 15;
-    const unsigned mask = (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
+    const int hl = threadIdx.x % kLanes;
+    const unsigned mask = 0xffu << (threadIdx.x & 24);
     const int t0 = blockIdx.x * tokens_per_block, nt = min(tokens_per_block, a.num_tokens - t0);
     const unsigned per_token = 2u * (unsigned)a.num_kv_heads, rows = (unsigned)nt * per_token;
-    for (unsigned r0 = threadIdx.x >> 4; r0 < rows; r0 += kThreads / 16 * kUnroll) {
-        uint4 raw[kUnroll];
-        int slot[kUnroll], kvh[kUnroll];
+    for (unsigned r0 = threadIdx.x / kLanes; r0 < rows; r0 += kGroups * kWriteRows) {
+        uint4 raw[kWriteRows][2];
+        int slot[kWriteRows], kvh[kWriteRows];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const unsigned r = r0 + u * (kThreads / 16);
+        for (int u = 0; u < kWriteRows; ++u) {
+            const unsigned r = r0 + u * kGroups;
             slot[u] = -1;
             kvh[u] = 0;
-            raw[u] = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows) {
                 const unsigned tl = r / per_token;
                 const int t = t0 + (int)tl;
@@ -66,12 +75,13 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteArgs a,
                 const bool is_v = kvh[u] >= a.num_kv_heads;
                 const __nv_bfloat16* src = is_v ? a.v + t * a.v_stride + (kvh[u] - a.num_kv_heads) * kHeadDim
                                                 : a.k + t * a.k_stride + kvh[u] * kHeadDim;
-                raw[u] = reinterpret_cast<const uint4*>(src)[hl];
+                raw[u][0] = reinterpret_cast<const uint4*>(src)[2 * hl];
+                raw[u][1] = reinterpret_cast<const uint4*>(src)[2 * hl + 1];
             }
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (slot[u] < 0) continue;  // padding (or no row): uniform over the half-warp
+        for (int u = 0; u < kWriteRows; ++u) {
+            if (slot[u] < 0) continue;  // padding (or no row): uniform over the row's lanes
             const int page = slot[u] / kChunk, off = slot[u] % kChunk;
             if (page >= a.num_pages) {
                 if (hl == 0 && a.err) atomicOr(a.err, (int)HPC_DEVERR_PAGE_OUT_OF_RANGE);
@@ -80,31 +90,37 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteArgs a,
             const bool is_v = kvh[u] >= a.num_kv_heads;
             const int h = is_v ? kvh[u] - a.num_kv_heads : kvh[u];
             void* cache = is_v ? a.v_cache : a.k_cache;
-            const long long dst = ((long long)slot[u] * a.num_kv_heads + h) * kHeadDim + 8 * hl;
+            const long long dst = ((long long)slot[u] * a.num_kv_heads + h) * kHeadDim + 16 * hl;
             if constexpr (!FP8) {
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + dst) = raw[u];
+                uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + dst);
+                out[0] = raw[u][0];
+                out[1] = raw[u][1];
             } else {
-                float y[8];
-                unpack8(raw[u], y);
-                float am = 0.f;
+                float y[2][8];
+                unpack8(raw[u][0], y[0]);
+                unpack8(raw[u][1], y[1]);
+                float am = fmaxf(fabsf(y[0][0]), fabsf(y[1][0]));
 #pragma unroll
-                for (int k = 0; k < 8; ++k) am = fmaxf(am, fabsf(y[k]));
+                for (int k = 1; k < 8; ++k) am = max3(am, fabsf(y[0][k]), fabsf(y[1][k]));
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(mask, am, o));
+                for (int o = kLanes / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(mask, am, o));
                 float scale = __fdiv_rn(am, kE4m3Max);
                 if (!(scale > 0.f)) scale = 1.f;
-                // x / scale: a product with the reciprocal and one correction step (the
-                // quotient rounded, but for results near float32's ends, where the codes
-                // do not see the difference)
-                const float inv = __frcp_rn(scale);
-                const bool plain = inv <= 3.0e38f && scale >= 1.2e-38f;
+                // x / scale. A product with the reciprocal and one correction step give the
+                // rounded quotient where scale and reciprocal are ordinary numbers
+                if (scale >= 1e-30f && scale <= 1e30f) {
+                    const float inv = __frcp_rn(scale);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float q = y[k] * inv;
-                    const float c = fmaf(fmaf(-q, scale, y[k]), inv, q);
-                    y[k] = plain && fabsf(q) <= 3.0e38f ? c : __fdiv_rn(y[k], scale);
+                    for (int k = 0; k < 16; ++k) {
+                        const float x = y[k >> 3][k & 7], q = x * inv;
+                        y[k >> 3][k & 7] = fmaf(fmaf(-q, scale, x), inv, q);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) y[k >> 3][k & 7] = __fdiv_rn(y[k >> 3][k & 7], scale);
                 }
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + dst) = pack_e4m3x8(y);
+                const uint2 lo = pack_e4m3x8(y[0]), hi = pack_e4m3x8(y[1]);
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(cache) + dst) = make_uint4(lo.x, lo.y, hi.x, hi.y);
                 if (hl == 0)
                     (is_v ? a.v_scale : a.k_scale)[((long long)page * a.num_kv_heads + h) * kChunk + off] = scale;
             }
@@ -210,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a, i
     }
 }
 
-// Tokens of a block: as many as leave four blocks per SM, at most 64.
+// Tokens of a block: as many as leave four blocks per SM, at most kMaxTokens.
 int tokens_per_block(int tokens) {
     int n = kMaxTokens;
     while (n > 1 && (tokens + n - 1) / n < 152 * 4) n >>= 1;
