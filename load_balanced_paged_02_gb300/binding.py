@@ -482,8 +482,9 @@ def _on_device(what, *tensors):
             raise HpcError(what, detail=f"tensors on {tensors[0].device} and {t.device}")
     if index < 0:
         raise HpcError(what, detail="tensors must be on a CUDA device")
-    if index != torch.cuda.current_device():
-        raise HpcError(what, detail=f"tensors on cuda:{index}, but the current device is cuda:{torch.cuda.current_device()}")
+    current = torch._C._cuda_getDevice()
+    if index != current:
+        raise HpcError(what, detail=f"tensors on cuda:{index}, but the current device is cuda:{current}")
     return index
 
 
@@ -566,32 +567,34 @@ class TilePlan:
         return ctypes.byref(self.struct)
 
 
-_CTAS = {}
+_CTAS = {}  # what each device answered
 
 
 def tile_num_ctas() -> int:
     """hpc_tile_default_num_ctas: one CTA per SM of the current device."""
-    dev = torch.cuda.current_device()
-    n = _CTAS.get(("tile", dev), 0)
-    if n <= 0:
-        n = _CTAS[("tile", dev)] = lib().hpc_tile_default_num_ctas()
+    key = ("tile", torch.cuda.current_device())
+    if key not in _CTAS:
+        n = lib().hpc_tile_default_num_ctas()
         if n <= 0:
             raise HpcError("hpc_tile_default_num_ctas", detail="device query failed")
-    return n
+        _CTAS[key] = n
+    return _CTAS[key]
 
 
 def _decode_num_ctas(kvd):
-    dev = torch.cuda.current_device()
-    n = _CTAS.get((kvd, dev), 0)
-    if n <= 0:
-        n = _CTAS[(kvd, dev)] = default_num_ctas(kvd)
-    return n
+    key = (kvd, torch.cuda.current_device())
+    if key not in _CTAS:
+        _CTAS[key] = default_num_ctas(kvd)
+    return _CTAS[key]
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(stream):
     """Allocations for work on ``stream`` belong to it."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
 
 
@@ -684,18 +687,18 @@ def prefill(q, k_cache, v_cache, page_table, q_starts, seq_lens, k_scale=None, v
     dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, q_starts, seq_lens, out, out_lse, workspace)
     num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
     L = lib()
-    need = L.hpc_prefill_workspace_bytes(B, num_ctas)
-    with _on(stream):
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if out is None:
-            out = torch.empty_like(q)
-        else:
-            _tensor("out", out, q.shape, torch.bfloat16)
-        if out_lse is None:
-            out_lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-        else:
-            _tensor("out_lse", out_lse, (T, Hq), torch.float32)
+    if out is not None:
+        _tensor("out", out, q.shape, torch.bfloat16)
+    if out_lse is not None:
+        _tensor("out_lse", out_lse, (T, Hq), torch.float32)
+    if workspace is None or out is None or out_lse is None:
+        with _on(stream):
+            if workspace is None:
+                workspace = torch.empty(L.hpc_prefill_workspace_bytes(B, num_ctas), dtype=torch.uint8, device=q.device)
+            if out is None:
+                out = torch.empty_like(q)
+            if out_lse is None:
+                out_lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     plan = TilePlan.of_workspace(TilePlanStruct(), workspace)
     rc = L.hpc_prefill(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), kvd, pages,
