@@ -601,8 +601,9 @@ hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens
  *   out_lse    device float32 [num_tokens][num_q_heads] or NULL
  * A row that sees no key gets out = 0 and out_lse = -inf. Scores and sums are
  * float32; probabilities enter the second product as bf16 (f16 with an e4m3
- * cache, where V enters as code x scale rounded to f16: |v| <= 65504, and values
- * under 2^-14 keep multiples of 2^-24). Keys and values of tokens that a row does
+ * cache, where V enters as code x scale rounded to f16: |v| <= 65504, and values,
+ * and probabilities relative to the row's reference, under 2^-14 keep multiples of
+ * 2^-24). Keys and values of tokens that a row does
  * not see never reach it through its maximum and sum; a value of V that is not
  * finite reaches every row of the 128-token blocks that hold its token.
  * A page id outside [0, num_pages) hides its 64 tokens

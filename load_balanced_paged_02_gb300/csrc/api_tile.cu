@@ -27,10 +27,11 @@ bool tokens_ok(int num_tokens, int num_seqs, int num_kv_heads) {
     return num_tokens >= 0 && ((long long)num_tokens / kTileCta + num_seqs) * num_kv_heads < 2147483647LL;
 }
 
-// Tiles of 64 tokens on pairs of CTAs where the sequences fill them, of 32 on
-// single CTAs otherwise.
+// Tiles of 64 tokens on pairs of CTAs from 96 query tokens per sequence on, of 32 on
+// single CTAs below. A pair halves the copies and the shared memory traffic of a
+// row, a single CTA wastes fewer rows on short sequences.
 int auto_tile(int num_tokens, int num_seqs) {
-    return (long long)num_tokens >= 2LL * kTilePair * num_seqs ? kTilePair : kTileCta;
+    return 2LL * num_tokens >= 3LL * kTilePair * num_seqs ? kTilePair : kTileCta;
 }
 
 hpc_status plan_common(const int32_t* d_starts, const int32_t* d_lens, int num_seqs, int num_tokens, int num_kv_heads,

@@ -69,14 +69,14 @@ def make_q(shape, seed, device="cuda", scale=1.0):
 
 def attend(q, k, v, visible):
     """q [n, hq, 128], k / v [t, hkv, 128] in float64; row i sees the first visible[i] tokens. Returns out,
-    lse, the values' weighted mean sizes sum w |v|, and each row's bound on the score's products, the
-    largest sum_d |q_d k_d| / sqrt(128) among the tokens it sees."""
+    lse, the values' weighted mean sizes sum w |v|, each row's bound on the score's products, the
+    largest sum_d |q_d k_d| / sqrt(128) among the tokens it sees, and sum |v| over the tokens it sees."""
     n, hq, _ = q.shape
     t, hkv, _ = k.shape
     if t == 0:
         z = torch.zeros((n, hq, DIM), dtype=torch.float64, device=q.device)
         s = torch.zeros((n, hq), dtype=torch.float64, device=q.device)
-        return z, s - INF, z, s
+        return z, s - INF, z, s, z
     qg = q.double().view(n, hkv, GROUP, DIM)
     s = torch.einsum("nhgd,thd->nhgt", qg, k) / math.sqrt(DIM)
     size = torch.einsum("nhgd,thd->nhgt", qg.abs(), k.abs()) / math.sqrt(DIM)
@@ -87,7 +87,8 @@ def attend(q, k, v, visible):
     w = torch.where(torch.isfinite(lse).unsqueeze(-1), torch.exp(s - torch.where(torch.isfinite(lse), lse, 0.0).unsqueeze(-1)), 0.0)
     out = torch.einsum("nhgt,thd->nhgd", w, v)
     absv = torch.einsum("nhgt,thd->nhgd", w, v.abs())
-    return (out.reshape(n, hq, DIM), lse.reshape(n, hq), absv.reshape(n, hq, DIM), size.reshape(n, hq))
+    seen = torch.einsum("nt,thd->nhd", (~hidden.view(n, t)).double(), v.abs()).repeat_interleave(GROUP, dim=1)
+    return (out.reshape(n, hq, DIM), lse.reshape(n, hq), absv.reshape(n, hq, DIM), size.reshape(n, hq), seen)
 
 
 def check_rows(got, got_lse, ref, fp8, what=""):
@@ -98,15 +99,17 @@ def check_rows(got, got_lse, ref, fp8, what=""):
     the row's largest element per product: less than es, counted by doubling it. exp2 and the sums add 2^-20.
     So a probability is off by 2 es + 2^-20 relative to the row's sum. Probabilities enter the second
     product rounded to bf16 (2^-8), or to f16 (2^-11) with V rounded to f16 twice (scale and product,
-    2^-11 each, and 2^-25 per element for results under f16's normal range). The output is rounded to bf16
-    (2^-8)."""
-    out, lse, absv, size = ref
+    2^-11 each, and 2^-25 per element for results under f16's normal range). A probability below 2^-14 of
+    the reference is under f16's normal range too: off by at most 2^-25 whatever its size, so a token adds
+    2^-25 |v| / l, and l >= 1, for the key that set the reference counts as 1. The output is rounded to
+    bf16 (2^-8)."""
+    out, lse, absv, size, seen = ref
     assert torch.equal(torch.isfinite(lse), torch.isfinite(got_lse)), f"{what}: rows that see nothing differ"
     assert torch.isfinite(got.float()).all(), f"{what}: non-finite outputs"
     es = (2 if fp8 else 1) * 128 * 2.0 ** -23 * size
     p_err = 2 * es.unsqueeze(-1) + 2.0 ** -20
     prod = 3 * 2.0 ** -11 if fp8 else 2.0 ** -8
-    tol = (p_err + prod) * absv * 1.01 + (2.0 ** -24 if fp8 else 0.0)
+    tol = (p_err + prod) * absv * 1.01 + (2.0 ** -24 + 2.0 ** -25 * seen if fp8 else 0.0)
     tol = tol + 2.0 ** -8 * (out.abs() + tol) + 1e-30
     err = (got.double() - out).abs()
     worst = (err / tol).max().item() if err.numel() else 0.0
