@@ -35,6 +35,7 @@
 // Every wait is bounded; on expiry the CTA records HPC_DEVERR_WAIT_TIMEOUT.
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "tcgen05.cuh"
@@ -68,8 +69,8 @@ struct Cfg {
     static constexpr int kThreads = kWarps * 32;
     // registers per thread after the split (setmaxnreg): the launch's total, 384 x
     // 168 or 512 x 128, is what the two softmax warpgroups and the others share
-    static constexpr int kRegsSoftmax = FP8 ? 168 : 208;
-    static constexpr int kRegsOther = FP8 ? 88 : 88;
+    static constexpr int kRegsSoftmax = FP8 ? 192 : 208;
+    static constexpr int kRegsOther = FP8 ? 64 : 88;
     static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * (FP8 ? 128 : 168), "register split");
 };
 
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
     uint64_t* sfull = qempty + 2;
     uint64_t* pfull = sfull + 2;
     uint64_t* pvdone = pfull + 4;  // (two P barriers per half: its first 64 keys, its last)
-    uint64_t* ofull = pvdone + 2;  // pvdone: the product with the first 64 is done
+    uint64_t* ofull = pvdone + 2;  // pvdone (bf16): the product with the first 64 is done
     uint64_t* ofree = ofull + 2;
     uint64_t* q8full = ofree + 2;  // e4m3 from here on
     uint64_t* wfull = q8full + 2;
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                             for (int kk = 4 * u; kk < 4 * u + 4; ++kk)
                                 mma_ts_16<CG>(el, tmem + 256 + 128 * t, tmem + 128 * t + kk * 8, v + kk * 128, kIdO,
                                               b > it.b0 || kk > 0);
-                            if (u == 0) mma_commit<CG>(el, &pvdone[t]);
+                            if (!FP8 && u == 0) mma_commit<CG>(el, &pvdone[t]);
                         }
                         if (!ok) break;
                         ++np[t];
@@ -843,78 +844,80 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                // which of the block's keys this row sees
-                const int nv = lim - b * kBlock, nv_w = lim_w - b * kBlock, pages_ok = meta[blks % kMetaRing];
-                // A page's 64 keys at a time: their product with V runs while the softmax works
-                // on the next ones.
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float s[kChunk];
-                    tmem_ld32(scol + kChunk * u, s);
-                    tmem_ld32(scol + kChunk * u + 32, s + 32);
-                    const bool page_ok = (pages_ok >> u) & 1;
+                if constexpr (FP8) {
+                    // Both pages at once: the maximum of all 128 scores is known before any P goes
+                    // out. (Page by page, as below, the first product started sooner and then
+                    // kept the other half's waiting while this half scaled its second page: 304
+                    // in place of 278 us for 128 requests over a 65536-token prefix.)
+                    float s[128];
+                    tmem_ld32(scol, s);
+                    tmem_ld32(scol + 32, s + 32);
+                    tmem_ld32(scol + 64, s + 64);
+                    tmem_ld32(scol + 96, s + 96);
+                    // which of the block's keys this row sees, found while the scores arrive
+                    const int nv = lim - b * kBlock, pages_ok = meta[blks % kMetaRing];
+                    const bool all_seen = lim_w - b * kBlock >= kBlock && pages_ok == 3;
                     tmem_ld_wait();
-                    if constexpr (FP8) {
-                        // (the scores exist, so the splitter's row scales do too)
-                        if (u == 0 && b == it.b0)
-                            sc = p.scale_log2 * reinterpret_cast<const float*>(smem + LY::kQs)[(nd & 1) * 256 + t * 128 + row];
-                        const float4* ks = reinterpret_cast<const float4*>(smem + LY::kKs + (blks % kMetaRing) * 512) + u * 16;
+                    // (the scores exist, so the splitter's row scales do too)
+                    if (b == it.b0) sc = p.scale_log2 * reinterpret_cast<const float*>(smem + LY::kQs)[(nd & 1) * 256 + t * 128 + row];
+                    const float4* ks = reinterpret_cast<const float4*>(smem + LY::kKs + (blks % kMetaRing) * 512);
 #pragma unroll
-                        for (int c = 0; c < kChunk; c += 4) {
-                            const float4 f = ks[c / 4];
-                            const float2 x = mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
-                            const float2 y = mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
-                            s[c] = x.x, s[c + 1] = x.y, s[c + 2] = y.x, s[c + 3] = y.y;
+                    for (int c = 0; c < 128; c += 4) {
+                        const float4 f = ks[c / 4];
+                        const float2 x = mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
+                        const float2 y = mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
+                        s[c] = x.x, s[c + 1] = x.y, s[c + 2] = y.x, s[c + 3] = y.y;
+                    }
+                    if (!all_seen) {
+                        const int n0 = (pages_ok & 1) ? min(nv, kChunk) : 0, n1 = (pages_ok & 2) ? nv - kChunk : 0;
+#pragma unroll
+                        for (int c = 0; c < kChunk; ++c) {
+                            if (c >= n0) s[c] = kNegInf;
+                            if (c >= n1) s[c + kChunk] = kNegInf;
                         }
                     }
-                    if (nv_w < kChunk * (u + 1) || !page_ok) {
-                        const int n = page_ok ? nv - kChunk * u : 0;
-#pragma unroll
-                        for (int c = 0; c < kChunk; ++c)
-                            if (c >= n) s[c] = kNegInf;
-                    }
-                    // P = exp2(s sc - m), to TMEM as 16-bit pairs; returns the sum
-                    auto exps = [&](float neg) {
+                    // P = exp2(s sc - m) of 64 columns, to TMEM as 16-bit pairs; returns their sum
+                    // and, with MAX, takes the maximum of all 128 scores along the way: four per
+                    // pair of exponentials, whose unit has a quarter of the others' rate, so that
+                    // the two run side by side
+                    float mx[8];
+                    auto exps = [&](int c0, float neg, auto max_too) {
+                        constexpr bool kMax = decltype(max_too)::value;
                         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                        for (int c = 0; c < kChunk; c += 32) {
+                        for (int c = c0; c < c0 + 64; c += 32) {
                             uint32_t pk[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float2 x = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), make_float2(sc, sc), make_float2(neg, neg));
+                            for (int u = 0; u < 16; ++u) {
+                                float2 x = fma2(make_float2(s[c + 2 * u], s[c + 2 * u + 1]), make_float2(sc, sc), make_float2(neg, neg));
                                 x.x = fast_exp2(x.x);
+                                if constexpr (kMax) {
+                                    const int i = 2 * (c + 2 * u);
+                                    mx[(i / 2) & 7] = i < 16 ? fmaxf(s[i], s[i + 1]) : max3(mx[(i / 2) & 7], s[i], s[i + 1]);
+                                }
                                 x.y = fast_exp2(x.y);
-                                sum[i & 1] = add2(sum[i & 1], x);
-                                pk[i] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
+                                if constexpr (kMax) {
+                                    const int i = 2 * (c + 2 * u) + 2;
+                                    mx[(i / 2) & 7] = i < 16 ? fmaxf(s[i], s[i + 1]) : max3(mx[(i / 2) & 7], s[i], s[i + 1]);
+                                }
+                                sum[u & 1] = add2(sum[u & 1], x);
+                                pk[u] = pack_f16x2(x.x, x.y);
                             }
-                            tmem_st16(scol + (kChunk * u + c) / 2, pk);
+                            tmem_st16(scol + c / 2, pk);
                         }
                         return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     };
-                    // Against the reference as it stands, while the keys' maximum is found: the
-                    // reference moves only when that is far above it, which after a tile's first
-                    // blocks is rare, and they are then done again.
-                    float sum = exps(m == kNegInf ? 0.f : -m);
-                    float mx[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx[i] = fmaxf(s[i], s[60 + i]);
-#pragma unroll
-                    for (int c = 4; c < 60; c += 8)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[c + i], s[c + 4 + i]);
-                    const float mraw = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
+                    // The first 64 columns against the reference as it stands, while the block's
+                    // maximum is found: the reference moves only when that is far above it, which
+                    // after a tile's first blocks is rare, and they are then done again.
+                    float sum0 = exps(0, m == kNegInf ? 0.f : -m, std::true_type{});
+                    const float mraw = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
                     const bool move = mraw > m + kRescaleLog2 || (m == kNegInf && mraw != kNegInf);
                     if (__any_sync(0xffffffffu, move)) {
                         const bool resc = move && m != kNegInf;
                         if (__any_sync(0xffffffffu, resc)) {
-                            // O holds everything before these keys once their predecessors' product
-                            // is done: the last block's is (it was issued before this block's
-                            // scores), the first page's of this block says so
-                            if (u == 1 && !wait_warp(&pvdone[t], ns & 1, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
+                            // (the product of the block before is done: it was issued before this
+                            // block's scores)
                             const float al = resc ? fast_exp2(m - mraw) : 1.f;
 #pragma unroll 1
                             for (int c = 0; c < 128; c += 32) {
@@ -922,19 +925,105 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                                 tmem_ld32(ocol + c, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= al;
+                                for (int u = 0; u < 32; ++u) o[u] *= al;
                                 tmem_st32(ocol + c, o);
                             }
                             l *= al;
                         }
                         if (move) m = mraw;
-                        sum = exps(m == kNegInf ? 0.f : -m);
+                        sum0 = exps(0, m == kNegInf ? 0.f : -m, std::false_type{});
                     }
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_leader<CG>(&pfull[2 * t + u]);
-                    l += sum;
+                    if (lane == 0) arrive_leader<CG>(&pfull[2 * t]);
+                    const float sum1 = exps(64, m == kNegInf ? 0.f : -m, std::false_type{});
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_leader<CG>(&pfull[2 * t + 1]);
+                    l += sum0 + sum1;
+                } else {
+                    // which of the block's keys this row sees
+                    const int nv = lim - b * kBlock, nv_w = lim_w - b * kBlock, pages_ok = meta[blks % kMetaRing];
+                    // A page's 64 keys at a time: their product with V runs while the softmax works
+                    // on the next ones.
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float s[kChunk];
+                        tmem_ld32(scol + kChunk * u, s);
+                        tmem_ld32(scol + kChunk * u + 32, s + 32);
+                        const bool page_ok = (pages_ok >> u) & 1;
+                        tmem_ld_wait();
+                        if (nv_w < kChunk * (u + 1) || !page_ok) {
+                            const int n = page_ok ? nv - kChunk * u : 0;
+#pragma unroll
+                            for (int c = 0; c < kChunk; ++c)
+                                if (c >= n) s[c] = kNegInf;
+                        }
+                        // P = exp2(s sc - m), to TMEM as 16-bit pairs; returns the sum
+                        auto exps = [&](float neg) {
+                            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                            for (int c = 0; c < kChunk; c += 32) {
+                                uint32_t pk[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    float2 x = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), make_float2(sc, sc), make_float2(neg, neg));
+                                    x.x = fast_exp2(x.x);
+                                    x.y = fast_exp2(x.y);
+                                    sum[i & 1] = add2(sum[i & 1], x);
+                                    pk[i] = pack_bf16x2(x.x, x.y);
+                                }
+                                tmem_st16(scol + (kChunk * u + c) / 2, pk);
+                            }
+                            return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                        };
+                        // Against the reference as it stands, while the keys' maximum is found: the
+                        // reference moves only when that is far above it, which after a tile's first
+                        // blocks is rare, and they are then done again.
+                        float sum = exps(m == kNegInf ? 0.f : -m);
+                        float mx[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(s[i], s[60 + i]);
+#pragma unroll
+                        for (int c = 4; c < 60; c += 8)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[c + i], s[c + 4 + i]);
+                        const float mraw = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
+                        const bool move = mraw > m + kRescaleLog2 || (m == kNegInf && mraw != kNegInf);
+                        if (__any_sync(0xffffffffu, move)) {
+                            const bool resc = move && m != kNegInf;
+                            if (__any_sync(0xffffffffu, resc)) {
+                                // O holds everything before these keys once their predecessors' product
+                                // is done: the last block's is (it was issued before this block's
+                                // scores), the first page's of this block says so
+                                if (u == 1 && !wait_warp(&pvdone[t], ns & 1, abort_flag)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                                const float al = resc ? fast_exp2(m - mraw) : 1.f;
+#pragma unroll 1
+                                for (int c = 0; c < 128; c += 32) {
+                                    float o[32];
+                                    tmem_ld32(ocol + c, o);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] *= al;
+                                    tmem_st32(ocol + c, o);
+                                }
+                                l *= al;
+                            }
+                            if (move) m = mraw;
+                            sum = exps(m == kNegInf ? 0.f : -m);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_leader<CG>(&pfull[2 * t + u]);
+                        l += sum;
+                    }
                 }
                 if (!ok) break;
             }
