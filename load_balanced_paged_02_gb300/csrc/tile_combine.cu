@@ -119,8 +119,9 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16* out, float* out_lse, l
 }
 static_assert(kRows * kBatch == 32 && kGroup % kRows == 0, "a warp's lanes; rows of one token");
 
+template <int T>
 __global__ void __launch_bounds__(kWarps * 32)
-    prefill_combine_kernel(const int32_t* plan, long long seqs_off, long long units_off, int Hq, int T,
+    prefill_combine_kernel(const int32_t* plan, long long seqs_off, long long units_off, int Hq,
                            const float* split_o, const float* split_lse, __nv_bfloat16* out, float* out_lse) {
     grid_dependency_wait();  // the pieces come from the attention kernel
     grid_launch_dependents();
@@ -151,8 +152,9 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
 }
 
+template <int T>
 __global__ void __launch_bounds__(kWarps * 32)
-    prefix_combine_kernel(const int32_t* prefix_plan, long long seqs_off, long long units_off, int S, int T,
+    prefix_combine_kernel(const int32_t* prefix_plan, long long seqs_off, long long units_off, int S,
                           const float* prefix_o, const float* prefix_lse, const int32_t* pair_nsplit,
                           const int32_t* pair_split0, const float* split_o, const float* split_lse, __nv_bfloat16* out,
                           float* out_lse, int B, int Hq, int Q) {
@@ -199,8 +201,8 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 cudaError_t launch_prefill_combine(const int32_t* plan, int S, int Hq, int C, int T, const float* split_o,
                                    const float* split_lse, void* out, float* out_lse, cudaStream_t s) {
-    return launch_pdl(prefill_combine_kernel, dim3(C, kParts), dim3(kWarps * 32), 0, s, plan, tile_layout(S, C).seqs,
-                      tile_layout(S, C).units, Hq, T, split_o, split_lse, static_cast<__nv_bfloat16*>(out), out_lse);
+    return launch_pdl(T == kTilePair ? prefill_combine_kernel<kTilePair> : prefill_combine_kernel<kTileCta>, dim3(C, kParts), dim3(kWarps * 32), 0, s, plan, tile_layout(S, C).seqs,
+                      tile_layout(S, C).units, Hq, split_o, split_lse, static_cast<__nv_bfloat16*>(out), out_lse);
 }
 
 cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_workers, int T, const float* prefix_o,
@@ -210,8 +212,8 @@ cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_
     const TileLayout t = tile_layout(S, prefix_workers);
     const PlanLayout L = plan_layout(B, Hkv, ctas);
     const long long blocks = ((long long)B * q_len * Hq / kRows + kWarps - 1) / kWarps;
-    return launch_pdl(prefix_combine_kernel, dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, prefix_plan, t.seqs, t.units,
-                      S, T, prefix_o, prefix_lse, plan + L.pair_nsplit, plan + L.pair_split0, split_o, split_lse, out, out_lse,
+    return launch_pdl(T == kTilePair ? prefix_combine_kernel<kTilePair> : prefix_combine_kernel<kTileCta>, dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, prefix_plan, t.seqs, t.units,
+                      S, prefix_o, prefix_lse, plan + L.pair_nsplit, plan + L.pair_split0, split_o, split_lse, out, out_lse,
                       B, Hq, q_len);
 }
 

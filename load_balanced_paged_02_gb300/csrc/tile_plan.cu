@@ -12,37 +12,47 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 
-// Exclusive scan over the block; *total receives the sum. All threads call it.
-__device__ long long scan_exclusive(long long v, long long* total, long long* warp_sums) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// Exclusive scans of two values over the block; the totals receive the sums. All
+// threads call it.
+__device__ __forceinline__ void scan_exclusive(long long& v, int& w, long long& v_total, int& w_total, long long* v_sums,
+                                               int* w_sums) {
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     long long x = v;
+    int y = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const long long a = __shfl_up_sync(0xffffffffu, x, o);
+        const int b = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) x += a, y += b;
     }
-    if (lane == 31) warp_sums[w] = x;
+    if (lane == 31) v_sums[wp] = x, w_sums[wp] = y;
     __syncthreads();
-    if (w == 0) {
-        long long y = warp_sums[lane];
+    if (wp == 0) {
+        long long c = v_sums[lane];
+        int d = w_sums[lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
+            const long long a = __shfl_up_sync(0xffffffffu, c, o);
+            const int b = __shfl_up_sync(0xffffffffu, d, o);
+            if (lane >= o) c += a, d += b;
         }
-        warp_sums[lane] = y;
+        v_sums[lane] = c, w_sums[lane] = d;
     }
     __syncthreads();
-    const long long before = w > 0 ? warp_sums[w - 1] : 0;
-    *total = warp_sums[kWarps - 1];
+    v = x - v + (wp > 0 ? v_sums[wp - 1] : 0);
+    w = y - w + (wp > 0 ? w_sums[wp - 1] : 0);
+    v_total = v_sums[kWarps - 1];
+    w_total = w_sums[kWarps - 1];
     __syncthreads();
-    return before + x - v;
 }
 
+// T is a constant here, so that the closed forms of tile_units divide by shifts.
+template <int T>
 __global__ void __launch_bounds__(kThreads)
     tile_plan_kernel(const int32_t* q_starts, const int32_t* lens, int S, int num_tokens,
-                     int Hkv, int C, int min_blocks, int max_len, int mode, int q_len, int T, int32_t* buf) {
-    __shared__ long long sums[kWarps];
+                     int Hkv, int C, int min_blocks, int max_len, int mode, int q_len, int32_t* buf) {
+    __shared__ long long unit_sums[kWarps];
+    __shared__ int tile_sums[kWarps];
     __shared__ int err_sh;
     grid_dependency_wait();  // the lengths may come from the kernel before
     grid_launch_dependents();
@@ -51,7 +61,8 @@ __global__ void __launch_bounds__(kThreads)
     long long* units = reinterpret_cast<long long*>(buf + lay.units);
     if (threadIdx.x == 0) err_sh = 0;
     __syncthreads();
-    long long unit_base = 0, tile_base = 0;
+    long long unit_base = 0;
+    int tile_base = 0;
     int err = 0;
     for (int s0 = 0; s0 < S; s0 += kThreads) {
         const int s = s0 + threadIdx.x;
@@ -76,13 +87,12 @@ __global__ void __launch_bounds__(kThreads)
         }
         const bool any = n > 0 && (mode == kModePrefill || L > 0);
         const int tiles = any ? tile_count(n, T) : 0;
-        const long long u = any ? tile_units(mode, n, L, tiles, T) : 0;
-        long long u_total, t_total;
-        const long long ub = unit_base + scan_exclusive(u, &u_total, sums);
-        const long long tb = tile_base + scan_exclusive(tiles, &t_total, sums);
+        long long u = any ? tile_units(mode, n, L, tiles, T) : 0, u_total;
+        int t = tiles, t_total;
+        scan_exclusive(u, t, u_total, t_total, unit_sums, tile_sums);
         if (s < S) {
-            seqs[s] = make_int4(q0, n, L, (int)tb);
-            units[s] = ub;
+            seqs[s] = make_int4(q0, n, L, tile_base + t);
+            units[s] = unit_base + u;
         }
         unit_base += u_total;
         tile_base += t_total;
@@ -108,7 +118,7 @@ __global__ void __launch_bounds__(kThreads)
             case kTNumWorkers: v = C; break;
             case kTNumTokens: v = num_tokens; break;
             case kTMode: v = mode; break;
-            case kTTilesPerHead: v = (int)tile_base; break;
+            case kTTilesPerHead: v = tile_base; break;
             case kTQLen: v = q_len; break;
             case kTError: v = err_sh; break;
             case kTTileTokens: v = T; break;
@@ -120,7 +130,7 @@ __global__ void __launch_bounds__(kThreads)
         int4 a = make_int4(Hkv, 0, 0, 0), b = make_int4(0, 0, 0, 0);
         if (g < total) {
             const int h = (int)(g / per_head);
-            const long long r = g % per_head;
+            const long long r = g - h * per_head;
             int lo = 0, hi = S;  // the last sequence with units[s] <= r
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -153,8 +163,8 @@ __global__ void __launch_bounds__(kThreads)
 
 cudaError_t launch_tile_plan(const int32_t* q_starts, const int32_t* lens, int S, int num_tokens, int Hkv, int C,
                              int min_blocks, int max_len, int mode, int q_len, int T, int32_t* buf, cudaStream_t s) {
-    return launch_pdl(tile_plan_kernel, dim3(1), dim3(kThreads), 0, s, q_starts, lens, S, num_tokens, Hkv, C, min_blocks,
-                      max_len, mode, q_len, T, buf);
+    return launch_pdl(T == kTilePair ? tile_plan_kernel<kTilePair> : tile_plan_kernel<kTileCta>, dim3(1), dim3(kThreads), 0, s,
+                      q_starts, lens, S, num_tokens, Hkv, C, min_blocks, max_len, mode, q_len, buf);
 }
 
 }  // namespace hpc
