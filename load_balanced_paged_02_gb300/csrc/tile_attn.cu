@@ -35,7 +35,6 @@
 // Every wait is bounded; on expiry the CTA records HPC_DEVERR_WAIT_TIMEOUT.
 #include <atomic>
 #include <cstring>
-#include <type_traits>
 
 #include "attn_common.cuh"
 #include "tcgen05.cuh"
@@ -52,7 +51,8 @@ using attn::wait_bounded;
 
 constexpr int kHalfRows = 128;
 constexpr int kQBytes = 32768;           // a half's query rows: [2 dim halves][128 rows][128 B]
-constexpr float kRescaleLog2 = 8.0f;     // lazy rescale threshold: P <= 2^8
+constexpr float kRescaleLog2 = 4.0f;     // the reference moves when a maximum is 2^4 above it,
+constexpr float kSumLimit = 1024.f;      // which is looked at when 64 keys' P add up to more than this
 constexpr int kMetaRing = 8;             // blocks whose page checks (and, e4m3, scales) are kept
 constexpr int kWide = 2;                 // e4m3: f16 V tiles
 constexpr int kOutBytes = 2048;          // a softmax warp's staging of 32 output rows x 64 B
@@ -62,15 +62,15 @@ template <bool FP8, int CG>
 struct Cfg {
     static constexpr int kStageBytes = (FP8 ? 16384 : 32768) / CG;  // 128 tokens of K or of V, or this CTA's half
     static constexpr int kWideBytes = 32768 / CG;
-    // an even number: a stage serves K always, or V always
-    static constexpr int kStages = 4 * CG;
-    static_assert(kStages % 2 == 0 && kStages <= kMetaRing, "stages");
+    static constexpr int kSlots = 2 * CG;  // blocks in the ring: a K stage and a V stage each
+    static constexpr int kStages = 2 * kSlots;
+    static_assert(kSlots <= kMetaRing, "slots");
     static constexpr int kWarps = FP8 ? 16 : 12;
     static constexpr int kThreads = kWarps * 32;
     // registers per thread after the split (setmaxnreg): the launch's total, 384 x
     // 168 or 512 x 128, is what the two softmax warpgroups and the others share
-    static constexpr int kRegsSoftmax = FP8 ? 192 : 208;
-    static constexpr int kRegsOther = FP8 ? 64 : 88;
+    static constexpr int kRegsSoftmax = FP8 ? 168 : 208;
+    static constexpr int kRegsOther = 88;
     static_assert(256 * kRegsSoftmax + (kThreads - 256) * kRegsOther <= kThreads * (FP8 ? 128 : 168), "register split");
 };
 
@@ -86,9 +86,9 @@ struct Smem {
     static constexpr size_t kQs = kVs + (FP8 ? kMetaRing * 512 : 0);           // float [2 parities][2 halves][128]
     static constexpr size_t kMeta = kQs + (FP8 ? 2048 : 0);
     static constexpr size_t kBars = kMeta + kMetaRing * 4;
-    // full, empty, rfull (stages); qfull, rqfull, qempty, sfull, pfull (2), pvdone,
-    // ofull, ofree (halves); e4m3: q8full (halves), wfull, wempty (wide tiles)
-    static constexpr int kNumBars = 3 * C::kStages + 18 + (FP8 ? 2 + 2 * kWide : 0);
+    // full (slots), empty (stages); qfull, qempty, sfull, pfull (2), pvdone, ofull,
+    // ofree (halves); e4m3: q8full (halves), wfull, wempty (wide tiles)
+    static constexpr int kNumBars = 3 * C::kSlots + 16 + (FP8 ? 2 + 2 * kWide : 0);
     static constexpr size_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr size_t kFlag = kTmemSlot + 8;
     static constexpr size_t kAlloc = kFlag + 8 + 1024;
@@ -98,8 +98,10 @@ struct Smem {
 
 // ------------------------------------------------------------------ waits and arrivals
 
-// A whole warp waits; one answer for all its lanes.
+// A whole warp waits; one answer for all its lanes. (The issuer meets most of its
+// barriers ready: a test and a vote are all that it then pays.)
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, kWaitLimitNs));
 }
 
@@ -468,21 +470,19 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                      const __grid_constant__ CUtensorMap tm_vs, const TileParams p) {
     using C = Cfg<FP8, CG>;
     using LY = Smem<FP8, CG>;
-    constexpr int NS = C::kStages;
+    constexpr int NB = C::kSlots;
     constexpr int T = kTileCta * CG;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem =
         reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + LY::kBars);
-    uint64_t* empty = full + NS;
-    uint64_t* rfull = empty + NS;  // leader of a pair: the other CTA's stage is filled
-    uint64_t* qfull = rfull + NS;
-    uint64_t* rqfull = qfull + 2;  // leader of a pair: the other CTA's query rows
-    uint64_t* qempty = rqfull + 2;
+    uint64_t* empty = full + NB;   // K and V stage of slot i at 2 i and 2 i + 1
+    uint64_t* qfull = empty + 2 * NB;
+    uint64_t* qempty = qfull + 2;
     uint64_t* sfull = qempty + 2;
     uint64_t* pfull = sfull + 2;
     uint64_t* pvdone = pfull + 4;  // (two P barriers per half: its first 64 keys, its last)
-    uint64_t* ofull = pvdone + 2;  // pvdone (bf16): the product with the first 64 is done
+    uint64_t* ofull = pvdone + 2;  // pvdone: the product with the first 64 is done
     uint64_t* ofree = ofull + 2;
     uint64_t* q8full = ofree + 2;  // e4m3 from here on
     uint64_t* wfull = q8full + 2;
@@ -496,14 +496,15 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0, worker = (int)blockIdx.x / CG;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
-            mbar_init(&rfull[i], 1);
+        // the leader of a pair is also told when the other CTA's copies have landed
+        const int told = CG == 2 && rank == 0 ? 2 : 1;
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(&full[i], told);
+            mbar_init(&empty[2 * i], 1);
+            mbar_init(&empty[2 * i + 1], 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&qfull[t], 1);
-            mbar_init(&rqfull[t], 1);
+            mbar_init(&qfull[t], FP8 ? 1 : told);
             mbar_init(&qempty[t], 1);
             mbar_init(&sfull[t], 1);
             mbar_init(&pfull[2 * t], 4 * CG);  // one arrival per softmax warp
@@ -554,8 +555,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
         reg_dec<C::kRegsOther>();
         if (warp == 8) {
             // ============================ producer
-            uint32_t kv = 0;    // stages filled
-            uint32_t blks = 0;  // blocks
+            uint32_t blks = 0, started = 0;  // blocks filled, and begun
             int nd[2] = {0, 0};
             while (ok && walk.next(it)) {
                 if (lane == 0) {
@@ -592,50 +592,52 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                         const int pg0 = __shfl_sync(0xffffffffu, page, 2 * b);
                         const int pg1 = __shfl_sync(0xffffffffu, page, 2 * b + 1);
                         if (lane == 0) {
-                            for (int kvi = 0; kvi < 2 && ok; ++kvi, ++kv) {
-                                const uint32_t st = kv % NS;
-                                ok = wait_bounded(&empty[st], ((kv / NS) & 1) ^ 1, abort_flag, kWaitLimitNs);
+                            const uint32_t slot = blks % NB;
+                            for (int kvi = 0; kvi < 2 && ok; ++kvi) {
+                                ok = wait_bounded(&empty[2 * slot + kvi], ((blks / NB) & 1) ^ 1, abort_flag, kWaitLimitNs);
                                 if (!ok) break;
-                                if (kvi == 0) meta[blks % kMetaRing] = (pg0 < p.num_pages ? 1 : 0) | (pg1 < p.num_pages ? 2 : 0);
+                                if (kvi == 0) {
+                                    meta[blks % kMetaRing] = (pg0 < p.num_pages ? 1 : 0) | (pg1 < p.num_pages ? 2 : 0);
+                                    mbar_arrive_expect_tx(&full[slot], 2 * (C::kStageBytes + (FP8 ? kBlock * 4 : 0)));
+                                    started = blks + 1;
+                                }
                                 const CUtensorMap* tm = kvi == 0 ? &tm_k : &tm_v;
-                                uint8_t* dst = ring + (size_t)st * C::kStageBytes;
-                                mbar_arrive_expect_tx(&full[st], C::kStageBytes + (FP8 ? kBlock * 4 : 0));
+                                uint8_t* dst = ring + (size_t)(2 * slot + kvi) * C::kStageBytes;
                                 if constexpr (FP8) {
                                     float* sc = reinterpret_cast<float*>(smem + (kvi == 0 ? LY::kKs : LY::kVs)) +
                                                 (blks % kMetaRing) * kBlock;
                                     const CUtensorMap* ts = kvi == 0 ? &tm_ks : &tm_vs;
-                                    tma_load_2d_plain(sc, ts, &full[st], 0, pg0 * p.num_kv_heads + it.h);
-                                    tma_load_2d_plain(sc + kChunk, ts, &full[st], 0, pg1 * p.num_kv_heads + it.h);
+                                    tma_load_2d_plain(sc, ts, &full[slot], 0, pg0 * p.num_kv_heads + it.h);
+                                    tma_load_2d_plain(sc + kChunk, ts, &full[slot], 0, pg1 * p.num_kv_heads + it.h);
                                 }
                                 if constexpr (CG == 2) {
                                     // K: this CTA's page, both dim halves; V: both pages, this CTA's dim half
                                     if (kvi == 0) {
                                         const int tok = (rank ? pg1 : pg0) * kChunk;
-                                        tma_load_3d_plain(dst, tm, &full[st], 0, it.h, tok);
-                                        if constexpr (!FP8) tma_load_3d_plain(dst + 8192, tm, &full[st], 64, it.h, tok);
+                                        tma_load_3d_plain(dst, tm, &full[slot], 0, it.h, tok);
+                                        if constexpr (!FP8) tma_load_3d_plain(dst + 8192, tm, &full[slot], 64, it.h, tok);
                                     } else {
-                                        tma_load_3d_plain(dst, tm, &full[st], 64 * rank, it.h, pg0 * kChunk);
-                                        tma_load_3d_plain(dst + (FP8 ? 4096 : 8192), tm, &full[st], 64 * rank, it.h, pg1 * kChunk);
+                                        tma_load_3d_plain(dst, tm, &full[slot], 64 * rank, it.h, pg0 * kChunk);
+                                        tma_load_3d_plain(dst + (FP8 ? 4096 : 8192), tm, &full[slot], 64 * rank, it.h, pg1 * kChunk);
                                     }
                                 } else {
-                                    tma_load_3d_plain(dst, tm, &full[st], 0, it.h, pg0 * kChunk);
-                                    tma_load_3d_plain(dst + 8192, tm, &full[st], 0, it.h, pg1 * kChunk);
+                                    tma_load_3d_plain(dst, tm, &full[slot], 0, it.h, pg0 * kChunk);
+                                    tma_load_3d_plain(dst + 8192, tm, &full[slot], 0, it.h, pg1 * kChunk);
                                     if constexpr (!FP8) {
-                                        tma_load_3d_plain(dst + 16384, tm, &full[st], 64, it.h, pg0 * kChunk);
-                                        tma_load_3d_plain(dst + 24576, tm, &full[st], 64, it.h, pg1 * kChunk);
+                                        tma_load_3d_plain(dst + 16384, tm, &full[slot], 64, it.h, pg0 * kChunk);
+                                        tma_load_3d_plain(dst + 24576, tm, &full[slot], 64, it.h, pg1 * kChunk);
                                     }
                                 }
                             }
                         }
                         ok = __shfl_sync(0xffffffffu, ok, 0);
-                        kv = __shfl_sync(0xffffffffu, kv, 0);
                     }
                 }
             }
             // no copy is in flight when the CTA ends, whichever way the walk ended
             if (lane == 0) {
-                for (uint32_t k = kv > (uint32_t)NS ? kv - NS : 0u; k < kv; ++k)
-                    wait_bounded(&full[k % NS], (k / NS) & 1, nullptr, kDrainLimitNs);
+                for (uint32_t k = started > (uint32_t)NB ? started - NB : 0u; k < started; ++k)
+                    wait_bounded(&full[k % NB], (k / NB) & 1, nullptr, kDrainLimitNs);
                 for (int t = 0; t < 2; ++t)
                     if (nd[t] > 0) wait_bounded(&qfull[t], (nd[t] - 1) & 1, nullptr, kDrainLimitNs);
             }
@@ -644,23 +646,19 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
             constexpr uint32_t kIdS = FP8 ? idesc_e4m3(CG * kHalfRows, kBlock) : idesc_16bit(false, CG * kHalfRows, kBlock, 0);
             constexpr uint32_t kIdO = idesc_16bit(FP8, CG * kHalfRows, kHeadDim, 1);
             constexpr uint32_t kKHalf = 16384 / CG;  // bytes of a K tile's dim half
-            uint32_t kv = 0;            // stages taken
-            uint32_t blks = 0;          // V blocks taken
+            uint32_t blks = 0;          // blocks
             uint32_t np[2] = {0, 0};    // P tiles taken
             int nd[2] = {0, 0};         // items
-            // stage number kv filled (in both CTAs)
-            auto wait_stage = [&](uint32_t k) {
-                return wait_warp(&full[k % NS], (k / NS) & 1, abort_flag) &&
-                       (CG == 1 || wait_warp(&rfull[k % NS], (k / NS) & 1, abort_flag));
-            };
+            // block number k is filled (in both CTAs)
+            auto wait_block = [&](uint32_t k) { return wait_warp(&full[k % NB], (k / NB) & 1, abort_flag); };
             const uint32_t el = elect_one();
             // descriptors of the first query tile, stage and V tile; the others lie at
             // fixed distances (in 16-byte units, the low bits of a descriptor)
             const uint64_t dq = sdesc_sw128(smem_u32(qbuf), 16, 1024), dk = sdesc_sw128(smem_u32(ring), 16, 1024);
             const uint64_t dv = sdesc_sw128(smem_u32(FP8 ? smem + LY::kWideV : ring), 16384, 1024);
-            // S of half t from the K tile in stage st
-            auto issue_s = [&](int t, uint32_t st) {
-                const uint64_t q = dq + (uint32_t)t * (kQBytes >> 4), k = dk + st * (C::kStageBytes >> 4);
+            // S of half t from the K tile in slot sl
+            auto issue_s = [&](int t, uint32_t sl) {
+                const uint64_t q = dq + (uint32_t)t * (kQBytes >> 4), k = dk + sl * (2 * C::kStageBytes >> 4);
                 if constexpr (FP8) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
@@ -678,31 +676,27 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
             while (ok && walk.next(it)) {
                 const int halves = it.n - it.i * T > kHalfTokens * CG ? 2 : 1;
                 // first S of both halves
-                ok = wait_stage(kv);
+                ok = wait_block(blks);
                 for (int t = 0; t < halves && ok; ++t) {
-                    ok = wait_warp(FP8 ? &q8full[t] : &qfull[t], nd[t] & 1, abort_flag) &&
-                         (FP8 || CG == 1 || wait_warp(&rqfull[t], nd[t] & 1, abort_flag));
+                    ok = wait_warp(FP8 ? &q8full[t] : &qfull[t], nd[t] & 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_s(t, kv % NS);
+                    issue_s(t, blks % NB);
                     if (it.b1 - it.b0 == 1) mma_commit<CG>(el, &qempty[t]);
-                    if (t == halves - 1) mma_commit<CG>(el, &empty[kv % NS]);
+                    if (t == halves - 1) mma_commit<CG>(el, &empty[2 * (blks % NB)]);
                 }
-                ++kv;
                 for (int b = it.b0; b < it.b1 && ok; ++b, ++blks) {
-                    const uint32_t vst = kv % NS;
+                    const uint32_t vst = 2 * (blks % NB) + 1, next = (blks + 1) % NB;
                     const bool more = b + 1 < it.b1;
                     uint8_t* vt = FP8 ? smem + LY::kWideV + (blks % kWide) * C::kWideBytes : ring + (size_t)vst * C::kStageBytes;
                     const uint64_t v = dv + (FP8 ? (blks % kWide) * (C::kWideBytes >> 4) : vst * (C::kStageBytes >> 4));
                     if constexpr (FP8) {
                         ok = wait_warp(&wfull[blks % kWide], (blks / kWide) & 1, abort_flag);
+                        if (!ok) break;
                     } else {
-                        ok = wait_stage(kv);
                         const int nv = it.L - b * kBlock;
-                        if (ok && nv < kBlock && (nv & (kChunk - 1)) != 0) zero_tail<CG>(vt, nv, lane);
+                        if (nv < kBlock && (nv & (kChunk - 1)) != 0) zero_tail<CG>(vt, nv, lane);
                     }
-                    if (!ok) break;
-                    ++kv;
                     for (int t = 0; t < halves && ok; ++t) {
                         // the first product of an item overwrites O: the item before must have left it
                         if (b == it.b0 && nd[t] > 0) ok = wait_warp(&ofree[t], (nd[t] - 1) & 1, abort_flag);
@@ -717,53 +711,48 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                             for (int kk = 4 * u; kk < 4 * u + 4; ++kk)
                                 mma_ts_16<CG>(el, tmem + 256 + 128 * t, tmem + 128 * t + kk * 8, v + kk * 128, kIdO,
                                               b > it.b0 || kk > 0);
-                            if (!FP8 && u == 0) mma_commit<CG>(el, &pvdone[t]);
+                            if (u == 0) mma_commit<CG>(el, &pvdone[t]);
                         }
                         if (!ok) break;
                         ++np[t];
                         if (t == halves - 1) mma_commit<CG>(el, FP8 ? &wempty[blks % kWide] : &empty[vst]);
                         if (more) {
                             if (t == 0) {
-                                ok = wait_stage(kv);
+                                ok = wait_block(blks + 1);
                                 if (!ok) break;
                                 tc_fence_after();
                             }
-                            issue_s(t, kv % NS);
+                            issue_s(t, next);
                             if (b + 2 == it.b1) mma_commit<CG>(el, &qempty[t]);
-                            if (t == halves - 1) mma_commit<CG>(el, &empty[kv % NS]);
+                            if (t == halves - 1) mma_commit<CG>(el, &empty[2 * next]);
                         } else {
                             mma_commit<CG>(el, &ofull[t]);
                         }
                     }
-                    if (more) ++kv;
                 }
                 for (int t = 0; t < halves; ++t) ++nd[t];
             }
         } else if (warp == 9) {
             // ============================ the other CTA of a pair: its filled query rows and
-            // stages, told to the leader in order
-            uint32_t kv = 0;
+            // slots, told to the leader in order
+            uint32_t blks = 0;
             int nd[2] = {0, 0};
-            auto relay = [&](uint64_t* bar, uint32_t parity, uint64_t* to) {
-                ok = ok && wait_warp(bar, parity, abort_flag);
-                if (ok && lane == 0) arrive_leader<CG>(to);
-            };
             while (ok && walk.next(it)) {
                 const int halves = it.n - it.i * T > kHalfTokens * CG ? 2 : 1;
                 if constexpr (!FP8)
-                    for (int t = 0; t < halves; ++t, ++nd[t - 1]) relay(&qfull[t], nd[t] & 1, &rqfull[t]);
-                for (int b = it.b0; b < it.b1 && ok; ++b) {
-                    relay(&full[kv % NS], (kv / NS) & 1, &rfull[kv % NS]);
-                    ++kv;
+                    for (int t = 0; t < halves && ok; ++t, ++nd[t - 1]) {
+                        ok = wait_warp(&qfull[t], nd[t] & 1, abort_flag);
+                        if (ok && lane == 0) arrive_leader<CG>(&qfull[t]);
+                    }
+                for (int b = it.b0; b < it.b1 && ok; ++b, ++blks) {
+                    ok = wait_warp(&full[blks % NB], (blks / NB) & 1, abort_flag);
+                    if (!ok) break;
                     if constexpr (!FP8) {
                         const int nv = it.L - b * kBlock;
-                        if (nv < kBlock && (nv & (kChunk - 1)) != 0) {
-                            ok = ok && wait_warp(&full[kv % NS], (kv / NS) & 1, abort_flag);
-                            if (ok) zero_tail<CG>(ring + (size_t)(kv % NS) * C::kStageBytes, nv, lane);
-                        }
-                        relay(&full[kv % NS], (kv / NS) & 1, &rfull[kv % NS]);
+                        if (nv < kBlock && (nv & (kChunk - 1)) != 0)
+                            zero_tail<CG>(ring + (size_t)(2 * (blks % NB) + 1) * C::kStageBytes, nv, lane);
                     }
-                    ++kv;
+                    if (lane == 0) arrive_leader<CG>(&full[blks % NB]);
                 }
             }
         }
@@ -793,9 +782,9 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                 // (a warp that gave up must not leave the others at a barrier)
                 ok = !named_any_128(!ok);
                 for (int b = it.b0; b < it.b1 && ok; ++b, ++blks) {
-                    const uint32_t kv = 2 * blks + 1, st = kv % NS;  // V of the CTA's block number blks
+                    const uint32_t st = 2 * (blks % NB) + 1;  // V of the CTA's block number blks
                     ok = wait_warp(&wempty[blks % kWide], ((blks / kWide) & 1) ^ 1, abort_flag) &&
-                         wait_warp(&full[st], (kv / NS) & 1, abort_flag);
+                         wait_warp(&full[blks % NB], (blks / NB) & 1, abort_flag);
                     ok = !named_any_128(!ok);
                     if (!ok) break;
                     widen_v<CG>(ring + (size_t)st * C::kStageBytes,
@@ -844,145 +833,61 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                if constexpr (FP8) {
-                    // Both pages at once: the maximum of all 128 scores is known before any P goes
-                    // out. (Page by page, as below, the first product started sooner and then
-                    // kept the other half's waiting while this half scaled its second page: 304
-                    // in place of 278 us for 128 requests over a 65536-token prefix.)
-                    float s[128];
-                    tmem_ld32(scol, s);
-                    tmem_ld32(scol + 32, s + 32);
-                    tmem_ld32(scol + 64, s + 64);
-                    tmem_ld32(scol + 96, s + 96);
-                    // which of the block's keys this row sees, found while the scores arrive
-                    const int nv = lim - b * kBlock, pages_ok = meta[blks % kMetaRing];
-                    const bool all_seen = lim_w - b * kBlock >= kBlock && pages_ok == 3;
+                // which of the block's keys this row sees
+                const int nv = lim - b * kBlock, nv_w = lim_w - b * kBlock, pages_ok = meta[blks % kMetaRing];
+                // A page's 64 keys at a time: their product with V runs while the softmax works
+                // on the next ones.
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float s[kChunk];
+                    tmem_ld32(scol + kChunk * u, s);
+                    tmem_ld32(scol + kChunk * u + 32, s + 32);
+                    const bool page_ok = (pages_ok >> u) & 1;
                     tmem_ld_wait();
-                    // (the scores exist, so the splitter's row scales do too)
-                    if (b == it.b0) sc = p.scale_log2 * reinterpret_cast<const float*>(smem + LY::kQs)[(nd & 1) * 256 + t * 128 + row];
-                    const float4* ks = reinterpret_cast<const float4*>(smem + LY::kKs + (blks % kMetaRing) * 512);
+                    if constexpr (FP8) {
+                        // (the scores exist, so the splitter's row scales do too)
+                        if (u == 0 && b == it.b0)
+                            sc = p.scale_log2 * reinterpret_cast<const float*>(smem + LY::kQs)[(nd & 1) * 256 + t * 128 + row];
+                        const float4* ks = reinterpret_cast<const float4*>(smem + LY::kKs + (blks % kMetaRing) * 512) + u * 16;
 #pragma unroll
-                    for (int c = 0; c < 128; c += 4) {
-                        const float4 f = ks[c / 4];
-                        const float2 x = mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
-                        const float2 y = mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
-                        s[c] = x.x, s[c + 1] = x.y, s[c + 2] = y.x, s[c + 3] = y.y;
-                    }
-                    if (!all_seen) {
-                        const int n0 = (pages_ok & 1) ? min(nv, kChunk) : 0, n1 = (pages_ok & 2) ? nv - kChunk : 0;
-#pragma unroll
-                        for (int c = 0; c < kChunk; ++c) {
-                            if (c >= n0) s[c] = kNegInf;
-                            if (c >= n1) s[c + kChunk] = kNegInf;
+                        for (int c = 0; c < kChunk; c += 4) {
+                            const float4 f = ks[c / 4];
+                            const float2 x = mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
+                            const float2 y = mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
+                            s[c] = x.x, s[c + 1] = x.y, s[c + 2] = y.x, s[c + 3] = y.y;
                         }
                     }
-                    // P = exp2(s sc - m) of 64 columns, to TMEM as 16-bit pairs; returns their sum
-                    // and, with MAX, takes the maximum of all 128 scores along the way: four per
-                    // pair of exponentials, whose unit has a quarter of the others' rate, so that
-                    // the two run side by side
-                    float mx[8];
-                    auto exps = [&](int c0, float neg, auto max_too) {
-                        constexpr bool kMax = decltype(max_too)::value;
+                    if (nv_w < kChunk * (u + 1) || !page_ok) {
+                        const int n = page_ok ? nv - kChunk * u : 0;
+#pragma unroll
+                        for (int c = 0; c < kChunk; ++c)
+                            if (c >= n) s[c] = kNegInf;
+                    }
+                    // P = exp2(s sc - m), to TMEM as 16-bit pairs; returns the sum
+                    auto exps = [&](float neg) {
                         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                        for (int c = c0; c < c0 + 64; c += 32) {
+                        for (int c = 0; c < kChunk; c += 32) {
                             uint32_t pk[16];
 #pragma unroll
-                            for (int u = 0; u < 16; ++u) {
-                                float2 x = fma2(make_float2(s[c + 2 * u], s[c + 2 * u + 1]), make_float2(sc, sc), make_float2(neg, neg));
+                            for (int i = 0; i < 16; ++i) {
+                                float2 x = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), make_float2(sc, sc), make_float2(neg, neg));
                                 x.x = fast_exp2(x.x);
-                                if constexpr (kMax) {
-                                    const int i = 2 * (c + 2 * u);
-                                    mx[(i / 2) & 7] = i < 16 ? fmaxf(s[i], s[i + 1]) : max3(mx[(i / 2) & 7], s[i], s[i + 1]);
-                                }
                                 x.y = fast_exp2(x.y);
-                                if constexpr (kMax) {
-                                    const int i = 2 * (c + 2 * u) + 2;
-                                    mx[(i / 2) & 7] = i < 16 ? fmaxf(s[i], s[i + 1]) : max3(mx[(i / 2) & 7], s[i], s[i + 1]);
-                                }
-                                sum[u & 1] = add2(sum[u & 1], x);
-                                pk[u] = pack_f16x2(x.x, x.y);
+                                sum[i & 1] = add2(sum[i & 1], x);
+                                pk[i] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
                             }
-                            tmem_st16(scol + c / 2, pk);
+                            tmem_st16(scol + (kChunk * u + c) / 2, pk);
                         }
                         return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     };
-                    // The first 64 columns against the reference as it stands, while the block's
-                    // maximum is found: the reference moves only when that is far above it, which
-                    // after a tile's first blocks is rare, and they are then done again.
-                    float sum0 = exps(0, m == kNegInf ? 0.f : -m, std::true_type{});
-                    const float mraw = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
-                    const bool move = mraw > m + kRescaleLog2 || (m == kNegInf && mraw != kNegInf);
-                    if (__any_sync(0xffffffffu, move)) {
-                        const bool resc = move && m != kNegInf;
-                        if (__any_sync(0xffffffffu, resc)) {
-                            // (the product of the block before is done: it was issued before this
-                            // block's scores)
-                            const float al = resc ? fast_exp2(m - mraw) : 1.f;
-#pragma unroll 1
-                            for (int c = 0; c < 128; c += 32) {
-                                float o[32];
-                                tmem_ld32(ocol + c, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int u = 0; u < 32; ++u) o[u] *= al;
-                                tmem_st32(ocol + c, o);
-                            }
-                            l *= al;
-                        }
-                        if (move) m = mraw;
-                        sum0 = exps(0, m == kNegInf ? 0.f : -m, std::false_type{});
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_leader<CG>(&pfull[2 * t]);
-                    const float sum1 = exps(64, m == kNegInf ? 0.f : -m, std::false_type{});
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_leader<CG>(&pfull[2 * t + 1]);
-                    l += sum0 + sum1;
-                } else {
-                    // which of the block's keys this row sees
-                    const int nv = lim - b * kBlock, nv_w = lim_w - b * kBlock, pages_ok = meta[blks % kMetaRing];
-                    // A page's 64 keys at a time: their product with V runs while the softmax works
-                    // on the next ones.
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float s[kChunk];
-                        tmem_ld32(scol + kChunk * u, s);
-                        tmem_ld32(scol + kChunk * u + 32, s + 32);
-                        const bool page_ok = (pages_ok >> u) & 1;
-                        tmem_ld_wait();
-                        if (nv_w < kChunk * (u + 1) || !page_ok) {
-                            const int n = page_ok ? nv - kChunk * u : 0;
-#pragma unroll
-                            for (int c = 0; c < kChunk; ++c)
-                                if (c >= n) s[c] = kNegInf;
-                        }
-                        // P = exp2(s sc - m), to TMEM as 16-bit pairs; returns the sum
-                        auto exps = [&](float neg) {
-                            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                            for (int c = 0; c < kChunk; c += 32) {
-                                uint32_t pk[16];
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    float2 x = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), make_float2(sc, sc), make_float2(neg, neg));
-                                    x.x = fast_exp2(x.x);
-                                    x.y = fast_exp2(x.y);
-                                    sum[i & 1] = add2(sum[i & 1], x);
-                                    pk[i] = pack_bf16x2(x.x, x.y);
-                                }
-                                tmem_st16(scol + (kChunk * u + c) / 2, pk);
-                            }
-                            return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                        };
-                        // Against the reference as it stands, while the keys' maximum is found: the
-                        // reference moves only when that is far above it, which after a tile's first
-                        // blocks is rare, and they are then done again.
-                        float sum = exps(m == kNegInf ? 0.f : -m);
+                    // Against the reference as it stands. The sum tells whether that still serves:
+                    // one up to kSumLimit bounds every P. Only where it is above, or where a row has
+                    // no reference yet, the keys' maximum is taken and they are done again.
+                    const bool fresh = __any_sync(0xffffffffu, m == kNegInf);
+                    float sum = 0.f;
+                    if (!fresh) sum = exps(-m);
+                    if (fresh || __any_sync(0xffffffffu, !(sum <= kSumLimit))) {
                         float mx[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) mx[i] = fmaxf(s[i], s[60 + i]);
@@ -992,38 +897,36 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                             for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[c + i], s[c + 4 + i]);
                         const float mraw = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
                         const bool move = mraw > m + kRescaleLog2 || (m == kNegInf && mraw != kNegInf);
-                        if (__any_sync(0xffffffffu, move)) {
-                            const bool resc = move && m != kNegInf;
-                            if (__any_sync(0xffffffffu, resc)) {
-                                // O holds everything before these keys once their predecessors' product
-                                // is done: the last block's is (it was issued before this block's
-                                // scores), the first page's of this block says so
-                                if (u == 1 && !wait_warp(&pvdone[t], ns & 1, abort_flag)) {
-                                    ok = false;
-                                    break;
-                                }
-                                tc_fence_after();
-                                const float al = resc ? fast_exp2(m - mraw) : 1.f;
-#pragma unroll 1
-                                for (int c = 0; c < 128; c += 32) {
-                                    float o[32];
-                                    tmem_ld32(ocol + c, o);
-                                    tmem_ld_wait();
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] *= al;
-                                    tmem_st32(ocol + c, o);
-                                }
-                                l *= al;
+                        const bool resc = move && m != kNegInf;
+                        if (__any_sync(0xffffffffu, resc)) {
+                            // O holds everything before these keys once their predecessors' product
+                            // is done: the last block's is (it was issued before this block's
+                            // scores), the first page's of this block says so
+                            if (u == 1 && !wait_warp(&pvdone[t], ns & 1, abort_flag)) {
+                                ok = false;
+                                break;
                             }
-                            if (move) m = mraw;
-                            sum = exps(m == kNegInf ? 0.f : -m);
+                            tc_fence_after();
+                            const float al = resc ? fast_exp2(m - mraw) : 1.f;
+#pragma unroll 1
+                            for (int c = 0; c < 128; c += 32) {
+                                float o[32];
+                                tmem_ld32(ocol + c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] *= al;
+                                tmem_st32(ocol + c, o);
+                            }
+                            l *= al;
                         }
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_leader<CG>(&pfull[2 * t + u]);
-                        l += sum;
+                        if (move) m = mraw;
+                        sum = exps(m == kNegInf ? 0.f : -m);
                     }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_leader<CG>(&pfull[2 * t + u]);
+                    l += sum;
                 }
                 if (!ok) break;
             }
