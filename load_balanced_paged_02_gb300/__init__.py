@@ -23,5 +23,8 @@ _BINDING_NAMES = {
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        return getattr(importlib.import_module(".binding", __name__), name)
+        # kept, so that only the first access comes through here (1 us each on the way to
+        # calls whose kernels take two)
+        value = globals()[name] = getattr(importlib.import_module(".binding", __name__), name)
+        return value
     raise AttributeError(name)
