@@ -282,6 +282,43 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 
+// 64 columns of 16 lanes (16x256b shape): register 4 j + 2 k + e of thread t holds
+// lane t / 4 + 8 k, column 8 j + 2 (t % 4) + e.
+__device__ __forceinline__ void tmem_ld16x(uint32_t taddr, float (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+          "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+          "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// 32 columns of 16 lanes (16x128b shape): register 2 j + k of thread t goes to lane
+// t / 4 + 8 k, column 4 j + t % 4.
+__device__ __forceinline__ void tmem_st16x(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Values of four rows per thread (row t / 4 + 8 i of the warp's 32, the same in the
+// row's four threads) -> the value of row `lane`.
+__device__ __forceinline__ float row_value(const float (&x)[4], int lane) {
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float z = __shfl_sync(0xffffffffu, x[i], 4 * (lane & 7));
+        if ((lane >> 3) == i) y = z;
+    }
+    return y;
+}
+
 // (a.x b.x + c.x, a.y b.y + c.y) and (a.x + b.x, a.y + b.y) in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -807,7 +844,6 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
         reg_inc<C::kRegsSoftmax>();
         // ============================ softmax warpgroup of half t, one thread per row
         const int t = warp >> 2;
-        const int row = threadIdx.x & 127;
         const uint32_t lane_addr = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t scol = tmem + lane_addr + 128 * t, ocol = tmem + lane_addr + 256 + 128 * t;
         const int half_tok = (t * CG + rank) * kHalfTokens;  // the half's first token in the tile
@@ -826,7 +862,13 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
             const int lim_w = p.mode == kModePrefix ? it.L : min(it.L, lim0);
             const int lim = p.mode == kModePrefix ? it.L : min(it.L, lim0 + lane / kGroup);
             float m = kNegInf, l = 0.f;  // reference maximum (log2 domain) and sum
-            float sc = p.scale_log2;
+            const float sc = p.scale_log2;
+            // e4m3: the same of the four rows that the thread has parts of
+            float mq[4], lq[4], scq[4];
+            if constexpr (FP8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mq[i] = kNegInf, lq[i] = 0.f;
+            }
             for (int b = it.b0; b < it.b1; ++b, ++blks, ++ns) {
                 if (!wait_warp(&sfull[t], ns & 1, abort_flag)) {
                     ok = false;
@@ -834,99 +876,207 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                 }
                 tc_fence_after();
                 // which of the block's keys this row sees
-                const int nv = lim - b * kBlock, nv_w = lim_w - b * kBlock, pages_ok = meta[blks % kMetaRing];
-                // A page's 64 keys at a time: their product with V runs while the softmax works
-                // on the next ones.
+                const int nv_w = lim_w - b * kBlock, pages_ok = meta[blks % kMetaRing];
+                if constexpr (FP8) {
+                    // The key scales come from shared memory, and with a row per thread every
+                    // thread would read them all. Here a thread has parts of four rows: query
+                    // head hq of the warp's tokens i = 2 gi + k, columns 8 j + 2 cq and the next
+                    // (the 16x256b shape's layout, for TMEM lanes 16 gi ..): a quarter of them.
+                    const int hq = lane >> 2, cq = lane & 3;
+                    const int left = it.L - b * kBlock - 2 * cq;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float s[kChunk];
-                    tmem_ld32(scol + kChunk * u, s);
-                    tmem_ld32(scol + kChunk * u + 32, s + 32);
-                    const bool page_ok = (pages_ok >> u) & 1;
-                    tmem_ld_wait();
-                    if constexpr (FP8) {
-                        // (the scores exist, so the splitter's row scales do too)
-                        if (u == 0 && b == it.b0)
-                            sc = p.scale_log2 * reinterpret_cast<const float*>(smem + LY::kQs)[(nd & 1) * 256 + t * 128 + row];
-                        const float4* ks = reinterpret_cast<const float4*>(smem + LY::kKs + (blks % kMetaRing) * 512) + u * 16;
+                    for (int u = 0; u < 2; ++u) {
+                        float s[2][32];  // [gi][4 j + 2 k + column parity]
+                        tmem_ld16x(scol + kChunk * u, s[0]);
+                        tmem_ld16x(scol + kChunk * u + (16u << 16), s[1]);
+                        const bool page_ok = (pages_ok >> u) & 1;
+                        tmem_ld_wait();
+                        if (u == 0 && b == it.b0) {
+                            // (the scores exist, so the splitter's row scales do too)
+                            const float* qs = reinterpret_cast<const float*>(smem + LY::kQs) + (nd & 1) * 256 + t * 128 + 32 * (warp & 3) + hq;
 #pragma unroll
-                        for (int c = 0; c < kChunk; c += 4) {
-                            const float4 f = ks[c / 4];
-                            const float2 x = mul2(make_float2(s[c], s[c + 1]), make_float2(f.x, f.y));
-                            const float2 y = mul2(make_float2(s[c + 2], s[c + 3]), make_float2(f.z, f.w));
-                            s[c] = x.x, s[c + 1] = x.y, s[c + 2] = y.x, s[c + 3] = y.y;
+                            for (int i = 0; i < 4; ++i) scq[i] = sc * qs[8 * i];
                         }
-                    }
-                    if (nv_w < kChunk * (u + 1) || !page_ok) {
-                        const int n = page_ok ? nv - kChunk * u : 0;
+                        const float2* ks = reinterpret_cast<const float2*>(smem + LY::kKs + (blks % kMetaRing) * 512) + 32 * u + cq;
 #pragma unroll
-                        for (int c = 0; c < kChunk; ++c)
-                            if (c >= n) s[c] = kNegInf;
-                    }
-                    // P = exp2(s sc - m), to TMEM as 16-bit pairs; returns the sum
-                    auto exps = [&](float neg) {
-                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 f = ks[4 * j];
 #pragma unroll
-                        for (int c = 0; c < kChunk; c += 32) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float2 x = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), make_float2(sc, sc), make_float2(neg, neg));
-                                x.x = fast_exp2(x.x);
-                                x.y = fast_exp2(x.y);
-                                sum[i & 1] = add2(sum[i & 1], x);
-                                pk[i] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
+                            for (int i = 0; i < 4; ++i) {
+                                float* x = s[i >> 1] + 4 * j + 2 * (i & 1);
+                                const float2 y = mul2(make_float2(x[0], x[1]), f);
+                                x[0] = y.x, x[1] = y.y;
                             }
-                            tmem_st16(scol + (kChunk * u + c) / 2, pk);
                         }
-                        return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    };
-                    // Against the reference as it stands. The sum tells whether that still serves:
-                    // one up to kSumLimit bounds every P. Only where it is above, or where a row has
-                    // no reference yet, the keys' maximum is taken and they are done again.
-                    const bool fresh = __any_sync(0xffffffffu, m == kNegInf);
-                    float sum = 0.f;
-                    if (!fresh) sum = exps(-m);
-                    if (fresh || __any_sync(0xffffffffu, !(sum <= kSumLimit))) {
-                        float mx[4];
+                        if (nv_w < kChunk * (u + 1) || !page_ok) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(s[i], s[60 + i]);
+                            for (int i = 0; i < 4; ++i) {
+                                const int see = p.mode == kModePrefix ? left : min(left, lim0 + i - b * kBlock - 2 * cq);
+                                const int n = page_ok ? see - kChunk * u : 0;
 #pragma unroll
-                        for (int c = 4; c < 60; c += 8)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[c + i], s[c + 4 + i]);
-                        const float mraw = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
-                        const bool move = mraw > m + kRescaleLog2 || (m == kNegInf && mraw != kNegInf);
-                        const bool resc = move && m != kNegInf;
-                        if (__any_sync(0xffffffffu, resc)) {
-                            // O holds everything before these keys once their predecessors' product
-                            // is done: the last block's is (it was issued before this block's
-                            // scores), the first page's of this block says so
-                            if (u == 1 && !wait_warp(&pvdone[t], ns & 1, abort_flag)) {
-                                ok = false;
-                                break;
+                                for (int j = 0; j < 8; ++j) {
+                                    float* x = s[i >> 1] + 4 * j + 2 * (i & 1);
+                                    if (8 * j >= n) x[0] = kNegInf;
+                                    if (8 * j + 1 >= n) x[1] = kNegInf;
+                                }
                             }
-                            tc_fence_after();
-                            const float al = resc ? fast_exp2(m - mraw) : 1.f;
+                        }
+                        // P of the page, to TMEM as f16 pairs; the thread's parts of the rows' sums
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        auto exps = [&]() {
+#pragma unroll
+                            for (int gi = 0; gi < 2; ++gi) {
+                                uint32_t pk[16];
+                                float2 a[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k) {
+                                        const int i = 2 * gi + k;
+                                        const float neg = mq[i] == kNegInf ? 0.f : -mq[i];
+                                        const float* y = s[gi] + 4 * j + 2 * k;
+                                        float2 x = fma2(make_float2(y[0], y[1]), make_float2(scq[i], scq[i]), make_float2(neg, neg));
+                                        x.x = fast_exp2(x.x);
+                                        x.y = fast_exp2(x.y);
+                                        a[k] = add2(a[k], x);
+                                        pk[2 * j + k] = pack_f16x2(x.x, x.y);
+                                    }
+                                tmem_st16x(scol + ((uint32_t)(16 * gi) << 16) + 32 * u, pk);
+                                sum[2 * gi] = a[0].x + a[0].y;
+                                sum[2 * gi + 1] = a[1].x + a[1].y;
+                            }
+                        };
+                        // as below, the sum being of 16 keys
+                        const bool fresh = __any_sync(0xffffffffu, mq[0] == kNegInf || mq[1] == kNegInf || mq[2] == kNegInf || mq[3] == kNegInf);
+                        if (!fresh) exps();
+                        bool high = false;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) high |= !(sum[i] <= kSumLimit / 4);
+                        if (fresh || __any_sync(0xffffffffu, high)) {
+                            float al[4];
+                            bool resc = false;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float* x = s[i >> 1] + 2 * (i & 1);
+                                float mx = fmaxf(x[0], x[1]);
+#pragma unroll
+                                for (int j = 1; j < 8; ++j) mx = max3(mx, x[4 * j], x[4 * j + 1]);
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * scq[i];
+                                const bool move = mx > mq[i] + kRescaleLog2 || (mq[i] == kNegInf && mx != kNegInf);
+                                al[i] = move && mq[i] != kNegInf ? fast_exp2(mq[i] - mx) : 1.f;
+                                resc |= move && mq[i] != kNegInf;
+                                if (move) mq[i] = mx;
+                                lq[i] *= al[i];
+                            }
+                            if (__any_sync(0xffffffffu, resc)) {
+                                if (u == 1 && !wait_warp(&pvdone[t], ns & 1, abort_flag)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                                const float alr = row_value(al, lane);
 #pragma unroll 1
-                            for (int c = 0; c < 128; c += 32) {
-                                float o[32];
-                                tmem_ld32(ocol + c, o);
-                                tmem_ld_wait();
+                                for (int c = 0; c < 128; c += 32) {
+                                    float o[32];
+                                    tmem_ld32(ocol + c, o);
+                                    tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= al;
-                                tmem_st32(ocol + c, o);
+                                    for (int i = 0; i < 32; ++i) o[i] *= alr;
+                                    tmem_st32(ocol + c, o);
+                                }
                             }
-                            l *= al;
+                            exps();
                         }
-                        if (move) m = mraw;
-                        sum = exps(m == kNegInf ? 0.f : -m);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_leader<CG>(&pfull[2 * t + u]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) lq[i] += sum[i];
                     }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_leader<CG>(&pfull[2 * t + u]);
-                    l += sum;
+                } else {
+                    const int nv = lim - b * kBlock;
+                    // A page's 64 keys at a time: their product with V runs while the softmax works
+                    // on the next ones.
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float s[kChunk];
+                        tmem_ld32(scol + kChunk * u, s);
+                        tmem_ld32(scol + kChunk * u + 32, s + 32);
+                        const bool page_ok = (pages_ok >> u) & 1;
+                        tmem_ld_wait();
+                        if (nv_w < kChunk * (u + 1) || !page_ok) {
+                            const int n = page_ok ? nv - kChunk * u : 0;
+#pragma unroll
+                            for (int c = 0; c < kChunk; ++c)
+                                if (c >= n) s[c] = kNegInf;
+                        }
+                        // P = exp2(s sc - m), to TMEM as 16-bit pairs; returns the sum
+                        auto exps = [&](float neg) {
+                            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                            for (int c = 0; c < kChunk; c += 32) {
+                                uint32_t pk[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    float2 x = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), make_float2(sc, sc), make_float2(neg, neg));
+                                    x.x = fast_exp2(x.x);
+                                    x.y = fast_exp2(x.y);
+                                    sum[i & 1] = add2(sum[i & 1], x);
+                                    pk[i] = pack_bf16x2(x.x, x.y);
+                                }
+                                tmem_st16(scol + (kChunk * u + c) / 2, pk);
+                            }
+                            return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                        };
+                        // Against the reference as it stands. The sum tells whether that still serves:
+                        // one up to kSumLimit bounds every P. Only where it is above, or where a row has
+                        // no reference yet, the keys' maximum is taken and they are done again.
+                        const bool fresh = __any_sync(0xffffffffu, m == kNegInf);
+                        float sum = 0.f;
+                        if (!fresh) sum = exps(-m);
+                        if (fresh || __any_sync(0xffffffffu, !(sum <= kSumLimit))) {
+                            float mx[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(s[i], s[60 + i]);
+#pragma unroll
+                            for (int c = 4; c < 60; c += 8)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[c + i], s[c + 4 + i]);
+                            const float mraw = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
+                            const bool move = mraw > m + kRescaleLog2 || (m == kNegInf && mraw != kNegInf);
+                            const bool resc = move && m != kNegInf;
+                            if (__any_sync(0xffffffffu, resc)) {
+                                // O holds everything before these keys once their predecessors' product
+                                // is done: the last block's is (it was issued before this block's
+                                // scores), the first page's of this block says so
+                                if (u == 1 && !wait_warp(&pvdone[t], ns & 1, abort_flag)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                                const float al = resc ? fast_exp2(m - mraw) : 1.f;
+#pragma unroll 1
+                                for (int c = 0; c < 128; c += 32) {
+                                    float o[32];
+                                    tmem_ld32(ocol + c, o);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] *= al;
+                                    tmem_st32(ocol + c, o);
+                                }
+                                l *= al;
+                            }
+                            if (move) m = mraw;
+                            sum = exps(m == kNegInf ? 0.f : -m);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_leader<CG>(&pfull[2 * t + u]);
+                        l += sum;
+                    }
                 }
                 if (!ok) break;
             }
@@ -937,6 +1087,15 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                 break;
             }
             tc_fence_after();
+            if constexpr (FP8) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    lq[i] += __shfl_xor_sync(0xffffffffu, lq[i], 1);
+                    lq[i] += __shfl_xor_sync(0xffffffffu, lq[i], 2);
+                }
+                m = row_value(mq, lane);
+                l = row_value(lq, lane);
+            }
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             const float lse = l > 0.f || l != l ? (m == kNegInf ? 0.f : m) * kLn2 + logf(l) : kNegInf;
             const bool direct = p.mode == kModePrefill && it.whole;
