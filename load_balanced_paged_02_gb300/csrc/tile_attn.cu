@@ -1,38 +1,66 @@
 // Prompt attention and shared-prefix attention on the fifth-generation tensor
-// cores, over the paged cache. Both are the same product: a tile of 32 query
-// tokens x 8 query heads (256 rows, two halves of 128) against a run of
-// 128-token KV blocks, with the running maximum and sum of a softmax:
+// cores, over the paged cache. Both are the same product: a tile of query tokens
+// x 8 query heads against a run of 128-token KV blocks, with the running maximum
+// and sum of a softmax:
 //   S_j = Q K_j^T,  m = max(m, rowmax S_j),  P_j = exp(S_j - m),
 //   l += rowsum P_j,  O += P_j V_j   (O and l scaled when m moves),
 // then O / l and m + ln l. Prompts add the causal limit (query token t of a
 // sequence of n tokens and L keys sees keys [0, L - n + t]); a prefix is seen
-// whole by every row of its group. A tile map (tile.cuh) gives every CTA an
-// equal run of blocks; a tile that falls to one CTA is written to the output,
+// whole by every row of its group. A tile map (tile.cuh) gives every worker an
+// equal run of blocks; a tile that falls to one worker is written to the output,
 // a cut one (and every prefix piece) as normalised float32 rows with their LSE,
 // which the kernels in tile_combine.cu merge.
 //
-// One CTA per SM, 12 warps (e4m3: 16). A tile of 32 query tokens belongs to one
-// CTA (CG = 1), one of 64 to a pair of CTAs (CG = 2) whose products run on both
-// SMs' tensor cores at once (cta_group::2, M = 256): each CTA keeps its own query
-// rows, scores and sums, and loads only half of every K and V block (one page of
-// K, one dim half of V), which halves the copies and the shared memory that the
-// products read. The leader (rank 0) issues for both.
-//  * warps 0-3 and 4-7, the softmax warpgroups of the two halves: one thread
-//    per query row. Scores come from TMEM, P goes back over them as 16-bit
-//    pairs (the A operand of the second product), O is scaled in TMEM only when
-//    a row's maximum has grown by more than 2^8 since its reference was taken.
+// One CTA per SM, 12 warps (e4m3: 16). A tile of 32 query tokens (two halves of
+// 128 rows) belongs to one CTA (CG = 1), one of 64 to a pair of CTAs (CG = 2)
+// whose products run on both SMs' tensor cores at once (cta_group::2, M = 256):
+// each CTA keeps its own query rows, scores and sums, and loads only half of every
+// K and V block (one page of K, one dim half of V), which halves the copies and the
+// shared memory that the products read. The leader (rank 0) issues for both.
+//  * warps 0-3 and 4-7, the softmax warpgroups of the two halves, a page of 64 keys
+//    at a time: one thread per query row (e4m3: four threads per four rows). Scores
+//    come from TMEM, P goes back over them as 16-bit pairs (the A operand of the
+//    second product). The reference m is not the running maximum itself: P is made
+//    against m as it stands, and its sum, which is needed anyway, tells whether the
+//    maximum has to be looked at (kSumLimit). O is scaled in TMEM only then. P is
+//    relative to m, so bf16 loses nothing by a P above 1, and f16 holds up to 65504.
 //  * warp 8, producer: one thread issues TMA copies of the tile's query rows
 //    and of K_0 V_0 K_1 V_1 ... into a ring of stages, pages through the table.
-//  * warp 9, issuer: one thread issues the MMAs in the order
+//  * warp 9, issuer: the MMAs in the order
 //      S0(0) S1(0) | PV0(0) S0(1) PV1(0) S1(1) | PV0(1) ...
 //    so that one half's products run while the other half's softmax does. MMAs
-//    of one thread run in order, so S(j+1) may overwrite P(j) once PV(j) has
+//    run in the order of their issue, so S(j+1) may overwrite P(j) once PV(j) has
 //    been issued. In the other CTA of a pair this warp tells the leader which of
-//    its stages are filled.
+//    its blocks have landed.
 //  * e4m3, warps 12-15: the query rows split into two e4m3 tiles of codes
 //    (Q = (Q_hi + Q_lo) 2^e, as in attn_tc.cu), so that Q K^T runs on the K
 //    codes as they are; V widened to f16 (code x scale) into a ring of its own.
 // Every wait is bounded; on expiry the CTA records HPC_DEVERR_WAIT_TIMEOUT.
+//
+// Bound by: the tensor core and its power, over bf16 caches. Prompt of 8192 tokens,
+// 64 / 8 heads: 680 us, 1618 TFLOP/s (0.85 of the library's 8192^3 product in
+// bursts, 0.94 of the same over seconds); the tensor pipe is active for 75 % of the
+// cycles and the clock falls from 2070 to 1950 MHz at the board's power limit. A
+// half's chain (its scores, 750 clocks of softmax per page, its product) leaves the
+// rest: measured per block of two halves 2900 clocks of which 2048 are MMAs. Over
+// e4m3 caches the softmax threads set the pace (the key scales' products and the
+// other layout cost half as much again, the widening of V takes issue slots):
+// 128 requests over a 65536-token prefix 208 us, 169 us over a bf16 cache.
+// Few blocks (8192-token prefix, 64 requests: 22 us for seven blocks per CTA) are
+// bound by latency: 1.3 us a block, and some 10 us of start, first copies and rows.
+//
+// What else was measured (8192-token prompt unless said otherwise):
+//  * the maximum of each block taken before its P goes out: 749 us; page by page:
+//    734 us; the sum as the test, and one barrier per block for K and V in place of
+//    two (four in a pair: each test costs the issuer 150 to 200 clocks): 680 us.
+//  * two threads per row (16 softmax warps of 96 registers): 775 against 735 us.
+//  * scores double-buffered as two products of 64 keys: 811 us (an MMA of N = 64
+//    takes 48 clocks, not 32). An issuer that polls for whichever half is ready:
+//    1184 us; an issuer warp per half: 892 us (their tests take issue slots from the
+//    softmax warps of the same scheduler).
+//  * e4m3 with a thread per row, each reading all of a page's key scales from shared
+//    memory: 512-token pieces of four prompts beside 28 single tokens 615 us; as it
+//    is 588 us.
 #include <atomic>
 #include <cstring>
 
@@ -51,8 +79,10 @@ using attn::wait_bounded;
 
 constexpr int kHalfRows = 128;
 constexpr int kQBytes = 32768;           // a half's query rows: [2 dim halves][128 rows][128 B]
-constexpr float kRescaleLog2 = 4.0f;     // the reference moves when a maximum is 2^4 above it,
-constexpr float kSumLimit = 1024.f;      // which is looked at when 64 keys' P add up to more than this
+// 64 keys' P that add up to more than 2^10 hold one above 2^4: then the maximum is
+// looked at and the reference moves to it. Up to there every P is at most 2^10.
+constexpr float kSumLimit = 1024.f;
+constexpr float kRescaleLog2 = 4.0f;
 constexpr int kMetaRing = 8;             // blocks whose page checks (and, e4m3, scales) are kept
 constexpr int kWide = 2;                 // e4m3: f16 V tiles
 constexpr int kOutBytes = 2048;          // a softmax warp's staging of 32 output rows x 64 B
