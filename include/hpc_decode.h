@@ -577,7 +577,8 @@ size_t hpc_prefix_split_rows(int num_groups, int batch, int q_len, int num_kv_he
  *   page_table_stride  of the table that the attention call gets
  *   min_blocks_per_cta  least units of a worker's run (fewer workers get work in
  *                 small batches); 0 or 1: no floor
- *   tile_tokens   32, 64, or 0: the one that is faster for the average sequence
+ *   tile_tokens   32, 64, or 0: the one that is faster for the average sequence,
+ *                 of a bf16 cache here, of the call's cache in hpc_prefill
  *                 (num_ctas 1 takes 32)
  * One block, integer only, reads the lengths on the device. A sequence whose
  * starts decrease or leave [0, num_tokens] is passed over
@@ -638,7 +639,7 @@ hpc_status hpc_prefix_plan(const int32_t* d_group_starts, const int32_t* d_prefi
 
 /*
  * Attention of every query row over its group's prefix, each prefix read once
- * per 32 query tokens of the group instead of once per request: partial rows and LSEs for
+ * per tile of the group's query tokens instead of once per request: partial rows and LSEs for
  * hpc_prefix_combine.
  *   q             device bf16 [batch][q_len][num_q_heads][128], 16-byte aligned
  *   prefix_table  device int32 [num_groups][prefix_table_stride]

@@ -28,16 +28,16 @@ bool tokens_ok(int num_tokens, int num_seqs, int num_kv_heads) {
 }
 
 // Tiles of 64 tokens on pairs of CTAs from an average of 64 query tokens per prompt on
-// (96 per prefix group), of 32 on single CTAs below. A pair halves the copies and the
-// shared memory traffic of a row, a single CTA wastes fewer rows on short sequences.
-// Whole calls, us, tile 32 / 64: eight prompts of 4096 keys with 32 new tokens each
-// 51 / 55, with 64 75 / 66, with 96 100 / 98, with 512 383 / 326 (e4m3: 55 / 65,
-// 89 / 80, 124 / 121, 511 / 423); the attention over an 8192-token prefix with 48
-// requests 20 / 22, 64 22 / 22, 128 31 / 31, 256 49 / 47 (e4m3: 28 / 30, 31 / 30,
-// 45 / 42, 72 / 65). Groups of unlike sizes favour 32 up to a larger average: 16, 5, 1
-// and 42 requests of four tokens 43 / 54.
-int auto_tile(int mode, int num_tokens, int num_seqs) {
-    const long long from = (mode == kModePrefill ? kTilePair : 3 * kTilePair / 2) * (long long)num_seqs;
+// (96 over e4m3 caches and for prefix groups), of 32 on single CTAs below. A pair halves
+// the copies and the shared memory traffic of a row, a single CTA wastes fewer rows on
+// short sequences. Whole calls, us, tile 32 / 64, eight prompts of 4096 keys: 32 new
+// tokens each 51 / 55, 64 75 / 66, 96 100 / 98, 512 383 / 326; e4m3 54 / 65, 85 / 79,
+// 115 / 120, 471 / 421. 512-token pieces of four prompts beside 28 single tokens (64 on
+// average): 496 / 455, e4m3 548 / 609. Attention over an 8192-token prefix: 48 requests
+// 20 / 22, 64 22 / 22, 128 31 / 31, 256 49 / 47; e4m3 27 / 29, 31 / 30, 43 / 42, 67 / 65.
+// Groups of 16, 5, 1 and 42 requests of four tokens: 43 / 54.
+int auto_tile(int mode, bool fp8, int num_tokens, int num_seqs) {
+    const long long from = (mode == kModePrefill && !fp8 ? kTilePair : 3 * kTilePair / 2) * (long long)num_seqs;
     return num_tokens >= from ? kTilePair : kTileCta;
 }
 
@@ -50,7 +50,7 @@ hpc_status plan_common(const int32_t* d_starts, const int32_t* d_lens, int num_s
         return HPC_ERR_INVALID_ARG;
     if (tile_tokens != 0 && tile_tokens != kTileCta && tile_tokens != kTilePair) return HPC_ERR_INVALID_ARG;
     if (plan->bytes < hpc_tile_plan_bytes(num_seqs, num_ctas)) return HPC_ERR_WORKSPACE_TOO_SMALL;
-    if (tile_tokens == 0) tile_tokens = auto_tile(mode, num_tokens, num_seqs);
+    if (tile_tokens == 0) tile_tokens = auto_tile(mode, false, num_tokens, num_seqs);
     if (num_ctas == 1) tile_tokens = kTileCta;
     plan->num_seqs = num_seqs;
     plan->num_tokens = num_tokens;
@@ -273,6 +273,7 @@ hpc_status hpc_prefill(const void* q, const void* k_cache, const void* v_cache, 
     if ((st = cache_check(k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, num_kv_heads)) != HPC_OK) return st;
     if (!page_table) return HPC_ERR_INVALID_ARG;
     if (num_tokens != 0 && (!q || !aligned(q, 16) || !out || !aligned(out, 16))) return HPC_ERR_INVALID_ARG;
+    if (tile_tokens == 0 && num_tokens >= 0) tile_tokens = auto_tile(kModePrefill, kv_dtype == HPC_KV_FP8_E4M3, num_tokens, batch);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     plan->buf = reinterpret_cast<int32_t*>(ws + w.plan);
     plan->bytes = hpc_tile_plan_bytes(batch, num_ctas);

@@ -44,7 +44,7 @@
 // half's chain (its scores, 750 clocks of softmax per page, its product) leaves the
 // rest: measured per block of two halves 2900 clocks of which 2048 are MMAs. Over
 // e4m3 caches the softmax threads set the pace (the key scales' products and the
-// other layout cost half as much again, the widening of V takes issue slots):
+// other layout cost half as much again, the widening of V takes turns from them):
 // 128 requests over a 65536-token prefix 208 us, 169 us over a bf16 cache.
 // Few blocks (8192-token prefix, 64 requests: 22 us for seven blocks per CTA) are
 // bound by latency: 1.3 us a block, and some 10 us of start, first copies and rows.
@@ -59,8 +59,8 @@
 //    1184 us; an issuer warp per half: 892 us (their tests take issue slots from the
 //    softmax warps of the same scheduler).
 //  * e4m3 with a thread per row, each reading all of a page's key scales from shared
-//    memory: 512-token pieces of four prompts beside 28 single tokens 615 us; as it
-//    is 588 us.
+//    memory: 512-token pieces of four prompts beside 28 single tokens 615 us, not 588.
+//    V widened by rows of a thread, one 16-byte piece after the other: 548 us.
 #include <atomic>
 #include <cstring>
 
@@ -468,50 +468,47 @@ __device__ __forceinline__ void split_query_rows(uint8_t* qt, float* qs, int wq,
 // nv on zero), [dim halves][128 rows][128 B] swizzled: both dim halves from rows of
 // 128 swizzled bytes (CG 1), or this CTA's half from plain rows of 64 bytes (CG 2).
 // The scale is taken as (f 2^a) (2^b) with 1 <= |f| < 2, so that a scale far below
-// f16's smallest normal number keeps its bits until the last product. Thread tg
-// takes the 16-code pieces (tg & 3) + 4 hf of rows 32 rr + tg / 4: loads and stores
-// of a warp spread over all banks.
+// f16's smallest normal number keeps its bits until the last product. Thread tg takes
+// row tg: one scale and one look at it per block, and stores that spread over all
+// banks (so do the loads of swizzled rows; plain rows of 64 bytes take four turns, an
+// eighth of what the stores of the block take).
 template <int CG>
 __device__ __forceinline__ void widen_v(const uint8_t* codes, const float* vs, uint8_t* wide, int nv, int tg) {
+    const bool in = tg < nv;
+    const float sv = in ? vs[tg] : 0.f;
+    const uint32_t sb = __float_as_uint(sv);
+    const int e = (int)((sb >> 23) & 255u) - 127;
+    // one product where the scale is a normal f16 number (or zero) in all the warp's rows
+    const bool small = __any_sync(0xffffffffu, sv != 0.f && e < -14);
+    uint32_t s2 = pack_f16x2(sv, sv), p2 = 0;
+    if (small) {
+        // f 2^a (NaN or infinity stay what they are) and 2^b, b = e - a (0 where it underflows)
+        const int a = e < -14 ? -10 : 0;
+        const float fa = e == 128 ? sv : __uint_as_float((sb & 0x807fffffu) | (uint32_t)(127 + a) << 23);
+        const float fb = e == 128 ? 1.f : __uint_as_float((uint32_t)max(e - a + 127, 0) << 23);
+        s2 = pack_f16x2(fa, fa), p2 = pack_f16x2(fb, fb);
+    }
+    // One piece after the other: batches of loads and stores, which end sooner, hold up the
+    // softmax warps (pieces and decode, tile 32: four at once 619 us, two 584, one 546).
 #pragma unroll 1
-    for (int rr = 0; rr < 4; ++rr) {
-        const int row = 32 * rr + (tg >> 2);
-        const bool in = row < nv;
-        const float sv = in ? vs[row] : 0.f;
-        const uint32_t sb = __float_as_uint(sv);
-        const int e = (int)((sb >> 23) & 255u) - 127;
-        // one product where the scale is a normal f16 number (or zero) in all the warp's rows
-        const bool small = __any_sync(0xffffffffu, sv != 0.f && e < -14);
-        uint32_t s2 = pack_f16x2(sv, sv), p2 = 0;
+    for (int c16 = 0; c16 < 8 / CG; ++c16) {
+        uint4 w = *reinterpret_cast<const uint4*>(CG == 1 ? codes + tg * 128 + ((c16 ^ (tg & 7)) << 4) : codes + tg * 64 + c16 * 16);
+        if (!in) w = make_uint4(0, 0, 0, 0);
+        uint4 vl, vh;
+        e4m3x4_to_f16x2x2(w.x, vl.x, vl.y);
+        e4m3x4_to_f16x2x2(w.y, vl.z, vl.w);
+        e4m3x4_to_f16x2x2(w.z, vh.x, vh.y);
+        e4m3x4_to_f16x2x2(w.w, vh.z, vh.w);
+        vl.x = hmul2_u32(vl.x, s2), vl.y = hmul2_u32(vl.y, s2), vl.z = hmul2_u32(vl.z, s2), vl.w = hmul2_u32(vl.w, s2);
+        vh.x = hmul2_u32(vh.x, s2), vh.y = hmul2_u32(vh.y, s2), vh.z = hmul2_u32(vh.z, s2), vh.w = hmul2_u32(vh.w, s2);
         if (small) {
-            // f 2^a (NaN or infinity stay what they are) and 2^b, b = e - a (0 where it underflows)
-            const int a = e < -14 ? -10 : 0;
-            const float fa = e == 128 ? sv : __uint_as_float((sb & 0x807fffffu) | (uint32_t)(127 + a) << 23);
-            const float fb = e == 128 ? 1.f : __uint_as_float((uint32_t)max(e - a + 127, 0) << 23);
-            s2 = pack_f16x2(fa, fa), p2 = pack_f16x2(fb, fb);
+            vl.x = hmul2_u32(vl.x, p2), vl.y = hmul2_u32(vl.y, p2), vl.z = hmul2_u32(vl.z, p2), vl.w = hmul2_u32(vl.w, p2);
+            vh.x = hmul2_u32(vh.x, p2), vh.y = hmul2_u32(vh.y, p2), vh.z = hmul2_u32(vh.z, p2), vh.w = hmul2_u32(vh.w, p2);
         }
-#pragma unroll
-        for (int hf = 0; hf < 2 / CG; ++hf) {
-            const int c16 = (tg & 3) + 4 * hf;
-            uint4 vl = make_uint4(0, 0, 0, 0), vh = vl;
-            if (in) {
-                const uint4 w = *reinterpret_cast<const uint4*>(
-                    CG == 1 ? codes + row * 128 + ((c16 ^ (row & 7)) << 4) : codes + row * 64 + c16 * 16);
-                e4m3x4_to_f16x2x2(w.x, vl.x, vl.y);
-                e4m3x4_to_f16x2x2(w.y, vl.z, vl.w);
-                e4m3x4_to_f16x2x2(w.z, vh.x, vh.y);
-                e4m3x4_to_f16x2x2(w.w, vh.z, vh.w);
-                vl.x = hmul2_u32(vl.x, s2), vl.y = hmul2_u32(vl.y, s2), vl.z = hmul2_u32(vl.z, s2), vl.w = hmul2_u32(vl.w, s2);
-                vh.x = hmul2_u32(vh.x, s2), vh.y = hmul2_u32(vh.y, s2), vh.z = hmul2_u32(vh.z, s2), vh.w = hmul2_u32(vh.w, s2);
-                if (small) {
-                    vl.x = hmul2_u32(vl.x, p2), vl.y = hmul2_u32(vl.y, p2), vl.z = hmul2_u32(vl.z, p2), vl.w = hmul2_u32(vl.w, p2);
-                    vh.x = hmul2_u32(vh.x, p2), vh.y = hmul2_u32(vh.y, p2), vh.z = hmul2_u32(vh.z, p2), vh.w = hmul2_u32(vh.w, p2);
-                }
-            }
-            const int f0 = 2 * (tg & 3);
-            *reinterpret_cast<uint4*>(wide + hf * 16384 + row * 128 + ((f0 ^ (row & 7)) << 4)) = vl;
-            *reinterpret_cast<uint4*>(wide + hf * 16384 + row * 128 + (((f0 + 1) ^ (row & 7)) << 4)) = vh;
-        }
+        uint8_t* dst = wide + (c16 >> 2) * 16384 + tg * 128;
+        const int f0 = 2 * (c16 & 3);
+        *reinterpret_cast<uint4*>(dst + ((f0 ^ (tg & 7)) << 4)) = vl;
+        *reinterpret_cast<uint4*>(dst + (((f0 + 1) ^ (tg & 7)) << 4)) = vh;
     }
 }
 
