@@ -219,7 +219,7 @@ hpc_status hpc_prefill_combine(const hpc_tile_plan* plan, const float* split_o, 
     if (!split_o || !split_lse || !aligned(split_o, 16)) return HPC_ERR_INVALID_ARG;
     if (plan->num_tokens == 0) return HPC_OK;
     if (!out || !aligned(out, 16)) return HPC_ERR_INVALID_ARG;
-    return launched(launch_prefill_combine(plan->buf, plan->num_seqs, num_q_heads, plan->num_workers, plan->tile_tokens, split_o, split_lse,
+    return launched(launch_prefill_combine(plan->buf, plan->num_seqs, plan->num_tokens, num_q_heads, plan->num_workers, plan->tile_tokens, split_o, split_lse,
                                            out, out_lse, static_cast<cudaStream_t>(stream)));
 }
 

@@ -116,7 +116,7 @@ struct TileAttnArgs {
 cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s);
 int tile_default_ctas();
 
-cudaError_t launch_prefill_combine(const int32_t* plan, int S, int Hq, int C, int T, const float* split_o,
+cudaError_t launch_prefill_combine(const int32_t* plan, int S, int num_tokens, int Hq, int C, int T, const float* split_o,
                                    const float* split_lse, void* out, float* out_lse, cudaStream_t s);
 
 cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_workers, int T, const float* prefix_o,
@@ -125,6 +125,14 @@ cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_
                                   int q_len, cudaStream_t s);
 
 #if defined(__CUDACC__)
+
+// Whether a map in device memory is the one that the call's sizes describe (another
+// may have been planned into its buffer since).
+__device__ __forceinline__ bool tile_map_is(const int32_t* plan, int S, int Hkv, int C, int num_tokens, int mode, int T) {
+    const int4 a = *reinterpret_cast<const int4*>(plan + 4), b = *reinterpret_cast<const int4*>(plan + 8);
+    return a.y == S && a.z == Hkv && a.w == C && b.x == num_tokens && b.y == mode && plan[kTTileTokens] == T;
+}
+static_assert(kTBatch == 5 && kTNumKvHeads == 6 && kTNumWorkers == 7 && kTNumTokens == 8 && kTMode == 9, "header words");
 
 struct TilePos {
     int h, s, i, blk;

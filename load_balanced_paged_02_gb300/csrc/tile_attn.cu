@@ -164,7 +164,7 @@ struct TileParams {
     const int32_t* page_table;
     long long pt_stride;
     int* err;
-    int S, mode, num_q_heads, num_pages, num_kv_heads;
+    int S, mode, num_tokens, num_q_heads, num_pages, num_kv_heads;
     float* split_o;
     float* split_lse;
     __nv_bfloat16* out;
@@ -615,7 +615,9 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
     TileItem it;
     bool ok = true;
 
-    if (warp >= 8 && warp < 12) {
+    if (!tile_map_is(p.plan, p.S, p.num_kv_heads, (int)gridDim.x / CG, p.num_tokens, p.mode, T)) {
+        if (threadIdx.x == 0) atomicOr(p.err, (int)HPC_DEVERR_BAD_DESCRIPTOR);
+    } else if (warp >= 8 && warp < 12) {
         reg_dec<C::kRegsOther>();
         if (warp == 8) {
             // ============================ producer
@@ -1317,6 +1319,7 @@ cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s) {
     p.err = a.plan + kTError;
     p.S = a.S;
     p.mode = a.mode;
+    p.num_tokens = a.num_tokens;
     p.num_q_heads = a.num_q_heads;
     p.num_kv_heads = a.num_kv_heads;
     p.num_pages = a.num_pages;

@@ -121,12 +121,13 @@ static_assert(kRows * kBatch == 32 && kGroup % kRows == 0, "a warp's lanes; rows
 
 template <int T>
 __global__ void __launch_bounds__(kWarps * 32)
-    prefill_combine_kernel(const int32_t* plan, long long seqs_off, long long units_off, int Hq,
+    prefill_combine_kernel(const int32_t* plan, long long seqs_off, long long units_off, int S, int num_tokens, int Hq,
                            const float* split_o, const float* split_lse, __nv_bfloat16* out, float* out_lse) {
     grid_dependency_wait();  // the pieces come from the attention kernel
     grid_launch_dependents();
     const int4* starts = reinterpret_cast<const int4*>(plan + kHdrInts);
     const int j = blockIdx.x;
+    if (!tile_map_is(plan, S, Hq / kGroup, gridDim.x, num_tokens, kModePrefill, T)) return;
     const int4 a = starts[2 * j], e = starts[2 * (j + 1)];
     // the tile at the end of worker j's part is cut there, and began in it
     if (e.w == 0) return;
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 template <int T>
 __global__ void __launch_bounds__(kWarps * 32)
-    prefix_combine_kernel(const int32_t* prefix_plan, long long seqs_off, long long units_off, int S,
+    prefix_combine_kernel(const int32_t* prefix_plan, long long seqs_off, long long units_off, int S, int workers,
                           const float* prefix_o, const float* prefix_lse, const int32_t* pair_nsplit,
                           const int32_t* pair_split0, const float* split_o, const float* split_lse, __nv_bfloat16* out,
                           float* out_lse, int B, int Hq, int Q) {
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kWarps * 32)
             hi = mid;
     }
     const int4 q = seqs[lo];
-    if (tok >= q.x && tok < q.x + q.y && q.z > 0) {
+    if (tok >= q.x && tok < q.x + q.y && q.z > 0 && tile_map_is(prefix_plan, S, Hq / kGroup, workers, B * Q, kModePrefix, T)) {
         const long long per_head = *reinterpret_cast<const long long*>(prefix_plan + kTUnitsPerHead);
         const long long bucket = *reinterpret_cast<const long long*>(prefix_plan + kTBucket);
         const int i = (tok - q.x) / T, r = (tok - q.x) % T * kGroup + j;
@@ -199,10 +200,10 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 }  // namespace
 
-cudaError_t launch_prefill_combine(const int32_t* plan, int S, int Hq, int C, int T, const float* split_o,
+cudaError_t launch_prefill_combine(const int32_t* plan, int S, int num_tokens, int Hq, int C, int T, const float* split_o,
                                    const float* split_lse, void* out, float* out_lse, cudaStream_t s) {
     return launch_pdl(T == kTilePair ? prefill_combine_kernel<kTilePair> : prefill_combine_kernel<kTileCta>, dim3(C, kParts), dim3(kWarps * 32), 0, s, plan, tile_layout(S, C).seqs,
-                      tile_layout(S, C).units, Hq, split_o, split_lse, static_cast<__nv_bfloat16*>(out), out_lse);
+                      tile_layout(S, C).units, S, num_tokens, Hq, split_o, split_lse, static_cast<__nv_bfloat16*>(out), out_lse);
 }
 
 cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_workers, int T, const float* prefix_o,
@@ -213,7 +214,7 @@ cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_
     const PlanLayout L = plan_layout(B, Hkv, ctas);
     const long long blocks = ((long long)B * q_len * Hq / kRows + kWarps - 1) / kWarps;
     return launch_pdl(T == kTilePair ? prefix_combine_kernel<kTilePair> : prefix_combine_kernel<kTileCta>, dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, prefix_plan, t.seqs, t.units,
-                      S, prefix_o, prefix_lse, plan + L.pair_nsplit, plan + L.pair_split0, split_o, split_lse, out, out_lse,
+                      S, prefix_workers, prefix_o, prefix_lse, plan + L.pair_nsplit, plan + L.pair_split0, split_o, split_lse, out, out_lse,
                       B, Hq, q_len);
 }
 

@@ -299,3 +299,20 @@ def test_binding_refusals():
         hb.prefill(*[good[n] for n in "qkvtsl"], num_pages=c["pages"] + 1)
     with pytest.raises(hb.HpcError):
         hb.prefill(*[good[n] for n in "qkvtsl"], workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+def test_another_map_in_the_plans_buffer():
+    """A map planned for other sizes into the same buffer: the old plan's calls compute nothing and say so."""
+    for tile in (32, 64):
+        c = case([40, 3], [200, 3], 1, "bf16", 91)
+        plan = hb.hpc_prefill_plan(c["q_starts"], c["seq_lens"], 43, 1, c["table"].shape[1], num_ctas=8, tile_tokens=tile)
+        old = hb.TilePlanStruct.from_buffer_copy(plan.struct)
+        hb.hpc_prefill_plan(tl.i32([0, 43]), tl.i32([200]), 43, 1, c["table"].shape[1], num_ctas=8, tile_tokens=tile, plan=plan)
+        plan.struct = old
+        so, sl = hb.prefill_split_buffers(plan)
+        out = torch.full_like(c["q"], 7.0)
+        lse = torch.full((43, 8), 7.0, device="cuda")
+        hb.hpc_prefill_attn(c["q"], c["k_cache"], c["v_cache"], c["table"], plan, so, sl, out, lse)
+        hb.hpc_prefill_combine(plan, so, sl, out, lse)
+        assert hb.hpc_tile_read_error(plan) & 16  # HPC_DEVERR_BAD_DESCRIPTOR
+        assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
