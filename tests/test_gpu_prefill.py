@@ -316,3 +316,38 @@ def test_another_map_in_the_plans_buffer():
         hb.hpc_prefill_combine(plan, so, sl, out, lse)
         assert hb.hpc_tile_read_error(plan) & 16  # HPC_DEVERR_BAD_DESCRIPTOR
         assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
+
+
+@pytest.mark.parametrize("tile", [32, 64])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("growth", ["steady", "late page", "steps", "falling", "beyond exp2"])
+def test_scores_that_grow(growth, kv, tile):
+    """The reference maximum moves in the first page of a block, in its second, in every block, never,
+    and by more than float32's exponents hold."""
+    n, hkv = 520, 2
+    c = case([90, 1], [n, n - 64], hkv, kv, 97)
+    t = torch.arange(n, dtype=torch.float64)
+    size = {"steady": t / n * 40.0, "late page": torch.where(t % 128 >= 100, 30.0 + t / 16.0, 0.0), "steps": (t // 64) * 12.0,
+            "falling": 60.0 - t / n * 60.0, "beyond exp2": (t // 128) * 150.0}[growth]
+    sign = torch.where(torch.arange(128) % 3 == 0, -1.0, 1.0).double()
+    for b in range(2):
+        m = c["lens"][b]
+        gen = torch.Generator().manual_seed(b)
+        k = size[:m, None, None] * sign / np.sqrt(128.0) + 0.1 * torch.randn((m, hkv, 128), generator=gen, dtype=torch.float64)
+        v = torch.randn((m, hkv, 128), generator=gen, dtype=torch.float64)
+        pages = c["table"][b].cpu().long()
+        at = torch.arange(m)
+        slots = (pages[at // 64] * 64 + at % 64).int().cuda()
+        hb.hpc_kv_write(k.bfloat16().cuda(), v.bfloat16().cuda(), slots, c["k_cache"], c["v_cache"], c["k_scale"], c["v_scale"])
+        torch.cuda.synchronize()
+        for name in "kv":
+            page, off = slots.long() // 64, slots.long() % 64
+            x = c[name + "_cache"][page, off].float().double()
+            if kv == "e4m3":
+                x = x * c[name + "_scale"].double()[page, :, off].unsqueeze(-1)
+            c[name][0][b] = x
+    q = (sign.float() + 0.05 * torch.randn((91, 8 * hkv, 128), generator=torch.Generator().manual_seed(9)))
+    c["q"] = q.bfloat16().cuda()
+    for ctas in (None, 8):
+        out, lse, _ = run(c, tile_tokens=tile, num_ctas=ctas)
+        check(c, out, lse, growth)
