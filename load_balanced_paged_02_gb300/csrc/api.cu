@@ -151,21 +151,12 @@ int hpc_decode_suggest_num_ctas(const int32_t* h_seq_lens, int batch, int num_kv
 
 hpc_status hpc_decode_plan(const int32_t* d_seq_lens, int batch, int num_kv_heads, int num_ctas,
                            int min_chunks_per_cta, hpc_plan* plan, void* stream) {
-    if (!d_seq_lens || !plan || !plan->buf || min_chunks_per_cta < 0) return HPC_ERR_INVALID_ARG;
-    if (!sizes_ok(batch, num_kv_heads, num_ctas)) return HPC_ERR_INVALID_ARG;
-    if ((long long)num_kv_heads * batch > HPC_MAX_CTAS || !aligned(plan->buf, 16)) return HPC_ERR_INVALID_ARG;
-    if (plan->bytes < plan_bytes_ll(batch, num_kv_heads, num_ctas)) return HPC_ERR_WORKSPACE_TOO_SMALL;
-    plan->batch = batch;
-    plan->num_kv_heads = num_kv_heads;
-    plan->num_ctas = num_ctas;
-    plan->min_chunks = min_chunks_per_cta;
-    plan->mode = 0;
-    plan->max_tasks = (int)plan_layout(batch, num_kv_heads, num_ctas).max_tasks;
+    const hpc_status st = decode_plan_fill(d_seq_lens, batch, num_kv_heads, num_ctas, min_chunks_per_cta, plan);
+    if (st != HPC_OK) return st;
     cudaError_t e = launch_plan(d_seq_lens, batch, num_kv_heads, num_ctas, min_chunks_per_cta, plan->buf,
                                 static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? HPC_OK : HPC_ERR_CUDA;
 }
-
 hpc_status hpc_decode_plan_static(const int32_t* d_seq_lens, int batch, int num_kv_heads, int num_splits,
                                   hpc_plan* plan, void* stream) {
     if (!d_seq_lens || !plan || !plan->buf || num_splits < 1) return HPC_ERR_INVALID_ARG;
@@ -276,6 +267,22 @@ hpc_status attn_common(const void* q, const float* q_scale, const void* k_cache,
 }
 
 }  // namespace
+
+// hpc_decode_plan's checks, and the header it fills.
+hpc_status hpc::decode_plan_fill(const int32_t* d_seq_lens, int batch, int num_kv_heads, int num_ctas,
+                                 int min_chunks_per_cta, hpc_plan* plan) {
+    if (!d_seq_lens || !plan || !plan->buf || min_chunks_per_cta < 0) return HPC_ERR_INVALID_ARG;
+    if (!sizes_ok(batch, num_kv_heads, num_ctas)) return HPC_ERR_INVALID_ARG;
+    if ((long long)num_kv_heads * batch > HPC_MAX_CTAS || !aligned(plan->buf, 16)) return HPC_ERR_INVALID_ARG;
+    if (plan->bytes < plan_bytes_ll(batch, num_kv_heads, num_ctas)) return HPC_ERR_WORKSPACE_TOO_SMALL;
+    plan->batch = batch;
+    plan->num_kv_heads = num_kv_heads;
+    plan->num_ctas = num_ctas;
+    plan->min_chunks = min_chunks_per_cta;
+    plan->mode = 0;
+    plan->max_tasks = (int)plan_layout(batch, num_kv_heads, num_ctas).max_tasks;
+    return HPC_OK;
+}
 
 // Every host-side check that hpc_decode_plan, hpc_decode_attn and
 // hpc_decode_combine make for one step with one new token per request, except

@@ -41,9 +41,10 @@ int auto_tile(int mode, bool fp8, int num_tokens, int num_seqs) {
     return num_tokens >= from ? kTilePair : kTileCta;
 }
 
+// Checks of a planner's call; fills the header and the launch's arguments.
 hpc_status plan_common(const int32_t* d_starts, const int32_t* d_lens, int num_seqs, int num_tokens, int num_kv_heads,
                        int table_stride, int num_ctas, int min_blocks, int tile_tokens, int mode, int q_len,
-                       hpc_tile_plan* plan, void* stream) {
+                       hpc_tile_plan* plan, TilePlanArgs* args) {
     if (!d_starts || !d_lens || !plan || !plan->buf || !aligned(plan->buf, 16) || min_blocks < 0 || table_stride < 1)
         return HPC_ERR_INVALID_ARG;
     if (!seqs_ok(num_seqs, num_ctas) || !heads_ok(num_kv_heads) || !tokens_ok(num_tokens, num_seqs, num_kv_heads))
@@ -61,9 +62,17 @@ hpc_status plan_common(const int32_t* d_starts, const int32_t* d_lens, int num_s
     plan->q_len = q_len;
     plan->table_stride = table_stride;
     const long long max_len = (long long)table_stride * kChunk;
-    return launched(launch_tile_plan(d_starts, d_lens, num_seqs, num_tokens, num_kv_heads, plan->num_workers,
-                                     min_blocks, max_len > 2147483647LL ? 2147483647 : (int)max_len, mode, q_len, tile_tokens, plan->buf,
-                                     static_cast<cudaStream_t>(stream)));
+    *args = TilePlanArgs{d_starts, d_lens, num_seqs, num_tokens, num_kv_heads, plan->num_workers, min_blocks,
+                         max_len > 2147483647LL ? 2147483647 : (int)max_len, mode, q_len, tile_tokens, plan->buf};
+    return HPC_OK;
+}
+
+hpc_status prefix_plan_fill(const int32_t* d_group_starts, const int32_t* d_prefix_lens, int num_groups, int batch, int q_len,
+                            int num_kv_heads, int prefix_table_stride, int num_ctas, int min_blocks_per_cta, int tile_tokens,
+                            hpc_tile_plan* plan, TilePlanArgs* args) {
+    if (batch < 1 || batch > HPC_MAX_BATCH || q_len < 1 || q_len > HPC_MAX_Q_LEN) return HPC_ERR_INVALID_ARG;
+    return plan_common(d_group_starts, d_prefix_lens, num_groups, batch * q_len, num_kv_heads, prefix_table_stride, num_ctas,
+                       min_blocks_per_cta, tile_tokens, kModePrefix, q_len, plan, args);
 }
 
 hpc_status plan_check(const hpc_tile_plan* plan, int mode, int num_kv_heads) {
@@ -189,16 +198,19 @@ size_t hpc_prefix_split_rows(int num_groups, int batch, int q_len, int num_kv_he
 hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens, int batch, int num_tokens,
                             int num_kv_heads, int page_table_stride, int num_ctas, int min_blocks_per_cta,
                             int tile_tokens, hpc_tile_plan* plan, void* stream) {
-    return plan_common(d_q_starts, d_seq_lens, batch, num_tokens, num_kv_heads, page_table_stride, num_ctas,
-                       min_blocks_per_cta, tile_tokens, kModePrefill, 1, plan, stream);
+    TilePlanArgs a;
+    const hpc_status st = plan_common(d_q_starts, d_seq_lens, batch, num_tokens, num_kv_heads, page_table_stride, num_ctas,
+                                      min_blocks_per_cta, tile_tokens, kModePrefill, 1, plan, &a);
+    return st != HPC_OK ? st : launched(launch_tile_plan(a, static_cast<cudaStream_t>(stream)));
 }
 
 hpc_status hpc_prefix_plan(const int32_t* d_group_starts, const int32_t* d_prefix_lens, int num_groups, int batch,
                            int q_len, int num_kv_heads, int prefix_table_stride, int num_ctas, int min_blocks_per_cta,
                            int tile_tokens, hpc_tile_plan* plan, void* stream) {
-    if (batch < 1 || batch > HPC_MAX_BATCH || q_len < 1 || q_len > HPC_MAX_Q_LEN) return HPC_ERR_INVALID_ARG;
-    return plan_common(d_group_starts, d_prefix_lens, num_groups, batch * q_len, num_kv_heads, prefix_table_stride,
-                       num_ctas, min_blocks_per_cta, tile_tokens, kModePrefix, q_len, plan, stream);
+    TilePlanArgs a;
+    const hpc_status st = prefix_plan_fill(d_group_starts, d_prefix_lens, num_groups, batch, q_len, num_kv_heads,
+                                           prefix_table_stride, num_ctas, min_blocks_per_cta, tile_tokens, plan, &a);
+    return st != HPC_OK ? st : launched(launch_tile_plan(a, static_cast<cudaStream_t>(stream)));
 }
 
 hpc_status hpc_prefill_attn(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -326,10 +338,14 @@ hpc_status hpc_decode_shared_prefix(const void* q, const void* k_cache, const vo
     float* pl = reinterpret_cast<float*>(ws + w.prefix_lse);
     float* so = reinterpret_cast<float*>(ws + w.split_o);
     float* sl = reinterpret_cast<float*>(ws + w.split_lse);
-    if ((st = hpc_prefix_plan(group_starts, prefix_lens, num_groups, batch, q_len, num_kv_heads, prefix_table_stride,
-                              prefix_num_ctas, min_blocks_per_cta, tile_tokens, prefix_plan, stream)) != HPC_OK)
+    TilePlanArgs ta;
+    if ((st = prefix_plan_fill(group_starts, prefix_lens, num_groups, batch, q_len, num_kv_heads, prefix_table_stride,
+                               prefix_num_ctas, min_blocks_per_cta, tile_tokens, prefix_plan, &ta)) != HPC_OK)
         return st;
-    if ((st = hpc_decode_plan(seq_lens, batch, num_kv_heads, num_ctas, min_chunks_per_cta, plan, stream)) != HPC_OK) return st;
+    if ((st = decode_plan_fill(seq_lens, batch, num_kv_heads, num_ctas, min_chunks_per_cta, plan)) != HPC_OK) return st;
+    if ((st = launched(launch_both_plans(ta, seq_lens, batch, num_kv_heads, num_ctas, min_chunks_per_cta, plan->buf,
+                                         static_cast<cudaStream_t>(stream)))) != HPC_OK)
+        return st;
     if ((st = hpc_prefix_attn(q, k_cache, v_cache, k_scale, v_scale, kv_dtype, num_pages, prefix_table, prefix_table_stride,
                               num_q_heads, num_kv_heads, head_dim, page_size, prefix_plan, po, pl, stream)) != HPC_OK)
         return st;

@@ -88,6 +88,9 @@ int attn_default_ctas(int fp8);
 // CTAs of the shallow one-token instance resident in one wave (SMs x its CTAs per SM).
 int attn_shallow_ctas(int fp8);
 
+// hpc_decode_plan's host part (api.cu): its checks, and the header it fills.
+hpc_status decode_plan_fill(const int32_t* d_seq_lens, int batch, int num_kv_heads, int num_ctas, int min_chunks_per_cta,
+                            hpc_plan* plan);
 // Host-side checks of one decode step's arguments (api.cu): those that
 // hpc_decode_plan, hpc_decode_attn and hpc_decode_combine make, minus the ones
 // on a task map and split buffers, for entry points that provide those

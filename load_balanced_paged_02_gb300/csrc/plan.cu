@@ -14,6 +14,7 @@
 // Its split index s is the running descriptor count, and its task row is
 // s + cta (every earlier CTA contributed one terminator row).
 #include "hpc_internal.cuh"
+#include "tile_plan.cuh"
 
 namespace hpc {
 namespace {
@@ -141,17 +142,15 @@ __device__ void write_header(int32_t* buf, long long T, long long bucket, long l
     buf[13] = buf[14] = buf[15] = 0;
 }
 
-__global__ void __launch_bounds__(kPlanThreads, 1)
-    plan_balanced_kernel(const int32_t* __restrict__ seq_lens, int B, int Hkv, int C, int m,
-                         int32_t* __restrict__ buf) {
+// Block `block` of `blocks`.
+__device__ __forceinline__ void plan_balanced(int block, int blocks, const int32_t* __restrict__ seq_lens, int B, int Hkv,
+                                              int C, int m, int32_t* __restrict__ buf) {
     extern __shared__ int32_t pre[];  // [B + 1]
     __shared__ long long warp_sums[32];
     __shared__ unsigned warp_sums32[32];
     __shared__ int s_err;
     const int tid = threadIdx.x;
     if (tid == 0) s_err = 0;
-    grid_dependency_wait();   // seq_lens may come from the previous kernel
-    grid_launch_dependents();
     __syncthreads();
 
     const PlanLayout L = plan_layout(B, Hkv, C);
@@ -180,8 +179,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     // block computes the same chunk prefixes, bucket and error bits itself, and
     // starts its split indices at the number of descriptors of all earlier pairs,
     // which it sums in closed form (no block waits for another).
-    const int per_block = (int)(((P + kPlanThreads - 1) / kPlanThreads + gridDim.x - 1) / gridDim.x) * kPlanThreads;
-    const int p_lo = min(Pi, (int)blockIdx.x * per_block), p_hi = min(Pi, p_lo + per_block);
+    const int per_block = (int)(((P + kPlanThreads - 1) / kPlanThreads + blocks - 1) / blocks) * kPlanThreads;
+    const int p_lo = min(Pi, block * per_block), p_hi = min(Pi, p_lo + per_block);
     auto pair_splits = [&](int p) -> unsigned {
         const unsigned h = by_batch.div((unsigned)p), b = (unsigned)p - h * uB;
         const unsigned nb = (unsigned)(pre[b + 1] - pre[b]);
@@ -235,7 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         }
     }
     // the last block, whose running count is now every pair's, fills the rest
-    if (blockIdx.x != gridDim.x - 1) return;
+    if (block != blocks - 1) return;
     const long long total = running;
 
     // unused CTAs: an empty task list each, then terminators up to the row capacity
@@ -245,6 +244,29 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     if (tid == 0)
         write_header(buf, T, bucket, used, total, C, B, Hkv, m, L.max_tasks, 0, N, s_err);
 }
+
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    plan_balanced_kernel(const int32_t* __restrict__ seq_lens, int B, int Hkv, int C, int m,
+                         int32_t* __restrict__ buf) {
+    grid_dependency_wait();   // seq_lens may come from the previous kernel
+    grid_launch_dependents();
+    plan_balanced(blockIdx.x, gridDim.x, seq_lens, B, Hkv, C, m, buf);
+}
+
+// A tile map by block 0 and a task map by the others: decode over shared prefixes
+// needs both, and the two launches in turn cost 3.5 us more.
+template <int T>
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    both_plans_kernel(const TilePlanArgs a, const int32_t* __restrict__ seq_lens, int B, int Hkv, int C, int m,
+                      int32_t* __restrict__ buf) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (blockIdx.x == 0)
+        tileplan::tile_plan_block<T>(a);
+    else
+        plan_balanced(blockIdx.x - 1, gridDim.x - 1, seq_lens, B, Hkv, C, m, buf);
+}
+static_assert(kPlanThreads == tileplan::kThreads, "one launch for both planners");
 
 __global__ void __launch_bounds__(kPlanThreads, 1)
     plan_static_kernel(const int32_t* __restrict__ seq_lens, int B, int Hkv, int S,
@@ -328,13 +350,28 @@ cudaError_t set_smem(const void* fn, size_t bytes) {
 
 }  // namespace
 
+namespace {
+int balanced_blocks(int B, int Hkv) {
+    const long long tiles = ((long long)Hkv * B + kPlanThreads - 1) / kPlanThreads;
+    return (int)(tiles < kPlanMaxBlocks ? tiles : kPlanMaxBlocks);
+}
+}  // namespace
+
+cudaError_t launch_both_plans(const TilePlanArgs& a, const int32_t* seq_lens, int B, int Hkv, int C, int m, int32_t* buf,
+                              cudaStream_t s) {
+    const size_t smem = sizeof(int32_t) * ((size_t)B + 1);
+    const auto kernel = a.T == kTilePair ? both_plans_kernel<kTilePair> : both_plans_kernel<kTileCta>;
+    cudaError_t e = set_smem((const void*)kernel, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3(1 + balanced_blocks(B, Hkv)), dim3(kPlanThreads), smem, s, a, seq_lens, B, Hkv, C, m, buf);
+}
+
 cudaError_t launch_plan(const int32_t* seq_lens, int B, int Hkv, int C, int m, int32_t* buf,
                         cudaStream_t s) {
     const size_t smem = sizeof(int32_t) * ((size_t)B + 1);
     cudaError_t e = set_smem((const void*)plan_balanced_kernel, smem);
     if (e != cudaSuccess) return e;
-    const long long tiles = ((long long)Hkv * B + kPlanThreads - 1) / kPlanThreads;
-    const int blocks = (int)(tiles < kPlanMaxBlocks ? tiles : kPlanMaxBlocks);
+    const int blocks = balanced_blocks(B, Hkv);
     return launch_pdl(plan_balanced_kernel, dim3(blocks), dim3(kPlanThreads), smem, s, seq_lens, B, Hkv, C, m, buf);
 }
 

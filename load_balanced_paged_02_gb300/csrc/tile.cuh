@@ -92,8 +92,16 @@ __host__ __device__ inline long long tile_units(int mode, int n, int L, int i, i
 
 // ----------------------------------------------------------------- launchers
 
-cudaError_t launch_tile_plan(const int32_t* q_starts, const int32_t* lens, int S, int num_tokens, int Hkv, int C,
-                             int min_blocks, int max_len, int mode, int q_len, int T, int32_t* buf, cudaStream_t s);
+struct TilePlanArgs {
+    const int32_t* q_starts;
+    const int32_t* lens;
+    int S, num_tokens, Hkv, C, min_blocks, max_len, mode, q_len, T;
+    int32_t* buf;
+};
+cudaError_t launch_tile_plan(const TilePlanArgs& a, cudaStream_t s);
+// The same and the decode planner's map (launch_plan), in one launch.
+cudaError_t launch_both_plans(const TilePlanArgs& a, const int32_t* seq_lens, int B, int Hkv, int C, int m, int32_t* buf,
+                              cudaStream_t s);
 
 struct TileAttnArgs {
     const void* q;  // bf16 [num_tokens][Hq][128]
