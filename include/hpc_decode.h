@@ -535,7 +535,7 @@ hpc_status hpc_decode_noalloc(const void* q, const void* k_cache, const void* v_
  *             sequence's row of seqs: where each worker's run begins
  *   seqs      [num_seqs][4] {first query token, query tokens, keys, tiles before}
  *   units     int64 [num_seqs + 1]: units of the sequences before (a block is one
- *             unit; a tile of a prompt costs one more)
+ *             unit; a tile costs two more)
  * The buffer is deterministic: the same lengths give the same bytes.
  */
 typedef struct hpc_tile_plan {

@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kWarps * 32)
         const long long bucket = *reinterpret_cast<const long long*>(prefix_plan + kTBucket);
         const int i = (tok - q.x) / T, r = (tok - q.x) % T * kGroup + j;
         const int blocks = tile_blocks(kModePrefix, q.y, q.z, i, T);
-        const long long g0 = h * per_head + reinterpret_cast<const long long*>(prefix_plan + units_off)[lo] + (long long)i * blocks;
+        const long long g0 = h * per_head + reinterpret_cast<const long long*>(prefix_plan + units_off)[lo] +
+                             (long long)i * (blocks + kTileCost) + kTileCost;
         const long long tile = (long long)h * prefix_plan[kTTilesPerHead] + q.w + i;
         const long long c0 = g0 / bucket;  // one piece per worker that the tile's blocks touch
         prefix.row = (tile + c0) * (T * kGroup) + r;

@@ -155,7 +155,7 @@ __device__ __forceinline__ void tile_plan_block(const TilePlanArgs& a) {
                 else
                     i1 = mid;
             }
-            const long long blk = u - tile_units(mode, q.y, q.z, i0, T) - tile_cost(mode);
+            const long long blk = u - tile_units(mode, q.y, q.z, i0, T) - kTileCost;
             a = make_int4(h, lo, i0, blk > 0 ? (int)blk : 0);
             b = q;
         }

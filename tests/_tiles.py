@@ -134,7 +134,7 @@ def tile_map(mode, q_starts, lens, num_tokens, hkv, workers, min_blocks, T, q_le
     into equal runs."""
     S = len(lens)
     seqs, units_before, tiles_before = [], [0], 0
-    walk = []  # of one head: (sequence, tile, block or -1 for the fixed cost)
+    walk = []  # of one head: (sequence, tile, block, or -1 twice for the fixed cost)
     err = 0
     for s in range(S):
         a, b, L = q_starts[s] * q_len, q_starts[s + 1] * q_len, lens[s]
@@ -157,7 +157,7 @@ def tile_map(mode, q_starts, lens, num_tokens, hkv, workers, min_blocks, T, q_le
             for i in range(tiles):
                 end = L if mode == 1 else max(0, L - n + min(n, T * (i + 1)))
                 blocks = max(1, -(-end // 128)) if mode == 0 else -(-end // 128)
-                walk += ([(s, i, -1)] if mode == 0 else []) + [(s, i, blk) for blk in range(blocks)]
+                walk += [(s, i, -1)] * 2 + [(s, i, blk) for blk in range(blocks)]
         tiles_before += tiles
         units_before.append(len(walk))
     per_head, total = len(walk), len(walk) * hkv
