@@ -162,25 +162,22 @@ struct TileItem {
 // Walks the items of one worker's part of the map.
 template <int T>
 struct TileWalk {
-    const int4* seqs;
-    int S, mode, tiles_per_head;
+    int tiles_per_head;
     TilePos at, end;
     int4 q;  // at.s's row of seqs
 
-    __device__ __forceinline__ void start(const int32_t* plan, int S_, int mode_, int worker, long long seqs_off) {
+    __device__ __forceinline__ void start(const int32_t* plan, int worker) {
         const int4* st = reinterpret_cast<const int4*>(plan + kHdrInts + (long long)worker * 8);
         const int4 a = st[0], e = st[2];
         q = st[1];
         at = TilePos{a.x, a.y, a.z, a.w};
         end = TilePos{e.x, e.y, e.z, e.w};
-        seqs = reinterpret_cast<const int4*>(plan + seqs_off);
-        S = S_;
-        mode = mode_;
         tiles_per_head = plan[kTTilesPerHead];
     }
 
-    // The next item; false at the end of the worker's part.
-    __device__ __forceinline__ bool next(TileItem& it) {
+    // The next item; false at the end of the worker's part. (What the call knows is given
+    // each time, from its parameters, and takes no registers in between.)
+    __device__ __forceinline__ bool next(TileItem& it, int S, int mode, const int4* seqs) {
         for (;;) {
             const bool last = at.h == end.h && at.s == end.s && at.i == end.i;
             if (last && at.blk >= end.blk) return false;

@@ -405,62 +405,118 @@ __device__ __forceinline__ bool named_any_128(bool x) {
     return r != 0;
 }
 
+// Two e4m3 codes of two f16 numbers (round to nearest even, saturated), and back.
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t x) {
+    uint16_t y;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(x));
+    return y;
+}
+
+// This thread's row of O times al.
+__device__ __forceinline__ void scale_o(uint32_t ocol, float al) {
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+        float o[32];
+        tmem_ld32(ocol + c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= al;
+        tmem_st32(ocol + c, o);
+    }
+}
+
 // One half's bf16 query rows -> e4m3 hi / lo tiles in place ([128 rows][128 B]
 // each) and their power-of-two row scales. Lanes 4 j .. 4 j + 3 of warp wq take row
 // 32 wq + j + 8 u, u < 4; lane quarter qq reads bf16 dims [32 qq, 32 qq + 32), which
 // sit where row r of the hi tile (qq < 2) or of the lo tile goes, and writes the hi
 // and lo codes of its dims once all four have read.
+// An element x / scale, at most 448, has eight significant bits: an f16 number without
+// loss from 2^-17 on (below, both codes are zero). hi is its rounding to e4m3's four
+// bits, lo the exact remainder's (its loss: split_e4m3x8). In f16 pairs a row takes a
+// third fewer instructions than in float32, and a tile of few blocks waits for its rows.
 __device__ __forceinline__ void split_query_rows(uint8_t* qt, float* qs, int wq, int lane) {
 #pragma unroll 1
-    for (int u = 0; u < 4; ++u) {
-        const int r = 32 * wq + 8 * u + (lane >> 2), qq = lane & 3;
-        uint4 raw[4];
-        float amax = 0.f;
+    for (int u0 = 0; u0 < 4; ++u0) {
+        const int qq = lane & 3;
+        uint4 raw[1][4];
+        float amax[1], qinv[1];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            raw[c] = *reinterpret_cast<const uint4*>(qt + (qq >> 1) * 16384 + r * 128 + (((4 * (qq & 1) + c) ^ (r & 7)) << 4));
-            const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+        for (int u = 0; u < 1; ++u) {
+            const int r = 32 * wq + 8 * (u0 + u) + (lane >> 2);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+            for (int c = 0; c < 4; ++c)
+                raw[u][c] = *reinterpret_cast<const uint4*>(qt + (qq >> 1) * 16384 + r * 128 + (((4 * (qq & 1) + c) ^ (r & 7)) << 4));
         }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        __syncwarp();  // the row's other lanes have read it
-        // the smallest power of two 2^ex with amax / 2^ex <= 448: q / 2^ex is exact
-        // (rows under 2^-90 keep fewer bits: their scores are 0 to float32 anyway; an
-        // infinite element makes the row's scores infinite or NaN)
-        float qscale = 1.f, qinv = 1.f;
-        if (amax > 3.4e38f) {
-            qscale = amax;
-        } else if (amax > 0.f) {
-            int e;
-            const float m = frexpf(amax * (1.f / 448.f), &e);
-            const int ex = max(m == 0.5f ? e - 1 : e, -100);
-            qscale = ldexpf(1.f, ex);
-            qinv = ldexpf(1.f, -ex);
-        }
-        if (qq == 0) qs[r] = qscale;
 #pragma unroll
-        for (int c2 = 0; c2 < 2; ++c2) {
-            uint2 hp[2], lp[2];
+        for (int u = 0; u < 1; ++u) {
+            __nv_bfloat162 am2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const uint4 x4 = raw[2 * c2 + v];
-                const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
-                float x[8];
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t w[4] = {raw[u][c].x, raw[u][c].y, raw[u][c].z, raw[u][c].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[2 * j] = __uint_as_float(w[j] << 16) * qinv;
-                    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * qinv;
+                    const uint32_t x = w[j] & 0x7fff7fffu;
+                    am2 = __hmax2(am2, *reinterpret_cast<const __nv_bfloat162*>(&x));
                 }
-                split_e4m3x8(x, hp[v], lp[v]);
             }
-            const int off = r * 128 + (((2 * qq + c2) ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(qt + off) = make_uint4(hp[0].x, hp[0].y, hp[1].x, hp[1].y);
-            *reinterpret_cast<uint4*>(qt + 16384 + off) = make_uint4(lp[0].x, lp[0].y, lp[1].x, lp[1].y);
+            amax[u] = fmaxf(__low2float(am2), __high2float(am2));
         }
-        __syncwarp();
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+            for (int u = 0; u < 1; ++u) amax[u] = fmaxf(amax[u], __shfl_xor_sync(0xffffffffu, amax[u], o));
+        __syncwarp();  // the rows' other lanes have read them
+#pragma unroll
+        for (int u = 0; u < 1; ++u) {
+            // the smallest power of two 2^ex with amax / 2^ex <= 448 = 1.75 2^8: q / 2^ex is exact
+            // (rows under 2^-90 keep fewer bits: their scores are 0 to float32 anyway; an
+            // infinite element makes the row's scores infinite or NaN)
+            const uint32_t ab = __float_as_uint(amax[u]);
+            const int ex = max((int)(ab >> 23) - 127 - 8 + ((ab & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
+            float qscale = 1.f;
+            qinv[u] = 1.f;
+            if (amax[u] > 3.4e38f) {
+                qscale = amax[u];
+            } else if (amax[u] > 0.f) {
+                qscale = __uint_as_float((uint32_t)(127 + ex) << 23);
+                qinv[u] = __uint_as_float((uint32_t)(127 - ex) << 23);
+            }
+            if (qq == 0) qs[32 * wq + 8 * (u0 + u) + (lane >> 2)] = qscale;
+        }
+#pragma unroll
+        for (int u = 0; u < 1; ++u) {
+            const int r = 32 * wq + 8 * (u0 + u) + (lane >> 2);
+#pragma unroll
+            for (int c2 = 0; c2 < 2; ++c2) {
+                uint32_t hp[4], lp[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint4 x4 = raw[u][2 * c2 + (v >> 1)];
+                    const uint32_t w[2] = {v & 1 ? x4.z : x4.x, v & 1 ? x4.w : x4.y};
+                    uint16_t h[2], l[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 y = mul2(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)),
+                                              make_float2(qinv[u], qinv[u]));
+                        const uint32_t x = pack_f16x2(y.x, y.y);
+                        h[j] = f16x2_to_e4m3x2(x);
+                        const uint32_t hb = e4m3x2_to_f16x2(h[j]);
+                        const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&hb));
+                        l[j] = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
+                    }
+                    hp[v] = h[0] | (uint32_t)h[1] << 16;
+                    lp[v] = l[0] | (uint32_t)l[1] << 16;
+                }
+                const int off = r * 128 + (((2 * qq + c2) ^ (r & 7)) << 4);
+                *reinterpret_cast<uint4*>(qt + off) = make_uint4(hp[0], hp[1], hp[2], hp[3]);
+                *reinterpret_cast<uint4*>(qt + 16384 + off) = make_uint4(lp[0], lp[1], lp[2], lp[3]);
+            }
+        }
     }
 }
 
@@ -611,7 +667,8 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
     grid_launch_dependents();
 
     TileWalk<T> walk;
-    walk.start(p.plan, p.S, p.mode, worker, p.seqs_off);
+    walk.start(p.plan, worker);
+    auto next = [&](TileItem& x) { return walk.next(x, p.S, p.mode, reinterpret_cast<const int4*>(p.plan + p.seqs_off)); };
     TileItem it;
     bool ok = true;
 
@@ -623,7 +680,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
             // ============================ producer
             uint32_t blks = 0, started = 0;  // blocks filled, and begun
             int nd[2] = {0, 0};
-            while (ok && walk.next(it)) {
+            while (ok && next(it)) {
                 if (lane == 0) {
                     for (int t = 0; t < 2 && ok; ++t) {
                         if (it.i * T + t * kHalfTokens * CG >= it.n) break;
@@ -739,7 +796,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                 }
                 mma_commit<CG>(el, &sfull[t]);
             };
-            while (ok && walk.next(it)) {
+            while (ok && next(it)) {
                 const int halves = it.n - it.i * T > kHalfTokens * CG ? 2 : 1;
                 // first S of both halves
                 ok = wait_block(blks);
@@ -752,7 +809,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                     if (t == halves - 1) mma_commit<CG>(el, &empty[2 * (blks % NB)]);
                 }
                 for (int b = it.b0; b < it.b1 && ok; ++b, ++blks) {
-                    const uint32_t vst = 2 * (blks % NB) + 1, next = (blks + 1) % NB;
+                    const uint32_t vst = 2 * (blks % NB) + 1, after = (blks + 1) % NB;
                     const bool more = b + 1 < it.b1;
                     uint8_t* vt = FP8 ? smem + LY::kWideV + (blks % kWide) * C::kWideBytes : ring + (size_t)vst * C::kStageBytes;
                     const uint64_t v = dv + (FP8 ? (blks % kWide) * (C::kWideBytes >> 4) : vst * (C::kStageBytes >> 4));
@@ -788,9 +845,9 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                                 if (!ok) break;
                                 tc_fence_after();
                             }
-                            issue_s(t, next);
+                            issue_s(t, after);
                             if (b + 2 == it.b1) mma_commit<CG>(el, &qempty[t]);
-                            if (t == halves - 1) mma_commit<CG>(el, &empty[2 * next]);
+                            if (t == halves - 1) mma_commit<CG>(el, &empty[2 * after]);
                         } else {
                             mma_commit<CG>(el, &ofull[t]);
                         }
@@ -803,7 +860,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
             // slots, told to the leader in order
             uint32_t blks = 0;
             int nd[2] = {0, 0};
-            while (ok && walk.next(it)) {
+            while (ok && next(it)) {
                 const int halves = it.n - it.i * T > kHalfTokens * CG ? 2 : 1;
                 if constexpr (!FP8)
                     for (int t = 0; t < halves && ok; ++t, ++nd[t - 1]) {
@@ -833,7 +890,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
             const int tg = threadIdx.x & 127, wq = warp & 3;
             uint32_t blks = 0;
             int nd[2] = {0, 0};
-            while (ok && walk.next(it)) {
+            while (ok && next(it)) {
                 const int halves = it.n - it.i * T > kHalfTokens * CG ? 2 : 1;
                 for (int t = 0; t < halves && ok; ++t) {
                     ok = wait_warp(&qfull[t], nd[t] & 1, abort_flag);
@@ -880,7 +937,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
         uint32_t blks = 0;  // blocks of this CTA
         uint32_t ns = 0;    // score tiles of this half
         int nd = 0;
-        while (ok && walk.next(it)) {
+        while (ok && next(it)) {
             if (it.n - it.i * T <= t * kHalfTokens * CG) {  // an empty half
                 blks += it.b1 - it.b0;
                 continue;
@@ -975,13 +1032,24 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                                 sum[2 * gi + 1] = a[1].x + a[1].y;
                             }
                         };
-                        // as below, the sum being of 16 keys
-                        const bool fresh = __any_sync(0xffffffffu, mq[0] == kNegInf || mq[1] == kNegInf || mq[2] == kNegInf || mq[3] == kNegInf);
-                        if (!fresh) exps();
-                        bool high = false;
+                        // As below, the sum being of 16 keys, and the second pass by the same
+                        // instructions: a tile of few blocks waits for the instruction cache (32
+                        // prompts of 512 tokens behind 88: 324 us with a copy of its own, 306 so;
+                        // over bf16 caches the copy is the faster form, 650 against 690 us for an
+                        // 8192-token prompt).
+                        bool take = __any_sync(0xffffffffu, mq[0] == kNegInf || mq[1] == kNegInf || mq[2] == kNegInf || mq[3] == kNegInf);
+                        bool taken = false;
+#pragma unroll 1
+                        for (;;) {
+                            if (!take) {
+                                exps();
+                                bool high = false;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) high |= !(sum[i] <= kSumLimit / 4);
-                        if (fresh || __any_sync(0xffffffffu, high)) {
+                                for (int i = 0; i < 4; ++i) high |= !(sum[i] <= kSumLimit / 4);
+                                if (taken || !__any_sync(0xffffffffu, high)) break;
+                            }
+                            take = false;
+                            taken = true;
                             float al[4];
                             bool resc = false;
 #pragma unroll
@@ -1004,19 +1072,10 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                                     break;
                                 }
                                 tc_fence_after();
-                                const float alr = row_value(al, lane);
-#pragma unroll 1
-                                for (int c = 0; c < 128; c += 32) {
-                                    float o[32];
-                                    tmem_ld32(ocol + c, o);
-                                    tmem_ld_wait();
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] *= alr;
-                                    tmem_st32(ocol + c, o);
-                                }
+                                scale_o(ocol, row_value(al, lane));
                             }
-                            exps();
                         }
+                        if (!ok) break;
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
@@ -1086,15 +1145,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                                 }
                                 tc_fence_after();
                                 const float al = resc ? fast_exp2(m - mraw) : 1.f;
-#pragma unroll 1
-                                for (int c = 0; c < 128; c += 32) {
-                                    float o[32];
-                                    tmem_ld32(ocol + c, o);
-                                    tmem_ld_wait();
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] *= al;
-                                    tmem_st32(ocol + c, o);
-                                }
+                                scale_o(ocol, al);
                                 l *= al;
                             }
                             if (move) m = mraw;
