@@ -31,11 +31,11 @@ bool tokens_ok(int num_tokens, int num_seqs, int num_kv_heads) {
 // (96 over e4m3 caches and for prefix groups), of 32 on single CTAs below. A pair halves
 // the copies and the shared memory traffic of a row, a single CTA wastes fewer rows on
 // short sequences. Whole calls, us, tile 32 / 64, eight prompts of 4096 keys: 32 new
-// tokens each 51 / 55, 64 75 / 66, 96 100 / 98, 512 383 / 326; e4m3 54 / 65, 85 / 79,
-// 115 / 120, 471 / 421. 512-token pieces of four prompts beside 28 single tokens (64 on
-// average): 496 / 455, e4m3 548 / 609. Attention over an 8192-token prefix: 48 requests
-// 20 / 22, 64 22 / 22, 128 31 / 31, 256 49 / 47; e4m3 27 / 29, 31 / 30, 43 / 42, 67 / 65.
-// Groups of 16, 5, 1 and 42 requests of four tokens: 43 / 54.
+// tokens each 52 / 56, 64 75 / 65, 96 101 / 98, 512 378 / 320; e4m3 53 / 65, 83 / 79,
+// 112 / 121, 455 / 419. 512-token pieces of four prompts beside 28 single tokens (64 on
+// average): 492 / 450, e4m3 552 / 607. Attention over an 8192-token prefix: 48 requests
+// 18 / 19, 64 20 / 19, 128 29 / 28, 256 47 / 46; e4m3 25 / 26, 27 / 27, 39 / 38, 64 / 63.
+// Groups of 16, 5, 1 and 42 requests of four tokens: 37 / 43.
 int auto_tile(int mode, bool fp8, int num_tokens, int num_seqs) {
     const long long from = (mode == kModePrefill && !fp8 ? kTilePair : 3 * kTilePair / 2) * (long long)num_seqs;
     return num_tokens >= from ? kTilePair : kTileCta;

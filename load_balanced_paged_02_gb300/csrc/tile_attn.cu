@@ -38,16 +38,17 @@
 // Every wait is bounded; on expiry the CTA records HPC_DEVERR_WAIT_TIMEOUT.
 //
 // Bound by: the tensor core and its power, over bf16 caches. Prompt of 8192 tokens,
-// 64 / 8 heads: 680 us, 1618 TFLOP/s (0.85 of the library's 8192^3 product in
-// bursts, 0.94 of the same over seconds); the tensor pipe is active for 75 % of the
+// 64 / 8 heads: 660 us, 1665 TFLOP/s (0.87 of the library's 8192^3 product in
+// bursts, 0.97 of the same over seconds); the tensor pipe is active for 75 % of the
 // cycles and the clock falls from 2070 to 1950 MHz at the board's power limit. A
 // half's chain (its scores, 750 clocks of softmax per page, its product) leaves the
 // rest: measured per block of two halves 2900 clocks of which 2048 are MMAs. Over
 // e4m3 caches the softmax threads set the pace (the key scales' products and the
 // other layout cost half as much again, the widening of V takes turns from them):
-// 128 requests over a 65536-token prefix 208 us, 169 us over a bf16 cache.
-// Few blocks (8192-token prefix, 64 requests: 22 us for seven blocks per CTA) are
-// bound by latency: 1.3 us a block, and some 10 us of start, first copies and rows.
+// 128 requests over a 65536-token prefix 207 us, 160 us over a bf16 cache.
+// Few blocks (8192-token prefix, 64 requests: 20 us for seven blocks per CTA) are
+// bound by latency: 1.4 us a block, 2.5 us to the first one, 3.2 us for a tile's
+// float32 rows.
 //
 // What else was measured (8192-token prompt unless said otherwise):
 //  * the maximum of each block taken before its P goes out: 749 us; page by page:
@@ -61,6 +62,7 @@
 //  * e4m3 with a thread per row, each reading all of a page's key scales from shared
 //    memory: 512-token pieces of four prompts beside 28 single tokens 615 us, not 588.
 //    V widened by rows of a thread, one 16-byte piece after the other: 548 us.
+//  * output rows with the next columns' load under way: 668 against 660 us.
 #include <atomic>
 #include <cstring>
 

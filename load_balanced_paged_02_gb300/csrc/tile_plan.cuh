@@ -6,7 +6,9 @@
 // in place of requests.
 //
 // A block of 1024 threads runs tile_plan_block: alone (tile_plan.cu), or beside the
-// decode planner's blocks (plan.cu).
+// decode planner's blocks (plan.cu). Bound by latency: 3.5 us for a prefix, 4.5 us for
+// 4 to 60 prompts, launch included (7 us with the tile size as a variable, whose closed
+// forms then divide in 64 bits, and a scan for each of the two sums).
 #pragma once
 
 #include "tile.cuh"
