@@ -81,10 +81,9 @@ using attn::wait_bounded;
 
 constexpr int kHalfRows = 128;
 constexpr int kQBytes = 32768;           // a half's query rows: [2 dim halves][128 rows][128 B]
-// 64 keys' P that add up to more than 2^10 hold one above 2^4: then the maximum is
-// looked at and the reference moves to it. Up to there every P is at most 2^10.
+// 64 keys' P that add up to more than 2^10 hold one above 2^4: then the row's reference
+// moves to their maximum. Up to there every P is at most 2^10.
 constexpr float kSumLimit = 1024.f;
-constexpr float kRescaleLog2 = 4.0f;
 constexpr int kMetaRing = 8;             // blocks whose page checks (and, e4m3, scales) are kept
 constexpr int kWide = 2;                 // e4m3: f16 V tiles
 constexpr int kOutBytes = 2048;          // a softmax warp's staging of 32 output rows x 64 B
@@ -1010,7 +1009,9 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                             }
                         }
                         // P of the page, to TMEM as f16 pairs; the thread's parts of the rows' sums
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f}, neg[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) neg[i] = -mq[i];  // (no finite sum where mq is not)
                         auto exps = [&]() {
 #pragma unroll
                             for (int gi = 0; gi < 2; ++gi) {
@@ -1021,9 +1022,8 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
 #pragma unroll
                                     for (int k = 0; k < 2; ++k) {
                                         const int i = 2 * gi + k;
-                                        const float neg = mq[i] == kNegInf ? 0.f : -mq[i];
                                         const float* y = s[gi] + 4 * j + 2 * k;
-                                        float2 x = fma2(make_float2(y[0], y[1]), make_float2(scq[i], scq[i]), make_float2(neg, neg));
+                                        float2 x = fma2(make_float2(y[0], y[1]), make_float2(scq[i], scq[i]), make_float2(neg[i], neg[i]));
                                         x.x = fast_exp2(x.x);
                                         x.y = fast_exp2(x.y);
                                         a[k] = add2(a[k], x);
@@ -1039,7 +1039,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                         // prompts of 512 tokens behind 88: 324 us with a copy of its own, 306 so;
                         // over bf16 caches the copy is the faster form, 650 against 690 us for an
                         // 8192-token prompt).
-                        bool take = __any_sync(0xffffffffu, mq[0] == kNegInf || mq[1] == kNegInf || mq[2] == kNegInf || mq[3] == kNegInf);
+                        bool take = __all_sync(0xffffffffu, mq[0] == kNegInf && mq[1] == kNegInf && mq[2] == kNegInf && mq[3] == kNegInf);
                         bool taken = false;
 #pragma unroll 1
                         for (;;) {
@@ -1062,10 +1062,14 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                                 for (int j = 1; j < 8; ++j) mx = max3(mx, x[4 * j], x[4 * j + 1]);
                                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * scq[i];
-                                const bool move = mx > mq[i] + kRescaleLog2 || (mq[i] == kNegInf && mx != kNegInf);
+                                float all = sum[i];  // the row's
+                                all += __shfl_xor_sync(0xffffffffu, all, 1);
+                                all += __shfl_xor_sync(0xffffffffu, all, 2);
+                                const bool move = mq[i] == kNegInf ? mx != kNegInf : mx > mq[i] && !(all <= kSumLimit);
                                 al[i] = move && mq[i] != kNegInf ? fast_exp2(mq[i] - mx) : 1.f;
                                 resc |= move && mq[i] != kNegInf;
                                 if (move) mq[i] = mx;
+                                neg[i] = mq[i] == kNegInf ? 0.f : -mq[i];
                                 lq[i] *= al[i];
                             }
                             if (__any_sync(0xffffffffu, resc)) {
@@ -1123,10 +1127,12 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                         // Against the reference as it stands. The sum tells whether that still serves:
                         // one up to kSumLimit bounds every P. Only where it is above, or where a row has
                         // no reference yet, the keys' maximum is taken and they are done again.
-                        const bool fresh = __any_sync(0xffffffffu, m == kNegInf);
+                        // (A row's own sum decides, so that its result does not depend on the warp's
+                        // other rows.)
+                        const bool fresh = m == kNegInf, all_fresh = __all_sync(0xffffffffu, fresh);
                         float sum = 0.f;
-                        if (!fresh) sum = exps(-m);
-                        if (fresh || __any_sync(0xffffffffu, !(sum <= kSumLimit))) {
+                        if (!all_fresh) sum = exps(-m);  // (not finite where m is not)
+                        if (all_fresh || __any_sync(0xffffffffu, !(sum <= kSumLimit))) {
                             float mx[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) mx[i] = fmaxf(s[i], s[60 + i]);
@@ -1135,7 +1141,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[c + i], s[c + 4 + i]);
                             const float mraw = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
-                            const bool move = mraw > m + kRescaleLog2 || (m == kNegInf && mraw != kNegInf);
+                            const bool move = fresh ? mraw != kNegInf : mraw > m && !(sum <= kSumLimit);
                             const bool resc = move && m != kNegInf;
                             if (__any_sync(0xffffffffu, resc)) {
                                 // O holds everything before these keys once their predecessors' product

@@ -321,7 +321,7 @@ def test_another_map_in_the_plans_buffer():
 @pytest.mark.parametrize("tile", [32, 64])
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("growth", ["steady", "late page", "steps", "falling", "beyond exp2"])
-def test_scores_that_grow(growth, kv, tile):
+def test_references_that_move(growth, kv, tile):
     """The reference maximum moves in the first page of a block, in its second, in every block, never,
     and by more than float32's exponents hold."""
     n, hkv = 520, 2
@@ -351,3 +351,33 @@ def test_scores_that_grow(growth, kv, tile):
     for ctas in (None, 8):
         out, lse, _ = run(c, tile_tokens=tile, num_ctas=ctas)
         check(c, out, lse, growth)
+
+
+@pytest.mark.parametrize("tile", [32, 64])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_queries_of_every_size(kv, tile):
+    """Query rows from 1e-30 to 1e4, rows whose elements span 2^40, rows of zeros; then rows with an
+    infinity or a NaN, which leave the others bit for bit as they were."""
+    c = case([70, 33], [200, 333], 1, kv, seed=131)
+    gen = torch.Generator().manual_seed(7)
+    rows = torch.tensor([1e-30, 1e-10, 1e-4, 1.0, 30.0, 1e4]).repeat(200)[:103 * 8].view(103, 8, 1)
+    spans = torch.exp2(-40.0 * torch.rand((103, 8, 128), generator=gen)) * (torch.arange(103) % 5 == 0).view(103, 1, 1)
+    q = torch.randn((103, 8, 128), generator=gen) * rows
+    q = torch.where(spans > 0, torch.sign(q) * spans * 4.0, q)
+    q[11] = 0.0
+    c["q"] = q.bfloat16().cuda()
+    for ctas in (None, 5):
+        out, lse, _ = run(c, tile_tokens=tile, num_ctas=ctas)
+        check(c, out, lse, "sizes")
+        kept = c["q"]
+        c["q"] = kept.clone()
+        bad = [(3, 1, 5, float("inf")), (40, 7, 0, float("nan")), (69, 0, 127, -float("inf")), (100, 3, 64, float("nan"))]
+        for t, h, d, x in bad:
+            c["q"][t, h, d] = x
+        out2, lse2, _ = run(c, tile_tokens=tile, num_ctas=ctas)
+        same = torch.ones((103, 8), dtype=torch.bool, device="cuda")
+        for t, h, d, x in bad:
+            same[t, h] = False
+            assert not torch.isfinite(out2[t, h].float()).all()
+        assert torch.equal(out[same], out2[same]) and torch.equal(lse[same], lse2[same])
+        c["q"] = kept
