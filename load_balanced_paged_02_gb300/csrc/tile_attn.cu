@@ -40,12 +40,12 @@
 // Bound by: the tensor core and its power, over bf16 caches. Prompt of 8192 tokens,
 // 64 / 8 heads: 660 us, 1665 TFLOP/s (0.87 of the library's 8192^3 product in
 // bursts, 0.97 of the same over seconds); the tensor pipe is active for 75 % of the
-// cycles and the clock falls from 2070 to 1950 MHz at the board's power limit. A
+// cycles and the clock falls from 2070 to 1750-1790 MHz at the board's power limit. A
 // half's chain (its scores, 750 clocks of softmax per page, its product) leaves the
 // rest: measured per block of two halves 2900 clocks of which 2048 are MMAs. Over
 // e4m3 caches the softmax threads set the pace (the key scales' products and the
 // other layout cost half as much again, the widening of V takes turns from them):
-// 128 requests over a 65536-token prefix 207 us, 160 us over a bf16 cache.
+// 128 requests over a 65536-token prefix 215 us, 158 us over a bf16 cache.
 // Few blocks (8192-token prefix, 64 requests: 20 us for seven blocks per CTA) are
 // bound by latency: 1.4 us a block, 2.5 us to the first one, 3.2 us for a tile's
 // float32 rows.
