@@ -216,3 +216,26 @@ def test_the_operators_together(kv):
         ref = tl.attend(q[P + st[b]:P + st[b + 1]], ke[rowsb], ve[rowsb], [P + i + 1 for i in range(n)])
         tl.check_rows(wo[st[b]:st[b + 1]], wl[st[b]:st[b + 1]], ref, fp8, f"request {b}")
         tl.check_rows(do[b:b + 1], dl[b:b + 1], tuple(x[-1:] for x in ref), fp8, f"decode {b}")
+
+
+def test_another_map_in_the_plans_buffer():
+    """A prefix map planned for other groups into the same buffer: the old plan's call computes nothing and
+    says so, and the merge takes the requests' own tokens alone."""
+    for tile in (32, 64):
+        c = case([5, 3], [200, 70], [9, 64, 1, 130, 20, 7, 65, 3], 1, "bf16", 1, 171)
+        pplan = hb.hpc_prefix_plan(c["gstarts"], c["plens"], 8, 1, c["ptable"].shape[1], num_ctas=8, tile_tokens=tile)
+        old = hb.TilePlanStruct.from_buffer_copy(pplan.struct)
+        hb.hpc_prefix_plan(tl.i32([0, 8]), tl.i32([70]), 8, 1, c["ptable"].shape[1], num_ctas=8, tile_tokens=tile, plan=pplan)
+        pplan.struct = old
+        po, pl = hb.prefix_split_buffers(pplan)
+        po.fill_(float("nan"))
+        hb.hpc_prefix_attn(c["q"], c["k_cache"], c["v_cache"], c["ptable"], pplan, po, pl)
+        assert hb.hpc_tile_read_error(pplan) & 16  # HPC_DEVERR_BAD_DESCRIPTOR
+        plan = hb.hpc_decode_plan(c["seq_lens"], 1)
+        so, sl = hb.split_buffers(plan)
+        hb.hpc_decode_attn(c["q"], c["k_cache"], c["v_cache"], c["table"], c["seq_lens"], plan, so, sl)
+        out, lse = torch.empty_like(c["q"]), torch.empty((8, 8), device="cuda")
+        hb.hpc_prefix_combine(pplan, po, pl, plan, so, sl, out, lse)
+        for b in range(8):
+            n = c["lens"][b]
+            tl.check_rows(out[b:b + 1], lse[b:b + 1], tl.attend(c["q"][b:b + 1], c["k"][0][b], c["v"][0][b], [n]), False, f"request {b}")
