@@ -239,3 +239,21 @@ def test_another_map_in_the_plans_buffer():
         for b in range(8):
             n = c["lens"][b]
             tl.check_rows(out[b:b + 1], lse[b:b + 1], tl.attend(c["q"][b:b + 1], c["k"][0][b], c["v"][0][b], [n]), False, f"request {b}")
+
+
+def test_the_largest_batch():
+    """As many requests as the planners take (their length sums no longer fit the default shared memory)."""
+    B = 16384
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(0, 4, B)]
+    c = case([B - 5, 3], [70, 129], lens, 1, "bf16", 1, 181, first=1)
+    out, lse, pplan, plan = run(c)
+    assert hb.hpc_tile_read_error(pplan) == 0
+    for b in [0, 1, 2, 31, 32, 33, 4095, 8191, 12288, B - 5, B - 4, B - 3, B - 2, B - 1] + [int(x) for x in rng.integers(0, B, 40)]:
+        k, v, n = c["k"][0][b], c["v"][0][b], c["lens"][b]
+        p = 0
+        for g in range(2):
+            if c["starts"][g] <= b < c["starts"][g + 1]:
+                p = c["prefixes"][g]
+                k, v = torch.cat([c["k"][1][g], k]), torch.cat([c["v"][1][g], v])
+        tl.check_rows(out[b:b + 1], lse[b:b + 1], tl.attend(c["q"][b:b + 1], k, v, [p + n]), False, f"request {b}")
