@@ -7,9 +7,9 @@
 // worker) into the output rows; whole tiles were written by the attention kernel.
 // prefix_combine_kernel: for every (request, new token, query head) the pieces
 // of its group's prefix tile and the splits of its own suffix.
-// Both: a warp per four rows, lane k owning dims [4 k, 4 k + 4). Bound by the reads
+// Both: a warp per few rows, lane k owning dims [4 k, 4 k + 4). Bound by the reads
 // of the partial rows, mostly from L2 (20 MB of an 8192-token prefix and 64 requests
-// in 6.7 us, 3 TB/s), and by launch latency and a chain of dependent loads for small
+// in 5.6 us, 3.6 TB/s), and by launch latency and a chain of dependent loads for small
 // batches (4.7 us).
 #include "tile.cuh"
 
@@ -19,6 +19,11 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 8;
 constexpr int kParts = 8;  // blocks per tile
+// Rows that a warp merges at once. Prefixes: two (64 requests over an 8192-token prefix
+// 5.6 us; four 6.8 us, one 8.3 us: more warps against more loads of the same map). Prompts,
+// whose kParts blocks go over a tile's rows in turns: four (four short prompts 4.9 us, two
+// 6.3 us).
+constexpr int kPromptRows = 4, kPrefixRows = 2;
 
 __device__ __forceinline__ void store_row(__nv_bfloat16* out, long long row, int lane, const float4& v) {
     __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
@@ -37,13 +42,14 @@ struct Run {
     int n;
 };
 
-constexpr int kRows = 4;   // neighbouring rows (query heads of one token) that a warp merges at once
-constexpr int kBatch = 8;  // pieces whose LSEs the warp holds at once: lane 8 r + i has piece i of row r
-
-// A warp merges two runs into kRows neighbouring rows: v[r] gets dims [4 k, 4 k + 4)
-// of row r (k the lane), lse the LSE of row lane / kBatch. A piece without a visible
-// key (LSE -inf) has weight 0 and is not added.
+// A warp merges two runs into kRows neighbouring rows (query heads of one token): v[r]
+// gets dims [4 k, 4 k + 4) of row r (k the lane), lse the LSE of row lane / kBatch. A
+// piece without a visible key (LSE -inf) has weight 0 and is not added. The warp holds
+// the LSEs of kBatch pieces at once: lane kBatch r + i has piece i of row r.
+template <int kRows>
 __device__ __forceinline__ void merge_runs(const Run& a, const Run& b, int lane, float4 (&v)[kRows], float& lse) {
+    constexpr int kBatch = 32 / kRows;
+    static_assert(kGroup % kRows == 0, "rows of one token");
     const int n = a.n + b.n, lr = lane / kBatch, li = lane % kBatch;
     float m = -INFINITY, sum = 0.f;  // of row lr
 #pragma unroll
@@ -113,13 +119,14 @@ __device__ __forceinline__ void merge_runs(const Run& a, const Run& b, int lane,
 }
 
 // Writes merged rows to output rows orow, orow + 1, ...
+template <int kRows>
 __device__ __forceinline__ void store_rows(__nv_bfloat16* out, float* out_lse, long long orow, int lane,
                                            const float4 (&v)[kRows], float lse) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) store_row(out, orow + r, lane, v[r]);
+    constexpr int kBatch = 32 / kRows;
     if (out_lse && lane % kBatch == 0) out_lse[orow + lane / kBatch] = lse;
 }
-static_assert(kRows * kBatch == 32 && kGroup % kRows == 0, "a warp's lanes; rows of one token");
 
 template <int T>
 __global__ void __launch_bounds__(kWarps * 32)
@@ -141,6 +148,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     const long long end = e.x * per_head + reinterpret_cast<const long long*>(plan + units_off)[e.y] +
                           tile_units(kModePrefill, q.y, q.z, e.z + 1, T);
     const int last = (int)((end - 1) / bucket);  // the worker with the tile's last block
+    constexpr int kRows = kPromptRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int r = (blockIdx.y * kWarps + warp) * kRows; r < T * kGroup; r += kParts * kWarps * kRows) {
         const int tok = e.z * T + r / kGroup;
@@ -163,6 +171,7 @@ __global__ void __launch_bounds__(kWarps * 32)
                           float* out_lse, int B, int Hq, int Q) {
     grid_dependency_wait();  // the pieces come from the attention kernels
     grid_launch_dependents();
+    constexpr int kRows = kPrefixRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long orow = ((long long)blockIdx.x * kWarps + warp) * kRows;  // (request, new token, query head)
     if (orow >= (long long)B * Q * Hq) return;
@@ -215,9 +224,10 @@ cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_
                                   int q_len, cudaStream_t s) {
     const TileLayout t = tile_layout(S, prefix_workers);
     const PlanLayout L = plan_layout(B, Hkv, ctas);
-    const long long blocks = ((long long)B * q_len * Hq / kRows + kWarps - 1) / kWarps;
-    return launch_pdl(T == kTilePair ? prefix_combine_kernel<kTilePair> : prefix_combine_kernel<kTileCta>, dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, prefix_plan, t.seqs, t.units,
-                      S, prefix_workers, prefix_o, prefix_lse, plan + L.pair_nsplit, plan + L.pair_split0, split_o, split_lse, out, out_lse,
+    const long long rows = (long long)B * q_len * Hq;
+    const long long blocks = (rows / kPrefixRows + kWarps - 1) / kWarps;
+    return launch_pdl(T == kTilePair ? prefix_combine_kernel<kTilePair> : prefix_combine_kernel<kTileCta>, dim3((unsigned)blocks),
+                      dim3(kWarps * 32), 0, s, prefix_plan, t.seqs, t.units, S, prefix_workers, prefix_o, prefix_lse, plan + L.pair_nsplit, plan + L.pair_split0, split_o, split_lse, out, out_lse,
                       B, Hq, q_len);
 }
 
