@@ -18,12 +18,12 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 8;
-constexpr int kParts = 8;  // blocks per tile
 // Rows that a warp merges at once. Prefixes: two (64 requests over an 8192-token prefix
-// 5.6 us; four 6.8 us, one 8.3 us: more warps against more loads of the same map). Prompts,
-// whose kParts blocks go over a tile's rows in turns: four (four short prompts 4.9 us, two
-// 6.3 us).
+// 5.6 us; four 6.8 us, one 8.3 us: more warps against more loads of the same map). Prompts:
+// four, with as many blocks per tile as it has rows for (four short prompts 4.9 us, 6.4 us
+// in two turns of half as many; two rows 5.8 us and more).
 constexpr int kPromptRows = 4, kPrefixRows = 2;
+constexpr int prompt_parts(int T) { return T * kGroup / (kWarps * kPromptRows); }  // blocks per tile
 
 __device__ __forceinline__ void store_row(__nv_bfloat16* out, long long row, int lane, const float4& v) {
     __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
@@ -150,17 +150,16 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int last = (int)((end - 1) / bucket);  // the worker with the tile's last block
     constexpr int kRows = kPromptRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int r = (blockIdx.y * kWarps + warp) * kRows; r < T * kGroup; r += kParts * kWarps * kRows) {
-        const int tok = e.z * T + r / kGroup;
-        if (tok >= q.y) break;
-        // worker j's piece, and one of every worker after it up to the last
-        const Run head{split_o, split_lse, (2LL * j + 1) * (T * kGroup) + r, 0, 1};
-        const Run rest{split_o, split_lse, (2LL * j + 2) * (T * kGroup) + r, 2LL * T * kGroup, last - j};
-        float4 v[kRows];
-        float lse;
-        merge_runs(head, rest, lane, v, lse);
-        store_rows(out, out_lse, (long long)(q.x + tok) * Hq + e.x * kGroup + r % kGroup, lane, v, lse);
-    }
+    const int r = (blockIdx.y * kWarps + warp) * kRows;
+    const int tok = e.z * T + r / kGroup;
+    if (tok >= q.y) return;
+    // worker j's piece, and one of every worker after it up to the last
+    const Run head{split_o, split_lse, (2LL * j + 1) * (T * kGroup) + r, 0, 1};
+    const Run rest{split_o, split_lse, (2LL * j + 2) * (T * kGroup) + r, 2LL * T * kGroup, last - j};
+    float4 v[kRows];
+    float lse;
+    merge_runs(head, rest, lane, v, lse);
+    store_rows(out, out_lse, (long long)(q.x + tok) * Hq + e.x * kGroup + r % kGroup, lane, v, lse);
 }
 
 template <int T>
@@ -214,8 +213,10 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 cudaError_t launch_prefill_combine(const int32_t* plan, int S, int num_tokens, int Hq, int C, int T, const float* split_o,
                                    const float* split_lse, void* out, float* out_lse, cudaStream_t s) {
-    return launch_pdl(T == kTilePair ? prefill_combine_kernel<kTilePair> : prefill_combine_kernel<kTileCta>, dim3(C, kParts), dim3(kWarps * 32), 0, s, plan, tile_layout(S, C).seqs,
-                      tile_layout(S, C).units, S, num_tokens, Hq, split_o, split_lse, static_cast<__nv_bfloat16*>(out), out_lse);
+    const TileLayout t = tile_layout(S, C);
+    return launch_pdl(T == kTilePair ? prefill_combine_kernel<kTilePair> : prefill_combine_kernel<kTileCta>,
+                      dim3(C, prompt_parts(T)), dim3(kWarps * 32), 0, s, plan, t.seqs, t.units, S, num_tokens, Hq, split_o,
+                      split_lse, static_cast<__nv_bfloat16*>(out), out_lse);
 }
 
 cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_workers, int T, const float* prefix_o,
@@ -226,9 +227,9 @@ cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_
     const PlanLayout L = plan_layout(B, Hkv, ctas);
     const long long rows = (long long)B * q_len * Hq;
     const long long blocks = (rows / kPrefixRows + kWarps - 1) / kWarps;
-    return launch_pdl(T == kTilePair ? prefix_combine_kernel<kTilePair> : prefix_combine_kernel<kTileCta>, dim3((unsigned)blocks),
-                      dim3(kWarps * 32), 0, s, prefix_plan, t.seqs, t.units, S, prefix_workers, prefix_o, prefix_lse, plan + L.pair_nsplit, plan + L.pair_split0, split_o, split_lse, out, out_lse,
-                      B, Hq, q_len);
+    return launch_pdl(T == kTilePair ? prefix_combine_kernel<kTilePair> : prefix_combine_kernel<kTileCta>,
+                      dim3((unsigned)blocks), dim3(kWarps * 32), 0, s, prefix_plan, t.seqs, t.units, S, prefix_workers, prefix_o,
+                      prefix_lse, plan + L.pair_nsplit, plan + L.pair_split0, split_o, split_lse, out, out_lse, B, Hq, q_len);
 }
 
 }  // namespace hpc
