@@ -581,8 +581,9 @@ size_t hpc_prefix_split_rows(int num_groups, int batch, int q_len, int num_kv_he
  *                 of a bf16 cache here, of the call's cache in hpc_prefill
  *                 (num_ctas 1 takes 32)
  * One block, integer only, reads the lengths on the device. A sequence whose
- * starts decrease or leave [0, num_tokens] is passed over
- * (HPC_DEVERR_BAD_DESCRIPTOR); keys beyond the page table's row are not seen
+ * starts decrease or leave [0, num_tokens] is passed over, and so is one that
+ * begins before the end of an earlier sequence whose starts do neither
+ * (HPC_DEVERR_BAD_DESCRIPTOR): no query row has two sequences; keys beyond the page table's row are not seen
  * (HPC_DEVERR_PAGE_OUT_OF_RANGE); a negative length counts as 0
  * (HPC_DEVERR_NEGATIVE_LENGTH).
  * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_WORKSPACE_TOO_SMALL, HPC_ERR_CUDA.

@@ -53,6 +53,29 @@ __device__ __forceinline__ void scan_exclusive(long long& v, int& w, long long& 
     __syncthreads();
 }
 
+// Exclusive running maximum of values >= 0 over the block; the total receives the maximum.
+// All threads call it.
+__device__ __forceinline__ int max_exclusive(int v, int& total, int* sums) {
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x = max(x, a);
+    }
+    if (lane == 31) sums[wp] = x;
+    __syncthreads();
+    int before = 0;  // of the warps before, and of the lanes before
+    total = 0;
+    for (int k = 0; k < kWarps; ++k) {
+        total = max(total, sums[k]);
+        if (k == wp - 1) before = total;
+    }
+    const int left = __shfl_up_sync(0xffffffffu, x, 1);
+    __syncthreads();
+    return lane > 0 ? max(before, left) : before;
+}
+
 // T is a constant here, so that the closed forms of tile_units divide by shifts.
 template <int T>
 __device__ __forceinline__ void tile_plan_block(const TilePlanArgs& a) {
@@ -72,9 +95,15 @@ __device__ __forceinline__ void tile_plan_block(const TilePlanArgs& a) {
     long long unit_base = 0;
     int tile_base = 0;
     int err = 0;
+    // A query row belongs to one sequence: split rows are counted on that. While no sequence's
+    // starts decrease or leave the range, every sequence begins where the one before ends; from
+    // the first one that does, each has to begin at or past the ends of all before it.
+    bool apart = true;
+    int ends = 0;  // the largest end so far of a sequence whose starts are in order (kept once !apart)
     for (int s0 = 0; s0 < S; s0 += kThreads) {
         const int s = s0 + threadIdx.x;
         int q0 = 0, n = 0, L = 0;
+        bool fits = true;
         if (s < S) {
             const long long a = (long long)q_starts[s] * q_len, b = (long long)q_starts[s + 1] * q_len;
             L = lens[s];
@@ -86,11 +115,23 @@ __device__ __forceinline__ void tile_plan_block(const TilePlanArgs& a) {
                 err |= (int)HPC_DEVERR_PAGE_OUT_OF_RANGE;
                 L = max_len;
             }
-            if (a < 0 || b < a || b > num_tokens) {
-                err |= (int)HPC_DEVERR_BAD_DESCRIPTOR;
-            } else {
+            fits = a >= 0 && b >= a && b <= num_tokens;
+            if (fits) {
                 q0 = (int)a;
                 n = (int)(b - a);
+            }
+        }
+        if (__syncthreads_or(!fits) && apart) {
+            apart = false;
+            ends = s0 > 0 ? q_starts[s0] * q_len : 0;  // (in range: all before were in order)
+        }
+        if (!apart) {
+            int most;
+            const int before = max(ends, max_exclusive(fits ? q0 + n : 0, most, tile_sums));
+            ends = max(ends, most);
+            if (s < S && (!fits || q0 < before)) {
+                err |= (int)HPC_DEVERR_BAD_DESCRIPTOR;
+                q0 = n = 0;
             }
         }
         const bool any = n > 0 && (mode == kModePrefill || L > 0);
