@@ -533,7 +533,9 @@ hpc_status hpc_decode_noalloc(const void* q, const void* k_cache, const void* v_
  *             tiles_per_head, q_len, error word, tile_tokens, 0, 0}
  *   starts    [num_workers + 1][8] {kv head, sequence, tile, block} and that
  *             sequence's row of seqs: where each worker's run begins
- *   seqs      [num_seqs][4] {first query token, query tokens, keys, tiles before}
+ *   seqs      [num_seqs][4] {first query token, query tokens, keys, tiles before};
+ *             a sequence that is passed over has no query tokens and begins at the
+ *             largest end before it, so that first query tokens never decrease
  *   units     int64 [num_seqs + 1]: units of the sequences before (a block is one
  *             unit; a tile costs two more)
  * The buffer is deterministic: the same lengths give the same bytes.

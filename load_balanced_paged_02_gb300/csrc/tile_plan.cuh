@@ -131,7 +131,8 @@ __device__ __forceinline__ void tile_plan_block(const TilePlanArgs& a) {
             ends = max(ends, most);
             if (s < S && (!fits || q0 < before)) {
                 err |= (int)HPC_DEVERR_BAD_DESCRIPTOR;
-                q0 = n = 0;
+                q0 = before;  // first rows never fall: prefix_combine_kernel searches them
+                n = 0;
             }
         }
         const bool any = n > 0 && (mode == kModePrefill || L > 0);

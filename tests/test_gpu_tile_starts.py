@@ -107,6 +107,7 @@ def test_maps(mode, T):
         before = words[at + 4 * S:at + 4 * S + 2 * (S + 1)].view(np.int64)
         for s, ((a, n), (t, u)) in enumerate(zip(seqs, walk)):
             assert list(rows[s][1:]) == [n, lens[s], tiles] and (a is None or rows[s][0] == a), f"map {rep}, sequence {s}"
+            assert s == 0 or rows[s][0] >= rows[s - 1][0], f"map {rep}: first rows fall at {s}"
             assert before[s] == units
             tiles, units = tiles + t, units + u
         assert before[S] == units
@@ -166,3 +167,26 @@ def test_prefix_attention_of_such_starts():
         hb.hpc_prefix_attn(q, c["k_cache"], c["v_cache"], c["tables"][0], plan, po[:rows], pl[:rows])
         assert hb.hpc_tile_read_error(plan) == 16
         assert bool((po[rows:] == 7).all()) and bool((pl[rows:] == 7).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tile", [32, 64])
+@pytest.mark.parametrize("q_len", [1, 2])
+def test_groups_beside_passed_over_ones_keep_their_prefix(q_len, tile):
+    """A merged row finds its group's prefix whatever groups around it are passed over."""
+    own, hkv = [5, 64, 0, 130, 17, 1, 70, 9], 1
+    for st in ([0, 4, 99, 4, 8], [0, 3, 1, 3, 8], [-2, 0, 5, 2, 8], [2, 2, 6, 0, 6], [0, 8, 0, 8, 0], [4, 0, 4, 4, 9]):
+        plens = [200, 128, 70, 300]
+        c = tl.make_cache([own, plens], hkv, "bf16", 21)
+        q = tl.make_q((8, 8, 128) if q_len == 1 else (8, q_len, 8, 128), 22)
+        out, lse, pplan, plan = hb.decode_shared_prefix(q, c["k_cache"], c["v_cache"], c["tables"][0], tl.i32(own), c["tables"][1],
+                                                        tl.i32(plens), tl.i32(st), tile_tokens=tile, prefix_num_ctas=6)
+        assert hb.hpc_tile_read_error(pplan) == 16 and hb.hpc_decode_read_error(plan) == 0
+        groups = taken(st, 8)
+        for b in range(8):
+            k, v, p = c["k"][0][b], c["v"][0][b], 0
+            for g, (a, n) in enumerate(groups):
+                if n and a <= b < a + n:
+                    k, v, p = torch.cat([c["k"][1][g], k]), torch.cat([c["v"][1][g], v]), plens[g]
+            ref = tl.attend(q[b].reshape(q_len, 8, 128), k, v, [p + max(0, own[b] - q_len + i + 1) for i in range(q_len)])
+            tl.check_rows(out[b].reshape(q_len, 8, 128), lse[b].reshape(q_len, 8), ref, False, f"starts {st}, request {b}")
