@@ -611,8 +611,11 @@ hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens
  * not see never reach it through its maximum and sum; a value of V that is not
  * finite reaches every row of the 128-token blocks that hold its token.
  * A page id outside [0, num_pages) hides its 64 tokens
- * (HPC_DEVERR_PAGE_OUT_OF_RANGE). Where another map has been planned into the
- * plan's buffer since, nothing is computed (HPC_DEVERR_BAD_DESCRIPTOR).
+ * (HPC_DEVERR_PAGE_OUT_OF_RANGE). Where a map of other sizes (sequences, tokens, KV
+ * heads, workers, tile, new tokens per request) has been planned into the plan's
+ * buffer since, nothing is computed (HPC_DEVERR_BAD_DESCRIPTOR); one of the same sizes
+ * is taken for the call's, and its keys beyond this call's table are not seen
+ * (HPC_DEVERR_PAGE_OUT_OF_RANGE).
  * Errors: HPC_ERR_INVALID_ARG (also a plan made for other sizes or by
  * hpc_prefix_plan), HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA.
  */

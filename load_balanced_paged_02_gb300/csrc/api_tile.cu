@@ -134,6 +134,7 @@ hpc_status attn_common(const void* q, const void* k_cache, const void* v_cache, 
     a.num_workers = plan->num_workers;
     a.tile_tokens = plan->tile_tokens;
     a.mode = mode;
+    a.q_len = plan->q_len;
     a.split_o = split_o;
     a.split_lse = split_lse;
     a.out = out;

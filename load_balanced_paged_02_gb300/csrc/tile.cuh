@@ -119,7 +119,7 @@ struct TileAttnArgs {
     int pt_stride;
     int S, num_tokens, num_q_heads, num_kv_heads;
     int32_t* plan;
-    int num_workers, mode, tile_tokens;
+    int num_workers, mode, tile_tokens, q_len;
     float* split_o;
     float* split_lse;
     void* out;       // prompts only
@@ -138,13 +138,16 @@ cudaError_t launch_prefix_combine(const int32_t* prefix_plan, int S, int prefix_
 
 #if defined(__CUDACC__)
 
-// Whether a map in device memory is the one that the call's sizes describe (another
-// may have been planned into its buffer since).
-__device__ __forceinline__ bool tile_map_is(const int32_t* plan, int S, int Hkv, int C, int num_tokens, int mode, int T) {
+// Whether a map in device memory has the sizes that the call describes (another may have
+// been planned into its buffer since).
+__device__ __forceinline__ bool tile_map_is(const int32_t* plan, int S, int Hkv, int C, int num_tokens, int mode, int q_len,
+                                            int T) {
     const int4 a = *reinterpret_cast<const int4*>(plan + 4), b = *reinterpret_cast<const int4*>(plan + 8);
-    return a.y == S && a.z == Hkv && a.w == C && b.x == num_tokens && b.y == mode && plan[kTTileTokens] == T;
+    return a.y == S && a.z == Hkv && a.w == C && b.x == num_tokens && b.y == mode && b.w == q_len &&
+           plan[kTTileTokens] == T;
 }
-static_assert(kTBatch == 5 && kTNumKvHeads == 6 && kTNumWorkers == 7 && kTNumTokens == 8 && kTMode == 9, "header words");
+static_assert(kTBatch == 5 && kTNumKvHeads == 6 && kTNumWorkers == 7 && kTNumTokens == 8 && kTMode == 9 && kTQLen == 11,
+              "header words");
 
 struct TilePos {
     int h, s, i, blk;

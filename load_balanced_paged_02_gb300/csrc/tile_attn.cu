@@ -165,7 +165,7 @@ struct TileParams {
     const int32_t* page_table;
     long long pt_stride;
     int* err;
-    int S, mode, num_tokens, num_q_heads, num_pages, num_kv_heads;
+    int S, mode, q_len, num_tokens, num_q_heads, num_pages, num_kv_heads;
     float* split_o;
     float* split_lse;
     __nv_bfloat16* out;
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
     TileItem it;
     bool ok = true;
 
-    if (!tile_map_is(p.plan, p.S, p.num_kv_heads, (int)gridDim.x / CG, p.num_tokens, p.mode, T)) {
+    if (!tile_map_is(p.plan, p.S, p.num_kv_heads, (int)gridDim.x / CG, p.num_tokens, p.mode, p.q_len, T)) {
         if (threadIdx.x == 0) atomicOr(p.err, (int)HPC_DEVERR_BAD_DESCRIPTOR);
     } else if (warp >= 8 && warp < 12) {
         reg_dec<C::kRegsOther>();
@@ -702,10 +702,11 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                 for (int c0 = 2 * it.b0; c0 < 2 * it.b1 && ok; c0 += 32) {
                     const int c = c0 + lane;
                     // a page past the last or with an id out of range becomes the page after
-                    // the pool's last one: the copy fills its rows with zeros
+                    // the pool's last one: the copy fills its rows with zeros. (Pages past the
+                    // table's row: only a map planned since for a wider table has such.)
                     int page = p.num_pages;
                     if (c < 2 * it.b1 && c < pages) {
-                        page = prow[c];
+                        page = c < p.pt_stride ? prow[c] : -1;
                         if ((unsigned)page >= (unsigned)p.num_pages) {
                             atomicOr(p.err, (int)HPC_DEVERR_PAGE_OUT_OF_RANGE);
                             page = p.num_pages;
@@ -1378,6 +1379,7 @@ cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s) {
     p.err = a.plan + kTError;
     p.S = a.S;
     p.mode = a.mode;
+    p.q_len = a.q_len;
     p.num_tokens = a.num_tokens;
     p.num_q_heads = a.num_q_heads;
     p.num_kv_heads = a.num_kv_heads;

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     grid_launch_dependents();
     const int4* starts = reinterpret_cast<const int4*>(plan + kHdrInts);
     const int j = blockIdx.x;
-    if (!tile_map_is(plan, S, Hq / kGroup, gridDim.x, num_tokens, kModePrefill, T)) return;
+    if (!tile_map_is(plan, S, Hq / kGroup, gridDim.x, num_tokens, kModePrefill, 1, T)) return;
     const int4 a = starts[2 * j], e = starts[2 * (j + 1)];
     // the tile at the end of worker j's part is cut there, and began in it
     if (e.w == 0) return;
@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(kWarps * 32)
             hi = mid;
     }
     const int4 q = seqs[lo];
-    if (tok >= q.x && tok < q.x + q.y && q.z > 0 && tile_map_is(prefix_plan, S, Hq / kGroup, workers, B * Q, kModePrefix, T)) {
+    if (tok >= q.x && tok < q.x + q.y && q.z > 0 &&
+        tile_map_is(prefix_plan, S, Hq / kGroup, workers, B * Q, kModePrefix, Q, T)) {
         const long long per_head = *reinterpret_cast<const long long*>(prefix_plan + kTUnitsPerHead);
         const long long bucket = *reinterpret_cast<const long long*>(prefix_plan + kTBucket);
         const int i = (tok - q.x) / T, r = (tok - q.x) % T * kGroup + j;
