@@ -515,7 +515,7 @@ def _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages):
     """Checks of a paged cache; returns its hpc_kv_dtype, pages in use, page size and KV heads."""
     kvd = kv_dtype_of(k_cache)
     shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
+    if len(shape) != 4 or shape[3] != HEAD_DIM or v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
         raise HpcError(what, detail="k_cache and v_cache must be [pages, 64, heads, 128] of one type")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise HpcError(what, detail="k_cache and v_cache must be contiguous")

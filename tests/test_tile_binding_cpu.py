@@ -1,0 +1,49 @@
+"""Refusals of the prompt, shared-prefix and cache calls in the Python binding, by shapes alone (CPU tensors, which
+the calls refuse too, but later: each test looks for the earlier message)."""
+import pytest
+import torch
+
+from load_balanced_paged_02_gb300 import _build
+from load_balanced_paged_02_gb300 import binding as hb
+
+
+@pytest.fixture(scope="module", autouse=True)
+def L():
+    _build.build()
+    return hb.lib()
+
+
+def cache(dim=128, pages=4, heads=1):
+    return torch.zeros((pages, 64, heads, dim), dtype=torch.bfloat16)
+
+
+def i32(*values):
+    return torch.tensor(values, dtype=torch.int32)
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def prefill(q=None, k=None, v=None, **kw):
+    return hb.prefill(bf16(9, 8, 128) if q is None else q, cache() if k is None else k, cache() if v is None else v,
+                      i32(0).view(1, 1), i32(0, 9), i32(9), num_ctas=4, **kw)
+
+
+def shared(q=None, k=None, v=None, batch=2, **kw):
+    return hb.decode_shared_prefix(bf16(batch, 8, 128) if q is None else q, cache() if k is None else k,
+                                   cache() if v is None else v, torch.zeros((batch, 1), dtype=torch.int32),
+                                   torch.zeros(batch, dtype=torch.int32), i32(0).view(1, 1), i32(9), i32(0, batch), num_ctas=4,
+                                   prefix_num_ctas=4, **kw)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 256])
+def test_caches_of_another_head_dimension(dim):
+    """The kernels read rows of 128 elements whatever the cache's last dimension is."""
+    k = cache(dim)
+    calls = [lambda: prefill(k=k, v=k), lambda: shared(k=k, v=k),
+             lambda: hb.hpc_kv_write(bf16(3, 1, 128), bf16(3, 1, 128), i32(0, 1, 2), k, k),
+             lambda: hb.hpc_kv_read(k, k, i32(0).view(1, 1), i32(0, 3), bf16(3, 1, 128), bf16(3, 1, 128))]
+    for call in calls:
+        with pytest.raises(hb.HpcError, match="heads, 128"):
+            call()
