@@ -506,9 +506,13 @@ def _tensor(what, t, shape, dtype):
         raise HpcError(what, detail=f"must be a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
-def _query(what, q):
+def _query(what, q, new_tokens=False):
+    """A packed query [tokens, heads, 128], or with new_tokens one of a decode step: [B, heads, 128] or
+    [B, q_len, heads, 128]."""
     if q.dtype != torch.bfloat16 or not q.is_contiguous():
         raise HpcError(what, detail="q must be a contiguous bfloat16 tensor")
+    if not (q.dim() == 3 or new_tokens and q.dim() == 4):
+        raise HpcError(what, detail="q must have 3 or 4 dimensions" if new_tokens else "q must have 3 dimensions")
 
 
 def _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages):
@@ -658,6 +662,8 @@ def hpc_prefill_attn(q, k_cache, v_cache, page_table, plan: TilePlan, split_o, s
 def hpc_prefill_combine(plan: TilePlan, split_o, split_lse, out, out_lse=None, stream=None):
     """Merges the pieces of cut tiles into out and out_lse."""
     what = "hpc_prefill_combine"
+    if out.dim() != 3:
+        raise HpcError(what, detail="out must have 3 dimensions")
     T, Hq, D = out.shape
     dev = _on_device(what, out, split_o, split_lse, out_lse, plan.buf)
     _tensor("out", out, (plan.struct.num_tokens, Hq, D), torch.bfloat16)
@@ -749,7 +755,7 @@ def hpc_prefix_attn(q, k_cache, v_cache, prefix_table, plan: TilePlan, split_o, 
     [B, q_len, Hq, 128]) over its group's prefix; partial rows for hpc_prefix_combine."""
     what = "hpc_prefix_attn"
     kvd, pages, page, Hkv = _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages)
-    _query(what, q)
+    _query(what, q, new_tokens=True)
     Hq, D = q.shape[-2:]
     _table("prefix_table", prefix_table, plan.struct.num_seqs)
     dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, prefix_table, split_o, split_lse)
@@ -768,6 +774,8 @@ def hpc_prefix_combine(prefix_plan: TilePlan, prefix_o, prefix_lse, plan: Plan, 
     """Merges the prefix pieces and the splits of the requests' own tokens into out
     ([B, Hq, 128] or [B, q_len, Hq, 128] bf16) and out_lse."""
     what = "hpc_prefix_combine"
+    if out.dim() not in (3, 4):
+        raise HpcError(what, detail="out must have 3 or 4 dimensions")
     B, Hq, D = out.shape[0], out.shape[-2], out.shape[-1]
     q_len = out.shape[1] if out.dim() == 4 else 1
     dev = _on_device(what, out, prefix_o, prefix_lse, split_o, split_lse, out_lse)
@@ -805,7 +813,7 @@ def decode_shared_prefix(q, k_cache, v_cache, page_table, seq_lens, prefix_table
     (out, lse, prefix_plan, plan)."""
     what = "hpc_decode_shared_prefix"
     kvd, pages, page, Hkv = _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages)
-    _query(what, q)
+    _query(what, q, new_tokens=True)
     B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
     q_len = q.shape[1] if q.dim() == 4 else 1
     _i32("seq_lens", seq_lens, B)

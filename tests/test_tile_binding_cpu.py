@@ -47,3 +47,18 @@ def test_caches_of_another_head_dimension(dim):
     for call in calls:
         with pytest.raises(hb.HpcError, match="heads, 128"):
             call()
+
+
+def test_queries_and_outputs_of_other_dimensions():
+    """[64, 128] would pass for 64 requests of 64 heads, and be read far past its end."""
+    flat = bf16(64, 128)
+    plan = type("Plan", (), {"buf": i32(0), "struct": hb.TilePlanStruct(0, 0, 1, 64, 8, 4, 1, 32, 1, 1)})()
+    for call in (lambda: shared(q=flat, k=cache(heads=8), v=cache(heads=8), batch=64),
+                 lambda: shared(q=bf16(1, 2, 1, 8, 128)),
+                 lambda: prefill(q=flat), lambda: prefill(q=bf16(9, 1, 8, 128)),
+                 lambda: hb.hpc_prefix_attn(flat, cache(heads=8), cache(heads=8), i32(0).view(1, 1), plan, None, None),
+                 lambda: hb.hpc_prefill_attn(flat, cache(), cache(), i32(0).view(1, 1), plan, None, None, flat),
+                 lambda: hb.hpc_prefix_combine(plan, None, None, None, None, None, flat),
+                 lambda: hb.hpc_prefill_combine(plan, None, None, flat)):
+        with pytest.raises(hb.HpcError, match="dimensions"):
+            call()
