@@ -515,6 +515,11 @@ def _query(what, q, new_tokens=False):
         raise HpcError(what, detail="q must have 3 or 4 dimensions" if new_tokens else "q must have 3 dimensions")
 
 
+def _workspace(what, t):
+    if t is not None and not t.is_contiguous():
+        raise HpcError(what, detail="workspace must be a contiguous tensor")
+
+
 def _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages):
     """Checks of a paged cache; returns its hpc_kv_dtype, pages in use, page size and KV heads."""
     kvd = kv_dtype_of(k_cache)
@@ -690,6 +695,7 @@ def prefill(q, k_cache, v_cache, page_table, q_starts, seq_lens, k_scale=None, v
     B = seq_lens.numel()
     _i32("q_starts", q_starts, B + 1)
     _table("page_table", page_table, B)
+    _workspace(what, workspace)
     dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, q_starts, seq_lens, out, out_lse, workspace)
     num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
     L = lib()
@@ -822,6 +828,7 @@ def decode_shared_prefix(q, k_cache, v_cache, page_table, seq_lens, prefix_table
     G = prefix_lens.numel()
     _i32("group_starts", group_starts, G + 1)
     _table("prefix_table", prefix_table, G)
+    _workspace(what, workspace)
     dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, prefix_table, prefix_lens,
                      group_starts, workspace)
     num_ctas = _decode_num_ctas(kvd) if num_ctas is None else num_ctas

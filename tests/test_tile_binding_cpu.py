@@ -62,3 +62,12 @@ def test_queries_and_outputs_of_other_dimensions():
                  lambda: hb.hpc_prefill_combine(plan, None, None, flat)):
         with pytest.raises(hb.HpcError, match="dimensions"):
             call()
+
+
+def test_workspaces_with_gaps():
+    """A workspace's bytes are counted from its first one on: a repeated or strided view does not have them."""
+    need = hb.prefill_workspace_bytes(1, 4)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(need), torch.zeros(2 * need, dtype=torch.uint8)[::2]):
+        for call in (prefill, shared):
+            with pytest.raises(hb.HpcError, match="workspace"):
+                call(workspace=ws)
