@@ -625,7 +625,7 @@ def hpc_prefill_plan(q_starts, seq_lens, num_tokens: int, num_kv_heads: int, pag
     _i32("seq_lens", seq_lens)
     B = seq_lens.numel()
     _i32("q_starts", q_starts, B + 1)
-    dev = _on_device("hpc_prefill_plan", seq_lens, q_starts)
+    dev = _on_device("hpc_prefill_plan", seq_lens, q_starts, None if plan is None else plan.buf)
     num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
     if plan is None:
         with _on(stream):
@@ -650,7 +650,8 @@ def hpc_prefill_attn(q, k_cache, v_cache, page_table, plan: TilePlan, split_o, s
     _query(what, q)
     T, Hq, D = q.shape
     _table("page_table", page_table, plan.struct.num_seqs)
-    dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, split_o, split_lse, out, out_lse)
+    dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, split_o, split_lse, out, out_lse,
+                     plan.buf)
     if T != plan.struct.num_tokens:
         raise HpcError(what, detail=f"q has {T} tokens, the plan {plan.struct.num_tokens}")
     _tensor("out", out, (T, Hq, D), torch.bfloat16)
@@ -733,7 +734,7 @@ def hpc_prefix_plan(group_starts, prefix_lens, batch: int, num_kv_heads: int, pr
     _i32("prefix_lens", prefix_lens)
     G = prefix_lens.numel()
     _i32("group_starts", group_starts, G + 1)
-    dev = _on_device("hpc_prefix_plan", prefix_lens, group_starts)
+    dev = _on_device("hpc_prefix_plan", prefix_lens, group_starts, None if plan is None else plan.buf)
     num_ctas = tile_num_ctas() if num_ctas is None else num_ctas
     if plan is None:
         with _on(stream):
@@ -764,7 +765,7 @@ def hpc_prefix_attn(q, k_cache, v_cache, prefix_table, plan: TilePlan, split_o, 
     _query(what, q, new_tokens=True)
     Hq, D = q.shape[-2:]
     _table("prefix_table", prefix_table, plan.struct.num_seqs)
-    dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, prefix_table, split_o, split_lse)
+    dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, prefix_table, split_o, split_lse, plan.buf)
     if q.numel() != plan.struct.num_tokens * Hq * D or (q.shape[1] if q.dim() == 4 else 1) != plan.struct.q_len:
         raise HpcError(what, detail="q and the plan differ in requests or new tokens")
     _check_splits(what, _prefix_rows(plan), split_o, split_lse)
@@ -784,7 +785,7 @@ def hpc_prefix_combine(prefix_plan: TilePlan, prefix_o, prefix_lse, plan: Plan, 
         raise HpcError(what, detail="out must have 3 or 4 dimensions")
     B, Hq, D = out.shape[0], out.shape[-2], out.shape[-1]
     q_len = out.shape[1] if out.dim() == 4 else 1
-    dev = _on_device(what, out, prefix_o, prefix_lse, split_o, split_lse, out_lse)
+    dev = _on_device(what, out, prefix_o, prefix_lse, split_o, split_lse, out_lse, prefix_plan.buf, plan.buf)
     _tensor("out", out, out.shape, torch.bfloat16)
     if out_lse is not None:
         _tensor("out_lse", out_lse, out.shape[:-1], torch.float32)
