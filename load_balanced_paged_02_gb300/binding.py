@@ -797,15 +797,26 @@ def hpc_prefix_combine(prefix_plan: TilePlan, prefix_o, prefix_lse, plan: Plan, 
     _check(what, rc)
 
 
-class _WorkspacePlan:
-    """The task map that decode_shared_prefix left in its workspace: what hpc_decode_read_error takes."""
+class _WorkspacePlan(Plan):
+    """The task map that decode_shared_prefix left in its workspace, for the decode calls that take one."""
 
     def __init__(self, struct, workspace):
         self.struct = struct
         self.workspace = workspace
 
-    def ref(self):
-        return ctypes.byref(self.struct)
+    @property
+    def buf(self):
+        at = self.struct.buf - self.workspace.data_ptr()
+        return self.workspace.view(torch.uint8)[at:at + self.struct.bytes].view(torch.int32)
+
+    @property
+    def split_capacity(self):
+        p = self.struct
+        return int(lib().hpc_decode_split_capacity(p.batch, p.num_kv_heads, p.num_ctas))
+
+    @property
+    def capacity_ctas(self):
+        return self.struct.num_ctas
 
 
 def decode_shared_prefix(q, k_cache, v_cache, page_table, seq_lens, prefix_table, prefix_lens, group_starts, k_scale=None,
