@@ -822,13 +822,13 @@ class _WorkspacePlan(Plan):
 def decode_shared_prefix(q, k_cache, v_cache, page_table, seq_lens, prefix_table, prefix_lens, group_starts, k_scale=None,
                          v_scale=None, num_ctas: int | None = None, min_chunks_per_cta: int = 2,
                          prefix_num_ctas: int | None = None, min_blocks_per_cta: int = 1, tile_tokens: int = 0,
-                         num_pages: int | None = None, workspace=None, stream=None):
+                         num_pages: int | None = None, workspace=None, stream=None, out=None, out_lse=None):
     """One decode step of a batch whose groups share prefixes: requests
     [group_starts[g], group_starts[g + 1]) see the prefix_lens[g] tokens that
     prefix_table[g] names, then their own seq_lens[b] tokens (page_table). Each
-    prefix is computed once for its group. q bf16 [B, Hq, 128] or [B, q_len, Hq, 128]; a
-    given ``workspace`` is a uint8 tensor of decode_shared_prefix_workspace_bytes. Returns
-    (out, lse, prefix_plan, plan)."""
+    prefix is computed once for its group. q bf16 [B, Hq, 128] or [B, q_len, Hq, 128]. Buffers
+    that are not given are allocated here; a given ``workspace`` is a uint8 tensor of
+    decode_shared_prefix_workspace_bytes. Returns (out, lse, prefix_plan, plan)."""
     what = "hpc_decode_shared_prefix"
     kvd, pages, page, Hkv = _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages)
     _query(what, q, new_tokens=True)
@@ -841,26 +841,33 @@ def decode_shared_prefix(q, k_cache, v_cache, page_table, seq_lens, prefix_table
     _i32("group_starts", group_starts, G + 1)
     _table("prefix_table", prefix_table, G)
     _workspace(what, workspace)
+    if out is not None:
+        _tensor("out", out, q.shape, torch.bfloat16)
+    if out_lse is not None:
+        _tensor("out_lse", out_lse, q.shape[:-1], torch.float32)
     dev = _on_device(what, q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, prefix_table, prefix_lens,
-                     group_starts, workspace)
+                     group_starts, workspace, out, out_lse)
     num_ctas = _decode_num_ctas(kvd) if num_ctas is None else num_ctas
     prefix_num_ctas = tile_num_ctas() if prefix_num_ctas is None else prefix_num_ctas
     L = lib()
-    with _on(stream):
-        if workspace is None:
-            need = L.hpc_decode_shared_prefix_workspace_bytes(G, B, q_len, Hkv, prefix_num_ctas, num_ctas)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        out = torch.empty_like(q)
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    if workspace is None or out is None or out_lse is None:
+        with _on(stream):
+            if workspace is None:
+                need = L.hpc_decode_shared_prefix_workspace_bytes(G, B, q_len, Hkv, prefix_num_ctas, num_ctas)
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            if out is None:
+                out = torch.empty_like(q)
+            if out_lse is None:
+                out_lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
     pplan, plan = TilePlan.of_workspace(TilePlanStruct(), workspace), _WorkspacePlan(PlanStruct(), workspace)
     rc = L.hpc_decode_shared_prefix(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), kvd, pages,
         page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(), prefix_table.data_ptr(), prefix_table.shape[1],
         prefix_lens.data_ptr(), group_starts.data_ptr(), G, B, q_len, Hq, Hkv, D, page, num_ctas, min_chunks_per_cta,
         prefix_num_ctas, min_blocks_per_cta, tile_tokens, workspace.data_ptr(), workspace.nbytes, pplan.ref(), plan.ref(),
-        out.data_ptr(), lse.data_ptr(), _raw_stream(stream, dev))
+        out.data_ptr(), out_lse.data_ptr(), _raw_stream(stream, dev))
     _check(what, rc)
-    return out, lse, pplan, plan
+    return out, out_lse, pplan, plan
 
 
 def decode_shared_prefix_workspace_bytes(num_groups: int, batch: int, num_kv_heads: int, q_len: int = 1,

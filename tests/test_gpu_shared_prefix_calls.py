@@ -36,3 +36,16 @@ def test_its_plans_serve_the_single_calls(q_len, kv):
     assert hb.hpc_decode_read_error(plan) == 0 and hb.hpc_tile_read_error(pplan) == 0
     # (hpc_decode_attn runs one token on the kernel that hpc_decode_attn_multi runs it on)
     assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("q_len", [1, 2])
+def test_outputs_that_are_given(q_len):
+    c, args = case("bf16", q_len, 71)
+    out, lse, _, _ = hb.decode_shared_prefix(*args)
+    ws = torch.empty(hb.decode_shared_prefix_workspace_bytes(2, 6, 2, q_len), dtype=torch.uint8, device="cuda")
+    o2, l2 = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    got = hb.decode_shared_prefix(*args, workspace=ws, out=o2, out_lse=l2)
+    assert got[0] is o2 and got[1] is l2 and torch.equal(o2, out) and torch.equal(l2, lse)
+    for kw in (dict(out=o2.float()), dict(out=o2[:5]), dict(out_lse=l2[..., :8]), dict(out_lse=l2.double()), dict(out=o2.cpu())):
+        with pytest.raises(hb.HpcError):
+            hb.decode_shared_prefix(*args, workspace=ws, **kw)
