@@ -21,10 +21,13 @@ _BINDING_NAMES = {
 }
 
 
+_module = None  # the binding, once imported (looking it up costs 1 us, and some calls' kernels take two)
+
+
 def __getattr__(name):
+    global _module
     if name in _BINDING_NAMES:
-        # kept, so that only the first access comes through here (1 us each on the way to
-        # calls whose kernels take two)
-        value = globals()[name] = getattr(importlib.import_module(".binding", __name__), name)
-        return value
+        if _module is None:
+            _module = importlib.import_module(".binding", __name__)
+        return getattr(_module, name)
     raise AttributeError(name)

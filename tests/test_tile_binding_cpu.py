@@ -71,3 +71,15 @@ def test_workspaces_with_gaps():
         for call in (prefill, shared):
             with pytest.raises(hb.HpcError, match="workspace"):
                 call(workspace=ws)
+
+
+def test_the_package_shows_the_binding_as_it_is(monkeypatch):
+    """A binding function replaced later is the one that the package gives."""
+    import load_balanced_paged_02_gb300 as pkg
+    assert pkg.prefill is hb.prefill and pkg.hpc_kv_read is hb.hpc_kv_read
+    monkeypatch.setattr(hb, "prefill", lambda: "other")
+    assert pkg.prefill() == "other"
+    monkeypatch.undo()
+    assert pkg.prefill is hb.prefill
+    with pytest.raises(AttributeError):
+        pkg.no_such_name
