@@ -106,9 +106,14 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteArgs a,
                 for (int o = kLanes / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(mask, am, o));
                 float scale = __fdiv_rn(am, kE4m3Max);
                 if (!(scale > 0.f)) scale = 1.f;
-                // x / scale. A product with the reciprocal and one correction step give the
-                // rounded quotient where scale and reciprocal are ordinary numbers
-                if (scale >= 1e-30f && scale <= 1e30f) {
+                // x / scale, correctly rounded, by Markstein's correction step (IBM J. Res. Dev.
+                // 34(1), 1990): y = RN(1 / scale), q = RN(x y), r = RN(x - q scale), RN(q + r y).
+                // His theorem asks for a q within one ulp. That may be missed here (1.4 ulp), but
+                // while nothing leaves the normal range the answer is one of 128 x 128, for the
+                // significands of the row's largest element and of x, and all of them are the
+                // rounded quotients (checked one by one in the tests). From 1e-24 on the residual of
+                // a quotient that has a code above zero (2^-11 and more) is no subnormal number.
+                if (scale >= 1e-24f && scale <= 1e30f) {
                     const float inv = __frcp_rn(scale);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
