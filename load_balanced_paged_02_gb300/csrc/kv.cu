@@ -13,6 +13,7 @@
 // the first is used. Blocks of 16 tokens measured best (96k tokens at 8 heads, e4m3
 // read: 64 tokens 170 us, 32 161 us, 16 156 us).
 #include "kv.cuh"
+#include "tile.cuh"
 
 namespace hpc {
 namespace {
@@ -233,8 +234,9 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a, i
 
 // Tokens of a block: as many as leave four blocks per SM, at most kMaxTokens.
 int tokens_per_block(int tokens) {
+    const int blocks = 4 * tile_default_ctas();
     int n = kMaxTokens;
-    while (n > 1 && (tokens + n - 1) / n < 152 * 4) n >>= 1;
+    while (n > 1 && (tokens + n - 1) / n < blocks) n >>= 1;
     return n;
 }
 

@@ -126,7 +126,7 @@ struct TileAttnArgs {
     float* out_lse;  // prompts only, nullable
 };
 cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s);
-int tile_default_ctas();
+int tile_default_ctas();  // SMs of the current device (0: it cannot be asked)
 
 cudaError_t launch_prefill_combine(const int32_t* plan, int S, int num_tokens, int Hq, int C, int T, const float* split_o,
                                    const float* split_lse, void* out, float* out_lse, cudaStream_t s);
