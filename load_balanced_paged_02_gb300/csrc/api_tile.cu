@@ -63,7 +63,7 @@ hpc_status plan_common(const int32_t* d_starts, const int32_t* d_lens, int num_s
     plan->table_stride = table_stride;
     const long long max_len = (long long)table_stride * kChunk;
     *args = TilePlanArgs{d_starts, d_lens, num_seqs, num_tokens, num_kv_heads, plan->num_workers, min_blocks,
-                         max_len > 2147483647LL ? 2147483647 : (int)max_len, mode, q_len, tile_tokens, plan->buf};
+                         max_len > kMaxKeys ? kMaxKeys : (int)max_len, mode, q_len, tile_tokens, plan->buf};
     return HPC_OK;
 }
 

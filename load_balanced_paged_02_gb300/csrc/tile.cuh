@@ -25,6 +25,8 @@ namespace hpc {
 constexpr int kHalfTokens = 16;                   // query tokens of an MMA's 128 rows
 constexpr int kTileCta = 2 * kHalfTokens, kTilePair = 4 * kHalfTokens;
 constexpr int kBlock = 128;                       // keys of a block: two pages
+// Most keys of a sequence: a tile's limits, up to T past the last key, stay in int32.
+constexpr int kMaxKeys = 2147483647 - 255;
 constexpr int kModePrefill = 0, kModePrefix = 1;
 
 enum TileHdrSlot {

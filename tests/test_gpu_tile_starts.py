@@ -190,3 +190,15 @@ def test_groups_beside_passed_over_ones_keep_their_prefix(q_len, tile):
                     k, v, p = torch.cat([c["k"][1][g], k]), torch.cat([c["v"][1][g], v]), plens[g]
             ref = tl.attend(q[b].reshape(q_len, 8, 128), k, v, [p + max(0, own[b] - q_len + i + 1) for i in range(q_len)])
             tl.check_rows(out[b].reshape(q_len, 8, 128), lse[b].reshape(q_len, 8), ref, False, f"starts {st}, request {b}")
+
+
+@pytest.mark.gpu
+def test_lengths_at_the_end_of_31_bits():
+    """On the map alone: a tile's last limit, up to 64 past the last key, must not pass 2^31 - 1."""
+    lens = [2147483647, 2147483392, 2147483391, 2147483393]
+    plan = hb.hpc_prefill_plan(tl.i32([0, 3, 6, 9, 12]), tl.i32(lens), 12, 1, 1 << 26, num_ctas=4, tile_tokens=32)
+    assert hb.hpc_tile_read_error(plan) == 4
+    rows = plan.words()[16 + 8 * 5:16 + 8 * 5 + 16].view(4, 4)
+    assert rows[:, 2].tolist() == [2147483392, 2147483392, 2147483391, 2147483392]
+    plan = hb.hpc_prefill_plan(tl.i32([0, 3]), tl.i32([2147483392]), 3, 1, 1 << 26, num_ctas=4, tile_tokens=32)
+    assert hb.hpc_tile_read_error(plan) == 0 and plan.words()[0].item() == 2 + 2147483392 // 128
