@@ -585,10 +585,10 @@ size_t hpc_prefix_split_rows(int num_groups, int batch, int q_len, int num_kv_he
  * One block, integer only, reads the lengths on the device. A sequence whose
  * starts decrease or leave [0, num_tokens] is passed over, and so is one that
  * begins before the end of an earlier sequence whose starts do neither
- * (HPC_DEVERR_BAD_DESCRIPTOR): no query row has two sequences; keys beyond the page table's row are not seen
- * (HPC_DEVERR_PAGE_OUT_OF_RANGE); a negative length counts as 0
- * (HPC_DEVERR_NEGATIVE_LENGTH). Lengths go up to 2^31 - 256; a longer one is reported
- * like one beyond the table's row.
+ * (HPC_DEVERR_BAD_DESCRIPTOR): no query row has two sequences. A length
+ * beyond the page table's row counts as the row's, page_table_stride * 64, which moves
+ * every limit of the sequence with it (HPC_DEVERR_PAGE_OUT_OF_RANGE), one beyond
+ * 2^31 - 256 as that; a negative length counts as 0 (HPC_DEVERR_NEGATIVE_LENGTH).
  * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_WORKSPACE_TOO_SMALL, HPC_ERR_CUDA.
  */
 hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens, int batch, int num_tokens,
