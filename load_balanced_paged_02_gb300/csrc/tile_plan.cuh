@@ -90,8 +90,7 @@ __device__ __forceinline__ void tile_plan_block(const TilePlanArgs& a) {
     const TileLayout lay = tile_layout(S, C);
     int4* seqs = reinterpret_cast<int4*>(buf + lay.seqs);
     long long* units = reinterpret_cast<long long*>(buf + lay.units);
-    if (threadIdx.x == 0) err_sh = 0;
-    __syncthreads();
+    if (threadIdx.x == 0) err_sh = 0;  // (the loop's first barrier comes before any use)
     long long unit_base = 0;
     int tile_base = 0;
     int err = 0;
