@@ -608,9 +608,9 @@ hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens
  * float32; probabilities enter the second product as bf16 (f16 with an e4m3
  * cache, where V enters as code x scale rounded to f16: |v| <= 65504, and values,
  * and probabilities relative to the row's reference, under 2^-14 keep multiples of
- * 2^-24). Keys and values of tokens that a row does
- * not see never reach it through its maximum and sum; a value of V that is not
- * finite reaches every row of the 128-token blocks that hold its token.
+ * 2^-24). Nothing of a token that a row does not see reaches it, infinities and NaN
+ * in K and V included (tiles that hold such values of V in tokens that some of their
+ * rows do not see take far longer).
  * A page id outside [0, num_pages) hides its 64 tokens
  * (HPC_DEVERR_PAGE_OUT_OF_RANGE). Where a map of other sizes (sequences, tokens, KV
  * heads, workers, tile, new tokens per request) has been planned into the plan's

@@ -173,6 +173,16 @@ struct TileParams {
     float scale_log2;
 };
 
+// The operands as they are in memory, for redo_rows. (A parameter of its own: within
+// TileParams they make the bf16 instances spill.)
+struct TileSources {
+    const __nv_bfloat16* q;
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+};
+
 __device__ __forceinline__ void tma_load_3d_plain(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
                                                   int c2) {
     asm volatile(
@@ -584,11 +594,167 @@ __device__ __forceinline__ void zero_tail(uint8_t* vt, int nv, int lane) {
     __syncwarp();
 }
 
+// acc + 0 x for two bf16 numbers, or for one float: stays zero unless one is infinite or NaN
+__device__ __forceinline__ uint32_t wild2(uint32_t x, uint32_t acc) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(acc));
+    return d;
+}
+__device__ __forceinline__ float wild1(float x, float acc) {
+    float d;
+    asm("fma.rn.f32 %0, %1, 0f00000000, %2;" : "=f"(d) : "f"(x), "f"(acc));
+    return d;
+}
+
+// Eight elements of a cache row, from element `at` on (e4m3: without their scale).
+template <bool FP8>
+__device__ __forceinline__ void cache8(const void* cache, long long at, float (&x)[8]) {
+    if constexpr (FP8) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + at);
+        uint32_t h[4];
+        e4m3x4_to_f16x2x2(w.x, h[0], h[1]);
+        e4m3x4_to_f16x2x2(w.y, h[2], h[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        }
+    } else {
+        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(cache) + at);
+        const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(h[i] << 16), x[2 * i + 1] = __uint_as_float(h[i] & 0xffff0000u);
+    }
+}
+
+// Rows of an item of a prompt whose sums came out infinite or NaN. In blocks of which a row
+// does not see every key, the products multiply values that it must not see by zero, and 0
+// x inf is NaN. So where such keys of the item hold a value that is not finite, the warp
+// computes its rows again, key by key over those that the row sees, in float32 (m and inv
+// are right: values have no part in them). `rows`: the warp's rows to look at; lim0: the
+// keys that its first token sees. Not entered while all values are finite; a tile over 8192
+// keys then takes 18 ms. (Looking at V before the products instead, in the issuer, in a
+// warp of its own or while it is widened, cost every prompt 2 to 5 %, e4m3 9 %; the look at
+// the rows on their way out costs nothing over bf16 caches and 1.5 % over e4m3.)
+template <bool FP8>
+__device__ __forceinline__ void redo_rows(const TileParams& p, const TileSources& src, const TileItem& it, uint32_t rows, int lim0, int tok0, float m,
+                                          float inv, bool direct, long long split_row0, int lane) {
+    // the sequence, found again by its first query token
+    const int4* seqs = reinterpret_cast<const int4*>(p.plan + p.seqs_off);
+    int s0 = 0, s1 = p.S;
+    while (s1 - s0 > 1) {
+        const int mid = (s0 + s1) >> 1;
+        if (seqs[mid].x <= it.q0)
+            s0 = mid;
+        else
+            s1 = mid;
+    }
+    const int32_t* const table = p.page_table + (long long)s0 * p.pt_stride;
+    // element and scale of key k's row; false: no valid page
+    auto locate = [&](int k, long long& at, long long& sc) {
+        const int c = k / kChunk, off = k % kChunk;
+        const int page = c < p.pt_stride ? table[c] : -1;
+        at = (((long long)page * kChunk + off) * p.num_kv_heads + it.h) * kHeadDim;
+        sc = ((long long)page * p.num_kv_heads + it.h) * kChunk + off;
+        return (unsigned)page < (unsigned)p.num_pages;
+    };
+    const int k_end = min(it.L, it.b1 * kBlock);
+    float wild = 0.f;
+#pragma unroll 1
+    for (int k = max(max(lim0, 0), it.b0 * kBlock) + (lane >> 4); k < k_end; k += 2) {  // 16 lanes a row of V
+        long long at, sc;
+        float x[8];
+        if (!locate(k, at, sc)) continue;
+        cache8<FP8>(src.v_cache, at + 8 * (lane & 15), x);
+        // (past f16's range counts as infinite: widen_v makes it so)
+        if constexpr (FP8) wild = fabsf(src.v_scale[sc]) * 448.f <= 65504.f ? wild : 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wild = wild1(x[i], wild);
+    }
+    if (!__any_sync(0xffffffffu, wild != 0.f)) return;  // infinite or NaN for other reasons
+    const long long step = (long long)p.num_kv_heads * kHeadDim;  // from key to key of a page
+    // a token's eight rows at once: they see the same keys
+#pragma unroll 1
+    for (int u = 0; u < 4; ++u) {
+        if (((rows >> (8 * u)) & 0xffu) == 0) continue;
+        const int lim = min(k_end, lim0 + u);
+        const long long qrow = (long long)(it.q0 + tok0 + u) * p.num_q_heads + it.h * kGroup;
+        float o[kGroup][4];  // dims 4 lane ..
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[g][i] = 0.f;
+#pragma unroll 1
+        for (int k0 = it.b0 * kBlock; k0 < lim; k0 += 32) {  // 32 keys lie in one page
+            long long at, sc;
+            if (!locate(k0, at, sc)) continue;
+            const int n = min(32, lim - k0);
+            float w[kGroup];  // of key k0 + lane
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g) w[g] = 0.f;
+            if (lane < n) {
+#pragma unroll 2
+                for (int c = 0; c < kHeadDim; c += 8) {
+                    float x[8];
+                    cache8<FP8>(src.k_cache, at + lane * step + c, x);
+#pragma unroll
+                    for (int g = 0; g < kGroup; ++g) {
+                        float y[8];
+                        cache8<false>(src.q, (qrow + g) * kHeadDim + c, y);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[g] = fmaf(x[i], y[i], w[g]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g) {
+                if constexpr (FP8) w[g] *= src.k_scale[sc + lane];
+                w[g] = fast_exp2(fmaf(w[g], p.scale_log2, -__shfl_sync(0xffffffffu, m, 8 * u + g)));
+                if constexpr (FP8) w[g] *= src.v_scale[sc + lane];
+            }
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) {
+                float x[4];
+                if constexpr (FP8) {
+                    uint32_t h[2];
+                    e4m3x4_to_f16x2x2(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(src.v_cache) + at + j * step + 4 * lane),
+                                      h[0], h[1]);
+                    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h[0])),
+                                 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
+                    x[0] = f0.x, x[1] = f0.y, x[2] = f1.x, x[3] = f1.y;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(src.v_cache) + at + j * step + 4 * lane);
+                    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+                    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
+                }
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) {
+                    const float f = __shfl_sync(0xffffffffu, w[g], j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[g][i] = fmaf(f, x[i], o[g][i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+            const float f = __shfl_sync(0xffffffffu, inv, 8 * u + g);
+            if (((rows >> (8 * u + g)) & 1u) == 0) continue;
+            if (direct)
+                *reinterpret_cast<uint2*>(p.out + (qrow + g) * kHeadDim + 4 * lane) =
+                    make_uint2(pack_bf16x2(o[g][0] * f, o[g][1] * f), pack_bf16x2(o[g][2] * f, o[g][3] * f));
+            else
+                *reinterpret_cast<float4*>(p.split_o + (split_row0 + 8 * u + g) * kHeadDim + 4 * lane) =
+                    make_float4(o[g][0] * f, o[g][1] * f, o[g][2] * f, o[g][3] * f);
+        }
+    }
+}
+
 template <bool FP8, int CG>
 __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
     tile_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
-                     const __grid_constant__ CUtensorMap tm_vs, const TileParams p) {
+                     const __grid_constant__ CUtensorMap tm_vs, const TileParams p,
+                     const __grid_constant__ TileSources src) {
     using C = Cfg<FP8, CG>;
     using LY = Smem<FP8, CG>;
     constexpr int NB = C::kSlots;
@@ -1197,6 +1363,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
             const int sw = (lane >> 1) & 3, hd = lane >> 2;
             uint4* const put = reinterpret_cast<uint4*>(stage + lane * 64);
             const uint8_t* const get = stage + hd * 64 + (((lane & 3) ^ ((hd >> 1) & 3)) << 4);
+            uint32_t wild = 0;  // not zero: this thread's row has an infinity or NaN
             if (direct) {
                 const long long row0 = (long long)(it.q0 + tok0 + wtok) * p.num_q_heads + it.h * kGroup;
                 const long long step = (long long)p.num_q_heads * kHeadDim;
@@ -1212,11 +1379,14 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                         for (int u = 0; u < 32; ++u) o[u] = 0.f;
                     }
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        put[u ^ sw] = make_uint4(pack_bf16x2(o[8 * u] * inv, o[8 * u + 1] * inv),
-                                                 pack_bf16x2(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
-                                                 pack_bf16x2(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
-                                                 pack_bf16x2(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
+                    for (int u = 0; u < 4; ++u) {
+                        const uint4 x = make_uint4(pack_bf16x2(o[8 * u] * inv, o[8 * u + 1] * inv),
+                                                   pack_bf16x2(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
+                                                   pack_bf16x2(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
+                                                   pack_bf16x2(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
+                        put[u ^ sw] = x;
+                        wild = wild2(x.x, wild2(x.y, wild2(x.z, wild2(x.w, wild))));
+                    }
                     __syncwarp();
                     uint4 v[4];
 #pragma unroll
@@ -1241,9 +1411,11 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                         for (int u = 0; u < 16; ++u) o[u] = 0.f;
                     }
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        reinterpret_cast<float4*>(put)[u ^ sw] =
-                            make_float4(o[4 * u] * inv, o[4 * u + 1] * inv, o[4 * u + 2] * inv, o[4 * u + 3] * inv);
+                    for (int u = 0; u < 4; ++u) {
+                        const float4 x = make_float4(o[4 * u] * inv, o[4 * u + 1] * inv, o[4 * u + 2] * inv, o[4 * u + 3] * inv);
+                        reinterpret_cast<float4*>(put)[u ^ sw] = x;
+                        wild |= __float_as_uint(wild1(x.x, wild1(x.y, wild1(x.z, wild1(x.w, 0.f)))));
+                    }
                     __syncwarp();
                     float4 v[4];
 #pragma unroll
@@ -1255,6 +1427,10 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                 }
                 if ((lane >> 3) < live) p.split_lse[row0 + lane] = lse;
             }
+            const uint32_t again = __ballot_sync(0xffffffffu, wild != 0 && (lane >> 3) < live);
+            if (again != 0 && p.mode == kModePrefill)
+                redo_rows<FP8>(p, src, it, again, it.L - it.n + tok0 + wtok + 1, tok0 + wtok, m, inv, direct,
+                               tile_slot(p.mode, worker, it) * (T * kGroup) + (half_tok + wtok) * kGroup, lane);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_leader<CG>(&ofree[t]);
@@ -1314,7 +1490,7 @@ bool make_v_half_map(CUtensorMap* map, const void* base, int num_pages, int Hkv)
 }
 
 template <bool FP8, int CG>
-cudaError_t launch(const CUtensorMap (&maps)[5], const TileParams& p, int workers, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap (&maps)[5], const TileParams& p, const TileSources& src, int workers, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1340,7 +1516,7 @@ cudaError_t launch(const CUtensorMap (&maps)[5], const TileParams& p, int worker
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, tile_attn_kernel<FP8, CG>, maps[0], maps[1], maps[2], maps[3], maps[4], p);
+    e = cudaLaunchKernelEx(&cfg, tile_attn_kernel<FP8, CG>, maps[0], maps[1], maps[2], maps[3], maps[4], p, src);
     // a refused launch is reported through the return value, not left pending
     if (e != cudaSuccess) (void)cudaGetLastError();
     return e;
@@ -1388,10 +1564,11 @@ cudaError_t launch_tile_attn(const TileAttnArgs& a, cudaStream_t s) {
     p.split_lse = a.split_lse;
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.out_lse = a.out_lse;
+    const TileSources src{static_cast<const __nv_bfloat16*>(a.q), a.k_cache, a.v_cache, a.k_scale, a.v_scale};
     p.scale_log2 = 1.4426950408889634f / sqrtf((float)kHeadDim);
     if (pair)
-        return a.fp8 ? launch<true, 2>(maps, p, a.num_workers, s) : launch<false, 2>(maps, p, a.num_workers, s);
-    return a.fp8 ? launch<true, 1>(maps, p, a.num_workers, s) : launch<false, 1>(maps, p, a.num_workers, s);
+        return a.fp8 ? launch<true, 2>(maps, p, src, a.num_workers, s) : launch<false, 2>(maps, p, src, a.num_workers, s);
+    return a.fp8 ? launch<true, 1>(maps, p, src, a.num_workers, s) : launch<false, 1>(maps, p, src, a.num_workers, s);
 }
 
 }  // namespace hpc
