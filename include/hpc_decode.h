@@ -606,9 +606,9 @@ hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens
  *   out_lse    device float32 [num_tokens][num_q_heads] or NULL
  * A row that sees no key gets out = 0 and out_lse = -inf. Scores and sums are
  * float32; probabilities enter the second product as bf16 (f16 with an e4m3
- * cache, where V enters as code x scale rounded to f16: |v| <= 65504, and values,
- * and probabilities relative to the row's reference, under 2^-14 keep multiples of
- * 2^-24). Nothing of a token that a row does not see reaches it, infinities and NaN
+ * cache, where V enters as code x scale rounded to f16: |v| <= 65504, values under
+ * 2^-14 keep multiples of 2^-24, and probabilities under 2^-19 of the largest that set
+ * the row's reference multiples of 2^-29). Nothing of a token that a row does not see reaches it, infinities and NaN
  * in K and V included (tiles that hold such values of V in tokens that some of their
  * rows do not see take far longer).
  * A page id outside [0, num_pages) hides its 64 tokens

@@ -84,6 +84,11 @@ constexpr int kQBytes = 32768;           // a half's query rows: [2 dim halves][
 // 64 keys' P that add up to more than 2^10 hold one above 2^4: then the row's reference
 // moves to their maximum. Up to there every P is at most 2^10.
 constexpr float kSumLimit = 1024.f;
+// Over e4m3 caches P is f16, whose normal numbers end at 2^-14 and whose last one is 2^-24:
+// its reference is 2^5 below the maximum, so that weights down to 2^-30 of the largest have
+// a part in O as they have in the sum, and P is at most 2^15.
+constexpr float kHeadroom = 5.f, kSumLimitF16 = 32.f * kSumLimit;
+static_assert(kSumLimitF16 <= 65504.f, "a P may be as large as its row's sum");
 constexpr int kMetaRing = 8;             // blocks whose page checks (and, e4m3, scales) are kept
 constexpr int kWide = 2;                 // e4m3: f16 V tiles
 constexpr int kOutBytes = 2048;          // a softmax warp's staging of 32 output rows x 64 B
@@ -1214,7 +1219,7 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
                                 exps();
                                 bool high = false;
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) high |= !(sum[i] <= kSumLimit / 4);
+                                for (int i = 0; i < 4; ++i) high |= !(sum[i] <= kSumLimitF16 / 4);
                                 if (taken || !__any_sync(0xffffffffu, high)) break;
                             }
                             take = false;
@@ -1228,11 +1233,11 @@ __global__ void __launch_bounds__(Cfg<FP8, CG>::kThreads, 1)
 #pragma unroll
                                 for (int j = 1; j < 8; ++j) mx = max3(mx, x[4 * j], x[4 * j + 1]);
                                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * scq[i];
+                                mx = fmaf(fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)), scq[i], -kHeadroom);
                                 float all = sum[i];  // the row's
                                 all += __shfl_xor_sync(0xffffffffu, all, 1);
                                 all += __shfl_xor_sync(0xffffffffu, all, 2);
-                                const bool move = mq[i] == kNegInf ? mx != kNegInf : mx > mq[i] && !(all <= kSumLimit);
+                                const bool move = mq[i] == kNegInf ? mx != kNegInf : mx > mq[i] && !(all <= kSumLimitF16);
                                 al[i] = move && mq[i] != kNegInf ? fast_exp2(mq[i] - mx) : 1.f;
                                 resc |= move && mq[i] != kNegInf;
                                 if (move) mq[i] = mx;
