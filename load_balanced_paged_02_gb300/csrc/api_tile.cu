@@ -27,18 +27,31 @@ bool tokens_ok(int num_tokens, int num_seqs, int num_kv_heads) {
     return num_tokens >= 0 && ((long long)num_tokens / kTileCta + num_seqs) * num_kv_heads < 2147483647LL;
 }
 
-// Tiles of 64 tokens on pairs of CTAs from an average of 64 query tokens per prompt on
-// (96 over e4m3 caches and for prefix groups), of 32 on single CTAs below. A pair halves
-// the copies and the shared memory traffic of a row, a single CTA wastes fewer rows on
-// short sequences. Whole calls, us, tile 32 / 64, eight prompts of 4096 keys: 32 new
-// tokens each 52 / 56, 64 75 / 65, 96 101 / 98, 512 378 / 320; e4m3 53 / 65, 83 / 79,
-// 112 / 121, 455 / 419. 512-token pieces of four prompts beside 28 single tokens (64 on
-// average): 492 / 450, e4m3 552 / 607. Attention over an 8192-token prefix: 48 requests
-// 18 / 19, 64 20 / 19, 128 29 / 28, 256 47 / 46; e4m3 25 / 26, 27 / 27, 39 / 38, 64 / 63.
-// Groups of 16, 5, 1 and 42 requests of four tokens: 37 / 43.
+// Tiles of 64 tokens on pairs of CTAs, or of 32 on single ones, by the average of query
+// tokens per sequence (the lengths are on the device): pairs from 64 on for prompts over bf16
+// caches, above 96 for prompts over e4m3 caches and for prefix groups. A pair halves the
+// copies and the shared memory traffic of a row, a single CTA wastes fewer rows on the last
+// tile of a sequence, so neither wins everywhere. us, tile 32 / 64 (prompts: whole calls at
+// 64/8 heads; prefixes: the attention alone):
+//   8 prompts of 4096 keys   new tokens  32       48       64       80       96       112      128      512
+//     bf16                              52 / 55  71 / 62  76 / 65 101 / 96 102 / 97 126 / 104 129 / 104 386 / 325
+//     e4m3                              54 / 65  80 / 78  85 / 80 111 / 121 116 / 122 142 / 133 147 / 134 474 / 426
+//   30 whole prompts, lengths log-uniform, average about 36, 70, 105, 140
+//     bf16                              25 / 28  34 / 36  51 / 50  65 / 62
+//     e4m3                              35 / 33  50 / 45  73 / 62  94 / 79
+//   pieces beside single tokens: 4 x 512 and 28 (average 65), 4 x 512 and 12 (129), 2048 and 30 (67),
+//   2048 and 15 (129), 2 x 1024 and 20 (94)
+//     bf16                             491 / 453 418 / 392 375 / 413 337 / 355 348 / 350
+//     e4m3                             553 / 614 509 / 526 497 / 564 453 / 480 433 / 471
+//   a prefix of 8192           requests  64       80       96       112      128      160      192
+//     bf16                              22 / 22  25 / 28  27 / 29  32 / 30  32 / 30  37 / 38  41 / 39
+//     e4m3                              26 / 25  32 / 36  32 / 36  38 / 38  39 / 38  46 / 49  52 / 51
+// Up to 96 rows a second 64-token tile is half empty, which costs e4m3 tiles and short walks
+// more than the copies: hence 96 there, between whole prompts (for which pairs win earlier)
+// and mixes with single tokens (for which they win later).
 int auto_tile(int mode, bool fp8, int num_tokens, int num_seqs) {
-    const long long from = (mode == kModePrefill && !fp8 ? kTilePair : 3 * kTilePair / 2) * (long long)num_seqs;
-    return num_tokens >= from ? kTilePair : kTileCta;
+    const bool pairs = mode == kModePrefill && !fp8 ? num_tokens >= 64LL * num_seqs : num_tokens > 96LL * num_seqs;
+    return pairs ? kTilePair : kTileCta;
 }
 
 // Checks of a planner's call; fills the header and the launch's arguments.
