@@ -9,6 +9,8 @@ The binding is imported on first attribute access, so that
 :mod:`.workloads` (the seeded input generator) can be used on its own.
 """
 import importlib
+import sys
+import types
 
 _BINDING_NAMES = {
     "KV_BF16", "KV_FP8_E4M3", "HpcError", "Plan", "build", "default_num_ctas",
@@ -21,13 +23,25 @@ _BINDING_NAMES = {
 }
 
 
-_module = None  # the binding, once imported (looking it up costs 1 us, and some calls' kernels take two)
+class _Package(types.ModuleType):
+    """This package: an attribute of the binding is looked up there at each access. (Descriptors of the
+    module's class: a module's __getattr__ costs a microsecond, and some calls' kernels take two.)"""
 
 
-def __getattr__(name):
-    global _module
-    if name in _BINDING_NAMES:
-        if _module is None:
-            _module = importlib.import_module(".binding", __name__)
-        return getattr(_module, name)
-    raise AttributeError(name)
+class _BindingName:
+    def __init__(self, name):
+        self.name = name
+
+    def __get__(self, package, cls):
+        module = _BindingName.module
+        if module is None:
+            module = _BindingName.module = importlib.import_module(".binding", __name__)
+        return getattr(module, self.name)
+
+    module = None
+
+
+for _name in _BINDING_NAMES:
+    setattr(_Package, _name, _BindingName(_name))
+del _name
+sys.modules[__name__].__class__ = _Package

@@ -83,3 +83,8 @@ def test_the_package_shows_the_binding_as_it_is(monkeypatch):
     assert pkg.prefill is hb.prefill
     with pytest.raises(AttributeError):
         pkg.no_such_name
+    # and a name set on the package itself is the package's, until it is taken away
+    monkeypatch.setattr(pkg, "prefill", len)
+    assert pkg.prefill is len and hb.prefill is not len
+    monkeypatch.delattr(pkg, "prefill")
+    assert pkg.prefill is hb.prefill
