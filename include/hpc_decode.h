@@ -244,6 +244,8 @@ hpc_status hpc_decode_attn_q8(const void* q8, const float* q_scale, const void* 
  *   split_o[.][:]  = normalised attention of q[b][i][8h+j] over tokens
  *                    [64*c0, min(64*c1, seq_lens[b] - q_len + i + 1))
  *   split_lse[.]   = its natural-log LSE (-inf and 0 outputs when empty)
+ * V of a new token is multiplied by zero in the rows of the new tokens before it,
+ * so an infinity or NaN there reaches them (and no other request).
  *   q          device bf16 [batch][q_len][num_q_heads][128], 16-byte aligned
  *   q_len      1 <= q_len <= HPC_MAX_Q_LEN (1 runs hpc_decode_attn's kernel)
  *   split_o    device float32 [split_capacity][q_len][8][128]
@@ -696,7 +698,8 @@ hpc_status hpc_prefill(const void* q, const void* k_cache, const void* v_cache, 
  * the combine, with maps and split rows in a workspace (device, 256-byte aligned;
  * calls that overlap on the GPU need one each). seq_lens and page_table hold the
  * tokens behind the prefix alone; prefix_plan and plan get the maps' headers, for
- * hpc_tile_read_error and hpc_decode_read_error. Errors: as the chained calls.
+ * hpc_tile_read_error and hpc_decode_read_error. Numerics and errors: as the chained
+ * calls (values of V that are not finite: hpc_decode_attn_multi).
  */
 size_t hpc_decode_shared_prefix_workspace_bytes(int num_groups, int batch, int q_len, int num_kv_heads,
                                                 int prefix_num_ctas, int num_ctas);

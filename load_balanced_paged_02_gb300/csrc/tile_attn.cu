@@ -38,15 +38,16 @@
 // Every wait is bounded; on expiry the CTA records HPC_DEVERR_WAIT_TIMEOUT.
 //
 // Bound by: the tensor core and its power, over bf16 caches. Prompt of 8192 tokens,
-// 64 / 8 heads: 660 us, 1665 TFLOP/s (0.87 of the library's 8192^3 product in
-// bursts, 0.97 of the same over seconds); the tensor pipe is active for 75 % of the
+// 64 / 8 heads: 670 to 682 us called back to back, 1610 to 1640 TFLOP/s (0.93 to 0.95 of
+// the library's 8192^3 product over seconds), 648 to 662 us in short replays (0.87 to
+// 0.89 of it in bursts); the tensor pipe is active for 75 % of the
 // cycles and the clock falls from 2070 to 1750-1790 MHz at the board's power limit. A
 // half's chain (its scores, 750 clocks of softmax per page, its product) leaves the
 // rest: measured per block of two halves 2900 clocks of which 2048 are MMAs. Over
 // e4m3 caches the softmax threads set the pace (the key scales' products and the
 // other layout cost half as much again, the widening of V takes turns from them):
-// 128 requests over a 65536-token prefix 215 us, 158 us over a bf16 cache.
-// Few blocks (8192-token prefix, 64 requests: 20 us for seven blocks per CTA) are
+// 128 requests over a 65536-token prefix 210 us, 158 us over a bf16 cache.
+// Few blocks (8192-token prefix, 64 requests: 22 us for seven blocks per CTA) are
 // bound by latency: 1.4 us a block, 2.5 us to the first one, 3.2 us for a tile's
 // float32 rows.
 //
@@ -639,8 +640,9 @@ __device__ __forceinline__ void cache8(const void* cache, long long at, float (&
 // are right: values have no part in them). `rows`: the warp's rows to look at; lim0: the
 // keys that its first token sees. Not entered while all values are finite; a tile over 8192
 // keys then takes 18 ms. (Looking at V before the products instead, in the issuer, in a
-// warp of its own or while it is widened, cost every prompt 2 to 5 %, e4m3 9 %; the look at
-// the rows on their way out costs nothing over bf16 caches and 1.5 % over e4m3.)
+// warp of its own or while it is widened, cost every prompt 2 to 5 %, e4m3 9 %. With the look
+// at the rows on their way out an 8192-token prompt takes 647 us, 648 before; e4m3 pieces and
+// decode 554, 544 before, a 65536-token prefix 260, 265 before.)
 template <bool FP8>
 __device__ __forceinline__ void redo_rows(const TileParams& p, const TileSources& src, const TileItem& it, uint32_t rows, int lim0, int tok0, float m,
                                           float inv, bool direct, long long split_row0, int lane) {
