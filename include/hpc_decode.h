@@ -612,7 +612,8 @@ hpc_status hpc_prefill_plan(const int32_t* d_q_starts, const int32_t* d_seq_lens
  * 2^-14 keep multiples of 2^-24, and probabilities under 2^-19 of the largest that set
  * the row's reference multiples of 2^-29). Nothing of a token that a row does not see reaches it, infinities and NaN
  * in K and V included (tiles that hold such values of V in tokens that some of their
- * rows do not see take far longer).
+ * rows do not see take far longer: 18 ms per 8192 keys; from some 900,000 keys of one
+ * tile and worker on, a wait may run out, HPC_DEVERR_WAIT_TIMEOUT).
  * A page id outside [0, num_pages) hides its 64 tokens
  * (HPC_DEVERR_PAGE_OUT_OF_RANGE). Where a map of other sizes (sequences, tokens, KV
  * heads, workers, tile, new tokens per request) has been planned into the plan's
