@@ -570,7 +570,7 @@ class TilePlan:
 
     def words(self):
         """The map as an int32 tensor."""
-        return self.buf.view(torch.int32)[:self.struct.bytes // 4]
+        return self.buf.view(-1).view(torch.uint8)[:self.struct.bytes].view(torch.int32)
 
     def ref(self):
         return ctypes.byref(self.struct)
@@ -807,7 +807,7 @@ class _WorkspacePlan(Plan):
     @property
     def buf(self):
         at = self.struct.buf - self.workspace.data_ptr()
-        return self.workspace.view(torch.uint8)[at:at + self.struct.bytes].view(torch.int32)
+        return self.workspace.view(-1).view(torch.uint8)[at:at + self.struct.bytes].view(torch.int32)
 
     @property
     def split_capacity(self):

@@ -88,3 +88,15 @@ def test_the_package_shows_the_binding_as_it_is(monkeypatch):
     assert pkg.prefill is len and hb.prefill is not len
     monkeypatch.delattr(pkg, "prefill")
     assert pkg.prefill is hb.prefill
+
+
+@pytest.mark.parametrize("shape,dtype", [((4096,), torch.uint8), ((2, 2048), torch.uint8), ((1023,), torch.int32), ((4099,), torch.uint8)])
+def test_maps_within_workspaces_of_any_shape(shape, dtype):
+    ws = torch.zeros(shape, dtype=dtype)
+    flat = ws.view(-1).view(torch.uint8)
+    flat[256:256 + 80] = torch.arange(80, dtype=torch.uint8)
+    flat[:64] = 7
+    plan = hb._WorkspacePlan(hb.PlanStruct(ws.data_ptr() + 256, 80, 2, 1, 4, 2, 0, 10), ws)
+    assert torch.equal(plan.buf, torch.arange(80, dtype=torch.uint8).view(torch.int32)) and plan.split_capacity == 2 + 4 - 1
+    tiles = hb.TilePlan.of_workspace(hb.TilePlanStruct(ws.data_ptr(), 64, 1, 1, 1, 1, 0, 32, 1, 1), ws)
+    assert tiles.words().tolist() == [0x07070707] * 16
