@@ -86,12 +86,14 @@ typedef enum hpc_kv_dtype { HPC_KV_BF16 = 0, HPC_KV_FP8_E4M3 = 1 } hpc_kv_dtype;
 #define HPC_DEVERR_WAIT_TIMEOUT 8u       /* a bounded wait inside the kernel ran out */
 #define HPC_DEVERR_BAD_DESCRIPTOR 16u    /* a task descriptor outside the call's shapes */
 #define HPC_DEVERR_BAD_POSITION 32u      /* prologue: a position outside [0, max_pos): not rotated */
+#define HPC_DEVERR_BAD_TOKEN 64u         /* verification: a drafted token outside [0, vocab): refused */
 
 /* Limits checked on the host. */
 #define HPC_MAX_BATCH 16384
 #define HPC_MAX_KV_HEADS 256
 #define HPC_MAX_CTAS (1 << 22)
 #define HPC_MAX_Q_LEN 8          /* new tokens per request in hpc_decode_attn_multi */
+#define HPC_MAX_DRAFTS 31        /* drafted tokens per request in hpc_verify_drafts */
 
 /*
  * Task map ([SGL] "Scheduling around live KV work": a global task map built
@@ -754,6 +756,137 @@ hpc_status hpc_kv_read(const void* k_cache, const void* v_cache, const float* k_
                        int num_pages, const int32_t* page_table, int page_table_stride, const int32_t* first,
                        const int32_t* out_starts, int batch, int num_rows, int num_kv_heads, int head_dim, int page_size,
                        void* k_out, void* v_out, int* d_error_word, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Between two attention steps of a decode loop: verification of drafted tokens,
+ * the attention weight that cached tokens received, and eviction by it. A loop
+ * that drafts and evicts runs hpc_decode_attn_multi over the drafted rows,
+ * hpc_verify_drafts, hpc_attn_weights over the accepted rows, and, where a
+ * request has grown past its budget, hpc_kv_select and hpc_kv_compact; it goes
+ * on with the new pages and lengths. (Keys carry their rotation, so positions
+ * go on as before.)
+ */
+
+/*
+ * Attention weight that the cached tokens of each KV head receive from this call's
+ * query rows, given the rows' log-sum-exps from the attention call (out_lse of
+ * hpc_decode_combine, hpc_decode_combine_multi or hpc_prefill). Sequence b has the n
+ * query rows [q_starts[b], q_starts[b + 1]), row i at position seq_lens[b] - n + i
+ * (as in hpc_prefill_plan). Of them the last `window` of the first row_counts[b]
+ * count. With L = seq_lens[b], for every token t < L and KV head h
+ *   weights[b][h][t] = (t < L - n ? decay * weights[b][h][t] : 0)
+ *       + sum over counted rows i with t <= L - n + i, over the 8 query heads j of h,
+ *         of exp(q[i][j] . k[t][h] / sqrt(128) - lse[i][j]).
+ * The sequence's own n tokens are new: what their places held before is not read, so
+ * the array needs no zeros at the start. With decay 0 nothing is read. Weights at
+ * t >= L, and those of a sequence without rows, are left as they were.
+ *   q          device bf16 [num_tokens][num_q_heads][128], 16-byte aligned
+ *   q_starts   device int32 [batch + 1], not decreasing, inside [0, num_tokens]; NULL:
+ *              num_tokens / batch rows each, one sequence after the other (a decode
+ *              batch's [batch][q_len]; num_tokens is a multiple of batch then)
+ *   row_counts device int32 [batch] or NULL (all rows); outside [0, n] as the nearest
+ *   window     rows that count at most; 0: all
+ *   lse        device float32 [num_tokens][num_q_heads]; a row of -inf has no weight
+ *   decay      in [0, 1]; 1 adds to the weights received before
+ *   weights    device float32 [batch][num_kv_heads][weights_stride], weights_stride
+ *              >= page_table_stride * 64
+ *   d_error_word  device int32 or NULL. A sequence whose starts decrease or leave
+ *              [0, num_tokens] is passed over (HPC_DEVERR_BAD_DESCRIPTOR); a length
+ *              beyond the page table's row counts as the row's, and a page id outside
+ *              [0, num_pages) gives its 64 tokens no weight from this call
+ *              (HPC_DEVERR_PAGE_OUT_OF_RANGE); a negative length counts as 0
+ *              (HPC_DEVERR_NEGATIVE_LENGTH)
+ * Sums are float32, in an order that does not depend on the batch. Values of K
+ * that are not finite reach the weights of their own token alone. Errors:
+ * HPC_ERR_INVALID_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA. num_tokens == 0 enqueues nothing.
+ */
+hpc_status hpc_attn_weights(const void* q, const void* k_cache, const float* k_scale, int kv_dtype, int num_pages,
+                            const int32_t* page_table, int page_table_stride, const int32_t* q_starts,
+                            const int32_t* seq_lens, const int32_t* row_counts, int window, const float* lse, int batch,
+                            int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int page_size, float decay,
+                            float* weights, long long weights_stride, int* d_error_word, void* stream);
+
+/*
+ * The tokens of each (request, KV head) that stay when at most `budget` do: the
+ * first num_first, the last num_recent, and of those between them the ones with the
+ * largest weights, of equal weights the lowest index (NaN counts as less than every
+ * number, -0 as 0). A request of at most `budget` tokens keeps all.
+ *   weights    device float32 [batch][num_kv_heads][weights_stride]
+ *   keep       device int32 [batch][num_kv_heads][budget]: indices in rising order,
+ *              -1 behind the last
+ *   keep_lens  device int32 [batch]: min(seq_lens[b], budget)
+ *   d_error_word  device int32 or NULL: a length beyond weights_stride counts as that
+ *              (HPC_DEVERR_PAGE_OUT_OF_RANGE), a negative one as 0
+ *              (HPC_DEVERR_NEGATIVE_LENGTH)
+ * num_first + num_recent <= budget. Errors: HPC_ERR_INVALID_ARG, HPC_ERR_CUDA.
+ */
+hpc_status hpc_kv_select(const float* weights, long long weights_stride, const int32_t* seq_lens, int batch,
+                         int num_kv_heads, int budget, int num_first, int num_recent, int32_t* keep, int32_t* keep_lens,
+                         int* d_error_word, void* stream);
+
+/*
+ * Moves the kept tokens into new pages of the same cache: slot j of request b's new
+ * pages gets, for KV head h, the K and V rows (with their scales) of its token
+ * keep[b][h][j], j < keep_lens[b]; and new_weights[b][h][j] = weights[b][h][keep[b][h][j]]
+ * where weights are given. Bits are copied. The attention calls then take new_table and
+ * keep_lens.
+ *   keep       device int32 [batch][num_kv_heads][keep_stride]
+ *   new_table  device int32 [batch][new_table_stride]; the first ceil(keep_lens[b] / 64)
+ *              entries of row b are read
+ *   weights    device float32 [batch][num_kv_heads][weights_stride] or NULL,
+ *              weights_stride >= page_table_stride * 64; new_weights likewise, another
+ *              array, new_weights_stride >= min(keep_stride, new_table_stride * 64)
+ *   d_error_word  device int32 or NULL: HPC_DEVERR_PAGE_OUT_OF_RANGE (a token or page
+ *              out of range: its row is not written; or keep_lens[b] beyond keep_stride
+ *              or the new table's row: counts as that), HPC_DEVERR_NEGATIVE_LENGTH
+ * The new pages must not be pages that the call reads, or what they then hold is not
+ * determined; but a request whose tokens all stay where they are may name its own.
+ * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA.
+ */
+hpc_status hpc_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int kv_dtype, int num_pages,
+                          const int32_t* page_table, int page_table_stride, const int32_t* keep, int keep_stride,
+                          const int32_t* keep_lens, const int32_t* new_table, int new_table_stride, int batch,
+                          int num_kv_heads, int head_dim, int page_size, const float* weights, long long weights_stride,
+                          float* new_weights, long long new_weights_stride, int* d_error_word, void* stream);
+
+typedef enum hpc_probs_dtype { HPC_PROBS_F32 = 0, HPC_PROBS_BF16 = 1 } hpc_probs_dtype;
+
+/*
+ * Verification of drafted tokens against the target's probabilities. Request b has
+ * n = draft_counts[b] drafted tokens d_0 .. d_{n-1}; p_i is the target's row after i of
+ * them, q_i the draft's row that d_i was drawn from. Draft i is accepted, one after
+ * the other, while
+ *   accept_rand[b][i] * q_i(d_i) < p_i(d_i).
+ * With r accepted, the next token is the least v with C(v) > sample_rand[b] * C(vocab - 1),
+ * C the running sum of max(p_r - q_r, 0) after a refusal and of p_n after the last draft.
+ * Products, differences and sums are exact to 2^-40 of the whole sum or better.
+ *   target_probs  device, row (b, i) of vocab values at (b * (num_drafts + 1) + i) *
+ *              target_stride elements; sums need not be 1
+ *   draft_probs   device, row (b, i) at (b * num_drafts + i) * draft_stride, or NULL: each
+ *              draft was certain (q is 1 at its token and 0 elsewhere)
+ *   probs_dtype   HPC_PROBS_F32 or HPC_PROBS_BF16, of both
+ *   draft_tokens  device int32 [batch][num_drafts]; one outside [0, vocab) is refused
+ *              (HPC_DEVERR_BAD_TOKEN)
+ *   draft_counts  device int32 [batch] or NULL (num_drafts each); outside [0, num_drafts]
+ *              as the nearest
+ *   accept_rand   device float32 [batch][num_drafts], sample_rand [batch]: uniform on [0, 1)
+ *   num_accepted  device int32 [batch]
+ *   tokens     device int32 [batch][num_drafts + 1]: the accepted drafts, the next token,
+ *              then -1
+ *   seq_lens   device int32 [batch] or NULL, lengths that count all num_drafts + 1 new
+ *              tokens of the step, as hpc_decode_attn_multi takes them;
+ *   kept_lens  device int32 [batch] or NULL: the lengths without the tokens that were not
+ *              accepted, max(0, seq_lens[b] - num_drafts + r). It may be seq_lens itself.
+ * Entries (and differences) that are not above 0 and below 2^64, NaN among them, count
+ * as 0. Where nothing is left after a refusal the token is drawn from p_r; where that is
+ * 0 everywhere, it is -1. A sample_rand of 1 or more gives the last entry above 0.
+ * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA.
+ */
+hpc_status hpc_verify_drafts(const void* target_probs, long long target_stride, const void* draft_probs,
+                             long long draft_stride, int probs_dtype, const int32_t* draft_tokens,
+                             const int32_t* draft_counts, const float* accept_rand, const float* sample_rand, int batch,
+                             int num_drafts, int vocab, int32_t* num_accepted, int32_t* tokens, const int32_t* seq_lens,
+                             int32_t* kept_lens, int* d_error_word, void* stream);
 
 /* Synchronises the device, then reads the task map's error word into
  * *device_error_word. Returns HPC_ERR_DEVICE_CHECK when it is non-zero.

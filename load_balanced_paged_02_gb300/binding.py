@@ -108,6 +108,12 @@ SIGNATURES = {
     "hpc_tile_read_error": (_i, [_TP, ctypes.POINTER(_i)]),
     "hpc_kv_write": (_i, [_vp, _vp, _ll, _ll, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp]),
     "hpc_kv_read": (_i, [_vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "hpc_attn_weights": (_i, [_vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, ctypes.c_float,
+                              _vp, _ll, _vp, _vp]),
+    "hpc_kv_select": (_i, [_vp, _ll, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "hpc_kv_compact": (_i, [_vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _ll, _vp, _ll,
+                            _vp, _vp]),
+    "hpc_verify_drafts": (_i, [_vp, _ll, _vp, _ll, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 
 _lock = threading.Lock()
@@ -937,3 +943,174 @@ def hpc_kv_read(k_cache, v_cache, page_table, out_starts, k_out, v_out, k_scale=
                            page_table.data_ptr(), width, _addr(first), out_starts.data_ptr(), B, rows, Hkv, HEAD_DIM, page,
                            k_out.data_ptr(), v_out.data_ptr(), _addr(error_word), _raw_stream(stream, dev))
     _check(what, rc)
+
+
+# ---------------------------------------------------------------- between two attention steps
+
+PROBS_F32, PROBS_BF16 = 0, 1
+
+
+def _error_word(t):
+    if t is not None:
+        _i32("error_word", t)
+
+
+def _weight_rows(what, t, batch=None, heads=None):
+    """Checks of an array [batch, heads, tokens] of weights; its tokens may be the first of longer rows."""
+    if t.dtype != torch.float32 or t.dim() != 3 or (batch is not None and t.shape[0] != batch) or \
+            (heads is not None and t.shape[1] != heads):
+        raise HpcError(what, detail="must be a float32 tensor [batch, KV heads, tokens]")
+    if not t.is_contiguous():
+        raise HpcError(what, detail="must be contiguous")
+
+
+def hpc_attn_weights(q, k_cache, page_table, seq_lens, lse, weights, q_starts=None, k_scale=None, counts=None, window: int = 0,
+                     decay: float = 1.0, num_pages: int | None = None, error_word=None, stream=None):
+    """Adds to ``weights`` (float32 [B, Hkv, tokens], tokens >= page_table.shape[1] * 64) the attention weight
+    that each cached token gets from the query rows, summed over the 8 heads of its KV head; ``decay`` scales
+    what was there, and the places of the call's own tokens are set. q and lse are those of the attention call: a
+    decode batch's [B, Hq, 128] or [B, q_len, Hq, 128], or packed rows [tokens, Hq, 128] with ``q_starts``. Of each
+    sequence the last ``window`` (0: all) of its first ``counts[b]`` (None: all) rows count."""
+    what = "hpc_attn_weights"
+    kvd, pages, page, Hkv = _caches(what, k_cache, k_cache, k_scale, k_scale, num_pages)
+    _query(what, q, new_tokens=q_starts is None)
+    Hq, D = q.shape[-2:]
+    _i32("seq_lens", seq_lens)
+    B = seq_lens.numel()
+    rows = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    if q_starts is None:
+        if q.shape[0] != B:
+            raise HpcError(what, detail="q and seq_lens differ in requests (packed rows need q_starts)")
+    else:
+        _i32("q_starts", q_starts, B + 1)
+    _table("page_table", page_table, B)
+    _tensor("lse", lse, q.shape[:-1], torch.float32)
+    if counts is not None:
+        _i32("counts", counts, B)
+    _weight_rows("weights", weights, B, Hkv)
+    _error_word(error_word)
+    dev = _on_device(what, q, k_cache, k_scale, page_table, seq_lens, lse, weights, q_starts, counts, error_word)
+    rc = lib().hpc_attn_weights(
+        q.data_ptr(), k_cache.data_ptr(), _addr(k_scale), kvd, pages, page_table.data_ptr(), page_table.shape[1],
+        _addr(q_starts), seq_lens.data_ptr(), _addr(counts), window, lse.data_ptr(), B, rows, Hq, Hkv, D, page, decay,
+        weights.data_ptr(), weights.shape[2], _addr(error_word), _raw_stream(stream, dev))
+    _check(what, rc)
+
+
+def hpc_kv_select(weights, seq_lens, budget: int, num_first: int = 0, num_recent: int = 0, keep=None, keep_lens=None,
+                  error_word=None, stream=None):
+    """The tokens of each (request, KV head) that stay: the first, the recent and, of the others, those with the
+    largest ``weights`` (float32 [B, Hkv, tokens]). Returns (keep, keep_lens): int32 [B, Hkv, budget], rising, -1
+    behind the last, and int32 [B]; allocated here unless given."""
+    what = "hpc_kv_select"
+    _i32("seq_lens", seq_lens)
+    B = seq_lens.numel()
+    _weight_rows("weights", weights, B)
+    Hkv = weights.shape[1]
+    if budget < 1:
+        raise HpcError(what, detail="budget must be at least 1")
+    if keep is not None:
+        _tensor("keep", keep, (B, Hkv, budget), torch.int32)
+    if keep_lens is not None:
+        _i32("keep_lens", keep_lens, B)
+    _error_word(error_word)
+    dev = _on_device(what, weights, seq_lens, keep, keep_lens, error_word)
+    if keep is None or keep_lens is None:
+        with _on(stream):
+            if keep is None:
+                keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=weights.device)
+            if keep_lens is None:
+                keep_lens = torch.empty(B, dtype=torch.int32, device=weights.device)
+    rc = lib().hpc_kv_select(weights.data_ptr(), weights.shape[2], seq_lens.data_ptr(), B, Hkv, budget, num_first, num_recent,
+                             keep.data_ptr(), keep_lens.data_ptr(), _addr(error_word), _raw_stream(stream, dev))
+    _check(what, rc)
+    return keep, keep_lens
+
+
+def hpc_kv_compact(k_cache, v_cache, page_table, keep, keep_lens, new_table, k_scale=None, v_scale=None, weights=None,
+                   weights_out=None, num_pages: int | None = None, error_word=None, stream=None):
+    """Moves the kept tokens (``keep`` int32 [B, Hkv, n], the first keep_lens[b] of each row) into the pages that
+    ``new_table`` names, and their ``weights`` into ``weights_out``. New pages must not be pages that the call reads."""
+    what = "hpc_kv_compact"
+    kvd, pages, page, Hkv = _caches(what, k_cache, v_cache, k_scale, v_scale, num_pages)
+    _i32("keep", keep)
+    if keep.dim() != 3 or keep.shape[1] != Hkv:
+        raise HpcError("keep", detail=f"must be [batch, {Hkv}, tokens]")
+    B, _, n = keep.shape
+    _i32("keep_lens", keep_lens, B)
+    _table("page_table", page_table, B)
+    _table("new_table", new_table, B)
+    if (weights is None) != (weights_out is None):
+        raise HpcError(what, detail="weights and weights_out go together")
+    if weights is not None:
+        _weight_rows("weights", weights, B, Hkv)
+        _weight_rows("weights_out", weights_out, B, Hkv)
+    _error_word(error_word)
+    dev = _on_device(what, k_cache, v_cache, k_scale, v_scale, page_table, keep, keep_lens, new_table, weights, weights_out,
+                     error_word)
+    rc = lib().hpc_kv_compact(
+        k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), kvd, pages, page_table.data_ptr(),
+        page_table.shape[1], keep.data_ptr(), n, keep_lens.data_ptr(), new_table.data_ptr(), new_table.shape[1], B, Hkv, HEAD_DIM,
+        page, _addr(weights), 0 if weights is None else weights.shape[2], _addr(weights_out),
+        0 if weights_out is None else weights_out.shape[2], _addr(error_word), _raw_stream(stream, dev))
+    _check(what, rc)
+
+
+def _prob_rows(what, t, batch, rows, vocab, dtype):
+    """The distance in elements between rows of t [batch, rows, vocab], which must be the same from row to row."""
+    if t.dtype != dtype or tuple(t.shape) != (batch, rows, vocab):
+        raise HpcError(what, detail=f"must be a {dtype} tensor of shape {(batch, rows, vocab)}")
+    st = t.stride()
+    row = st[1] if rows > 1 else st[0]
+    if batch * rows == 1:
+        row = vocab
+    if (vocab > 1 and st[2] != 1) or row < vocab or (batch > 1 and rows > 1 and st[0] != rows * row):
+        raise HpcError(what, detail="must have its rows evenly spaced, each contiguous")
+    return row
+
+
+def hpc_verify_drafts(target_probs, draft_tokens, accept_rand, sample_rand, draft_probs=None, draft_counts=None,
+                      num_accepted=None, tokens=None, seq_lens=None, kept_lens=None, error_word=None, stream=None):
+    """Verifies drafted tokens (int32 [B, n]) against target_probs (float32 or bfloat16 [B, n + 1, vocab]; rows may
+    be padded) with the given random numbers (float32 [B, n] and [B]). draft_probs [B, n, vocab]; None: the drafts were
+    certain. Returns (num_accepted [B], tokens [B, n + 1]): the accepted drafts, the next token, then -1.
+    With seq_lens (which count all n + 1 new tokens), kept_lens gets the lengths without the refused tokens."""
+    what = "hpc_verify_drafts"
+    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+        raise HpcError("target_probs", detail=f"unsupported dtype {target_probs.dtype}")
+    if draft_tokens.dim() != 2 or target_probs.dim() != 3:
+        raise HpcError(what, detail="target_probs must be [B, n + 1, vocab] and draft_tokens [B, n]")
+    B, n = draft_tokens.shape
+    V = target_probs.shape[2]
+    if V < 1 or B < 1:
+        raise HpcError(what, detail="no requests, or an empty vocabulary")
+    _i32("draft_tokens", draft_tokens)
+    t_row = _prob_rows("target_probs", target_probs, B, n + 1, V, target_probs.dtype)
+    d_row = V
+    if draft_probs is not None and n > 0:
+        d_row = _prob_rows("draft_probs", draft_probs, B, n, V, target_probs.dtype)
+    _tensor("accept_rand", accept_rand, (B, n), torch.float32)
+    _tensor("sample_rand", sample_rand, (B,), torch.float32)
+    for t, name in ((draft_counts, "draft_counts"), (num_accepted, "num_accepted"), (seq_lens, "seq_lens"), (kept_lens, "kept_lens")):
+        if t is not None:
+            _i32(name, t, B)
+    if tokens is not None:
+        _tensor("tokens", tokens, (B, n + 1), torch.int32)
+    if kept_lens is not None and seq_lens is None:
+        raise HpcError("kept_lens", detail="needs seq_lens")
+    _error_word(error_word)
+    dev = _on_device(what, target_probs, draft_tokens, accept_rand, sample_rand, draft_probs, draft_counts, num_accepted, tokens,
+                     seq_lens, kept_lens, error_word)
+    if num_accepted is None or tokens is None:
+        with _on(stream):
+            if num_accepted is None:
+                num_accepted = torch.empty(B, dtype=torch.int32, device=target_probs.device)
+            if tokens is None:
+                tokens = torch.empty((B, n + 1), dtype=torch.int32, device=target_probs.device)
+    rc = lib().hpc_verify_drafts(
+        target_probs.data_ptr(), t_row, _addr(draft_probs) if n > 0 else None, d_row,
+        PROBS_BF16 if target_probs.dtype == torch.bfloat16 else PROBS_F32, draft_tokens.data_ptr(), _addr(draft_counts),
+        accept_rand.data_ptr(), sample_rand.data_ptr(), B, n, V, num_accepted.data_ptr(), tokens.data_ptr(), _addr(seq_lens),
+        _addr(kept_lens), _addr(error_word), _raw_stream(stream, dev))
+    _check(what, rc)
+    return num_accepted, tokens
