@@ -9,10 +9,11 @@
 // heads is a chain of additions in that thread, without a shuffle or an atomic. K goes from
 // the page into shared memory by TMA and into the product as it is, e4m3 codes too (the
 // query is split into two e4m3 numbers, whose products add up in the accumulator; the key's
-// scale multiplies the score). One CTA per SM, 14 warps:
+// scale multiplies the score). One CTA per SM, 12 warps
+// (three per sub-partition, so that a thread can have 168 registers):
 //   * warp 0, producer: tiles of 128 tokens (two pages) into a ring of stages;
 //   * warp 1, issuer: the MMAs of each tile with every query slot, 16 rows (128 columns) a slot;
-//   * warps 2, 3, 12, 13, stagers: query rows into the slots (4, so that a pass takes up to
+//   * warps 2 and 3, stagers: query rows into the slots (4, so that a pass takes up to
 //     64 rows), bf16 as they are or split, with each row's constants;
 //   * warps 4-7 and 8-11, two groups that take the even and the odd tiles: exp2 and sums.
 // More than 64 rows are several passes over the CTA's tiles, the last rows (which see most)
@@ -43,8 +44,8 @@ constexpr int kCols = kSlotRows * kGroup;     // accumulator columns of a slot
 constexpr int kSlots = 4;
 constexpr int kPassRows = kSlots * kSlotRows;
 constexpr int kSlotBytes = 32768;             // bf16 [2 dim halves][128][128 B], or e4m3 [hi, lo][128][128 B]
-constexpr int kThreads = 448;
-constexpr int kStagers = 128;
+constexpr int kThreads = 384;
+constexpr int kStagers = 64;
 constexpr uint32_t kTmemCols = 512;           // two accumulators of 128 columns per group
 constexpr int kTileCost = 24;                 // query rows
 constexpr int kSeqCost = 8;                   // a sequence's start in a CTA, in rows
@@ -56,19 +57,16 @@ struct Layout {
     static constexpr int kStages = FP8 ? 5 : 3;
     static constexpr int kStageBytes = FP8 ? 16384 : 32768;
     static constexpr size_t kQ = (size_t)kStages * kStageBytes;
-    static constexpr size_t kKs = kQ + kSlots * kSlotBytes;                   // e4m3: float [stage][128] key scales
-    static constexpr size_t kNl = kKs + (FP8 ? kStages * kTile * 4 : 0);      // float [slot][128]: -lse log2(e)
+    static constexpr size_t kNl = kQ + kSlots * kSlotBytes;                   // float [slot][128]: -lse log2(e)
     static constexpr size_t kQc = kNl + kSlots * kCols * 4;                   // e4m3: float [slot][128]: score factors
     static constexpr size_t kScan = kQc + (FP8 ? kSlots * kCols * 4 : 0);     // int64 [warps]
     static constexpr size_t kRun = kScan + kThreads / 32 * 8;                 // int [8]
-    static constexpr size_t kMeta = kRun + 32;                                // int [stage]: which pages are there
-    static constexpr size_t kBars = kMeta + 32;
+    static constexpr size_t kBars = kRun + 32;
     static constexpr int kNumBars = 2 * kStages + 2 * kSlots + 8;
     static constexpr size_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr size_t kFlag = kTmemSlot + 4;
     static constexpr size_t kTotal = kFlag + 4;
     static_assert(kTotal <= 232448, "over the 227 KB shared-memory limit of a CTA");
-    static_assert(kStages <= 8, "meta words");
 };
 
 struct WeightParams {
@@ -78,6 +76,7 @@ struct WeightParams {
     const int32_t* q_starts;
     const int32_t* seq_lens;
     const int32_t* counts;
+    const float* k_scale;
     const float* lse;
     float* weights;
     long long w_stride;
@@ -221,17 +220,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 // 32 lanes from the warp's base lane x N consecutive columns: register k of thread t is
 // lane t, column k.
-__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, float (&r)[8]) {
-    uint32_t u[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-                 : "r"(taddr)
-                 : "memory");
-    tmem_ld_wait();
-#pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = __uint_as_float(u[k]);
-}
-
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -244,33 +232,102 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
         : "memory");
 }
 
-// The weights of one query row's 8 heads for the thread's token, summed. nl, qc: the row's
-// constants in shared memory.
+// Pairs of floats in one 64-bit register: two additions or products for one issue slot.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t exp2_2(uint64_t x) {
+    const float2 v = unpair(x);
+    return pair(fast_exp2(v.x), fast_exp2(v.y));
+}
+
+// The weights of one query row's 8 heads for the thread's token, as two sums of four. s: the
+// scores; nl, qc: the row's constants in shared memory; factor: twice the token's.
 template <bool FP8>
-__device__ __forceinline__ float row_weight(const float (&s)[8], const float* nl, const float* qc, float factor) {
-    float e[8];
+__device__ __forceinline__ uint64_t row_weight(const uint32_t* s, const float* nl, const float* qc, uint64_t factor) {
+    uint64_t e[4];
 #pragma unroll
-    for (int k = 0; k < 8; k += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(nl + k);
+    for (int k = 0; k < 2; ++k) {
+        const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(nl + 4 * k);
+        const uint64_t x = pair(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1]));
+        const uint64_t y = pair(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3]));
         if constexpr (FP8) {
-            const float4 c = *reinterpret_cast<const float4*>(qc + k);
-            e[k] = fast_exp2(fmaf(s[k] * factor, c.x, l.x));
-            e[k + 1] = fast_exp2(fmaf(s[k + 1] * factor, c.y, l.y));
-            e[k + 2] = fast_exp2(fmaf(s[k + 2] * factor, c.z, l.z));
-            e[k + 3] = fast_exp2(fmaf(s[k + 3] * factor, c.w, l.w));
+            const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(qc + 4 * k);
+            e[2 * k] = exp2_2(fma2(mul2(x, factor), c.x, l.x));
+            e[2 * k + 1] = exp2_2(fma2(mul2(y, factor), c.y, l.y));
         } else {
-            e[k] = fast_exp2(fmaf(s[k], factor, l.x));
-            e[k + 1] = fast_exp2(fmaf(s[k + 1], factor, l.y));
-            e[k + 2] = fast_exp2(fmaf(s[k + 2], factor, l.z));
-            e[k + 3] = fast_exp2(fmaf(s[k + 3], factor, l.w));
+            e[2 * k] = exp2_2(fma2(x, factor, l.x));
+            e[2 * k + 1] = exp2_2(fma2(y, factor, l.y));
         }
     }
-    return ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    return add2(add2(e[0], e[1]), add2(e[2], e[3]));
+}
+
+// Rows [r, r + 4) of a slot, those there are: added where they see the token (MASK; else
+// all of them do).
+template <bool FP8, bool MASK>
+__device__ __forceinline__ void four_rows(const uint32_t (&s)[32], int r, int rows, int sees, const float* nl, const float* qc,
+                                          uint64_t factor, uint64_t& sum) {
+    nl += r * kGroup;
+    qc += r * kGroup;
+    if (r + 4 <= rows) {
+        uint64_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[k] = row_weight<FP8>(s + 8 * k, nl + k * kGroup, qc + k * kGroup, factor);
+            if (MASK && r + k < sees) w[k] = 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum = add2(sum, w[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (r + k < rows) {
+                const uint64_t w = row_weight<FP8>(s + 8 * k, nl + k * kGroup, qc + k * kGroup, factor);
+                if (!MASK || r + k >= sees) sum = add2(sum, w);
+            }
+        }
+    }
+}
+
+// All rows of a slot.
+template <bool FP8, bool MASK>
+__device__ __forceinline__ void slot_rows(uint32_t ta, int rows, int sees, const float* nl, const float* qc, uint64_t factor,
+                                          uint64_t& sum) {
+#pragma unroll 1
+    for (int r = 0; r < rows; r += 4) {
+        uint32_t v[32];
+        tmem_ld_x32(ta + r * kGroup, v);
+        tmem_ld_wait();
+        four_rows<FP8, MASK>(v, r, rows, sees, nl, qc, factor, sum);
+    }
 }
 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_ks, const WeightParams p) {
+    attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const WeightParams p) {
     using LY = Layout<FP8>;
     constexpr int NS = LY::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -282,7 +339,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* accfree = accfull + 4;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + LY::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kFlag);
-    volatile int* meta = reinterpret_cast<volatile int*>(smem + LY::kMeta);
     int* run = reinterpret_cast<int*>(smem + LY::kRun);
     float* nl = reinterpret_cast<float*>(smem + LY::kNl);
     float* qc = reinterpret_cast<float*>(smem + LY::kQc);
@@ -291,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1 + 4);  // the MMAs that read the keys; a group's warps (scales and page word)
+            mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&qfull[i], kStagers);
@@ -410,19 +466,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) {
                         ok = wait_bounded(&empty[st], ((seq / NS) & 1) ^ 1, abort_flag, kWaitLimitNs);
                         if (ok) {
-                            meta[st] = there;
                             if (there == 0) {
                                 mbar_arrive(&full[st]);
                             } else {
-                                constexpr uint32_t kPageBytes = FP8 ? 8192 + 256 : 16384;
+                                constexpr uint32_t kPageBytes = FP8 ? 8192 : 16384;
                                 mbar_arrive_expect_tx(&full[st], (there == 3 ? 2 : 1) * kPageBytes);
 #pragma unroll
                                 for (int u = 0; u < 2; ++u) {
                                     if (!(there >> u & 1)) continue;
                                     uint8_t* dst = smem + st * LY::kStageBytes + u * 8192;
-                                    if constexpr (FP8)
-                                        tma_load_2d(smem + LY::kKs + (st * kTile + u * kChunk) * 4, &tm_ks, &full[st], 0,
-                                                    page[u] * p.num_kv_heads + x.h, pol);
                                     tma_load_3d(dst, &tm_k, &full[st], 0, x.h, page[u] * kChunk, pol);
                                     if constexpr (!FP8)
                                         tma_load_3d(dst + 16384, &tm_k, &full[st], 64, x.h, page[u] * kChunk, pol);
@@ -443,83 +495,106 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t k = seq > (uint32_t)NS ? seq - NS : 0u; k < seq; ++k)
                 wait_bounded(&full[k % NS], (k / NS) & 1, nullptr, kDrainLimitNs);
     } else if (warp == 1) {
-        // ============================ MMA issuer (one thread)
-        if (lane == 0) {
-            constexpr uint32_t kId = FP8 ? idesc_e4m3(kTile, 0) : idesc_16bit(false, kTile, 0, 0);
-            uint32_t seq = 0, qseq = 0, turn[2] = {0, 0};
-            while (ok && walk.next(p, x)) {
-                const int ns = x.slots();
-                for (int j = x.j0; j < x.jl && ok; ++j, ++seq) {
-                    const uint32_t st = seq % NS, g = j & 1;
-                    ok = wait_bounded(&full[st], (seq / NS) & 1, abort_flag, kWaitLimitNs);
-                    const uint32_t ka = smem_u32(smem + st * LY::kStageBytes);
-                    for (int s = 0; s < ns && ok; ++s) {
-                        const uint32_t sl = (qseq + s) % kSlots;
-                        if (j == x.j0) ok = wait_bounded(&qfull[sl], ((qseq + s) / kSlots) & 1, abort_flag, kWaitLimitNs);
-                        const uint32_t c = g ? turn[1]++ : turn[0]++;
-                        const uint32_t acc = 2 * g + (c & 1);
-                        if (ok) ok = wait_bounded(&accfree[acc], ((c >> 1) & 1) ^ 1, abort_flag, kWaitLimitNs);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const int rows = min(kSlotRows, x.hi - x.lo - s * kSlotRows);
-                        const uint32_t n16 = (uint32_t)(rows + 1) / 2;  // columns in sixteens
-                        const uint32_t id = kId | (n16 << 18);
-                        const uint32_t qa = smem_u32(smem + LY::kQ + sl * kSlotBytes);
-                        const uint32_t d = tmem + acc * kCols;
-                        if constexpr (FP8) {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                umma_e4m3(d, sdesc_sw128(ka + kk * 32, 16, 1024), sdesc_sw128(qa + kk * 32, 16, 1024), id, kk > 0);
-                                umma_e4m3(d, sdesc_sw128(ka + kk * 32, 16, 1024), sdesc_sw128(qa + 16384 + kk * 32, 16, 1024), id, 1);
-                            }
-                        } else {
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
-                                const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
-                                umma_f16(d, sdesc_sw128(ka + off, 16, 1024), sdesc_sw128(qa + off, 16, 1024), id, kk > 0);
-                            }
-                        }
-                        umma_commit(&accfull[acc]);
-                        if (j + 1 == x.jl) umma_commit(&qfree[sl]);
-                    }
-                    if (ok) umma_commit(&empty[st]);
-                }
-                if (x.jl > x.j0) qseq += ns;
-            }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-    } else if (warp >= 4 && warp < 12) {
-        // ============================ groups g = 0, 1: tiles j with j % 2 == g; thread = token
-        const int g = (warp >> 2) - 1, wq = warp & 3;
-        const float scale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
-        uint32_t seq = 0, qseq = 0, turn = 0;
+        // ============================ MMA issuer (one lane; the warp goes along)
+        const uint32_t el = elect_lane();
+        constexpr uint32_t kId = FP8 ? idesc_e4m3(kTile, 0) : idesc_16bit(false, kTile, 0, 0);
+        // descriptors of the first stage and slot; the others lie at fixed distances (in
+        // 16-byte units, the low bits of a descriptor)
+        const uint64_t dk = sdesc_sw128(smem_u32(smem), 16, 1024), dq = sdesc_sw128(smem_u32(smem + LY::kQ), 16, 1024);
+        uint32_t seq = 0, qseq = 0, turn0 = 0, turn1 = 0;
         while (ok && walk.next(p, x)) {
             const int ns = x.slots();
+            for (int j = x.j0; j < x.jl && ok; ++j, ++seq) {
+                const uint32_t st = seq % NS, g = j & 1;
+                ok = warp_wait(&full[st], (seq / NS) & 1, abort_flag);
+                const uint64_t k = dk + st * (LY::kStageBytes >> 4);
+                for (int s = 0; s < ns && ok; ++s) {
+                    const uint32_t sl = (qseq + s) % kSlots;
+                    if (j == x.j0) ok = warp_wait(&qfull[sl], ((qseq + s) / kSlots) & 1, abort_flag);
+                    const uint32_t c = g ? turn1++ : turn0++;
+                    const uint32_t acc = 2 * g + (c & 1);
+                    if (ok) ok = warp_wait(&accfree[acc], ((c >> 1) & 1) ^ 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int rows = min(kSlotRows, x.hi - x.lo - s * kSlotRows);
+                    const uint32_t id = kId | (uint32_t)((rows + 1) / 2) << 18;  // columns: a multiple of 16
+                    const uint64_t q = dq + sl * (kSlotBytes >> 4);
+                    const uint32_t d = tmem + acc * kCols;
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            umma_e4m3_el(el, d, k + kk * 2, q + kk * 2, id, kk > 0);
+                            umma_e4m3_el(el, d, k + kk * 2, q + 1024 + kk * 2, id, 1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
+                            umma_f16_el(el, d, k + off, q + off, id, kk > 0);
+                        }
+                    }
+                    umma_commit_el(el, &accfull[acc]);
+                    if (j + 1 == x.jl) umma_commit_el(el, &qfree[sl]);
+                }
+                if (ok) umma_commit_el(el, &empty[st]);
+            }
+            if (x.jl > x.j0) qseq += ns;
+        }
+    } else if (warp >= 4) {
+        // ============================ groups g = 0, 1: tiles j with j % 2 == g; thread = token
+        const int g = (warp >> 2) - 1, wq = warp & 3;
+        constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
+        // What a tile needs from memory comes a tile ahead, its page id two tiles: across
+        // passes too, unless a pass goes on from the sums of the one before.
+        struct Token {
+            float old, factor;
+            bool there;
+        };
+        auto first_tile = [&](const Pass& y) { return y.j0 + ((y.j0 & 1) ^ g); };
+        auto page_of = [&](const Pass& y, int j) {
+            const int c = 2 * j + (wq >> 1);
+            return j < y.j1 && (long long)c * kChunk < y.L ? p.page_table[y.b * p.pt_stride + c] : -1;
+        };
+        auto fetch = [&](const Pass& y, int j, int page) {
+            Token k{0.f, kScale, (unsigned)page < (unsigned)p.num_pages};
+            const int t = j * kTile + 32 * wq + lane;
+            if (j < y.j1 && t < (y.first ? y.p0 : y.L) && !(y.first && p.decay == 0.f))
+                k.old = p.weights[((long long)y.b * p.num_kv_heads + y.h) * p.w_stride + t];
+            if (FP8 && k.there) k.factor = p.k_scale[((long long)page * p.num_kv_heads + y.h) * kChunk + (t & (kChunk - 1))];
+            return k;
+        };
+        uint32_t qseq = 0, turn = 0;
+        bool have = walk.next(p, x);
+        Token ahead{0.f, 0.f, false};
+        int page = -1;  // of the tile after the one ahead
+        if (have) {
+            ahead = fetch(x, first_tile(x), page_of(x, first_tile(x)));
+            page = page_of(x, first_tile(x) + 2);
+        }
+        while (have && ok) {
+            Pass y;
+            have = walk.next(p, y);
+            const int jy = have ? first_tile(y) : 0;
+            const int page_y = have ? page_of(y, jy) : -1;
+            const int ns = x.slots();
             float* wrow = p.weights + ((long long)x.b * p.num_kv_heads + x.h) * p.w_stride;
-            bool any = false;  // this group has seen the pass's slots
-            for (int j = x.j0; j < x.j1 && ok; ++j) {
-                const bool live = j < x.jl;
-                const uint32_t at = seq;
-                seq += live;
-                if ((j & 1) != g) continue;
+            bool any = false;      // this group has seen the pass's slots
+            bool fetched = false;  // ahead is of the next pass
+            for (int j = first_tile(x); j < x.j1; j += 2) {
                 const int t = j * kTile + 32 * wq + lane;
-                float old = 0.f;
-                if (t < x.L) {
-                    if (!x.first)
-                        old = wrow[t];
-                    else if (p.decay != 0.f && t < x.p0)
-                        old = p.decay * wrow[t];
+                const Token now = ahead;
+                if (j + 2 < x.j1) {
+                    ahead = fetch(x, j + 2, page);
+                    page = page_of(x, j + 4);
+                } else if (have && y.first) {
+                    ahead = fetch(y, jy, page_y);
+                    page = page_of(y, jy + 2);
+                    fetched = true;
                 }
                 float sum = 0.f;
-                if (live) {
-                    const uint32_t st = at % NS;
-                    ok = warp_wait(&full[st], (at / NS) & 1, abort_flag);
-                    if (!ok) break;
-                    const bool there = meta[st] >> (wq >> 1) & 1;
-                    float factor = scale;
-                    if constexpr (FP8) factor = reinterpret_cast<const float*>(smem + LY::kKs)[st * kTile + 32 * wq + lane];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[st]);
+                if (j < x.jl) {
+                    uint64_t sum2 = 0;
+                    const uint64_t factor = pair(now.factor, now.factor);
                     for (int s = 0; s < ns; ++s) {
                         const uint32_t sl = (qseq + s) % kSlots;
                         if (!any) ok = warp_wait(&qfull[sl], ((qseq + s) / kSlots) & 1, abort_flag);
@@ -532,23 +607,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t ta = tmem + ((uint32_t)(32 * wq) << 16) + acc * kCols;
                         const float* nls = nl + sl * kCols;
                         const float* qcs = qc + sl * kCols;
-                        const int sees = t - x.p0 - r0;  // rows of the slot from this one on see the token
-#pragma unroll 1
-                        for (int r = 0; r < rows; ++r) {
-                            float v[8];
-                            tmem_ld_x8(ta + r * 8, v);
-                            const float wgt = row_weight<FP8>(v, nls + r * 8, qcs + r * 8, factor);
-                            if (r >= sees) sum += wgt;
-                        }
+                        // rows of the slot from t - p0 - r0 on see token t: all of them before the last tiles
+                        if (j * kTile + kTile - 1 <= (long long)x.p0 + r0)
+                            slot_rows<FP8, false>(ta, rows, 0, nls, qcs, factor, sum2);
+                        else
+                            slot_rows<FP8, true>(ta, rows, t - x.p0 - r0, nls, qcs, factor, sum2);
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&accfree[acc]);
                     }
                     if (!ok) break;
                     any = true;
-                    if (!there) sum = 0.f;
+                    const float2 v = unpair(sum2);
+                    if (now.there) sum = v.x + v.y;
                 }
-                if (t < x.L) wrow[t] = old + sum;
+                if (t < x.L) wrow[t] = (x.first ? p.decay * now.old : now.old) + sum;
             }
             if (x.jl > x.j0) {
                 // the slots are this pass's until both groups have seen them
@@ -560,10 +633,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 qseq += ns;
             }
+            if (have && !fetched) {
+                ahead = fetch(y, jy, page_y);
+                page = page_of(y, jy + 2);
+            }
+            x = y;
         }
     } else {
         // ============================ stagers: query rows into slots
-        const int sid = (warp < 4 ? warp - 2 : warp - 10) * 32 + lane;
+        const int sid = (warp - 2) * 32 + lane;
         uint32_t qseq = 0;
         while (ok && walk.next(p, x)) {
             if (x.jl <= x.j0) continue;
@@ -575,24 +653,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r0 = x.lo + s * kSlotRows, rows = min(kSlotRows, x.hi - r0);
                 uint8_t* slot = smem + LY::kQ + sl * kSlotBytes;
                 const long long row0 = ((long long)x.q0 + r0) * p.num_q_heads + x.h * kGroup;
-                if (sid < rows * kGroup) {
-                    const float l = p.lse[row0 + (long long)(sid / kGroup) * p.num_q_heads + sid % kGroup];
-                    nl[sl * kCols + sid] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row of -inf: no weight
+                for (int c = sid; c < rows * kGroup; c += kStagers) {
+                    const float l = p.lse[row0 + (long long)(c / kGroup) * p.num_q_heads + c % kGroup];
+                    nl[sl * kCols + c] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row of -inf: no weight
                 }
                 if constexpr (!FP8) {
-                    // row r in step r: a head's 16 pieces of 16 bytes by 16 threads
-                    const int head = sid >> 4, c = sid & 15;
-                    const __nv_bfloat16* src = p.q + (row0 + head) * kHeadDim + c * 8;
+                    // a head's 16 pieces of 16 bytes by 16 threads, eight rows at once
+                    const int c = sid & 15;
                     const long long step = (long long)p.num_q_heads * kHeadDim;
-                    uint8_t* dst = slot + (c >> 3) * 16384 + head * 128 + (((c & 7) ^ head) << 4);
-                    for (int r = 0; r < rows; r += 8) {
+                    for (int i = 0; i < 2 * rows; i += 8) {  // i: 2 row + half of the heads
                         uint4 v[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (r + k < rows) v[k] = *reinterpret_cast<const uint4*>(src + (r + k) * step);
+                        for (int k = 0; k < 8; ++k) {
+                            const int head = (sid >> 4) + 4 * (k & 1), r = (i + k) >> 1;
+                            if (i + k < 2 * rows) v[k] = *reinterpret_cast<const uint4*>(p.q + row0 * kHeadDim + r * step + head * kHeadDim + c * 8);
+                        }
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (r + k < rows) *reinterpret_cast<uint4*>(dst + (r + k) * kGroup * 128) = v[k];
+                        for (int k = 0; k < 8; ++k) {
+                            const int head = (sid >> 4) + 4 * (k & 1), r = (i + k) >> 1;
+                            if (i + k < 2 * rows)
+                                *reinterpret_cast<uint4*>(slot + (c >> 3) * 16384 + (r * kGroup + head) * 128 + (((c & 7) ^ head) << 4)) = v[k];
+                        }
                     }
                 } else {
                     // two threads per row of 128: half hh of its dims each, split into hi and lo codes
@@ -670,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool FP8>
-cudaError_t launch(const CUtensorMap (&maps)[2], const WeightParams& p, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tm_k, const WeightParams& p, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -687,16 +768,15 @@ cudaError_t launch(const CUtensorMap (&maps)[2], const WeightParams& p, cudaStre
     }
     const int ctas = tile_default_ctas();
     if (ctas < 1) return cudaErrorUnknown;
-    return launch_pdl(attn_weights_kernel<FP8>, dim3(ctas), dim3(kThreads), Layout<FP8>::kTotal, s, maps[0], maps[1], p);
+    return launch_pdl(attn_weights_kernel<FP8>, dim3(ctas), dim3(kThreads), Layout<FP8>::kTotal, s, tm_k, p);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_weights(const AttnWeightsArgs& a, cudaStream_t s) {
-    CUtensorMap maps[2];  // K, K scales
-    memset(maps, 0, sizeof maps);
-    if (!make_kv_map(&maps[0], a.k_cache, a.fp8, a.num_pages, a.num_kv_heads)) return cudaErrorInvalidValue;
-    if (a.fp8 && !make_scale_map(&maps[1], a.k_scale, a.num_pages, a.num_kv_heads)) return cudaErrorInvalidValue;
+    CUtensorMap tm_k;
+    memset(&tm_k, 0, sizeof tm_k);
+    if (!make_kv_map(&tm_k, a.k_cache, a.fp8, a.num_pages, a.num_kv_heads)) return cudaErrorInvalidValue;
     WeightParams p;
     p.q = static_cast<const __nv_bfloat16*>(a.q);
     p.page_table = a.page_table;
@@ -704,6 +784,7 @@ cudaError_t launch_attn_weights(const AttnWeightsArgs& a, cudaStream_t s) {
     p.q_starts = a.q_starts;
     p.seq_lens = a.seq_lens;
     p.counts = a.counts;
+    p.k_scale = a.k_scale;
     p.lse = a.lse;
     p.weights = a.weights;
     p.w_stride = a.w_stride;
@@ -718,7 +799,7 @@ cudaError_t launch_attn_weights(const AttnWeightsArgs& a, cudaStream_t s) {
     const long long most = a.pt_stride * kChunk;
     p.max_len = most > kMaxKeys ? kMaxKeys : (int)most;
     p.decay = a.decay;
-    return a.fp8 ? launch<true>(maps, p, s) : launch<false>(maps, p, s);
+    return a.fp8 ? launch<true>(tm_k, p, s) : launch<false>(tm_k, p, s);
 }
 
 }  // namespace hpc
