@@ -8,7 +8,9 @@
 // answer with a neighbour. Differences and sums are therefore kept as unevaluated pairs of
 // floats (Knuth's two-sum and its difference form: exact errors, The Art of Computer
 // Programming, vol. 2, 4.2.2), which holds 48 bits at the rate of 32-bit additions; 64-bit
-// ones would bound the kernel. Per-thread sums are joined in 64 bits.
+// ones are so slow here (a warp's addition takes 16 cycles of its SM and more) that joining
+// the threads' sums with them alone took 10 us; only the comparisons with the border are in
+// 64 bits, in one warp.
 //
 // Only row r of p and q is read whole. A cluster of CTAs takes a request, each warp a
 // contiguous part of the vocabulary; the parts' sums say which warp holds the token, and
@@ -16,20 +18,22 @@
 #include "loop.cuh"
 #include "tile.cuh"
 
+#include <atomic>
+
 namespace hpc {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kAhead = 4;
 constexpr int kMaxCluster = 8;
-constexpr int kRun = 8;  // consecutive entries of a lane in the second pass
+constexpr int kRun = 8;     // consecutive entries of a lane in the second pass
+constexpr int kPart = 256;  // a warp's part is a multiple of this many entries
 constexpr float kMost = 18446744073709551616.f;  // entries from 2^64 on count as 0
 
 struct Pair {
     float s, e;
 };
 
-// The weight of an entry, exact as s + e: p, or p - q where that is above 0.
+// The weight of an entry, exact as s + e: p, or p - q, where that is above 0 and below 2^64.
 __device__ __forceinline__ Pair entry(float p, float q, bool both) {
     if (!both) q = 0.f;
     const float s = p - q;
@@ -54,11 +58,180 @@ __device__ __forceinline__ float load(const void* p, long long i) {
         return static_cast<const float*>(p)[i];
 }
 
+// Value k of 16 bytes of a row.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, int cluster) {
-    __shared__ int accepted_sh;
-    __shared__ double warp_sum[kWarps];
-    __shared__ double cta_sum[2];  // of the residual, and of p alone
+__device__ __forceinline__ float at(const uint4& r, int k) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    if constexpr (BF16) return __uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
+    return __uint_as_float(w[k]);
+}
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two pairs side by side, in 64-bit registers: two additions for one issue slot.
+struct Pair2 {
+    uint64_t s, e;
+};
+__device__ __forceinline__ uint64_t pack(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float2 unpack(uint64_t v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void add(Pair2& a, uint64_t s) {  // e is left alone where it is 0
+    const uint64_t t = add2(a.s, s), bb = sub2(t, a.s);
+    a.e = add2(a.e, add2(sub2(a.s, sub2(t, bb)), sub2(s, bb)));
+    a.s = t;
+}
+
+// Two entries whose values lie in [0, 2^64) or are below 0 or NaN (larger ones make the sum
+// too large, which the caller sees). With q' = min(q, p), p' = max(p, 0) (either takes the
+// number where the other is NaN) p' >= q', so that the difference's error is (p' - s) - q'.
+template <bool BOTH>
+__device__ __forceinline__ void add_entries(Pair2& acc, float p0, float p1, float q0, float q1) {
+    p0 = fmaxf(p0, 0.f);
+    p1 = fmaxf(p1, 0.f);
+    if constexpr (BOTH) {
+        const uint64_t p = pack(p0, p1), q = pack(fminf(q0, p0), fminf(q1, p1));
+        const uint64_t s = sub2(p, q);
+        acc.e = add2(acc.e, sub2(sub2(p, s), q));
+        add(acc, s);
+    } else {
+        add(acc, pack(p0, p1));
+    }
+}
+
+// A lane's part of the sum over entries [v0, v1) of a row. EACH looks at every entry on its
+// own, for parts with an entry that is left out (`out`) or too large to be a probability.
+// Rows on 16-byte boundaries come through shared memory, kAhead pieces of 16 bytes per lane
+// and row on their way without a register: `ring` is this thread's [kAhead][2], kThreads apart.
+template <int kThreads, bool BF16, bool BOTH, bool EACH>
+__device__ __forceinline__ Pair lane_sum(const void* p, const void* q, long long v0, long long v1, int out, int lane, uint4* ring) {
+    constexpr int kVec = BF16 ? 8 : 4, kSize = BF16 ? 2 : 4;
+    Pair one{0.f, 0.f};
+    Pair2 two{0, 0};
+    long long v = v0;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p) | (BOTH ? reinterpret_cast<uintptr_t>(q) : 0)) & 15) == 0;
+    if (!EACH && wide) {
+        const int n = (int)((v1 - v0) / (32 * kVec));  // pieces of a lane
+        const uint8_t* ps = static_cast<const uint8_t*>(p) + v0 * kSize + lane * 16;
+        const uint8_t* qs = BOTH ? static_cast<const uint8_t*>(q) + v0 * kSize + lane * 16 : nullptr;
+        auto fetch = [&](int i) {
+            if (i < n) {
+                copy16(ring + (i % kAhead) * 2 * kThreads, ps + i * 512);
+                if (BOTH) copy16(ring + ((i % kAhead) * 2 + 1) * kThreads, qs + i * 512);
+            }
+            copy_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            copy_wait<kAhead - 1>();
+            const uint4 x = ring[(i % kAhead) * 2 * kThreads];
+            const uint4 y = BOTH ? ring[((i % kAhead) * 2 + 1) * kThreads] : make_uint4(0u, 0u, 0u, 0u);
+            fetch(i + kAhead);
+#pragma unroll
+            for (int k = 0; k < kVec; k += 2)
+                add_entries<BOTH>(two, at<BF16>(x, k), at<BF16>(x, k + 1), at<BF16>(y, k), at<BF16>(y, k + 1));
+        }
+        copy_wait<0>();
+        v += (long long)n * 32 * kVec;
+    }
+    for (; v < v1; v += 32 * 8) {
+        float x[8], y[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const long long i = v + 32 * u + lane;
+            x[u] = i < v1 ? load<BF16>(p, i) : 0.f;
+            y[u] = BOTH && i < v1 ? load<BF16>(q, i) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; u += 2) {
+            if constexpr (EACH) {
+#pragma unroll
+                for (int k = u; k < u + 2; ++k)
+                    if (v + 32 * k + lane != out) add(one, entry(x[k], y[k], BOTH));
+            } else {
+                add_entries<BOTH>(two, x[u], x[u + 1], y[u], y[u + 1]);
+            }
+        }
+    }
+    if (!EACH) {
+        const float2 s = unpack(two.s), e = unpack(two.e);
+        one = Pair{s.x, e.x};
+        add(one, Pair{s.y, e.y});
+    }
+    return one;
+}
+
+template <int kThreads, bool BF16>
+__device__ __forceinline__ Pair lane_sum(const void* p, const void* q, long long v0, long long v1, int out, int lane, uint4* ring) {
+    if (out < v0 || out >= v1) {
+        const Pair x = q ? lane_sum<kThreads, BF16, true, false>(p, q, v0, v1, -1, lane, ring) : lane_sum<kThreads, BF16, false, false>(p, q, v0, v1, -1, lane, ring);
+        if (__all_sync(0xffffffffu, x.s < kMost)) return x;
+    }
+    return q ? lane_sum<kThreads, BF16, true, true>(p, q, v0, v1, out, lane, ring) : lane_sum<kThreads, BF16, false, true>(p, q, v0, v1, out, lane, ring);
+}
+
+__device__ __forceinline__ Pair shfl_up(const Pair& x, int o) {
+    return Pair{__shfl_up_sync(0xffffffffu, x.s, o), __shfl_up_sync(0xffffffffu, x.e, o)};
+}
+
+// Sum of the lanes up to this one.
+__device__ __forceinline__ Pair scan(Pair x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Pair y = shfl_up(x, o);
+        if (lane >= o) add(x, y);
+    }
+    return x;
+}
+
+__device__ __forceinline__ double value(const Pair& x) { return (double)x.s + (double)x.e; }
+
+// The first lane whose sum, after `before`, exceeds the border, or else the last with a
+// weight at all; -1 if there is none. `before` becomes the sum before that lane.
+__device__ __forceinline__ int find(const Pair& x, Pair& before, double border, int lane) {
+    const Pair incl = scan(x, lane);
+    Pair upto = before;
+    add(upto, incl);
+    const bool some = x.s > 0.f;
+    const uint32_t over = __ballot_sync(0xffffffffu, some && value(upto) > border), any = __ballot_sync(0xffffffffu, some);
+    if (!any) return -1;
+    const int l = over ? __ffs(over) - 1 : 31 - __clz(any);
+    if (l > 0) add(before, Pair{__shfl_sync(0xffffffffu, incl.s, l - 1), __shfl_sync(0xffffffffu, incl.e, l - 1)});
+    return l;
+}
+
+template <int kThreads, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const VerifyArgs a, int cluster) {
+    constexpr int kWarps = kThreads / 32;
+    extern __shared__ uint4 ring[];  // [kAhead][2][kThreads]
+    __shared__ int accepted_sh, again_sh;
+    __shared__ Pair warp_sum[kWarps];
+    __shared__ Pair cta_sum[2];  // of the row's weights, and of p alone
     const int rank = (int)(blockIdx.x % (unsigned)cluster);
     const long long b = blockIdx.x / (unsigned)cluster;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -98,30 +271,23 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, in
     // without the draft's probabilities a refused token alone is out
     int out = refused && !a.draft ? a.drafted[b * a.drafts + r] : -1;
     const long long parts = (long long)cluster * kWarps;
-    const long long part = ((a.vocab + parts - 1) / parts + 31) / 32 * 32;
+    const long long part = ((a.vocab + parts - 1) / parts + kPart - 1) / kPart * kPart;
     const long long v0 = min((long long)a.vocab, (rank * kWarps + warp) * part), v1 = min((long long)a.vocab, v0 + part);
-    double pre = 0., border = 0.;  // the sum before this CTA's part, and u times the whole sum
-    int owner = -1;  // the CTA of the cluster that holds the token
+    int owner = -1;      // warp 0: the CTA of the cluster that holds the token
+    Pair before{0.f, 0.f};  // the sum before its part
+    double border = 0.;  // u times the whole sum
     for (int mode = 0; mode < 2; ++mode) {
         if (mode == 1) {  // nothing is left of the row: the target's probabilities alone
             q = nullptr;
             out = -1;
         }
-        Pair acc{0.f, 0.f};
-        for (long long v = v0 + lane; v < v1; v += 32) {
-            Pair x = entry(load<BF16>(p, v), q ? load<BF16>(q, v) : 0.f, q != nullptr);
-            if (v == out) x = Pair{0.f, 0.f};
-            add(acc, x);
-        }
-        double s = (double)acc.s + (double)acc.e;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) warp_sum[warp] = s;
+        Pair s = lane_sum<kThreads, BF16>(p, q, v0, v1, out, lane, ring + tid);
+        s = scan(s, lane);
+        if (lane == 31) warp_sum[warp] = s;
         __syncthreads();
-        if (tid == 0) {
-            double c = 0.;
-            for (int k = 0; k < kWarps; ++k) c += warp_sum[k];
-            cta_sum[mode] = c;
+        if (warp == 0) {
+            s = scan(lane < kWarps ? warp_sum[lane] : Pair{0.f, 0.f}, lane);
+            if (lane == 31) cta_sum[mode] = s;
         }
         if (cluster > 1) {
             cluster_arrive();
@@ -129,95 +295,95 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, in
         } else {
             __syncthreads();
         }
-        double sums[kMaxCluster];
-        double total = 0.;
-        for (int k = 0; k < cluster; ++k) {
-            sums[k] = cluster > 1 ? cluster_load_f64(cluster_addr(&cta_sum[mode], k)) : cta_sum[mode];
-            total += sums[k];
-        }
-        if (total > 0.) {
-            border = (double)a.sample_rand[b] * total;
-            double c = 0.;
-            for (int k = 0; k < cluster; ++k) {
-                if (sums[k] > 0.) {
-                    owner = k;
-                    pre = c;
-                    if (c + sums[k] > border) break;
-                }
-                c += sums[k];
+        if (warp == 0) {
+            Pair c{0.f, 0.f};
+            if (lane < cluster) {
+                const uint32_t at = cluster_addr(&cta_sum[mode], lane);
+                c = Pair{__uint_as_float(cluster_load_u32(at)), __uint_as_float(cluster_load_u32(at + 4))};
             }
-            break;
+            const Pair all = scan(c, lane);
+            const double total = (double)__shfl_sync(0xffffffffu, all.s, 31) + (double)__shfl_sync(0xffffffffu, all.e, 31);
+            border = (double)a.sample_rand[b] * total;
+            owner = find(c, before, border, lane);
+            if (lane == 0) again_sh = owner < 0;
         }
+        __syncthreads();
+        if (!again_sh) break;
     }
     if (cluster > 1) cluster_arrive();
-    if (owner < 0) {
-        if (rank == 0 && tid == 0) a.tokens[b * (a.drafts + 1) + r] = -1;
-    } else if (owner == rank) {
-        int mine = -1;
-        double c = pre;
-        for (int k = 0; k < kWarps; ++k) {
-            if (warp_sum[k] > 0.) {
-                mine = k;
-                pre = c;
-                if (c + warp_sum[k] > border) break;
-            }
-            c += warp_sum[k];
-        }
-        if (warp == mine) {
-            long long token = -1, last = -1;
-            for (long long i = v0; i < v1; i += 32 * kRun) {
-                double x[kRun], s = 0.;
-                int top = -1;
+    if (warp == 0) {
+        int32_t* token = a.tokens + b * (a.drafts + 1) + r;
+        if (owner < 0) {
+            if (rank == 0 && lane == 0) *token = -1;
+        } else if (owner == rank) {
+            const int w = find(lane < kWarps ? warp_sum[lane] : Pair{0.f, 0.f}, before, border, lane);
+            const long long w0 = min((long long)a.vocab, (rank * kWarps + w) * part), w1 = min((long long)a.vocab, w0 + part);
+            long long last = w0;  // where the run with the token begins
+            bool hit = false;
+            auto weight = [&](long long v) {
+                return v < w1 && v != out ? entry(load<BF16>(p, v), q ? load<BF16>(q, v) : 0.f, q != nullptr) : Pair{0.f, 0.f};
+            };
+#pragma unroll 1
+            for (long long i = w0; i < w1; i += 32 * kRun) {  // kRun consecutive entries per lane
+                Pair s{0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < kRun; ++k) {
-                    const long long v = i + lane * kRun + k;
-                    Pair y{0.f, 0.f};
-                    if (v < v1 && v != out) y = entry(load<BF16>(p, v), q ? load<BF16>(q, v) : 0.f, q != nullptr);
-                    x[k] = (double)y.s + (double)y.e;
-                    if (y.s > 0.f) top = k;
-                    s += x[k];
-                }
-                double incl = s;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += y;
-                }
-                const uint32_t over = __ballot_sync(0xffffffffu, s > 0. && pre + incl > border);
-                const uint32_t some = __ballot_sync(0xffffffffu, top >= 0);
-                if (some) {
-                    const int l = 31 - __clz(some);
-                    last = i + l * kRun + __shfl_sync(0xffffffffu, top, l);
-                }
+                for (int k = 0; k < kRun; ++k) add(s, weight(i + lane * kRun + k));
+                const Pair incl = scan(s, lane);
+                Pair upto = before;
+                add(upto, incl);
+                const uint32_t some = __ballot_sync(0xffffffffu, s.s > 0.f);
+                const uint32_t over = __ballot_sync(0xffffffffu, s.s > 0.f && value(upto) > border);
+                if (some) last = i + (31 - __clz(some)) * kRun;
                 if (over) {
                     const int l = __ffs(over) - 1;
-                    double upto = pre + (incl - s);
-                    int at = -1;
-#pragma unroll
-                    for (int k = 0; k < kRun; ++k) {
-                        upto += x[k];
-                        if (at < 0 && x[k] > 0. && upto > border) at = k;
-                    }
-                    if (at < 0) at = top;  // the lane's sum was rounded up past the border
-                    token = i + l * kRun + __shfl_sync(0xffffffffu, at, l);
+                    if (l > 0) add(before, Pair{__shfl_sync(0xffffffffu, incl.s, l - 1), __shfl_sync(0xffffffffu, incl.e, l - 1)});
+                    last = i + l * kRun;
+                    hit = true;
                     break;
                 }
-                pre += __shfl_sync(0xffffffffu, incl, 31);
+                add(before, Pair{__shfl_sync(0xffffffffu, incl.s, 31), __shfl_sync(0xffffffffu, incl.e, 31)});
             }
-            if (lane == 0) a.tokens[b * (a.drafts + 1) + r] = (int32_t)(token >= 0 ? token : last);
+            // should rounding leave no run over the border, it is the last entry with a weight
+            if (!hit) border = INFINITY;
+            last += find(lane < kRun ? weight(last + lane) : Pair{0.f, 0.f}, before, border, lane);
+            if (lane == 0) *token = (int32_t)last;
         }
     }
     if (cluster > 1) cluster_wait();  // the others read this CTA's sums
 }
 
+template <int kThreads, bool BF16>
+cudaError_t launch(const VerifyArgs& a, int cluster, cudaStream_t s) {
+    static std::atomic<unsigned long long> done{0};
+    constexpr size_t kSmem = sizeof(uint4) * kAhead * 2 * kThreads;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&verify_kernel<kThreads, BF16>), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
+            return e;
+        }
+        done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    return launch_pdl_cluster(verify_kernel<kThreads, BF16>, dim3((unsigned)((long long)a.batch * cluster)), dim3(kThreads), kSmem, cluster, s, a, cluster);
+}
+
 }  // namespace
 
+// CTAs per request: more of them until there are eight per SM. CTAs of 512 threads while a
+// request's eight leave an SM two or fewer, of 256 from there on, of which an SM takes four.
+// us for 131072 entries with the draft's, 512 / 256 threads: 1 request 10.8 / 14.7, 32
+// 15.4 / 18.8, 256 64 / 60; 128 requests of 100003 entries 43 / 34; 4 in place of 8 CTAs for
+// 256 requests of 256 threads 64.
 cudaError_t launch_verify(const VerifyArgs& a, bool bf16, cudaStream_t s) {
+    const long long sms = tile_default_ctas();
     int cluster = 1;
-    while (cluster < kMaxCluster && (long long)a.batch * cluster < tile_default_ctas() && a.vocab > 4096LL * cluster) cluster *= 2;
-    const dim3 grid((unsigned)((long long)a.batch * cluster));
-    return bf16 ? launch_pdl_cluster(verify_kernel<true>, grid, dim3(kThreads), 0, cluster, s, a, cluster)
-                : launch_pdl_cluster(verify_kernel<false>, grid, dim3(kThreads), 0, cluster, s, a, cluster);
+    while (cluster < kMaxCluster && a.batch * cluster < 8 * sms && a.vocab > 4096LL * cluster) cluster *= 2;
+    if (a.batch * kMaxCluster <= 2 * sms) return bf16 ? launch<512, true>(a, cluster, s) : launch<512, false>(a, cluster, s);
+    return bf16 ? launch<256, true>(a, cluster, s) : launch<256, false>(a, cluster, s);
 }
 
 }  // namespace hpc
