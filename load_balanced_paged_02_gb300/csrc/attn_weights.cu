@@ -9,13 +9,17 @@
 // heads is a chain of additions in that thread, without a shuffle or an atomic. K goes from
 // the page into shared memory by TMA and into the product as it is, e4m3 codes too (the
 // query is split into two e4m3 numbers, whose products add up in the accumulator; the key's
-// scale multiplies the score). One CTA per SM, 12 warps
-// (three per sub-partition, so that a thread can have 168 registers):
-//   * warp 0, producer: tiles of 128 tokens (two pages) into a ring of stages;
-//   * warp 1, issuer: the MMAs of each tile with every query slot, 16 rows (128 columns) a slot;
-//   * warps 2 and 3, stagers: query rows into the slots (4, so that a pass takes up to
-//     64 rows), bf16 as they are or split, with each row's constants;
-//   * warps 4-7 and 8-11, two groups that take the even and the odd tiles: exp2 and sums.
+// scale multiplies the score). One CTA per SM, 20 warps (five per sub-partition, so that a
+// thread can have 96 registers):
+//   * warp 0, producer: the passes (below) to the other warps, and tiles of 128 tokens (two
+//     pages) into a ring of stages;
+//   * warps 1 and 2, issuers that take turns by tiles: MMAs with every query slot, 16
+//     rows (128 columns) a slot. One issuer's waits and commits took 0.39 us a tile, more than
+//     an e4m3 tile's bytes;
+//   * warp 3, stager: query rows into the slots (4, so that a pass takes up to 64 rows) by
+//     TMA, e4m3 splits, each row's constants;
+//   * warps 4-19, four groups that take turns too: exp2 and sums. A group has 128
+//     accumulator columns: one slot's, or two of 8 rows in turn.
 // More than 64 rows are several passes over the CTA's tiles, the last rows (which see most)
 // first; a token's thread is the same in each, so it adds to what it wrote itself.
 //
@@ -44,9 +48,12 @@ constexpr int kCols = kSlotRows * kGroup;     // accumulator columns of a slot
 constexpr int kSlots = 4;
 constexpr int kPassRows = kSlots * kSlotRows;
 constexpr int kSlotBytes = 32768;             // bf16 [2 dim halves][128][128 B], or e4m3 [hi, lo][128][128 B]
-constexpr int kThreads = 384;
-constexpr int kStagers = 64;
-constexpr uint32_t kTmemCols = 512;           // two accumulators of 128 columns per group
+constexpr int kThreads = 640;
+constexpr int kGroups = 4;
+constexpr int kNarrow = 8;                    // rows of a pass whose accumulators take turns
+constexpr uint32_t kTmemCols = 512;           // 128 per group
+constexpr int kPasses = 4;                    // passes that the other warps may be behind the producer
+constexpr int kPassInts = 12;
 constexpr int kTileCost = 24;                 // query rows
 constexpr int kSeqCost = 8;                   // a sequence's start in a CTA, in rows
 constexpr int kMostRows = 65536;              // rows counted in a tile's cost at most (sums stay in 64 bits)
@@ -61,8 +68,9 @@ struct Layout {
     static constexpr size_t kQc = kNl + kSlots * kCols * 4;                   // e4m3: float [slot][128]: score factors
     static constexpr size_t kScan = kQc + (FP8 ? kSlots * kCols * 4 : 0);     // int64 [warps]
     static constexpr size_t kRun = kScan + kThreads / 32 * 8;                 // int [8]
-    static constexpr size_t kBars = kRun + 32;
-    static constexpr int kNumBars = 2 * kStages + 2 * kSlots + 8;
+    static constexpr size_t kPass = kRun + 32;                                // Pass [kPasses]
+    static constexpr size_t kBars = kPass + kPasses * kPassInts * 4;
+    static constexpr int kNumBars = 3 * kStages + 3 * kSlots + 4 * kGroups + 2 * kPasses;
     static constexpr size_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr size_t kFlag = kTmemSlot + 4;
     static constexpr size_t kTotal = kFlag + 4;
@@ -147,12 +155,15 @@ __device__ __forceinline__ int tile_at(const Seq& s, long long u) {
 
 // One pass of a CTA over its tiles of a sequence and KV head: rows [lo, hi) of it, tiles
 // [j0, j1), of which the rows see those before jl.
-struct Pass {
-    int h, b, q0, lo, hi, p0, L;
+struct alignas(16) Pass {
+    int h, b, q0, lo, hi, p0, L;  // h < 0: the run is over
     int j0, jl, j1;
     int first;  // the pass that takes over or clears what was there
+    int shift;  // tile j is the turn of issuer (j + shift) % 2 and group (j + shift) % 4
     __device__ __forceinline__ int slots() const { return (hi - lo + kSlotRows - 1) / kSlotRows; }
 };
+
+static_assert(sizeof(Pass) == kPassInts * 4, "pass ring");
 
 struct PassWalk {
     int h, b, j;      // next sequence and its first tile
@@ -208,9 +219,18 @@ struct PassWalk {
         x.j0 = ja;
         x.jl = jl;
         x.j1 = x.first ? jb : jl;
+        x.shift = (hs + bs) & (kGroups - 1);  // the first tiles of short sequences fall to all of them
         return true;
     }
 };
+
+__device__ __forceinline__ void tma_load_3d_nohint(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
 
 // Every lane's wait has to succeed: a warp goes on, or gives up, as one.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -325,20 +345,75 @@ __device__ __forceinline__ void slot_rows(uint32_t ta, int rows, int sees, const
     }
 }
 
+// A row of bf16 queries in shared memory, as TMA left it ([2 dim halves][128 rows][128 B], swizzled),
+// into hi and lo e4m3 codes in its place, by two lanes; returns its scale. `in`: there is such a row.
+__device__ __forceinline__ float split_row(uint8_t* slot, int r, int hh, bool in) {
+    uint4 raw[8];
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        raw[c] = in ? *reinterpret_cast<const uint4*>(slot + hh * 16384 + r * 128 + ((c ^ (r & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    __syncwarp();  // the partner lane has read its half row
+    // the smallest power of two 2^ex with amax / 2^ex <= 448: q / 2^ex is exact
+    float up = 1.f, down = 1.f;
+    if (amax > 0.f && amax <= 3.0e38f) {
+        int e;
+        const float m = frexpf(amax * (1.f / 448.f), &e);
+        const int ex = m == 0.5f ? e - 1 : e;
+        up = ldexpf(1.f, ex);
+        down = ldexpf(1.f, -ex);
+    }
+#pragma unroll
+    for (int c2 = 0; c2 < 4; ++c2) {
+        uint2 hp[2], lp[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint4 x4 = raw[2 * c2 + u];
+            const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[2 * j] = __uint_as_float(w[j] << 16) * down;
+                y[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * down;
+            }
+            split_e4m3x8(y, hp[u], lp[u]);
+        }
+        if (in) {
+            const int off = r * 128 + (((4 * hh + c2) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(slot + off) = make_uint4(hp[0].x, hp[0].y, hp[1].x, hp[1].y);
+            *reinterpret_cast<uint4*>(slot + 16384 + off) = make_uint4(lp[0].x, lp[0].y, lp[1].x, lp[1].y);
+        }
+    }
+    __syncwarp();
+    return up;
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const WeightParams p) {
+    attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q1,
+                        const __grid_constant__ CUtensorMap tm_q4, const WeightParams p) {
     using LY = Layout<FP8>;
     constexpr int NS = LY::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
+    // one per issuer and stage, as an issuer sees the stages that its tiles are in alone
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + LY::kBars);
-    uint64_t* empty = full + NS;
+    uint64_t* empty = full + 2 * NS;
     uint64_t* qfull = empty + NS;
     uint64_t* qfree = qfull + kSlots;
-    uint64_t* accfull = qfree + kSlots;  // accumulator 2 g + (turn of group g) % 2
-    uint64_t* accfree = accfull + 4;
+    uint64_t* qraw = qfree + kSlots;          // e4m3: the copies of a slot's rows
+    uint64_t* accfull = qraw + kSlots;        // accumulator 2 g + i: columns 128 g + 64 i of group g
+    uint64_t* accfree = accfull + 2 * kGroups;
+    uint64_t* passfull = accfree + 2 * kGroups;
+    uint64_t* passfree = passfull + kPasses;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + LY::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kFlag);
+    Pass* passes = reinterpret_cast<Pass*>(smem + LY::kPass);
     int* run = reinterpret_cast<int*>(smem + LY::kRun);
     float* nl = reinterpret_cast<float*>(smem + LY::kNl);
     float* qc = reinterpret_cast<float*>(smem + LY::kQc);
@@ -347,15 +422,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 1);
+            mbar_init(&full[NS + i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&qfull[i], kStagers);
-            mbar_init(&qfree[i], 1 + 8);  // the MMAs; both groups' warps
+            mbar_init(&qfull[i], FP8 ? 1 : 2);          // the split; or the copies and the constants
+            mbar_init(&qfree[i], 2 + 4 * kGroups);      // both issuers' MMAs; the groups' warps
+            mbar_init(&qraw[i], 1);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2 * kGroups; ++i) {
             mbar_init(&accfull[i], 1);
             mbar_init(&accfree[i], 4);
+        }
+        for (int i = 0; i < kPasses; ++i) {
+            mbar_init(&passfull[i], 1);
+            mbar_init(&passfree[i], 3 + 4 * kGroups);   // issuers, stager and the groups' warps
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -430,201 +511,315 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    PassWalk walk;
-    walk.start(run);
-    Pass x;
     bool ok = true;
+    // Pass number k as the producer told it.
+    auto pass_ready = [&](uint32_t k) { return warp_wait(&passfull[k % kPasses], (k / kPasses) & 1, abort_flag); };
+    auto pass_done = [&](uint32_t k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&passfree[k % kPasses]);
+    };
 
     if (warp == 0) {
-        // ============================ producer: the tiles that counted rows see
+        // ============================ producer: passes, and the tiles that counted rows see
         const uint64_t pol = l2_evict_first_policy();
-        uint32_t seq = 0;
-        auto pages = [&](const Pass& y, int j) {  // the lanes' page ids of tiles j, j + 1, ...
+        PassWalk walk;
+        walk.start(run);
+        Pass x, y;
+        uint32_t seq = 0, k = 0;
+        uint32_t uses[2] = {0, 0};  // bit st: of barrier st of an issuer, odd or even
+        auto publish = [&](uint32_t n, bool have, Pass& z) {
+            if (!have) z.h = -1;
+            if (n >= (uint32_t)kPasses && !warp_wait(&passfree[n % kPasses], ((n / kPasses) - 1) & 1, abort_flag)) return false;
+            if (lane == 0) {
+                passes[n % kPasses] = z;
+                mbar_arrive(&passfull[n % kPasses]);
+            }
+            return true;
+        };
+        auto pages = [&](const Pass& z, int j) {  // the lanes' page ids of tiles j, j + 1, ...
             const int c = 2 * j + lane;
-            return c < 2 * y.jl && (long long)c * kChunk < y.L ? p.page_table[y.b * p.pt_stride + c] : -1;
+            return c < 2 * z.jl && (long long)c * kChunk < z.L ? p.page_table[z.b * p.pt_stride + c] : -1;
         };
         bool have = walk.next(p, x);
+        ok = publish(0, have, x);
         int pg = have ? pages(x, x.j0) : -1;
         while (have && ok) {
-            Pass y;  // the pass after, whose first pages are on their way meanwhile
-            const bool have2 = walk.next(p, y);
-            const int pg2 = have2 ? pages(y, y.j0) : -1;
+            // the pass after, whose first pages are on their way meanwhile
+            have = walk.next(p, y);
+            ok = publish(++k, have, y);
+            const int pg2 = have ? pages(y, y.j0) : -1;
             for (int j = x.j0; j < x.jl && ok; j += 16) {
                 if (j != x.j0) pg = pages(x, j);
                 const int nt = min(16, x.jl - j);
-                for (int k = 0; k < nt; ++k, ++seq) {
+                for (int i = 0; i < nt; ++i, ++seq) {
                     int page[2], there = 0;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        page[u] = __shfl_sync(0xffffffffu, pg, 2 * k + u);
+                        page[u] = __shfl_sync(0xffffffffu, pg, 2 * i + u);
                         if ((unsigned)page[u] < (unsigned)p.num_pages)
                             there |= 1 << u;
-                        else if (lane == 0 && p.err && (long long)(2 * (j + k) + u) * kChunk < x.L)
+                        else if (lane == 0 && p.err && (long long)(2 * (j + i) + u) * kChunk < x.L)
                             atomicOr(p.err, (int)HPC_DEVERR_PAGE_OUT_OF_RANGE);
                     }
                     const uint32_t st = seq % NS;
+                    ok = warp_wait(&empty[st], ((seq / NS) & 1) ^ 1, abort_flag);
+                    if (!ok) break;
+                    uint64_t* bar = full + ((j + i + x.shift) & 1) * NS + st;
                     if (lane == 0) {
-                        ok = wait_bounded(&empty[st], ((seq / NS) & 1) ^ 1, abort_flag, kWaitLimitNs);
-                        if (ok) {
-                            if (there == 0) {
-                                mbar_arrive(&full[st]);
-                            } else {
-                                constexpr uint32_t kPageBytes = FP8 ? 8192 : 16384;
-                                mbar_arrive_expect_tx(&full[st], (there == 3 ? 2 : 1) * kPageBytes);
+                        if (there == 0) {
+                            mbar_arrive(bar);
+                        } else {
+                            constexpr uint32_t kPageBytes = FP8 ? 8192 : 16384;
+                            mbar_arrive_expect_tx(bar, (there == 3 ? 2 : 1) * kPageBytes);
 #pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    if (!(there >> u & 1)) continue;
-                                    uint8_t* dst = smem + st * LY::kStageBytes + u * 8192;
-                                    tma_load_3d(dst, &tm_k, &full[st], 0, x.h, page[u] * kChunk, pol);
-                                    if constexpr (!FP8)
-                                        tma_load_3d(dst + 16384, &tm_k, &full[st], 64, x.h, page[u] * kChunk, pol);
-                                }
+                            for (int u = 0; u < 2; ++u) {
+                                if (!(there >> u & 1)) continue;
+                                uint8_t* dst = smem + st * LY::kStageBytes + u * 8192;
+                                tma_load_3d(dst, &tm_k, bar, 0, x.h, page[u] * kChunk, pol);
+                                if constexpr (!FP8) tma_load_3d(dst + 16384, &tm_k, bar, 64, x.h, page[u] * kChunk, pol);
                             }
                         }
                     }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) break;
+                    uses[0] ^= ((j + i + x.shift) & 1) == 0 ? 1u << st : 0u;
+                    uses[1] ^= ((j + i + x.shift) & 1) == 1 ? 1u << st : 0u;
+                    __syncwarp();
                 }
             }
             x = y;
             pg = pg2;
-            have = have2;
         }
-        // copies in flight land before the CTA can end
+        // copies in flight land before the CTA can end: each barrier's last use
         if (lane == 0)
-            for (uint32_t k = seq > (uint32_t)NS ? seq - NS : 0u; k < seq; ++k)
-                wait_bounded(&full[k % NS], (k / NS) & 1, nullptr, kDrainLimitNs);
-    } else if (warp == 1) {
-        // ============================ MMA issuer (one lane; the warp goes along)
+            for (int i = 0; i < 2 * NS; ++i)
+                wait_bounded(&full[i], (uses[i / NS] >> (i % NS) & 1) ^ 1, nullptr, kDrainLimitNs);
+    } else if (warp <= 2) {
+        // ============================ issuers: warp 1 the even, warp 2 the odd turns (one lane issues;
+        // the warp goes along)
         const uint32_t el = elect_lane();
+        const int odd = warp - 1;
         constexpr uint32_t kId = FP8 ? idesc_e4m3(kTile, 0) : idesc_16bit(false, kTile, 0, 0);
         // descriptors of the first stage and slot; the others lie at fixed distances (in
         // 16-byte units, the low bits of a descriptor)
         const uint64_t dk = sdesc_sw128(smem_u32(smem), 16, 1024), dq = sdesc_sw128(smem_u32(smem + LY::kQ), 16, 1024);
-        uint32_t seq = 0, qseq = 0, turn0 = 0, turn1 = 0;
-        while (ok && walk.next(p, x)) {
-            const int ns = x.slots();
-            for (int j = x.j0; j < x.jl && ok; ++j, ++seq) {
-                const uint32_t st = seq % NS, g = j & 1;
-                ok = warp_wait(&full[st], (seq / NS) & 1, abort_flag);
-                const uint64_t k = dk + st * (LY::kStageBytes >> 4);
+        // uses of both accumulators of this issuer's two groups, whether a group's last one was
+        // wide; bit st: uses of stage st by this issuer, odd or even
+        uint32_t seq = 0, qseq = 0, uses = 0, use0[2] = {0, 0}, use1[2] = {0, 0};
+        bool was_wide[2] = {false, false};
+        for (uint32_t k = 0; ok; ++k) {
+            ok = pass_ready(k);
+            if (!ok) break;
+            const Pass& z = passes[k % kPasses];
+            const int j0 = z.j0, jl = z.jl, rows_all = z.hi - z.lo, shift = z.shift;
+            if (z.h < 0) break;
+            pass_done(k);
+            if (jl <= j0) continue;
+            const int ns = (rows_all + kSlotRows - 1) / kSlotRows;
+            const bool wide = rows_all > kNarrow;
+            int j = j0 + ((j0 + shift + odd) & 1);
+            seq += j - j0;
+            if (j >= jl) {  // none of the tiles is this issuer's
+                for (int s = 0; s < ns && ok; ++s) {
+                    ok = warp_wait(&qfull[(qseq + s) % kSlots], ((qseq + s) / kSlots) & 1, abort_flag);
+                    if (ok && lane == 0) mbar_arrive(&qfree[(qseq + s) % kSlots]);
+                }
+                seq -= j - jl;
+                qseq += ns;
+                continue;
+            }
+            bool fresh = true;
+            for (; j < jl && ok; j += 2, seq += 2) {
+                const uint32_t st = seq % NS, g = (j + shift) & 3, gi = g >> 1;
+                ok = warp_wait(&full[odd * NS + st], uses >> st & 1, abort_flag);
+                uses ^= 1u << st;
+                const uint64_t dks = dk + st * (LY::kStageBytes >> 4);
                 for (int s = 0; s < ns && ok; ++s) {
                     const uint32_t sl = (qseq + s) % kSlots;
-                    if (j == x.j0) ok = warp_wait(&qfull[sl], ((qseq + s) / kSlots) & 1, abort_flag);
-                    const uint32_t c = g ? turn1++ : turn0++;
-                    const uint32_t acc = 2 * g + (c & 1);
-                    if (ok) ok = warp_wait(&accfree[acc], ((c >> 1) & 1) ^ 1, abort_flag);
+                    if (fresh) ok = warp_wait(&qfull[sl], ((qseq + s) / kSlots) & 1, abort_flag);
                     if (!ok) break;
+                    // wide: all the group's columns, as accumulator 0, once both are free; else the
+                    // two in turn, accumulator 1 after a wide one once that is free
+                    const uint32_t u0 = gi ? use0[1] : use0[0], u1 = gi ? use1[1] : use1[0];
+                    const bool second = !wide && u0 != u1 && !(gi ? was_wide[1] : was_wide[0]);
+                    const bool check0 = !second, check1 = wide || second || (gi ? was_wide[1] : was_wide[0]);
+                    if (check0) ok = warp_wait(&accfree[2 * g], (u0 & 1) ^ 1, abort_flag);
+                    if (ok && check1) ok = warp_wait(&accfree[2 * g + 1], (u1 & 1) ^ 1, abort_flag);
+                    if (!ok) break;
+                    if (gi) {
+                        second ? ++use1[1] : ++use0[1];
+                        was_wide[1] = wide;
+                    } else {
+                        second ? ++use1[0] : ++use0[0];
+                        was_wide[0] = wide;
+                    }
                     tc_fence_after();
-                    const int rows = min(kSlotRows, x.hi - x.lo - s * kSlotRows);
+                    const int rows = min(kSlotRows, rows_all - s * kSlotRows);
                     const uint32_t id = kId | (uint32_t)((rows + 1) / 2) << 18;  // columns: a multiple of 16
                     const uint64_t q = dq + sl * (kSlotBytes >> 4);
-                    const uint32_t d = tmem + acc * kCols;
+                    const uint32_t d = tmem + g * kCols + (second ? 64u : 0u);
                     if constexpr (FP8) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            umma_e4m3_el(el, d, k + kk * 2, q + kk * 2, id, kk > 0);
-                            umma_e4m3_el(el, d, k + kk * 2, q + 1024 + kk * 2, id, 1);
+                            umma_e4m3_el(el, d, dks + kk * 2, q + kk * 2, id, kk > 0);
+                            umma_e4m3_el(el, d, dks + kk * 2, q + 1024 + kk * 2, id, 1);
                         }
                     } else {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {
                             const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-                            umma_f16_el(el, d, k + off, q + off, id, kk > 0);
+                            umma_f16_el(el, d, dks + off, q + off, id, kk > 0);
                         }
                     }
-                    umma_commit_el(el, &accfull[acc]);
-                    if (j + 1 == x.jl) umma_commit_el(el, &qfree[sl]);
+                    umma_commit_el(el, &accfull[2 * g + second]);
+                    if (j + 2 >= jl) umma_commit_el(el, &qfree[sl]);
                 }
                 if (ok) umma_commit_el(el, &empty[st]);
+                fresh = false;
             }
-            if (x.jl > x.j0) qseq += ns;
+            seq -= j - jl;
+            qseq += ns;
         }
-    } else if (warp >= 4) {
-        // ============================ groups g = 0, 1: tiles j with j % 2 == g; thread = token
+    } else if (warp == 3) {
+        // ============================ stager: query rows into slots
+        uint32_t qseq = 0;
+        for (uint32_t k = 0; ok; ++k) {
+            ok = pass_ready(k);
+            if (!ok) break;
+            const Pass x = passes[k % kPasses];
+            if (x.h < 0) break;
+            pass_done(k);
+            if (x.jl <= x.j0) continue;
+            const int ns = x.slots();
+            for (int s = 0; s < ns && ok; ++s, ++qseq) {
+                const uint32_t sl = qseq % kSlots;
+                ok = warp_wait(&qfree[sl], ((qseq / kSlots) & 1) ^ 1, abort_flag);
+                if (!ok) break;
+                const int r0 = x.lo + s * kSlotRows, rows = min(kSlotRows, x.hi - r0);
+                uint8_t* slot = smem + LY::kQ + sl * kSlotBytes;
+                uint64_t* bar = FP8 ? &qraw[sl] : &qfull[sl];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, (uint32_t)rows * (2 * kGroup * 128));
+                    for (int r = 0; r < rows;) {  // four rows a copy, then one
+                        const int n = rows - r >= 4 ? 4 : 1;
+                        const CUtensorMap* tm = n == 4 ? &tm_q4 : &tm_q1;
+                        uint8_t* dst = slot + r * (kGroup * 128);
+                        tma_load_3d_nohint(dst, tm, bar, 0, x.h * kGroup, x.q0 + r0 + r);
+                        tma_load_3d_nohint(dst + 16384, tm, bar, 64, x.h * kGroup, x.q0 + r0 + r);
+                        r += n;
+                    }
+                }
+                const long long row0 = ((long long)x.q0 + r0) * p.num_q_heads + x.h * kGroup;
+                for (int c = lane; c < rows * kGroup; c += 32) {
+                    const float l = p.lse[row0 + (long long)(c / kGroup) * p.num_q_heads + c % kGroup];
+                    nl[sl * kCols + c] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row of -inf: no weight
+                }
+                if constexpr (FP8) {
+                    ok = warp_wait(bar, (qseq / kSlots) & 1, abort_flag);
+                    if (!ok) break;
+                    for (int c0 = 0; c0 < rows * kGroup; c0 += 16) {
+                        const int c = c0 + (lane >> 1);
+                        const float up = split_row(slot, c, lane & 1, c < rows * kGroup);
+                        if (c < rows * kGroup && (lane & 1) == 0) qc[sl * kCols + c] = up * (kLog2e * 0.08838834764831845f);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&qfull[sl]);
+            }
+        }
+        // copies in flight land before the CTA can end
+        if (lane == 0)
+            for (uint32_t i = qseq > (uint32_t)kSlots ? qseq - kSlots : 0u; i < qseq; ++i)
+                wait_bounded(FP8 ? &qraw[i % kSlots] : &qfull[i % kSlots], (i / kSlots) & 1, nullptr, kDrainLimitNs);
+    } else {
+        // ============================ groups g = 0 .. 3: thread = token of every fourth tile
         const int g = (warp >> 2) - 1, wq = warp & 3;
         constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
-        // What a tile needs from memory comes a tile ahead, its page id two tiles: across
+        // What a tile needs from memory comes a tile of the group ahead, its page id two: across
         // passes too, unless a pass goes on from the sums of the one before.
-        struct Token {
-            float old, factor;
-            bool there;
-        };
-        auto first_tile = [&](const Pass& y) { return y.j0 + ((y.j0 & 1) ^ g); };
+        float old = 0.f, factor = 0.f;
+        bool there = false;
+        int page = -1;  // of the tile after the one ahead
+        auto first_tile = [&](const Pass& y) { return y.j0 + ((g - y.shift - y.j0) & (kGroups - 1)); };
         auto page_of = [&](const Pass& y, int j) {
             const int c = 2 * j + (wq >> 1);
             return j < y.j1 && (long long)c * kChunk < y.L ? p.page_table[y.b * p.pt_stride + c] : -1;
         };
-        auto fetch = [&](const Pass& y, int j, int page) {
-            Token k{0.f, kScale, (unsigned)page < (unsigned)p.num_pages};
+        auto fetch = [&](const Pass& y, int j, int pg) {
+            old = 0.f;
+            factor = kScale;
+            there = (unsigned)pg < (unsigned)p.num_pages;
             const int t = j * kTile + 32 * wq + lane;
             if (j < y.j1 && t < (y.first ? y.p0 : y.L) && !(y.first && p.decay == 0.f))
-                k.old = p.weights[((long long)y.b * p.num_kv_heads + y.h) * p.w_stride + t];
-            if (FP8 && k.there) k.factor = p.k_scale[((long long)page * p.num_kv_heads + y.h) * kChunk + (t & (kChunk - 1))];
-            return k;
+                old = p.weights[((long long)y.b * p.num_kv_heads + y.h) * p.w_stride + t];
+            if (FP8 && there) factor = p.k_scale[((long long)pg * p.num_kv_heads + y.h) * kChunk + (t & (kChunk - 1))];
         };
-        uint32_t qseq = 0, turn = 0;
-        bool have = walk.next(p, x);
-        Token ahead{0.f, 0.f, false};
-        int page = -1;  // of the tile after the one ahead
-        if (have) {
-            ahead = fetch(x, first_tile(x), page_of(x, first_tile(x)));
-            page = page_of(x, first_tile(x) + 2);
+        uint32_t qseq = 0, use0 = 0, use1 = 0;
+        bool was_wide = false;
+        ok = pass_ready(0);
+        if (ok && passes[0].h >= 0) {
+            const Pass& y = passes[0];
+            fetch(y, first_tile(y), page_of(y, first_tile(y)));
+            page = page_of(y, first_tile(y) + kGroups);
         }
-        while (have && ok) {
-            Pass y;
-            have = walk.next(p, y);
-            const int jy = have ? first_tile(y) : 0;
-            const int page_y = have ? page_of(y, jy) : -1;
+        for (uint32_t k = 0; ok; ++k) {
+            const Pass x = passes[k % kPasses];
+            if (x.h < 0) break;
+            ok = pass_ready(k + 1);
+            if (!ok) break;
+            const Pass& y = passes[(k + 1) % kPasses];  // stays until this warp is done with it
+            const bool have = y.h >= 0;
+            const int page_y = have ? page_of(y, first_tile(y)) : -1;
             const int ns = x.slots();
+            const bool wide = x.hi - x.lo > kNarrow;
             float* wrow = p.weights + ((long long)x.b * p.num_kv_heads + x.h) * p.w_stride;
-            bool any = false;      // this group has seen the pass's slots
-            bool fetched = false;  // ahead is of the next pass
-            for (int j = first_tile(x); j < x.j1; j += 2) {
+            bool any = false;      // this warp has seen the pass's slots
+            bool fetched = false;  // what is ahead is of the next pass
+            for (int j = first_tile(x); j < x.j1; j += kGroups) {
                 const int t = j * kTile + 32 * wq + lane;
-                const Token now = ahead;
-                if (j + 2 < x.j1) {
-                    ahead = fetch(x, j + 2, page);
-                    page = page_of(x, j + 4);
+                const float now_old = x.first ? p.decay * old : old;
+                const uint64_t now_factor = pair(factor, factor);
+                const bool now_there = there;
+                if (j + kGroups < x.j1) {
+                    fetch(x, j + kGroups, page);
+                    page = page_of(x, j + 2 * kGroups);
                 } else if (have && y.first) {
-                    ahead = fetch(y, jy, page_y);
-                    page = page_of(y, jy + 2);
+                    fetch(y, first_tile(y), page_y);
+                    page = page_of(y, first_tile(y) + kGroups);
                     fetched = true;
                 }
                 float sum = 0.f;
                 if (j < x.jl) {
                     uint64_t sum2 = 0;
-                    const uint64_t factor = pair(now.factor, now.factor);
                     for (int s = 0; s < ns; ++s) {
                         const uint32_t sl = (qseq + s) % kSlots;
                         if (!any) ok = warp_wait(&qfull[sl], ((qseq + s) / kSlots) & 1, abort_flag);
-                        const uint32_t acc = 2 * g + (turn & 1);
-                        if (ok) ok = warp_wait(&accfull[acc], (turn >> 1) & 1, abort_flag);
+                        // as the issuer chose
+                        const bool second = !wide && use0 != use1 && !was_wide;
+                        if (ok) ok = warp_wait(&accfull[2 * g + second], (second ? use1 : use0) & 1, abort_flag);
                         if (!ok) break;
-                        ++turn;
+                        second ? ++use1 : ++use0;
+                        was_wide = wide;
                         tc_fence_after();
                         const int r0 = x.lo + s * kSlotRows, rows = min(kSlotRows, x.hi - r0);
-                        const uint32_t ta = tmem + ((uint32_t)(32 * wq) << 16) + acc * kCols;
-                        const float* nls = nl + sl * kCols;
-                        const float* qcs = qc + sl * kCols;
+                        const uint32_t ta = tmem + ((uint32_t)(32 * wq) << 16) + g * kCols + (second ? 64u : 0u);
                         // rows of the slot from t - p0 - r0 on see token t: all of them before the last tiles
                         if (j * kTile + kTile - 1 <= (long long)x.p0 + r0)
-                            slot_rows<FP8, false>(ta, rows, 0, nls, qcs, factor, sum2);
+                            slot_rows<FP8, false>(ta, rows, 0, nl + sl * kCols, qc + sl * kCols, now_factor, sum2);
                         else
-                            slot_rows<FP8, true>(ta, rows, t - x.p0 - r0, nls, qcs, factor, sum2);
+                            slot_rows<FP8, true>(ta, rows, t - x.p0 - r0, nl + sl * kCols, qc + sl * kCols, now_factor, sum2);
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&accfree[acc]);
+                        if (lane == 0) mbar_arrive(&accfree[2 * g + second]);
                     }
                     if (!ok) break;
                     any = true;
                     const float2 v = unpair(sum2);
-                    if (now.there) sum = v.x + v.y;
+                    if (now_there) sum = v.x + v.y;
                 }
-                if (t < x.L) wrow[t] = (x.first ? p.decay * now.old : now.old) + sum;
+                if (t < x.L) wrow[t] = now_old + sum;
             }
             if (x.jl > x.j0) {
-                // the slots are this pass's until both groups have seen them
+                // the slots are this pass's until every warp has seen them
                 for (int s = 0; s < ns && ok; ++s) {
                     const uint32_t sl = (qseq + s) % kSlots;
                     if (!any) ok = warp_wait(&qfull[sl], ((qseq + s) / kSlots) & 1, abort_flag);
@@ -634,101 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 qseq += ns;
             }
             if (have && !fetched) {
-                ahead = fetch(y, jy, page_y);
-                page = page_of(y, jy + 2);
+                fetch(y, first_tile(y), page_y);
+                page = page_of(y, first_tile(y) + kGroups);
             }
-            x = y;
-        }
-    } else {
-        // ============================ stagers: query rows into slots
-        const int sid = (warp - 2) * 32 + lane;
-        uint32_t qseq = 0;
-        while (ok && walk.next(p, x)) {
-            if (x.jl <= x.j0) continue;
-            const int ns = x.slots();
-            for (int s = 0; s < ns && ok; ++s, ++qseq) {
-                const uint32_t sl = qseq % kSlots;
-                ok = warp_wait(&qfree[sl], ((qseq / kSlots) & 1) ^ 1, abort_flag);
-                if (!ok) break;
-                const int r0 = x.lo + s * kSlotRows, rows = min(kSlotRows, x.hi - r0);
-                uint8_t* slot = smem + LY::kQ + sl * kSlotBytes;
-                const long long row0 = ((long long)x.q0 + r0) * p.num_q_heads + x.h * kGroup;
-                for (int c = sid; c < rows * kGroup; c += kStagers) {
-                    const float l = p.lse[row0 + (long long)(c / kGroup) * p.num_q_heads + c % kGroup];
-                    nl[sl * kCols + c] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row of -inf: no weight
-                }
-                if constexpr (!FP8) {
-                    // a head's 16 pieces of 16 bytes by 16 threads, eight rows at once
-                    const int c = sid & 15;
-                    const long long step = (long long)p.num_q_heads * kHeadDim;
-                    for (int i = 0; i < 2 * rows; i += 8) {  // i: 2 row + half of the heads
-                        uint4 v[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int head = (sid >> 4) + 4 * (k & 1), r = (i + k) >> 1;
-                            if (i + k < 2 * rows) v[k] = *reinterpret_cast<const uint4*>(p.q + row0 * kHeadDim + r * step + head * kHeadDim + c * 8);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int head = (sid >> 4) + 4 * (k & 1), r = (i + k) >> 1;
-                            if (i + k < 2 * rows)
-                                *reinterpret_cast<uint4*>(slot + (c >> 3) * 16384 + (r * kGroup + head) * 128 + (((c & 7) ^ head) << 4)) = v[k];
-                        }
-                    }
-                } else {
-                    // two threads per row of 128: half hh of its dims each, split into hi and lo codes
-                    for (int c0 = 0; c0 < rows * kGroup; c0 += kStagers / 2) {
-                        const int c = c0 + (sid >> 1), hh = sid & 1;
-                        const bool in = c < rows * kGroup;
-                        const __nv_bfloat16* src =
-                            p.q + (row0 + (long long)(c / kGroup) * p.num_q_heads + c % kGroup) * kHeadDim + hh * 64;
-                        uint4 raw[8];
-                        float amax = 0.f;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            raw[k] = in ? reinterpret_cast<const uint4*>(src)[k] : make_uint4(0, 0, 0, 0);
-                            const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-                            for (int m = 0; m < 4; ++m)
-                                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[m] << 16)), fabsf(__uint_as_float(w[m] & 0xffff0000u))));
-                        }
-                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                        // the smallest power of two 2^ex with amax / 2^ex <= 448: q / 2^ex is exact
-                        float up = 1.f, down = 1.f;
-                        if (amax > 0.f && amax <= 3.0e38f) {
-                            int e;
-                            const float m = frexpf(amax * (1.f / 448.f), &e);
-                            const int ex = m == 0.5f ? e - 1 : e;
-                            up = ldexpf(1.f, ex);
-                            down = ldexpf(1.f, -ex);
-                        }
-                        if (in && hh == 0) qc[sl * kCols + c] = up * (kLog2e * 0.08838834764831845f);
-#pragma unroll
-                        for (int c2 = 0; c2 < 4; ++c2) {
-                            uint2 hp[2], lp[2];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const uint4 x4 = raw[2 * c2 + u];
-                                const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
-                                float y[8];
-#pragma unroll
-                                for (int m = 0; m < 4; ++m) {
-                                    y[2 * m] = __uint_as_float(w[m] << 16) * down;
-                                    y[2 * m + 1] = __uint_as_float(w[m] & 0xffff0000u) * down;
-                                }
-                                split_e4m3x8(y, hp[u], lp[u]);
-                            }
-                            if (in) {
-                                const int off = c * 128 + (((4 * hh + c2) ^ (c & 7)) << 4);
-                                *reinterpret_cast<uint4*>(slot + off) = make_uint4(hp[0].x, hp[0].y, hp[1].x, hp[1].y);
-                                *reinterpret_cast<uint4*>(slot + 16384 + off) = make_uint4(lp[0].x, lp[0].y, lp[1].x, lp[1].y);
-                            }
-                        }
-                    }
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&qfull[sl]);
-            }
+            pass_done(k);
         }
     }
     if (!ok && lane == 0) {
@@ -750,8 +854,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// 3-D map over the query rows [num_tokens][Hq][128] bf16: box = 64 dims x 8 heads x `rows`,
+// 128-byte swizzle (rows of an MMA operand tile).
+bool make_q_rows_map(CUtensorMap* map, const void* q, int num_tokens, int Hq, int rows) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)Hq, (cuuint64_t)num_tokens};
+    cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)Hq * kHeadDim * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)kGroup, (cuuint32_t)rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 template <bool FP8>
-cudaError_t launch(const CUtensorMap& tm_k, const WeightParams& p, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap (&maps)[3], const WeightParams& p, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -768,15 +887,18 @@ cudaError_t launch(const CUtensorMap& tm_k, const WeightParams& p, cudaStream_t 
     }
     const int ctas = tile_default_ctas();
     if (ctas < 1) return cudaErrorUnknown;
-    return launch_pdl(attn_weights_kernel<FP8>, dim3(ctas), dim3(kThreads), Layout<FP8>::kTotal, s, tm_k, p);
+    return launch_pdl(attn_weights_kernel<FP8>, dim3(ctas), dim3(kThreads), Layout<FP8>::kTotal, s, maps[0], maps[1], maps[2], p);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_weights(const AttnWeightsArgs& a, cudaStream_t s) {
-    CUtensorMap tm_k;
-    memset(&tm_k, 0, sizeof tm_k);
-    if (!make_kv_map(&tm_k, a.k_cache, a.fp8, a.num_pages, a.num_kv_heads)) return cudaErrorInvalidValue;
+    CUtensorMap maps[3];  // K; one and four rows of Q
+    memset(maps, 0, sizeof maps);
+    if (!make_kv_map(&maps[0], a.k_cache, a.fp8, a.num_pages, a.num_kv_heads) ||
+        !make_q_rows_map(&maps[1], a.q, a.num_tokens, a.num_q_heads, 1) ||
+        !make_q_rows_map(&maps[2], a.q, a.num_tokens, a.num_q_heads, 4))
+        return cudaErrorInvalidValue;
     WeightParams p;
     p.q = static_cast<const __nv_bfloat16*>(a.q);
     p.page_table = a.page_table;
@@ -799,7 +921,7 @@ cudaError_t launch_attn_weights(const AttnWeightsArgs& a, cudaStream_t s) {
     const long long most = a.pt_stride * kChunk;
     p.max_len = most > kMaxKeys ? kMaxKeys : (int)most;
     p.decay = a.decay;
-    return a.fp8 ? launch<true>(tm_k, p, s) : launch<false>(tm_k, p, s);
+    return a.fp8 ? launch<true>(maps, p, s) : launch<false>(maps, p, s);
 }
 
 }  // namespace hpc
