@@ -13,14 +13,15 @@
 // thread can have 96 registers):
 //   * warp 0, producer: the passes (below) to the other warps, and tiles of 128 tokens (two
 //     pages) into a ring of stages;
-//   * warps 1 and 2, issuers that take turns by tiles: MMAs with every query slot, 16
-//     rows (128 columns) a slot. One issuer's waits and commits took 0.39 us a tile, more than
+//   * warps 1 and 2, issuers that take turns by tiles: MMAs with every query slot, 8
+//     rows (64 columns) a slot. One issuer's waits and commits took 0.39 us a tile, more than
 //     an e4m3 tile's bytes;
-//   * warp 3, stager: query rows into the slots (4, so that a pass takes up to 64 rows) by
-//     TMA, e4m3 splits, each row's constants;
-//   * warps 4-19, four groups that take turns too: exp2 and sums. A group has 128
-//     accumulator columns: one slot's, or two of 8 rows in turn.
-// More than 64 rows are several passes over the CTA's tiles, the last rows (which see most)
+//   * warp 3, stager: query rows into the slots (a pass takes up to 32 rows, four of five
+//     slots) by TMA, e4m3 splits, each row's constants;
+//   * warps 4-19, four groups: exp2 and sums, a tile by one of them, or, where a sequence has
+//     more than 8 rows, by two that share its slots. A group has two
+//     accumulators, one filled while the other is read.
+// More than 32 rows are several passes over the CTA's tiles, the last rows (which see most)
 // first; a token's thread is the same in each, so it adds to what it wrote itself.
 //
 // All tiles, walked KV head by KV head and sequence by sequence, are cut into runs of equal
@@ -43,17 +44,18 @@ namespace {
 using namespace attn;
 
 constexpr int kTile = 128;                    // tokens of a tile: two pages
-constexpr int kSlotRows = 16;                 // query rows of a slot
+constexpr int kSlotRows = 8;                  // query rows of a slot
 constexpr int kCols = kSlotRows * kGroup;     // accumulator columns of a slot
-constexpr int kSlots = 4;
-constexpr int kPassRows = kSlots * kSlotRows;
-constexpr int kSlotBytes = 32768;             // bf16 [2 dim halves][128][128 B], or e4m3 [hi, lo][128][128 B]
+constexpr int kSlots = 5;
+constexpr int kPassRows = 32;                 // the fifth slot is filled for the pass after
+constexpr int kSlotBytes = 16384;             // bf16 [2 dim halves][64][128 B], or e4m3 [hi, lo][64][128 B]
+constexpr int kSlotHalf = kSlotBytes / 2;
 constexpr int kThreads = 640;
 constexpr int kGroups = 4;
-constexpr int kNarrow = 8;                    // rows of a pass whose accumulators take turns
-constexpr uint32_t kTmemCols = 512;           // 128 per group
+constexpr uint32_t kTmemCols = 512;           // two accumulators of 64 columns per group
 constexpr int kPasses = 4;                    // passes that the other warps may be behind the producer
 constexpr int kPassInts = 12;
+constexpr int kPoly = 0;                      // of a row's four pairs, those without the special function unit
 constexpr int kTileCost = 24;                 // query rows
 constexpr int kSeqCost = 8;                   // a sequence's start in a CTA, in rows
 constexpr int kMostRows = 65536;              // rows counted in a tile's cost at most (sums stay in 64 bits)
@@ -61,16 +63,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 template <bool FP8>
 struct Layout {
-    static constexpr int kStages = FP8 ? 5 : 3;
+    static constexpr int kStages = FP8 ? 8 : 4;
     static constexpr int kStageBytes = FP8 ? 16384 : 32768;
     static constexpr size_t kQ = (size_t)kStages * kStageBytes;
-    static constexpr size_t kNl = kQ + kSlots * kSlotBytes;                   // float [slot][128]: -lse log2(e)
-    static constexpr size_t kQc = kNl + kSlots * kCols * 4;                   // e4m3: float [slot][128]: score factors
+    static constexpr size_t kNl = kQ + kSlots * kSlotBytes;                   // float [slot][64]: -lse log2(e)
+    static constexpr size_t kQc = kNl + kSlots * kCols * 4;                   // e4m3: float [slot][64]: score factors
     static constexpr size_t kScan = kQc + (FP8 ? kSlots * kCols * 4 : 0);     // int64 [warps]
-    static constexpr size_t kRun = kScan + kThreads / 32 * 8;                 // int [8]
+    static constexpr size_t kBorder = kScan + kThreads / 32 * 8;              // Border [4]
+    static constexpr size_t kRun = kBorder + 64;                              // int [8]
     static constexpr size_t kPass = kRun + 32;                                // Pass [kPasses]
-    static constexpr size_t kBars = kPass + kPasses * kPassInts * 4;
-    static constexpr int kNumBars = 3 * kStages + 3 * kSlots + 4 * kGroups + 2 * kPasses;
+    static constexpr size_t kPart = kPass + kPasses * kPassInts * 4;          // float [2][2][128]: sums of upper groups
+    static constexpr size_t kBars = kPart + 4 * kTile * 4;
+    static constexpr int kNumBars = 3 * kStages + 3 * kSlots + 4 * kGroups + 2 * kPasses + 8;
     static constexpr size_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr size_t kFlag = kTmemSlot + 4;
     static constexpr size_t kTotal = kFlag + 4;
@@ -140,18 +144,30 @@ __device__ __forceinline__ long long units_before(const Seq& s, int j) {
     return u + rows * m1 + (m2 - m1) * a - 64 * (m1 + m2 - 1) * (m2 - m1) + kTileCost * (j - m2);
 }
 
-// The first tile with at least u units before it.
-__device__ __forceinline__ int tile_at(const Seq& s, long long u) {
-    int lo = 0, hi = s.tiles;
+// The first tile with at least u units before it, by a warp: 32 places at a time.
+__device__ __forceinline__ int tile_at(const Seq& s, long long u, int lane) {
+    int lo = 0, hi = s.tiles;  // the answer is in [lo, hi]
     while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (units_before(s, mid) >= u)
-            hi = mid;
-        else
-            lo = mid + 1;
+        const int step = (hi - lo + 31) / 32, at = min(hi, lo + lane * step);
+        const uint32_t enough = __ballot_sync(0xffffffffu, units_before(s, at) >= u);
+        if (enough == 0) {
+            lo = min(hi, lo + 31 * step) + 1;  // behind the last place
+            if (lo > hi) lo = hi;
+        } else {
+            const int k = __ffs(enough) - 1;
+            hi = min(hi, lo + k * step);
+            if (k > 0) lo = min(hi, lo + (k - 1) * step + 1);
+            else lo = hi;
+        }
     }
     return lo;
 }
+
+// Where a CTA's run begins or ends: rem units into the tiles of a KV head and sequence.
+struct Border {
+    long long rem;
+    int h, b;
+};
 
 // One pass of a CTA over its tiles of a sequence and KV head: rows [lo, hi) of it, tiles
 // [j0, j1), of which the rows see those before jl.
@@ -159,7 +175,11 @@ struct alignas(16) Pass {
     int h, b, q0, lo, hi, p0, L;  // h < 0: the run is over
     int j0, jl, j1;
     int first;  // the pass that takes over or clears what was there
-    int shift;  // tile j is the turn of issuer (j + shift) % 2 and group (j + shift) % 4
+    // Tile j is number n = j + shift: issuer n % 2 has it. Of a sequence of up to 8 rows group n %
+    // 4 sums it (shift below 4); of one of more rows groups n % 2 and n % 2 + 2 do, the even
+    // and the odd slots.
+    int shift;
+    __device__ __forceinline__ bool split() const { return shift >= kGroups; }
     __device__ __forceinline__ int slots() const { return (hi - lo + kSlotRows - 1) / kSlotRows; }
 };
 
@@ -219,7 +239,7 @@ struct PassWalk {
         x.j0 = ja;
         x.jl = jl;
         x.j1 = x.first ? jb : jl;
-        x.shift = (hs + bs) & (kGroups - 1);  // the first tiles of short sequences fall to all of them
+        x.shift = ((hs + bs) & (kGroups - 1)) + (s.hi - s.lo > kSlotRows ? kGroups : 0);  // short sequences fall to all groups
         return true;
     }
 };
@@ -283,9 +303,32 @@ __device__ __forceinline__ uint64_t exp2_2(uint64_t x) {
     return pair(fast_exp2(v.x), fast_exp2(v.y));
 }
 
+// The same without the special function unit, which else sets the pace (16 a clock): 2^n
+// p(f) with n the nearest whole number, from the sum with 1.5 2^23, and p the polynomial of
+// degree 6 with p(0) = 1 whose largest relative error on [-1/2, 1/2] is smallest (2.6e-9, by
+// Remez's exchange; with the roundings 2^-23). 0 up to -127, infinite from 128 on.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
+    float2 v = unpair(x);
+    v.x = fminf(fmaxf(v.x, -127.f), 128.f);
+    v.y = fminf(fmaxf(v.y, -127.f), 128.f);
+    x = pair(v.x, v.y);
+    const uint64_t magic = pair(12582912.f, 12582912.f);
+    const uint64_t t = add2(x, magic);
+    const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x);
+    uint64_t r = fma2(pair(0.00015594677f, 0.00015594677f), f, pair(0.0013406644f, 0.0013406644f));
+    r = fma2(r, f, pair(0.009617693f, 0.009617693f));
+    r = fma2(r, f, pair(0.055503104f, 0.055503104f));
+    r = fma2(r, f, pair(0.24022652f, 0.24022652f));
+    r = fma2(r, f, pair(0.6931472f, 0.6931472f));
+    r = fma2(r, f, pair(1.f, 1.f));
+    const float2 n = unpair(t), q = unpair(r);
+    return pair(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(n.x) << 23)),
+                __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
+}
+
 // The weights of one query row's 8 heads for the thread's token, as two sums of four. s: the
 // scores; nl, qc: the row's constants in shared memory; factor: twice the token's.
-template <bool FP8>
+template <bool FP8, int POLY>
 __device__ __forceinline__ uint64_t row_weight(const uint32_t* s, const float* nl, const float* qc, uint64_t factor) {
     uint64_t e[4];
 #pragma unroll
@@ -295,13 +338,15 @@ __device__ __forceinline__ uint64_t row_weight(const uint32_t* s, const float* n
         const uint64_t y = pair(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3]));
         if constexpr (FP8) {
             const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(qc + 4 * k);
-            e[2 * k] = exp2_2(fma2(mul2(x, factor), c.x, l.x));
-            e[2 * k + 1] = exp2_2(fma2(mul2(y, factor), c.y, l.y));
+            e[2 * k] = fma2(mul2(x, factor), c.x, l.x);
+            e[2 * k + 1] = fma2(mul2(y, factor), c.y, l.y);
         } else {
-            e[2 * k] = exp2_2(fma2(x, factor, l.x));
-            e[2 * k + 1] = exp2_2(fma2(y, factor, l.y));
+            e[2 * k] = fma2(x, factor, l.x);
+            e[2 * k + 1] = fma2(y, factor, l.y);
         }
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) e[k] = k < POLY ? exp2_poly2(e[k]) : exp2_2(e[k]);
     return add2(add2(e[0], e[1]), add2(e[2], e[3]));
 }
 
@@ -316,7 +361,7 @@ __device__ __forceinline__ void four_rows(const uint32_t (&s)[32], int r, int ro
         uint64_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            w[k] = row_weight<FP8>(s + 8 * k, nl + k * kGroup, qc + k * kGroup, factor);
+            w[k] = row_weight<FP8, kPoly>(s + 8 * k, nl + k * kGroup, qc + k * kGroup, factor);
             if (MASK && r + k < sees) w[k] = 0;
         }
 #pragma unroll
@@ -325,7 +370,7 @@ __device__ __forceinline__ void four_rows(const uint32_t (&s)[32], int r, int ro
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             if (r + k < rows) {
-                const uint64_t w = row_weight<FP8>(s + 8 * k, nl + k * kGroup, qc + k * kGroup, factor);
+                const uint64_t w = row_weight<FP8, kPoly>(s + 8 * k, nl + k * kGroup, qc + k * kGroup, factor);
                 if (!MASK || r + k >= sees) sum = add2(sum, w);
             }
         }
@@ -336,8 +381,9 @@ __device__ __forceinline__ void four_rows(const uint32_t (&s)[32], int r, int ro
 template <bool FP8, bool MASK>
 __device__ __forceinline__ void slot_rows(uint32_t ta, int rows, int sees, const float* nl, const float* qc, uint64_t factor,
                                           uint64_t& sum) {
-#pragma unroll 1
-    for (int r = 0; r < rows; r += 4) {
+#pragma unroll
+    for (int r = 0; r < kSlotRows; r += 4) {
+        if (r >= rows) break;
         uint32_t v[32];
         tmem_ld_x32(ta + r * kGroup, v);
         tmem_ld_wait();
@@ -345,14 +391,14 @@ __device__ __forceinline__ void slot_rows(uint32_t ta, int rows, int sees, const
     }
 }
 
-// A row of bf16 queries in shared memory, as TMA left it ([2 dim halves][128 rows][128 B], swizzled),
+// A row of bf16 queries in shared memory, as TMA left it ([2 dim halves][64 rows][128 B], swizzled),
 // into hi and lo e4m3 codes in its place, by two lanes; returns its scale. `in`: there is such a row.
 __device__ __forceinline__ float split_row(uint8_t* slot, int r, int hh, bool in) {
     uint4 raw[8];
     float amax = 0.f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-        raw[c] = in ? *reinterpret_cast<const uint4*>(slot + hh * 16384 + r * 128 + ((c ^ (r & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+        raw[c] = in ? *reinterpret_cast<const uint4*>(slot + hh * kSlotHalf + r * 128 + ((c ^ (r & 7)) << 4)) : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -387,7 +433,7 @@ __device__ __forceinline__ float split_row(uint8_t* slot, int r, int hh, bool in
         if (in) {
             const int off = r * 128 + (((4 * hh + c2) ^ (r & 7)) << 4);
             *reinterpret_cast<uint4*>(slot + off) = make_uint4(hp[0].x, hp[0].y, hp[1].x, hp[1].y);
-            *reinterpret_cast<uint4*>(slot + 16384 + off) = make_uint4(lp[0].x, lp[0].y, lp[1].x, lp[1].y);
+            *reinterpret_cast<uint4*>(slot + kSlotHalf + off) = make_uint4(lp[0].x, lp[0].y, lp[1].x, lp[1].y);
         }
     }
     __syncwarp();
@@ -407,14 +453,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* qfull = empty + NS;
     uint64_t* qfree = qfull + kSlots;
     uint64_t* qraw = qfree + kSlots;          // e4m3: the copies of a slot's rows
-    uint64_t* accfull = qraw + kSlots;        // accumulator 2 g + i: columns 128 g + 64 i of group g
+    uint64_t* accfull = qraw + kSlots;        // accumulator 2 g + (turn of group g) % 2
     uint64_t* accfree = accfull + 2 * kGroups;
     uint64_t* passfull = accfree + 2 * kGroups;
     uint64_t* passfree = passfull + kPasses;
+    uint64_t* partfull = passfree + kPasses;  // buffer 2 (issuer) + (meeting) % 2
+    uint64_t* partfree = partfull + 4;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + LY::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + LY::kFlag);
     Pass* passes = reinterpret_cast<Pass*>(smem + LY::kPass);
     int* run = reinterpret_cast<int*>(smem + LY::kRun);
+    float* part = reinterpret_cast<float*>(smem + LY::kPart);
     float* nl = reinterpret_cast<float*>(smem + LY::kNl);
     float* qc = reinterpret_cast<float*>(smem + LY::kQc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -437,6 +486,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kPasses; ++i) {
             mbar_init(&passfull[i], 1);
             mbar_init(&passfree[i], 3 + 4 * kGroups);   // issuers, stager and the groups' warps
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&partfull[i], 4);
+            mbar_init(&partfree[i], 4);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -477,33 +530,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const long long total = per_head * p.num_kv_heads;
         const long long bucket = max((total + gridDim.x - 1) / gridDim.x, (long long)kTileCost);
-#pragma unroll 1
+        // which sequence each border falls into, by the thread that has summed it
+        Border* border = reinterpret_cast<Border*>(smem + LY::kBorder);
+        if (warp < 2) {  // (a division in 64 bits: by one warp for each border)
+            const long long u = (long long)(blockIdx.x + warp) * bucket;
+            const int h = u < total ? (int)(u / per_head) : p.num_kv_heads;
+            if (lane == 0) border[warp] = Border{u < total ? u - h * per_head : 0, h, 0};
+        }
+        __syncthreads();
+#pragma unroll
         for (int end = 0; end < 2; ++end) {
-            const long long u = min(total, (long long)(blockIdx.x + end) * bucket);
-            int* at = run + 3 * end;
-            if (u >= total) {
-                if (tid == 0) {
-                    at[0] = p.num_kv_heads;
-                    at[1] = 0;
-                    at[2] = 0;
-                }
-                continue;
-            }
-            const int h = (int)(u / per_head);
-            const long long rem = u - h * per_head;
-            if (rem >= before && rem < before + sum) {
-                long long c = before;
+            const int h = border[end].h;
+            long long rem = border[end].rem - before;
+            if (h < p.num_kv_heads && rem >= 0 && rem < sum) {
                 for (int b = b0; b < b1; ++b) {
                     const Seq s = seq_of<false>(p, b);
                     const long long all = units_before(s, s.tiles);
-                    if (rem < c + all) {
-                        at[0] = h;
-                        at[1] = b;
-                        at[2] = tile_at(s, rem - c);
+                    if (rem < all) {
+                        border[2 + end] = Border{rem, h, b};
                         break;
                     }
-                    c += all;
+                    rem -= all;
                 }
+            }
+        }
+        __syncthreads();
+        // and which tile, by a warp for each
+        if (warp < 2) {
+            const Border x = border[warp].h < p.num_kv_heads ? border[2 + warp] : border[warp];
+            int j = 0;
+            if (x.rem > 0) j = tile_at(seq_of<false>(p, x.b), x.rem, lane);
+            if (lane == 0) {
+                run[3 * warp] = x.h;
+                run[3 * warp + 1] = x.b;
+                run[3 * warp + 2] = j;
             }
         }
     }
@@ -601,10 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // descriptors of the first stage and slot; the others lie at fixed distances (in
         // 16-byte units, the low bits of a descriptor)
         const uint64_t dk = sdesc_sw128(smem_u32(smem), 16, 1024), dq = sdesc_sw128(smem_u32(smem + LY::kQ), 16, 1024);
-        // uses of both accumulators of this issuer's two groups, whether a group's last one was
-        // wide; bit st: uses of stage st by this issuer, odd or even
-        uint32_t seq = 0, qseq = 0, uses = 0, use0[2] = {0, 0}, use1[2] = {0, 0};
-        bool was_wide[2] = {false, false};
+        // accumulators of this issuer's two groups so far; bit st of uses: its uses of stage st, odd or even
+        uint32_t seq = 0, qseq = 0, uses = 0, turn0 = 0, turn1 = 0;
         for (uint32_t k = 0; ok; ++k) {
             ok = pass_ready(k);
             if (!ok) break;
@@ -614,7 +672,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             pass_done(k);
             if (jl <= j0) continue;
             const int ns = (rows_all + kSlotRows - 1) / kSlotRows;
-            const bool wide = rows_all > kNarrow;
             int j = j0 + ((j0 + shift + odd) & 1);
             seq += j - j0;
             if (j >= jl) {  // none of the tiles is this issuer's
@@ -628,48 +685,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             bool fresh = true;
             for (; j < jl && ok; j += 2, seq += 2) {
-                const uint32_t st = seq % NS, g = (j + shift) & 3, gi = g >> 1;
+                const uint32_t st = seq % NS;
                 ok = warp_wait(&full[odd * NS + st], uses >> st & 1, abort_flag);
                 uses ^= 1u << st;
                 const uint64_t dks = dk + st * (LY::kStageBytes >> 4);
                 for (int s = 0; s < ns && ok; ++s) {
                     const uint32_t sl = (qseq + s) % kSlots;
                     if (fresh) ok = warp_wait(&qfull[sl], ((qseq + s) / kSlots) & 1, abort_flag);
+                    const bool upper = shift >= kGroups ? s & 1 : (j + shift) >> 1 & 1;  // group odd + 2, or odd
+                    const uint32_t c = upper ? turn1++ : turn0++;
+                    const uint32_t acc = 2 * (odd + 2 * upper) + (c & 1);
+                    if (ok) ok = warp_wait(&accfree[acc], ((c >> 1) & 1) ^ 1, abort_flag);
                     if (!ok) break;
-                    // wide: all the group's columns, as accumulator 0, once both are free; else the
-                    // two in turn, accumulator 1 after a wide one once that is free
-                    const uint32_t u0 = gi ? use0[1] : use0[0], u1 = gi ? use1[1] : use1[0];
-                    const bool second = !wide && u0 != u1 && !(gi ? was_wide[1] : was_wide[0]);
-                    const bool check0 = !second, check1 = wide || second || (gi ? was_wide[1] : was_wide[0]);
-                    if (check0) ok = warp_wait(&accfree[2 * g], (u0 & 1) ^ 1, abort_flag);
-                    if (ok && check1) ok = warp_wait(&accfree[2 * g + 1], (u1 & 1) ^ 1, abort_flag);
-                    if (!ok) break;
-                    if (gi) {
-                        second ? ++use1[1] : ++use0[1];
-                        was_wide[1] = wide;
-                    } else {
-                        second ? ++use1[0] : ++use0[0];
-                        was_wide[0] = wide;
-                    }
                     tc_fence_after();
                     const int rows = min(kSlotRows, rows_all - s * kSlotRows);
                     const uint32_t id = kId | (uint32_t)((rows + 1) / 2) << 18;  // columns: a multiple of 16
                     const uint64_t q = dq + sl * (kSlotBytes >> 4);
-                    const uint32_t d = tmem + g * kCols + (second ? 64u : 0u);
+                    const uint32_t d = tmem + acc * kCols;
                     if constexpr (FP8) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             umma_e4m3_el(el, d, dks + kk * 2, q + kk * 2, id, kk > 0);
-                            umma_e4m3_el(el, d, dks + kk * 2, q + 1024 + kk * 2, id, 1);
+                            umma_e4m3_el(el, d, dks + kk * 2, q + (kSlotHalf >> 4) + kk * 2, id, 1);
                         }
                     } else {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-                            umma_f16_el(el, d, dks + off, q + off, id, kk > 0);
-                        }
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_f16_el(el, d, dks + (kk >> 2) * 1024 + (kk & 3) * 2, q + (kk >> 2) * (kSlotHalf >> 4) + (kk & 3) * 2, id,
+                                        kk > 0);
                     }
-                    umma_commit_el(el, &accfull[2 * g + second]);
+                    umma_commit_el(el, &accfull[acc]);
                     if (j + 2 >= jl) umma_commit_el(el, &qfree[sl]);
                 }
                 if (ok) umma_commit_el(el, &empty[st]);
@@ -703,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const CUtensorMap* tm = n == 4 ? &tm_q4 : &tm_q1;
                         uint8_t* dst = slot + r * (kGroup * 128);
                         tma_load_3d_nohint(dst, tm, bar, 0, x.h * kGroup, x.q0 + r0 + r);
-                        tma_load_3d_nohint(dst + 16384, tm, bar, 64, x.h * kGroup, x.q0 + r0 + r);
+                        tma_load_3d_nohint(dst + kSlotHalf, tm, bar, 64, x.h * kGroup, x.q0 + r0 + r);
                         r += n;
                     }
                 }
@@ -734,103 +779,155 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ============================ groups g = 0 .. 3: thread = token of every fourth tile
         const int g = (warp >> 2) - 1, wq = warp & 3;
         constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
+        const bool upper = g >= 2;
+        // This warp's part of a pass: tiles j, j + step, ... below j1, of which those below jl have
+        // accumulators. A tile's half of 64 tokens is page pages[2 j] while 2 j < num_pages; the
+        // thread's token is number 128 j + mine, its weight weights[128 j], read below `read` and
+        // written below `write`.
+        const int mine = 32 * wq + lane;
+        struct View {
+            const int32_t* pages;
+            float* weights;
+            const float* scales;
+            int j, step, num_pages, read, write;
+        };
+        auto view = [&](const Pass& y) {
+            View v;
+            v.step = y.split() ? 2 : kGroups;
+            v.j = y.j0 + ((g - y.shift - y.j0) & (v.step - 1));
+            v.pages = p.page_table + y.b * p.pt_stride + (wq >> 1);
+            v.num_pages = min(2 * y.j1, (y.L + kChunk - 1) / kChunk) - (wq >> 1);
+            v.weights = p.weights + ((long long)y.b * p.num_kv_heads + y.h) * p.w_stride + mine;
+            v.scales = FP8 ? p.k_scale + y.h * kChunk + (mine & (kChunk - 1)) : nullptr;
+            const bool quiet = y.split() && upper;  // the other group of the tile has the sums
+            v.read = quiet ? 0 : !y.first ? y.L : p.decay != 0.f ? y.p0 : 0;
+            v.write = quiet ? 0 : y.L;
+            return v;
+        };
         // What a tile needs from memory comes a tile of the group ahead, its page id two: across
         // passes too, unless a pass goes on from the sums of the one before.
-        float old = 0.f, factor = 0.f;
+        float old = 0.f, factor = kScale;
         bool there = false;
         int page = -1;  // of the tile after the one ahead
-        auto first_tile = [&](const Pass& y) { return y.j0 + ((g - y.shift - y.j0) & (kGroups - 1)); };
-        auto page_of = [&](const Pass& y, int j) {
-            const int c = 2 * j + (wq >> 1);
-            return j < y.j1 && (long long)c * kChunk < y.L ? p.page_table[y.b * p.pt_stride + c] : -1;
-        };
-        auto fetch = [&](const Pass& y, int j, int pg) {
-            old = 0.f;
-            factor = kScale;
+        auto page_of = [&](const View& v, int j) { return 2 * j < v.num_pages ? v.pages[2 * j] : -1; };
+        auto fetch = [&](const View& v, int j, int pg) {
             there = (unsigned)pg < (unsigned)p.num_pages;
-            const int t = j * kTile + 32 * wq + lane;
-            if (j < y.j1 && t < (y.first ? y.p0 : y.L) && !(y.first && p.decay == 0.f))
-                old = p.weights[((long long)y.b * p.num_kv_heads + y.h) * p.w_stride + t];
-            if (FP8 && there) factor = p.k_scale[((long long)pg * p.num_kv_heads + y.h) * kChunk + (t & (kChunk - 1))];
+            old = 0.f;
+            if (j * kTile + mine < v.read) old = v.weights[(long long)j * kTile];
+            if (FP8 && there) factor = v.scales[(long long)pg * p.num_kv_heads * kChunk];
         };
-        uint32_t qseq = 0, use0 = 0, use1 = 0;
-        bool was_wide = false;
+        uint32_t sl0 = 0, sl_lap = 0;  // the pass's first slot, and its lap's parity
+        uint32_t turn = 0, met = 0;    // accumulators; meetings with the other group of the tile
+        View v{};
         ok = pass_ready(0);
         if (ok && passes[0].h >= 0) {
-            const Pass& y = passes[0];
-            fetch(y, first_tile(y), page_of(y, first_tile(y)));
-            page = page_of(y, first_tile(y) + kGroups);
+            v = view(passes[0]);
+            fetch(v, v.j, page_of(v, v.j));
+            page = page_of(v, v.j + v.step);
         }
         for (uint32_t k = 0; ok; ++k) {
-            const Pass x = passes[k % kPasses];
+            const Pass& x = passes[k % kPasses];  // stays until this warp is done with it
             if (x.h < 0) break;
             ok = pass_ready(k + 1);
             if (!ok) break;
-            const Pass& y = passes[(k + 1) % kPasses];  // stays until this warp is done with it
-            const bool have = y.h >= 0;
-            const int page_y = have ? page_of(y, first_tile(y)) : -1;
-            const int ns = x.slots();
-            const bool wide = x.hi - x.lo > kNarrow;
-            float* wrow = p.weights + ((long long)x.b * p.num_kv_heads + x.h) * p.w_stride;
+            const Pass& y = passes[(k + 1) % kPasses];
+            int page_y = -1;
+            if (y.h >= 0) {
+                const View w = view(y);
+                page_y = page_of(w, w.j);
+            }
+            const int rows_all = x.hi - x.lo, ns = x.slots(), j1 = x.j1, jl = x.jl;
+            const int p0 = x.p0 + x.lo;  // the last token that the pass's first row sees
+            const int first_slot = x.split() && upper ? 1 : 0, slot_step = x.split() ? 2 : 1;
+            const bool meet = x.split() && ns > 1, first = x.first;
             bool any = false;      // this warp has seen the pass's slots
             bool fetched = false;  // what is ahead is of the next pass
-            for (int j = first_tile(x); j < x.j1; j += kGroups) {
-                const int t = j * kTile + 32 * wq + lane;
-                const float now_old = x.first ? p.decay * old : old;
+            int j = v.j;
+            for (; j < j1; j += v.step) {
+                const float now_old = first ? p.decay * old : old;
                 const uint64_t now_factor = pair(factor, factor);
                 const bool now_there = there;
-                if (j + kGroups < x.j1) {
-                    fetch(x, j + kGroups, page);
-                    page = page_of(x, j + 2 * kGroups);
-                } else if (have && y.first) {
-                    fetch(y, first_tile(y), page_y);
-                    page = page_of(y, first_tile(y) + kGroups);
+                const int t = j * kTile + mine;
+                float* to = v.weights + (long long)j * kTile;
+                const bool writes = t < v.write;
+                const int next = j + v.step;
+                if (next < j1) {
+                    fetch(v, next, page);
+                    page = page_of(v, next + v.step);
+                } else if (y.h >= 0 && y.first) {
+                    v = view(y);
+                    fetch(v, v.j, page_y);
+                    page = page_of(v, v.j + v.step);
                     fetched = true;
                 }
                 float sum = 0.f;
-                if (j < x.jl) {
+                if (j < jl) {
                     uint64_t sum2 = 0;
-                    for (int s = 0; s < ns; ++s) {
-                        const uint32_t sl = (qseq + s) % kSlots;
-                        if (!any) ok = warp_wait(&qfull[sl], ((qseq + s) / kSlots) & 1, abort_flag);
-                        // as the issuer chose
-                        const bool second = !wide && use0 != use1 && !was_wide;
-                        if (ok) ok = warp_wait(&accfull[2 * g + second], (second ? use1 : use0) & 1, abort_flag);
+                    const bool clear = (j + 1) * kTile - 1 <= p0;  // every row sees every token
+                    for (int s = first_slot; s < ns; s += slot_step) {
+                        const uint32_t over = sl0 + s >= kSlots, sl = sl0 + s - (over ? kSlots : 0);
+                        if (!any) ok = warp_wait(&qfull[sl], (sl_lap ^ over) & 1, abort_flag);
+                        const uint32_t acc = 2 * g + (turn & 1);
+                        if (ok) ok = warp_wait(&accfull[acc], (turn >> 1) & 1, abort_flag);
                         if (!ok) break;
-                        second ? ++use1 : ++use0;
-                        was_wide = wide;
+                        ++turn;
                         tc_fence_after();
-                        const int r0 = x.lo + s * kSlotRows, rows = min(kSlotRows, x.hi - r0);
-                        const uint32_t ta = tmem + ((uint32_t)(32 * wq) << 16) + g * kCols + (second ? 64u : 0u);
-                        // rows of the slot from t - p0 - r0 on see token t: all of them before the last tiles
-                        if (j * kTile + kTile - 1 <= (long long)x.p0 + r0)
-                            slot_rows<FP8, false>(ta, rows, 0, nl + sl * kCols, qc + sl * kCols, now_factor, sum2);
-                        else
-                            slot_rows<FP8, true>(ta, rows, t - x.p0 - r0, nl + sl * kCols, qc + sl * kCols, now_factor, sum2);
+                        const int rows = min(kSlotRows, rows_all - s * kSlotRows);
+                        const uint32_t ta = tmem + ((uint32_t)(32 * wq) << 16) + acc * kCols;
+                        if (clear && rows == kSlotRows)
+                            slot_rows<FP8, false>(ta, kSlotRows, 0, nl + sl * kCols, qc + sl * kCols, now_factor, sum2);
+                        else  // row r of the slot sees the token from t - p0 - 8 s on
+                            slot_rows<FP8, true>(ta, rows, t - p0 - s * kSlotRows, nl + sl * kCols, qc + sl * kCols, now_factor, sum2);
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&accfree[2 * g + second]);
+                        if (lane == 0) mbar_arrive(&accfree[acc]);
                     }
                     if (!ok) break;
                     any = true;
-                    const float2 v = unpair(sum2);
-                    if (now_there) sum = v.x + v.y;
+                    const float2 both = unpair(sum2);
+                    sum = both.x + both.y;
+                    if (meet) {
+                        // the upper group's sum to the lower one's thread of the token, through one of two buffers
+                        const uint32_t at = 2 * (g & 1) + (met & 1), turns = met >> 1;
+                        float* half = part + at * kTile + mine;
+                        ++met;
+                        if (upper) {
+                            ok = warp_wait(&partfree[at], (turns & 1) ^ 1, abort_flag);
+                            if (!ok) break;
+                            *half = sum;
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&partfull[at]);
+                        } else {
+                            ok = warp_wait(&partfull[at], turns & 1, abort_flag);
+                            if (!ok) break;
+                            sum += *half;
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&partfree[at]);
+                        }
+                    }
+                    if (!now_there) sum = 0.f;
                 }
-                if (t < x.L) wrow[t] = now_old + sum;
+                if (writes) *to = now_old + sum;
+                if (fetched) break;
             }
-            if (x.jl > x.j0) {
+            if (!ok) break;
+            if (jl > x.j0) {
                 // the slots are this pass's until every warp has seen them
                 for (int s = 0; s < ns && ok; ++s) {
-                    const uint32_t sl = (qseq + s) % kSlots;
-                    if (!any) ok = warp_wait(&qfull[sl], ((qseq + s) / kSlots) & 1, abort_flag);
-                    __syncwarp();
+                    const uint32_t over = sl0 + s >= kSlots, sl = sl0 + s - (over ? kSlots : 0);
+                    ok = warp_wait(&qfull[sl], (sl_lap ^ over) & 1, abort_flag);
                     if (ok && lane == 0) mbar_arrive(&qfree[sl]);
                 }
-                qseq += ns;
+                sl0 += ns;
+                if (sl0 >= (uint32_t)kSlots) {
+                    sl0 -= kSlots;
+                    sl_lap ^= 1;
+                }
             }
-            if (have && !fetched) {
-                fetch(y, first_tile(y), page_y);
-                page = page_of(y, first_tile(y) + kGroups);
+            if (y.h >= 0 && !fetched) {
+                v = view(y);
+                fetch(v, v.j, page_y);
+                page = page_of(v, v.j + v.step);
             }
             pass_done(k);
         }
