@@ -31,6 +31,7 @@
 // Every wait is bounded (2 s); on expiry the CTA reports HPC_DEVERR_WAIT_TIMEOUT, gives
 // copies and MMAs in flight time to end, frees its TMEM and returns.
 #include <atomic>
+#include <climits>
 #include <cstring>
 
 #include "attn_common.cuh"
@@ -56,8 +57,8 @@ constexpr uint32_t kTmemCols = 512;           // two accumulators of 64 columns 
 constexpr int kPasses = 4;                    // passes that the other warps may be behind the producer
 constexpr int kPassInts = 12;
 constexpr int kPoly = 0;                      // of a row's four pairs, those without the special function unit
-constexpr int kTileCost = 24;                 // query rows
-constexpr int kSeqCost = 8;                   // a sequence's start in a CTA, in rows
+constexpr int kTileCost = 16;                 // query rows
+constexpr int kSeqCost = 4;                   // a sequence's start in a CTA, in rows
 constexpr int kMostRows = 65536;              // rows counted in a tile's cost at most (sums stay in 64 bits)
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -105,27 +106,22 @@ struct Seq {
 
 template <bool REPORT>
 __device__ __forceinline__ Seq seq_of(const WeightParams& p, int b) {
+    // (every load before the first is used)
+    const int len = p.seq_lens[b], count = p.counts ? p.counts[b] : INT_MAX;
+    const int begin = p.q_starts ? p.q_starts[b] : b * p.rows_per_seq, end = p.q_starts ? p.q_starts[b + 1] : begin + p.rows_per_seq;
     Seq s{0, 0, 0, 0, 0, 0};
-    int n = p.rows_per_seq;
-    if (p.q_starts) {
-        s.q0 = p.q_starts[b];
-        const int end = p.q_starts[b + 1];
-        if (s.q0 < 0 || end < s.q0 || end > p.num_tokens) {
-            if (REPORT && p.err) atomicOr(p.err, (int)HPC_DEVERR_BAD_DESCRIPTOR);
-            return s;
-        }
-        n = end - s.q0;
-    } else {
-        s.q0 = b * n;
+    if (begin < 0 || end < begin || end > p.num_tokens) {
+        if (REPORT && p.err) atomicOr(p.err, (int)HPC_DEVERR_BAD_DESCRIPTOR);
+        return s;
     }
-    const int len = p.seq_lens[b];
+    const int n = end - begin;
     if (REPORT && p.err && n > 0) {
         if (len < 0) atomicOr(p.err, (int)HPC_DEVERR_NEGATIVE_LENGTH);
         if (len > p.max_len) atomicOr(p.err, (int)HPC_DEVERR_PAGE_OUT_OF_RANGE);
     }
-    s.L = max(0, min(len, p.max_len));
-    if (n == 0) s.L = 0;
-    s.hi = p.counts ? max(0, min(n, p.counts[b])) : n;
+    s.q0 = begin;
+    s.L = n > 0 ? max(0, min(len, p.max_len)) : 0;
+    s.hi = max(0, min(n, count));
     s.lo = p.window > 0 ? max(0, s.hi - p.window) : 0;
     s.p0 = s.L - n;
     s.tiles = (int)(((long long)s.L + kTile - 1) / kTile);
@@ -468,32 +464,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* qc = reinterpret_cast<float*>(smem + LY::kQc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&full[NS + i], 1);
-            mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&qfull[i], FP8 ? 1 : 2);          // the split; or the copies and the constants
-            mbar_init(&qfree[i], 2 + 4 * kGroups);      // both issuers' MMAs; the groups' warps
-            mbar_init(&qraw[i], 1);
-        }
-        for (int i = 0; i < 2 * kGroups; ++i) {
-            mbar_init(&accfull[i], 1);
-            mbar_init(&accfree[i], 4);
-        }
-        for (int i = 0; i < kPasses; ++i) {
-            mbar_init(&passfull[i], 1);
-            mbar_init(&passfree[i], 3 + 4 * kGroups);   // issuers, stager and the groups' warps
-        }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&partfull[i], 4);
-            mbar_init(&partfree[i], 4);
-        }
-        *abort_flag = 0;
+    if (tid < LY::kNumBars) {  // arrivals that each barrier waits for, in the order above
+        int i = tid;
+        uint32_t n = 1;  // full, empty, qraw, accfull and passfull
+        if ((i -= 3 * NS) >= 0 && i < kSlots) n = FP8 ? 1 : 2;                     // qfull: the split; or copies and constants
+        if ((i -= kSlots) >= 0 && i < kSlots) n = 2 + 4 * kGroups;                 // qfree: both issuers' MMAs; the groups' warps
+        if ((i -= 2 * kSlots + 2 * kGroups) >= 0 && i < 2 * kGroups) n = 4;        // accfree: a group's warps
+        if ((i -= 2 * kGroups + kPasses) >= 0 && i < kPasses) n = 3 + 4 * kGroups; // passfree: issuers, stager, the groups' warps
+        if ((i -= kPasses) >= 0) n = 4;                                            // partfull and partfree: a group's warps
+        mbar_init(&full[tid], n);
         fence_mbar_init();
     }
+    if (tid == 0) *abort_flag = 0;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(const_cast<uint32_t*>(tmem_slot))),
@@ -532,9 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long bucket = max((total + gridDim.x - 1) / gridDim.x, (long long)kTileCost);
         // which sequence each border falls into, by the thread that has summed it
         Border* border = reinterpret_cast<Border*>(smem + LY::kBorder);
-        if (warp < 2) {  // (a division in 64 bits: by one warp for each border)
+        if (warp < 2) {  // the head of each border: how many end before it
             const long long u = (long long)(blockIdx.x + warp) * bucket;
-            const int h = u < total ? (int)(u / per_head) : p.num_kv_heads;
+            int h = 0;
+            for (int i = lane; i < p.num_kv_heads; i += 32) h += (i + 1) * per_head <= u;
+            h = u < total ? __reduce_add_sync(0xffffffffu, h) : p.num_kv_heads;
             if (lane == 0) border[warp] = Border{u < total ? u - h * per_head : 0, h, 0};
         }
         __syncthreads();
@@ -609,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = publish(++k, have, y);
             const int pg2 = have ? pages(y, y.j0) : -1;
             for (int j = x.j0; j < x.jl && ok; j += 16) {
-                if (j != x.j0) pg = pages(x, j);
+                // (16 tiles' page ids are on their way while the 16 before are copied)
+                const int pg3 = pages(x, j + 16);
                 const int nt = min(16, x.jl - j);
                 for (int i = 0; i < nt; ++i, ++seq) {
                     int page[2], there = 0;
@@ -644,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uses[1] ^= ((j + i + x.shift) & 1) == 1 ? 1u << st : 0u;
                     __syncwarp();
                 }
+                pg = pg3;
             }
             x = y;
             pg = pg2;
