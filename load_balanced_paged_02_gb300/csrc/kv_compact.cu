@@ -53,12 +53,23 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvCompactArg
     }
     if (bad && a.err) atomicOr(a.err, (int)HPC_DEVERR_PAGE_OUT_OF_RANGE);
     __syncthreads();
+    if constexpr (FP8) {  // the scales of a head's slots lie side by side
+        for (int i = threadIdx.x; i < nj * H; i += kThreads) {
+            const int h = i / nj, jl = i - h * nj;
+            const int src = src_sh[h * slots_per_block + jl], dst = dst_sh[jl];
+            if (src < 0 || dst < 0) continue;
+            const long long from = ((long long)(src / kChunk) * H + h) * kChunk + src % kChunk;
+            const long long to = ((long long)(dst / kChunk) * H + h) * kChunk + dst % kChunk;
+            const float ks = a.k_scale[from], vs = a.v_scale[from];
+            a.k_scale[to] = ks;
+            a.v_scale[to] = vs;
+        }
+    }
     constexpr int kLanes = FP8 ? 8 : 16, kRowBytes = FP8 ? kHeadDim : 2 * kHeadDim;
     const int hl = threadIdx.x % kLanes;
     const unsigned per_slot = 2u * (unsigned)H, rows = (unsigned)nj * per_slot;
     for (unsigned r0 = threadIdx.x / kLanes; r0 < rows; r0 += kThreads / kLanes * kUnroll) {
         uint4 raw[kUnroll];
-        float scale[kUnroll];
         int dst[kUnroll], head[kUnroll];  // dst < 0: nothing to write
         bool is_v[kUnroll];
 #pragma unroll
@@ -77,18 +88,12 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(const KvCompactArg
             dst[u] = dst_sh[jl];
             const uint8_t* cache = static_cast<const uint8_t*>(is_v[u] ? a.v_cache : a.k_cache);
             raw[u] = *reinterpret_cast<const uint4*>(cache + ((long long)src * H + head[u]) * kRowBytes + 16 * hl);
-            if constexpr (FP8)
-                scale[u] = (is_v[u] ? a.v_scale : a.k_scale)[((long long)(src / kChunk) * H + head[u]) * kChunk + src % kChunk];
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             if (dst[u] < 0) continue;
             uint8_t* cache = static_cast<uint8_t*>(is_v[u] ? a.v_cache : a.k_cache);
             *reinterpret_cast<uint4*>(cache + ((long long)dst[u] * H + head[u]) * kRowBytes + 16 * hl) = raw[u];
-            if constexpr (FP8) {
-                if (hl == 0)
-                    (is_v[u] ? a.v_scale : a.k_scale)[((long long)(dst[u] / kChunk) * H + head[u]) * kChunk + dst[u] % kChunk] = scale[u];
-            }
         }
     }
 }
