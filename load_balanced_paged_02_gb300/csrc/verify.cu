@@ -186,13 +186,20 @@ __device__ __forceinline__ Pair lane_sum(const void* p, const void* q, long long
     return one;
 }
 
+// (out of line: it is rare, and would take registers from the usual path)
+template <int kThreads, bool BF16>
+__device__ __noinline__ Pair lane_sum_each(const void* p, const void* q, long long v0, long long v1, int out, int lane) {
+    return q ? lane_sum<kThreads, BF16, true, true>(p, q, v0, v1, out, lane, nullptr)
+             : lane_sum<kThreads, BF16, false, true>(p, q, v0, v1, out, lane, nullptr);
+}
+
 template <int kThreads, bool BF16>
 __device__ __forceinline__ Pair lane_sum(const void* p, const void* q, long long v0, long long v1, int out, int lane, uint4* ring) {
     if (out < v0 || out >= v1) {
         const Pair x = q ? lane_sum<kThreads, BF16, true, false>(p, q, v0, v1, -1, lane, ring) : lane_sum<kThreads, BF16, false, false>(p, q, v0, v1, -1, lane, ring);
         if (__all_sync(0xffffffffu, x.s < kMost)) return x;
     }
-    return q ? lane_sum<kThreads, BF16, true, true>(p, q, v0, v1, out, lane, ring) : lane_sum<kThreads, BF16, false, true>(p, q, v0, v1, out, lane, ring);
+    return lane_sum_each<kThreads, BF16>(p, q, v0, v1, out, lane);
 }
 
 __device__ __forceinline__ Pair shfl_up(const Pair& x, int o) {
