@@ -811,7 +811,7 @@ hpc_status hpc_attn_weights(const void* q, const void* k_cache, const float* k_s
  * first num_first, the last num_recent, and of those between them the ones with the
  * largest weights, of equal weights the lowest index (NaN counts as less than every
  * number, -0 as 0). A request of at most `budget` tokens keeps all.
- *   weights    device float32 [batch][num_kv_heads][weights_stride]
+ *   weights    device float32 [batch][num_kv_heads][weights_stride], weights_stride <= 2^30
  *   keep       device int32 [batch][num_kv_heads][budget]: indices in rising order,
  *              -1 behind the last
  *   keep_lens  device int32 [batch]: min(seq_lens[b], budget)
@@ -839,8 +839,9 @@ hpc_status hpc_kv_select(const float* weights, long long weights_stride, const i
  *   d_error_word  device int32 or NULL: HPC_DEVERR_PAGE_OUT_OF_RANGE (a token or page
  *              out of range: its row is not written; or keep_lens[b] beyond keep_stride
  *              or the new table's row: counts as that), HPC_DEVERR_NEGATIVE_LENGTH
- * The new pages must not be pages that the call reads, or what they then hold is not
- * determined; but a request whose tokens all stay where they are may name its own.
+ * The new pages must not be pages that the call reads, and no page may be named twice, or
+ * what they then hold is not determined; but a request whose tokens all stay where they
+ * are may name its own.
  * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA.
  */
 hpc_status hpc_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int kv_dtype, int num_pages,

@@ -79,7 +79,7 @@ hpc_status hpc_kv_select(const float* weights, long long weights_stride, const i
                          int num_kv_heads, int budget, int num_first, int num_recent, int32_t* keep, int32_t* keep_lens,
                          int* d_error_word, void* stream) {
     if (!batch_ok(batch, num_kv_heads) || !weights || !seq_lens || !keep || !keep_lens) return HPC_ERR_INVALID_ARG;
-    if (weights_stride < 1 || weights_stride > 2147483647LL || budget < 1) return HPC_ERR_INVALID_ARG;
+    if (weights_stride < 1 || weights_stride > (1LL << 30) || budget < 1) return HPC_ERR_INVALID_ARG;
     if (num_first < 0 || num_recent < 0 || (long long)num_first + num_recent > budget) return HPC_ERR_INVALID_ARG;
     const KvSelectArgs a{weights, weights_stride, seq_lens, batch, num_kv_heads, budget, num_first, num_recent, keep, keep_lens,
                          d_error_word};

@@ -41,7 +41,7 @@ def test_kv_select_refusals(L):
     for name in ("w", "sl", "keep", "kl"):
         assert call(**{name: None}) == INVALID, name
     assert call(B=0) == INVALID and call(B=16385) == INVALID and call(H=0) == INVALID and call(H=257) == INVALID
-    assert call(ws=0) == INVALID and call(ws=2147483648) == INVALID and call(n=0) == INVALID
+    assert call(ws=0) == INVALID and call(ws=(1 << 30) + 1) == INVALID and call(n=0) == INVALID
     assert call(first=-1) == INVALID and call(recent=-1) == INVALID
     assert call(first=60, recent=5) == INVALID and call(first=2147483647, recent=2147483647) == INVALID
 
