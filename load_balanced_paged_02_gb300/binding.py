@@ -956,7 +956,7 @@ def _error_word(t):
 
 
 def _weight_rows(what, t, batch=None, heads=None):
-    """Checks of an array [batch, heads, tokens] of weights; its tokens may be the first of longer rows."""
+    """Checks of an array [batch, heads, tokens] of weights."""
     if t.dtype != torch.float32 or t.dim() != 3 or (batch is not None and t.shape[0] != batch) or \
             (heads is not None and t.shape[1] != heads):
         raise HpcError(what, detail="must be a float32 tensor [batch, KV heads, tokens]")
@@ -1060,6 +1060,8 @@ def _prob_rows(what, t, batch, rows, vocab, dtype):
     """The distance in elements between rows of t [batch, rows, vocab], which must be the same from row to row."""
     if t.dtype != dtype or tuple(t.shape) != (batch, rows, vocab):
         raise HpcError(what, detail=f"must be a {dtype} tensor of shape {(batch, rows, vocab)}")
+    if t.is_contiguous():
+        return vocab
     st = t.stride()
     row = st[1] if rows > 1 else st[0]
     if batch * rows == 1:
