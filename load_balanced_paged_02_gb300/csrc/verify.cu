@@ -14,7 +14,12 @@
 //
 // Only row r of p and q is read whole. A cluster of CTAs takes a request, each warp a
 // contiguous part of the vocabulary; the parts' sums say which warp holds the token, and
-// that warp alone goes through its part again.
+// that warp alone goes through its part again, 2048 entries at a time in shared memory.
+//
+// The rows' bytes are the floor (256 requests of 131072 entries in 32 bits, target and draft:
+// 268 MB, 40 us at the rate of a copy); 52 us is what it takes, 5.1 TB/s. The stream alone runs at
+// that rate or above; what is left is the search at each request's end, round trips that the
+// other CTAs of the SM cover in part.
 #include "loop.cuh"
 #include "tile.cuh"
 
@@ -25,7 +30,6 @@ namespace {
 
 constexpr int kAhead = 4;
 constexpr int kMaxCluster = 8;
-constexpr int kRun = 8;     // consecutive entries of a lane in the second pass
 constexpr int kPart = 256;  // a warp's part is a multiple of this many entries
 constexpr float kMost = 18446744073709551616.f;  // entries from 2^64 on count as 0
 
@@ -60,7 +64,7 @@ __device__ __forceinline__ float load(const void* p, long long i) {
 
 // Value k of 16 bytes of a row.
 template <bool BF16>
-__device__ __forceinline__ float at(const uint4& r, int k) {
+__device__ __forceinline__ float at_k(const uint4& r, int k) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     if constexpr (BF16) return __uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
     return __uint_as_float(w[k]);
@@ -154,7 +158,7 @@ __device__ __forceinline__ Pair lane_sum(const void* p, const void* q, long long
             fetch(i + kAhead);
 #pragma unroll
             for (int k = 0; k < kVec; k += 2)
-                add_entries<BOTH>(two, at<BF16>(x, k), at<BF16>(x, k + 1), at<BF16>(y, k), at<BF16>(y, k + 1));
+                add_entries<BOTH>(two, at_k<BF16>(x, k), at_k<BF16>(x, k + 1), at_k<BF16>(y, k), at_k<BF16>(y, k + 1));
         }
         copy_wait<0>();
         v += (long long)n * 32 * kVec;
@@ -218,18 +222,124 @@ __device__ __forceinline__ Pair scan(Pair x, int lane) {
 
 __device__ __forceinline__ double value(const Pair& x) { return (double)x.s + (double)x.e; }
 
-// The first lane whose sum, after `before`, exceeds the border, or else the last with a
-// weight at all; -1 if there is none. `before` becomes the sum before that lane.
-__device__ __forceinline__ int find(const Pair& x, Pair& before, double border, int lane) {
+// The first lane whose sum, after `before`, exceeds the border, or else the last with a weight at
+// all (32 if `more` are to come); -1 if there is none. `before` becomes the sum before that lane.
+__device__ __forceinline__ int find(const Pair& x, Pair& before, double& border, int lane, bool more = false) {
     const Pair incl = scan(x, lane);
     Pair upto = before;
     add(upto, incl);
     const bool some = x.s > 0.f;
     const uint32_t over = __ballot_sync(0xffffffffu, some && value(upto) > border), any = __ballot_sync(0xffffffffu, some);
     if (!any) return -1;
-    const int l = over ? __ffs(over) - 1 : 31 - __clz(any);
+    const int l = over ? __ffs(over) - 1 : more ? 32 : 31 - __clz(any);
+    if (!over && !more) border = INFINITY;  // the last one it stays
     if (l > 0) add(before, Pair{__shfl_sync(0xffffffffu, incl.s, l - 1), __shfl_sync(0xffffffffu, incl.e, l - 1)});
     return l;
+}
+
+// What the warp that looks for the token has a piece of the rows copied into: 32 lines, one for
+// a lane, of 1 << log entries each (up to kLine), with room for 16 bytes more, so that the lanes'
+// reads of 16 bytes fall into different banks.
+constexpr int kLine = 64;
+constexpr int kLeastLog = 3;  // 16 bytes of the shorter type
+template <bool BF16>
+struct Desk {
+    static constexpr int kSize = BF16 ? 2 : 4, kPer16 = 16 / kSize;
+    static constexpr int kStride = kLine * kSize + 16;
+    static constexpr int kBytes = 32 * kStride;
+};
+
+// Entries [v0, v1) of a row, at most 32 << log, to the desk, zeros behind them: all of them on their
+// way at once, as a round trip takes microseconds while others stream.
+template <bool BF16>
+__device__ __forceinline__ void to_desk(uint8_t* desk, const void* row, long long v0, long long v1, int log, int lane) {
+    using D = Desk<BF16>;
+    const int n = (int)(v1 - v0);
+    const uint8_t* src = static_cast<const uint8_t*>(row) + v0 * D::kSize;
+    if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+        const int per = log - (BF16 ? 3 : 2);  // of them in a line, as a power of two
+#pragma unroll 4
+        for (int i = lane; i < 32 << per; i += 32) {
+            uint8_t* to = desk + (i >> per) * D::kStride + (i & (1 << per) - 1) * 16;
+            const int bytes = max(0, min(16, (n - i * D::kPer16) * D::kSize));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(src + (bytes ? i * 16 : 0)), "r"(bytes) : "memory");
+        }
+    } else {
+#pragma unroll 8
+        for (int i = lane; i < 32 << log; i += 32) {
+            uint8_t* to = desk + (i >> log) * D::kStride + (i & (1 << log) - 1) * D::kSize;
+            if constexpr (BF16)
+                *reinterpret_cast<uint16_t*>(to) = i < n ? reinterpret_cast<const uint16_t*>(src)[i] : (uint16_t)0;
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(src + (i < n ? i * 4 : 0)), "r"(i < n ? 4 : 0)
+                             : "memory");
+        }
+    }
+}
+
+// The least entry of [w0, w1) whose running sum, from `before` on, exceeds the border, by a warp;
+// should rounding leave none over it, the last entry with a weight. First the line, then the pair
+// of entries, then the entry.
+template <bool BF16>
+__device__ __forceinline__ int search(uint8_t* desk, const void* p, const void* q, long long w0, long long w1, int out, Pair before, double border,
+                                   int lane) {
+    using D = Desk<BF16>;
+    const uint8_t* pl = desk + lane * D::kStride;
+    long long found = -1;
+    for (long long v0 = w0;; v0 += 32 * kLine) {
+        if (v0 >= w1) {  // no later part had a weight after all: the last entry with one is in an earlier part
+            if (found < 0) return (int)w0;
+            v0 = found;
+            w1 = min(w1, v0 + 32 * kLine);
+            border = INFINITY;
+        }
+        const long long v1 = min(w1, v0 + 32 * kLine);
+        int log = kLeastLog;
+        while (32 << log < v1 - v0) ++log;
+        __syncwarp();
+        to_desk<BF16>(desk, p, v0, v1, log, lane);
+        if (q) to_desk<BF16>(desk + D::kBytes, q, v0, v1, log, lane);
+        copy_commit();
+        copy_wait<0>();
+        __syncwarp();
+        if (out >= v0 && out < v1 && lane == 0) {  // an entry that is left out
+            const int i = (int)(out - v0);
+            uint8_t* at = desk + (i >> log) * D::kStride + (i & (1 << log) - 1) * D::kSize;
+            if constexpr (BF16)
+                *reinterpret_cast<uint16_t*>(at) = 0;
+            else
+                *reinterpret_cast<float*>(at) = 0.f;
+        }
+        __syncwarp();
+        Pair s[4] = {};
+#pragma unroll 2
+        for (int i = 0; i < 1 << log; i += D::kPer16) {
+            const uint4 x = *reinterpret_cast<const uint4*>(pl + i * D::kSize);
+            const uint4 y = q ? *reinterpret_cast<const uint4*>(pl + D::kBytes + i * D::kSize) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < D::kPer16; ++k) add(s[k & 3], entry(at_k<BF16>(x, k), at_k<BF16>(y, k), q != nullptr));
+        }
+        add(s[0], s[1]);
+        add(s[2], s[3]);
+        add(s[0], s[2]);
+        const int line = find(s[0], before, border, lane, v1 < w1);
+        if (line < 0) continue;
+        found = v0;
+        if (line == 32) continue;
+        Pair e[2], two{0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint8_t* at = desk + line * D::kStride + (2 * lane + k) * D::kSize;
+            e[k] = Pair{0.f, 0.f};
+            if (2 * lane + k < 1 << log) e[k] = entry(load<BF16>(at, 0), q ? load<BF16>(at + D::kBytes, 0) : 0.f, q != nullptr);
+            add(two, e[k]);
+        }
+        const int l = find(two, before, border, lane);
+        Pair first = before;
+        add(first, e[0]);
+        const bool second = !(e[0].s > 0.f) || (e[1].s > 0.f && !(value(first) > border));
+        return (int)(v0 + (line << log) + 2 * l + __shfl_sync(0xffffffffu, (int)second, l));
+    }
 }
 
 template <int kThreads, bool BF16>
@@ -325,35 +435,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
         } else if (owner == rank) {
             const int w = find(lane < kWarps ? warp_sum[lane] : Pair{0.f, 0.f}, before, border, lane);
             const long long w0 = min((long long)a.vocab, (rank * kWarps + w) * part), w1 = min((long long)a.vocab, w0 + part);
-            long long last = w0;  // where the run with the token begins
-            bool hit = false;
-            auto weight = [&](long long v) {
-                return v < w1 && v != out ? entry(load<BF16>(p, v), q ? load<BF16>(q, v) : 0.f, q != nullptr) : Pair{0.f, 0.f};
-            };
-#pragma unroll 1
-            for (long long i = w0; i < w1; i += 32 * kRun) {  // kRun consecutive entries per lane
-                Pair s{0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < kRun; ++k) add(s, weight(i + lane * kRun + k));
-                const Pair incl = scan(s, lane);
-                Pair upto = before;
-                add(upto, incl);
-                const uint32_t some = __ballot_sync(0xffffffffu, s.s > 0.f);
-                const uint32_t over = __ballot_sync(0xffffffffu, s.s > 0.f && value(upto) > border);
-                if (some) last = i + (31 - __clz(some)) * kRun;
-                if (over) {
-                    const int l = __ffs(over) - 1;
-                    if (l > 0) add(before, Pair{__shfl_sync(0xffffffffu, incl.s, l - 1), __shfl_sync(0xffffffffu, incl.e, l - 1)});
-                    last = i + l * kRun;
-                    hit = true;
-                    break;
-                }
-                add(before, Pair{__shfl_sync(0xffffffffu, incl.s, 31), __shfl_sync(0xffffffffu, incl.e, 31)});
-            }
-            // should rounding leave no run over the border, it is the last entry with a weight
-            if (!hit) border = INFINITY;
-            last += find(lane < kRun ? weight(last + lane) : Pair{0.f, 0.f}, before, border, lane);
-            if (lane == 0) *token = (int32_t)last;
+            // (the CTA is done with the ring)
+            const int v = search<BF16>(reinterpret_cast<uint8_t*>(ring), p, q, w0, w1, out, before, border, lane);
+            if (lane == 0) *token = v;
         }
     }
     if (cluster > 1) cluster_wait();  // the others read this CTA's sums
@@ -363,6 +447,7 @@ template <int kThreads, bool BF16>
 cudaError_t launch(const VerifyArgs& a, int cluster, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
     constexpr size_t kSmem = sizeof(uint4) * kAhead * 2 * kThreads;
+    static_assert(kSmem >= 2 * Desk<BF16>::kBytes, "the desk takes the ring's place");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -380,15 +465,15 @@ cudaError_t launch(const VerifyArgs& a, int cluster, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs per request: more of them until there are eight per SM. CTAs of 512 threads while a
-// request's eight leave an SM two or fewer, of 256 from there on, of which an SM takes four.
-// us for 131072 entries with the draft's, 512 / 256 threads: 1 request 10.8 / 14.7, 32
-// 15.4 / 18.8, 256 64 / 60; 128 requests of 100003 entries 43 / 34; 4 in place of 8 CTAs for
-// 256 requests of 256 threads 64.
+// CTAs per request: more of them until there are four per SM, what an SM takes of 256 threads.
+// CTAs of 512 threads while a request's eight leave an SM two or fewer, of 256 from there on.
+// us for 131072 entries with the draft's, 512 / 256 threads: 1 request 11.1 / 12.6, 32
+// 13.7 / 13.4, 256 72.7 / 55; 128 requests of 100003 entries 39.8 / 29.0. Until there are two, four
+// or eight CTAs per SM: 256 requests 59.7, 53.3, 54.6, 128 of 100003 27.1, 29.3, 28.9.
 cudaError_t launch_verify(const VerifyArgs& a, bool bf16, cudaStream_t s) {
     const long long sms = tile_default_ctas();
     int cluster = 1;
-    while (cluster < kMaxCluster && a.batch * cluster < 8 * sms && a.vocab > 4096LL * cluster) cluster *= 2;
+    while (cluster < kMaxCluster && a.batch * cluster < 4 * sms && a.vocab > 4096LL * cluster) cluster *= 2;
     if (a.batch * kMaxCluster <= 2 * sms) return bf16 ? launch<512, true>(a, cluster, s) : launch<512, false>(a, cluster, s);
     return bf16 ? launch<256, true>(a, cluster, s) : launch<256, false>(a, cluster, s);
 }
