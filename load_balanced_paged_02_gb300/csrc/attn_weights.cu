@@ -56,7 +56,6 @@ constexpr int kGroups = 4;
 constexpr uint32_t kTmemCols = 512;           // two accumulators of 64 columns per group
 constexpr int kPasses = 4;                    // passes that the other warps may be behind the producer
 constexpr int kPassInts = 12;
-constexpr int kPoly = 0;                      // of a row's four pairs, those without the special function unit
 constexpr int kTileCost = 16;                 // query rows
 constexpr int kSeqCost = 4;                   // a sequence's start in a CTA, in rows
 constexpr int kMostRows = 65536;              // rows counted in a tile's cost at most (sums stay in 64 bits)
@@ -299,32 +298,9 @@ __device__ __forceinline__ uint64_t exp2_2(uint64_t x) {
     return pair(fast_exp2(v.x), fast_exp2(v.y));
 }
 
-// The same without the special function unit, which else sets the pace (16 a clock): 2^n
-// p(f) with n the nearest whole number, from the sum with 1.5 2^23, and p the polynomial of
-// degree 6 with p(0) = 1 whose largest relative error on [-1/2, 1/2] is smallest (2.6e-9, by
-// Remez's exchange; with the roundings 2^-23). 0 up to -127, infinite from 128 on.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x) {
-    float2 v = unpair(x);
-    v.x = fminf(fmaxf(v.x, -127.f), 128.f);
-    v.y = fminf(fmaxf(v.y, -127.f), 128.f);
-    x = pair(v.x, v.y);
-    const uint64_t magic = pair(12582912.f, 12582912.f);
-    const uint64_t t = add2(x, magic);
-    const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x);
-    uint64_t r = fma2(pair(0.00015594677f, 0.00015594677f), f, pair(0.0013406644f, 0.0013406644f));
-    r = fma2(r, f, pair(0.009617693f, 0.009617693f));
-    r = fma2(r, f, pair(0.055503104f, 0.055503104f));
-    r = fma2(r, f, pair(0.24022652f, 0.24022652f));
-    r = fma2(r, f, pair(0.6931472f, 0.6931472f));
-    r = fma2(r, f, pair(1.f, 1.f));
-    const float2 n = unpair(t), q = unpair(r);
-    return pair(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(n.x) << 23)),
-                __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
-}
-
 // The weights of one query row's 8 heads for the thread's token, as two sums of four. s: the
 // scores; nl, qc: the row's constants in shared memory; factor: twice the token's.
-template <bool FP8, int POLY>
+template <bool FP8>
 __device__ __forceinline__ uint64_t row_weight(const uint32_t* s, const float* nl, const float* qc, uint64_t factor) {
     uint64_t e[4];
 #pragma unroll
@@ -342,7 +318,7 @@ __device__ __forceinline__ uint64_t row_weight(const uint32_t* s, const float* n
         }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) e[k] = k < POLY ? exp2_poly2(e[k]) : exp2_2(e[k]);
+    for (int k = 0; k < 4; ++k) e[k] = exp2_2(e[k]);
     return add2(add2(e[0], e[1]), add2(e[2], e[3]));
 }
 
@@ -357,7 +333,7 @@ __device__ __forceinline__ void four_rows(const uint32_t (&s)[32], int r, int ro
         uint64_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            w[k] = row_weight<FP8, kPoly>(s + 8 * k, nl + k * kGroup, qc + k * kGroup, factor);
+            w[k] = row_weight<FP8>(s + 8 * k, nl + k * kGroup, qc + k * kGroup, factor);
             if (MASK && r + k < sees) w[k] = 0;
         }
 #pragma unroll
@@ -366,7 +342,7 @@ __device__ __forceinline__ void four_rows(const uint32_t (&s)[32], int r, int ro
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             if (r + k < rows) {
-                const uint64_t w = row_weight<FP8, kPoly>(s + 8 * k, nl + k * kGroup, qc + k * kGroup, factor);
+                const uint64_t w = row_weight<FP8>(s + 8 * k, nl + k * kGroup, qc + k * kGroup, factor);
                 if (!MASK || r + k >= sees) sum = add2(sum, w);
             }
         }
