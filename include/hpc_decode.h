@@ -784,9 +784,10 @@ hpc_status hpc_kv_read(const void* k_cache, const void* v_cache, const float* k_
  *   q_starts   device int32 [batch + 1], not decreasing, inside [0, num_tokens]; NULL:
  *              num_tokens / batch rows each, one sequence after the other (a decode
  *              batch's [batch][q_len]; num_tokens is a multiple of batch then)
+ *   page_table_stride  <= 2^24
  *   row_counts device int32 [batch] or NULL (all rows); outside [0, n] as the nearest
  *   window     rows that count at most; 0: all
- *   lse        device float32 [num_tokens][num_q_heads]; a row of -inf has no weight
+ *   lse        device float32 [num_tokens][num_q_heads]; a row of -inf and finite queries has no weight
  *   decay      in [0, 1]; 1 adds to the weights received before
  *   weights    device float32 [batch][num_kv_heads][weights_stride], weights_stride
  *              >= page_table_stride * 64
@@ -818,7 +819,8 @@ hpc_status hpc_attn_weights(const void* q, const void* k_cache, const float* k_s
  *   d_error_word  device int32 or NULL: a length beyond weights_stride counts as that
  *              (HPC_DEVERR_PAGE_OUT_OF_RANGE), a negative one as 0
  *              (HPC_DEVERR_NEGATIVE_LENGTH)
- * num_first + num_recent <= budget. Errors: HPC_ERR_INVALID_ARG, HPC_ERR_CUDA.
+ * num_first + num_recent <= budget <= 2^30; keep_lens is another array than seq_lens.
+ * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_CUDA.
  */
 hpc_status hpc_kv_select(const float* weights, long long weights_stride, const int32_t* seq_lens, int batch,
                          int num_kv_heads, int budget, int num_first, int num_recent, int32_t* keep, int32_t* keep_lens,
@@ -830,7 +832,7 @@ hpc_status hpc_kv_select(const float* weights, long long weights_stride, const i
  * keep[b][h][j], j < keep_lens[b]; and new_weights[b][h][j] = weights[b][h][keep[b][h][j]]
  * where weights are given. Bits are copied. The attention calls then take new_table and
  * keep_lens.
- *   keep       device int32 [batch][num_kv_heads][keep_stride]
+ *   keep       device int32 [batch][num_kv_heads][keep_stride], keep_stride <= 2^30
  *   new_table  device int32 [batch][new_table_stride]; the first ceil(keep_lens[b] / 64)
  *              entries of row b are read
  *   weights    device float32 [batch][num_kv_heads][weights_stride] or NULL,
@@ -871,7 +873,7 @@ typedef enum hpc_probs_dtype { HPC_PROBS_F32 = 0, HPC_PROBS_BF16 = 1 } hpc_probs
  *   draft_counts  device int32 [batch] or NULL (num_drafts each); outside [0, num_drafts]
  *              as the nearest
  *   accept_rand   device float32 [batch][num_drafts], sample_rand [batch]: uniform on [0, 1)
- *   num_accepted  device int32 [batch]
+ *   num_accepted  device int32 [batch], another array than draft_counts
  *   tokens     device int32 [batch][num_drafts + 1]: the accepted drafts, the next token,
  *              then -1
  *   seq_lens   device int32 [batch] or NULL, lengths that count all num_drafts + 1 new

@@ -955,6 +955,13 @@ def _error_word(t):
         _i32("error_word", t)
 
 
+def _whole(what, **numbers):
+    """Numbers that the C call takes as int32: what does not fit is refused, not cut off."""
+    for name, x in numbers.items():
+        if not 0 <= x < 1 << 31:
+            raise HpcError(what, detail=f"{name} must be in [0, 2^31)")
+
+
 def _weight_rows(what, t, batch=None, heads=None):
     """Checks of an array [batch, heads, tokens] of weights."""
     if t.dtype != torch.float32 or t.dim() != 3 or (batch is not None and t.shape[0] != batch) or \
@@ -988,6 +995,7 @@ def hpc_attn_weights(q, k_cache, page_table, seq_lens, lse, weights, q_starts=No
     if counts is not None:
         _i32("counts", counts, B)
     _weight_rows("weights", weights, B, Hkv)
+    _whole(what, window=window)
     _error_word(error_word)
     dev = _on_device(what, q, k_cache, k_scale, page_table, seq_lens, lse, weights, q_starts, counts, error_word)
     rc = lib().hpc_attn_weights(
@@ -1009,6 +1017,7 @@ def hpc_kv_select(weights, seq_lens, budget: int, num_first: int = 0, num_recent
     Hkv = weights.shape[1]
     if budget < 1:
         raise HpcError(what, detail="budget must be at least 1")
+    _whole(what, budget=budget, num_first=num_first, num_recent=num_recent)
     if keep is not None:
         _tensor("keep", keep, (B, Hkv, budget), torch.int32)
     if keep_lens is not None:

@@ -44,7 +44,8 @@ hpc_status hpc_attn_weights(const void* q, const void* k_cache, const float* k_s
     if (st != HPC_OK) return st;
     const bool fp8 = kv_dtype == HPC_KV_FP8_E4M3;
     if (!k_cache || !aligned(k_cache, 16) || (fp8 && (!k_scale || !aligned(k_scale, 16)))) return HPC_ERR_INVALID_ARG;
-    if (!page_table || page_table_stride < 1 || !seq_lens || !weights || window < 0 || num_tokens < 0) return HPC_ERR_INVALID_ARG;
+    if (!page_table || page_table_stride < 1 || page_table_stride > (1 << 24)) return HPC_ERR_INVALID_ARG;  // up to 2^30 tokens
+    if (!seq_lens || !weights || window < 0 || num_tokens < 0) return HPC_ERR_INVALID_ARG;
     if (!(decay >= 0.f && decay <= 1.f)) return HPC_ERR_INVALID_ARG;
     if (weights_stride < (long long)page_table_stride * kChunk) return HPC_ERR_INVALID_ARG;
     if (!q_starts && num_tokens % batch != 0) return HPC_ERR_INVALID_ARG;
@@ -79,7 +80,8 @@ hpc_status hpc_kv_select(const float* weights, long long weights_stride, const i
                          int num_kv_heads, int budget, int num_first, int num_recent, int32_t* keep, int32_t* keep_lens,
                          int* d_error_word, void* stream) {
     if (!batch_ok(batch, num_kv_heads) || !weights || !seq_lens || !keep || !keep_lens) return HPC_ERR_INVALID_ARG;
-    if (weights_stride < 1 || weights_stride > (1LL << 30) || budget < 1) return HPC_ERR_INVALID_ARG;
+    if (weights_stride < 1 || weights_stride > (1LL << 30) || budget < 1 || budget > (1 << 30)) return HPC_ERR_INVALID_ARG;
+    if (keep_lens == seq_lens) return HPC_ERR_INVALID_ARG;  // (every head's CTAs read the lengths)
     if (num_first < 0 || num_recent < 0 || (long long)num_first + num_recent > budget) return HPC_ERR_INVALID_ARG;
     const KvSelectArgs a{weights, weights_stride, seq_lens, batch, num_kv_heads, budget, num_first, num_recent, keep, keep_lens,
                          d_error_word};
@@ -100,7 +102,7 @@ hpc_status hpc_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v
     if (fp8 && (!k_scale || !v_scale)) return HPC_ERR_INVALID_ARG;
     if (!page_table || page_table_stride < 1 || !keep || keep_stride < 1 || !keep_lens || !new_table || new_table_stride < 1)
         return HPC_ERR_INVALID_ARG;
-    if (!weights != !new_weights) return HPC_ERR_INVALID_ARG;
+    if (keep_stride > (1 << 30) || !weights != !new_weights) return HPC_ERR_INVALID_ARG;
     if (weights) {
         const long long room = (long long)new_table_stride * kChunk;
         if (weights_stride < (long long)page_table_stride * kChunk || weights == new_weights) return HPC_ERR_INVALID_ARG;
@@ -143,6 +145,7 @@ hpc_status hpc_verify_drafts(const void* target_probs, long long target_stride, 
         if (!draft_tokens || !accept_rand) return HPC_ERR_INVALID_ARG;
     }
     if (!sample_rand || !num_accepted || !tokens || (kept_lens && !seq_lens)) return HPC_ERR_INVALID_ARG;
+    if (num_accepted == draft_counts) return HPC_ERR_INVALID_ARG;  // (all of a request's CTAs read the count)
     VerifyArgs a;
     a.target = target_probs;
     a.target_stride = target_stride;

@@ -71,3 +71,19 @@ def test_verify_refusals(L):
     assert call(n=-1) == INVALID and call(n=32) == INVALID and call(V=0) == INVALID
     assert call(ps=99) == INVALID and call(qs=99) == INVALID and call(p=0x10002) == INVALID and call(q=0x10001, dt=1) == INVALID
     assert call(kl=FAKE) == INVALID                                                 # new lengths of no lengths
+
+
+def test_sizes_that_leave_32_bits(L):
+    def weights(stride, ws):
+        return L.hpc_attn_weights(FAKE, FAKE, None, 0, 16, FAKE, stride, FAKE, FAKE, None, 0, FAKE, 2, 10, 8, 1, 128, 64, 1.0, FAKE, ws, None,
+                                  None)
+    assert weights((1 << 24) + 1, ((1 << 24) + 1) * 64) == INVALID and weights(2147483647, 2147483647 * 64) == INVALID
+    for n in ((1 << 30) + 1, 2147483647):
+        assert L.hpc_kv_select(FAKE, 256, OTHER, 2, 1, n, 4, 8, FAKE, FAKE, None, None) == INVALID
+        assert L.hpc_kv_compact(FAKE, FAKE, None, None, 0, 16, FAKE, 4, FAKE, n, FAKE, FAKE, 1, 2, 1, 128, 64, None, 0, None, 0, None,
+                                None) == INVALID
+
+
+def test_outputs_that_other_blocks_still_read(L):
+    assert L.hpc_kv_select(FAKE, 256, OTHER, 2, 1, 64, 4, 8, FAKE, OTHER, None, None) == INVALID    # lengths in place
+    assert L.hpc_verify_drafts(FAKE, 100, FAKE, 100, 0, FAKE, OTHER, FAKE, FAKE, 2, 3, 100, OTHER, FAKE, None, None, None, None) == INVALID

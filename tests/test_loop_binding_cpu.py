@@ -103,6 +103,19 @@ def test_verify_drafts():
     refused(lambda: call(kept_lens=i32(2)), "seq_lens")
 
 
+def test_numbers_are_not_cut_to_32_bits():
+    def weights(window):
+        return hb.hpc_attn_weights(bf16(2, 8, 128), bf16(4, 64, 1, 128), i32(2, 3), i32(2), f32(2, 8), f32(2, 1, 192), window=window)
+
+    def select(budget=8, **kw):
+        return hb.hpc_kv_select(f32(2, 1, 100), i32(2), budget, **kw)
+    for x in ((1 << 32) + 5, 1 << 31, -1):
+        refused(lambda: weights(x), "window")
+        refused(lambda: select(num_first=x), "num_first")
+        refused(lambda: select(num_recent=x), "num_recent")
+    refused(lambda: select(budget=(1 << 32) + 5), "budget")
+
+
 def test_the_package_names_them():
     import load_balanced_paged_02_gb300 as pkg
     for name in ("hpc_attn_weights", "hpc_kv_select", "hpc_kv_compact", "hpc_verify_drafts"):
