@@ -4,118 +4,80 @@
 //
 // Radix selection on the weights' bits, mapped to unsigned numbers of the same order: three
 // histograms (11, 11 and 10 bits) give the smallest weight that stays and how many of its
-// equals do. The keys stay in shared memory, and all of them are gone through three times:
-// loaded and put into the first histogram; looked through for the ones in the bin found,
-// which go to a list that gives the other two histograms (a bin of too many is gone through
-// again instead); and written, each thread a run of its own at the place that the counts
-// give. Nothing in these loops branches on a key.
+// equals do. All weights are gone through twice: for the first histogram, by their own upper bits
+// (its bins are brought in order when it is summed), and for the list of those that reach the bin
+// found, which each warp keeps in shared memory for its part of the row, in order. Whatever
+// follows, the other two histograms, the counts and the indices, needs the lists alone. A warp
+// that has more of them than its list has room for goes through its part again each time (24 x 8
+// rows of 65536, half of them kept: 70 us; through the rows in shared memory, as before the lists, 99).
 //
-// A CTA takes a row. Rows differ in length, and the time is that of the longest, so where
-// the array has room for more than 8192 tokens CTAs have 1024 threads and take the rows in
-// order of falling length (512 rows of lengths log-uniform in [128, 65536]: 41 us, in the
-// batch's order 52; 512 rows of 4096 tokens with 512 threads 21 us, with 1024 and in order 35).
-// Where rows are fewer than SMs, clusters of up to 8 CTAs share each, a contiguous part of its
-// tokens for each CTA, and sum the histograms through distributed shared memory (8 rows of
-// 262144: 28 us, 317 by single CTAs of 512 threads). Clusters for every row, whose CTAs leave
-// where it is short, are placed as one and took 64 us for the first batch. What bounds a row
-// is the instructions of the three passes, about 30 for 32 keys each, and five barriers.
+// A CTA of 512 threads takes a row, two of them an SM: a row's fixed costs, five barriers and
+// the round trips between them, about 5 us, are covered by the other's (512 rows of lengths
+// log-uniform in [128, 65536]: 23 us; one CTA of 1024 threads per SM 29, four of 256 25). Where the
+// array has room for more than 8192 tokens they take the rows in order of falling length
+// (in the batch's order 27; finding the order costs rows of 4096 tokens 2 us of 19). Where rows are
+// fewer than SMs, clusters of up to 8 CTAs share each, a contiguous part of its tokens for
+// each CTA, and sum the histograms through distributed shared memory: 64 groups of bins, then
+// the one group's (8 rows of 262144: 19 us, 137 by single CTAs; whole histograms, read by
+// every CTA, 23). Clusters for every row, whose CTAs leave where it is short, are
+// placed as one and took 64 us for the first batch. What bounds a row of 65536 is its two
+// passes, 5 us each for one CTA, at about 15 instructions for 32 weights.
 #include "loop.cuh"
 #include "tile.cuh"
 
 #include <atomic>
+#include <climits>
 
 namespace hpc {
 namespace {
 
 constexpr int kBins = 2048;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kLeastPart = 4096;                 // tokens of a CTA at least, before another takes part
-constexpr int kChunkKeys = 32768;                // keys that a CTA keeps in shared memory
-constexpr int kList = 4096;                      // keys of one bin that the list has room for
-constexpr int kLoads = 8;                        // keys that a thread has on their way at once
+constexpr int kMostListed = 640;                 // tokens that a warp's list has room for at most
+constexpr int kLoads = 8;                        // weights that a thread has on their way at once
+constexpr long long kShort = 8192;               // rows up to this are taken as they come
 constexpr int kOrdered = 1024;                   // batches up to this are taken in order of length
 
 struct Smem {
-    uint32_t hist[2][kBins + 32];  // a lane that has nothing to count adds behind the bins: no branch
-    uint2 list[kList + 32];        // key and place (likewise)
+    uint32_t hist[3][kBins];
+    uint32_t group[3][kBins / 32];
     uint32_t scan[32], scan2[32];
-    uint32_t owned[1024];          // per thread: its tokens of the list, as counted by `count`
-    uint32_t found[2];             // bin, tokens in higher bins
+    uint32_t found[2];             // bin, and how many of its tokens stay
     uint32_t above, equal;         // tokens of this CTA's part
-    uint32_t listed;
     int32_t request;
-    uint32_t keys[1];              // [the longest part, at most kChunkKeys, and 1024 kLoads more]
+    uint2 list[1];                 // [warps][room]: weight and place
 };
 
-// Unsigned numbers in the order of the floats; -0 counts as 0, and NaN as less than all.
+// Unsigned numbers in the order of the floats x + 0 (-0 counts as 0), NaN as less than all.
 __device__ __forceinline__ uint32_t order_key(float x) {
-    const uint32_t u = __float_as_uint(x + 0.f);  // -0 + 0 is 0
+    const uint32_t u = __float_as_uint(x);
     const uint32_t k = u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
     return x != x ? 0u : k;
 }
 
-__device__ __forceinline__ void store_if(uint32_t yes, int32_t* p, int32_t v) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.b32 [%1], %2;\n\t}" ::"r"(yes), "l"(p), "r"(v) : "memory");
+// The first histogram is of the weights' own upper 11 bits (an addition's NaN is 0x7fffffff): where
+// bin number `o` of order_key's is in it.
+__device__ __forceinline__ int bin_of(int o) {
+    if (o == 0) return 1023;     // NaN
+    if (o == 2047) return 2047;  // (what would be NaN of the other sign: none)
+    return o >= 1024 ? o - 1024 : 2047 - o;
 }
 
-// The sum of x over the threads before this one.
-template <int kThreads>
-__device__ __forceinline__ uint32_t block_before(uint32_t* scan, uint32_t x, int lane, int warp) {
-    uint32_t incl = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    return __reduce_add_sync(0xffffffffu, lane < warp ? scan[lane] : 0u) + incl - x;
-}
-
-// Bins [first, first + N) summed over the cluster's `active` CTAs.
-template <int N>
-__device__ __forceinline__ void cluster_bins(const uint32_t* hist, int first, int active, uint32_t (&sum)[N]) {
-    if (active == 1) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) sum[k] = hist[first + k];
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < N; ++k) sum[k] = 0;
-    uint32_t x[kMaxCluster][N];
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-        if (r >= active) break;
-        const uint32_t at = cluster_addr(hist + first, r);
-#pragma unroll
-        for (int k = 0; k < N; k += 2)
-            asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(x[r][k]), "=r"(x[r][k + 1]) : "r"(at + 4 * k));
-    }
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-        if (r >= active) break;
-#pragma unroll
-        for (int k = 0; k < N; ++k) sum[k] += x[r][k];
-    }
-}
-
-template <int kThreads>
-__global__ void __launch_bounds__(kThreads, 1536 / kThreads) kv_select_kernel(const KvSelectArgs a, int cluster) {
-    constexpr int kWarps = kThreads / 32, kOwnBins = kBins / kThreads;
+__global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const KvSelectArgs a, int cluster, int room, bool ordered) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     const int rank = (int)(blockIdx.x % (unsigned)cluster);
     const long long turn = blockIdx.x / (unsigned)cluster;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < 2 * (kBins + 32); i += kThreads) (&sm.hist[0][0])[i] = 0u;
-    sm.owned[tid] = 0u;
-    if (tid == 0) sm.listed = 0u;
+    for (int i = tid; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0u;
     grid_dependency_wait();
     grid_launch_dependents();
     int b = (int)(turn / a.num_kv_heads);
-    if (kThreads == 1024 && a.batch > 1 && a.batch <= kOrdered) {
+    if (ordered && a.batch > 1 && a.batch <= kOrdered) {
         // the request that has b longer ones (of equals, the ones before it)
-        int32_t* lens = reinterpret_cast<int32_t*>(sm.keys);
+        int32_t* lens = reinterpret_cast<int32_t*>(sm.list);
         for (int i = tid; i < a.batch; i += kThreads) lens[i] = a.seq_lens[i];
         __syncthreads();
         for (int i = tid; i < a.batch; i += kThreads) {
@@ -127,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) kv_select_kernel(co
         }
         __syncthreads();
         b = sm.request;
-        __syncthreads();  // (the keys take the place of the lengths)
+        __syncthreads();  // (the list takes the place of the lengths)
     }
     const long long row = (long long)b * a.num_kv_heads + turn % a.num_kv_heads;
     const long long L64 = a.seq_lens[b];
@@ -152,174 +114,186 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) kv_select_kernel(co
     for (int i = at; i < a.recent; i += step) keep[a.budget - a.recent + i] = L - a.recent + i;
     uint32_t need = (uint32_t)(a.budget - a.first - a.recent);
     if (need == 0) return;
-    const int lo = rank * part, n = min(M, lo + part) - lo;
-    const float* w = a.weights + row * a.w_stride + a.first + lo;
 
-    // A chunk of up to kChunkKeys tokens in shared memory; each thread has a run of them, of odd
-    // length, so that the lanes' reads fall into different banks.
-    const int chunks = (n + kChunkKeys - 1) / kChunkKeys;
-    int c0 = 0, m = 0, run = 0;  // the chunk's first token, its tokens, and a thread's
-    auto load = [&](int c, uint32_t* hist) {  // hist: the first histogram, or null
-        if (chunks > 1) __syncthreads();
-        c0 = c * kChunkKeys;
-        m = min(kChunkKeys, n - c0);
-        run = ((m + kThreads - 1) / kThreads) | 1;
+    // This warp's tokens: [s0, s1) of the middle.
+    const int lo = rank * part, n = min(M, lo + part) - lo;
+    const int seg = ((n + kWarps - 1) / kWarps + 31) & ~31;
+    const int s0 = lo + min(n, warp * seg), s1 = lo + min(n, (warp + 1) * seg);
+    const float* w = a.weights + row * a.w_stride + a.first;
+    const uint32_t before_me = (1u << lane) - 1u;
+    // f(weight + 0, place, whether there is one) for all of them in order, 32 at a time.
+    auto sweep = [&](auto&& f) {
+        const float* at = w + lane;
+        int i = s0;
+        float x[kLoads];
+        if (i + 32 * kLoads <= s1) {
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) x[k] = __ldg(at + i + 32 * k);
+            bool next;
 #pragma unroll 1
-        for (int i = tid; i < m; i += kThreads * kLoads) {
-            float x[kLoads];
+            do {
+                next = i + 2 * 32 * kLoads <= s1;
+                float y[kLoads];
+                if (next) {
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k)
-                if (i + kThreads * k < m) x[k] = __ldg(w + c0 + i + kThreads * k);
+                    for (int k = 0; k < kLoads; ++k) y[k] = __ldg(at + i + 32 * (kLoads + k));
+                }
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) {
-                const uint32_t key = order_key(x[k]);
-                const bool in = i + kThreads * k < m;
-                sm.keys[i + kThreads * k] = key;
-                if (hist) atomicAdd(&hist[in ? key >> 21 : kBins + lane], 1u);
-            }
+                for (int k = 0; k < kLoads; ++k) f(x[k] + 0.f, i + 32 * k + lane, true);
+                i += 32 * kLoads;
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) x[k] = y[k];
+            } while (next);
+        }
+        if (i >= s1) return;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k)
+            if (i + 32 * k + lane < s1) x[k] = __ldg(at + i + 32 * k);
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            if (i + 32 * k >= s1) break;
+            f(x[k] + 0.f, i + 32 * k + lane, i + 32 * k + lane < s1);
         }
     };
-    // Of the bins of a histogram, the one with the token number `need` from the largest down.
-    auto find = [&](const uint32_t* hist) {
-        if (active > 1) {
-            cluster_arrive();
-            cluster_wait();
-        } else {
-            __syncthreads();
-        }
-        uint32_t v[kOwnBins], sum = 0;
-        const int first_bin = kBins - kOwnBins * (tid + 1);
-        cluster_bins<kOwnBins>(hist, first_bin, active, v);
+    // Of the bins of a histogram, the one with the token number `need` from the largest down. In
+    // a cluster first among groups of 32 bins, then in the group, both summed over its CTAs.
+    auto find = [&](int turn) {
+        const uint32_t* hist = sm.hist[turn];
+        auto at = [&](int bin) { return hist + (turn == 0 ? bin_of(bin) : bin); };
+        __syncthreads();
+        if (active == 1) {  // each thread a few bins
+            constexpr int kOwn = kBins / kThreads;
+            uint32_t v[kOwn], sum = 0;
+            const int first_bin = kBins - kOwn * (tid + 1);
 #pragma unroll
-        for (int k = 0; k < kOwnBins; ++k) sum += v[k];
-        uint32_t higher = block_before<kThreads>(sm.scan, sum, lane, warp);
+            for (int k = 0; k < kOwn; ++k) sum += v[k] = *at(first_bin + k);
+            uint32_t incl = sum;
 #pragma unroll
-        for (int k = kOwnBins - 1; k >= 0; --k) {
-            if (higher < need && need <= higher + v[k]) {
-                sm.found[0] = first_bin + k;
-                sm.found[1] = higher;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
             }
-            higher += v[k];
+            if (lane == 31) sm.scan[warp] = incl;
+            __syncthreads();
+            uint32_t higher = __reduce_add_sync(0xffffffffu, lane < warp ? sm.scan[lane] : 0u) + incl - sum;
+#pragma unroll
+            for (int k = kOwn - 1; k >= 0; --k) {
+                if (higher < need && need <= higher + v[k]) {
+                    sm.found[0] = first_bin + k;
+                    sm.found[1] = need - higher;
+                }
+                higher += v[k];
+            }
+            __syncthreads();
+            need = sm.found[1];
+            return sm.found[0];
+        }
+        for (int g = warp; g < kBins / 32; g += kWarps) {
+            const uint32_t x = __reduce_add_sync(0xffffffffu, *at(32 * g + lane));
+            if (lane == 0) sm.group[turn][g] = x;
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (warp == 0) {
+            auto total = [&](const uint32_t* p) {
+                uint32_t x[kMaxCluster], sum = 0;
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) x[r] = r < active ? cluster_load_u32(cluster_addr(p, r)) : 0u;
+#pragma unroll
+                for (int r = 0; r < kMaxCluster; ++r) sum += x[r];
+                return sum;
+            };
+            // lane 0 has the highest; the lane that reaches `need`, which becomes what is left of it there
+            auto lane_of = [&](uint32_t x) {
+                uint32_t incl = x;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                const int l = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
+                need -= __shfl_sync(0xffffffffu, incl - x, l);
+                return l;
+            };
+            const uint32_t x = total(&sm.group[turn][63 - 2 * lane]), y = total(&sm.group[turn][62 - 2 * lane]);
+            const int l = lane_of(x + y);
+            const uint32_t higher = __shfl_sync(0xffffffffu, x, l);
+            const bool second = need > higher;
+            if (second) need -= higher;
+            const int g = 63 - 2 * l - (second ? 1 : 0), bin = 32 * g + 31 - lane_of(total(at(32 * g + 31 - lane)));
+            if (lane == 0) {
+                sm.found[0] = (uint32_t)bin;
+                sm.found[1] = need;
+            }
         }
         __syncthreads();
-        need -= sm.found[1];
+        need = sm.found[1];
         return sm.found[0];
     };
-    for (int c = 0; c < chunks; ++c) load(c, sm.hist[0]);
-    const uint32_t top = find(sm.hist[0]);
-    // the keys of that bin; and how many of this thread's run are above it (one chunk only)
-    uint32_t mine = 0;  // above in the upper, equals in the lower half word
-    for (int c = 0; c < chunks; ++c) {
-        if (chunks > 1) {
-            load(c, nullptr);
-            __syncthreads();
-        }
-        const int i0 = min(m, tid * run), i1 = min(m, i0 + run);
-#pragma unroll 1
-        for (int i = i0; i < i1; i += kLoads) {
-            uint32_t key[kLoads], in_bin = 0;
-#pragma unroll
-            for (int k = 0; k < kLoads; ++k) key[k] = sm.keys[i + k];
-#pragma unroll
-            for (int k = 0; k < kLoads; ++k) {
-                const uint32_t in = i + k < i1, d = key[k] >> 21;
-                mine += (in & (d > top)) << 16;
-                in_bin |= (in & (d == top)) << k;
-            }
-            if (in_bin) {
-                uint32_t place = atomicAdd(&sm.listed, (uint32_t)__popc(in_bin));
-#pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    sm.list[(in_bin >> k & 1u) && place < kList ? place : kList + lane] = make_uint2(key[k], (uint32_t)tid);
-                    place += in_bin >> k & 1u;
-                }
-            }
-        }
+    sweep([&](float x, int, bool in) {
+        if (in) atomicAdd(&sm.hist[0][__float_as_uint(x) >> 21], 1u);
+    });
+    uint32_t prefix = find(0) << 21;
+
+    // Only keys from here on can stay: the warp's list of them, in order
+    uint2* list = sm.list + warp * room;
+    int listed = 0;
+    const float least = __uint_as_float(prefix ^ (prefix & 0x80000000u ? 0x80000000u : 0xffffffffu));
+    if (prefix < 0x00800000u) {
+        listed = INT_MAX;  // down to -infinity or NaN: no number is the least
+    } else {
+        sweep([&](float x, int i, bool in) {
+            const bool stays = in && x >= least;
+            const uint32_t those = __ballot_sync(0xffffffffu, stays);
+            const int place = listed + __popc(those & before_me);
+            if (stays && place < room) list[place] = make_uint2(__float_as_uint(x), (uint32_t)i);
+            listed += __popc(those);
+        });
     }
-    __syncthreads();
-    const int listed = (int)sm.listed;
-    const bool all = listed > kList;  // too many: gone through again
-    // histogram of (key >> shift) & digit of the keys with key & mask == prefix
-    auto refine = [&](uint32_t* hist, uint32_t prefix, uint32_t mask, int shift, uint32_t digit) {
-        if (!all) {
-            for (int i = tid; i < listed; i += kThreads) {
-                const uint32_t key = sm.list[i].x;
-                atomicAdd(&hist[(key & mask) == prefix ? (key >> shift) & digit : kBins + lane], 1u);
-            }
+    __syncwarp();
+    // f(key, place, whether there is one) for the list's, or, where it had no room for them, for all again.
+    auto candidates = [&](auto&& f) {
+        if (listed > room) {
+            sweep([&](float x, int i, bool in) { f(order_key(x), i, in); });
             return;
         }
-        for (int c = 0; c < chunks; ++c) {
-            if (chunks > 1) {
-                load(c, nullptr);
-                __syncthreads();
-            }
-#pragma unroll 1
-            for (int i = tid; i < m; i += kThreads * kLoads) {
-                uint32_t key[kLoads];
-#pragma unroll
-                for (int k = 0; k < kLoads; ++k) key[k] = sm.keys[i + kThreads * k];
-#pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    const bool one = i + kThreads * k < m && (key[k] & mask) == prefix;
-                    atomicAdd(&hist[one ? (key[k] >> shift) & digit : kBins + lane], 1u);
-                }
-            }
+#pragma unroll 2
+        for (int i = 0; i < listed; i += 32) {
+            const uint2 x = i + lane < listed ? list[i + lane] : make_uint2(0u, 0u);
+            f(order_key(__uint_as_float(x.x)), (int)x.y, i + lane < listed);
         }
     };
-    uint32_t prefix = top << 21;
-    refine(sm.hist[1], prefix, 0xffe00000u, 10, 2047u);
-    prefix |= find(sm.hist[1]) << 10;
-    // (the third histogram takes the first one's place, which every CTA read before the second's barrier)
-    for (int i = tid; i < kBins; i += kThreads) sm.hist[0][i] = 0u;
-    __syncthreads();
-    refine(sm.hist[0], prefix, 0xfffffc00u, 0, 1023u);
-    prefix |= find(sm.hist[0]);
+    candidates([&](uint32_t key, int, bool in) {
+        if (in && key >> 21 == prefix >> 21) atomicAdd(&sm.hist[1][key >> 10 & 2047u], 1u);
+    });
+    prefix |= find(1) << 10;
+    candidates([&](uint32_t key, int, bool in) {
+        if (in && key >> 10 == prefix >> 10) atomicAdd(&sm.hist[2][key & 1023u], 1u);
+    });
+    prefix |= find(2);
 
-    // `prefix` is the smallest key that stays, and `need` of its equals do. Counts first, above
-    // in the upper and equals in the lower half of a word (a chunk has fewer than 2^16), then places.
-    auto weigh = [&](uint32_t key) { return ((uint32_t)(key > prefix) << 16) + (uint32_t)(key == prefix); };
-    static_assert(kChunkKeys < 65536, "counts of a chunk in half words");
-    auto count = [&]() {  // of the run in the chunk that is there
-        uint32_t x = 0;
-        const int i1 = min(m, (tid + 1) * run);
-#pragma unroll 8
-        for (int i = min(m, tid * run); i < i1; ++i) x += weigh(sm.keys[i]);
-        return x;
-    };
-    const bool again = all || chunks > 1;  // the counts are taken from all the keys, or from the list's
-    if (!again) {
-        for (int i = tid; i < listed; i += kThreads) {
-            const uint2 x = sm.list[i];
-            atomicAdd(&sm.owned[x.y], weigh(x.x));
-        }
-        __syncthreads();
-        mine += sm.owned[tid];
+    // `prefix` is the smallest key that stays, and `need` of its equals do. First how many are before this warp's.
+    uint32_t above = 0, equal = 0;
+    candidates([&](uint32_t key, int, bool in) {
+        above += in && key > prefix;
+        equal += in && key == prefix;
+    });
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {
+        sm.scan[warp] = above;
+        sm.scan2[warp] = equal;
     }
-    uint32_t na = 0, ne = 0;  // kept for certain, and equals, among the tokens before this chunk
+    __syncthreads();
+    const uint32_t above_of = lane < kWarps ? sm.scan[lane] : 0u, equal_of = lane < kWarps ? sm.scan2[lane] : 0u;
+    above = __reduce_add_sync(0xffffffffu, lane < warp ? above_of : 0u);
+    equal = __reduce_add_sync(0xffffffffu, lane < warp ? equal_of : 0u);
     if (active > 1) {
-        uint32_t above = again ? 0 : mine >> 16, equal = again ? 0 : mine & 0xffffu;
-        for (int c = 0; again && c < chunks; ++c) {
-            if (chunks > 1) {
-                load(c, nullptr);
-                __syncthreads();
-            }
-            const uint32_t x = count();
-            above += x >> 16;
-            equal += x & 0xffffu;
-        }
-        above = __reduce_add_sync(0xffffffffu, above);
-        equal = __reduce_add_sync(0xffffffffu, equal);
-        if (lane == 0) {
-            sm.scan[warp] = above;
-            sm.scan2[warp] = equal;
-        }
-        __syncthreads();
         if (warp == 0) {
-            above = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm.scan[lane] : 0u);
-            equal = __reduce_add_sync(0xffffffffu, lane < kWarps ? sm.scan2[lane] : 0u);
+            const uint32_t x = __reduce_add_sync(0xffffffffu, above_of), y = __reduce_add_sync(0xffffffffu, equal_of);
             if (lane == 0) {
-                sm.above = above;
-                sm.equal = equal;
+                sm.above = x;
+                sm.equal = y;
             }
         }
         cluster_arrive();
@@ -329,68 +303,45 @@ __global__ void __launch_bounds__(kThreads, 1536 / kThreads) kv_select_kernel(co
             x = cluster_load_u32(cluster_addr(&sm.above, lane));
             y = cluster_load_u32(cluster_addr(&sm.equal, lane));
         }
-        na = __reduce_add_sync(0xffffffffu, x);
-        ne = __reduce_add_sync(0xffffffffu, y);
+        above += __reduce_add_sync(0xffffffffu, x);
+        equal += __reduce_add_sync(0xffffffffu, y);
         cluster_arrive();  // (waited for at the end: the others read this CTA's counts)
     }
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-        if (chunks > 1) load(c, nullptr);
-        __syncthreads();
-        if (again) mine = count();
-        const uint32_t before = block_before<kThreads>(sm.scan, mine, lane, warp);
-        uint32_t above = na + (before >> 16), equal = ne + (before & 0xffffu);
-        const int i0 = min(m, tid * run), i1 = min(m, i0 + run);
-        const int32_t first_token = a.first + lo + c0;
-#pragma unroll 1
-        for (int i = i0; i < i1; i += kLoads) {
-            uint32_t key[kLoads];
-#pragma unroll
-            for (int k = 0; k < kLoads; ++k) key[k] = sm.keys[i + k];
-#pragma unroll
-            for (int k = 0; k < kLoads; ++k) {
-                const uint32_t in = i + k < i1, more = in & (key[k] > prefix), same = in & (key[k] == prefix);
-                store_if(more | (same & (equal < need)), keep + a.first + above + min(equal, need), first_token + i + k);
-                above += more;
-                equal += same;
-            }
-        }
-        if (chunks > 1) {
-            if (tid == kThreads - 1) {
-                sm.scan2[0] = above;
-                sm.scan2[1] = equal;
-            }
-            __syncthreads();
-            na = sm.scan2[0];
-            ne = sm.scan2[1];
-        }
-    }
+    keep += a.first;
+    candidates([&](uint32_t key, int i, bool in) {
+        const bool more = in && key > prefix, same = in && key == prefix;
+        const uint32_t mores = __ballot_sync(0xffffffffu, more), sames = __ballot_sync(0xffffffffu, same);
+        const uint32_t equals = equal + __popc(sames & before_me);
+        if (more || (same && equals < need)) keep[above + __popc(mores & before_me) + min(equals, need)] = a.first + i;
+        above += __popc(mores);
+        equal += __popc(sames);
+    });
     if (active > 1) cluster_wait();
 }
 
-template <int kThreads>
 cudaError_t launch(const KvSelectArgs& a, int cluster, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
-    constexpr size_t kMost = sizeof(Smem) + (kChunkKeys + kThreads * kLoads) * sizeof(uint32_t);
-    static_assert(kMost <= 232448, "over the 227 KB shared-memory limit of a CTA");
+    constexpr size_t kMost = sizeof(Smem) + kWarps * kMostListed * sizeof(uint2);
+    static_assert(kMost <= 115712, "two CTAs per SM");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&kv_select_kernel<kThreads>), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&kv_select_kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
         if (e != cudaSuccess) {
             (void)cudaGetLastError();
             return e;
         }
         done.fetch_or(bit, std::memory_order_acq_rel);
     }
-    long long part = (a.w_stride + cluster - 1) / cluster;
-    if (part < kLeastPart) part = kLeastPart;
-    if (part > kChunkKeys) part = kChunkKeys;
-    part += kThreads * kLoads;  // written or read past the last key, and not used
-    return launch_pdl_cluster(kv_select_kernel<kThreads>, dim3((unsigned)((long long)a.batch * a.num_kv_heads * cluster)), dim3(kThreads),
-                              sizeof(Smem) + (size_t)part * sizeof(uint32_t), cluster, s, a, cluster);
+    long long room = (a.w_stride + cluster - 1) / cluster;  // a warp's tokens of the longest part
+    if (room < kLeastPart) room = kLeastPart;
+    room = ((room + kWarps - 1) / kWarps + 31) / 32 * 32;
+    if (room > kMostListed) room = kMostListed;
+    const size_t smem = sizeof(Smem) + kWarps * (size_t)room * sizeof(uint2);
+    return launch_pdl_cluster(kv_select_kernel, dim3((unsigned)((long long)a.batch * a.num_kv_heads * cluster)), dim3(kThreads), smem,
+                              cluster, s, a, cluster, (int)room, a.w_stride > kShort);
 }
 
 }  // namespace
@@ -400,7 +351,7 @@ cudaError_t launch_kv_select(const KvSelectArgs& a, cudaStream_t s) {
     const long long rows = (long long)a.batch * a.num_kv_heads, sms = tile_default_ctas();
     int cluster = 1;
     while (cluster < kMaxCluster && rows * cluster * 2 <= sms && a.w_stride > (long long)kLeastPart * cluster) cluster *= 2;
-    return a.w_stride > 8192 ? launch<1024>(a, cluster, s) : launch<512>(a, cluster, s);
+    return launch(a, cluster, s);
 }
 
 }  // namespace hpc

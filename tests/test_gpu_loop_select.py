@@ -101,3 +101,27 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     want, wl = _loop.select(w2, [100, 2999], 256, 4, 64)
     assert torch.equal(keep.cpu(), want) and torch.equal(kl.cpu(), wl)
+
+
+@pytest.mark.parametrize("B, hkv, n, budget", [(1, 1, 60000, 55000), (2, 8, 30000, 20000), (20, 8, 20000, 18000), (200, 1, 11000, 10800)])
+@pytest.mark.parametrize("kind", ["plain", "ties", "wild"])
+def test_more_stay_than_a_list_holds(B, hkv, n, budget, kind):
+    lens = [n - 13 * b for b in range(B)]
+    assert check(weights(B, hkv, n, n + 1, kind), lens, budget, 4, 30) == 0
+
+
+@pytest.mark.parametrize("B, n", [(1, 50000), (3, 300), (170, 9000)])
+@pytest.mark.parametrize("share", [0.3, 0.7, 0.95])
+def test_down_to_infinities_and_undefined_values(B, n, share):
+    """The budget reaches -infinity, or NaN of either sign."""
+    w = weights(B, 2, n, 17, "plain").cpu()
+    gen = torch.Generator().manual_seed(18)
+    pick = torch.rand(w.shape, generator=gen)
+    bits = w.view(torch.int32)
+    bits[pick < 0.9] = 0x7fc00000
+    bits[pick < 0.6] = 0x7f800001
+    bits[pick < 0.5] = -0x00000001  # 0xffffffff
+    bits[pick < 0.4] = -0x007fffff  # 0xff800001
+    w[pick < 0.3] = -float("inf")
+    assert torch.isnan(w).float().mean() > 0.5
+    assert check(w.cuda(), [n - b for b in range(B)], int(share * n), 2, 5) == 0
