@@ -17,7 +17,7 @@
 // that warp alone goes through its part again, 2048 entries at a time in shared memory.
 //
 // The rows' bytes are the floor (256 requests of 131072 entries in 32 bits, target and draft:
-// 268 MB, 40 us at the rate of a copy); 52 us is what it takes, 5.1 TB/s. Without the
+// 268 MB, 40 us at the rate of a copy); 50-52 us is what it takes, 5.3 TB/s. Without the
 // search it takes 47: a request begins with three round trips in a row (count, drafted token,
 // its probabilities) and ends with two more, which the SM's other CTAs cover in part.
 #include "loop.cuh"
