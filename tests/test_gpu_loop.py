@@ -201,3 +201,43 @@ def test_limits():
     hpc.hpc_attn_weights(q, c["k_cache"], c["tables"][0], _tiles.i32([200]), torch.full((2, 8), -math.inf, device="cuda"), w,
                          q_starts=_tiles.i32([0, 2]), decay=0.25)
     assert (w[0, 0, :198] == 0.25).all() and (w[0, 0, 198:200] == 0).all() and (w[0, 0, 200:] == 1).all()
+
+
+def test_calls_at_once():
+    """The operators on two streams, over and over, beside one another: each gives what it gives alone."""
+    def problem(seed):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        lens = [3000 - 700 * seed, 129, 2000, 40 + seed]
+        c = _tiles.make_cache([lens], 2, "bf16", seed)
+        q = _tiles.make_q((4, 16, 128), seed + 9)
+        lse = 3.0 + torch.rand((4, 16), generator=gen, device="cuda")
+        width = c["tables"][0].shape[1] * 64
+        p = torch.softmax(2.0 * torch.randn((4, 3, 9001), generator=gen, device="cuda"), -1)
+        d = torch.randint(0, 9001, (4, 2), generator=gen, device="cuda", dtype=torch.int32)
+        u, us = torch.rand((4, 2), generator=gen, device="cuda"), torch.rand(4, generator=gen, device="cuda")
+        sl, w = _tiles.i32(lens), torch.empty((4, 2, width), device="cuda")
+
+        def run(stream):
+            w.zero_()
+            hpc.hpc_attn_weights(q, c["k_cache"], c["tables"][0], sl, lse, w, stream=stream)
+            keep, kl = hpc.hpc_kv_select(w, sl, 500, 4, 32, stream=stream)
+            acc, tok = hpc.hpc_verify_drafts(p, d, u, us, stream=stream)
+            return [w.clone(), keep, kl, acc, tok]
+        return run
+    runs = [problem(0), problem(1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = []
+    for run, s in zip(runs, streams):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            want.append(run(s))
+        torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for _ in range(3):
+            for run, s in zip(runs, streams):
+                with torch.cuda.stream(s):
+                    got.append(run(s))
+        torch.cuda.synchronize()
+        for i, g in enumerate(got):
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))

@@ -125,3 +125,10 @@ def test_down_to_infinities_and_undefined_values(B, n, share):
     w[pick < 0.3] = -float("inf")
     assert torch.isnan(w).float().mean() > 0.5
     assert check(w.cuda(), [n - b for b in range(B)], int(share * n), 2, 5) == 0
+
+
+@pytest.mark.parametrize("lens", [[70000, 100, 9000], [0, 70000], [5000, 4200, 4097, 1, 8000, 4096, 70000, 30000]])
+def test_short_rows_beside_long_ones(lens):
+    """Clusters of which a row uses all CTAs, some, or one; and rows that need none."""
+    for budget, first, recent in ((64, 4, 32), (4096, 0, 0), (1, 0, 1), (100, 50, 50)):
+        assert check(weights(len(lens), 2, 70001, budget, "ties"), lens, budget, first, recent) == 0

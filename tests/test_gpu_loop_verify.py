@@ -160,3 +160,29 @@ def test_padded_rows_streams_and_graphs():
     torch.cuda.synchronize()
     wa, wt = _loop.verify(*t2)
     assert torch.equal(acc.cpu(), wa) and torch.equal(tok.cpu(), wt)
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B, V, pad", [(1, 600000, 0), (2, 700001, 0), (300, 150000, 0), (3, 500000, 3), (260, 140001, 5)])
+def test_parts_longer_than_a_piece(B, V, pad, kind):
+    """A warp's part of the vocabulary in several pieces: dense rows, weight in few places, and rows that are zero but for
+    a stretch; rows that begin off 16 bytes."""
+    gen = torch.Generator(device="cuda").manual_seed(V + pad)
+    target = torch.zeros((B, 2, V + pad), device="cuda", dtype=kind)[:, :, :V]
+    draft = torch.zeros((B, 1, V + 2 * pad), device="cuda", dtype=kind)[:, :, :V]
+    drafted = torch.randint(0, V, (B, 1), generator=gen, device="cuda", dtype=torch.int32)
+    accept = torch.rand((B, 1), generator=gen, device="cuda")
+    for step in range(3):
+        for x in (target, draft):
+            if step == 0:
+                x.copy_(torch.rand(x.shape, generator=gen, device="cuda") / V)
+            elif step == 1:
+                x.zero_()
+                x.scatter_(2, torch.randint(0, V, (*x.shape[:2], 40), generator=gen, device="cuda"), 0.025)
+            else:
+                x.zero_()
+                x[:, :, V // 3:V // 3 + 5000] = torch.rand((*x.shape[:2], 5000), generator=gen, device="cuda").to(kind)
+        for u in (None, 0.0, 1.0 - 2.0 ** -24, 1.0):
+            sample = torch.rand(B, generator=gen, device="cuda") if u is None else torch.full((B,), u, device="cuda")
+            check(target, draft, drafted, accept, sample)
+            check(target, None, drafted, accept, sample)
