@@ -258,10 +258,14 @@ __device__ __forceinline__ void tma_load_3d_nohint(void* dst, const CUtensorMap*
         : "memory");
 }
 
-// Every lane's wait has to succeed: a warp goes on, or gives up, as one.
+// A warp goes on, or gives up, as one: its lanes test the barrier together, without a branch of their own.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    const bool ok = wait_bounded(bar, parity, abort_flag, kWaitLimitNs);
-    return __all_sync(0xffffffffu, ok);
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((it & 15) == 0 && __any_sync(0xffffffffu, *abort_flag != 0 || global_timer_ns() - t0 > kWaitLimitNs)) return false;
+    }
 }
 
 // 32 lanes from the warp's base lane x N consecutive columns: register k of thread t is
