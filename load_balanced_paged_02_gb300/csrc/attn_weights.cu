@@ -32,13 +32,14 @@
 // tokens: 86 us with 4, 88 with none).
 //
 // What it measured, bf16 unless said, 8 KV heads, lengths log-uniform: 64 sequences of one row,
-// up to 65536 tokens, 277 us, 6.6 TB/s: HBM. 48 of four rows over e4m3, 127 us, 5.7 TB/s: an
-// e4m3 tile takes 0.45 us of an SM, and the small loads (scales, weights, page ids) wait behind the
-// key stream. 10 of 32 rows, up to 32768 tokens, 95 us, 3.7 TB/s and 920 TFLOP/s: issue
-// slots 56 % busy, exp2 42 %, the tensor core 42 % (a product of 64 columns takes 48
-// clocks for its operands' bytes, where its arithmetic takes 34), each waiting on the next. Two slots in one product of
-// 128 columns: 94 us for it, but 317 in place of 295 where passes of 32 and of 4 rows alternate,
-// as the two groups then wait for one another.
+// up to 65536 tokens, 277 us, 6.6 TB/s: HBM. 48 of four rows over e4m3, 121 us, 6.0 TB/s:
+// an issuer takes 880 clocks for a tile's waits, products and commits beside the summing warps, and the
+// keys come once in 800 (as fast with 6 stages as with 11). 10 of 32 rows, up to 32768 tokens,
+// 93 us, 3.8 TB/s and 940 TFLOP/s: issue slots 55 % busy, exp2 42 %, the tensor core 42 % (a product of 64
+// columns takes 48 clocks for its operands' bytes, where its arithmetic takes 34). The products alone would
+// take 85, the sums alone 87, neither 64. Two slots in one product of 128 columns: 91 us, but rows of 4
+// or 16 then take 3 to 5 % more; an issuer per group: registers for 22 warps are too few; half a slot's scores on
+// their way while the other half is summed: as before.
 // Every wait is bounded (2 s); on expiry the CTA reports HPC_DEVERR_WAIT_TIMEOUT, gives
 // copies and MMAs in flight time to end, frees its TMEM and returns.
 #include <atomic>
