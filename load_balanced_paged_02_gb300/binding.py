@@ -508,7 +508,7 @@ def _table(what, t, rows):
 
 
 def _tensor(what, t, shape, dtype):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise HpcError(what, detail=f"must be a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
@@ -1067,7 +1067,7 @@ def hpc_kv_compact(k_cache, v_cache, page_table, keep, keep_lens, new_table, k_s
 
 def _prob_rows(what, t, batch, rows, vocab, dtype):
     """The distance in elements between rows of t [batch, rows, vocab], which must be the same from row to row."""
-    if t.dtype != dtype or tuple(t.shape) != (batch, rows, vocab):
+    if t.dtype != dtype or t.shape != (batch, rows, vocab):
         raise HpcError(what, detail=f"must be a {dtype} tensor of shape {(batch, rows, vocab)}")
     if t.is_contiguous():
         return vocab
@@ -1102,9 +1102,14 @@ def hpc_verify_drafts(target_probs, draft_tokens, accept_rand, sample_rand, draf
         d_row = _prob_rows("draft_probs", draft_probs, B, n, V, target_probs.dtype)
     _tensor("accept_rand", accept_rand, (B, n), torch.float32)
     _tensor("sample_rand", sample_rand, (B,), torch.float32)
-    for t, name in ((draft_counts, "draft_counts"), (num_accepted, "num_accepted"), (seq_lens, "seq_lens"), (kept_lens, "kept_lens")):
-        if t is not None:
-            _i32(name, t, B)
+    if draft_counts is not None:
+        _i32("draft_counts", draft_counts, B)
+    if num_accepted is not None:
+        _i32("num_accepted", num_accepted, B)
+    if seq_lens is not None:
+        _i32("seq_lens", seq_lens, B)
+    if kept_lens is not None:
+        _i32("kept_lens", kept_lens, B)
     if tokens is not None:
         _tensor("tokens", tokens, (B, n + 1), torch.int32)
     if kept_lens is not None and seq_lens is None:
