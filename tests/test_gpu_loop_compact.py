@@ -139,3 +139,30 @@ def test_graph_and_stream():
         torch.cuda.synchronize()
         for n in names:
             assert torch.equal(bits(c[n]), want[n])
+
+
+def test_far_pages():
+    """Pages whose rows lie beyond 2^31 elements (and 2^32 bytes) of the cache, read and written; weights in rows as far apart."""
+    pages, hkv, lens, kept = 140000, 2, [300, 70], [130, 65]
+    c = make(lens, kept, hkv, "bf16", 61)
+    k, v = (torch.zeros((pages, 64, hkv, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    far = [torch.where(t >= 0, pages - 1 - t, t).contiguous() for t in c["tables"]]
+    for b, n in enumerate(lens):
+        for j in range(-(-n // 64)):
+            k[far[0][b, j]] = c["k_cache"][c["tables"][0][b, j]]
+            v[far[0][b, j]] = c["v_cache"][c["tables"][0][b, j]]
+    w = torch.empty((2, hkv, 700_000_000), device="cuda")
+    near = torch.rand((2, hkv, 320), device="cuda")
+    w[:, :, :320] = near
+    out = torch.empty((2, hkv, 700_000_000), device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    hb.hpc_kv_compact(k, v, far[0], c["keep"], c["kept"], far[1], weights=w, weights_out=out, error_word=word)
+    assert int(word.item()) == 0
+    for b, m in enumerate(kept):
+        j = torch.arange(m, device="cuda")
+        for h in range(hkv):
+            t = c["keep"][b, h, :m].long()
+            old, new = c["tables"][0][b].long()[t // 64], far[1][b].long()[j // 64]
+            assert torch.equal(k[new, j % 64, h], c["k_cache"][old, t % 64, h])
+            assert torch.equal(v[new, j % 64, h], c["v_cache"][old, t % 64, h])
+            assert torch.equal(out[b, h, :m], near[b, h, t])

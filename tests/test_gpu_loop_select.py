@@ -132,3 +132,14 @@ def test_short_rows_beside_long_ones(lens):
     """Clusters of which a row uses all CTAs, some, or one; and rows that need none."""
     for budget, first, recent in ((64, 4, 32), (4096, 0, 0), (1, 0, 1), (100, 50, 50)):
         assert check(weights(len(lens), 2, 70001, budget, "ties"), lens, budget, first, recent) == 0
+
+
+def test_rows_far_apart():
+    """Rows that begin beyond 2^31 elements of the weights, at the longest distance that the call takes."""
+    far = torch.empty((3, 1, 1 << 30), device="cuda")
+    near = weights(3, 1, 5000, 21, "ties")
+    far[:, :, :5000] = near
+    lens = [5000, 160, 4097]
+    keep, kl, word = run(far, lens, 160, 4, 32)
+    want, wl = _loop.select(near, lens, 160, 4, 32)
+    assert word == 0 and torch.equal(kl, wl) and torch.equal(keep, want)

@@ -186,3 +186,16 @@ def test_parts_longer_than_a_piece(B, V, pad, kind):
             sample = torch.rand(B, generator=gen, device="cuda") if u is None else torch.full((B,), u, device="cuda")
             check(target, draft, drafted, accept, sample)
             check(target, None, drafted, accept, sample)
+
+
+def test_rows_beyond_32_bits():
+    """Probabilities whose last rows begin beyond 2^31 elements."""
+    B, n, V = 3, 2, 3001
+    target, draft, drafted, accept, sample = make(B, n, V, torch.bfloat16, 23)
+    wide = 300_000_000
+    t = torch.empty((B, n + 1, wide), dtype=torch.bfloat16, device="cuda")[:, :, :V]
+    d = torch.empty((B, n, wide + 8), dtype=torch.bfloat16, device="cuda")[:, :, :V]
+    t.copy_(target)
+    d.copy_(draft)
+    for u in (0.0, 0.5, 1.0):
+        check(t, d, drafted, torch.full_like(accept, u), sample)
