@@ -446,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
 template <int kThreads, bool BF16>
 cudaError_t launch(const VerifyArgs& a, int cluster, cudaStream_t s) {
     static std::atomic<unsigned long long> done{0};
-    constexpr size_t kSmem = sizeof(uint4) * kAhead * 2 * kThreads;
-    static_assert(kSmem >= 2 * Desk<BF16>::kBytes, "the desk takes the ring's place");
+    constexpr size_t kRing = sizeof(uint4) * kAhead * 2 * kThreads, kDesk = 2 * Desk<BF16>::kBytes;  // one in the other's place
+    constexpr size_t kSmem = kRing > kDesk ? kRing : kDesk;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -465,17 +465,23 @@ cudaError_t launch(const VerifyArgs& a, int cluster, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs per request: more of them until there are four per SM, what an SM takes of 256 threads.
-// CTAs of 512 threads while a request's eight leave an SM two or fewer, of 256 from there on.
-// us for 131072 entries with the draft's, 512 / 256 threads: 1 request 11.1 / 12.6, 32
-// 13.7 / 13.4, 256 72.7 / 55; 128 requests of 100003 entries 39.8 / 29.0. Until there are two, four
-// or eight CTAs per SM: 256 requests 59.7, 53.3, 54.6, 128 of 100003 27.1, 29.3, 28.9.
-cudaError_t launch_verify(const VerifyArgs& a, bool bf16, cudaStream_t s) {
-    const long long sms = tile_default_ctas();
+template <int kThreads>
+cudaError_t launch_of(const VerifyArgs& a, bool bf16, long long sms, cudaStream_t s) {
     int cluster = 1;
-    while (cluster < kMaxCluster && a.batch * cluster < 4 * sms && a.vocab > 4096LL * cluster) cluster *= 2;
-    if (a.batch * kMaxCluster <= 2 * sms) return bf16 ? launch<512, true>(a, cluster, s) : launch<512, false>(a, cluster, s);
-    return bf16 ? launch<256, true>(a, cluster, s) : launch<256, false>(a, cluster, s);
+    while (cluster < kMaxCluster && a.batch * cluster < 1024 / kThreads * sms && a.vocab > 4096LL * cluster) cluster *= 2;
+    return bf16 ? launch<kThreads, true>(a, cluster, s) : launch<kThreads, false>(a, cluster, s);
+}
+
+// CTAs per request: more of them until the SMs have as many as they take, 1024 threads each. Of
+// 512 threads while a request's eight leave an SM two or fewer, of 256 up to four, of 128 from there on.
+// us for 131072 entries with the draft's, 512 / 256 / 128 threads: 1 request 11.1 / 12.6 / 12.1, 40
+// in float32 - / 14.9 / 16.9, 100 in bf16 - / 21.8 / 19.5, 256 72.7 / 53.7 / 53.4, 512 in bf16 - / 62.1 / 59.1;
+// 128 requests of 100003 entries 39.8 / 28.8 / 26.6. Half as many CTAs of 128 threads: 256 requests 57.
+cudaError_t launch_verify(const VerifyArgs& a, bool bf16, cudaStream_t s) {
+    const long long sms = tile_default_ctas(), most = (long long)a.batch * kMaxCluster;
+    if (most <= 2 * sms) return launch_of<512>(a, bf16, sms, s);
+    if (most <= 4 * sms) return launch_of<256>(a, bf16, sms, s);
+    return launch_of<128>(a, bf16, sms, s);
 }
 
 }  // namespace hpc
