@@ -388,60 +388,12 @@ __global__ void __maxnreg__(168)
                 ok = wait_bounded(&qfull[qs], (qd >> 1) & 1, abort_flag, kWaitLimitNs);
                 if (!ok) break;
                 uint8_t* qt = qbuf + qs * kQTile;
-                // Lane pair (2 j, 2 j + 1) takes query row r = j + 16 u, u < 4; half hh
-                // = lane & 1 reads bf16 dims [64 hh, 64 hh + 64), which sit where row r
-                // of the hi tile (hh = 0) or of the lo tile (hh = 1) goes; each lane
-                // writes the hi and lo codes of its dims once both lanes have read.
+                // lane pair (2 j, 2 j + 1) takes query row r = j + 16 u, u < 4
 #pragma unroll 1
                 for (int u = 0; u < 4; ++u) {
                     const int r = (lane >> 1) + 16 * u, hh = lane & 1;
-                    const bool in = r < kGroup * Q;
-                    uint4 raw[8];
-                    float amax = 0.f;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        raw[c] = in ? *reinterpret_cast<const uint4*>(qt + hh * 8192 + r * 128 + ((c ^ (r & 7)) << 4))
-                                    : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)),
-                                                     fabsf(__uint_as_float(w[j] & 0xffff0000u))));
-                    }
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                    __syncwarp();  // the partner lane has read its half row
-                    // the smallest power of two 2^ex with amax / 2^ex <= 448: q / 2^ex is exact
-                    float qscale = 1.f, qinv = 1.f;
-                    if (amax > 0.f && amax <= 3.0e38f) {
-                        int e;
-                        const float m = frexpf(amax * (1.f / 448.f), &e);
-                        const int ex = m == 0.5f ? e - 1 : e;
-                        qscale = ldexpf(1.f, ex);
-                        qinv = ldexpf(1.f, -ex);
-                    }
+                    const float qscale = split_query_row(qt, r, hh, r < kGroup * Q, true);
                     if (hh == 0) qsc[qs * 64 + r] = qscale;
-#pragma unroll
-                    for (int c2 = 0; c2 < 4; ++c2) {
-                        // bf16 pieces c = 2 c2 + v (dims 64 hh + 8 c ...) -> bytes 8 v of the
-                        // e4m3 row's 16-byte piece 4 hh + c2
-                        uint2 hp[2], lp[2];
-#pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            const uint4 x4 = raw[2 * c2 + v];
-                            const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
-                            float x[8];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                x[2 * j] = __uint_as_float(w[j] << 16) * qinv;
-                                x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * qinv;
-                            }
-                            split_e4m3x8(x, hp[v], lp[v]);
-                        }
-                        const int off = r * 128 + (((4 * hh + c2) ^ (r & 7)) << 4);
-                        *reinterpret_cast<uint4*>(qt + off) = make_uint4(hp[0].x, hp[0].y, hp[1].x, hp[1].y);
-                        *reinterpret_cast<uint4*>(qt + 8192 + off) = make_uint4(lp[0].x, lp[0].y, lp[1].x, lp[1].y);
-                    }
-                    __syncwarp();
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&q8full[qs]);

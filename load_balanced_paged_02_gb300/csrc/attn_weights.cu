@@ -379,55 +379,6 @@ __device__ __forceinline__ void slot_rows(uint32_t ta, int rows, int sees, const
     }
 }
 
-// A row of bf16 queries in shared memory, as TMA left it ([2 dim halves][64 rows][128 B], swizzled),
-// into hi and lo e4m3 codes in its place, by two lanes; returns its scale. `in`: there is such a row.
-__device__ __forceinline__ float split_row(uint8_t* slot, int r, int hh, bool in) {
-    uint4 raw[8];
-    float amax = 0.f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        raw[c] = in ? *reinterpret_cast<const uint4*>(slot + hh * kSlotHalf + r * 128 + ((c ^ (r & 7)) << 4)) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
-    }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    __syncwarp();  // the partner lane has read its half row
-    // the smallest power of two 2^ex with amax / 2^ex <= 448: q / 2^ex is exact
-    float up = 1.f, down = 1.f;
-    if (amax > 0.f && amax <= 3.0e38f) {
-        int e;
-        const float m = frexpf(amax * (1.f / 448.f), &e);
-        const int ex = m == 0.5f ? e - 1 : e;
-        up = ldexpf(1.f, ex);
-        down = ldexpf(1.f, -ex);
-    }
-#pragma unroll
-    for (int c2 = 0; c2 < 4; ++c2) {
-        uint2 hp[2], lp[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint4 x4 = raw[2 * c2 + u];
-            const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y[2 * j] = __uint_as_float(w[j] << 16) * down;
-                y[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * down;
-            }
-            split_e4m3x8(y, hp[u], lp[u]);
-        }
-        if (in) {
-            const int off = r * 128 + (((4 * hh + c2) ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(slot + off) = make_uint4(hp[0].x, hp[0].y, hp[1].x, hp[1].y);
-            *reinterpret_cast<uint4*>(slot + kSlotHalf + off) = make_uint4(lp[0].x, lp[0].y, lp[1].x, lp[1].y);
-        }
-    }
-    __syncwarp();
-    return up;
-}
-
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q1,
@@ -740,8 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     for (int c0 = 0; c0 < rows * kGroup; c0 += 16) {
                         const int c = c0 + (lane >> 1);
-                        const float up = split_row(slot, c, lane & 1, c < rows * kGroup);
-                        if (c < rows * kGroup && (lane & 1) == 0) qc[sl * kCols + c] = up * (kLog2e * 0.08838834764831845f);
+                        const bool in = c < rows * kGroup;
+                        const float up = split_query_row(slot, c, lane & 1, in, in);
+                        if (in && (lane & 1) == 0) qc[sl * kCols + c] = up * (kLog2e * 0.08838834764831845f);
                     }
                     fence_proxy_async_smem();
                 }

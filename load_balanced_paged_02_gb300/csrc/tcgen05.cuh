@@ -121,6 +121,71 @@ __device__ __forceinline__ void split_e4m3x8(const float (&x)[8], uint2& hi, uin
     lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
 }
 
+// The power of two 2^ex that a query row of largest magnitude amax is divided by before it is
+// split, the smallest with amax / 2^ex <= 448 = 1.75 2^8 (q / 2^ex is exact then), and its
+// inverse. Both stay finite: ex is -126 at least, where rows under 2^-117 begin to lose bits
+// (half a code's step of 2^-9, 2^-136 an element). An infinite element makes the row's scores
+// infinite or NaN.
+__device__ __forceinline__ void query_row_scale(float amax, float& scale, float& inverse) {
+    const uint32_t ab = __float_as_uint(amax);
+    const int ex = max((int)(ab >> 23) - 127 - 8 + ((ab & 0x7fffffu) > 0x600000u ? 1 : 0), -126);
+    scale = inverse = 1.f;
+    if (amax > 3.4e38f) {
+        scale = amax;
+    } else if (amax > 0.f) {
+        scale = __uint_as_float((uint32_t)(127 + ex) << 23);
+        inverse = __uint_as_float((uint32_t)(127 - ex) << 23);
+    }
+}
+
+// Row r of a tile of bf16 queries in shared memory ([2 dim halves][64 rows][128 B], swizzled)
+// into hi and lo e4m3 tiles ([64 rows][128 B] each) in its place, by two lanes: half hh reads
+// dims [64 hh, 64 hh + 64), which sit where row r of the hi tile (hh = 0) or of the lo tile
+// goes, and writes the hi and lo codes of its dims once both have read. A row that is not `in`
+// is zeros; `write` says whether codes are stored. Returns the row's scale.
+__device__ __forceinline__ float split_query_row(uint8_t* tile, int r, int hh, bool in, bool write) {
+    constexpr int kHalf = 64 * 128;
+    uint4 raw[8];
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        raw[c] = in ? *reinterpret_cast<const uint4*>(tile + hh * kHalf + r * 128 + ((c ^ (r & 7)) << 4)) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    __syncwarp();  // the partner lane has read its half row
+    float scale, inverse;
+    query_row_scale(amax, scale, inverse);
+#pragma unroll
+    for (int c2 = 0; c2 < 4; ++c2) {
+        // bf16 pieces c = 2 c2 + u (dims 64 hh + 8 c ...) -> bytes 8 u of the e4m3 row's
+        // 16-byte piece 4 hh + c2
+        uint2 hp[2], lp[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint4 x4 = raw[2 * c2 + u];
+            const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[2 * j] = __uint_as_float(w[j] << 16) * inverse;
+                y[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u) * inverse;
+            }
+            split_e4m3x8(y, hp[u], lp[u]);
+        }
+        if (write) {
+            const int off = r * 128 + (((4 * hh + c2) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(tile + off) = make_uint4(hp[0].x, hp[0].y, hp[1].x, hp[1].y);
+            *reinterpret_cast<uint4*>(tile + kHalf + off) = make_uint4(lp[0].x, lp[0].y, lp[1].x, lp[1].y);
+        }
+    }
+    __syncwarp();
+    return scale;
+}
+
 __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
