@@ -79,8 +79,8 @@ struct Layout {
     static constexpr int kStageBytes = FP8 ? 16384 : 32768;
     static constexpr size_t kQ = (size_t)kStages * kStageBytes;
     static constexpr size_t kNl = kQ + kSlots * kSlotBytes;                   // float [slot][64]: -lse log2(e)
-    static constexpr size_t kQc = kNl + kSlots * kCols * 4;                   // e4m3: float [slot][64]: score factors
-    static constexpr size_t kScan = kQc + (FP8 ? kSlots * kCols * 4 : 0);     // int64 [warps]
+    static constexpr size_t kQc = kNl + kSlots * kCols * 4;                   // e4m3: float [2][slot][64]: score factors
+    static constexpr size_t kScan = kQc + (FP8 ? 2 * kSlots * kCols * 4 : 0); // int64 [warps]
     static constexpr size_t kBorder = kScan + kThreads / 32 * 8;              // Border [4]
     static constexpr size_t kRun = kBorder + 64;                              // int [8]
     static constexpr size_t kPass = kRun + 32;                                // Pass [kPasses]
@@ -693,7 +693,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int c = c0 + (lane >> 1);
                         const bool in = c < rows * kGroup;
                         const float up = split_query_row(slot, c, lane & 1, in, in);
-                        if (in && (lane & 1) == 0) qc[sl * kCols + c] = up * (kLog2e * 0.08838834764831845f);
+                        if (in && (lane & 1) == 0) {
+                            const float f = up * (kLog2e * 0.08838834764831845f);
+                            qc[sl * kCols + c] = f;
+                            qc[(kSlots + sl) * kCols + c] = up > 3.4e38f ? f : fminf(f * 0x1p64f, 3.4e38f);
+                        }
                     }
                     fence_proxy_async_smem();
                 }
@@ -775,9 +779,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             int j = v.j;
             for (; j < j1; j += v.step) {
                 const float now_old = first ? p.decay * old : old;
-                const uint64_t now_factor = pair(factor, factor);
                 const bool now_there = there;
                 const int t = j * kTile + mine;
+                // Sums of products, up to 2^25, times a scale from 2^103 on are beyond float32 even where a tiny query's
+                // score is not: such warps take 2^64 from the scales and give it to the rows' factors.
+                const bool large = FP8 && __any_sync(0xffffffffu, t < x.L && fabsf(factor) >= 0x1p100f);
+                const float now_scale = large ? factor * 0x1p-64f : factor;
+                const uint64_t now_factor = pair(now_scale, now_scale);
+                const float* qct = large ? qc + kSlots * kCols : qc;
                 float* to = v.weights + (long long)j * kTile;
                 const bool writes = t < v.write;
                 const int next = j + v.step;
@@ -805,9 +814,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int rows = min(kSlotRows, rows_all - s * kSlotRows);
                         const uint32_t ta = tmem + ((uint32_t)(32 * wq) << 16) + acc * kCols;
                         if (clear && rows == kSlotRows)
-                            slot_rows<FP8, false>(ta, kSlotRows, 0, nl + sl * kCols, qc + sl * kCols, now_factor, sum2);
+                            slot_rows<FP8, false>(ta, kSlotRows, 0, nl + sl * kCols, qct + sl * kCols, now_factor, sum2);
                         else  // row r of the slot sees the token from t - p0 - 8 s on
-                            slot_rows<FP8, true>(ta, rows, t - p0 - s * kSlotRows, nl + sl * kCols, qc + sl * kCols, now_factor, sum2);
+                            slot_rows<FP8, true>(ta, rows, t - p0 - s * kSlotRows, nl + sl * kCols, qct + sl * kCols, now_factor, sum2);
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&accfree[acc]);

@@ -58,6 +58,42 @@ def test_weights_of_small_rows(size, key, new):
     assert ((w.double() - want).abs() <= bound)[bound > 0].all()
 
 
+@pytest.mark.parametrize("new", [[1, 3], [8, 40]])
+@pytest.mark.parametrize("size, key", [(1e-36, 2.0 ** 120), (1e-30, 2.0 ** 100), (1e-37, 2.0 ** 122), (1e-34, 2.0 ** 112)])
+def test_weights_of_small_rows_and_large_keys(size, key, new):
+    """Scores of about one from numbers at the ends of float32's range, and a token of small keys among the large ones."""
+    lens = [200, 321]
+    c = cache(lens, 2, 5, key)
+    page, slot = int(c["tables"][0][1, 1]), 9
+    c["k_scale"][page, :, slot] = 2.0 ** -70
+    c["k"][0][1][64 + slot] = c["k_cache"][page, slot].float().double() * 2.0 ** -70
+    starts = _tiles.starts(new)
+    q = _tiles.make_q((starts[-1], 16, 128), 6, scale=size)
+    q[:, 1, 3:] = 0.0
+    w, want, bound = weights(c, q, starts, lens)
+    assert torch.isfinite(w).all()
+    assert ((w.double() - want).abs() <= bound)[bound > 0].all()
+
+
+def test_scales_behind_the_length():
+    """Large scales in unused slots change no bit."""
+    lens, starts = [200, 321], [0, 2, 12]
+    c = cache(lens, 1, 31, 2.0 ** -80)
+    q = (_tiles.make_q((12, 8, 128), 32).float() * 2.0 ** 80).to(torch.bfloat16)
+    w0, want, bound = weights(c, q, starts, lens)
+    assert ((w0.double() - want).abs() <= bound)[bound > 0].all()
+    lse = _loop.row_lse(q, starts, c["k"][0], lens)
+    out = []
+    for value in (1.0, 2.0 ** 120):
+        ks = c["k_scale"].clone()
+        for b, n in enumerate(lens):
+            ks[int(c["tables"][0][b, n // 64]), :, n % 64:] = value
+        w = torch.zeros_like(w0)
+        hb.hpc_attn_weights(q, c["k_cache"], c["tables"][0], _tiles.i32(lens), lse, w, q_starts=_tiles.i32(starts), k_scale=ks)
+        out.append(w)
+    assert torch.equal(out[0], out[1])
+
+
 def test_a_small_row_without_a_weight():
     """Log-sum-exps of -inf: no weight, whatever the row's size."""
     lens, starts = [200], [0, 2]
