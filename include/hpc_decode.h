@@ -880,9 +880,12 @@ typedef enum hpc_probs_dtype { HPC_PROBS_F32 = 0, HPC_PROBS_BF16 = 1 } hpc_probs
  *              tokens of the step, as hpc_decode_attn_multi takes them;
  *   kept_lens  device int32 [batch] or NULL: the lengths without the tokens that were not
  *              accepted, max(0, seq_lens[b] - num_drafts + r). It may be seq_lens itself.
- * Entries (and differences) that are not above 0 and below 2^64, NaN among them, count
- * as 0. Where nothing is left after a refusal the token is drawn from p_r; where that is
- * 0 everywhere, it is -1. A sample_rand of 1 or more gives the last entry above 0.
+ * Of entries that are no probabilities: a q whose sign is set counts as 0. An entry of p
+ * that is compared or drawn from, and a difference p - q that is drawn from, counts as 0
+ * unless it is above 0 and below 2^64 (another q that is NaN or infinite leaves its token
+ * nothing). A comparison with NaN refuses. Where nothing is left after a refusal the token
+ * is drawn from p_r; where that is 0 everywhere, it is -1. A sample_rand of 1 or more gives
+ * the last entry above 0.
  * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA.
  */
 hpc_status hpc_verify_drafts(const void* target_probs, long long target_stride, const void* draft_probs,

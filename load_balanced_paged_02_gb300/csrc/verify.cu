@@ -37,13 +37,23 @@ struct Pair {
     float s, e;
 };
 
-// The weight of an entry, exact as s + e: p, or p - q, where that is above 0 and below 2^64.
+// What of the draft's probability counts beside p >= 0: at most p, so that the difference is not
+// below 0; 0 where q's sign is set; p, which leaves nothing, where q is NaN or infinite. Floats
+// that are not negative have the order of their bits, so that this is one instruction.
+__device__ __forceinline__ float within(float q, float p) {
+    int32_t d;
+    asm("min.relu.s32 %0, %1, %2;" : "=r"(d) : "r"(__float_as_int(q)), "r"(__float_as_int(p)));
+    return __int_as_float(d);
+}
+
+// The weight of an entry, exact as s + e: p, or p - q, where that is below 2^64. As p' >= q' >= 0
+// the difference's error is (p' - s) - q'.
 __device__ __forceinline__ Pair entry(float p, float q, bool both) {
-    if (!both) q = 0.f;
+    p = fmaxf(p, 0.f);  // (the number where p is NaN)
+    q = both ? within(q, p) : 0.f;
     const float s = p - q;
-    const float bb = s - p;
-    const float e = (p - (s - bb)) - (q + bb);
-    const bool ok = s > 0.f && s < kMost;
+    const float e = (p - s) - q;
+    const bool ok = s < kMost;
     return Pair{ok ? s : 0.f, ok ? e : 0.f};
 }
 
@@ -109,15 +119,13 @@ __device__ __forceinline__ void add(Pair2& a, uint64_t s) {  // e is left alone 
     a.s = t;
 }
 
-// Two entries whose values lie in [0, 2^64) or are below 0 or NaN (larger ones make the sum
-// too large, which the caller sees). With q' = min(q, p), p' = max(p, 0) (either takes the
-// number where the other is NaN) p' >= q', so that the difference's error is (p' - s) - q'.
+// Two entries; a weight from 2^64 on makes the sum too large, which the caller sees.
 template <bool BOTH>
 __device__ __forceinline__ void add_entries(Pair2& acc, float p0, float p1, float q0, float q1) {
     p0 = fmaxf(p0, 0.f);
     p1 = fmaxf(p1, 0.f);
     if constexpr (BOTH) {
-        const uint64_t p = pack(p0, p1), q = pack(fminf(q0, p0), fminf(q1, p1));
+        const uint64_t p = pack(p0, p1), q = pack(within(q0, p0), within(q1, p1));
         const uint64_t s = sub2(p, q);
         acc.e = add2(acc.e, sub2(sub2(p, s), q));
         add(acc, s);
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
             if ((unsigned)d < (unsigned)a.vocab) {
                 const float p = load<BF16>(a.target, (b * (a.drafts + 1) + lane) * a.target_stride + d);
                 const float q = a.draft ? load<BF16>(a.draft, (b * a.drafts + lane) * a.draft_stride + d) : 1.f;
-                yes = (double)a.accept_rand[b * a.drafts + lane] * (double)q < (double)p;
+                yes = (double)a.accept_rand[b * a.drafts + lane] * (double)(signbit(q) ? 0.f : q) < (double)p && p < kMost;
             } else if (rank == 0 && a.err) {
                 atomicOr(a.err, (int)HPC_DEVERR_BAD_TOKEN);
             }
