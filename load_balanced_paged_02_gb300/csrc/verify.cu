@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
             if (lane > r && lane <= a.drafts) a.tokens[b * (a.drafts + 1) + lane] = -1;
             if (lane == 0) {
                 a.accepted[b] = r;
-                if (a.kept_lens) a.kept_lens[b] = max(0, a.seq_lens[b] - (a.drafts - r));
+                if (a.kept_lens) a.kept_lens[b] = max(0, max(0, a.seq_lens[b]) - (a.drafts - r));
             }
         }
     }
