@@ -819,7 +819,7 @@ hpc_status hpc_attn_weights(const void* q, const void* k_cache, const float* k_s
  *   d_error_word  device int32 or NULL: a length beyond weights_stride counts as that
  *              (HPC_DEVERR_PAGE_OUT_OF_RANGE), a negative one as 0
  *              (HPC_DEVERR_NEGATIVE_LENGTH)
- * num_first + num_recent <= budget <= 2^30; keep_lens is another array than seq_lens.
+ * num_first + num_recent <= budget <= 2^30; keep, keep_lens and seq_lens do not overlap.
  * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_CUDA.
  */
 hpc_status hpc_kv_select(const float* weights, long long weights_stride, const int32_t* seq_lens, int batch,
@@ -873,13 +873,15 @@ typedef enum hpc_probs_dtype { HPC_PROBS_F32 = 0, HPC_PROBS_BF16 = 1 } hpc_probs
  *   draft_counts  device int32 [batch] or NULL (num_drafts each); outside [0, num_drafts]
  *              as the nearest
  *   accept_rand   device float32 [batch][num_drafts], sample_rand [batch]: uniform on [0, 1)
- *   num_accepted  device int32 [batch], another array than draft_counts
+ *   num_accepted  device int32 [batch]
  *   tokens     device int32 [batch][num_drafts + 1]: the accepted drafts, the next token,
  *              then -1
  *   seq_lens   device int32 [batch] or NULL, lengths that count all num_drafts + 1 new
  *              tokens of the step, as hpc_decode_attn_multi takes them;
  *   kept_lens  device int32 [batch] or NULL: the lengths without the tokens that were not
- *              accepted, max(0, seq_lens[b] - num_drafts + r). It may be seq_lens itself.
+ *              accepted, max(0, seq_lens[b] - num_drafts + r)
+ * The int32 outputs do not overlap one another nor draft_tokens, draft_counts and seq_lens;
+ * but kept_lens may be seq_lens itself, and one request's tokens its draft_tokens.
  * Of entries that are no probabilities: a q whose sign is set counts as 0. An entry of p
  * that is compared or drawn from, and a difference p - q that is drawn from, counts as 0
  * unless it is above 0 and below 2^64 (another q that is NaN or infinite leaves its token

@@ -16,6 +16,18 @@ inline hpc_status launched(cudaError_t e) {
     return e == cudaSuccess ? HPC_OK : HPC_ERR_CUDA;
 }
 
+// An int32 array of a call. What one block writes while another still reads it, or writes it
+// too, has no answer: such arrays must not overlap.
+struct Words {
+    const int32_t* p;
+    long long n;
+    bool overlaps(const Words& o) const {
+        if (!p || !o.p || n < 1 || o.n < 1) return false;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        return a < b ? b - a < (uintptr_t)n * 4 : a - b < (uintptr_t)o.n * 4;
+    }
+};
+
 bool batch_ok(int batch, int num_kv_heads) {
     return batch >= 1 && batch <= HPC_MAX_BATCH && num_kv_heads >= 1 && num_kv_heads <= HPC_MAX_KV_HEADS;
 }
@@ -81,8 +93,10 @@ hpc_status hpc_kv_select(const float* weights, long long weights_stride, const i
                          int* d_error_word, void* stream) {
     if (!batch_ok(batch, num_kv_heads) || !weights || !seq_lens || !keep || !keep_lens) return HPC_ERR_INVALID_ARG;
     if (weights_stride < 1 || weights_stride > (1LL << 30) || budget < 1 || budget > (1 << 30)) return HPC_ERR_INVALID_ARG;
-    if (keep_lens == seq_lens) return HPC_ERR_INVALID_ARG;  // (every head's CTAs read the lengths)
     if (num_first < 0 || num_recent < 0 || (long long)num_first + num_recent > budget) return HPC_ERR_INVALID_ARG;
+    // (every head's CTAs read the lengths)
+    const Words lens{seq_lens, batch}, kept{keep_lens, batch}, all{keep, (long long)batch * num_kv_heads * budget};
+    if (kept.overlaps(lens) || all.overlaps(lens) || all.overlaps(kept)) return HPC_ERR_INVALID_ARG;
     const KvSelectArgs a{weights, weights_stride, seq_lens, batch, num_kv_heads, budget, num_first, num_recent, keep, keep_lens,
                          d_error_word};
     return launched(launch_kv_select(a, static_cast<cudaStream_t>(stream)));
@@ -145,7 +159,16 @@ hpc_status hpc_verify_drafts(const void* target_probs, long long target_stride, 
         if (!draft_tokens || !accept_rand) return HPC_ERR_INVALID_ARG;
     }
     if (!sample_rand || !num_accepted || !tokens || (kept_lens && !seq_lens)) return HPC_ERR_INVALID_ARG;
-    if (num_accepted == draft_counts) return HPC_ERR_INVALID_ARG;  // (all of a request's CTAs read the count)
+    // All of a request's CTAs read its count and its drafts; its lengths the one that writes the new ones.
+    const Words drafted{draft_tokens, (long long)batch * num_drafts}, counts{draft_counts, batch}, lens{kept_lens ? seq_lens : nullptr, batch};
+    const Words acc{num_accepted, batch}, kept{kept_lens, batch}, out{tokens, (long long)batch * (num_drafts + 1)};
+    if (acc.overlaps(drafted) || acc.overlaps(counts) || acc.overlaps(lens) || acc.overlaps(kept) || acc.overlaps(out))
+        return HPC_ERR_INVALID_ARG;
+    if (kept.overlaps(drafted) || kept.overlaps(counts) || kept.overlaps(out) || (kept.overlaps(lens) && kept_lens != seq_lens))
+        return HPC_ERR_INVALID_ARG;
+    if (out.overlaps(counts) || out.overlaps(lens)) return HPC_ERR_INVALID_ARG;
+    // One request's tokens may take the place of its drafts: what is written there before they are read is what was there.
+    if (out.overlaps(drafted) && (batch > 1 || tokens != draft_tokens)) return HPC_ERR_INVALID_ARG;
     VerifyArgs a;
     a.target = target_probs;
     a.target_stride = target_stride;
