@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const KvSelectAr
         float x[kLoads];
         if (i + 32 * kLoads <= s1) {
 #pragma unroll
-            for (int k = 0; k < kLoads; ++k) x[k] = __ldg(at + i + 32 * k);
+            for (int k = 0; k < kLoads; ++k) x[k] = at[i + 32 * k];
             bool next;
 #pragma unroll 1
             do {
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const KvSelectAr
                 float y[kLoads];
                 if (next) {
 #pragma unroll
-                    for (int k = 0; k < kLoads; ++k) y[k] = __ldg(at + i + 32 * (kLoads + k));
+                    for (int k = 0; k < kLoads; ++k) y[k] = at[i + 32 * (kLoads + k)];
                 }
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k) f(x[k] + 0.f, i + 32 * k + lane, true);
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_select_kernel(const KvSelectAr
         if (i >= s1) return;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k)
-            if (i + 32 * k + lane < s1) x[k] = __ldg(at + i + 32 * k);
+            if (i + 32 * k + lane < s1) x[k] = at[i + 32 * k];
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
             if (i + 32 * k >= s1) break;
