@@ -98,6 +98,8 @@ __device__ __forceinline__ bool desc_ok(const Params& p, int h, int b, int c0, i
 // descriptor. Call next() right after copying the current fields, before the
 // descriptor's work. An entry past the current one is only read while the
 // current one is not the terminator, so every read stays inside the list.
+// Plain loads: the map is the kernel's before this one, which may still be
+// writing it when this kernel starts.
 // len and pg are 0 for an entry outside the call's shapes (desc_ok false).
 template <bool LEN, bool PAGES>
 struct TaskWalker {
@@ -108,15 +110,15 @@ struct TaskWalker {
     int slot;
 
     __device__ __forceinline__ static void fetch(const Params& p, int s, int4& a, int4& b) {
-        a = __ldg(reinterpret_cast<const int4*>(p.tasks + (long long)s * kTaskInts));
-        b = __ldg(reinterpret_cast<const int4*>(p.tasks + (long long)s * kTaskInts + 4));
+        a = *reinterpret_cast<const int4*>(p.tasks + (long long)s * kTaskInts);
+        b = *reinterpret_cast<const int4*>(p.tasks + (long long)s * kTaskInts + 4);
     }
     __device__ __forceinline__ void side(const Params& p, int lane) {
         len = 0;
         pg = 0;
         if ((LEN || PAGES) && t0.x >= 0 && desc_ok(p, t0.x, t0.y, t0.z, t0.w, t1.x)) {
-            if (LEN) len = __ldg(p.seq_lens + t0.y);
-            if (PAGES && t0.z + lane < t0.w) pg = __ldg(p.page_table + (long long)t0.y * p.pt_stride + t0.z + lane);
+            if (LEN) len = p.seq_lens[t0.y];
+            if (PAGES && t0.z + lane < t0.w) pg = p.page_table[(long long)t0.y * p.pt_stride + t0.z + lane];
         }
     }
     __device__ __forceinline__ void start(const Params& p, int list0, int lane) {
@@ -132,8 +134,8 @@ struct TaskWalker {
         ++slot;
         t0 = n0;
         t1 = n1;
-        side(p, lane);
         if (t0.x >= 0) fetch(p, slot + 1, n0, n1);
+        side(p, lane);
     }
 };
 
@@ -147,8 +149,8 @@ struct TaskAhead {
     int slot;
 
     __device__ __forceinline__ void fetch(const Params& p) {
-        t0 = __ldg(reinterpret_cast<const int4*>(p.tasks + (long long)slot * kTaskInts));
-        s = __ldg(p.tasks + (long long)slot * kTaskInts + 4);
+        t0 = *reinterpret_cast<const int4*>(p.tasks + (long long)slot * kTaskInts);
+        s = p.tasks[(long long)slot * kTaskInts + 4];
     }
     __device__ __forceinline__ void start(const Params& p, int list0) {
         slot = list0;
@@ -345,15 +347,15 @@ __device__ __forceinline__ void produce(const Params& p, const CUtensorMap* tm_k
         // contract and the map is not yet written (wrong values, no fault)
         const int l0 = p.cta_off[blockIdx.x];
         for (int slot = max(l0, 0); slot < p.max_tasks && npre < (uint32_t)STAGES; ++slot) {
-            const int4 t0 = __ldg(reinterpret_cast<const int4*>(p.tasks + (long long)slot * kTaskInts));
-            const int4 t1 = __ldg(reinterpret_cast<const int4*>(p.tasks + (long long)slot * kTaskInts + 4));
+            const int4 t0 = *reinterpret_cast<const int4*>(p.tasks + (long long)slot * kTaskInts);
+            const int4 t1 = *reinterpret_cast<const int4*>(p.tasks + (long long)slot * kTaskInts + 4);
             const int h = t0.x, b = t0.y, c0 = t0.z, c1 = t0.w;
             if (h < 0 || !desc_ok(p, h, b, c0, c1, t1.x)) break;
-            const int L = __ldg(p.seq_lens + b);
+            const int L = p.seq_lens[b];
             const int32_t* prow = p.page_table + (long long)b * p.pt_stride;
             bool stop = false;
             for (int cc = c0; cc < c1 && npre < (uint32_t)STAGES; ++cc) {
-                const int page = __ldg(prow + cc);
+                const int page = prow[cc];
                 if (kChunk * (cc + 1) > L - p.q_len || (unsigned)page >= (unsigned)p.num_pages) {
                     stop = true;
                     break;
@@ -431,7 +433,7 @@ __device__ __forceinline__ void produce(const Params& p, const CUtensorMap* tm_k
         const int32_t* prow = p.page_table + (long long)b * p.pt_stride;
         for (int cb = c0; cb < c1 && ok; cb += 32) {
             const int cl = cb + lane;
-            const int pg = cb == c0 ? pg0 : (cl < c1 ? __ldg(prow + cl) : 0);
+            const int pg = cb == c0 ? pg0 : (cl < c1 ? prow[cl] : 0);
             const int n = min(32, c1 - cb);
             for (int j = 0; j < n; ++j, ++seq) {
                 const int page = __shfl_sync(0xffffffffu, pg, j);

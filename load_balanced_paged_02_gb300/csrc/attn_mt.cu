@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(MtLayout<FP8, NTW, QS, TS, NG, STAGES>::kThrea
         if (h < 0) break;
         tw.next(p);
         if (!desc_ok(p, h, b, c0, c1, s)) continue;
-        const int L = __ldg(p.seq_lens + b);
+        const int L = p.seq_lens[b];
 
         uint32_t qf[NTW][8][2];
         const int qs = qd & 1;

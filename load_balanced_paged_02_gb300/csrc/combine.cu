@@ -55,8 +55,8 @@ __device__ __forceinline__ void load_lse8(const float* p, float (&l)[kGroup]) {
 }
 
 __global__ void __launch_bounds__(kCombineWarps * 32, 2)
-    combine_pairs_kernel(const int32_t* __restrict__ pair_nsplit, const int32_t* __restrict__ pair_split0,
-                   const float* __restrict__ split_o, const float* __restrict__ split_lse,
+    combine_pairs_kernel(const int32_t* pair_nsplit, const int32_t* pair_split0,
+                   const float* split_o, const float* split_lse,
                    __nv_bfloat16* __restrict__ out, float* __restrict__ out_lse, int B, int Hq, int Q) {
     __shared__ float wsh[kCombineWarps][kWTile][kGroup];
     grid_dependency_wait();  // the partials come from the attention kernel
@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32, 2)
 
 template <bool LONG>
 __global__ void __launch_bounds__(kCombineWarps * 32)
-    combine_rows_kernel(const int32_t* __restrict__ pair_nsplit, const int32_t* __restrict__ pair_split0,
-                   const float* __restrict__ split_o, const float* __restrict__ split_lse,
+    combine_rows_kernel(const int32_t* pair_nsplit, const int32_t* pair_split0,
+                   const float* split_o, const float* split_lse,
                    __nv_bfloat16* __restrict__ out, float* __restrict__ out_lse, int B, int Hq, int Q) {
     __shared__ float wsh[kCombineWarps][kRowTile];
     grid_dependency_wait();  // the partials come from the attention kernel

@@ -90,7 +90,7 @@ __device__ __forceinline__ void write_term(int32_t* row) {
 
 // Chunk prefix sums pre[0..B] (pre[B] = N) of n_b = ceil(max(L_b, 0) / 64).
 // Returns N, or 0 with every prefix zeroed when Hkv * N overflows int32.
-__device__ long long chunk_prefix(const int32_t* __restrict__ seq_lens, int B, int Hkv, int32_t* pre,
+__device__ long long chunk_prefix(const int32_t* seq_lens, int B, int Hkv, int32_t* pre,
                                   long long* warp_sums, int* s_err) {
     const int tid = threadIdx.x;
     long long running = 0;
@@ -143,8 +143,8 @@ __device__ void write_header(int32_t* buf, long long T, long long bucket, long l
 }
 
 // Block `block` of `blocks`.
-__device__ __forceinline__ void plan_balanced(int block, int blocks, const int32_t* __restrict__ seq_lens, int B, int Hkv,
-                                              int C, int m, int32_t* __restrict__ buf) {
+__device__ __forceinline__ void plan_balanced(int block, int blocks, const int32_t* seq_lens, int B, int Hkv,
+                                              int C, int m, int32_t* buf) {
     extern __shared__ int32_t pre[];  // [B + 1]
     __shared__ long long warp_sums[32];
     __shared__ unsigned warp_sums32[32];
@@ -246,8 +246,8 @@ __device__ __forceinline__ void plan_balanced(int block, int blocks, const int32
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1)
-    plan_balanced_kernel(const int32_t* __restrict__ seq_lens, int B, int Hkv, int C, int m,
-                         int32_t* __restrict__ buf) {
+    plan_balanced_kernel(const int32_t* seq_lens, int B, int Hkv, int C, int m,
+                         int32_t* buf) {
     grid_dependency_wait();   // seq_lens may come from the previous kernel
     grid_launch_dependents();
     plan_balanced(blockIdx.x, gridDim.x, seq_lens, B, Hkv, C, m, buf);
@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 // needs both, and the two launches in turn cost 3.5 us more.
 template <int T>
 __global__ void __launch_bounds__(kPlanThreads, 1)
-    both_plans_kernel(const TilePlanArgs a, const int32_t* __restrict__ seq_lens, int B, int Hkv, int C, int m,
-                      int32_t* __restrict__ buf) {
+    both_plans_kernel(const TilePlanArgs a, const int32_t* seq_lens, int B, int Hkv, int C, int m,
+                      int32_t* buf) {
     grid_dependency_wait();
     grid_launch_dependents();
     if (blockIdx.x == 0)
@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 static_assert(kPlanThreads == tileplan::kThreads, "one launch for both planners");
 
 __global__ void __launch_bounds__(kPlanThreads, 1)
-    plan_static_kernel(const int32_t* __restrict__ seq_lens, int B, int Hkv, int S,
-                       int32_t* __restrict__ buf) {
+    plan_static_kernel(const int32_t* seq_lens, int B, int Hkv, int S,
+                       int32_t* buf) {
     extern __shared__ int32_t pre[];  // [B + 1]
     __shared__ long long warp_sums[32];
     __shared__ int s_err;

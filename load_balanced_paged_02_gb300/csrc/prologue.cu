@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32, MINB) rope_norm_kernel(co
             const float inv = is_qk ? rsqrtf(s2 * (1.f / kHeadDim) + p.eps) : 1.f;
             if (is_qk) {
                 const float* wr = (is_q ? p.qw : p.kw) + 4 * hl;
-                const float4 w0 = __ldg(reinterpret_cast<const float4*>(wr));
-                const float4 w1 = __ldg(reinterpret_cast<const float4*>(wr + 64));
+                const float4 w0 = *reinterpret_cast<const float4*>(wr);
+                const float4 w1 = *reinterpret_cast<const float4*>(wr + 64);
                 const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
                 for (int k = 0; k < 8; ++k) y[k] *= inv * ww[k];
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(RingCfg<QW>::kThreads, 1) rope_norm_ring_kerne
     grid_launch_dependents();
     if (threadIdx.x < 2 * kHeadDim / 4) {  // the norm weights, into shared memory
         const float* src = threadIdx.x < kHeadDim / 4 ? p.qw + 4 * threadIdx.x : p.kw + 4 * (threadIdx.x - 32);
-        *reinterpret_cast<float4*>(wsm + 4 * threadIdx.x) = __ldg(reinterpret_cast<const float4*>(src));
+        *reinterpret_cast<float4*>(wsm + 4 * threadIdx.x) = *reinterpret_cast<const float4*>(src);
     }
     __syncthreads();
     const int H3 = rp.H3, G = rp.G;
@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(RingCfg<QW>::kThreads, 1) rope_norm_ring_kerne
         // position and slot of this lane's token of stage k, loaded one stage ahead
         int npos = 0, nslot = -1;
         if (k < rp.num_stages && lane < G && k * G + lane < p.T) {
-            npos = __ldg(p.pos + k * G + lane);
-            nslot = __ldg(p.slots + k * G + lane);
+            npos = p.pos[k * G + lane];
+            nslot = p.slots[k * G + lane];
         }
         for (; k < rp.num_stages; k += gridDim.x, ++i) {
             const int t0 = k * G;
@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(RingCfg<QW>::kThreads, 1) rope_norm_ring_kerne
             const int pos = npos, slot = nslot;
             const int kn = k + gridDim.x;
             if (kn < rp.num_stages && lane < G && kn * G + lane < p.T) {
-                npos = __ldg(p.pos + kn * G + lane);
-                nslot = __ldg(p.slots + kn * G + lane);
+                npos = p.pos[kn * G + lane];
+                nslot = p.slots[kn * G + lane];
             }
             const int st = (int)(i % kStages);
             if (lane == 0) ok = wait_bounded(&empty[st], ((i / kStages) & 1) ^ 1, abort_flag, kWaitLimitNs);
