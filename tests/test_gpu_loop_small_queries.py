@@ -164,3 +164,33 @@ def test_decode_of_large_rows():
     case["k_cache"].copy_(tiny_codes(case["k_cache"].shape, 24))
     case["k_scale"].fill_(2.0 ** -126)
     _gpu.check_full(case, _gpu.run(case, num_ctas=7, min_chunks=1, engine=hb.ENGINE_TCGEN05))
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_rows_that_are_not_finite_stay_alone(value):
+    """One head's row with an infinity or NaN: its weights' KV head and its own output are not numbers, all else has the
+    bits that it has beside an ordinary row."""
+    lens, starts = [200, 321], [0, 2, 12]
+    c = cache(lens, 2, 41, 1.0)
+    q = _tiles.make_q((12, 16, 128), 42)
+    lse = _loop.row_lse(q, starts, c["k"][0], lens)
+    bad = q.clone()
+    bad[5, 3, 17] = value
+    out = []
+    for x in (q, bad):
+        w = torch.zeros((2, 2, c["tables"][0].shape[1] * 64), device="cuda")
+        hb.hpc_attn_weights(x, c["k_cache"], c["tables"][0], _tiles.i32(lens), lse, w, q_starts=_tiles.i32(starts), k_scale=c["k_scale"])
+        out.append(w)
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1, 1], out[1][1, 1])
+    assert torch.equal(out[0][1, 0, 315:], out[1][1, 0, 315:])                 # tokens that row 5 does not see
+    seen = out[1][1, 0, :315]
+    assert (torch.isinf(seen) | torch.isnan(seen) | (seen < out[0][1, 0, :315])).all()   # exp(-inf): less by the row's part
+
+    case = wl.make_case(wl.Workload("t", 3, 8, 1, "fp8", 25, lens=[130, 700, 5], q_len=3), device="cuda:0")
+    clean = _gpu.run(case, num_ctas=7, min_chunks=1, engine=hb.ENGINE_TCGEN05)
+    case["q"][1, 1, 2, 9] = value
+    dirty = _gpu.run(case, num_ctas=7, min_chunks=1, engine=hb.ENGINE_TCGEN05)
+    same = torch.ones(clean["out"].shape[:-1], dtype=torch.bool, device="cuda")
+    same[1, 1, 2] = False
+    assert torch.equal(clean["out"][same], dirty["out"][same]) and torch.equal(clean["lse"][same], dirty["lse"][same])
+    assert not torch.equal(clean["out"][1, 1, 2], dirty["out"][1, 1, 2])

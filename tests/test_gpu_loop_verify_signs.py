@@ -118,3 +118,17 @@ def test_signs_of_nan(kind, bits):
     drafted = torch.tensor([[100], [200], [300], [400], [100], [39999]], dtype=torch.int32, device="cuda")
     for u in (0.0, 0.25, 0.75):
         check(target, draft, drafted, torch.full((B, 1), u, device="cuda"), torch.rand(B, generator=gen, device="cuda"))
+
+
+def test_random_numbers_that_are_none():
+    """A sample_rand of NaN gives the last entry above 0, one below 0 the first; an accept_rand of NaN refuses."""
+    B, V = 3, 50000
+    target = torch.zeros((B, 2, V), device="cuda")
+    target[:, :, 7000:9000] = 2.0 ** -12
+    draft = torch.full((B, 1, V), 2.0 ** -16, device="cuda")
+    drafted = torch.full((B, 1), 8000, dtype=torch.int32, device="cuda")
+    sample = torch.tensor([NAN, -1.0, 2.0], device="cuda")
+    for accept, r in ((0.0, 1), (NAN, 0)):
+        acc, tok = hb.hpc_verify_drafts(target, drafted, torch.full((B, 1), accept, device="cuda"), sample, draft_probs=draft)
+        assert acc.tolist() == [r] * B
+        assert [row[r] for row in tok.tolist()] == [8999, 7000, 8999]
