@@ -761,10 +761,10 @@ hpc_status hpc_kv_read(const void* k_cache, const void* v_cache, const float* k_
  * Between two attention steps of a decode loop: verification of drafted tokens,
  * the attention weight that cached tokens received, and eviction by it. A loop
  * that drafts and evicts runs hpc_decode_attn_multi over the drafted rows,
- * hpc_verify_drafts, hpc_attn_weights over the accepted rows, and, where a
- * request has grown past its budget, hpc_kv_select and hpc_kv_compact; it goes
- * on with the new pages and lengths. (Keys carry their rotation, so positions
- * go on as before.)
+ * hpc_verify_drafts, hpc_attn_weights over the rows that count (the last token's own and
+ * those of the accepted drafts: num_accepted + 1), and, where a request has grown past
+ * its budget, hpc_kv_select and hpc_kv_compact; it goes on with the new pages and
+ * lengths. (Keys carry their rotation, so positions go on as before.)
  */
 
 /*
@@ -785,7 +785,9 @@ hpc_status hpc_kv_read(const void* k_cache, const void* v_cache, const float* k_
  *              num_tokens / batch rows each, one sequence after the other (a decode
  *              batch's [batch][q_len]; num_tokens is a multiple of batch then)
  *   page_table_stride  <= 2^24
- *   row_counts device int32 [batch] or NULL (all rows); outside [0, n] as the nearest
+ *   row_counts device int32 [batch] or NULL (all rows); outside [0, n] as the nearest. After
+ *              hpc_verify_drafts it is num_accepted[b] + 1, not num_accepted[b]: row 0 is
+ *              that of the last token before the drafts
  *   window     rows that count at most; 0: all
  *   lse        device float32 [num_tokens][num_q_heads]; a row of -inf and finite queries has no weight
  *   decay      in [0, 1]; 1 adds to the weights received before
@@ -796,9 +798,14 @@ hpc_status hpc_kv_read(const void* k_cache, const void* v_cache, const float* k_
  *              beyond the page table's row counts as the row's, and a page id outside
  *              [0, num_pages) gives its 64 tokens no weight from this call
  *              (HPC_DEVERR_PAGE_OUT_OF_RANGE); a negative length counts as 0
- *              (HPC_DEVERR_NEGATIVE_LENGTH)
+ *              (HPC_DEVERR_NEGATIVE_LENGTH). A bounded wait that ran out
+ *              (HPC_DEVERR_WAIT_TIMEOUT) leaves the whole array undefined, some weights
+ *              changed and others not; without a word nothing tells of it
  * Sums are float32, in an order that does not depend on the batch. Values of K
- * that are not finite reach the weights of their own token alone. Errors:
+ * that are not finite reach the weights of their own token alone; a query row that is not
+ * finite, those of all tokens that it sees. Over an e4m3 cache a query row is the sum of two
+ * e4m3 numbers times a power of two, 2^-126 or more: exact to 2^-17 of its largest element,
+ * to 2^-136 for rows under 2^-117. Errors:
  * HPC_ERR_INVALID_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA. num_tokens == 0 enqueues nothing.
  */
 hpc_status hpc_attn_weights(const void* q, const void* k_cache, const float* k_scale, int kv_dtype, int num_pages,
@@ -839,7 +846,8 @@ hpc_status hpc_kv_select(const float* weights, long long weights_stride, const i
  *              weights_stride >= page_table_stride * 64; new_weights likewise, another
  *              array, new_weights_stride >= min(keep_stride, new_table_stride * 64)
  *   d_error_word  device int32 or NULL: HPC_DEVERR_PAGE_OUT_OF_RANGE (a token or page
- *              out of range: its row is not written; or keep_lens[b] beyond keep_stride
+ *              out of range: its K and V rows are not written, its weight only where the
+ *              token is within the table; or keep_lens[b] beyond keep_stride
  *              or the new table's row: counts as that), HPC_DEVERR_NEGATIVE_LENGTH
  * The new pages must not be pages that the call reads, and no page may be named twice, or
  * what they then hold is not determined; but a request whose tokens all stay where they
@@ -886,8 +894,8 @@ typedef enum hpc_probs_dtype { HPC_PROBS_F32 = 0, HPC_PROBS_BF16 = 1 } hpc_probs
  * that is compared or drawn from, and a difference p - q that is drawn from, counts as 0
  * unless it is above 0 and below 2^64 (another q that is NaN or infinite leaves its token
  * nothing). A comparison with NaN refuses. Where nothing is left after a refusal the token
- * is drawn from p_r; where that is 0 everywhere, it is -1. A sample_rand of 1 or more gives
- * the last entry above 0.
+ * is drawn from p_r; where that is 0 everywhere, it is -1. A sample_rand of 1 or more, or
+ * NaN, gives the last entry above 0.
  * Errors: HPC_ERR_INVALID_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA.
  */
 hpc_status hpc_verify_drafts(const void* target_probs, long long target_stride, const void* draft_probs,

@@ -977,7 +977,9 @@ def hpc_attn_weights(q, k_cache, page_table, seq_lens, lse, weights, q_starts=No
     that each cached token gets from the query rows, summed over the 8 heads of its KV head; ``decay`` scales
     what was there, and the places of the call's own tokens are set. q and lse are those of the attention call: a
     decode batch's [B, Hq, 128] or [B, q_len, Hq, 128], or packed rows [tokens, Hq, 128] with ``q_starts``. Of each
-    sequence the last ``window`` (0: all) of its first ``counts[b]`` (None: all) rows count."""
+    sequence the last ``window`` (0: all) of its first ``counts[b]`` (None: all) rows count; after hpc_verify_drafts
+    counts is num_accepted + 1, as row 0 is that of the token before the drafts. A wait that ran out inside the kernel
+    leaves ``weights`` undefined and is reported in ``error_word`` alone."""
     what = "hpc_attn_weights"
     kvd, pages, page, Hkv = _caches(what, k_cache, k_cache, k_scale, k_scale, num_pages)
     _query(what, q, new_tokens=q_starts is None)

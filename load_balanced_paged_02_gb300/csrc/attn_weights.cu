@@ -39,7 +39,8 @@
 // columns takes 48 clocks for its operands' bytes, where its arithmetic takes 34). The products alone would
 // take 85, the sums alone 87, neither 64. Two slots in one product of 128 columns: 91 us, but rows of 4
 // or 16 then take 3 to 5 % more; an issuer per group: registers for 22 warps are too few; half a slot's scores on
-// their way while the other half is summed: as before.
+// their way while the other half is summed: as before. The same windows over e4m3: 128 us. All 8192 rows of a
+// prompt: 1.62 ms, over e4m3 4.76 ms, where a pass's slots are for 3 to 4 tiles of a CTA.
 // Every wait is bounded (2 s); on expiry the CTA reports HPC_DEVERR_WAIT_TIMEOUT, gives
 // copies and MMAs in flight time to end, frees its TMEM and returns.
 #include <atomic>

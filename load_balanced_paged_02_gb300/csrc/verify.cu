@@ -19,7 +19,10 @@
 // The rows' bytes are the floor (256 requests of 131072 entries in 32 bits, target and draft:
 // 268 MB, 40 us at the rate of a copy); 50-52 us is what it takes, 5.3 TB/s. Without the
 // search it takes 47: a request begins with three round trips in a row (count, drafted token,
-// its probabilities) and ends with two more, which the SM's other CTAs cover in part.
+// its probabilities) and ends with two more, which the SM's other CTAs cover in part. In bf16 (512
+// requests, 49 us) the issue slots are 55 % busy; rows off 16 bytes have fewer loads on their way (128
+// requests of 100003 entries 27 us for 15 us of bytes), and so has the part that holds a certain
+// draft that was refused (256 requests 49 us for 20).
 #include "loop.cuh"
 #include "tile.cuh"
 
